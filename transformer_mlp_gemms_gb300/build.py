@@ -22,8 +22,11 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libkt_mlp.so")
 
 SOURCES = ["kt_gemm_act.cu", "kt_gemm_geglu.cu", "kt_gemm_down.cu", "kt_mlp_two_act_f16.cu", "kt_mlp_two_act_bf16.cu",
-           "kt_mlp_two_geglu.cu", "kt_fused.cu", "kt_mlp_kernels.cu", "kt_mlp_abi.cpp", "kt_planner.cpp"]
-HEADERS = [os.path.join(CSRC, "kt_internal.h"), os.path.join(CSRC, "kt_gemm.cuh"), os.path.join(INCLUDE, "kt_mlp.h")]
+           "kt_mlp_two_geglu.cu", "kt_fused.cu", "kt_mlp_kernels.cu", "kt_mlp_abi.cpp", "kt_planner.cpp",
+           "kt_ln_forward.cu", "kt_ln_backward.cu", "kt_quantize.cu", "kt_linear_i8.cu", "kt_moe.cu",
+           "kt_ops_abi.cpp"]
+HEADERS = [os.path.join(CSRC, "kt_internal.h"), os.path.join(CSRC, "kt_gemm.cuh"), os.path.join(INCLUDE, "kt_mlp.h"),
+           os.path.join(CSRC, "kt_ops_internal.h"), os.path.join(CSRC, "kt_rows.cuh"), os.path.join(INCLUDE, "kt_ops.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,256 @@
+// kt_ln_backward.cu -- the gradients of layer norm.  With xhat = (x - mean) rstd, g = dy gamma:
+//   dx = rstd (g - avg(g) - xhat avg(g xhat)),  dgamma = sum_rows dy xhat,  dbeta = sum_rows dy.
+//
+// Bound by HBM: 4 D bytes read and 2 D written per row.  One pass: a team of warps
+// (kt_rows.cuh) keeps its rows of x and dy in registers between the two averages and dx, and
+// adds each row's terms of dgamma and dbeta to fp32 sums of its own columns, in registers (in
+// shared memory for teams of 16 warps, whose threads have too few).  At the end a block adds
+// its teams' sums in team order and writes one row of partial sums; a second kernel adds the
+// rows of all blocks in order.  No atomics: the same bits from run to run.
+#include "kt_ops_internal.h"
+#include "kt_rows.cuh"
+
+namespace kt {
+namespace {
+
+template <int DT, int W, int V, bool VEC>
+__global__ void __launch_bounds__(row_block(W), 1) kt_ln_backward_kernel(const LnBackward p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int TL = 32 * W, teams = row_block(W) / TL;
+    constexpr bool kSmemSums = W == 16;
+    constexpr bool kAhead = W != 16;  // the next row's loads in flight during this row's sums
+    __shared__ TeamLines<W> lines;
+    extern __shared__ float sums[];  // [teams][TL * V * 8] for the final addition, or [2][..] (kSmemSums)
+    const int team = threadIdx.x / TL, l = threadIdx.x % TL;
+    const uint16_t* X = static_cast<const uint16_t*>(p.X);
+    const uint16_t* dY = static_cast<const uint16_t*>(p.dY);
+    uint16_t* dX = static_cast<uint16_t*>(p.dX);
+    const int D = p.D, step = (int)gridDim.x * teams;
+    const float inv = 1.0f / (float)D;
+    const bool affine = p.gamma != nullptr, want = p.dgamma != nullptr;
+    int row = (int)blockIdx.x * teams + team;
+    int turn = 0;
+
+    float dg[kSmemSums ? 1 : 8 * V], db[kSmemSums ? 1 : 8 * V];
+    if constexpr (kSmemSums) {
+        for (int i = threadIdx.x; i < 2 * TL * V * 8; i += row_block(W)) sums[i] = 0.0f;
+        __syncthreads();
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8 * V; ++i) dg[i] = db[i] = 0.0f;
+    }
+    uint4 cx[V], cy[V], gw[V];
+    float mean = 0.0f, rstd = 0.0f, next_mean = 0.0f, next_rstd = 0.0f;
+    if (row < p.M) {
+        mean = p.mean[row];
+        rstd = p.rstd[row];
+#pragma unroll
+        for (int s = 0; s < V; ++s) {
+            cx[s] = load_slot<VEC>(X + (int64_t)row * p.ldx, s, l, TL, D);
+            cy[s] = load_slot<VEC>(dY + (int64_t)row * p.lddy, s, l, TL, D);
+        }
+    }
+    if (affine) {
+#pragma unroll
+        for (int s = 0; s < V; ++s) gw[s] = load_slot<VEC>(static_cast<const uint16_t*>(p.gamma), s, l, TL, D);
+    }
+    while (row < p.M) {
+        const int next = p.M - row > step ? row + step : p.M;
+        uint4 nx[V], ny[V];
+        if (next < p.M) {
+            next_mean = p.mean[next];
+            next_rstd = p.rstd[next];
+        }
+        if (kAhead && next < p.M) {
+#pragma unroll
+            for (int s = 0; s < V; ++s) {
+                nx[s] = load_slot<VEC>(X + (int64_t)next * p.ldx, s, l, TL, D);
+                ny[s] = load_slot<VEC>(dY + (int64_t)next * p.lddy, s, l, TL, D);
+            }
+        }
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int s = 0; s < V; ++s) {
+            float x[8], y[8], g[8];
+            unpack8<DT>(cx[s], x);
+            unpack8<DT>(cy[s], y);
+            if (affine) unpack8<DT>(gw[s], g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float xh = (x[e] - mean) * rstd;
+                const float ge = affine ? y[e] * g[e] : y[e];
+                s1 += ge;
+                s2 = fmaf(ge, xh, s2);
+                if constexpr (kSmemSums) {
+                    if (want) {
+                        float* at = sums + (size_t)(s * 8 + e) * TL + l;
+                        at[0] = fmaf(y[e], xh, at[0]);
+                        at[TL * V * 8] += y[e];
+                    }
+                } else {
+                    dg[8 * s + e] = fmaf(y[e], xh, dg[8 * s + e]);
+                    db[8 * s + e] += y[e];
+                }
+            }
+        }
+        team_add2<W>(s1, s2, lines, turn, team);
+        s1 *= inv;
+        s2 *= inv;
+        uint16_t* xr = dX + (int64_t)row * p.lddx;
+#pragma unroll
+        for (int s = 0; s < V; ++s) {
+            float x[8], y[8], g[8];
+            unpack8<DT>(cx[s], x);
+            unpack8<DT>(cy[s], y);
+            if (affine) unpack8<DT>(gw[s], g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float xh = (x[e] - mean) * rstd;
+                const float ge = affine ? y[e] * g[e] : y[e];
+                y[e] = rstd * (ge - fmaf(xh, s2, s1));
+            }
+            store_slot<VEC>(xr, s, l, TL, D, pack8<DT>(y));
+        }
+        row = next;
+        mean = next_mean;
+        rstd = next_rstd;
+        if (kAhead) {
+#pragma unroll
+            for (int s = 0; s < V; ++s) {
+                cx[s] = nx[s];
+                cy[s] = ny[s];
+            }
+        } else if (row < p.M) {
+#pragma unroll
+            for (int s = 0; s < V; ++s) {
+                cx[s] = load_slot<VEC>(X + (int64_t)row * p.ldx, s, l, TL, D);
+                cy[s] = load_slot<VEC>(dY + (int64_t)row * p.lddy, s, l, TL, D);
+            }
+        }
+    }
+    if (!want) return;
+    float* out = p.partials + (size_t)blockIdx.x * 2 * D;
+#pragma unroll
+    for (int which = 0; which < 2; ++which, out += D) {
+        if constexpr (teams == 1) {
+#pragma unroll
+            for (int s = 0; s < V; ++s)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int c = slot_col<VEC>(s, e, l, TL);
+                    if (c < D) {
+                        if constexpr (kSmemSums)
+                            out[c] = sums[(size_t)which * TL * V * 8 + (size_t)(s * 8 + e) * TL + l];
+                        else
+                            out[c] = which ? db[8 * s + e] : dg[8 * s + e];
+                    }
+                }
+        } else {
+            constexpr int width = TL * V * 8;
+            if (which) __syncthreads();
+#pragma unroll
+            for (int s = 0; s < V; ++s)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    sums[team * width + (8 * s + e) * TL + l] = which ? db[8 * s + e] : dg[8 * s + e];
+            __syncthreads();
+            for (int i = threadIdx.x; i < width; i += row_block(W)) {
+                // i counts (element of a lane, lane): the columns in the teams' order
+                const int se = i / TL, li = i % TL, c = slot_col<VEC>(se / 8, se % 8, li, TL);
+                float v = 0.0f;
+#pragma unroll
+                for (int t = 0; t < teams; ++t) v += sums[t * width + i];
+                if (c < D) out[c] = v;
+            }
+        }
+    }
+}
+
+// Adds the blocks' rows of partial sums, in order: out[c] = sum_r partials[r][c] over the 2 D
+// columns (dgamma, then dbeta).  32 columns and 8 runs of rows per block.
+__global__ void __launch_bounds__(256) kt_ln_column_sums_kernel(const float* __restrict__ partials, int rows, int D,
+                                                                float* __restrict__ dgamma, float* __restrict__ dbeta) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ float part[8][32];
+    const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
+    const int c = (int)blockIdx.x * 32 + lane;
+    const int per = (rows + 7) / 8, r1 = min(rows, (run + 1) * per);
+    float v = 0.0f;
+    if (c < 2 * D) {
+#pragma unroll 8
+        for (int r = run * per; r < r1; ++r) v += partials[(size_t)r * 2 * D + c];
+    }
+    part[run][lane] = v;
+    __syncthreads();
+    if (run == 0 && c < 2 * D) {
+        v = part[0][lane];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) v += part[i][lane];
+        if (c < D)
+            dgamma[c] = v;
+        else
+            dbeta[c - D] = v;
+    }
+}
+
+}  // namespace
+
+// One block per SM: each keeps 8 / W rows in flight and the next ones' loads behind them.
+int ln_backward_blocks(int64_t M, int64_t D) {
+    RowShape shape;
+    if (M < 0 || D < 1 || !row_shape(D, &shape)) return 0;
+    const int teams = row_block(shape.W) / (32 * shape.W);
+    return (int)std::min<int64_t>((M + teams - 1) / teams, kMaxSms);
+}
+
+kt_status launch_ln_backward(int dtype, const LnBackward& p, int sms, void* stream, const char** why) {
+    RowShape shape;
+    if (!row_shape(p.D, &shape)) {
+        *why = "rows of this length are not supported";
+        return KT_ERR_UNSUPPORTED;
+    }
+    const int grid = std::min(ln_backward_blocks(p.M, p.D), sms);
+    cudaError_t e = cudaSuccess;
+    if (grid > 0) {
+        const auto al = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; };
+        const bool vec = p.D % 8 == 0 && p.ldx % 8 == 0 && p.lddy % 8 == 0 && p.lddx % 8 == 0 && al(p.X) && al(p.dY) &&
+                         al(p.dX) && al(p.gamma);
+        auto go = [&](auto dt, auto v16) {
+            return with_shape<decltype(v16)::value>(shape, [&](auto W, auto V) -> kt_status {
+                constexpr int w = decltype(W)::value, v = decltype(V)::value, teams = row_block(w) / (32 * w);
+                constexpr size_t smem = (w == 16 ? 2 : teams == 1 ? 0 : teams) * (size_t)(32 * w * v * 8) * sizeof(float);
+                auto kern = kt_ln_backward_kernel<decltype(dt)::value, w, v, decltype(v16)::value>;
+                cudaError_t le = cudaSuccess;
+                if (smem > 32 * 1024)
+                    le = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                if (le == cudaSuccess) le = launch_pdl(kern, (unsigned)grid, row_block(w), smem, stream, p);
+                if (le != cudaSuccess) {
+                    *why = cudaGetErrorString(le);
+                    return KT_ERR_CUDA;
+                }
+                return KT_OK;
+            });
+        };
+        using F16 = std::integral_constant<int, KT_F16>;
+        using BF16 = std::integral_constant<int, KT_BF16>;
+        kt_status s;
+        if (dtype == KT_F16)
+            s = vec ? go(F16{}, std::true_type{}) : go(F16{}, std::false_type{});
+        else
+            s = vec ? go(BF16{}, std::true_type{}) : go(BF16{}, std::false_type{});
+        if (s != KT_OK) return s;
+    }
+    if (p.dgamma) {
+        e = launch_pdl(kt_ln_column_sums_kernel, (unsigned)((2 * (int64_t)p.D + 31) / 32), 256, 0, stream, p.partials, grid,
+                       p.D, p.dgamma, p.dbeta);
+        if (e != cudaSuccess) {
+            *why = cudaGetErrorString(e);
+            return KT_ERR_CUDA;
+        }
+    }
+    return KT_OK;
+}
+
+}  // namespace kt

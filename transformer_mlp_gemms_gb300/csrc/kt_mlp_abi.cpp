@@ -20,6 +20,7 @@
 #include <vector>
 
 #include "kt_internal.h"
+#include "kt_ops_internal.h"
 
 namespace {
 
@@ -89,6 +90,16 @@ kt_mlp_options base_options(int64_t M, int64_t D, int64_t F, int act, int dtype,
 }
 
 }  // namespace
+
+// The calling thread's message, for the other translation units of the boundary ("" clears it).
+kt_status kt::report(kt_status s, const char* msg) {
+    try {
+        g_last_error = msg;
+    } catch (...) {
+        g_last_error.clear();
+    }
+    return s;
+}
 
 struct kt_mlp_plan_s {
     int64_t M, D, F, F_up;
