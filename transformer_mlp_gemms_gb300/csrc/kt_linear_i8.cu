@@ -93,10 +93,341 @@ __global__ void __launch_bounds__(kDotWarps * 32) kt_linear_i8_dot_kernel(const 
     }
 }
 
+// Many tokens: on the tensor cores.  This GPU has no 8-bit integer kind of tcgen05.mma and its
+// older integer products run at the rate of four-way dot products, but every int8 is a 16-bit
+// float, every product of two is below 2^15, and fp32 holds sums of them exactly up to 2^24: so
+// the operands become fp16 on their way into the tensor cores, and the bytes that move stay one
+// per element.
+//
+// One persistent CTA per SM, tiles of 128 tokens x BN channels, k-blocks of 64:
+//   warps 0-3    tokens: each thread takes 64 bytes of its own row from global memory, three
+//                k-blocks ahead in registers, and stores them as fp16 into tensor memory, where
+//                the product reads its first operand (32 columns per stage, 4 stages).  That
+//                operand never passes through shared memory, whose bandwidth would bound the
+//                kernel: 128 x 192 x 64 takes the tensor cores 384 cycles, writing and reading
+//                the second operand takes shared memory the same 384, and the first one's 16 KB
+//                would add 256.
+//   warps 4-11   channels: 16-byte pieces of the weight's rows, three k-blocks ahead, into shared
+//                memory as fp16, K-major with the 128-byte swizzle;
+//   warp 16      one thread issues tcgen05.mma (fp16, fp32 accumulators, two buffers of BN
+//                columns, so that a tile's epilogue runs beside the next tile's products);
+//   warps 12-15  epilogue: accumulator x token scale x channel scale (+ bias), one rounding,
+//                rows of 64 columns put together in shared memory and stored as full lines.
+// Four bytes become two pairs of fp16 in five instructions: with the sign bit flipped a byte is
+// q + 128, and next to the byte 0x64 it is the fp16 number 1024 + (q + 128); 1152 is subtracted.
+constexpr int kTcStages = 4, kTcAhead = 3;
+constexpr int kTcTokenWarps = 4, kTcChannelWarps = 8, kTcEpiWarps = 4;
+constexpr int kTcThreads = (kTcTokenWarps + kTcChannelWarps + kTcEpiWarps + 1) * 32;
+constexpr uint32_t kTcACol = 384;  // tensor-memory column of the first operand's stages
+__device__ int g_linear_i8_error;  // a bounded wait that ran out (never in normal operation)
+
+__device__ __forceinline__ void bytes_to_halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u, big = 0x64806480u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(big));
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(big));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// The product with its first operand in tensor memory.
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+template <int BN>
+struct TcSmem {
+    alignas(1024) uint8_t b[kTcStages][BN * 128];   // [channel][64 fp16], 128-byte swizzle
+    alignas(128) uint8_t out[kTcEpiWarps][32 * 128];  // a warp's 32 rows x 64 columns of the output
+    float2 ch[2][BN];                               // channel scale and bias of the tile
+    alignas(8) uint64_t full[kTcStages], empty[kTcStages], acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+    int abort;
+};
+
+template <int DT, int BN>
+__global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const LinearI8 p, int tiles_n, int tiles, uint32_t idesc,
+                                                                        int wide_y) {
+    extern __shared__ uint8_t raw[];
+    TcSmem<BN>& sm = *reinterpret_cast<TcSmem<BN>*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* abort_flag = &sm.abort;
+    constexpr unsigned long long kLimit = 4000000000ull;  // 4 s: far beyond any legitimate wait
+    auto bar = [&](uint64_t& b) { return smem_u32(&b); };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kTcStages; ++s) {
+            mbar_init(bar(sm.full[s]), kTcTokenWarps + kTcChannelWarps);
+            mbar_init(bar(sm.empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar(sm.acc_full[b]), 1);
+            mbar_init(bar(sm.acc_empty[b]), kTcEpiWarps);
+        }
+        mbar_init(bar(sm.drain), 1);
+        sm.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+    }
+    if (warp == 16) tmem_alloc<1>(smem_u32(&sm.tmem), kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int kblocks = (p.K + 63) / 64;
+    const int mine = tiles > (int)blockIdx.x ? (tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+    const int total = mine * kblocks;  // k-blocks of all this CTA's tiles, in order
+
+    if (warp < kTcTokenWarps + kTcChannelWarps) {
+        // ------------------- producers: bytes from global memory, fp16 to the operands -------------------
+        constexpr int kUnits = BN / 64;  // channels: 16-byte pieces per thread and k-block
+        const bool tokens = warp < kTcTokenWarps;
+        const int u0 = (int)threadIdx.x - kTcTokenWarps * 32;  // channel piece u: row u / 4, bytes 16 (u % 4)
+        uint4 reg[kTcAhead][4];  // tokens: 64 bytes of a row; channels: up to 3 pieces
+        // load cursor: k-block l of the CTA's sequence
+        int l_tile = (int)blockIdx.x, l_kb = 0;
+        const int8_t* l_row = nullptr;  // tokens: this thread's row (null past the last)
+        int l_n0 = 0;
+        auto load = [&](uint4 (&r)[4]) {
+            if (l_kb == 0) {
+                const int m0 = (l_tile / tiles_n) * 128;
+                l_n0 = (l_tile % tiles_n) * BN;
+                const int m = m0 + (int)threadIdx.x;
+                l_row = m < p.M ? p.Q + (int64_t)m * p.ldq : nullptr;
+            }
+            const int k = l_kb * 64;
+            if (tokens) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    r[j] = make_uint4(0u, 0u, 0u, 0u);
+                    if (l_row && k + 16 * j < p.K) r[j] = __ldg(reinterpret_cast<const uint4*>(l_row + k + 16 * j));
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kUnits; ++j) {
+                    const int u = u0 + j * kTcChannelWarps * 32, n = l_n0 + (u >> 2), kk = k + 16 * (u & 3);
+                    r[j] = make_uint4(0u, 0u, 0u, 0u);
+                    if (n < p.N && kk < p.K) r[j] = __ldg(reinterpret_cast<const uint4*>(p.W + (int64_t)n * p.ldw + kk));
+                }
+            }
+            if (++l_kb == kblocks) {
+                l_kb = 0;
+                l_tile += (int)gridDim.x;
+            }
+        };
+        uint32_t stage = 0, phase = 0;
+        auto convert = [&](uint4 (&r)[4]) -> bool {
+            bool ok = wait_phase(bar(sm.empty[stage]), phase ^ 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_PRODUCER, kLimit);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return false;
+            if (tokens) {
+                uint32_t h[32];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    bytes_to_halves(r[j].x, h[8 * j], h[8 * j + 1]);
+                    bytes_to_halves(r[j].y, h[8 * j + 2], h[8 * j + 3]);
+                    bytes_to_halves(r[j].z, h[8 * j + 4], h[8 * j + 5]);
+                    bytes_to_halves(r[j].w, h[8 * j + 6], h[8 * j + 7]);
+                }
+                tc_fence_after();
+                tmem_st32(tmem + ((uint32_t)(warp * 32) << 16) + kTcACol + stage * 32u, h);
+                tc_fence_before();
+            } else {
+                const uint32_t base = smem_u32(sm.b[stage]);
+#pragma unroll
+                for (int j = 0; j < kUnits; ++j) {
+                    const int u = u0 + j * kTcChannelWarps * 32, n = u >> 2;
+                    const uint32_t c = 2u * (u & 3), row = base + (uint32_t)n * 128u;
+                    uint32_t h[8];
+                    bytes_to_halves(r[j].x, h[0], h[1]);
+                    bytes_to_halves(r[j].y, h[2], h[3]);
+                    bytes_to_halves(r[j].z, h[4], h[5]);
+                    bytes_to_halves(r[j].w, h[6], h[7]);
+                    st_shared_v4(row + ((c ^ (n & 7u)) << 4), h[0], h[1], h[2], h[3]);
+                    st_shared_v4(row + (((c + 1u) ^ (n & 7u)) << 4), h[4], h[5], h[6], h[7]);
+                }
+                fence_async_smem();  // the tensor cores read it through the async proxy
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(sm.full[stage]));
+            if (++stage == kTcStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+            return true;
+        };
+#pragma unroll
+        for (int u = 0; u < kTcAhead; ++u)
+            if (u < total) load(reg[u]);
+        bool ok = true;
+        for (int i = 0; i < total && ok; i += kTcAhead) {
+#pragma unroll
+            for (int u = 0; u < kTcAhead; ++u) {
+                if (i + u < total && ok) {
+                    ok = convert(reg[u]);
+                    if (ok && i + u + kTcAhead < total) load(reg[u]);
+                }
+            }
+        }
+    } else if (warp == 16) {
+        // ------------------- one thread issues the products -------------------
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            bool ok = true;
+            for (int t = 0; t < mine && ok; ++t) {
+                const uint32_t buf = t & 1u, use = (uint32_t)t >> 1;
+                ok = wait_phase(bar(sm.acc_empty[buf]), (use & 1u) ^ 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_MMA, kLimit);
+                for (int kb = 0; kb < kblocks && ok; ++kb) {
+                    ok = wait_phase(bar(sm.full[stage]), phase, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_MMA, kLimit);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t bd = smem_desc(smem_u32(sm.b[stage]), 16u, 1024u);
+                    const uint32_t a = tmem + kTcACol + stage * 32u;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_f16_ta(tmem + buf * (uint32_t)BN, a + 8u * k, bd + (uint64_t)(2 * k), idesc, kb > 0 || k > 0);
+                    mma_commit(bar(sm.empty[stage]));
+                    if (++stage == kTcStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok) mma_commit(bar(sm.acc_full[buf]));
+            }
+            if (!ok) {  // no product may still be running when tensor memory is freed
+                mma_commit(bar(sm.drain));
+                wait_drain(bar(sm.drain), 0u, 100000000ull);
+            }
+        }
+    } else {
+        // ------------------- epilogue -------------------
+        const int q = warp & 3, ew = warp - 12;
+        uint8_t* out = sm.out[ew];
+        uint16_t* Y = static_cast<uint16_t*>(p.Y);
+        for (int t = 0; t < mine; ++t) {
+            const int tile = (int)blockIdx.x + t * (int)gridDim.x;
+            const int m0 = (tile / tiles_n) * 128 + q * 32, n0 = (tile % tiles_n) * BN;
+            const uint32_t buf = t & 1u, use = (uint32_t)t >> 1;
+            for (int i = ew * 32 + lane; i < BN; i += kTcEpiWarps * 32) {
+                float2 c = make_float2(0.0f, 0.0f);
+                if (n0 + i < p.N) {
+                    c.x = p.sw[n0 + i];
+                    if (p.bias) c.y = from_bits<DT>(static_cast<const uint16_t*>(p.bias)[n0 + i]);
+                }
+                sm.ch[buf][i] = c;
+            }
+            const float sx = m0 + lane < p.M ? p.sx[m0 + lane] : 0.0f;
+            const bool got = wait_phase(bar(sm.acc_full[buf]), use & 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_EPILOGUE, kLimit);
+            if (!epi_all<kTcEpiWarps>(got)) break;  // also: every warp's part of ch is in place
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < BN; c0 += 64) {
+                uint32_t w[32];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t r[32];
+                    tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * (uint32_t)BN + c0 + 32 * half, r);
+                    tmem_wait_ld_only();
+                    reg_fence32(r);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float4 c = *reinterpret_cast<const float4*>(&sm.ch[buf][c0 + 32 * half + i]);
+                        w[16 * half + i / 2] = pack2<DT>(fmaf(__uint_as_float(r[i]), sx * c.x, c.y),
+                                                         fmaf(__uint_as_float(r[i + 1]), sx * c.z, c.w));
+                    }
+                }
+                if (c0 + 64 >= BN) {  // the last columns are in registers: the next tile may have the buffer
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(sm.acc_empty[buf]));
+                }
+                if (m0 >= p.M) continue;
+                // 16-byte chunk i of row r at chunk i ^ (r & 7): no bank conflicts either way
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4*>(out + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                __syncwarp();
+                const int n = n0 + c0;
+                if (wide_y) {
+                    // eight lanes store a row's 128 bytes
+#pragma unroll
+                    for (int r0 = 0; r0 < 32; r0 += 4) {
+                        const int r = r0 + (lane >> 3), i = lane & 7;
+                        const uint4 v = *reinterpret_cast<const uint4*>(out + r * 128 + ((i ^ (r & 7)) << 4));
+                        if (m0 + r < p.M && n + 8 * i < p.N)
+                            *reinterpret_cast<uint4*>(Y + (int64_t)(m0 + r) * p.ldy + n + 8 * i) = v;
+                    }
+                } else {
+                    for (int r = 0; r < 32 && m0 + r < p.M; ++r)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int c = 32 * h + lane;
+                            const uint16_t v = *reinterpret_cast<const uint16_t*>(out + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + 2 * (c & 7));
+                            if (n + c < p.N) Y[(int64_t)(m0 + r) * p.ldy + n + c] = v;
+                        }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 16) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc<1>(tmem, kTmemCols);
+    }
+}
+
+template <int BN>
+kt_status launch_tc(int dtype, const LinearI8& p, int sms, void* stream, const char** why) {
+    const int tiles_m = (p.M + 127) / 128, tiles_n = (p.N + BN - 1) / BN, tiles = tiles_m * tiles_n;
+    // whole 16-byte pieces of Y's rows: the last one too, as N is a multiple of 8
+    const int wide = p.N % 8 == 0 && p.ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(p.Y) & 15u) == 0;
+    auto kern = dtype == KT_BF16 ? kt_linear_i8_tc_kernel<KT_BF16, BN> : kt_linear_i8_tc_kernel<KT_F16, BN>;
+    constexpr int smem = (int)sizeof(TcSmem<BN>) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+        e = launch_pdl(kern, (unsigned)std::min(tiles, sms), kTcThreads, smem, stream, p, tiles_n, tiles,
+                       make_idesc(KT_F16, BN, 128, 1), wide);
+    if (e != cudaSuccess) {
+        *why = cudaGetErrorString(e);
+        return KT_ERR_CUDA;
+    }
+    return KT_OK;
+}
+
 }  // namespace
 
 kt_status launch_linear_i8(int dtype, const LinearI8& p, int sms, void* stream, const char** why) {
-    (void)sms;
+    if (p.M > kDotTokens) {
+        // tile width: the fewest rounds over the SMs, each costing its products' cycles
+        const int64_t tm = (p.M + 127) / 128;
+        auto cost = [&](int bn, int per) { return ((tm * ((p.N + bn - 1) / bn) + sms - 1) / sms) * per; };
+        const int64_t c192 = cost(192, 384), c128 = cost(128, 290), c64 = cost(64, 220);
+        if (c192 <= c128 && c192 <= c64) return launch_tc<192>(dtype, p, sms, stream, why);
+        if (c128 <= c64) return launch_tc<128>(dtype, p, sms, stream, why);
+        return launch_tc<64>(dtype, p, sms, stream, why);
+    }
     const int chunk = std::min(kDotChunk, (p.K + 127) & ~127);
     const dim3 grid((unsigned)((p.N + kDotRows - 1) / kDotRows), (unsigned)((p.M + kDotTokens - 1) / kDotTokens));
     cudaLaunchConfig_t cfg = {};
