@@ -285,6 +285,10 @@ kt_status launch_mlp_two(int epi, int dtype, const void* const* maps, const Gemm
 bool encode_tmap(void* tmap128, const void* base, int dtype, uint64_t rows, uint64_t cols,
                  uint32_t box_rows, uint32_t box_cols, int swizzle_bytes, const char** why);
 
+// As encode_tmap, with `pitch` elements (a multiple of 8) from one row to the next.
+bool encode_tmap_pitch(void* tmap128, const void* base, int dtype, uint64_t rows, uint64_t cols, uint64_t pitch,
+                       uint32_t box_rows, uint32_t box_cols, int swizzle_bytes, const char** why);
+
 // tcgen05 instruction descriptor for kind::f16 with fp32 accumulation, A K-major,
 // B MN-major (b_kmajor = 0) or K-major (1), M = m (128, or 256 for a CTA pair), N = n.
 uint32_t make_idesc(int dtype, int n, int m, int b_kmajor = 0);

@@ -100,9 +100,11 @@ __global__ void __launch_bounds__(kDotWarps * 32) kt_linear_i8_dot_kernel(const 
 // per element.
 //
 // One persistent CTA per SM, tiles of 128 tokens x BN channels, k-blocks of 64:
-//   warps 0-3    tokens: each thread takes 64 bytes of its own row from global memory, three
-//                k-blocks ahead in registers, and stores them as fp16 into tensor memory, where
-//                the product reads its first operand (32 columns per stage, 4 stages).  That
+//   warps 0-3    tokens: 16-byte pieces of the tokens' rows from global memory, three k-blocks
+//                ahead in registers, stored as fp16 into tensor memory, where the product reads
+//                its first operand (32 columns per stage, 4 stages; four lanes of a warp share a
+//                row, and as a sum over k may take its terms in any order, each lane's 16 bytes
+//                go to the columns that the lane owns, and the channels follow suit).  That
 //                operand never passes through shared memory, whose bandwidth would bound the
 //                kernel: 128 x 192 x 64 takes the tensor cores 384 cycles, writing and reading
 //                the second operand takes shared memory the same 384, and the first one's 16 KB
@@ -128,17 +130,15 @@ __device__ __forceinline__ void bytes_to_halves(uint32_t w, uint32_t& lo, uint32
     asm("sub.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(big));
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+// 16 rows x 32 columns into tensor memory: lane 4 r + c holds columns c, c + 4, ... of row r in
+// its even registers and of row r + 8 in its odd ones.
+__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // The product with its first operand in tensor memory.
@@ -201,24 +201,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
         constexpr int kUnits = BN / 64;  // channels: 16-byte pieces per thread and k-block
         const bool tokens = warp < kTcTokenWarps;
         const int u0 = (int)threadIdx.x - kTcTokenWarps * 32;  // channel piece u: row u / 4, bytes 16 (u % 4)
-        uint4 reg[kTcAhead][4];  // tokens: 64 bytes of a row; channels: up to 3 pieces
+        uint4 reg[kTcAhead][4];  // tokens: a 16-byte piece of 4 rows; channels: up to 3 pieces
         // load cursor: k-block l of the CTA's sequence
         int l_tile = (int)blockIdx.x, l_kb = 0;
-        const int8_t* l_row = nullptr;  // tokens: this thread's row (null past the last)
-        int l_n0 = 0;
+        const int g = lane >> 2, q4 = lane & 3;
+        int l_m0 = 0, l_n0 = 0;
         auto load = [&](uint4 (&r)[4]) {
             if (l_kb == 0) {
-                const int m0 = (l_tile / tiles_n) * 128;
+                l_m0 = (l_tile / tiles_n) * 128 + warp * 32 + g;
                 l_n0 = (l_tile % tiles_n) * BN;
-                const int m = m0 + (int)threadIdx.x;
-                l_row = m < p.M ? p.Q + (int64_t)m * p.ldq : nullptr;
             }
             const int k = l_kb * 64;
             if (tokens) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     r[j] = make_uint4(0u, 0u, 0u, 0u);
-                    if (l_row && k + 16 * j < p.K) r[j] = __ldg(reinterpret_cast<const uint4*>(l_row + k + 16 * j));
+                    if (l_m0 + 8 * j < p.M && k + 16 * q4 < p.K)
+                        r[j] = __ldg(reinterpret_cast<const uint4*>(p.Q + (int64_t)(l_m0 + 8 * j) * p.ldq + k + 16 * q4));
                 }
             } else {
 #pragma unroll
@@ -239,30 +238,37 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return false;
             if (tokens) {
-                uint32_t h[32];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    bytes_to_halves(r[j].x, h[8 * j], h[8 * j + 1]);
-                    bytes_to_halves(r[j].y, h[8 * j + 2], h[8 * j + 3]);
-                    bytes_to_halves(r[j].z, h[8 * j + 4], h[8 * j + 5]);
-                    bytes_to_halves(r[j].w, h[8 * j + 6], h[8 * j + 7]);
-                }
                 tc_fence_after();
-                tmem_st32(tmem + ((uint32_t)(warp * 32) << 16) + kTcACol + stage * 32u, h);
+#pragma unroll
+                for (int j = 0; j < 4; j += 2) {  // rows g + 8 j and g + 8 j + 8 of the warp's 32
+                    uint32_t h[16];
+#pragma unroll
+                    for (int o = 0; o < 2; ++o) {
+                        bytes_to_halves(r[j + o].x, h[o], h[2 + o]);
+                        bytes_to_halves(r[j + o].y, h[4 + o], h[6 + o]);
+                        bytes_to_halves(r[j + o].z, h[8 + o], h[10 + o]);
+                        bytes_to_halves(r[j + o].w, h[12 + o], h[14 + o]);
+                    }
+                    tmem_st_16x32(tmem + ((uint32_t)(warp * 32 + 8 * j) << 16) + kTcACol + stage * 32u, h);
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
             } else {
                 const uint32_t base = smem_u32(sm.b[stage]);
 #pragma unroll
                 for (int j = 0; j < kUnits; ++j) {
                     const int u = u0 + j * kTcChannelWarps * 32, n = u >> 2;
-                    const uint32_t c = 2u * (u & 3), row = base + (uint32_t)n * 128u;
+                    const uint32_t row = base + (uint32_t)n * 128u + 4u * (u & 3);
                     uint32_t h[8];
                     bytes_to_halves(r[j].x, h[0], h[1]);
                     bytes_to_halves(r[j].y, h[2], h[3]);
                     bytes_to_halves(r[j].z, h[4], h[5]);
                     bytes_to_halves(r[j].w, h[6], h[7]);
-                    st_shared_v4(row + ((c ^ (n & 7u)) << 4), h[0], h[1], h[2], h[3]);
-                    st_shared_v4(row + (((c + 1u) ^ (n & 7u)) << 4), h[4], h[5], h[6], h[7]);
+                    // pair i goes to chunk i, word u % 4: the tokens' order of a k-block, whose
+                    // lane c holds bytes 16 c .. + 15 and fills columns c, c + 4, ...
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + ((i ^ (n & 7u)) << 4)), "r"(h[i]) : "memory");
                 }
                 fence_async_smem();  // the tensor cores read it through the async proxy
             }

@@ -437,13 +437,18 @@ kt_status launch_activation(int act, bool paired, const float* z, const float* g
 
 bool encode_tmap(void* tmap128, const void* base, int dtype, uint64_t rows, uint64_t cols,
                  uint32_t box_rows, uint32_t box_cols, int swizzle_bytes, const char** why) {
+    return encode_tmap_pitch(tmap128, base, dtype, rows, cols, cols, box_rows, box_cols, swizzle_bytes, why);
+}
+
+bool encode_tmap_pitch(void* tmap128, const void* base, int dtype, uint64_t rows, uint64_t cols, uint64_t pitch,
+                       uint32_t box_rows, uint32_t box_cols, int swizzle_bytes, const char** why) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
     if (!fn) {
         *why = "cuTensorMapEncodeTiled is not available from the driver";
         return false;
     }
     cuuint64_t dims[2] = {cols, rows};
-    cuuint64_t strides[1] = {cols * 2};
+    cuuint64_t strides[1] = {pitch * 2};
     cuuint32_t box[2] = {box_cols, box_rows};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(reinterpret_cast<CUtensorMap*>(tmap128),

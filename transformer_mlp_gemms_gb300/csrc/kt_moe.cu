@@ -5,96 +5,77 @@
 //
 // Bound by HBM: a few tokens touch up to top_k experts each, and every touched expert's
 // weights have to be read once, for all of its tokens together; each weight then meets 1 to 64
-// tokens.  One persistent grid of co-resident blocks goes through four phases with a barrier
-// over the grid after each of the first three:
+// tokens.  One persistent grid of co-resident blocks, one per SM:
 //
-//   0  logits: one warp per (token, expert), in pairs of fp32 numbers (below);
-//   1  every block finds all tokens' experts for itself (the order is the same everywhere) and
-//      takes its share of the up projections: H[pair][f] for each (token, expert) pair;
-//   2  its share of the down projections: Z[split][pair][d];
-//   3  its share of y: the weighted sum over a token's pairs.
+//   logits    one warp per (token, expert), as pairs of fp32 numbers (below);  grid barrier;
+//   routing   every block finds all tokens' experts for itself (the same order everywhere) and
+//             lists the (token, expert) pairs by expert;
+//   up        its share of the up projections: H[pair][f], pairs in the list's order;
+//   down      its share of the down projections: Z[split][pair][d], once every block's H is there;
+//   y         grid barrier; its share of y: the weighted sum over a token's pairs.
 //
-// The projections are mma.sync products with the weights as the 16-row operand: 16 weight rows
-// (GEGLU: 8 value rows and the 8 gate rows that belong to them) against the expert's tokens as
-// columns, 8 at a time.  Streaming weights is the whole cost, so they go from global memory
-// straight to the registers that the product reads, with no staging in between: lane (g, q) of
-// a warp loads 16 consecutive bytes of row g, and because a sum over k may take its terms in
-// any order, those 8 elements serve as the lane's k positions of two products as they are; the
-// tokens' operand is loaded with the same permutation.  The 8 warps of a block share a strip of
-// 16 rows, each taking every eighth 32 columns, four steps ahead in a register ring that runs
-// on across strips; their sums meet in shared memory in warp order.
+// The projections are tcgen05 products with the weights as the 128-row operand (GEGLU: 64 value
+// rows and the 64 gate rows that belong to them) and the tokens as the columns: all the tokens in
+// the up projection (an expert's own are picked when the sums are read), the expert's rows of H in
+// the down projection, once for H's 16-bit rounding and once for the remainder's.  The weights
+// come by TMA, 16 KB per stage of a ring that takes the rest of shared memory (100 to 180 KB in
+// flight per SM), issued by a thread that waits for nothing but free stages: it runs on from
+// the up into the down projections, so the memory is busy while the blocks wait for one another's
+// H.  A first form with mma.sync, whose warps took weights from global memory straight to
+// registers four steps ahead, spent its time on the tokens' operand and on strip ends: it read
+// 1.5 to 1.75 TB/s at every size (52 us for 1 of 8 x 1280 x 5120, 800 us for 64 tokens of 32).
 #include "kt_ops_internal.h"
 #include "kt_rows.cuh"
 
 namespace kt {
 namespace {
 
-constexpr int kMoeWarps = 8, kMoeThreads = kMoeWarps * 32;
-constexpr int kMoeRing = 4;             // steps of weights in flight per warp
-constexpr int kMoeStepK = kMoeWarps * 32;  // columns that the warps of a block take per step
+constexpr int kMoeWarps = 16, kMoeThreads = kMoeWarps * 32;
 constexpr int kMoePairs = KT_MOE_MAX_TOKENS * KT_MOE_MAX_TOP_K;
-constexpr int kMoeSplits = 8;           // most splits of a down projection along F
+constexpr int kMoeWeightBytes = 128 * 128;  // a stage's weights: 128 rows x 64 columns
+constexpr int kMoeMaxStages = 10;
+constexpr int kMoeEpiWarps = 4;             // warps 4-7
+constexpr uint32_t kMoeAccCols = 64;        // tensor-memory columns of one accumulator buffer
 
 // What every block knows after routing.
 struct MoeRoute {
     float weight[kMoePairs];           // of pair t * top_k + j
     short expert[kMoePairs];           // of pair t * top_k + j
     short list[kMoePairs];             // pairs in the order of their experts
+    short place[kMoePairs];            // where a pair stands in list
     short active[KT_MOE_MAX_EXPERTS];  // the experts that have pairs
     short start[KT_MOE_MAX_EXPERTS + 1];  // of each active expert's pairs in list
     short count[KT_MOE_MAX_EXPERTS];   // pairs per expert
     int n_active;
+    int splits, split_kblocks;         // of the down projections along F
 };
 
-__device__ __forceinline__ uint4 ld_weights(const uint16_t* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+// One thread waits until every block has arrived on `counter` (zero at the kernel's start).
+// Bounded: a wait that runs out, or another block's that did, records an error and returns false.
+__device__ __forceinline__ bool wait_blocks(const unsigned* counter, const MoeParams& p) {
+    const unsigned long long t0 = global_ns();
+    for (unsigned i = 1;; ++i) {
+        unsigned v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+        if (v >= gridDim.x) return true;
+        if ((i & 63u) == 0) {
+            if (*reinterpret_cast<volatile int*>(p.error) != 0) return false;
+            if (global_ns() - t0 > p.wait_limit_ns) {
+                atomicCAS(p.error, 0, DEV_TIMEOUT_PRODUCER);
+                return false;
+            }
+        }
+    }
 }
 
-template <int DT>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    if constexpr (DT == KT_BF16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Barrier over the grid: every block arrives once on `counter` (zero at the kernel's start) and
-// waits until all have.  Bounded: a wait that runs out, or another block's that did, records an
-// error and returns false in every thread of the block.
+// Barrier over the grid, for all threads of every block; false in all of them after a time-out.
 __device__ __forceinline__ bool grid_barrier(unsigned* counter, const MoeParams& p, int* ok_slot) {
     __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
         atomicAdd(counter, 1u);
-        bool ok = true;
-        const unsigned long long t0 = global_ns();
-        for (unsigned i = 1;; ++i) {
-            unsigned v;
-            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
-            if (v >= gridDim.x) break;
-            if ((i & 63u) == 0) {
-                if (*reinterpret_cast<volatile int*>(p.error) != 0) {
-                    ok = false;
-                    break;
-                }
-                if (global_ns() - t0 > p.wait_limit_ns) {
-                    atomicCAS(p.error, 0, DEV_TIMEOUT_PRODUCER);
-                    ok = false;
-                    break;
-                }
-            }
-        }
+        *ok_slot = wait_blocks(counter, p);
         __threadfence();
-        *ok_slot = ok;
     }
     __syncthreads();
     return *ok_slot != 0;
@@ -122,7 +103,7 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 }
 
 template <int DT>
-__device__ void moe_logits(const MoeParams& p) {
+__device__ __forceinline__ void moe_logits(const MoeParams& p) {
     const int lane = threadIdx.x & 31;
     const int warps = (int)gridDim.x * kMoeWarps;
     float2* logits = reinterpret_cast<float2*>(p.logits);
@@ -260,231 +241,330 @@ __device__ void moe_route(const MoeParams& p, MoeRoute& r) {
         for (int i = 0; i < pairs; i += 32) {
             const bool is = i + lane < pairs && r.expert[i + lane] == e;
             const uint32_t b = __ballot_sync(0xffffffffu, is);
-            if (is) r.list[at + __popc(b & ((1u << lane) - 1u))] = (short)(i + lane);
+            if (is) {
+                const int place = at + __popc(b & ((1u << lane) - 1u));
+                r.list[place] = (short)(i + lane);
+                r.place[i + lane] = (short)place;
+            }
             at += __popc(b);
         }
     }
     __syncthreads();
 }
 
-// One projection of all active experts: items (active expert, strip of 16 weight rows, split
-// along K), block b taking items b, b + grid, ...
-struct Projection {
-    const uint16_t* W;  // [E][rows][K]
-    int rows, K;        // weight rows per expert (UP with GEGLU: 2 F), columns
-    int strips, splits;
-    int split_k;        // columns of a split, a multiple of kMoeStepK
+// What the roles of a block share about the projections' items.  Up: (active expert, tile of 128
+// weight rows: 128 hidden columns, or 64 with their gates); down: (active expert, tile of 128
+// outputs, split along F).  Block b takes every gridDim-th up item from b on; the down items
+// start with the block after the last up item's, so that nobody gets both remainders.
+struct MoeItems {
+    int up_tiles, up_items, up_kblocks, down_tiles, down_items, first_down;
+    bool gated;
 };
-
-template <int DT, int NT, bool UP>
-__device__ void moe_project(const MoeParams& p, const MoeRoute& r, const Projection& q, int act, float* red) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
-    const bool gated = UP && act == KT_ACT_GEGLU;
-    const int items = r.n_active * q.strips * q.splits;
-    const int steps = q.split_k / kMoeStepK;
-    const int mine = items > (int)blockIdx.x ? (items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
-    const int total = mine * steps;
-    const int kofs = warp * 32 + t4 * 8;  // this lane's columns within a step
-
-    // where an item's rows are: the expert, the strip's first output, the split's first column
-    auto locate = [&](int item, int& a, int& f0, int& split) {
-        split = item % q.splits;
-        const int s = item / q.splits;
-        a = s / q.strips;
-        f0 = (s % q.strips) * (gated ? 8 : 16);
-    };
-    // load cursor
-    int l_item = (int)blockIdx.x, l_step = 0, l_k = 0, l_end = 0;
-    const uint16_t *row0 = nullptr, *row1 = nullptr;  // null: no such row
-    auto l_open = [&]() {
-        int a, f0, split;
-        locate(l_item, a, f0, split);
-        const int64_t e = r.active[a];
-        const int n0 = f0 + g, n1 = gated ? p.F + f0 + g : f0 + 8 + g;
-        const bool v0 = gated ? f0 + g < p.F : n0 < q.rows, v1 = gated ? v0 : n1 < q.rows;
-        row0 = v0 ? q.W + (e * q.rows + n0) * q.K : nullptr;
-        row1 = v1 ? q.W + (e * q.rows + n1) * q.K : nullptr;
-        l_k = split * q.split_k + kofs;
-        l_end = min(q.K, (split + 1) * q.split_k);
-    };
-    uint4 ring[kMoeRing][2];
-    auto load = [&](uint4 (&w)[2]) {
-        if (l_step == 0) l_open();
-        w[0] = w[1] = make_uint4(0u, 0u, 0u, 0u);
-        if (l_k < l_end) {
-            if (row0) w[0] = ld_weights(row0 + l_k);
-            if (row1) w[1] = ld_weights(row1 + l_k);
-        }
-        l_k += kMoeStepK;
-        if (++l_step == steps) {
-            l_step = 0;
-            l_item += (int)gridDim.x;
-        }
-    };
-    // product cursor
-    int item = (int)blockIdx.x, step = 0, a = 0, f0 = 0, split = 0, n = 0, nt = 0, k = 0, k_end = 0, buffer = 0;
-    const uint16_t* src[NT];  // the tokens' rows of this lane's column in each tile of 8; null: none
-    const int64_t lo_part = UP ? 0 : (int64_t)p.T * p.top_k * p.F;  // from H's first part to its second
-    float acc[NT][4];
-    auto open = [&]() {
-        locate(item, a, f0, split);
-        n = r.start[a + 1] - r.start[a];
-        nt = (n + 7) / 8;
-        k = split * q.split_k + kofs;
-        k_end = min(q.K, (split + 1) * q.split_k);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            src[j] = nullptr;
-            if (8 * j + g < n) {
-                const int pair = r.list[r.start[a] + 8 * j + g];
-                src[j] = UP ? static_cast<const uint16_t*>(p.X) + (int64_t)(pair / p.top_k) * p.ldx
-                            : p.H + (int64_t)pair * p.F;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-        }
-    };
-    auto multiply = [&](const uint4 (&w)[2]) {
-        if (step == 0) open();
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            if (j < nt) {
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                const bool in = src[j] != nullptr && k < k_end;
-                if (in) x = *reinterpret_cast<const uint4*>(src[j] + k);
-                mma16816<DT>(acc[j], w[0].x, w[1].x, w[0].y, w[1].y, x.x, x.y);
-                mma16816<DT>(acc[j], w[0].z, w[1].z, w[0].w, w[1].w, x.z, x.w);
-                if constexpr (!UP) {
-                    if (in) x = *reinterpret_cast<const uint4*>(src[j] + lo_part + k);
-                    mma16816<DT>(acc[j], w[0].x, w[1].x, w[0].y, w[1].y, x.x, x.y);
-                    mma16816<DT>(acc[j], w[0].z, w[1].z, w[0].w, w[1].w, x.z, x.w);
-                }
-            }
-        }
-        k += kMoeStepK;
-        if (++step < steps) return;
-        // the strip is complete: sums over the warps, in warp order, through shared memory (two
-        // buffers in turn, so one barrier per strip)
-        float* line = red + buffer * (kMoeWarps * NT * 128);
-        buffer ^= 1;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            if (j < nt) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) line[(warp * NT * 4 + j * 4 + i) * 32 + lane] = acc[j][i];
-            }
-        __syncthreads();
-        auto sum = [&](int slot, int ln) {
-            float v = 0.0f;
-#pragma unroll
-            for (int wi = 0; wi < kMoeWarps; ++wi) v += line[(wi * NT * 4 + slot) * 32 + ln];
-            return v;
-        };
-        // accumulator i of lane (g, t4): weight row g + 8 (i / 2), token column 2 t4 + i % 2
-        const int n_out = nt * (gated ? 64 : 128);
-        for (int o = threadIdx.x; o < n_out; o += kMoeThreads) {
-            const int ln = o & 31, i = gated ? (o >> 5) & 1 : (o >> 5) & 3, j = gated ? o >> 6 : o >> 7;
-            const int col = 8 * j + 2 * (ln & 3) + (i & 1), f = f0 + (ln >> 2) + (gated ? 0 : 8 * (i >> 1));
-            if (col >= n || f >= (gated ? p.F : q.rows)) continue;
-            const int pair = r.list[r.start[a] + col];
-            float v = sum(4 * j + i, ln);
-            if constexpr (UP) {
-                const int64_t e = r.active[a];
-                const uint16_t* b = static_cast<const uint16_t*>(p.b_up);
-                float bb[8];
-                if (b) {
-                    unpack8<DT>(make_uint4(b[e * q.rows + f], 0u, 0u, 0u), bb);
-                    v += bb[0];
-                }
-                f32x2 h = f2(v);
-                if (gated) {
-                    float gate = sum(4 * j + 2 + i, ln);
-                    if (b) {
-                        unpack8<DT>(make_uint4(b[e * q.rows + p.F + f], 0u, 0u, 0u), bb);
-                        gate += bb[0];
-                    }
-                    h = f2_mul<true>(h, gelu_erf_f2<true>(f2(gate)));
-                } else if (act == KT_ACT_GELU_ERF) {
-                    h = gelu_erf_f2<true>(h);
-                } else if (act == KT_ACT_GELU_TANH) {
-                    h = gelu_tanh_f2<true>(h);
-                } else if (act == KT_ACT_GELU_SIGMOID) {
-                    h = gelu_sigmoid_f2<true>(h);
-                } else if (act == KT_ACT_SILU) {
-                    h = silu_f2<true>(h);
-                }
-                // H in two 16-bit parts: its rounding, and the remainder's (none of an infinity)
-                const uint32_t hi = pack2<DT>(h.x, 0.0f) & 0xffffu;
-                float back[8];
-                unpack8<DT>(make_uint4(hi, 0u, 0u, 0u), back);
-                const float rest = fabsf(back[0]) < __uint_as_float(0x7f800000u) ? h.x - back[0] : 0.0f;
-                p.H[(int64_t)pair * p.F + f] = (uint16_t)hi;
-                p.H[(int64_t)(p.T * p.top_k + pair) * p.F + f] = (uint16_t)(pack2<DT>(rest, 0.0f) & 0xffffu);
-            } else {
-                p.Z[((int64_t)split * p.T * p.top_k + pair) * p.D + f] = v;
-            }
-        }
-        step = 0;
-        item += (int)gridDim.x;
-    };
-#pragma unroll
-    for (int u = 0; u < kMoeRing; ++u)
-        if (u < total) load(ring[u]);
-    for (int s = 0; s < total; s += kMoeRing) {
-#pragma unroll
-        for (int u = 0; u < kMoeRing; ++u) {
-            if (s + u < total) {
-                multiply(ring[u]);
-                if (s + u + kMoeRing < total) load(ring[u]);
-            }
-        }
+struct MoeItem {
+    int a, tile, kb0, kb1, split;
+};
+__device__ __forceinline__ MoeItems moe_items(const MoeParams& p, const MoeRoute& r, int act) {
+    MoeItems m;
+    m.gated = act == KT_ACT_GEGLU;
+    m.up_tiles = m.gated ? (p.F + 63) / 64 : (p.F + 127) / 128;
+    m.up_items = r.n_active * m.up_tiles;
+    m.up_kblocks = (p.D + 63) / 64;
+    m.down_tiles = (p.D + 127) / 128;
+    m.down_items = r.n_active * m.down_tiles * r.splits;
+    m.first_down = ((int)blockIdx.x + (int)gridDim.x - m.up_items % (int)gridDim.x) % (int)gridDim.x;
+    return m;
+}
+__device__ __forceinline__ MoeItem moe_item(const MoeParams& p, const MoeRoute& r, const MoeItems& m, bool up, int i) {
+    MoeItem it;
+    if (up) {
+        it.a = i / m.up_tiles;
+        it.tile = i % m.up_tiles;
+        it.split = 0;
+        it.kb0 = 0;
+        it.kb1 = m.up_kblocks;
+    } else {
+        it.split = i % r.splits;
+        const int t = i / r.splits;
+        it.a = t / m.down_tiles;
+        it.tile = t % m.down_tiles;
+        it.kb0 = it.split * r.split_kblocks;
+        it.kb1 = min((p.F + 63) / 64, it.kb0 + r.split_kblocks);
     }
+    return it;
 }
 
-template <int DT, int NT>
-__global__ void __launch_bounds__(kMoeThreads, 2) kt_moe_kernel(const MoeParams p, const int act) {
-    extern __shared__ float red[];  // [2][warps][NT * 4][32]
+struct MoeBars {
+    uint64_t full[kMoeMaxStages], empty[kMoeMaxStages], acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+    int abort, ok;
+};
+
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+    return r;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kMoeThreads, 1)
+    kt_moe_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_up,
+                  const __grid_constant__ CUtensorMap tm_down, const __grid_constant__ CUtensorMap tm_h, const MoeParams p,
+                  const int act, const int stages, const uint32_t stage_bytes, const uint32_t idesc0) {
+    extern __shared__ uint8_t raw[];
     __shared__ MoeRoute route;
-    __shared__ int ok;
+    __shared__ __align__(8) MoeBars bars;
+    const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
+    float* exchange = reinterpret_cast<float*>(raw + (ring - smem_u32(raw)) + (size_t)stages * stage_bytes);  // [T][64]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* abort_flag = &bars.abort;
+    auto bar = [](uint64_t& b) { return smem_u32(&b); };
     // a run that failed is not added to: kt_moe_status clears the word and the counters
-    if (threadIdx.x == 0) ok = *reinterpret_cast<volatile int*>(p.error) == 0;
+    if (threadIdx.x == 0) {
+        bars.ok = *reinterpret_cast<volatile int*>(p.error) == 0;
+        bars.abort = 0;
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(bar(bars.full[s]), 2);
+            mbar_init(bar(bars.empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar(bars.acc_full[b]), 1);
+            mbar_init(bar(bars.acc_empty[b]), kMoeEpiWarps);
+        }
+        mbar_init(bar(bars.drain), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+        prefetch_tmap(&tm_x);
+        prefetch_tmap(&tm_up);
+        prefetch_tmap(&tm_down);
+        prefetch_tmap(&tm_h);
+    }
     __syncthreads();
-    if (!ok) return;
+    if (!bars.ok) return;
 
     moe_logits<DT>(p);
-    if (!grid_barrier(p.barriers + 0, p, &ok)) return;
+    if (!grid_barrier(p.barriers + 0, p, &bars.ok)) return;
     moe_route(p, route);
-
-    Projection up;
-    up.W = static_cast<const uint16_t*>(p.W_up);
-    up.rows = p.F_up;
-    up.K = p.D;
-    up.strips = act == KT_ACT_GEGLU ? (p.F + 7) / 8 : (p.F + 15) / 16;
-    up.splits = 1;
-    up.split_k = (p.D + kMoeStepK - 1) / kMoeStepK * kMoeStepK;
-    moe_project<DT, NT, true>(p, route, up, act, red);
-    if (!grid_barrier(p.barriers + 1, p, &ok)) return;
-
-    Projection down;
-    down.W = static_cast<const uint16_t*>(p.W_down);
-    down.rows = p.D;
-    down.K = p.F;
-    down.strips = (p.D + 15) / 16;
-    // splits along F: the fewest step rounds over the grid, one more step counted per strip for
-    // its end
-    const int steps = (p.F + kMoeStepK - 1) / kMoeStepK, whole = route.n_active * down.strips;
-    int best = 0;
-    for (int s = 1; s <= moe_splits(p.T * p.top_k); ++s) {
-        const int cost = ((whole * s + (int)gridDim.x - 1) / (int)gridDim.x) * ((steps + s - 1) / s + 1);
-        if (s == 1 || cost < best) {
-            best = cost;
-            down.splits = s;
+    if (threadIdx.x == 0) {
+        // splits along F: the fewest k-blocks in a row on one block, two more counted per item for
+        // its start and end
+        const int kblocks = (p.F + 63) / 64, whole = route.n_active * ((p.D + 127) / 128), grid = (int)gridDim.x;
+        const int most = moe_splits(p.T * p.top_k);
+        int best = 0;
+        for (int s = 1; s <= most && s <= kblocks; ++s) {
+            const int per = (kblocks + s - 1) / s, n = (kblocks + per - 1) / per;
+            const int cost = ((whole * n + grid - 1) / grid) * (per + 2);
+            if (s == 1 || cost < best) {
+                best = cost;
+                route.splits = n;
+                route.split_kblocks = per;
+            }
         }
     }
-    down.split_k = (steps + down.splits - 1) / down.splits * kMoeStepK;
-    down.splits = (steps * kMoeStepK + down.split_k - 1) / down.split_k;
-    moe_project<DT, NT, false>(p, route, down, act, red);
-    if (!grid_barrier(p.barriers + 2, p, &ok)) return;
+    if (warp == 1) tmem_alloc<1>(smem_u32(&bars.tmem), 2 * kMoeAccCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem;
+    const MoeItems m = moe_items(p, route, act);
+    const int grid = (int)gridDim.x;
+    const uint32_t up_cols = (uint32_t)(p.T + 15) / 16 * 16;  // a product has a multiple of 16 columns
+
+    if ((warp == 0 || warp == 2) && lane == 0) {
+        // ------------------ producers: weights (warp 0), tokens (warp 2) ------------------
+        const bool weights = warp == 0;
+        uint32_t stage = 0, phase = 0, armed = 0, armed_phase = 0;
+        bool ok = true;
+        for (int ph = 0; ph < 2 && ok; ++ph) {
+            const bool up = ph == 0;
+            if (!up && !weights) {
+                ok = wait_blocks(p.barriers + 1, p);
+                if (!ok) *abort_flag = 1;
+                asm volatile("fence.proxy.async;" ::: "memory");  // H was stored by other threads; TMA reads it
+            }
+            const int n_items = up ? m.up_items : m.down_items;
+            for (int i = up ? (int)blockIdx.x : m.first_down; i < n_items && ok; i += grid) {
+                const MoeItem it = moe_item(p, route, m, up, i);
+                const int e = route.active[it.a], start = route.start[it.a], n = route.start[it.a + 1] - start;
+                const int boxes = up ? (p.T + 7) / 8 : (n + 7) / 8;
+                // rows of the weights' two boxes of 64
+                const int row0 = up ? e * p.F_up + it.tile * (m.gated ? 64 : 128) : e * p.D + it.tile * 128;
+                const int row1 = up && m.gated ? row0 + p.F : row0 + 64;
+                for (int kb = it.kb0; kb < it.kb1 && ok; ++kb) {
+                    ok = wait_phase(bar(bars.empty[stage]), phase ^ 1u, abort_flag, p.error, DEV_TIMEOUT_PRODUCER, p.wait_limit_ns);
+                    if (!ok) break;
+                    const uint32_t full = bar(bars.full[stage]), dst = ring + stage * stage_bytes;
+                    if (weights) {
+                        mbar_arrive_expect_tx(full, kMoeWeightBytes);
+                        const CUtensorMap* tm = up ? &tm_up : &tm_down;
+                        tma_load_2d(dst, tm, full, kb * 64, row0);
+                        tma_load_2d(dst + 8192u, tm, full, kb * 64, row1);
+                    } else if (up) {
+                        mbar_arrive_expect_tx(full, (uint32_t)boxes * 1024u);
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_2d(dst + kMoeWeightBytes + 1024u * b, &tm_x, full, kb * 64, 8 * b);
+                    } else {
+                        const uint32_t lo = dst + kMoeWeightBytes + (uint32_t)(n + 15) / 16 * 2048u;
+                        mbar_arrive_expect_tx(full, (uint32_t)boxes * 2048u);
+                        for (int b = 0; b < boxes; ++b) {
+                            tma_load_2d(dst + kMoeWeightBytes + 1024u * b, &tm_h, full, kb * 64, start + 8 * b);
+                            tma_load_2d(lo + 1024u * b, &tm_h, full, kb * 64, p.T * p.top_k + start + 8 * b);
+                        }
+                    }
+                    armed |= 1u << stage;
+                    armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+                    if (++stage == (uint32_t)stages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+        if (*abort_flag) {  // no copy may still be landing in shared memory that is about to be released
+            for (int s = 0; s < stages; ++s)
+                if (armed & (1u << s)) wait_drain(bar(bars.full[s]), (armed_phase >> s) & 1u, 100000000ull);
+        }
+    } else if (warp == 1 && lane == 0) {
+        // ------------------ one thread issues the products ------------------
+        uint32_t stage = 0, phase = 0, t = 0;
+        bool ok = true;
+        for (int ph = 0; ph < 2 && ok; ++ph) {
+            const bool up = ph == 0;
+            const int n_items = up ? m.up_items : m.down_items;
+            for (int i = up ? (int)blockIdx.x : m.first_down; i < n_items && ok; i += grid, ++t) {
+                const MoeItem it = moe_item(p, route, m, up, i);
+                const uint32_t cols = up ? up_cols : (uint32_t)(route.start[it.a + 1] - route.start[it.a] + 15) / 16 * 16;
+                const uint32_t idesc = idesc0 | ((cols >> 3) << 17), buf = t & 1u, d = tmem + buf * kMoeAccCols;
+                ok = wait_phase(bar(bars.acc_empty[buf]), ((t >> 1) & 1u) ^ 1u, abort_flag, p.error, DEV_TIMEOUT_MMA, p.wait_limit_ns);
+                tc_fence_after();
+                for (int kb = it.kb0; kb < it.kb1 && ok; ++kb) {
+                    ok = wait_phase(bar(bars.full[stage]), phase, abort_flag, p.error, DEV_TIMEOUT_MMA, p.wait_limit_ns);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t base = ring + stage * stage_bytes;
+                    const uint64_t ad = smem_desc(base, 16u, 1024u), bd = smem_desc(base + kMoeWeightBytes, 16u, 1024u);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_f16(d, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), idesc, kb > it.kb0 || k > 0);
+                    if (!up) {
+                        const uint64_t ld = smem_desc(base + kMoeWeightBytes + cols * 128u, 16u, 1024u);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mma_f16(d, ad + (uint64_t)(2 * k), ld + (uint64_t)(2 * k), idesc, 1u);
+                    }
+                    mma_commit(bar(bars.empty[stage]));
+                    if (++stage == (uint32_t)stages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok) mma_commit(bar(bars.acc_full[buf]));
+            }
+        }
+        if (!ok) {  // no product may still be running when tensor memory is freed
+            mma_commit(bar(bars.drain));
+            wait_drain(bar(bars.drain), 0u, 100000000ull);
+        }
+    } else if (warp >= 4 && warp < 4 + kMoeEpiWarps) {
+        // ------------------ epilogue: lane = weight row ------------------
+        const int q = warp & 3;
+        const uint32_t lanes = (uint32_t)(q * 32) << 16;
+        uint32_t t = 0;
+        bool live = true;
+        for (int ph = 0; ph < 2 && live; ++ph) {
+            const bool up = ph == 0;
+            const int n_items = up ? m.up_items : m.down_items;
+            for (int i = up ? (int)blockIdx.x : m.first_down; i < n_items; i += grid, ++t) {
+                const MoeItem it = moe_item(p, route, m, up, i);
+                const int64_t e = route.active[it.a];
+                const int start = route.start[it.a], n = route.start[it.a + 1] - start;
+                const uint32_t buf = t & 1u, d = tmem + lanes + buf * kMoeAccCols;
+                const bool gate = up && m.gated && q >= 2;  // these rows are gates: value rows' lanes take them over
+                const int f = up ? (m.gated ? it.tile * 64 + 32 * (q & 1) : it.tile * 128 + 32 * q) + lane : it.tile * 128 + 32 * q + lane;
+                const bool in = f < (up ? p.F : p.D);
+                float bias = 0.0f;
+                if (up && p.b_up && in) {
+                    float b[8];
+                    unpack8<DT>(make_uint4(static_cast<const uint16_t*>(p.b_up)[e * p.F_up + (gate ? p.F : 0) + f], 0u, 0u, 0u), b);
+                    bias = b[0];
+                }
+                const bool got = wait_phase(bar(bars.acc_full[buf]), (t >> 1) & 1u, abort_flag, p.error, DEV_TIMEOUT_EPILOGUE, p.wait_limit_ns);
+                if (!epi_all<kMoeEpiWarps>(got)) {
+                    live = false;
+                    break;
+                }
+                tc_fence_after();
+                auto column = [&](int c) { return up ? (uint32_t)(route.list[start + c] / p.top_k) : (uint32_t)c; };
+                if (gate) {
+                    for (int c0 = 0; c0 < n; c0 += 8) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) v[c] = tmem_ld1(d + column(min(c0 + c, n - 1)));
+                        tmem_wait_ld_only();
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            asm volatile("" : "+r"(v[c])::"memory");
+                            if (c0 + c < n) exchange[(c0 + c) * 64 + 32 * (q & 1) + lane] = __uint_as_float(v[c]) + bias;
+                        }
+                    }
+                }
+                if (up && m.gated) epi_bar_sync<kMoeEpiWarps>();
+                if (!gate) {
+                    for (int c0 = 0; c0 < n; c0 += 8) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) v[c] = tmem_ld1(d + column(min(c0 + c, n - 1)));
+                        tmem_wait_ld_only();
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            asm volatile("" : "+r"(v[c])::"memory");
+                            if (c0 + c >= n || !in) continue;
+                            const int64_t at = start + c0 + c;
+                            float z = __uint_as_float(v[c]);
+                            if (!up) {
+                                p.Z[((int64_t)it.split * p.T * p.top_k + at) * p.D + f] = z;
+                                continue;
+                            }
+                            f32x2 h = f2(z + bias);
+                            if (m.gated) h = f2_mul<true>(h, gelu_erf_f2<true>(f2(exchange[(c0 + c) * 64 + 32 * (q & 1) + lane])));
+                            else if (act == KT_ACT_GELU_ERF) h = gelu_erf_f2<true>(h);
+                            else if (act == KT_ACT_GELU_TANH) h = gelu_tanh_f2<true>(h);
+                            else if (act == KT_ACT_GELU_SIGMOID) h = gelu_sigmoid_f2<true>(h);
+                            else if (act == KT_ACT_SILU) h = silu_f2<true>(h);
+                            // H in two 16-bit parts: its rounding, and the remainder's (none of an infinity)
+                            const uint32_t hi = pack2<DT>(h.x, 0.0f) & 0xffffu;
+                            float back[8];
+                            unpack8<DT>(make_uint4(hi, 0u, 0u, 0u), back);
+                            const float rest = fabsf(back[0]) < __uint_as_float(0x7f800000u) ? h.x - back[0] : 0.0f;
+                            p.H[at * p.F + f] = (uint16_t)hi;
+                            p.H[((int64_t)p.T * p.top_k + at) * p.F + f] = (uint16_t)(pack2<DT>(rest, 0.0f) & 0xffffu);
+                        }
+                    }
+                }
+                tc_fence_before();
+                if (up && m.gated) epi_bar_sync<kMoeEpiWarps>();  // the gates have been read
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(bars.acc_empty[buf]));
+            }
+            if (up && live) {
+                // this block's part of H is stored: for the TMA reads of other blocks too
+                __threadfence();
+                asm volatile("fence.proxy.async;" ::: "memory");
+                epi_bar_sync<kMoeEpiWarps>();
+                if (warp == 4 && lane == 0) {
+                    __threadfence();
+                    atomicAdd(p.barriers + 1, 1u);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc<1>(tmem, 2 * kMoeAccCols);
+    }
+    if (*abort_flag) return;
+    if (!grid_barrier(p.barriers + 2, p, &bars.ok)) return;
 
     // y: a thread per 4 columns of a token
     const int quads = p.D / 4;
@@ -494,8 +574,8 @@ __global__ void __launch_bounds__(kMoeThreads, 2) kt_moe_kernel(const MoeParams 
         for (int j = 0; j < p.top_k; ++j) {
             const int pair = t * p.top_k + j;
             float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            for (int s = 0; s < down.splits; ++s) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(p.Z + ((int64_t)s * p.T * p.top_k + pair) * p.D + d));
+            for (int s = 0; s < route.splits; ++s) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(p.Z + ((int64_t)s * p.T * p.top_k + route.place[pair]) * p.D + d));
                 z[0] += v.x;
                 z[1] += v.y;
                 z[2] += v.z;
@@ -533,26 +613,35 @@ __global__ void __launch_bounds__(kMoeThreads, 2) kt_moe_kernel(const MoeParams 
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-template <int DT, int NT>
+template <int DT>
 kt_status launch_moe_t(int act, const MoeParams& p, int sms, void* stream, const char** why) {
-    auto kern = kt_moe_kernel<DT, NT>;
-    constexpr int smem = 2 * kMoeWarps * NT * 128 * (int)sizeof(float);
+    auto kern = kt_moe_kernel<DT>;
+    const int cols = (p.T + 15) / 16 * 16;
+    const uint32_t stage = kMoeWeightBytes + 2u * (uint32_t)cols * 128u;
+    const int fixed = 1024 + p.T * 64 * (int)sizeof(float);
+    const int room = kSmemBudget - (int)sizeof(MoeRoute) - (int)sizeof(MoeBars) - 64;
+    const int stages = std::min(kMoeMaxStages, (room - fixed) / (int)stage);
+    const int smem = fixed + stages * (int)stage;
+    alignas(64) CUtensorMap tx, tu, td, th;
+    const uint64_t pairs = (uint64_t)p.T * p.top_k;
+    if (!encode_tmap_pitch(&tx, p.X, DT, p.T, p.D, p.ldx, 8, 64, 128, why) ||
+        !encode_tmap_pitch(&tu, p.W_up, DT, (uint64_t)p.E * p.F_up, p.D, p.D, 64, 64, 128, why) ||
+        !encode_tmap_pitch(&td, p.W_down, DT, (uint64_t)p.E * p.D, p.F, p.F, 64, 64, 128, why) ||
+        !encode_tmap_pitch(&th, p.H, DT, 2 * pairs, p.F, p.F, 8, 64, 128, why))
+        return KT_ERR_CUDA;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    int per_sm = 0;
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kMoeThreads, smem);
-    if (e == cudaSuccess && per_sm < 1) e = cudaErrorLaunchOutOfResources;
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(sms * std::min(per_sm, 2)), 1, 1);
+        cfg.gridDim = dim3((unsigned)sms, 1, 1);
         cfg.blockDim = dim3(kMoeThreads, 1, 1);
-        cfg.dynamicSmemBytes = smem;
+        cfg.dynamicSmemBytes = (size_t)smem;
         cfg.stream = static_cast<cudaStream_t>(stream);
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeCooperative;  // all blocks resident: they wait for one another
         attr[0].val.cooperative = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, kern, p, act);
+        e = cudaLaunchKernelEx(&cfg, kern, tx, tu, td, th, p, act, stages, stage, make_idesc(DT, 0, 128, 1));
     }
     if (e != cudaSuccess) {
         *why = cudaGetErrorString(e);
@@ -583,15 +672,7 @@ void moe_carve(MoeParams* p, int64_t max_tokens, void* workspace) {
 }
 
 kt_status launch_moe(int act, int dtype, const MoeParams& p, int sms, void* stream, const char** why) {
-    // as many 8-token tiles as an expert can get
-    if (dtype == KT_BF16) {
-        if (p.T <= 8) return launch_moe_t<KT_BF16, 1>(act, p, sms, stream, why);
-        if (p.T <= 16) return launch_moe_t<KT_BF16, 2>(act, p, sms, stream, why);
-        return launch_moe_t<KT_BF16, 8>(act, p, sms, stream, why);
-    }
-    if (p.T <= 8) return launch_moe_t<KT_F16, 1>(act, p, sms, stream, why);
-    if (p.T <= 16) return launch_moe_t<KT_F16, 2>(act, p, sms, stream, why);
-    return launch_moe_t<KT_F16, 8>(act, p, sms, stream, why);
+    return dtype == KT_BF16 ? launch_moe_t<KT_BF16>(act, p, sms, stream, why) : launch_moe_t<KT_F16>(act, p, sms, stream, why);
 }
 
 }  // namespace kt

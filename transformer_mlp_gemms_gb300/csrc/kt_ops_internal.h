@@ -72,9 +72,11 @@ struct MoeParams {
     int* error;          // device error word
     unsigned long long wait_limit_ns;
 };
-// Splits of the down projection along F that there is room for: up to 8 while pairs are few.
-KT_HOST_DEVICE inline size_t moe_z_rows(size_t pairs) { return pairs >= 256 ? pairs : pairs * 8 < 256 ? pairs * 8 : 256; }
-KT_HOST_DEVICE inline int moe_splits(int pairs) { return pairs >= 256 ? 1 : pairs * 8 < 256 ? 8 : 256 / pairs; }
+// Splits of the down projection along F that there is room for: up to 32 while pairs are few.
+KT_HOST_DEVICE inline int moe_splits(int pairs) { return pairs >= 1024 ? 1 : pairs * 32 < 1024 ? 32 : 1024 / pairs; }
+inline size_t moe_z_rows(int max_pairs) {  // for any number of pairs up to max_pairs
+    return max_pairs >= 1024 ? max_pairs : max_pairs * 32 < 1024 ? max_pairs * 32 : 1024;
+}
 size_t moe_workspace(int64_t T, int64_t D, int64_t F, int64_t E, int64_t top_k);
 void moe_carve(MoeParams* p, int64_t max_tokens, void* workspace);
 kt_status launch_moe(int act, int dtype, const MoeParams& p, int sms, void* stream, const char** why);
