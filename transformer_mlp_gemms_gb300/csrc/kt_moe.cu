@@ -34,6 +34,10 @@ constexpr int kMoeWarps = 16, kMoeThreads = kMoeWarps * 32;
 constexpr int kMoePairs = KT_MOE_MAX_TOKENS * KT_MOE_MAX_TOP_K;
 constexpr int kMoeWeightBytes = 128 * 128;  // a stage's weights: 128 rows x 64 columns
 constexpr int kMoeMaxStages = 10;
+#ifndef BURST
+#define BURST 4
+#endif
+constexpr int kMoeBurst = BURST;
 constexpr int kMoeEpiWarps = 4;             // warps 4-7
 constexpr uint32_t kMoeAccCols = 64;        // tensor-memory columns of one accumulator buffer
 
@@ -46,18 +50,19 @@ struct MoeRoute {
     short active[KT_MOE_MAX_EXPERTS];  // the experts that have pairs
     short start[KT_MOE_MAX_EXPERTS + 1];  // of each active expert's pairs in list
     short count[KT_MOE_MAX_EXPERTS];   // pairs per expert
+    float2 logits[KT_MOE_MAX_EXPERTS]; // scratch of the choices
     int n_active;
     int splits, split_kblocks;         // of the down projections along F
 };
 
-// One thread waits until every block has arrived on `counter` (zero at the kernel's start).
+// One thread waits until `blocks` blocks have arrived on `counter` (zero at the kernel's start).
 // Bounded: a wait that runs out, or another block's that did, records an error and returns false.
-__device__ __forceinline__ bool wait_blocks(const unsigned* counter, const MoeParams& p) {
+__device__ __forceinline__ bool wait_blocks(const unsigned* counter, unsigned blocks, const MoeParams& p) {
     const unsigned long long t0 = global_ns();
     for (unsigned i = 1;; ++i) {
         unsigned v;
         asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
-        if (v >= gridDim.x) return true;
+        if (v >= blocks) return true;
         if ((i & 63u) == 0) {
             if (*reinterpret_cast<volatile int*>(p.error) != 0) return false;
             if (global_ns() - t0 > p.wait_limit_ns) {
@@ -74,7 +79,7 @@ __device__ __forceinline__ bool grid_barrier(unsigned* counter, const MoeParams&
     if (threadIdx.x == 0) {
         __threadfence();
         atomicAdd(counter, 1u);
-        *ok_slot = wait_blocks(counter, p);
+        *ok_slot = wait_blocks(counter, gridDim.x, p);
         __threadfence();
     }
     __syncthreads();
@@ -102,108 +107,160 @@ __device__ __forceinline__ uint32_t order_key(float f) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// One logit, by a warp; the result in every lane.
 template <int DT>
-__device__ __forceinline__ void moe_logits(const MoeParams& p) {
+__device__ __forceinline__ float2 moe_logit(const MoeParams& p, int t, int e) {
     const int lane = threadIdx.x & 31;
-    const int warps = (int)gridDim.x * kMoeWarps;
-    float2* logits = reinterpret_cast<float2*>(p.logits);
-    for (int i = (int)blockIdx.x * kMoeWarps + (threadIdx.x >> 5); i < p.T * p.E; i += warps) {
-        const int t = i / p.E, e = i % p.E;
-        const uint16_t* x = static_cast<const uint16_t*>(p.X) + (int64_t)t * p.ldx;
-        const uint16_t* w = static_cast<const uint16_t*>(p.W_router) + (int64_t)e * p.D;
-        Pair s = {0.0f, 0.0f};
-        for (int k = lane * 8; k < p.D; k += 256) {
-            float a[8], b[8];
-            unpack8<DT>(*reinterpret_cast<const uint4*>(x + k), a);
-            unpack8<DT>(*reinterpret_cast<const uint4*>(w + k), b);
+    const uint16_t* x = static_cast<const uint16_t*>(p.X) + (int64_t)t * p.ldx;
+    const uint16_t* w = static_cast<const uint16_t*>(p.W_router) + (int64_t)e * p.D;
+    Pair s = {0.0f, 0.0f};
+#pragma unroll 4
+    for (int k = lane * 8; k < p.D; k += 256) {
+        float a[8], b[8];
+        unpack8<DT>(*reinterpret_cast<const uint4*>(x + k), a);
+        unpack8<DT>(*reinterpret_cast<const uint4*>(w + k), b);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) pair_add(s, __fmul_rn(a[j], b[j]), 0.0f);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            pair_add(s, __shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o));
-        if (lane == 0) {
-            // hi alone where the sum is not finite (lo is then no number)
-            const float hi = __fadd_rn(s.hi, s.lo);
-            const bool finite = fabsf(s.hi) < __uint_as_float(0x7f800000u);
-            logits[i] = finite ? make_float2(hi, __fadd_rn(s.lo, __fsub_rn(s.hi, hi))) : make_float2(s.hi, 0.0f);
-        }
+        for (int j = 0; j < 8; ++j) pair_add(s, __fmul_rn(a[j], b[j]), 0.0f);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        pair_add(s, __shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o));
+    // hi alone where the sum is not finite (lo is then no number)
+    const float hi = __fadd_rn(s.hi, s.lo);
+    const bool finite = fabsf(s.hi) < __uint_as_float(0x7f800000u);
+    return finite ? make_float2(hi, __fadd_rn(s.lo, __fsub_rn(s.hi, hi))) : make_float2(s.hi, 0.0f);
 }
 
-// Every token's experts and weights, then the pairs by expert.
-__device__ void moe_route(const MoeParams& p, MoeRoute& r) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const float2* logits = reinterpret_cast<const float2*>(p.logits);
-    const int k = p.top_k, E = p.E, pairs = p.T * k;
+// One token's experts and their weights from its logits, by a warp: lane j < top_k returns the
+// j-th choice.
+__device__ __forceinline__ void moe_choose(const float2* logits, const MoeParams& p, int& expert, float& weight) {
+    const int lane = threadIdx.x & 31, E = p.E, n = (E + 31) / 32;
     constexpr int per = KT_MOE_MAX_EXPERTS / 32;
-    for (int t = warp; t < p.T; t += kMoeWarps) {
-        float2 v[per];
-        uint32_t used = 0;  // this lane's experts e = 32 i + lane that are taken or not there
-        bool nan = false;
+    float2 v[per];
+    uint32_t h[per], l[per], used = 0;  // used: this lane's experts e = 32 i + lane that are taken or not there
+    bool nan = false;
 #pragma unroll
-        for (int i = 0; i < per; ++i) {
-            const int e = 32 * i + lane;
-            v[i] = make_float2(0.0f, 0.0f);
-            if (e < E)
-                v[i] = __ldcg(&logits[t * E + e]);
-            else
-                used |= 1u << i;
+    for (int i = 0; i < per; ++i) {
+        const int e = 32 * i + lane;
+        v[i] = make_float2(0.0f, 0.0f);
+        if (i < n) {
+            if (e < E) v[i] = logits[e];
             nan |= v[i].x != v[i].x;
         }
-        nan = __any_sync(0xffffffffu, nan);
-        float2 top = make_float2(0.0f, 0.0f);
-        float total = 0.0f, mine = 0.0f;  // lane j keeps the j-th choice's term
-        for (int j = 0; j < k; ++j) {
-            uint32_t bh = 0, bl = 0, bi = 0xffffffffu;
+        if (e >= E) used |= 1u << i;
+        h[i] = order_key(v[i].x);
+        l[i] = order_key(v[i].y);
+    }
+    nan = __any_sync(0xffffffffu, nan);
+    float2 top = make_float2(0.0f, 0.0f);
+    float total = 0.0f, mine = 0.0f;
+    expert = 0;
+    for (int j = 0; j < p.top_k; ++j) {
+        uint32_t bh = 0, bl = 0, bi = 0xffffffffu;
+        float2 bv = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < per; ++i) {
-                const uint32_t h = order_key(v[i].x), l = order_key(v[i].y);
-                const bool better = bi == 0xffffffffu || h > bh || (h == bh && l > bl);
-                if (!((used >> i) & 1u) && better) {
-                    bh = h;
-                    bl = l;
-                    bi = (uint32_t)(32 * i + lane);
-                }
-            }
-            const bool any = bi != 0xffffffffu;
-            const uint32_t mh = __reduce_max_sync(0xffffffffu, any ? bh : 0u);
-            const uint32_t ml = __reduce_max_sync(0xffffffffu, any && bh == mh ? bl : 0u);
-            const uint32_t e = __reduce_min_sync(0xffffffffu, any && bh == mh && bl == ml ? bi : 0xffffffffu);
-            float2 chosen = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < per; ++i)
-                if (32 * i + lane == (int)e) {
-                    chosen = v[i];
-                    used |= 1u << i;
-                }
-            chosen.x = __shfl_sync(0xffffffffu, chosen.x, e & 31u);
-            chosen.y = __shfl_sync(0xffffffffu, chosen.y, e & 31u);
-            if (j == 0) top = chosen;
-            const float term = expf((chosen.x - top.x) + (chosen.y - top.y));
-            total += term;
-            if (lane == j) {
-                mine = term;
-                r.expert[t * k + j] = (short)e;
+        for (int i = 0; i < per; ++i) {
+            if (i < n && !((used >> i) & 1u) && (bi == 0xffffffffu || h[i] > bh || (h[i] == bh && l[i] > bl))) {
+                bh = h[i];
+                bl = l[i];
+                bi = (uint32_t)(32 * i + lane);
+                bv = v[i];
             }
         }
-        if (!p.normalize) {
-            total = 0.0f;
-#pragma unroll
-            for (int i = 0; i < per; ++i)
-                if (32 * i + lane < E) total += expf((v[i].x - top.x) + (v[i].y - top.y));
-            total = warp_add(total);
-        }
-        if (lane < k) {
-            const float w = nan ? __uint_as_float(0x7fffffffu) : mine / total;
-            r.weight[t * k + lane] = w;
-            if (blockIdx.x == 0) {
-                if (p.weights) p.weights[t * k + lane] = w;
-                if (p.ids) p.ids[t * k + lane] = r.expert[t * k + lane];
-            }
+        const bool any = bi != 0xffffffffu;
+        const uint32_t mh = __reduce_max_sync(0xffffffffu, any ? bh : 0u);
+        const uint32_t ml = __reduce_max_sync(0xffffffffu, any && bh == mh ? bl : 0u);
+        const uint32_t e = __reduce_min_sync(0xffffffffu, any && bh == mh && bl == ml ? bi : 0xffffffffu);
+        if (bi == e) used |= 1u << (e >> 5);
+        const float2 chosen = make_float2(__shfl_sync(0xffffffffu, bv.x, e & 31u), __shfl_sync(0xffffffffu, bv.y, e & 31u));
+        if (j == 0) top = chosen;
+        const float term = expf((chosen.x - top.x) + (chosen.y - top.y));
+        total += term;
+        if (lane == j) {
+            mine = term;
+            expert = (int)e;
         }
     }
+    if (!p.normalize) {
+        total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < per; ++i)
+            if (i < n && 32 * i + lane < E) total += expf((v[i].x - top.x) + (v[i].y - top.y));
+        total = warp_add(total);
+    }
+    weight = nan ? __uint_as_float(0x7fffffffu) : mine / total;
+}
+
+// Logits and choices.  Few of them (up to two logits a warp): every block computes them all and
+// nobody waits.  Else each token belongs to one block, which writes its choices to the workspace
+// and arrives at the first grid barrier, and all blocks read them.  (With the logits spread over
+// all warps of the grid and every block choosing for all tokens, 64 tokens of 32 experts took 20
+// us to get here, 13 of them for the choices.)
+template <int DT>
+__device__ bool moe_choices(const MoeParams& p, MoeRoute& r, int* ok_slot) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = p.top_k;
+    const auto publish = [&](int t, int e, float w) {
+        if (lane < k) {
+            if (p.weights) p.weights[t * k + lane] = w;
+            if (p.ids) p.ids[t * k + lane] = e;
+        }
+    };
+    float2* logits = r.logits;
+    int e;
+    float w;
+    if (p.T * p.E <= 2 * kMoeWarps) {
+        for (int i = warp; i < p.T * p.E; i += kMoeWarps) {
+            const float2 v = moe_logit<DT>(p, i / p.E, i % p.E);
+            if (lane == 0) logits[i] = v;
+        }
+        __syncthreads();
+        for (int t = warp; t < p.T; t += kMoeWarps) {
+            moe_choose(logits + t * p.E, p, e, w);
+            if (lane < k) {
+                r.expert[t * k + lane] = (short)e;
+                r.weight[t * k + lane] = w;
+            }
+            if (blockIdx.x == 0) publish(t, e, w);
+        }
+        __syncthreads();
+        return true;
+    }
+    bool any = false;
+    for (int t = (int)blockIdx.x; t < p.T; t += (int)gridDim.x) {
+        any = true;
+        for (int i = warp; i < p.E; i += kMoeWarps) {
+            const float2 v = moe_logit<DT>(p, t, i);
+            if (lane == 0) logits[i] = v;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            moe_choose(logits, p, e, w);
+            if (lane < k) p.choices[t * k + lane] = make_float2(__int_as_float(e), w);
+            publish(t, e, w);
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        if (any) {
+            __threadfence();
+            atomicAdd(p.barriers + 0, 1u);
+        }
+        *ok_slot = wait_blocks(p.barriers + 0, (unsigned)min(p.T, (int)gridDim.x), p);
+        __threadfence();
+    }
     __syncthreads();
+    for (int i = threadIdx.x; i < p.T * k; i += kMoeThreads) {
+        const float2 c = __ldcg(p.choices + i);
+        r.expert[i] = (short)__float_as_int(c.x);
+        r.weight[i] = c.y;
+    }
+    __syncthreads();
+    return *ok_slot != 0;
+}
+
+// The pairs by expert.
+__device__ void moe_route(const MoeParams& p, MoeRoute& r) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = p.E, pairs = p.T * p.top_k;
     for (int e = warp; e < E; e += kMoeWarps) {
         int n = 0;
         for (int i = 0; i < pairs; i += 32) n += __popc(__ballot_sync(0xffffffffu, i + lane < pairs && r.expert[i + lane] == e));
@@ -296,7 +353,7 @@ __device__ __forceinline__ MoeItem moe_item(const MoeParams& p, const MoeRoute& 
 struct MoeBars {
     uint64_t full[kMoeMaxStages], empty[kMoeMaxStages], acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
-    int abort, ok;
+    int abort, ok, failed;
 };
 
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
@@ -319,8 +376,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     volatile int* abort_flag = &bars.abort;
     auto bar = [](uint64_t& b) { return smem_u32(&b); };
     // a run that failed is not added to: kt_moe_status clears the word and the counters
+    if (warp == kMoeWarps - 1 && lane == 0) bars.failed = *reinterpret_cast<volatile int*>(p.error);
     if (threadIdx.x == 0) {
-        bars.ok = *reinterpret_cast<volatile int*>(p.error) == 0;
+        bars.ok = 1;
         bars.abort = 0;
         for (int s = 0; s < stages; ++s) {
             mbar_init(bar(bars.full[s]), 2);
@@ -338,26 +396,21 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         prefetch_tmap(&tm_down);
         prefetch_tmap(&tm_h);
     }
-    __syncthreads();
-    if (!bars.ok) return;
-
-    moe_logits<DT>(p);
-    if (!grid_barrier(p.barriers + 0, p, &bars.ok)) return;
+    const bool ready = moe_choices<DT>(p, route, &bars.ok);
+    if (!ready || bars.failed) return;  // (both the same in every thread: the choices end with a barrier)
     moe_route(p, route);
-    if (threadIdx.x == 0) {
-        // splits along F: the fewest k-blocks in a row on one block, two more counted per item for
-        // its start and end
+    if (warp == 0) {
+        // splits of the down projections along F, a lane for each count: the fewest k-blocks in a
+        // row on one block, two more counted per item for its start and end
         const int kblocks = (p.F + 63) / 64, whole = route.n_active * ((p.D + 127) / 128), grid = (int)gridDim.x;
-        const int most = moe_splits(p.T * p.top_k);
-        int best = 0;
-        for (int s = 1; s <= most && s <= kblocks; ++s) {
-            const int per = (kblocks + s - 1) / s, n = (kblocks + per - 1) / per;
-            const int cost = ((whole * n + grid - 1) / grid) * (per + 2);
-            if (s == 1 || cost < best) {
-                best = cost;
-                route.splits = n;
-                route.split_kblocks = per;
-            }
+        const int s = min(lane + 1, min(moe_splits(p.T * p.top_k), kblocks));
+        const int per = (kblocks + s - 1) / s, n = (kblocks + per - 1) / per;
+        const unsigned cost = (unsigned)(((whole * n + grid - 1) / grid) * (per + 2));
+        const unsigned best = __reduce_min_sync(0xffffffffu, cost);
+        const uint32_t who = __ballot_sync(0xffffffffu, cost == best);
+        if (lane == __ffs(who) - 1) {
+            route.splits = n;
+            route.split_kblocks = per;
         }
     }
     if (warp == 1) tmem_alloc<1>(smem_u32(&bars.tmem), 2 * kMoeAccCols);
@@ -377,7 +430,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         for (int ph = 0; ph < 2 && ok; ++ph) {
             const bool up = ph == 0;
             if (!up && !weights) {
-                ok = wait_blocks(p.barriers + 1, p);
+                ok = wait_blocks(p.barriers + 1, gridDim.x, p);
                 if (!ok) *abort_flag = 1;
                 asm volatile("fence.proxy.async;" ::: "memory");  // H was stored by other threads; TMA reads it
             }
@@ -389,15 +442,33 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                 // rows of the weights' two boxes of 64
                 const int row0 = up ? e * p.F_up + it.tile * (m.gated ? 64 : 128) : e * p.D + it.tile * 128;
                 const int row1 = up && m.gated ? row0 + p.F : row0 + 64;
-                for (int kb = it.kb0; kb < it.kb1 && ok; ++kb) {
-                    ok = wait_phase(bar(bars.empty[stage]), phase ^ 1u, abort_flag, p.error, DEV_TIMEOUT_PRODUCER, p.wait_limit_ns);
+                for (int kb = it.kb0; kb < it.kb1 && ok;) {
+                    // the weights' stages in bursts: neighbouring 128-byte pieces of a row follow
+                    // one another to the memory
+                    const int burst = weights ? min(kMoeBurst, it.kb1 - kb) : 1;
+                    uint32_t first = stage, s = stage, ph_s = phase;
+                    for (int b = 0; b < burst && ok; ++b) {
+                        ok = wait_phase(bar(bars.empty[s]), ph_s ^ 1u, abort_flag, p.error, DEV_TIMEOUT_PRODUCER, p.wait_limit_ns);
+                        if (!ok) break;
+                        armed |= 1u << s;
+                        armed_phase = (armed_phase & ~(1u << s)) | (ph_s << s);
+                        if (weights) mbar_arrive_expect_tx(bar(bars.full[s]), kMoeWeightBytes);
+                        if (++s == (uint32_t)stages) {
+                            s = 0;
+                            ph_s ^= 1u;
+                        }
+                    }
                     if (!ok) break;
                     const uint32_t full = bar(bars.full[stage]), dst = ring + stage * stage_bytes;
                     if (weights) {
-                        mbar_arrive_expect_tx(full, kMoeWeightBytes);
                         const CUtensorMap* tm = up ? &tm_up : &tm_down;
-                        tma_load_2d(dst, tm, full, kb * 64, row0);
-                        tma_load_2d(dst + 8192u, tm, full, kb * 64, row1);
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t at = first;
+                            for (int b = 0; b < burst; ++b) {
+                                tma_load_2d(ring + at * stage_bytes + 8192u * h, tm, bar(bars.full[at]), (kb + b) * 64, h ? row1 : row0);
+                                if (++at == (uint32_t)stages) at = 0;
+                            }
+                        }
                     } else if (up) {
                         mbar_arrive_expect_tx(full, (uint32_t)boxes * 1024u);
                         for (int b = 0; b < boxes; ++b)
@@ -410,12 +481,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                             tma_load_2d(lo + 1024u * b, &tm_h, full, kb * 64, p.T * p.top_k + start + 8 * b);
                         }
                     }
-                    armed |= 1u << stage;
-                    armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
-                    if (++stage == (uint32_t)stages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    stage = s;
+                    phase = ph_s;
+                    kb += burst;
                 }
             }
         }
@@ -566,14 +634,15 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     if (*abort_flag) return;
     if (!grid_barrier(p.barriers + 2, p, &bars.ok)) return;
 
-    // y: a thread per 4 columns of a token
+    // y: a thread per 4 columns of a token, warps dealt out to the blocks in turn
     const int quads = p.D / 4;
-    for (int i = (int)blockIdx.x * kMoeThreads + threadIdx.x; i < p.T * quads; i += (int)gridDim.x * kMoeThreads) {
+    for (int i = (warp * grid + (int)blockIdx.x) * 32 + lane; i < p.T * quads; i += grid * kMoeThreads) {
         const int t = i / quads, d = 4 * (i % quads);
         float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int j = 0; j < p.top_k; ++j) {
             const int pair = t * p.top_k + j;
             float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
             for (int s = 0; s < route.splits; ++s) {
                 const float4 v = __ldcg(reinterpret_cast<const float4*>(p.Z + ((int64_t)s * p.T * p.top_k + route.place[pair]) * p.D + d));
                 z[0] += v.x;
@@ -652,11 +721,11 @@ kt_status launch_moe_t(int act, const MoeParams& p, int sms, void* stream, const
 
 }  // namespace
 
-// Workspace: [barrier counters, error word: 256 bytes][logits][H][Z].
-size_t moe_workspace(int64_t T, int64_t D, int64_t F, int64_t E, int64_t top_k) {
+// Workspace: [barrier counters, error word: 256 bytes][choices][H][Z].
+size_t moe_workspace(int64_t T, int64_t D, int64_t F, int64_t top_k) {
     const size_t pairs = (size_t)(T * top_k);
-    return 256 + round256((size_t)(T * E) * sizeof(float2)) + round256(2 * pairs * (size_t)F * 2) +
-           round256(moe_z_rows(pairs) * (size_t)D * sizeof(float));
+    return 256 + round256(pairs * sizeof(float2)) + round256(2 * pairs * (size_t)F * 2) +
+           round256(moe_z_rows((int)pairs) * (size_t)D * sizeof(float));
 }
 
 void moe_carve(MoeParams* p, int64_t max_tokens, void* workspace) {
@@ -664,8 +733,8 @@ void moe_carve(MoeParams* p, int64_t max_tokens, void* workspace) {
     p->barriers = reinterpret_cast<unsigned*>(w);
     p->error = reinterpret_cast<int*>(w + 128);
     w += 256;
-    p->logits = reinterpret_cast<float*>(w);
-    w += round256((size_t)(max_tokens * p->E) * sizeof(float2));
+    p->choices = reinterpret_cast<float2*>(w);
+    w += round256((size_t)(max_tokens * p->top_k) * sizeof(float2));
     p->H = reinterpret_cast<uint16_t*>(w);
     w += round256(2 * (size_t)(max_tokens * p->top_k) * (size_t)p->F * 2);
     p->Z = reinterpret_cast<float*>(w);

@@ -183,7 +183,7 @@ kt_status kt_moe_plan(const kt_moe_options* o, kt_moe_plan_t* out) {
     plan->o = *o;
     plan->device = dev;
     plan->sms = sms;
-    const size_t bytes = kt::moe_workspace(o->max_tokens, o->D, o->F, o->experts, o->top_k);
+    const size_t bytes = kt::moe_workspace(o->max_tokens, o->D, o->F, o->top_k);
     cudaError_t e = cudaMalloc(&plan->workspace, bytes);
     // the counters and the error word start at zero, on the device before this returns
     if (e == cudaSuccess) e = cudaMemset(plan->workspace, 0, 256);

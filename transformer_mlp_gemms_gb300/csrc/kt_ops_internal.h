@@ -2,6 +2,8 @@
 // their kernels.  Not part of the public interface (that is include/kt_ops.h).
 #pragma once
 
+#include <vector_types.h>
+
 #include <cstddef>
 #include <cstdint>
 
@@ -65,7 +67,7 @@ struct MoeParams {
     int64_t ldx;
     int T, D, F, F_up, E, top_k, normalize;
     // workspace
-    float* logits;       // [T][E][2]: each logit as a sum of two fp32 numbers
+    float2* choices;     // [T][top_k]: each token's experts (as integer bits) and their weights
     uint16_t* H;         // [2][T * top_k][F]: the hidden layer's rounding, then the remainder's
     float* Z;            // [splits][T * top_k][D]: each pair's output before its weight
     unsigned* barriers;  // grid barrier counters, zero between runs
@@ -77,7 +79,7 @@ KT_HOST_DEVICE inline int moe_splits(int pairs) { return pairs >= 1024 ? 1 : pai
 inline size_t moe_z_rows(int max_pairs) {  // for any number of pairs up to max_pairs
     return max_pairs >= 1024 ? max_pairs : max_pairs * 32 < 1024 ? max_pairs * 32 : 1024;
 }
-size_t moe_workspace(int64_t T, int64_t D, int64_t F, int64_t E, int64_t top_k);
+size_t moe_workspace(int64_t T, int64_t D, int64_t F, int64_t top_k);
 void moe_carve(MoeParams* p, int64_t max_tokens, void* workspace);
 kt_status launch_moe(int act, int dtype, const MoeParams& p, int sms, void* stream, const char** why);
 
