@@ -285,9 +285,10 @@ kt_status launch_mlp_two(int epi, int dtype, const void* const* maps, const Gemm
 bool encode_tmap(void* tmap128, const void* base, int dtype, uint64_t rows, uint64_t cols,
                  uint32_t box_rows, uint32_t box_cols, int swizzle_bytes, const char** why);
 
-// As encode_tmap, with `pitch` elements (a multiple of 8) from one row to the next.
-bool encode_tmap_pitch(void* tmap128, const void* base, int dtype, uint64_t rows, uint64_t cols, uint64_t pitch,
-                       uint32_t box_rows, uint32_t box_cols, int swizzle_bytes, const char** why);
+// Encode a tiled tensor map over a 16-bit array of `rank` dimensions, the innermost first:
+// its extents, the byte strides of all but the innermost (multiples of 16), and the box.
+bool encode_tmap_nd(void* tmap128, const void* base, int dtype, int rank, const uint64_t* dims, const uint64_t* strides,
+                    const uint32_t* box, int swizzle_bytes, const char** why);
 
 // tcgen05 instruction descriptor for kind::f16 with fp32 accumulation, A K-major,
 // B MN-major (b_kmajor = 0) or K-major (1), M = m (128, or 256 for a CTA pair), N = n.

@@ -437,23 +437,33 @@ kt_status launch_activation(int act, bool paired, const float* z, const float* g
 
 bool encode_tmap(void* tmap128, const void* base, int dtype, uint64_t rows, uint64_t cols,
                  uint32_t box_rows, uint32_t box_cols, int swizzle_bytes, const char** why) {
-    return encode_tmap_pitch(tmap128, base, dtype, rows, cols, cols, box_rows, box_cols, swizzle_bytes, why);
+    const uint64_t dims[2] = {cols, rows}, strides[1] = {cols * 2};
+    const uint32_t box[2] = {box_cols, box_rows};
+    return encode_tmap_nd(tmap128, base, dtype, 2, dims, strides, box, swizzle_bytes, why);
 }
 
-bool encode_tmap_pitch(void* tmap128, const void* base, int dtype, uint64_t rows, uint64_t cols, uint64_t pitch,
-                       uint32_t box_rows, uint32_t box_cols, int swizzle_bytes, const char** why) {
+bool encode_tmap_nd(void* tmap128, const void* base, int dtype, int rank, const uint64_t* dims, const uint64_t* strides,
+                    const uint32_t* box, int swizzle_bytes, const char** why) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
     if (!fn) {
         *why = "cuTensorMapEncodeTiled is not available from the driver";
         return false;
     }
-    cuuint64_t dims[2] = {cols, rows};
-    cuuint64_t strides[1] = {pitch * 2};
-    cuuint32_t box[2] = {box_cols, box_rows};
-    cuuint32_t estr[2] = {1, 1};
+    if (rank < 1 || rank > 5) {
+        *why = "a tensor map has 1 to 5 dimensions";
+        return false;
+    }
+    cuuint64_t dim[5], stride[5];
+    cuuint32_t ext[5], estr[5];
+    for (int i = 0; i < rank; ++i) {
+        dim[i] = dims[i];
+        ext[i] = box[i];
+        estr[i] = 1;
+        if (i + 1 < rank) stride[i] = strides[i];
+    }
     CUresult r = fn(reinterpret_cast<CUtensorMap*>(tmap128),
-                    dtype == KT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                    const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    dtype == KT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
+                    const_cast<void*>(base), dim, stride, ext, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     swizzle_bytes == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
                     : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                           : CU_TENSOR_MAP_SWIZZLE_128B,

@@ -34,12 +34,9 @@ constexpr int kMoeWarps = 16, kMoeThreads = kMoeWarps * 32;
 constexpr int kMoePairs = KT_MOE_MAX_TOKENS * KT_MOE_MAX_TOP_K;
 constexpr int kMoeWeightBytes = 128 * 128;  // a stage's weights: 128 rows x 64 columns
 constexpr int kMoeMaxStages = 10;
-#ifndef BURST
-#define BURST 4
-#endif
-constexpr int kMoeBurst = BURST;
+constexpr int kMoeWeightThreads = 2;       // threads that issue the weights' copies, in turn
 constexpr int kMoeEpiWarps = 4;             // warps 4-7
-constexpr uint32_t kMoeAccCols = 64;        // tensor-memory columns of one accumulator buffer
+constexpr uint32_t kMoeAccCols = 128;       // tensor-memory columns of one accumulator buffer
 
 // What every block knows after routing.
 struct MoeRoute {
@@ -356,6 +353,24 @@ struct MoeBars {
     int abort, ok, failed;
 };
 
+// Pairs per group of the down products' columns, for T tokens.
+KT_HOST_DEVICE inline int moe_group(int T) { return T <= 8 ? 8 : 16; }
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int x, int y, int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
     uint32_t r;
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
@@ -421,11 +436,16 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     const MoeItems m = moe_items(p, route, act);
     const int grid = (int)gridDim.x;
     const uint32_t up_cols = (uint32_t)(p.T + 15) / 16 * 16;  // a product has a multiple of 16 columns
+    // the down products' columns: groups of pairs, H's rounding, then the remainder's, of each group
+    const int group = moe_group(p.T);
 
-    if ((warp == 0 || warp == 2) && lane == 0) {
-        // ------------------ producers: weights (warp 0), tokens (warp 2) ------------------
-        const bool weights = warp == 0;
-        uint32_t stage = 0, phase = 0, armed = 0, armed_phase = 0;
+    if ((warp == 0 || warp == 2 || warp == 3) && lane == 0) {
+        // ------------------ producers: weights (warps 0 and 3), tokens (warp 2) ------------------
+        // a copy costs the thread that issues it about 0.1 us whatever its size: one copy per
+        // stage and operand, and the weights' stages dealt to two threads
+        const bool weights = warp != 2;
+        const uint32_t every = weights ? kMoeWeightThreads : 1, mine = warp == 3 ? 1 : 0;
+        uint32_t stage = 0, phase = 0, armed = 0, armed_phase = 0, count = 0;
         bool ok = true;
         for (int ph = 0; ph < 2 && ok; ++ph) {
             const bool up = ph == 0;
@@ -438,52 +458,30 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             for (int i = up ? (int)blockIdx.x : m.first_down; i < n_items && ok; i += grid) {
                 const MoeItem it = moe_item(p, route, m, up, i);
                 const int e = route.active[it.a], start = route.start[it.a], n = route.start[it.a + 1] - start;
-                const int boxes = up ? (p.T + 7) / 8 : (n + 7) / 8;
-                // rows of the weights' two boxes of 64
-                const int row0 = up ? e * p.F_up + it.tile * (m.gated ? 64 : 128) : e * p.D + it.tile * 128;
-                const int row1 = up && m.gated ? row0 + p.F : row0 + 64;
-                for (int kb = it.kb0; kb < it.kb1 && ok;) {
-                    // the weights' stages in bursts: neighbouring 128-byte pieces of a row follow
-                    // one another to the memory
-                    const int burst = weights ? min(kMoeBurst, it.kb1 - kb) : 1;
-                    uint32_t first = stage, s = stage, ph_s = phase;
-                    for (int b = 0; b < burst && ok; ++b) {
-                        ok = wait_phase(bar(bars.empty[s]), ph_s ^ 1u, abort_flag, p.error, DEV_TIMEOUT_PRODUCER, p.wait_limit_ns);
+                const int groups = (n + group - 1) / group;
+                for (int kb = it.kb0; kb < it.kb1; ++kb, ++count) {
+                    if (count % every == mine) {
+                        ok = wait_phase(bar(bars.empty[stage]), phase ^ 1u, abort_flag, p.error, DEV_TIMEOUT_PRODUCER, p.wait_limit_ns);
                         if (!ok) break;
-                        armed |= 1u << s;
-                        armed_phase = (armed_phase & ~(1u << s)) | (ph_s << s);
-                        if (weights) mbar_arrive_expect_tx(bar(bars.full[s]), kMoeWeightBytes);
-                        if (++s == (uint32_t)stages) {
-                            s = 0;
-                            ph_s ^= 1u;
+                        const uint32_t full = bar(bars.full[stage]), dst = ring + stage * stage_bytes;
+                        if (weights) {
+                            mbar_arrive_expect_tx(full, kMoeWeightBytes);
+                            tma_load_4d(dst, up ? &tm_up : &tm_down, full, kb * 64, it.tile * (up && m.gated ? 64 : 128), 0, e);
+                        } else if (up) {
+                            mbar_arrive_expect_tx(full, (uint32_t)(p.T + 7) / 8 * 1024u);
+                            tma_load_2d(dst + kMoeWeightBytes, &tm_x, full, kb * 64, 0);
+                        } else {
+                            mbar_arrive_expect_tx(full, (uint32_t)(groups * group) * 256u);
+                            for (int b = 0; b < groups; ++b)
+                                tma_load_3d(dst + kMoeWeightBytes + (uint32_t)(b * group) * 256u, &tm_h, full, kb * 64, start + group * b, 0);
                         }
+                        armed |= 1u << stage;
+                        armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
                     }
-                    if (!ok) break;
-                    const uint32_t full = bar(bars.full[stage]), dst = ring + stage * stage_bytes;
-                    if (weights) {
-                        const CUtensorMap* tm = up ? &tm_up : &tm_down;
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t at = first;
-                            for (int b = 0; b < burst; ++b) {
-                                tma_load_2d(ring + at * stage_bytes + 8192u * h, tm, bar(bars.full[at]), (kb + b) * 64, h ? row1 : row0);
-                                if (++at == (uint32_t)stages) at = 0;
-                            }
-                        }
-                    } else if (up) {
-                        mbar_arrive_expect_tx(full, (uint32_t)boxes * 1024u);
-                        for (int b = 0; b < boxes; ++b)
-                            tma_load_2d(dst + kMoeWeightBytes + 1024u * b, &tm_x, full, kb * 64, 8 * b);
-                    } else {
-                        const uint32_t lo = dst + kMoeWeightBytes + (uint32_t)(n + 15) / 16 * 2048u;
-                        mbar_arrive_expect_tx(full, (uint32_t)boxes * 2048u);
-                        for (int b = 0; b < boxes; ++b) {
-                            tma_load_2d(dst + kMoeWeightBytes + 1024u * b, &tm_h, full, kb * 64, start + 8 * b);
-                            tma_load_2d(lo + 1024u * b, &tm_h, full, kb * 64, p.T * p.top_k + start + 8 * b);
-                        }
+                    if (++stage == (uint32_t)stages) {
+                        stage = 0;
+                        phase ^= 1u;
                     }
-                    stage = s;
-                    phase = ph_s;
-                    kb += burst;
                 }
             }
         }
@@ -500,7 +498,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             const int n_items = up ? m.up_items : m.down_items;
             for (int i = up ? (int)blockIdx.x : m.first_down; i < n_items && ok; i += grid, ++t) {
                 const MoeItem it = moe_item(p, route, m, up, i);
-                const uint32_t cols = up ? up_cols : (uint32_t)(route.start[it.a + 1] - route.start[it.a] + 15) / 16 * 16;
+                const uint32_t cols = up ? up_cols : (uint32_t)((route.start[it.a + 1] - route.start[it.a] + group - 1) / group * group * 2);
                 const uint32_t idesc = idesc0 | ((cols >> 3) << 17), buf = t & 1u, d = tmem + buf * kMoeAccCols;
                 ok = wait_phase(bar(bars.acc_empty[buf]), ((t >> 1) & 1u) ^ 1u, abort_flag, p.error, DEV_TIMEOUT_MMA, p.wait_limit_ns);
                 tc_fence_after();
@@ -513,11 +511,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         mma_f16(d, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), idesc, kb > it.kb0 || k > 0);
-                    if (!up) {
-                        const uint64_t ld = smem_desc(base + kMoeWeightBytes + cols * 128u, 16u, 1024u);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) mma_f16(d, ad + (uint64_t)(2 * k), ld + (uint64_t)(2 * k), idesc, 1u);
-                    }
                     mma_commit(bar(bars.empty[stage]));
                     if (++stage == (uint32_t)stages) {
                         stage = 0;
@@ -560,7 +553,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                auto column = [&](int c) { return up ? (uint32_t)(route.list[start + c] / p.top_k) : (uint32_t)c; };
+                auto column = [&](int c) { return up ? (uint32_t)(route.list[start + c] / p.top_k) : (uint32_t)(c / group * group + c); };
                 if (gate) {
                     for (int c0 = 0; c0 < n; c0 += 8) {
                         uint32_t v[8];
@@ -580,15 +573,20 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                         uint32_t v[8];
 #pragma unroll
                         for (int c = 0; c < 8; ++c) v[c] = tmem_ld1(d + column(min(c0 + c, n - 1)));
+                        uint32_t rest_of[8];
+                        if (!up) {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) rest_of[c] = tmem_ld1(d + column(min(c0 + c, n - 1)) + group);
+                        }
                         tmem_wait_ld_only();
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
-                            asm volatile("" : "+r"(v[c])::"memory");
+                            asm volatile("" : "+r"(v[c]), "+r"(rest_of[c])::"memory");
                             if (c0 + c >= n || !in) continue;
                             const int64_t at = start + c0 + c;
                             float z = __uint_as_float(v[c]);
                             if (!up) {
-                                p.Z[((int64_t)it.split * p.T * p.top_k + at) * p.D + f] = z;
+                                p.Z[((int64_t)it.split * p.T * p.top_k + at) * p.D + f] = z + __uint_as_float(rest_of[c]);
                                 continue;
                             }
                             f32x2 h = f2(z + bias);
@@ -685,18 +683,27 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 template <int DT>
 kt_status launch_moe_t(int act, const MoeParams& p, int sms, void* stream, const char** why) {
     auto kern = kt_moe_kernel<DT>;
-    const int cols = (p.T + 15) / 16 * 16;
-    const uint32_t stage = kMoeWeightBytes + 2u * (uint32_t)cols * 128u;
+    const int group = moe_group(p.T);
+    // a stage: the weights, then the larger of the up product's columns (all tokens) and the down
+    // product's (an expert's pairs, two parts each)
+    const uint32_t stage = kMoeWeightBytes + (uint32_t)((p.T + group - 1) / group * group) * 256u;
     const int fixed = 1024 + p.T * 64 * (int)sizeof(float);
     const int room = kSmemBudget - (int)sizeof(MoeRoute) - (int)sizeof(MoeBars) - 64;
     const int stages = std::min(kMoeMaxStages, (room - fixed) / (int)stage);
     const int smem = fixed + stages * (int)stage;
     alignas(64) CUtensorMap tx, tu, td, th;
-    const uint64_t pairs = (uint64_t)p.T * p.top_k;
-    if (!encode_tmap_pitch(&tx, p.X, DT, p.T, p.D, p.ldx, 8, 64, 128, why) ||
-        !encode_tmap_pitch(&tu, p.W_up, DT, (uint64_t)p.E * p.F_up, p.D, p.D, 64, 64, 128, why) ||
-        !encode_tmap_pitch(&td, p.W_down, DT, (uint64_t)p.E * p.D, p.F, p.F, 64, 64, 128, why) ||
-        !encode_tmap_pitch(&th, p.H, DT, 2 * pairs, p.F, p.F, 8, 64, 128, why))
+    const bool gated = act == KT_ACT_GEGLU;
+    const uint64_t D = p.D, F = p.F, E = p.E, T = p.T, pairs = T * p.top_k;
+    const uint64_t dx[2] = {D, T}, sx[1] = {2 * (uint64_t)p.ldx};
+    const uint32_t bx[2] = {64, (uint32_t)(T + 7) / 8 * 8};
+    const uint64_t du[4] = {D, F, gated ? 2u : 1u, E}, su[3] = {2 * D, 2 * D * F, 2 * D * (uint64_t)p.F_up};
+    const uint32_t bu[4] = {64, gated ? 64u : 128u, gated ? 2u : 1u, 1};
+    const uint64_t dd[4] = {F, D, 1, E}, sd[3] = {2 * F, 2 * D * F, 2 * D * F};
+    const uint32_t bd[4] = {64, 128, 1, 1};
+    const uint64_t dh[3] = {F, pairs, 2}, sh[2] = {2 * F, 2 * F * pairs};
+    const uint32_t bh[3] = {64, (uint32_t)group, 2};
+    if (!encode_tmap_nd(&tx, p.X, DT, 2, dx, sx, bx, 128, why) || !encode_tmap_nd(&tu, p.W_up, DT, 4, du, su, bu, 128, why) ||
+        !encode_tmap_nd(&td, p.W_down, DT, 4, dd, sd, bd, 128, why) || !encode_tmap_nd(&th, p.H, DT, 3, dh, sh, bh, 128, why))
         return KT_ERR_CUDA;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) {
