@@ -289,6 +289,20 @@ __device__ void moe_route(const MoeParams& p, MoeRoute& r) {
         }
     }
     __syncthreads();
+    if (warp == kMoeWarps - 1) {
+        // splits of the down projections along F, a lane for each count: the fewest k-blocks in a
+        // row on one block, two more counted per item for its start and end
+        const int kblocks = (p.F + 63) / 64, whole = r.n_active * ((p.D + 127) / 128), grid = (int)gridDim.x;
+        const int s = min(lane + 1, min(moe_splits(pairs), kblocks));
+        const int per = (kblocks + s - 1) / s, n = (kblocks + per - 1) / per;
+        const unsigned cost = (unsigned)(((whole * n + grid - 1) / grid) * (per + 2));
+        const unsigned best = __reduce_min_sync(0xffffffffu, cost);
+        const uint32_t who = __ballot_sync(0xffffffffu, cost == best);
+        if (lane == __ffs(who) - 1) {
+            r.splits = n;
+            r.split_kblocks = per;
+        }
+    }
     for (int a = warp; a < r.n_active; a += kMoeWarps) {
         const int e = r.active[a];
         int at = r.start[a];
@@ -411,27 +425,15 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         prefetch_tmap(&tm_down);
         prefetch_tmap(&tm_h);
     }
-    const bool ready = moe_choices<DT>(p, route, &bars.ok);
-    if (!ready || bars.failed) return;  // (both the same in every thread: the choices end with a barrier)
-    moe_route(p, route);
-    if (warp == 0) {
-        // splits of the down projections along F, a lane for each count: the fewest k-blocks in a
-        // row on one block, two more counted per item for its start and end
-        const int kblocks = (p.F + 63) / 64, whole = route.n_active * ((p.D + 127) / 128), grid = (int)gridDim.x;
-        const int s = min(lane + 1, min(moe_splits(p.T * p.top_k), kblocks));
-        const int per = (kblocks + s - 1) / s, n = (kblocks + per - 1) / per;
-        const unsigned cost = (unsigned)(((whole * n + grid - 1) / grid) * (per + 2));
-        const unsigned best = __reduce_min_sync(0xffffffffu, cost);
-        const uint32_t who = __ballot_sync(0xffffffffu, cost == best);
-        if (lane == __ffs(who) - 1) {
-            route.splits = n;
-            route.split_kblocks = per;
-        }
-    }
     if (warp == 1) tmem_alloc<1>(smem_u32(&bars.tmem), 2 * kMoeAccCols);
     tc_fence_before();
-    __syncthreads();
+    const bool ready = moe_choices<DT>(p, route, &bars.ok);  // ends with a barrier of the block
     tc_fence_after();
+    if (!ready || bars.failed) {  // the same in every thread
+        if (warp == 1) tmem_dealloc<1>(bars.tmem, 2 * kMoeAccCols);
+        return;
+    }
+    moe_route(p, route);
     const uint32_t tmem = bars.tmem;
     const MoeItems m = moe_items(p, route, act);
     const int grid = (int)gridDim.x;
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         }
     } else if (warp >= 4 && warp < 4 + kMoeEpiWarps) {
         // ------------------ epilogue: lane = weight row ------------------
-        const int q = warp & 3;
+        const int q = warp & 3, pairs = p.T * p.top_k;
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
         uint32_t t = 0;
         bool live = true;
@@ -553,55 +555,52 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                auto column = [&](int c) { return up ? (uint32_t)(route.list[start + c] / p.top_k) : (uint32_t)(c / group * group + c); };
-                if (gate) {
-                    for (int c0 = 0; c0 < n; c0 += 8) {
-                        uint32_t v[8];
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) v[c] = tmem_ld1(d + column(min(c0 + c, n - 1)));
+                // rolled loops, one column at a time: this code runs from a cold instruction cache (the
+                // weights have swept it out of L2 since the last call), and with 8 columns unrolled
+                // the first item's epilogue alone took 11 us
+                if (!up) {
+#pragma unroll 1
+                    for (int c = 0; c < n; ++c) {
+                        const uint32_t at = d + (uint32_t)(c / group * group + c);
+                        uint32_t z = tmem_ld1(at), rest = tmem_ld1(at + group);
                         tmem_wait_ld_only();
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            asm volatile("" : "+r"(v[c])::"memory");
-                            if (c0 + c < n) exchange[(c0 + c) * 64 + 32 * (q & 1) + lane] = __uint_as_float(v[c]) + bias;
+                        asm volatile("" : "+r"(z), "+r"(rest)::"memory");
+                        if (in) p.Z[((int64_t)it.split * pairs + start + c) * p.D + f] = __uint_as_float(z) + __uint_as_float(rest);
+                    }
+                } else {
+                    float* gates = exchange + 32 * (q & 1) + lane;
+                    if (gate) {
+#pragma unroll 1
+                        for (int c = 0; c < n; ++c) {
+                            uint32_t z = tmem_ld1(d + (uint32_t)(route.list[start + c] / p.top_k));
+                            tmem_wait_ld_only();
+                            asm volatile("" : "+r"(z)::"memory");
+                            gates[c * 64] = __uint_as_float(z) + bias;
                         }
                     }
-                }
-                if (up && m.gated) epi_bar_sync<kMoeEpiWarps>();
-                if (!gate) {
-                    for (int c0 = 0; c0 < n; c0 += 8) {
-                        uint32_t v[8];
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) v[c] = tmem_ld1(d + column(min(c0 + c, n - 1)));
-                        uint32_t rest_of[8];
-                        if (!up) {
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) rest_of[c] = tmem_ld1(d + column(min(c0 + c, n - 1)) + group);
-                        }
-                        tmem_wait_ld_only();
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            asm volatile("" : "+r"(v[c]), "+r"(rest_of[c])::"memory");
-                            if (c0 + c >= n || !in) continue;
-                            const int64_t at = start + c0 + c;
-                            float z = __uint_as_float(v[c]);
-                            if (!up) {
-                                p.Z[((int64_t)it.split * p.T * p.top_k + at) * p.D + f] = z + __uint_as_float(rest_of[c]);
-                                continue;
-                            }
-                            f32x2 h = f2(z + bias);
-                            if (m.gated) h = f2_mul<true>(h, gelu_erf_f2<true>(f2(exchange[(c0 + c) * 64 + 32 * (q & 1) + lane])));
-                            else if (act == KT_ACT_GELU_ERF) h = gelu_erf_f2<true>(h);
+                    if (m.gated) epi_bar_sync<kMoeEpiWarps>();
+                    if (!gate) {
+#pragma unroll 1
+                        for (int c = 0; c < n; ++c) {
+                            uint32_t z = tmem_ld1(d + (uint32_t)(route.list[start + c] / p.top_k));
+                            tmem_wait_ld_only();
+                            asm volatile("" : "+r"(z)::"memory");
+                            const float v = __uint_as_float(z) + bias;
+                            f32x2 h = f2(m.gated ? gates[c * 64] : v);
+                            if (m.gated || act == KT_ACT_GELU_ERF) h = gelu_erf_f2<true>(h);
                             else if (act == KT_ACT_GELU_TANH) h = gelu_tanh_f2<true>(h);
                             else if (act == KT_ACT_GELU_SIGMOID) h = gelu_sigmoid_f2<true>(h);
                             else if (act == KT_ACT_SILU) h = silu_f2<true>(h);
+                            if (m.gated) h.x = __fmul_rn(v, h.x);
                             // H in two 16-bit parts: its rounding, and the remainder's (none of an infinity)
                             const uint32_t hi = pack2<DT>(h.x, 0.0f) & 0xffffu;
                             float back[8];
                             unpack8<DT>(make_uint4(hi, 0u, 0u, 0u), back);
                             const float rest = fabsf(back[0]) < __uint_as_float(0x7f800000u) ? h.x - back[0] : 0.0f;
-                            p.H[at * p.F + f] = (uint16_t)hi;
-                            p.H[((int64_t)p.T * p.top_k + at) * p.F + f] = (uint16_t)(pack2<DT>(rest, 0.0f) & 0xffffu);
+                            if (in) {
+                                p.H[(int64_t)(start + c) * p.F + f] = (uint16_t)hi;
+                                p.H[(int64_t)(pairs + start + c) * p.F + f] = (uint16_t)(pack2<DT>(rest, 0.0f) & 0xffffu);
+                            }
                         }
                     }
                 }
@@ -632,43 +631,45 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     if (*abort_flag) return;
     if (!grid_barrier(p.barriers + 2, p, &bars.ok)) return;
 
-    // y: a thread per 4 columns of a token, warps dealt out to the blocks in turn
-    const int quads = p.D / 4;
-    for (int i = (warp * grid + (int)blockIdx.x) * 32 + lane; i < p.T * quads; i += grid * kMoeThreads) {
-        const int t = i / quads, d = 4 * (i % quads);
+    // y: 8 lanes per 4 columns of a token, each adding up every eighth (choice, split), so that
+    // the loads are in flight together; warps dealt out to the blocks in turn
+    const int quads = p.D / 4, pairs = p.T * p.top_k, parts = p.top_k * route.splits, sub = lane >> 2;
+    const int last = p.T * quads;
+    for (int w = warp * grid + (int)blockIdx.x; w * 4 < last; w += grid * kMoeWarps) {
+        const int i = min(w * 4 + (lane & 3), last - 1), t = i / quads, d = 4 * (i % quads);
         float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int j = 0; j < p.top_k; ++j) {
-            const int pair = t * p.top_k + j;
-            float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
-            for (int s = 0; s < route.splits; ++s) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(p.Z + ((int64_t)s * p.T * p.top_k + route.place[pair]) * p.D + d));
-                z[0] += v.x;
-                z[1] += v.y;
-                z[2] += v.z;
-                z[3] += v.w;
-            }
-            if (p.b_down) {
-                const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.b_down) +
+#pragma unroll 2
+        for (int c = sub; c < parts; c += 8) {
+            const int j = c / route.splits, s = c % route.splits, pair = t * p.top_k + j;
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.Z + ((int64_t)s * pairs + route.place[pair]) * p.D + d));
+            const float wt = route.weight[pair];
+            float b[8] = {};
+            if (p.b_down && s == 0) {
+                const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.b_down) +
                                                                 (int64_t)route.expert[pair] * p.D + d);
-                float b[8];
-                unpack8<DT>(make_uint4(w.x, w.y, 0u, 0u), b);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) z[c] += b[c];
+                unpack8<DT>(make_uint4(u.x, u.y, 0u, 0u), b);
             }
-            const float w = route.weight[pair];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) y[c] = fmaf(w, z[c], y[c]);
+            y[0] = fmaf(wt, v.x + b[0], y[0]);
+            y[1] = fmaf(wt, v.y + b[1], y[1]);
+            y[2] = fmaf(wt, v.z + b[2], y[2]);
+            y[3] = fmaf(wt, v.w + b[3], y[3]);
         }
-        const int64_t at = (int64_t)t * p.D + d;
-        if (p.R) {
-            const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.R) + at);
-            float b[8];
-            unpack8<DT>(make_uint4(w.x, w.y, 0u, 0u), b);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) y[c] += b[c];
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) y[c] += __shfl_xor_sync(0xffffffffu, y[c], o);
         }
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.Y) + at) = make_uint2(pack2<DT>(y[0], y[1]), pack2<DT>(y[2], y[3]));
+        if (sub == 0 && w * 4 + (lane & 3) < last) {
+            const int64_t at = (int64_t)t * p.D + d;
+            if (p.R) {
+                const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.R) + at);
+                float b[8];
+                unpack8<DT>(make_uint4(u.x, u.y, 0u, 0u), b);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) y[c] += b[c];
+            }
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.Y) + at) = make_uint2(pack2<DT>(y[0], y[1]), pack2<DT>(y[2], y[3]));
+        }
     }
     // the last block to get here leaves the counters at zero: every block is past every barrier
     __syncthreads();
