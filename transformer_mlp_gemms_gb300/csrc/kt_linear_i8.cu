@@ -405,13 +405,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
 }
 
 template <int BN>
-kt_status launch_tc(int dtype, const LinearI8& p, int sms, void* stream, const char** why) {
+kt_status launch_tc(int dtype, const LinearI8& p, int sms, int device, void* stream, const char** why) {
     const int tiles_m = (p.M + 127) / 128, tiles_n = (p.N + BN - 1) / BN, tiles = tiles_m * tiles_n;
     // whole 16-byte pieces of Y's rows: the last one too, as N is a multiple of 8
     const int wide = p.N % 8 == 0 && p.ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(p.Y) & 15u) == 0;
     auto kern = dtype == KT_BF16 ? kt_linear_i8_tc_kernel<KT_BF16, BN> : kt_linear_i8_tc_kernel<KT_F16, BN>;
     constexpr int smem = (int)sizeof(TcSmem<BN>) + 1024;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemOptIn opt_in[2];  // by dtype
+    cudaError_t e = opt_in[dtype == KT_BF16](kern, smem, device);
     if (e == cudaSuccess)
         e = launch_pdl(kern, (unsigned)std::min(tiles, sms), kTcThreads, smem, stream, p, tiles_n, tiles,
                        make_idesc(KT_F16, BN, 128, 1), wide);
@@ -424,15 +425,15 @@ kt_status launch_tc(int dtype, const LinearI8& p, int sms, void* stream, const c
 
 }  // namespace
 
-kt_status launch_linear_i8(int dtype, const LinearI8& p, int sms, void* stream, const char** why) {
+kt_status launch_linear_i8(int dtype, const LinearI8& p, int sms, int device, void* stream, const char** why) {
     if (p.M > kDotTokens) {
         // tile width: the fewest rounds over the SMs, each costing its products' cycles
         const int64_t tm = (p.M + 127) / 128;
         auto cost = [&](int bn, int per) { return ((tm * ((p.N + bn - 1) / bn) + sms - 1) / sms) * per; };
         const int64_t c192 = cost(192, 384), c128 = cost(128, 290), c64 = cost(64, 220);
-        if (c192 <= c128 && c192 <= c64) return launch_tc<192>(dtype, p, sms, stream, why);
-        if (c128 <= c64) return launch_tc<128>(dtype, p, sms, stream, why);
-        return launch_tc<64>(dtype, p, sms, stream, why);
+        if (c192 <= c128 && c192 <= c64) return launch_tc<192>(dtype, p, sms, device, stream, why);
+        if (c128 <= c64) return launch_tc<128>(dtype, p, sms, device, stream, why);
+        return launch_tc<64>(dtype, p, sms, device, stream, why);
     }
     const int chunk = std::min(kDotChunk, (p.K + 127) & ~127);
     const dim3 grid((unsigned)((p.N + kDotRows - 1) / kDotRows), (unsigned)((p.M + kDotTokens - 1) / kDotTokens));

@@ -205,7 +205,7 @@ int ln_backward_blocks(int64_t M, int64_t D) {
     return (int)std::min<int64_t>((M + teams - 1) / teams, kMaxSms);
 }
 
-kt_status launch_ln_backward(int dtype, const LnBackward& p, int sms, void* stream, const char** why) {
+kt_status launch_ln_backward(int dtype, const LnBackward& p, int sms, int device, void* stream, const char** why) {
     RowShape shape;
     if (!row_shape(p.D, &shape)) {
         *why = "rows of this length are not supported";
@@ -221,10 +221,11 @@ kt_status launch_ln_backward(int dtype, const LnBackward& p, int sms, void* stre
             return with_shape<decltype(v16)::value>(shape, [&](auto W, auto V) -> kt_status {
                 constexpr int w = decltype(W)::value, v = decltype(V)::value, teams = row_block(w) / (32 * w);
                 constexpr size_t smem = (w == 16 ? 2 : teams == 1 ? 0 : teams) * (size_t)(32 * w * v * 8) * sizeof(float);
+                static SmemOptIn opt_in;
                 auto kern = kt_ln_backward_kernel<decltype(dt)::value, w, v, decltype(v16)::value>;
                 cudaError_t le = cudaSuccess;
                 if (smem > 32 * 1024)
-                    le = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                    le = opt_in(kern, (int)smem, device);
                 if (le == cudaSuccess) le = launch_pdl(kern, (unsigned)grid, row_block(w), smem, stream, p);
                 if (le != cudaSuccess) {
                     *why = cudaGetErrorString(le);

@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 template <int DT>
-kt_status launch_moe_t(int act, const MoeParams& p, int sms, void* stream, const char** why) {
+kt_status launch_moe_t(int act, const MoeParams& p, int sms, int device, void* stream, const char** why) {
     auto kern = kt_moe_kernel<DT>;
     const int group = moe_group(p.T);
     // a stage: the weights, then the larger of the up product's columns (all tokens) and the down
@@ -706,7 +706,8 @@ kt_status launch_moe_t(int act, const MoeParams& p, int sms, void* stream, const
     if (!encode_tmap_nd(&tx, p.X, DT, 2, dx, sx, bx, 128, why) || !encode_tmap_nd(&tu, p.W_up, DT, 4, du, su, bu, 128, why) ||
         !encode_tmap_nd(&td, p.W_down, DT, 4, dd, sd, bd, 128, why) || !encode_tmap_nd(&th, p.H, DT, 3, dh, sh, bh, 128, why))
         return KT_ERR_CUDA;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemOptIn opt_in;
+    cudaError_t e = opt_in(kern, room, device);
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)sms, 1, 1);
@@ -748,8 +749,8 @@ void moe_carve(MoeParams* p, int64_t max_tokens, void* workspace) {
     p->Z = reinterpret_cast<float*>(w);
 }
 
-kt_status launch_moe(int act, int dtype, const MoeParams& p, int sms, void* stream, const char** why) {
-    return dtype == KT_BF16 ? launch_moe_t<KT_BF16>(act, p, sms, stream, why) : launch_moe_t<KT_F16>(act, p, sms, stream, why);
+kt_status launch_moe(int act, int dtype, const MoeParams& p, int sms, int device, void* stream, const char** why) {
+    return dtype == KT_BF16 ? launch_moe_t<KT_BF16>(act, p, sms, device, stream, why) : launch_moe_t<KT_F16>(act, p, sms, device, stream, why);
 }
 
 }  // namespace kt

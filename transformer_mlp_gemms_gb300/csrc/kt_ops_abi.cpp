@@ -119,7 +119,7 @@ kt_status kt_layernorm_backward(int64_t M, int64_t D, kt_dtype dtype, const void
     if ((s = current_device(&dev, &sms)) != KT_OK) return s;
     const char* why = "";
     kt::LnBackward p = {dY, X, gamma, mean, rstd, dX, dgamma, dbeta, static_cast<float*>(workspace), lddy, ldx, lddx, (int)M, (int)D};
-    return done(kt::launch_ln_backward(dtype, p, sms, stream, &why), why);
+    return done(kt::launch_ln_backward(dtype, p, sms, dev, stream, &why), why);
 }
 
 kt_status kt_quantize_rows(int64_t M, int64_t K, kt_dtype dtype, kt_act act, const void* X, int64_t ldx, int8_t* Q,
@@ -157,7 +157,7 @@ kt_status kt_linear_i8(int64_t M, int64_t N, int64_t K, kt_dtype dtype, const in
     if ((s = current_device(&dev, &sms)) != KT_OK) return s;
     const char* why = "";
     kt::LinearI8 p = {Q, W, scale_x, scale_w, bias, Y, ldq, ldw, ldy, (int)M, (int)N, (int)K};
-    return done(kt::launch_linear_i8(dtype, p, sms, stream, &why), why);
+    return done(kt::launch_linear_i8(dtype, p, sms, dev, stream, &why), why);
 }
 
 kt_status kt_moe_plan(const kt_moe_options* o, kt_moe_plan_t* out) {
@@ -242,7 +242,7 @@ kt_status kt_moe_run(kt_moe_plan_t plan, const kt_moe_tensors* t, void* stream) 
     plan->last_stream = stream;
     plan->ran = true;
     const char* why = "";
-    return done(kt::launch_moe(plan->o.act, plan->o.dtype, p, plan->sms, stream, &why), why);
+    return done(kt::launch_moe(plan->o.act, plan->o.dtype, p, plan->sms, plan->device, stream, &why), why);
 }
 
 kt_status kt_moe_status(kt_moe_plan_t plan) {

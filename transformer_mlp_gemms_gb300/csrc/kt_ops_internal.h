@@ -2,7 +2,9 @@
 // their kernels.  Not part of the public interface (that is include/kt_ops.h).
 #pragma once
 
-#include <vector_types.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
 
 #include <cstddef>
 #include <cstdint>
@@ -37,7 +39,7 @@ struct LnBackward {
 // Blocks (and rows of partial sums) of a backward call on any device of up to kMaxSms SMs.
 constexpr int kMaxSms = 160;
 int ln_backward_blocks(int64_t M, int64_t D);
-kt_status launch_ln_backward(int dtype, const LnBackward& p, int sms, void* stream, const char** why);
+kt_status launch_ln_backward(int dtype, const LnBackward& p, int sms, int device, void* stream, const char** why);
 
 struct QuantRows {
     const void* X;
@@ -56,7 +58,7 @@ struct LinearI8 {
     int64_t ldq, ldw, ldy;
     int M, N, K;
 };
-kt_status launch_linear_i8(int dtype, const LinearI8& p, int sms, void* stream, const char** why);
+kt_status launch_linear_i8(int dtype, const LinearI8& p, int sms, int device, void* stream, const char** why);
 
 // The mixture-of-experts layer (kt_moe.cu).
 struct MoeParams {
@@ -81,7 +83,21 @@ inline size_t moe_z_rows(int max_pairs) {  // for any number of pairs up to max_
 }
 size_t moe_workspace(int64_t T, int64_t D, int64_t F, int64_t top_k);
 void moe_carve(MoeParams* p, int64_t max_tokens, void* workspace);
-kt_status launch_moe(int act, int dtype, const MoeParams& p, int sms, void* stream, const char** why);
+kt_status launch_moe(int act, int dtype, const MoeParams& p, int sms, int device, void* stream, const char** why);
+
+// Opt a kernel in to `bytes` of dynamic shared memory on the current device, once per device: the
+// attribute stays.  `done` belongs to the kernel (a static of its launch function).
+struct SmemOptIn {
+    std::atomic<uint64_t> done{0};  // a bit per device ordinal
+    template <typename K>
+    cudaError_t operator()(K kern, int bytes, int device) {
+        const uint64_t bit = 1ull << (device & 63);
+        if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
 
 // A launch as a programmatic dependent of the previous kernel in the stream.
 template <typename... P, typename... A>

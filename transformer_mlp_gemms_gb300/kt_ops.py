@@ -16,7 +16,7 @@ import ctypes
 import torch
 
 from . import kt_mlp
-from .kt_mlp import KT_ACT_GEGLU, KT_ACT_NONE, KT_BF16, KT_ERR_INVALID, KT_F16, KtError, _check, _ptr
+from .kt_mlp import KT_ACT_GEGLU, KT_ACT_NONE, KT_BF16, KT_ERR_INVALID, KT_F16, KtError, _check
 
 _VP, _I64, _I32, _F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
 
@@ -50,24 +50,36 @@ SIGNATURES = {
 }
 
 _DTYPES = {torch.float16: KT_F16, torch.bfloat16: KT_BF16}
+_F32_T, _I8_T, _I32_T = torch.float32, torch.int8, torch.int32
 _lib = None
+_fwd = _bwd = _quant = _lin = _moe = None  # the functions of the hot calls, once loaded
 
 
 def load():
     """The shared library with this header's signatures set (``OSError`` if it has not been built)."""
-    global _lib
+    global _lib, _fwd, _bwd, _quant, _lin, _moe
     if _lib is None:
         lib = kt_mlp.load()
         for name, (args, res) in SIGNATURES.items():
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = res
+        _fwd, _bwd, _quant = lib.kt_layernorm_forward, lib.kt_layernorm_backward, lib.kt_quantize_rows
+        _lin, _moe = lib.kt_linear_i8, lib.kt_moe_run
         _lib = lib
     return _lib
 
 
 def _bad(where: str, message: str):
     raise KtError(KT_ERR_INVALID, where, message)
+
+
+def _size(where: str, name: str, t):
+    """(rows, columns, device index) of a matrix."""
+    shape = t.shape
+    if len(shape) != 2:
+        _bad(where, f"{name}: a matrix expected, got {list(shape)}")
+    return shape[0], shape[1], t.get_device()
 
 
 def _dtype(where: str, t) -> int:
@@ -77,57 +89,55 @@ def _dtype(where: str, t) -> int:
     return code
 
 
-def _matrix(where: str, name: str, t, rows, cols, dtype, device) -> int:
-    """Checks a [rows][cols] tensor with consecutive elements in a row; returns its row pitch."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        _bad(where, f"{name}: expected [{rows}][{cols}], got {list(t.shape)}")
-    if t.dtype != dtype or t.device != device:
-        _bad(where, f"{name}: expected {dtype} on {device}, got {t.dtype} on {t.device}")
+def _rows(where: str, name: str, t, shape, dtype, index) -> int:
+    """Checks a matrix with consecutive elements in a row; returns its row pitch."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        _bad(where, f"{name}: expected {dtype} {list(shape)} on device {index}, got {t.dtype} {list(t.shape)} on {t.device}")
     s0, s1 = t.stride()
-    if cols > 1 and s1 != 1:
+    rows, cols = shape
+    if s1 != 1 and cols > 1:
         _bad(where, f"{name}: elements of a row must be consecutive, strides are {t.stride()}")
-    if rows <= 1:
-        return max(s0, cols)
     if s0 < cols:
-        _bad(where, f"{name}: rows overlap, strides are {t.stride()}")
+        if rows > 1:
+            _bad(where, f"{name}: rows overlap, strides are {t.stride()}")
+        return cols  # the pitch of a single row is never used
     return s0
 
 
-def _whole(where: str, name: str, t, shape, dtype, device):
-    """Checks a contiguous tensor of the given shape."""
-    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        _bad(where, f"{name}: expected a contiguous {dtype} tensor {list(shape)} on {device}, got {t.dtype} "
+def _whole(where: str, name: str, t, shape, dtype, index) -> int:
+    """Checks a contiguous tensor of the given shape; returns its address."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        _bad(where, f"{name}: expected a contiguous {dtype} tensor {list(shape)} on device {index}, got {t.dtype} "
                     f"{list(t.shape)} on {t.device}, strides {t.stride()}")
+    return t.data_ptr()
 
 
-def _on(where: str, device, stream):
+def _on(where: str, index: int, stream) -> int:
     """The stream to launch on; the tensors' device must be the current one."""
-    if device.type != "cuda":
-        _bad(where, f"CUDA tensors expected, got {device}")
-    if device.index != torch.cuda.current_device():
-        _bad(where, f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    if index < 0:
+        _bad(where, "CUDA tensors expected")
+    if index != torch._C._cuda_getDevice():
+        _bad(where, f"the tensors are on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(index)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def kt_layernorm_forward(X, gamma, beta, eps, Y, mean=None, rstd=None, stream=None) -> None:
     """Y = layer norm of the rows of X; mean and rstd (fp32 [M]) receive the statistics if given."""
     w = "kt_layernorm_forward"
-    if X.dim() != 2:
-        _bad(w, f"X: a matrix expected, got {list(X.shape)}")
-    (M, D), dev, dt = X.shape, X.device, X.dtype
-    code = _dtype(w, X)
-    ldx, ldy = _matrix(w, "X", X, M, D, dt, dev), _matrix(w, "Y", Y, M, D, dt, dev)
-    for name, t in (("gamma", gamma), ("beta", beta)):
-        if t is not None:
-            _whole(w, name, t, (D,), dt, dev)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        if t is not None:
-            _whole(w, name, t, (M,), torch.float32, dev)
+    M, D, dev = _size(w, "X", X)
+    code, dt = _dtype(w, X), X.dtype
     s = _on(w, dev, stream)
-    _check(load().kt_layernorm_forward(M, D, code, X.data_ptr(), ldx, _ptr(gamma), _ptr(beta), eps, Y.data_ptr(), ldy,
-                                       _ptr(mean), _ptr(rstd), s), w)
+    ldx, ldy = _rows(w, "X", X, (M, D), dt, dev), _rows(w, "Y", Y, (M, D), dt, dev)
+    if _fwd is None:
+        load()
+    status = _fwd(M, D, code, X.data_ptr(), ldx, None if gamma is None else _whole(w, "gamma", gamma, (D,), dt, dev),
+                  None if beta is None else _whole(w, "beta", beta, (D,), dt, dev), eps, Y.data_ptr(), ldy,
+                  None if mean is None else _whole(w, "mean", mean, (M,), _F32_T, dev),
+                  None if rstd is None else _whole(w, "rstd", rstd, (M,), _F32_T, dev), s)
+    if status:
+        _check(status, w)
 
 
 def kt_layernorm_backward_workspace(M: int, D: int) -> int:
@@ -144,63 +154,60 @@ def kt_layernorm_backward(dY, X, gamma, mean, rstd, dX, dgamma=None, dbeta=None,
     """dX, and with dgamma and dbeta (fp32 [D]) their sums over the rows, which need ``workspace``
     (``layernorm_backward_workspace``)."""
     w = "kt_layernorm_backward"
-    if X.dim() != 2:
-        _bad(w, f"X: a matrix expected, got {list(X.shape)}")
-    (M, D), dev, dt = X.shape, X.device, X.dtype
-    code = _dtype(w, X)
-    ldx, lddy, lddx = (_matrix(w, n, t, M, D, dt, dev) for n, t in (("X", X), ("dY", dY), ("dX", dX)))
-    if gamma is not None:
-        _whole(w, "gamma", gamma, (D,), dt, dev)
-    _whole(w, "mean", mean, (M,), torch.float32, dev)
-    _whole(w, "rstd", rstd, (M,), torch.float32, dev)
-    for name, t in (("dgamma", dgamma), ("dbeta", dbeta)):
-        if t is not None:
-            _whole(w, name, t, (D,), torch.float32, dev)
-    size = 0
-    if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            _bad(w, f"workspace: a contiguous tensor on {dev} expected")
-        size = workspace.numel() * workspace.element_size()
+    M, D, dev = _size(w, "X", X)
+    code, dt, shape = _dtype(w, X), X.dtype, (M, D)
     s = _on(w, dev, stream)
-    _check(load().kt_layernorm_backward(M, D, code, dY.data_ptr(), lddy, X.data_ptr(), ldx, _ptr(gamma), mean.data_ptr(),
-                                        rstd.data_ptr(), dX.data_ptr(), lddx, _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
-                                        size, s), w)
+    ldx, lddy, lddx = _rows(w, "X", X, shape, dt, dev), _rows(w, "dY", dY, shape, dt, dev), _rows(w, "dX", dX, shape, dt, dev)
+    size = at = 0
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            _bad(w, f"workspace: a contiguous tensor on device {dev} expected")
+        size, at = workspace.nbytes, workspace.data_ptr()
+    if _bwd is None:
+        load()
+    status = _bwd(M, D, code, dY.data_ptr(), lddy, X.data_ptr(), ldx,
+                  None if gamma is None else _whole(w, "gamma", gamma, (D,), dt, dev),
+                  _whole(w, "mean", mean, (M,), _F32_T, dev), _whole(w, "rstd", rstd, (M,), _F32_T, dev), dX.data_ptr(), lddx,
+                  None if dgamma is None else _whole(w, "dgamma", dgamma, (D,), _F32_T, dev),
+                  None if dbeta is None else _whole(w, "dbeta", dbeta, (D,), _F32_T, dev), at, size, s)
+    if status:
+        _check(status, w)
 
 
 def kt_quantize_rows(X, Q, scale, act: int = KT_ACT_NONE, stream=None) -> None:
     """Q (int8 [M][K]) and scale (fp32 [M]) of act(X); X is [M][K], or [M][2K] for KT_ACT_GEGLU."""
     w = "kt_quantize_rows"
-    if X.dim() != 2 or Q.dim() != 2:
-        _bad(w, f"X and Q: matrices expected, got {list(X.shape)} and {list(Q.shape)}")
-    M, K, dev = X.shape[0], Q.shape[1], X.device
+    M, K, dev = _size(w, "Q", Q)
     code = _dtype(w, X)
-    ldx = _matrix(w, "X", X, M, 2 * K if act == KT_ACT_GEGLU else K, X.dtype, dev)
-    ldq = _matrix(w, "Q", Q, M, K, torch.int8, dev)
-    _whole(w, "scale", scale, (M,), torch.float32, dev)
     s = _on(w, dev, stream)
-    _check(load().kt_quantize_rows(M, K, code, act, X.data_ptr(), ldx, Q.data_ptr(), ldq, scale.data_ptr(), s), w)
+    ldx = _rows(w, "X", X, (M, 2 * K if act == KT_ACT_GEGLU else K), X.dtype, dev)
+    ldq = _rows(w, "Q", Q, (M, K), _I8_T, dev)
+    if _quant is None:
+        load()
+    status = _quant(M, K, code, act, X.data_ptr(), ldx, Q.data_ptr(), ldq, _whole(w, "scale", scale, (M,), _F32_T, dev), s)
+    if status:
+        _check(status, w)
 
 
 def kt_linear_i8(Q, scale_x, W, scale_w, bias, Y, stream=None) -> None:
     """Y[m][n] = scale_x[m] scale_w[n] sum_k Q[m][k] W[n][k] (+ bias[n])."""
     w = "kt_linear_i8"
-    if Q.dim() != 2 or W.dim() != 2:
-        _bad(w, f"Q and W: matrices expected, got {list(Q.shape)} and {list(W.shape)}")
-    (M, K), N, dev = Q.shape, W.shape[0], Q.device
-    code = _dtype(w, Y)
-    ldq, ldw = _matrix(w, "Q", Q, M, K, torch.int8, dev), _matrix(w, "W", W, N, K, torch.int8, dev)
-    ldy = _matrix(w, "Y", Y, M, N, Y.dtype, dev)
-    _whole(w, "scale_x", scale_x, (M,), torch.float32, dev)
-    _whole(w, "scale_w", scale_w, (N,), torch.float32, dev)
-    if bias is not None:
-        _whole(w, "bias", bias, (N,), Y.dtype, dev)
+    M, K, dev = _size(w, "Q", Q)
+    N = _size(w, "W", W)[0]
+    code, dt = _dtype(w, Y), Y.dtype
+    s = _on(w, dev, stream)
+    ldq, ldw, ldy = _rows(w, "Q", Q, (M, K), _I8_T, dev), _rows(w, "W", W, (N, K), _I8_T, dev), _rows(w, "Y", Y, (M, N), dt, dev)
     if M <= 1:
         ldq = (ldq + 15) // 16 * 16  # the pitch of a single row is never used
     if N <= 1:
         ldw = (ldw + 15) // 16 * 16
-    s = _on(w, dev, stream)
-    _check(load().kt_linear_i8(M, N, K, code, Q.data_ptr(), ldq, W.data_ptr(), ldw, scale_x.data_ptr(),
-                               scale_w.data_ptr(), _ptr(bias), Y.data_ptr(), ldy, s), w)
+    if _lin is None:
+        load()
+    status = _lin(M, N, K, code, Q.data_ptr(), ldq, W.data_ptr(), ldw, _whole(w, "scale_x", scale_x, (M,), _F32_T, dev),
+                  _whole(w, "scale_w", scale_w, (N,), _F32_T, dev),
+                  None if bias is None else _whole(w, "bias", bias, (N,), dt, dev), Y.data_ptr(), ldy, s)
+    if status:
+        _check(status, w)
 
 
 def kt_moe_plan(options: kt_moe_options) -> int:
@@ -210,7 +217,11 @@ def kt_moe_plan(options: kt_moe_options) -> int:
 
 
 def kt_moe_run(plan: int, tensors: kt_moe_tensors, stream=None) -> None:
-    _check(load().kt_moe_run(plan, ctypes.byref(tensors), kt_mlp._stream(stream)), "kt_moe_run")
+    if _moe is None:
+        load()
+    status = _moe(plan, ctypes.byref(tensors), kt_mlp._stream(stream))
+    if status:
+        _check(status, "kt_moe_run")
 
 
 def kt_moe_status(plan: int) -> int:
@@ -237,31 +248,21 @@ class MoePlan:
         self.torch_dtype = torch.float16 if dtype == KT_F16 else torch.bfloat16
 
     def run(self, X, W_router, W_up, W_down, Y, b_up=None, b_down=None, R=None, ids=None, weights=None, stream=None):
-        w, dt, dev = "kt_moe_run", self.torch_dtype, X.device
-        if X.dim() != 2:
-            _bad(w, f"X: a matrix expected, got {list(X.shape)}")
-        T, D, E = X.shape[0], self.D, self.experts
-        ldx = _matrix(w, "X", X, T, D, dt, dev)
+        w, dt = "kt_moe_run", self.torch_dtype
+        T, D, dev = _size(w, "X", X)
+        E, shape, chosen = self.experts, (T, self.D), (T, self.top_k)
+        s = _on(w, dev, stream)
+        ldx = _rows(w, "X", X, shape, dt, dev)
         if T <= 1:
             ldx = (ldx + 7) // 8 * 8  # the pitch of a single row is never used
-        _whole(w, "W_router", W_router, (E, D), dt, dev)
-        _whole(w, "W_up", W_up, (E, self.rows, D), dt, dev)
-        _whole(w, "W_down", W_down, (E, D, self.F), dt, dev)
-        _whole(w, "Y", Y, (T, D), dt, dev)
-        if b_up is not None:
-            _whole(w, "b_up", b_up, (E, self.rows), dt, dev)
-        if b_down is not None:
-            _whole(w, "b_down", b_down, (E, D), dt, dev)
-        if R is not None:
-            _whole(w, "R", R, (T, D), dt, dev)
-        if ids is not None:
-            _whole(w, "ids", ids, (T, self.top_k), torch.int32, dev)
-        if weights is not None:
-            _whole(w, "weights", weights, (T, self.top_k), torch.float32, dev)
-        s = _on(w, dev, stream)
-        kt_moe_run(self.handle, kt_moe_tensors(T, X.data_ptr(), ldx, W_router.data_ptr(), W_up.data_ptr(),
-                                               W_down.data_ptr(), _ptr(b_up), _ptr(b_down), _ptr(R), Y.data_ptr(),
-                                               _ptr(ids), _ptr(weights)), s)
+        kt_moe_run(self.handle, kt_moe_tensors(
+            T, X.data_ptr(), ldx, _whole(w, "W_router", W_router, (E, D), dt, dev),
+            _whole(w, "W_up", W_up, (E, self.rows, D), dt, dev), _whole(w, "W_down", W_down, (E, D, self.F), dt, dev),
+            None if b_up is None else _whole(w, "b_up", b_up, (E, self.rows), dt, dev),
+            None if b_down is None else _whole(w, "b_down", b_down, (E, D), dt, dev),
+            None if R is None else _whole(w, "R", R, shape, dt, dev), _whole(w, "Y", Y, shape, dt, dev),
+            None if ids is None else _whole(w, "ids", ids, chosen, _I32_T, dev),
+            None if weights is None else _whole(w, "weights", weights, chosen, _F32_T, dev)), s)
 
     def status(self) -> int:
         return kt_moe_status(self.handle)
