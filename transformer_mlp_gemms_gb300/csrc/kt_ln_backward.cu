@@ -13,6 +13,8 @@
 namespace kt {
 namespace {
 
+__device__ __forceinline__ float of_pair(const f32x2& v, int e) { return e & 1 ? v.y : v.x; }
+
 template <int DT, int W, int V, bool VEC>
 __global__ void __launch_bounds__(row_block(W), 1) kt_ln_backward_kernel(const LnBackward p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -32,13 +34,13 @@ __global__ void __launch_bounds__(row_block(W), 1) kt_ln_backward_kernel(const L
     int row = (int)blockIdx.x * teams + team;
     int turn = 0;
 
-    float dg[kSmemSums ? 1 : 8 * V], db[kSmemSums ? 1 : 8 * V];
+    f32x2 dg[kSmemSums ? 1 : 4 * V], db[kSmemSums ? 1 : 4 * V];
     if constexpr (kSmemSums) {
         for (int i = threadIdx.x; i < 2 * TL * V * 8; i += row_block(W)) sums[i] = 0.0f;
         __syncthreads();
     } else {
 #pragma unroll
-        for (int i = 0; i < 8 * V; ++i) dg[i] = db[i] = 0.0f;
+        for (int i = 0; i < 4 * V; ++i) dg[i] = db[i] = f2(0.0f);
     }
     uint4 cx[V], cy[V], gw[V];
     float mean = 0.0f, rstd = 0.0f, next_mean = 0.0f, next_rstd = 0.0f;
@@ -69,49 +71,57 @@ __global__ void __launch_bounds__(row_block(W), 1) kt_ln_backward_kernel(const L
                 ny[s] = load_slot<VEC>(dY + (int64_t)next * p.lddy, s, l, TL, D);
             }
         }
-        float s1 = 0.0f, s2 = 0.0f;
+        const f32x2 mu = f2(mean), scale = f2(rstd);
+        f32x2 a1 = f2(0.0f), a2 = f2(0.0f);
 #pragma unroll
         for (int s = 0; s < V; ++s) {
-            float x[8], y[8], g[8];
-            unpack8<DT>(cx[s], x);
-            unpack8<DT>(cy[s], y);
-            if (affine) unpack8<DT>(gw[s], g);
+            f32x2 x[4], y[4], g[4];
+            unpack_pairs<DT>(cx[s], x);
+            unpack_pairs<DT>(cy[s], y);
+            if (affine) unpack_pairs<DT>(gw[s], g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float xh = (x[e] - mean) * rstd;
-                const float ge = affine ? y[e] * g[e] : y[e];
-                s1 += ge;
-                s2 = fmaf(ge, xh, s2);
+            for (int e = 0; e < 4; ++e) {
+                // columns past the row's end have dy = 0 and add nothing to either average
+                const f32x2 xh = f2_mul<true>(f2_sub<true>(x[e], mu), scale);
+                const f32x2 ge = affine ? f2_mul<true>(y[e], g[e]) : y[e];
+                a1 = f2_add<true>(a1, ge);
+                a2 = f2_fma<true>(ge, xh, a2);
                 if constexpr (kSmemSums) {
                     if (want) {
-                        float* at = sums + (size_t)(s * 8 + e) * TL + l;
-                        at[0] = fmaf(y[e], xh, at[0]);
-                        at[TL * V * 8] += y[e];
+                        float* at = sums + (size_t)(s * 8 + 2 * e) * TL + l;
+                        at[0] = fmaf(y[e].x, xh.x, at[0]);
+                        at[TL] = fmaf(y[e].y, xh.y, at[TL]);
+                        at[TL * V * 8] += y[e].x;
+                        at[TL * V * 8 + TL] += y[e].y;
                     }
                 } else {
-                    dg[8 * s + e] = fmaf(y[e], xh, dg[8 * s + e]);
-                    db[8 * s + e] += y[e];
+                    dg[4 * s + e] = f2_fma<true>(y[e], xh, dg[4 * s + e]);
+                    db[4 * s + e] = f2_add<true>(db[4 * s + e], y[e]);
                 }
             }
         }
+        float s1 = a1.x + a1.y, s2 = a2.x + a2.y;
         team_add2<W>(s1, s2, lines, turn, team);
-        s1 *= inv;
-        s2 *= inv;
+        const f32x2 c1 = f2(s1 * inv), c2 = f2(s2 * inv);
+        forget_unpacked(cx);
+        forget_unpacked(cy);
+        if (affine) forget_unpacked(gw);
         uint16_t* xr = dX + (int64_t)row * p.lddx;
 #pragma unroll
         for (int s = 0; s < V; ++s) {
-            float x[8], y[8], g[8];
-            unpack8<DT>(cx[s], x);
-            unpack8<DT>(cy[s], y);
-            if (affine) unpack8<DT>(gw[s], g);
+            f32x2 x[4], y[4], g[4];
+            unpack_pairs<DT>(cx[s], x);
+            unpack_pairs<DT>(cy[s], y);
+            if (affine) unpack_pairs<DT>(gw[s], g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float xh = (x[e] - mean) * rstd;
-                const float ge = affine ? y[e] * g[e] : y[e];
-                y[e] = rstd * (ge - fmaf(xh, s2, s1));
+            for (int e = 0; e < 4; ++e) {
+                const f32x2 xh = f2_mul<true>(f2_sub<true>(x[e], mu), scale);
+                const f32x2 ge = affine ? f2_mul<true>(y[e], g[e]) : y[e];
+                y[e] = f2_mul<true>(scale, f2_sub<true>(ge, f2_fma<true>(xh, c2, c1)));
             }
-            store_slot<VEC>(xr, s, l, TL, D, pack8<DT>(y));
+            store_slot<VEC>(xr, s, l, TL, D, pack_pairs<DT>(y));
         }
+        if (affine) forget_unpacked(gw);
         row = next;
         mean = next_mean;
         rstd = next_rstd;
@@ -143,7 +153,7 @@ __global__ void __launch_bounds__(row_block(W), 1) kt_ln_backward_kernel(const L
                         if constexpr (kSmemSums)
                             out[c] = sums[(size_t)which * TL * V * 8 + (size_t)(s * 8 + e) * TL + l];
                         else
-                            out[c] = which ? db[8 * s + e] : dg[8 * s + e];
+                            out[c] = which ? of_pair(db[4 * s + e / 2], e) : of_pair(dg[4 * s + e / 2], e);
                     }
                 }
         } else {
@@ -153,7 +163,8 @@ __global__ void __launch_bounds__(row_block(W), 1) kt_ln_backward_kernel(const L
             for (int s = 0; s < V; ++s)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    sums[team * width + (8 * s + e) * TL + l] = which ? db[8 * s + e] : dg[8 * s + e];
+                    sums[team * width + (8 * s + e) * TL + l] =
+                        which ? of_pair(db[4 * s + e / 2], e) : of_pair(dg[4 * s + e / 2], e);
             __syncthreads();
             for (int i = threadIdx.x; i < width; i += row_block(W)) {
                 // i counts (element of a lane, lane): the columns in the teams' order

@@ -53,28 +53,37 @@ __global__ void __launch_bounds__(row_block(W), W == 16 ? 1 : 2) kt_ln_forward_k
 #pragma unroll
             for (int s = 0; s < V; ++s) n[s] = load_slot<VEC>(X + (int64_t)next * p.ldx, s, l, TL, D);
         }
-        float sum = 0.0f, none = 0.0f;
+        const f32x2 origin = f2(x0);
+        f32x2 acc = f2(0.0f);
 #pragma unroll
         for (int s = 0; s < V; ++s) {
-            float f[8];
-            unpack8<DT>(c[s], f);
+            f32x2 f[4];
+            unpack_pairs<DT>(c[s], f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (slot_col<VEC>(s, e, l, TL) < D) sum += f[e] - x0;
-        }
-        team_add2<W>(sum, none, lines, turn, team);
-        const float dmean = sum * inv;  // mean - x0
-        float sq = 0.0f;
-#pragma unroll
-        for (int s = 0; s < V; ++s) {
-            float f[8];
-            unpack8<DT>(c[s], f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float d = (f[e] - x0) - dmean;
-                if (slot_col<VEC>(s, e, l, TL) < D) sq = fmaf(d, d, sq);
+            for (int e = 0; e < 4; ++e) {
+                f32x2 d = f2_sub<true>(f[e], origin);
+                clear_past_end<VEC, W, V>(d, s, e, l, D);
+                acc = f2_add<true>(acc, d);
             }
         }
+        float sum = acc.x + acc.y, none = 0.0f;
+        team_add2<W>(sum, none, lines, turn, team);
+        const float dmean = sum * inv;  // mean - x0
+        const f32x2 shift = f2(dmean);
+        forget_unpacked(c);
+        acc = f2(0.0f);
+#pragma unroll
+        for (int s = 0; s < V; ++s) {
+            f32x2 f[4];
+            unpack_pairs<DT>(c[s], f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f32x2 d = f2_sub<true>(f2_sub<true>(f[e], origin), shift);
+                clear_past_end<VEC, W, V>(d, s, e, l, D);
+                acc = f2_fma<true>(d, d, acc);
+            }
+        }
+        float sq = acc.x + acc.y;
         none = 0.0f;
         team_add2<W>(sq, none, lines, turn, team);
         const float rstd = 1.0f / sqrtf(sq * inv + p.eps);
@@ -82,21 +91,27 @@ __global__ void __launch_bounds__(row_block(W), W == 16 ? 1 : 2) kt_ln_forward_k
             if (p.mean) p.mean[row] = x0 + dmean;
             if (p.rstd) p.rstd[row] = rstd;
         }
+        const f32x2 scale = f2(rstd);
+        forget_unpacked(c);
         uint16_t* yr = Y + (int64_t)row * p.ldy;
 #pragma unroll
         for (int s = 0; s < V; ++s) {
-            float f[8], y[8];
-            unpack8<DT>(c[s], f);
+            f32x2 f[4];
+            unpack_pairs<DT>(c[s], f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = ((f[e] - x0) - dmean) * rstd;
+            for (int e = 0; e < 4; ++e) f[e] = f2_mul<true>(f2_sub<true>(f2_sub<true>(f[e], origin), shift), scale);
             if (affine) {
-                float g[8], b[8];
-                unpack8<DT>(gw[s], g);
-                unpack8<DT>(bw[s], b);
+                f32x2 g[4], b[4];
+                unpack_pairs<DT>(gw[s], g);
+                unpack_pairs<DT>(bw[s], b);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = fmaf(y[e], g[e], b[e]);
+                for (int e = 0; e < 4; ++e) f[e] = f2_fma<true>(f[e], g[e], b[e]);
             }
-            store_slot<VEC>(yr, s, l, TL, D, pack8<DT>(y));
+            store_slot<VEC>(yr, s, l, TL, D, pack_pairs<DT>(f));
+        }
+        if (affine) {
+            forget_unpacked(gw);
+            forget_unpacked(bw);
         }
         if (next >= p.M) break;
         row = next;

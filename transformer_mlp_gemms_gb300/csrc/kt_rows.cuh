@@ -39,6 +39,24 @@ __device__ __forceinline__ int slot_col(int s, int e, int l, int TL) {
     return VEC ? 8 * (s * TL + l) + e : (8 * s + e) * TL + l;
 }
 
+// Whether slot s is full for every lane at any D that gets this shape (row_shape, with_shape):
+// with 16-byte loads all but the last of one warp's, and the first two of a wider team's.
+template <bool VEC, int W, int V>
+__device__ __forceinline__ constexpr bool slot_full(int s) {
+    return VEC && (W == 1 ? s + 1 < V : s < 2);
+}
+// Sets the elements of slot s past the row's end to zero.
+template <bool VEC, int W, int V>
+__device__ __forceinline__ void clear_past_end(f32x2& d, int s, int pair, int l, int D) {
+    if (slot_full<VEC, W, V>(s)) return;
+    if (VEC) {  // a 16-byte slot is in the row or not as a whole
+        if (slot_col<true>(s, 0, l, 32 * W) >= D) d = f2(0.0f);
+    } else {
+        if (slot_col<false>(s, 2 * pair, l, 32 * W) >= D) d.x = 0.0f;
+        if (slot_col<false>(s, 2 * pair + 1, l, 32 * W) >= D) d.y = 0.0f;
+    }
+}
+
 template <bool VEC>
 __device__ __forceinline__ uint4 load_slot(const uint16_t* __restrict__ row, int s, int l, int TL, int D) {
     uint4 w = make_uint4(0u, 0u, 0u, 0u);
@@ -70,6 +88,26 @@ __device__ __forceinline__ void store_slot(uint16_t* __restrict__ row, int s, in
             if (c < D) row[c] = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
         }
     }
+}
+
+// A slot's 8 values as pairs, for the paired fp32 instructions.
+template <int DT>
+__device__ __forceinline__ void unpack_pairs(const uint4& w, f32x2 (&f)[4]) {
+    float t[8];
+    unpack8<DT>(w, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2(t[2 * i], t[2 * i + 1]);
+}
+template <int DT>
+__device__ __forceinline__ uint4 pack_pairs(const f32x2 (&f)[4]) {
+    return make_uint4(pack2<DT>(f[0].x, f[0].y), pack2<DT>(f[1].x, f[1].y), pack2<DT>(f[2].x, f[2].y), pack2<DT>(f[3].x, f[3].y));
+}
+// Makes the next unpacking of these slots a new one: the unpacked values of an earlier pass would
+// take four times the packed ones' registers to keep.
+template <int V>
+__device__ __forceinline__ void forget_unpacked(uint4 (&c)[V]) {
+#pragma unroll
+    for (int s = 0; s < V; ++s) asm volatile("" : "+r"(c[s].x), "+r"(c[s].y), "+r"(c[s].z), "+r"(c[s].w));
 }
 
 template <int DT>
