@@ -196,48 +196,62 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
     const int mine = tiles > (int)blockIdx.x ? (tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
     const int total = mine * kblocks;  // k-blocks of all this CTA's tiles, in order
 
-    if (warp < kTcTokenWarps + kTcChannelWarps) {
-        // ------------------- producers: bytes from global memory, fp16 to the operands -------------------
-        constexpr int kUnits = BN / 64;  // channels: 16-byte pieces per thread and k-block
-        const bool tokens = warp < kTcTokenWarps;
-        const int u0 = (int)threadIdx.x - kTcTokenWarps * 32;  // channel piece u: row u / 4, bytes 16 (u % 4)
-        uint4 reg[kTcAhead][4];  // tokens: a 16-byte piece of 4 rows; channels: up to 3 pieces
-        // load cursor: k-block l of the CTA's sequence
-        int l_tile = (int)blockIdx.x, l_kb = 0;
-        const int g = lane >> 2, q4 = lane & 3;
-        int l_m0 = 0, l_n0 = 0;
-        auto load = [&](uint4 (&r)[4]) {
-            if (l_kb == 0) {
-                l_m0 = (l_tile / tiles_n) * 128 + warp * 32 + g;
-                l_n0 = (l_tile % tiles_n) * BN;
-            }
-            const int k = l_kb * 64;
-            if (tokens) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    r[j] = make_uint4(0u, 0u, 0u, 0u);
-                    if (l_m0 + 8 * j < p.M && k + 16 * q4 < p.K)
-                        r[j] = __ldg(reinterpret_cast<const uint4*>(p.Q + (int64_t)(l_m0 + 8 * j) * p.ldq + k + 16 * q4));
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < kUnits; ++j) {
-                    const int u = u0 + j * kTcChannelWarps * 32, n = l_n0 + (u >> 2), kk = k + 16 * (u & 3);
-                    r[j] = make_uint4(0u, 0u, 0u, 0u);
-                    if (n < p.N && kk < p.K) r[j] = __ldg(reinterpret_cast<const uint4*>(p.W + (int64_t)n * p.ldw + kk));
-                }
-            }
-            if (++l_kb == kblocks) {
-                l_kb = 0;
-                l_tile += (int)gridDim.x;
+    // A producer's loop over the CTA's k-blocks: pieces of kTcAhead k-blocks in registers; the piece
+    // of one k-block is converted when its stage is free, and the registers reloaded.
+    auto produce = [&](auto&& open_tile, auto&& load, auto&& convert) {
+        uint4 reg[kTcAhead][4];
+        int tile = (int)blockIdx.x, kb = 0;  // the next k-block to load
+        auto fetch = [&](uint4 (&r)[4]) {
+            if (kb == 0) open_tile((tile / tiles_n) * 128, (tile % tiles_n) * BN);
+            load(r, kb * 64);
+            if (++kb == kblocks) {
+                kb = 0;
+                tile += (int)gridDim.x;
             }
         };
         uint32_t stage = 0, phase = 0;
-        auto convert = [&](uint4 (&r)[4]) -> bool {
-            bool ok = wait_phase(bar(sm.empty[stage]), phase ^ 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_PRODUCER, kLimit);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) return false;
-            if (tokens) {
+#pragma unroll
+        for (int u = 0; u < kTcAhead; ++u)
+            if (u < total) fetch(reg[u]);
+        int left = total;
+        while (left > 0) {
+#pragma unroll
+            for (int u = 0; u < kTcAhead; ++u) {
+                if (left <= 0) break;
+                const bool ok = wait_phase(bar(sm.empty[stage]), phase ^ 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_PRODUCER, kLimit);
+                if (!__all_sync(0xffffffffu, ok)) return;
+                convert(reg[u], stage);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(sm.full[stage]));
+                if (++stage == kTcStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+                if (left > kTcAhead) fetch(reg[u]);
+                --left;
+            }
+        }
+    };
+    if (warp < kTcTokenWarps) {
+        // ------------------- tokens: bytes from global memory, fp16 to tensor memory -------------------
+        const int8_t* row = nullptr;  // row g of the warp's 32, at this lane's 16 bytes
+        int rows = 0;                 // rows from there on
+        const int64_t pitch8 = 8 * p.ldq;
+        const int k_end = p.K - 16 * (lane & 3);
+        produce(
+            [&](int m0, int) {
+                const int m = m0 + warp * 32 + (lane >> 2);
+                rows = p.M - m;
+                row = p.Q + (int64_t)m * p.ldq + 16 * (lane & 3);
+            },
+            [&](uint4 (&r)[4], int k) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    r[j] = make_uint4(0u, 0u, 0u, 0u);
+                    if (8 * j < rows && k < k_end) r[j] = __ldg(reinterpret_cast<const uint4*>(row + j * pitch8 + k));
+                }
+            },
+            [&](const uint4 (&r)[4], uint32_t stage) {
                 tc_fence_after();
 #pragma unroll
                 for (int j = 0; j < 4; j += 2) {  // rows g + 8 j and g + 8 j + 8 of the warp's 32
@@ -253,12 +267,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
                 }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
-            } else {
-                const uint32_t base = smem_u32(sm.b[stage]);
+            });
+    } else if (warp < kTcTokenWarps + kTcChannelWarps) {
+        // ------------------- channels: bytes from global memory, fp16 to shared memory -------------------
+        // 16-byte piece u of a k-block: row u / 4, bytes 16 (u % 4); this thread's pieces are 64 rows apart
+        constexpr int kUnits = BN / 64;
+        const int u0 = (int)threadIdx.x - kTcTokenWarps * 32, q4 = u0 & 3, n_in = u0 >> 2;
+        const int8_t* row = nullptr;
+        int rows = 0;
+        const int64_t pitch64 = 64 * p.ldw;
+        const int k_end = p.K - 16 * q4;
+        const uint32_t dst = smem_u32(sm.b[0]) + (uint32_t)n_in * 128u + 4u * q4, swz = (uint32_t)(n_in & 7) << 4;
+        produce(
+            [&](int, int n0) {
+                rows = p.N - (n0 + n_in);
+                row = p.W + (int64_t)(n0 + n_in) * p.ldw + 16 * q4;
+            },
+            [&](uint4 (&r)[4], int k) {
 #pragma unroll
                 for (int j = 0; j < kUnits; ++j) {
-                    const int u = u0 + j * kTcChannelWarps * 32, n = u >> 2;
-                    const uint32_t row = base + (uint32_t)n * 128u + 4u * (u & 3);
+                    r[j] = make_uint4(0u, 0u, 0u, 0u);
+                    if (64 * j < rows && k < k_end) r[j] = __ldg(reinterpret_cast<const uint4*>(row + j * pitch64 + k));
+                }
+            },
+            [&](const uint4 (&r)[4], uint32_t stage) {
+                const uint32_t at = dst + stage * (uint32_t)(BN * 128);
+#pragma unroll
+                for (int j = 0; j < kUnits; ++j) {
                     uint32_t h[8];
                     bytes_to_halves(r[j].x, h[0], h[1]);
                     bytes_to_halves(r[j].y, h[2], h[3]);
@@ -268,31 +303,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
                     // lane c holds bytes 16 c .. + 15 and fills columns c, c + 4, ...
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + ((i ^ (n & 7u)) << 4)), "r"(h[i]) : "memory");
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + j * 64u * 128u + (((uint32_t)i << 4) ^ swz)), "r"(h[i]) : "memory");
                 }
                 fence_async_smem();  // the tensor cores read it through the async proxy
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(sm.full[stage]));
-            if (++stage == kTcStages) {
-                stage = 0;
-                phase ^= 1u;
-            }
-            return true;
-        };
-#pragma unroll
-        for (int u = 0; u < kTcAhead; ++u)
-            if (u < total) load(reg[u]);
-        bool ok = true;
-        for (int i = 0; i < total && ok; i += kTcAhead) {
-#pragma unroll
-            for (int u = 0; u < kTcAhead; ++u) {
-                if (i + u < total && ok) {
-                    ok = convert(reg[u]);
-                    if (ok && i + u + kTcAhead < total) load(reg[u]);
-                }
-            }
-        }
+            });
     } else if (warp == 16) {
         // ------------------- one thread issues the products -------------------
         if (lane == 0) {
