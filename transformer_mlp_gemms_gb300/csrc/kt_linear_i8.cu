@@ -100,26 +100,30 @@ __global__ void __launch_bounds__(kDotWarps * 32) kt_linear_i8_dot_kernel(const 
 // per element.
 //
 // One persistent CTA per SM, tiles of 128 tokens x BN channels, k-blocks of 64:
-//   warps 0-3    tokens: 16-byte pieces of the tokens' rows from global memory, three k-blocks
-//                ahead in registers, stored as fp16 into tensor memory, where the product reads
-//                its first operand (32 columns per stage, 4 stages; four lanes of a warp share a
-//                row, and as a sum over k may take its terms in any order, each lane's 16 bytes
-//                go to the columns that the lane owns, and the channels follow suit).  That
-//                operand never passes through shared memory, whose bandwidth would bound the
-//                kernel: 128 x 192 x 64 takes the tensor cores 384 cycles, writing and reading
-//                the second operand takes shared memory the same 384, and the first one's 16 KB
-//                would add 256.
-//   warps 4-11   channels: 16-byte pieces of the weight's rows, three k-blocks ahead, into shared
-//                memory as fp16, K-major with the 128-byte swizzle;
-//   warp 16      one thread issues tcgen05.mma (fp16, fp32 accumulators, two buffers of BN
-//                columns, so that a tile's epilogue runs beside the next tile's products);
-//   warps 12-15  epilogue: accumulator x token scale x channel scale (+ bias), one rounding,
-//                rows of 64 columns put together in shared memory and stored as full lines.
+//   warps 0-7    tokens: rows of 128 bytes (4 lanes x 32) from global memory, stored as fp16 into
+//                tensor memory, where the product reads its first operand (32 columns per stage of
+//                64, 4 stages).  That operand never passes through shared memory, whose bandwidth
+//                would bound the kernel: 128 x 192 x 64 takes the tensor cores 384 cycles, writing
+//                and reading the second operand takes shared memory the same 384, the first one's
+//                16 KB would add 256;
+//   warps 8-15   channels: rows of the weight likewise, into shared memory as fp16, K-major with
+//                the 128-byte swizzle.  Both kinds are two groups of four warps that take the
+//                steps of 128 columns in turn, so that one's loads arrive while the other converts;
+//   warps 16-19  epilogue: accumulator x token scale x channel scale (+ bias), one rounding,
+//                rows of 64 columns put together in shared memory and stored as full lines;
+//   warp 20      one thread issues tcgen05.mma (fp16, fp32 accumulators, two buffers of BN
+//                columns, so that a tile's epilogue runs beside the next tile's products).
+// A sum over k may take its terms in any order.  So the bytes of a step go where their lanes' places
+// in tensor memory are (lane c of a row's four: words 2 c and 2 c + 1 of every eight; the first 16
+// of its 32 bytes in one stage, the others in the next), and the channels follow the same order.
 // Four bytes become two pairs of fp16 in five instructions: with the sign bit flipped a byte is
 // q + 128, and next to the byte 0x64 it is the fp16 number 1024 + (q + 128); 1152 is subtracted.
-constexpr int kTcStages = 4, kTcAhead = 3;
-constexpr int kTcTokenWarps = 4, kTcChannelWarps = 8, kTcEpiWarps = 4;
-constexpr int kTcThreads = (kTcTokenWarps + kTcChannelWarps + kTcEpiWarps + 1) * 32;
+constexpr int kTcStages = 4;  // of 64 columns; a step of 128 columns is two
+constexpr int kTcGroups = 2;  // producers of even and of odd steps
+constexpr int kTcTokenWarps = 4, kTcChannelWarps = 4, kTcEpiWarps = 4;  // tokens, channels: per group
+constexpr int kTcChannel0 = kTcGroups * kTcTokenWarps, kTcEpi0 = kTcChannel0 + kTcGroups * kTcChannelWarps;
+constexpr int kTcMmaWarp = kTcEpi0 + kTcEpiWarps, kTcThreads = (kTcMmaWarp + 1) * 32;
+static_assert(kTcStages == 2 * kTcGroups && kTcEpi0 % 4 == 0, "a group's step has two stages of its own; epilogue warp q: lanes 32 q");
 constexpr uint32_t kTcACol = 384;  // tensor-memory column of the first operand's stages
 __device__ int g_linear_i8_error;  // a bounded wait that ran out (never in normal operation)
 
@@ -130,15 +134,30 @@ __device__ __forceinline__ void bytes_to_halves(uint32_t w, uint32_t& lo, uint32
     asm("sub.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(big));
 }
 
-// 16 rows x 32 columns into tensor memory: lane 4 r + c holds columns c, c + 4, ... of row r in
-// its even registers and of row r + 8 in its odd ones.
+// 16 rows x 32 columns into tensor memory: lane 4 r + c holds, of every eight columns, 2 c and
+// 2 c + 1: of row r in the first two of four registers, of row r + 8 in the other two.
 __device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
             taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+// 32 bytes at p: one load where every row starts on a 32-byte boundary, else two.  Bytes at or
+// past `left` are zeros (left is a multiple of 16).
+__device__ __forceinline__ void load32(const int8_t* p, int left, bool wide, uint4& a, uint4& b) {
+    a = b = make_uint4(0u, 0u, 0u, 0u);
+    if (wide) {
+        if (left > 0)
+            asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                         : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                         : "l"(p));
+    } else {
+        if (left > 0) a = __ldg(reinterpret_cast<const uint4*>(p));
+        if (left > 16) b = __ldg(reinterpret_cast<const uint4*>(p + 16));
+    }
 }
 
 // The product with its first operand in tensor memory.
@@ -185,129 +204,130 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_smem();
     }
-    if (warp == 16) tmem_alloc<1>(smem_u32(&sm.tmem), kTmemCols);
+    if (warp == kTcMmaWarp) tmem_alloc<1>(smem_u32(&sm.tmem), kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int kblocks = (p.K + 63) / 64;
+    const int steps = (p.K + 127) / 128, kblocks = 2 * steps;
     const int mine = tiles > (int)blockIdx.x ? (tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
-    const int total = mine * kblocks;  // k-blocks of all this CTA's tiles, in order
+    const int total = mine * steps;  // steps of all this CTA's tiles, in order
 
-    // A producer's loop over the CTA's k-blocks: pieces of kTcAhead k-blocks in registers; the piece
-    // of one k-block is converted when its stage is free, and the registers reloaded.
-    auto produce = [&](auto&& open_tile, auto&& load, auto&& convert) {
-        uint4 reg[kTcAhead][4];
-        int tile = (int)blockIdx.x, kb = 0;  // the next k-block to load
-        auto fetch = [&](uint4 (&r)[4]) {
-            if (kb == 0) open_tile((tile / tiles_n) * 128, (tile % tiles_n) * BN);
-            load(r, kb * 64);
-            if (++kb == kblocks) {
-                kb = 0;
+    // A producer group's loop over its steps of 128 columns, every kTcGroups-th of the CTA's: N
+    // pieces of 32 bytes per thread in registers; when their stages are free, the pieces' first
+    // halves are converted into one and the second halves into the other, and the next step's
+    // loads go out, to arrive while the other group converts.
+    auto produce = [&](auto pieces, int group, auto&& open_tile, auto&& load, auto&& convert) {
+        constexpr int N = decltype(pieces)::value;
+        uint4 reg[2][N];
+        int tile = (int)blockIdx.x, k = group, opened = -1;
+        auto fetch = [&]() {
+            while (k >= steps) {
+                k -= steps;
                 tile += (int)gridDim.x;
             }
+            if (tile != opened) {
+                open_tile((tile / tiles_n) * 128, (tile % tiles_n) * BN);
+                opened = tile;
+            }
+            load(reg, k * 128);
+            k += kTcGroups;
         };
-        uint32_t stage = 0, phase = 0;
+        uint32_t phase = 0;
+        if (group < total) fetch();
+        for (int s = group; s < total; s += kTcGroups, phase ^= 1u) {
 #pragma unroll
-        for (int u = 0; u < kTcAhead; ++u)
-            if (u < total) fetch(reg[u]);
-        int left = total;
-        while (left > 0) {
-#pragma unroll
-            for (int u = 0; u < kTcAhead; ++u) {
-                if (left <= 0) break;
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t stage = 2u * group + h;
                 const bool ok = wait_phase(bar(sm.empty[stage]), phase ^ 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_PRODUCER, kLimit);
                 if (!__all_sync(0xffffffffu, ok)) return;
-                convert(reg[u], stage);
+                convert(reg[h], stage);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(sm.full[stage]));
-                if (++stage == kTcStages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-                if (left > kTcAhead) fetch(reg[u]);
-                --left;
             }
+            if (s + kTcGroups < total) fetch();
         }
     };
-    if (warp < kTcTokenWarps) {
+    const bool wide_q = ((reinterpret_cast<uintptr_t>(p.Q) | (uintptr_t)p.ldq | (uintptr_t)p.K) & 31u) == 0;
+    const bool wide_w = ((reinterpret_cast<uintptr_t>(p.W) | (uintptr_t)p.ldw | (uintptr_t)p.K) & 31u) == 0;
+    if (warp < kTcChannel0) {
         // ------------------- tokens: bytes from global memory, fp16 to tensor memory -------------------
-        const int8_t* row = nullptr;  // row g of the warp's 32, at this lane's 16 bytes
+        const int8_t* row = nullptr;  // row lane / 4 of the warp's 32, at this lane's 32 bytes of a step
         int rows = 0;                 // rows from there on
+        const int q = warp & 3;  // rows and tensor-memory lanes 32 q .. + 31
         const int64_t pitch8 = 8 * p.ldq;
-        const int k_end = p.K - 16 * (lane & 3);
+        const int k_end = p.K - 32 * (lane & 3);
         produce(
+            std::integral_constant<int, 4>{}, warp / kTcTokenWarps,
             [&](int m0, int) {
-                const int m = m0 + warp * 32 + (lane >> 2);
+                const int m = m0 + q * 32 + (lane >> 2);
                 rows = p.M - m;
-                row = p.Q + (int64_t)m * p.ldq + 16 * (lane & 3);
+                row = p.Q + (int64_t)m * p.ldq + 32 * (lane & 3);
             },
-            [&](uint4 (&r)[4], int k) {
+            [&](uint4 (&r)[2][4], int k) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    r[j] = make_uint4(0u, 0u, 0u, 0u);
-                    if (8 * j < rows && k < k_end) r[j] = __ldg(reinterpret_cast<const uint4*>(row + j * pitch8 + k));
-                }
+                for (int j = 0; j < 4; ++j) load32(row + j * pitch8 + k, 8 * j < rows ? k_end - k : 0, wide_q, r[0][j], r[1][j]);
             },
             [&](const uint4 (&r)[4], uint32_t stage) {
                 tc_fence_after();
 #pragma unroll
-                for (int j = 0; j < 4; j += 2) {  // rows g + 8 j and g + 8 j + 8 of the warp's 32
+                for (int j = 0; j < 4; j += 2) {  // rows lane / 4 + 8 j and + 8 j + 8 of the warp's 32
                     uint32_t h[16];
 #pragma unroll
                     for (int o = 0; o < 2; ++o) {
-                        bytes_to_halves(r[j + o].x, h[o], h[2 + o]);
-                        bytes_to_halves(r[j + o].y, h[4 + o], h[6 + o]);
-                        bytes_to_halves(r[j + o].z, h[8 + o], h[10 + o]);
-                        bytes_to_halves(r[j + o].w, h[12 + o], h[14 + o]);
+                        bytes_to_halves(r[j + o].x, h[2 * o], h[2 * o + 1]);
+                        bytes_to_halves(r[j + o].y, h[2 * o + 4], h[2 * o + 5]);
+                        bytes_to_halves(r[j + o].z, h[2 * o + 8], h[2 * o + 9]);
+                        bytes_to_halves(r[j + o].w, h[2 * o + 12], h[2 * o + 13]);
                     }
-                    tmem_st_16x32(tmem + ((uint32_t)(warp * 32 + 8 * j) << 16) + kTcACol + stage * 32u, h);
+                    tmem_st_16x32(tmem + ((uint32_t)(q * 32 + 8 * j) << 16) + kTcACol + stage * 32u, h);
                 }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
             });
-    } else if (warp < kTcTokenWarps + kTcChannelWarps) {
+    } else if (warp < kTcEpi0) {
         // ------------------- channels: bytes from global memory, fp16 to shared memory -------------------
-        // 16-byte piece u of a k-block: row u / 4, bytes 16 (u % 4); this thread's pieces are 64 rows apart
-        constexpr int kUnits = BN / 64;
-        const int u0 = (int)threadIdx.x - kTcTokenWarps * 32, q4 = u0 & 3, n_in = u0 >> 2;
+        // a warp's 8 rows in the order 0 2 4 6 1 3 5 7, so that the 16 lanes of a store's half
+        // touch all banks; this thread's rows are 32 apart
+        constexpr int kPieces = BN / 32;
+        const int c = lane & 3, r8 = lane >> 2, n_in = (warp & 3) * 8 + ((r8 & 3) << 1 | r8 >> 2);
         const int8_t* row = nullptr;
         int rows = 0;
-        const int64_t pitch64 = 64 * p.ldw;
-        const int k_end = p.K - 16 * q4;
-        const uint32_t dst = smem_u32(sm.b[0]) + (uint32_t)n_in * 128u + 4u * q4, swz = (uint32_t)(n_in & 7) << 4;
+        const int64_t pitch32 = 32 * p.ldw;
+        const int k_end = p.K - 32 * c;
+        // words 2 c and 2 c + 1 of every eight: chunk 2 i + c / 2 of the row, swizzled by its number
+        const uint32_t dst = smem_u32(sm.b[0]) + (uint32_t)n_in * 128u + 8u * (c & 1);
+        const uint32_t first = (uint32_t)((c >> 1) ^ (n_in & 7)) << 4;
         produce(
+            std::integral_constant<int, kPieces>{}, (warp - kTcChannel0) / kTcChannelWarps,
             [&](int, int n0) {
                 rows = p.N - (n0 + n_in);
-                row = p.W + (int64_t)(n0 + n_in) * p.ldw + 16 * q4;
+                row = p.W + (int64_t)(n0 + n_in) * p.ldw + 32 * c;
             },
-            [&](uint4 (&r)[4], int k) {
+            [&](uint4 (&r)[2][kPieces], int k) {
 #pragma unroll
-                for (int j = 0; j < kUnits; ++j) {
-                    r[j] = make_uint4(0u, 0u, 0u, 0u);
-                    if (64 * j < rows && k < k_end) r[j] = __ldg(reinterpret_cast<const uint4*>(row + j * pitch64 + k));
-                }
+                for (int j = 0; j < kPieces; ++j)
+                    load32(row + j * pitch32 + k, 32 * j < rows ? k_end - k : 0, wide_w, r[0][j], r[1][j]);
             },
-            [&](const uint4 (&r)[4], uint32_t stage) {
+            [&](const uint4 (&r)[kPieces], uint32_t stage) {
                 const uint32_t at = dst + stage * (uint32_t)(BN * 128);
 #pragma unroll
-                for (int j = 0; j < kUnits; ++j) {
-                    uint32_t h[8];
-                    bytes_to_halves(r[j].x, h[0], h[1]);
-                    bytes_to_halves(r[j].y, h[2], h[3]);
-                    bytes_to_halves(r[j].z, h[4], h[5]);
-                    bytes_to_halves(r[j].w, h[6], h[7]);
-                    // pair i goes to chunk i, word u % 4: the tokens' order of a k-block, whose
-                    // lane c holds bytes 16 c .. + 15 and fills columns c, c + 4, ...
+                for (int j = 0; j < kPieces; ++j) {
+                    const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + j * 64u * 128u + (((uint32_t)i << 4) ^ swz)), "r"(h[i]) : "memory");
+                    for (int i = 0; i < 4; ++i) {  // four bytes: two words
+                        uint32_t lo, hi;
+                        bytes_to_halves(w[i], lo, hi);
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + j * 32u * 128u + (first ^ (uint32_t)(2 * i) << 4)),
+                                     "r"(lo), "r"(hi)
+                                     : "memory");
+                    }
                 }
                 fence_async_smem();  // the tensor cores read it through the async proxy
             });
-    } else if (warp == 16) {
+    } else if (warp == kTcMmaWarp) {
         // ------------------- one thread issues the products -------------------
         if (lane == 0) {
             uint32_t stage = 0, phase = 0;
@@ -339,7 +359,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
         }
     } else {
         // ------------------- epilogue -------------------
-        const int q = warp & 3, ew = warp - 12;
+        const int q = warp & 3, ew = warp - kTcEpi0;
         uint8_t* out = sm.out[ew];
         uint16_t* Y = static_cast<uint16_t*>(p.Y);
         for (int t = 0; t < mine; ++t) {
@@ -360,32 +380,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
             tc_fence_after();
 #pragma unroll 1
             for (int c0 = 0; c0 < BN; c0 += 64) {
-                uint32_t w[32];
-#pragma unroll
+                __syncwarp();  // the previous columns' stores have read the buffer
+#pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     uint32_t r[32];
                     tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * (uint32_t)BN + c0 + 32 * half, r);
                     tmem_wait_ld_only();
                     reg_fence32(r);
+                    // 16-byte chunk i of row r at chunk i ^ (r & 7): no bank conflicts either way
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float4 c = *reinterpret_cast<const float4*>(&sm.ch[buf][c0 + 32 * half + i]);
-                        w[16 * half + i / 2] = pack2<DT>(fmaf(__uint_as_float(r[i]), sx * c.x, c.y),
-                                                         fmaf(__uint_as_float(r[i + 1]), sx * c.z, c.w));
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 c = *reinterpret_cast<const float4*>(&sm.ch[buf][c0 + 32 * half + 8 * i + 2 * e]);
+                            w[e] = pack2<DT>(fmaf(__uint_as_float(r[8 * i + 2 * e]), sx * c.x, c.y),
+                                             fmaf(__uint_as_float(r[8 * i + 2 * e + 1]), sx * c.z, c.w));
+                        }
+                        *reinterpret_cast<uint4*>(out + lane * 128 + (((4 * half + i) ^ (lane & 7)) << 4)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
-                if (c0 + 64 >= BN) {  // the last columns are in registers: the next tile may have the buffer
+                if (c0 + 64 >= BN) {  // the last columns have been read: the next tile may have the buffer
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(sm.acc_empty[buf]));
                 }
                 if (m0 >= p.M) continue;
-                // 16-byte chunk i of row r at chunk i ^ (r & 7): no bank conflicts either way
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    *reinterpret_cast<uint4*>(out + lane * 128 + ((i ^ (lane & 7)) << 4)) =
-                        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 __syncwarp();
                 const int n = n0 + c0;
                 if (wide_y) {
@@ -411,7 +432,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 16) {
+    if (warp == kTcMmaWarp) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc<1>(tmem, kTmemCols);
