@@ -122,7 +122,7 @@ constexpr int kTcStages = 4;  // of 64 columns; a step of 128 columns is two
 constexpr int kTcGroups = 2;  // producers of even and of odd steps
 constexpr int kTcTokenWarps = 4, kTcChannelWarps = 4, kTcEpiWarps = 4;  // tokens, channels: per group
 constexpr int kTcChannel0 = kTcGroups * kTcTokenWarps, kTcEpi0 = kTcChannel0 + kTcGroups * kTcChannelWarps;
-constexpr int kTcMmaWarp = kTcEpi0 + kTcEpiWarps, kTcThreads = (kTcMmaWarp + 1) * 32;
+constexpr int kTcMmaWarp = kTcEpi0 + kTcEpiWarps, kTcThreads = (kTcMmaWarp + kTcStages) * 32;
 static_assert(kTcStages == 2 * kTcGroups && kTcEpi0 % 4 == 0, "a group's step has two stages of its own; epilogue warp q: lanes 32 q");
 constexpr uint32_t kTcACol = 384;  // tensor-memory column of the first operand's stages
 __device__ int g_linear_i8_error;  // a bounded wait that ran out (never in normal operation)
@@ -160,20 +160,35 @@ __device__ __forceinline__ void load32(const int8_t* p, int left, bool wide, uin
     }
 }
 
-// The product with its first operand in tensor memory.
+// The product with its first operand in tensor memory (PAIR = 2: 128 rows in each CTA's, half of
+// the channels in each CTA's shared memory, at the same places).
+template <int PAIR>
 __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
+    if constexpr (PAIR == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+template <int PAIR>
+__device__ __forceinline__ void commit_ta(uint32_t bar) {
+    if constexpr (PAIR == 2) mma_commit_pair(bar);
+    else mma_commit(bar);
 }
 
-template <int BN>
+template <int BN, int PAIR>
 struct TcSmem {
-    alignas(1024) uint8_t b[kTcStages][BN * 128];   // [channel][64 fp16], 128-byte swizzle
+    alignas(1024) uint8_t b[kTcStages][BN / PAIR * 128];  // [channel][64 fp16], 128-byte swizzle
     alignas(128) uint8_t out[kTcEpiWarps][32 * 128];  // a warp's 32 rows x 64 columns of the output
     float2 ch[2][BN];                               // channel scale and bias of the tile
     alignas(8) uint64_t full[kTcStages], empty[kTcStages], acc_full[2], acc_empty[2], drain;
@@ -181,38 +196,44 @@ struct TcSmem {
     int abort;
 };
 
-template <int DT, int BN>
+template <int DT, int BN, int PAIR>
 __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const LinearI8 p, int tiles_n, int tiles, uint32_t idesc,
                                                                         int wide_y) {
     extern __shared__ uint8_t raw[];
-    TcSmem<BN>& sm = *reinterpret_cast<TcSmem<BN>*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+    using Smem = TcSmem<BN, PAIR>;
+    constexpr int kShare = BN / PAIR;  // channels whose weights this CTA stages
+    Smem& sm = *reinterpret_cast<Smem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int* abort_flag = &sm.abort;
     constexpr unsigned long long kLimit = 4000000000ull;  // 4 s: far beyond any legitimate wait
     auto bar = [&](uint64_t& b) { return smem_u32(&b); };
+    const int rank = PAIR == 2 ? (int)cluster_ctarank() : 0;
+    const int unit = (int)blockIdx.x / PAIR, units = (int)gridDim.x / PAIR;  // CTAs or pairs
     if (threadIdx.x == 0) {
         for (int s = 0; s < kTcStages; ++s) {
-            mbar_init(bar(sm.full[s]), kTcTokenWarps + kTcChannelWarps);
+            // the first CTA of a pair also waits for the other's forwarded arrival
+            mbar_init(bar(sm.full[s]), kTcTokenWarps + kTcChannelWarps + (PAIR == 2 && rank == 0 ? 1 : 0));
             mbar_init(bar(sm.empty[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar(sm.acc_full[b]), 1);
-            mbar_init(bar(sm.acc_empty[b]), kTcEpiWarps);
+            mbar_init(bar(sm.acc_empty[b]), kTcEpiWarps * PAIR);
         }
         mbar_init(bar(sm.drain), 1);
         sm.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_smem();
     }
-    if (warp == kTcMmaWarp) tmem_alloc<1>(smem_u32(&sm.tmem), kTmemCols);
+    if (warp == kTcMmaWarp) tmem_alloc<PAIR>(smem_u32(&sm.tmem), kTmemCols);
     tc_fence_before();
     __syncthreads();
+    if (PAIR == 2) cluster_sync_relaxed();  // the other CTA's barriers are initialised before any signal to them
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int steps = (p.K + 127) / 128, kblocks = 2 * steps;
-    const int mine = tiles > (int)blockIdx.x ? (tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+    const int mine = tiles > unit ? (tiles - 1 - unit) / units + 1 : 0;
     const int total = mine * steps;  // steps of all this CTA's tiles, in order
 
     // A producer group's loop over its steps of 128 columns, every kTcGroups-th of the CTA's: N
@@ -222,14 +243,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
     auto produce = [&](auto pieces, int group, auto&& open_tile, auto&& load, auto&& convert) {
         constexpr int N = decltype(pieces)::value;
         uint4 reg[2][N];
-        int tile = (int)blockIdx.x, k = group, opened = -1;
+        int tile = unit, k = group, opened = -1;
         auto fetch = [&]() {
             while (k >= steps) {
                 k -= steps;
-                tile += (int)gridDim.x;
+                tile += units;
             }
             if (tile != opened) {
-                open_tile((tile / tiles_n) * 128, (tile % tiles_n) * BN);
+                open_tile((tile / tiles_n * PAIR + rank) * 128, (tile % tiles_n) * BN + rank * kShare);
                 opened = tile;
             }
             load(reg, k * 128);
@@ -291,7 +312,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
         // ------------------- channels: bytes from global memory, fp16 to shared memory -------------------
         // a warp's 8 rows in the order 0 2 4 6 1 3 5 7, so that the 16 lanes of a store's half
         // touch all banks; this thread's rows are 32 apart
-        constexpr int kPieces = BN / 32;
+        constexpr int kPieces = kShare / 32;
         const int c = lane & 3, r8 = lane >> 2, n_in = (warp & 3) * 8 + ((r8 & 3) << 1 | r8 >> 2);
         const int8_t* row = nullptr;
         int rows = 0;
@@ -312,7 +333,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
                     load32(row + j * pitch32 + k, 32 * j < rows ? k_end - k : 0, wide_w, r[0][j], r[1][j]);
             },
             [&](const uint4 (&r)[kPieces], uint32_t stage) {
-                const uint32_t at = dst + stage * (uint32_t)(BN * 128);
+                const uint32_t at = dst + stage * (uint32_t)(kShare * 128);
 #pragma unroll
                 for (int j = 0; j < kPieces; ++j) {
                     const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
@@ -327,33 +348,48 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
                 }
                 fence_async_smem();  // the tensor cores read it through the async proxy
             });
-    } else if (warp == kTcMmaWarp) {
-        // ------------------- one thread issues the products -------------------
-        if (lane == 0) {
+    } else if (warp >= kTcMmaWarp) {
+        if (PAIR == 2 && rank == 1) {
+            // ------------------- the pair's second CTA: its full stages are told to the first -------------------
+            // (an arrival that orders what came before it at cluster scope costs its thread about
+            // 0.35 us, as long as a stage takes: one thread per stage)
+            if (lane == 0) {
+                const int s = warp - kTcMmaWarp;
+                const uint32_t first = mapa_rank(bar(sm.full[s]), 0u);
+                uint32_t phase = 0;
+                for (int i = s; i < 2 * total; i += kTcStages, phase ^= 1u) {
+                    if (!wait_phase(bar(sm.full[s]), phase, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_MMA, kLimit)) break;
+                    tc_fence_after();
+                    tc_fence_before();
+                    mbar_arrive_cluster(first);
+                }
+            }
+        } else if (warp == kTcMmaWarp && lane == 0) {
+            // ------------------- one thread issues the products -------------------
             uint32_t stage = 0, phase = 0;
             bool ok = true;
             for (int t = 0; t < mine && ok; ++t) {
                 const uint32_t buf = t & 1u, use = (uint32_t)t >> 1;
-                ok = wait_phase(bar(sm.acc_empty[buf]), (use & 1u) ^ 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_MMA, kLimit);
+                ok = wait_phase<PAIR == 2>(bar(sm.acc_empty[buf]), (use & 1u) ^ 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_MMA, kLimit);
                 for (int kb = 0; kb < kblocks && ok; ++kb) {
-                    ok = wait_phase(bar(sm.full[stage]), phase, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_MMA, kLimit);
+                    ok = wait_phase<PAIR == 2>(bar(sm.full[stage]), phase, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_MMA, kLimit);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t bd = smem_desc(smem_u32(sm.b[stage]), 16u, 1024u);
                     const uint32_t a = tmem + kTcACol + stage * 32u;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_f16_ta(tmem + buf * (uint32_t)BN, a + 8u * k, bd + (uint64_t)(2 * k), idesc, kb > 0 || k > 0);
-                    mma_commit(bar(sm.empty[stage]));
+                        mma_f16_ta<PAIR>(tmem + buf * (uint32_t)BN, a + 8u * k, bd + (uint64_t)(2 * k), idesc, kb > 0 || k > 0);
+                    commit_ta<PAIR>(bar(sm.empty[stage]));
                     if (++stage == kTcStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
-                if (ok) mma_commit(bar(sm.acc_full[buf]));
+                if (ok) commit_ta<PAIR>(bar(sm.acc_full[buf]));
             }
             if (!ok) {  // no product may still be running when tensor memory is freed
-                mma_commit(bar(sm.drain));
+                commit_ta<PAIR>(bar(sm.drain));
                 wait_drain(bar(sm.drain), 0u, 100000000ull);
             }
         }
@@ -363,8 +399,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
         uint8_t* out = sm.out[ew];
         uint16_t* Y = static_cast<uint16_t*>(p.Y);
         for (int t = 0; t < mine; ++t) {
-            const int tile = (int)blockIdx.x + t * (int)gridDim.x;
-            const int m0 = (tile / tiles_n) * 128 + q * 32, n0 = (tile % tiles_n) * BN;
+            const int tile = unit + t * units;
+            const int m0 = (tile / tiles_n * PAIR + rank) * 128 + q * 32, n0 = (tile % tiles_n) * BN;
             const uint32_t buf = t & 1u, use = (uint32_t)t >> 1;
             for (int i = ew * 32 + lane; i < BN; i += kTcEpiWarps * 32) {
                 float2 c = make_float2(0.0f, 0.0f);
@@ -404,7 +440,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
                 if (c0 + 64 >= BN) {  // the last columns have been read: the next tile may have the buffer
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(sm.acc_empty[buf]));
+                    if (lane == 0) {
+                        if (rank == 0) mbar_arrive(bar(sm.acc_empty[buf]));
+                        else mbar_arrive_cluster_relaxed(mapa_rank(bar(sm.acc_empty[buf]), 0u));
+                    }
                 }
                 if (m0 >= p.M) continue;
                 __syncwarp();
@@ -432,25 +471,39 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
     }
     tc_fence_before();
     __syncthreads();
+    if (PAIR == 2) cluster_sync_all();  // neither CTA leaves while the other may still signal it
     if (warp == kTcMmaWarp) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc<1>(tmem, kTmemCols);
+        tmem_dealloc<PAIR>(tmem, kTmemCols);
     }
 }
 
-template <int BN>
+template <int BN, int PAIR>
 kt_status launch_tc(int dtype, const LinearI8& p, int sms, int device, void* stream, const char** why) {
-    const int tiles_m = (p.M + 127) / 128, tiles_n = (p.N + BN - 1) / BN, tiles = tiles_m * tiles_n;
+    const int tiles_m = (p.M + 128 * PAIR - 1) / (128 * PAIR), tiles_n = (p.N + BN - 1) / BN, tiles = tiles_m * tiles_n;
     // whole 16-byte pieces of Y's rows: the last one too, as N is a multiple of 8
     const int wide = p.N % 8 == 0 && p.ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(p.Y) & 15u) == 0;
-    auto kern = dtype == KT_BF16 ? kt_linear_i8_tc_kernel<KT_BF16, BN> : kt_linear_i8_tc_kernel<KT_F16, BN>;
-    constexpr int smem = (int)sizeof(TcSmem<BN>) + 1024;
+    auto kern = dtype == KT_BF16 ? kt_linear_i8_tc_kernel<KT_BF16, BN, PAIR> : kt_linear_i8_tc_kernel<KT_F16, BN, PAIR>;
+    constexpr int smem = (int)sizeof(TcSmem<BN, PAIR>) + 1024;
     static SmemOptIn opt_in[2];  // by dtype
     cudaError_t e = opt_in[dtype == KT_BF16](kern, smem, device);
-    if (e == cudaSuccess)
-        e = launch_pdl(kern, (unsigned)std::min(tiles, sms), kTcThreads, smem, stream, p, tiles_n, tiles,
-                       make_idesc(KT_F16, BN, 128, 1), wide);
+    if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(std::min(tiles, sms / PAIR) * PAIR), 1, 1);
+        cfg.blockDim = dim3(kTcThreads, 1, 1);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = static_cast<cudaStream_t>(stream);
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = PAIR;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = PAIR == 2 ? 2 : 1;
+        e = cudaLaunchKernelEx(&cfg, kern, p, tiles_n, tiles, make_idesc(KT_F16, BN, 128 * PAIR, 1), wide);
+    }
     if (e != cudaSuccess) {
         *why = cudaGetErrorString(e);
         return KT_ERR_CUDA;
@@ -462,13 +515,19 @@ kt_status launch_tc(int dtype, const LinearI8& p, int sms, int device, void* str
 
 kt_status launch_linear_i8(int dtype, const LinearI8& p, int sms, int device, void* stream, const char** why) {
     if (p.M > kDotTokens) {
-        // tile width: the fewest rounds over the SMs, each costing its products' cycles
-        const int64_t tm = (p.M + 127) / 128;
-        auto cost = [&](int bn, int per) { return ((tm * ((p.N + bn - 1) / bn) + sms - 1) / sms) * per; };
+        // tile width: the fewest rounds over the CTAs (or pairs), each costing its products' cycles
+        const int pair = p.M > 128 ? 2 : 1;
+        const int64_t tm = (p.M + 128 * pair - 1) / (128 * pair), units = sms / pair;
+        auto cost = [&](int bn, int per) { return ((tm * ((p.N + bn - 1) / bn) + units - 1) / units) * per; };
         const int64_t c192 = cost(192, 384), c128 = cost(128, 290), c64 = cost(64, 220);
-        if (c192 <= c128 && c192 <= c64) return launch_tc<192>(dtype, p, sms, device, stream, why);
-        if (c128 <= c64) return launch_tc<128>(dtype, p, sms, device, stream, why);
-        return launch_tc<64>(dtype, p, sms, device, stream, why);
+        if (pair == 2) {
+            if (c192 <= c128 && c192 <= c64) return launch_tc<192, 2>(dtype, p, sms, device, stream, why);
+            if (c128 <= c64) return launch_tc<128, 2>(dtype, p, sms, device, stream, why);
+            return launch_tc<64, 2>(dtype, p, sms, device, stream, why);
+        }
+        if (c192 <= c128 && c192 <= c64) return launch_tc<192, 1>(dtype, p, sms, device, stream, why);
+        if (c128 <= c64) return launch_tc<128, 1>(dtype, p, sms, device, stream, why);
+        return launch_tc<64, 1>(dtype, p, sms, device, stream, why);
     }
     const int chunk = std::min(kDotChunk, (p.K + 127) & ~127);
     const dim3 grid((unsigned)((p.N + kDotRows - 1) / kDotRows), (unsigned)((p.M + kDotTokens - 1) / kDotTokens));
