@@ -97,7 +97,7 @@ kt_status kt_quantize_rows(int64_t M, int64_t K, kt_dtype dtype, kt_act act, con
  * for K <= 1024; for longer rows unless |Q| and |W| are near 127 throughout with equal signs),
  * and beyond that rounded as fp32 sums are.  One rounding to dtype at the end.
  */
-#define KT_LINEAR_I8_DOT_ROWS 8
+#define KT_LINEAR_I8_DOT_ROWS 16
 kt_status kt_linear_i8(int64_t M, int64_t N, int64_t K, kt_dtype dtype, const int8_t* Q, int64_t ldq, const int8_t* W,
                        int64_t ldw, const float* scale_x, const float* scale_w, const void* bias, void* Y, int64_t ldy,
                        void* stream);

@@ -21,51 +21,82 @@ __device__ __forceinline__ float from_bits(uint16_t u) {
 // tokens in four-way integer products into 32-bit sums.  Eight lanes share a weight row (128
 // consecutive bytes per step), a warp covers 8 rows, and the tokens' rows are in shared
 // memory, read as 128-byte broadcasts to the four groups of a warp.
-constexpr int kDotWarps = 4, kDotTokens = KT_LINEAR_I8_DOT_ROWS, kDotRows = kDotWarps * 8;
-constexpr int kDotChunk = 4096;  // columns of the tokens staged at a time
+constexpr int kDotWarps = 4, kDotTokens = 8;
+constexpr int kDotAhead = 4;     // steps of 128 columns in registers
+constexpr int kDotChunk = 4096;  // columns of the tokens staged at a time, a multiple of kDotAhead * 128
 
-template <int DT>
+template <int DT, int KS>
 __global__ void __launch_bounds__(kDotWarps * 32) kt_linear_i8_dot_kernel(const LinearI8 p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(16) int8_t sq[];  // [8][chunk]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane >> 3, k8 = lane & 7;
-    const int n0 = (int)blockIdx.x * kDotRows + warp * 8 + group * 2;
+    constexpr int kDotRows = kDotWarps / KS * 8, kStep = kDotAhead * 128;
+    const int split = warp % KS;  // this warp's steps: every KS-th
+    const int n0 = (int)blockIdx.x * kDotRows + warp / KS * 8 + group * 2;
     const int m0 = (int)blockIdx.y * kDotTokens;
     const int tokens = min(kDotTokens, p.M - m0);
     const int8_t* w0 = p.W + (int64_t)min(n0, p.N - 1) * p.ldw;
     const int8_t* w1 = p.W + (int64_t)min(n0 + 1, p.N - 1) * p.ldw;
+    // the block's weights start on their way to L2 while the kernel before this one still runs
+    // (a prefetch reads nothing)
+    for (int i = threadIdx.x; i < kDotRows * ((p.K + 127) / 128); i += kDotWarps * 32) {
+        const int n = (int)blockIdx.x * kDotRows + i % kDotRows;
+        if (n < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.W + (int64_t)n * p.ldw + i / kDotRows * 128));
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int acc[2][kDotTokens];
 #pragma unroll
     for (int t = 0; t < kDotTokens; ++t) acc[0][t] = acc[1][t] = 0;
-    for (int k0 = 0; k0 < p.K; k0 += kDotChunk) {
-        const int kc = min(kDotChunk, p.K - k0), kp = (kc + 127) & ~127;  // padded to whole steps with zeros
-        if (k0) __syncthreads();
-        for (int i = threadIdx.x; i < kDotTokens * (kp / 16); i += kDotWarps * 32) {
-            const int t = i / (kp / 16), k = (i % (kp / 16)) * 16;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (t < tokens && k < kc) v = *reinterpret_cast<const uint4*>(p.Q + (int64_t)(m0 + t) * p.ldq + k0 + k);
-            *reinterpret_cast<uint4*>(sq + t * kp + k) = v;
-        }
-        __syncthreads();
-#pragma unroll 4
-        for (int k = k8 * 16; k < kp; k += 128) {
-            uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-            if (k < kc) {
-                a = __ldg(reinterpret_cast<const uint4*>(w0 + k0 + k));
-                b = __ldg(reinterpret_cast<const uint4*>(w1 + k0 + k));
+    // weights of kDotAhead steps of 128 columns in registers, the next ones' loads in flight behind them
+    uint4 a[2][kDotAhead], b[2][kDotAhead];
+    auto load = [&](int k, uint4 (&x)[kDotAhead], uint4 (&y)[kDotAhead]) {
+#pragma unroll
+        for (int u = 0; u < kDotAhead; ++u) {
+            x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (k + 128 * u + k8 * 16 < p.K) {
+                x[u] = __ldg(reinterpret_cast<const uint4*>(w0 + k + 128 * u + k8 * 16));
+                y[u] = __ldg(reinterpret_cast<const uint4*>(w1 + k + 128 * u + k8 * 16));
             }
+        }
+    };
+    load(split * kStep, a[0], b[0]);
+    for (int k0 = 0; k0 < p.K; k0 += kDotChunk) {
+        const int kc = min(kDotChunk, p.K - k0);
+        const int kp = (kc + KS * kStep - 1) / (KS * kStep) * (KS * kStep);  // padded with zeros
+        if (k0) __syncthreads();
+        for (int k = threadIdx.x * 16; k < kp; k += kDotWarps * 32 * 16) {
+            uint4 v[kDotTokens];
 #pragma unroll
             for (int t = 0; t < kDotTokens; ++t) {
-                const uint4 q = *reinterpret_cast<const uint4*>(sq + t * kp + k);
-                acc[0][t] = __dp4a((int)a.x, (int)q.x, acc[0][t]);
-                acc[1][t] = __dp4a((int)b.x, (int)q.x, acc[1][t]);
-                acc[0][t] = __dp4a((int)a.y, (int)q.y, acc[0][t]);
-                acc[1][t] = __dp4a((int)b.y, (int)q.y, acc[1][t]);
-                acc[0][t] = __dp4a((int)a.z, (int)q.z, acc[0][t]);
-                acc[1][t] = __dp4a((int)b.z, (int)q.z, acc[1][t]);
-                acc[0][t] = __dp4a((int)a.w, (int)q.w, acc[0][t]);
-                acc[1][t] = __dp4a((int)b.w, (int)q.w, acc[1][t]);
+                v[t] = make_uint4(0u, 0u, 0u, 0u);
+                if (t < tokens && k < kc) v[t] = *reinterpret_cast<const uint4*>(p.Q + (int64_t)(m0 + t) * p.ldq + k0 + k);
+            }
+#pragma unroll
+            for (int t = 0; t < kDotTokens; ++t) *reinterpret_cast<uint4*>(sq + t * kp + k) = v[t];
+        }
+        __syncthreads();
+        for (int k = split * kStep; k < kp; k += KS * kStep) {
+            load(k0 + k + KS * kStep, a[1], b[1]);
+#pragma unroll
+            for (int u = 0; u < kDotAhead; ++u) {
+                const uint4 x = a[0][u], y = b[0][u];
+#pragma unroll
+                for (int t = 0; t < kDotTokens; ++t) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(sq + t * kp + k + 128 * u + k8 * 16);
+                    acc[0][t] = __dp4a((int)x.x, (int)q.x, acc[0][t]);
+                    acc[1][t] = __dp4a((int)y.x, (int)q.x, acc[1][t]);
+                    acc[0][t] = __dp4a((int)x.y, (int)q.y, acc[0][t]);
+                    acc[1][t] = __dp4a((int)y.y, (int)q.y, acc[1][t]);
+                    acc[0][t] = __dp4a((int)x.z, (int)q.z, acc[0][t]);
+                    acc[1][t] = __dp4a((int)y.z, (int)q.z, acc[1][t]);
+                    acc[0][t] = __dp4a((int)x.w, (int)q.w, acc[0][t]);
+                    acc[1][t] = __dp4a((int)y.w, (int)q.w, acc[1][t]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kDotAhead; ++u) {
+                a[0][u] = a[1][u];
+                b[0][u] = b[1][u];
             }
         }
     }
@@ -81,6 +112,18 @@ __global__ void __launch_bounds__(kDotWarps * 32) kt_linear_i8_dot_kernel(const 
             v += __shfl_xor_sync(0xffffffffu, v, 4);
             if (t == k8) sum[r] = v;
         }
+    if constexpr (KS > 1) {
+        __shared__ int2 part[kDotWarps][32];
+        part[warp][lane] = make_int2(sum[0], sum[1]);
+        __syncthreads();
+        if (split != 0) return;
+#pragma unroll
+        for (int s = 1; s < KS; ++s) {
+            const int2 v = part[warp + s][lane];
+            sum[0] += v.x;
+            sum[1] += v.y;
+        }
+    }
     if (k8 >= tokens) return;
     const float sx = p.sx[m0 + k8];
 #pragma unroll
@@ -479,6 +522,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
     }
 }
 
+template <int KS>
+kt_status launch_dot(int dtype, const LinearI8& p, void* stream, const char** why) {
+    constexpr int rows = kDotWarps / KS * 8, step = KS * kDotAhead * 128;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.N + rows - 1) / rows), (unsigned)((p.M + kDotTokens - 1) / kDotTokens));
+    cfg.blockDim = dim3(kDotWarps * 32, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)kDotTokens * std::min(kDotChunk, (p.K + step - 1) / step * step);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = dtype == KT_BF16 ? cudaLaunchKernelEx(&cfg, kt_linear_i8_dot_kernel<KT_BF16, KS>, p)
+                                           : cudaLaunchKernelEx(&cfg, kt_linear_i8_dot_kernel<KT_F16, KS>, p);
+    if (e != cudaSuccess) {
+        *why = cudaGetErrorString(e);
+        return KT_ERR_CUDA;
+    }
+    return KT_OK;
+}
+
 template <int BN, int PAIR>
 kt_status launch_tc(int dtype, const LinearI8& p, int sms, int device, void* stream, const char** why) {
     const int tiles_m = (p.M + 128 * PAIR - 1) / (128 * PAIR), tiles_n = (p.N + BN - 1) / BN, tiles = tiles_m * tiles_n;
@@ -514,7 +579,7 @@ kt_status launch_tc(int dtype, const LinearI8& p, int sms, int device, void* str
 }  // namespace
 
 kt_status launch_linear_i8(int dtype, const LinearI8& p, int sms, int device, void* stream, const char** why) {
-    if (p.M > kDotTokens) {
+    if (p.M > KT_LINEAR_I8_DOT_ROWS) {
         // tile width: the fewest rounds over the CTAs (or pairs), each costing its products' cycles
         const int pair = p.M > 128 ? 2 : 1;
         const int64_t tm = (p.M + 128 * pair - 1) / (128 * pair), units = sms / pair;
@@ -529,25 +594,12 @@ kt_status launch_linear_i8(int dtype, const LinearI8& p, int sms, int device, vo
         if (c128 <= c64) return launch_tc<128, 1>(dtype, p, sms, device, stream, why);
         return launch_tc<64, 1>(dtype, p, sms, device, stream, why);
     }
-    const int chunk = std::min(kDotChunk, (p.K + 127) & ~127);
-    const dim3 grid((unsigned)((p.N + kDotRows - 1) / kDotRows), (unsigned)((p.M + kDotTokens - 1) / kDotTokens));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kDotWarps * 32, 1, 1);
-    cfg.dynamicSmemBytes = (size_t)kDotTokens * chunk;
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = dtype == KT_BF16 ? cudaLaunchKernelEx(&cfg, kt_linear_i8_dot_kernel<KT_BF16>, p)
-                                     : cudaLaunchKernelEx(&cfg, kt_linear_i8_dot_kernel<KT_F16>, p);
-    if (e != cudaSuccess) {
-        *why = cudaGetErrorString(e);
-        return KT_ERR_CUDA;
-    }
-    return KT_OK;
+    // warps of a block that share a weight row's columns: as many as leave a step of 512 to each and
+    // the SMs with no more than four blocks each
+    auto blocks = [&](int ks) { return (int64_t)((p.N * ks + kDotWarps * 8 - 1) / (kDotWarps * 8)) * ((p.M + kDotTokens - 1) / kDotTokens); };
+    if (p.K > 3 * kDotAhead * 128 && blocks(4) <= 4 * sms) return launch_dot<4>(dtype, p, stream, why);
+    if (p.K > kDotAhead * 128 && blocks(2) <= 4 * sms) return launch_dot<2>(dtype, p, stream, why);
+    return launch_dot<1>(dtype, p, stream, why);
 }
 
 }  // namespace kt

@@ -21,7 +21,7 @@ from .kt_mlp import KT_ACT_GEGLU, KT_ACT_NONE, KT_BF16, KT_ERR_INVALID, KT_F16, 
 _VP, _I64, _I32, _F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
 
 KT_LAYERNORM_MAX_D = 16384
-KT_LINEAR_I8_DOT_ROWS = 8
+KT_LINEAR_I8_DOT_ROWS = 16
 KT_MOE_MAX_TOKENS, KT_MOE_MAX_EXPERTS, KT_MOE_MAX_TOP_K = 64, 256, 16
 
 
