@@ -15,15 +15,25 @@ namespace {
 
 __device__ __forceinline__ float of_pair(const f32x2& v, int e) { return e & 1 ? v.y : v.x; }
 
-template <int DT, int W, int V, bool VEC>
-__global__ void __launch_bounds__(row_block(W), 1) kt_ln_backward_kernel(const LnBackward p) {
+// Resident blocks per SM, and whether a row's xhat and g stay in registers between the averages
+// and dx (else they are computed twice): what the registers allow beside the sums of dgamma and dbeta.
+constexpr int ln_back_per_sm(int W, int V) { return W == 16 ? 1 : V <= 1 ? 3 : V == 2 ? 2 : 1; }
+constexpr bool ln_back_keeps(int W, int V) { return W < 16 && V >= 3; }
+constexpr int kLnBackStagedWarps = 2;  // gamma in shared memory up to so many warps per row
+
+template <int DT, int W, int V, bool VEC, bool RING>
+__global__ void __launch_bounds__(row_block(W), ln_back_per_sm(W, V)) kt_ln_backward_kernel(const LnBackward p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int TL = 32 * W, teams = row_block(W) / TL;
     constexpr bool kSmemSums = W == 16;
-    constexpr bool kAhead = W != 16;  // the next row's loads in flight during this row's sums
+    constexpr bool kAhead = !RING && W != 16;  // the next row's loads in flight during this row's sums
+    constexpr bool kKeep = ln_back_keeps(W, V), kStaged = W <= kLnBackStagedWarps;
     __shared__ TeamLines<W> lines;
-    extern __shared__ float sums[];  // [teams][TL * V * 8] for the final addition, or [2][..] (kSmemSums)
+    // gamma, then the ring; the final addition's [teams][TL * V * 8] where they were; or [2][..] (kSmemSums)
+    extern __shared__ __align__(16) uint8_t smem[];
+    float* sums = reinterpret_cast<float*>(smem);
+    float4* gs = reinterpret_cast<float4*>(smem);
     const int team = threadIdx.x / TL, l = threadIdx.x % TL;
     const uint16_t* X = static_cast<const uint16_t*>(p.X);
     const uint16_t* dY = static_cast<const uint16_t*>(p.dY);
@@ -42,22 +52,45 @@ __global__ void __launch_bounds__(row_block(W), 1) kt_ln_backward_kernel(const L
 #pragma unroll
         for (int i = 0; i < 4 * V; ++i) dg[i] = db[i] = f2(0.0f);
     }
-    uint4 cx[V], cy[V], gw[V];
+    RowRing<W, V, 2> ring;  // x, then dy
+    int slot = 0;
+    const auto copy = [&](int at, int64_t r) {
+        ring.copy(at, 0, X + r * p.ldx, l, D);
+        ring.copy(at, 1, dY + r * p.lddy, l, D);
+    };
+    uint4 cx[V], cy[V], gw[kStaged ? 1 : V];
     float mean = 0.0f, rstd = 0.0f, next_mean = 0.0f, next_rstd = 0.0f;
     if (row < p.M) {
         mean = p.mean[row];
         rstd = p.rstd[row];
+        if constexpr (RING) {
+            ring.open(smem + (kStaged ? staged_bytes(W, V) : 0), team, l);
+#pragma unroll
+            for (int i = 0; i < ring.rows; ++i) {
+                if (p.M - row > (int64_t)i * step) copy(i, row + (int64_t)i * step);
+                ring.commit();
+            }
+        } else
 #pragma unroll
         for (int s = 0; s < V; ++s) {
             cx[s] = load_slot<VEC>(X + (int64_t)row * p.ldx, s, l, TL, D);
             cy[s] = load_slot<VEC>(dY + (int64_t)row * p.lddy, s, l, TL, D);
         }
     }
-    if (affine) {
+    if (kStaged && affine) {
+        stage_vector<DT, VEC, W, V>(static_cast<const uint16_t*>(p.gamma), gs, D);
+        __syncthreads();
+    }
+    if (!kStaged && affine) {
 #pragma unroll
-        for (int s = 0; s < V; ++s) gw[s] = load_slot<VEC>(static_cast<const uint16_t*>(p.gamma), s, l, TL, D);
+        for (int s = 0; s < (kStaged ? 0 : V); ++s) gw[s] = load_slot<VEC>(static_cast<const uint16_t*>(p.gamma), s, l, TL, D);
     }
     while (row < p.M) {
+        if constexpr (RING) {
+            ring.wait_oldest();
+            ring.read(slot, 0, cx);
+            ring.read(slot, 1, cy);
+        }
         const int next = p.M - row > step ? row + step : p.M;
         uint4 nx[V], ny[V];
         if (next < p.M) {
@@ -73,55 +106,80 @@ __global__ void __launch_bounds__(row_block(W), 1) kt_ln_backward_kernel(const L
         }
         const f32x2 mu = f2(mean), scale = f2(rstd);
         f32x2 a1 = f2(0.0f), a2 = f2(0.0f);
-#pragma unroll
-        for (int s = 0; s < V; ++s) {
-            f32x2 x[4], y[4], g[4];
+        f32x2 keep_xh[kKeep ? 4 * V : 1], keep_g[kKeep ? 4 * V : 1];
+        // xhat, dy and g of slot s
+        auto terms = [&](int s, f32x2 (&xh)[4], f32x2 (&y)[4], f32x2 (&ge)[4]) {
+            f32x2 x[4], g[4];
             unpack_pairs<DT>(cx[s], x);
             unpack_pairs<DT>(cy[s], y);
-            if (affine) unpack_pairs<DT>(gw[s], g);
+            if (affine) {
+                if constexpr (kStaged) staged_pairs<W>(gs, s, l, g);
+                else unpack_pairs<DT>(gw[s], g);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                xh[e] = f2_mul<true>(f2_sub<true>(x[e], mu), scale);
+                ge[e] = affine ? f2_mul<true>(y[e], g[e]) : y[e];
+            }
+        };
+#pragma unroll
+        for (int s = 0; s < V; ++s) {
+            f32x2 xh[4], y[4], ge[4];
+            terms(s, xh, y, ge);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 // columns past the row's end have dy = 0 and add nothing to either average
-                const f32x2 xh = f2_mul<true>(f2_sub<true>(x[e], mu), scale);
-                const f32x2 ge = affine ? f2_mul<true>(y[e], g[e]) : y[e];
-                a1 = f2_add<true>(a1, ge);
-                a2 = f2_fma<true>(ge, xh, a2);
+                a1 = f2_add<true>(a1, ge[e]);
+                a2 = f2_fma<true>(ge[e], xh[e], a2);
+                if constexpr (kKeep) {
+                    keep_xh[4 * s + e] = xh[e];
+                    keep_g[4 * s + e] = ge[e];
+                }
                 if constexpr (kSmemSums) {
                     if (want) {
                         float* at = sums + (size_t)(s * 8 + 2 * e) * TL + l;
-                        at[0] = fmaf(y[e].x, xh.x, at[0]);
-                        at[TL] = fmaf(y[e].y, xh.y, at[TL]);
+                        at[0] = fmaf(y[e].x, xh[e].x, at[0]);
+                        at[TL] = fmaf(y[e].y, xh[e].y, at[TL]);
                         at[TL * V * 8] += y[e].x;
                         at[TL * V * 8 + TL] += y[e].y;
                     }
                 } else {
-                    dg[4 * s + e] = f2_fma<true>(y[e], xh, dg[4 * s + e]);
+                    dg[4 * s + e] = f2_fma<true>(y[e], xh[e], dg[4 * s + e]);
                     db[4 * s + e] = f2_add<true>(db[4 * s + e], y[e]);
                 }
             }
         }
         float s1 = a1.x + a1.y, s2 = a2.x + a2.y;
         team_add2<W>(s1, s2, lines, turn, team);
+        if constexpr (RING) {  // this lane has its part of the row: its slots take the row `rows` ahead
+            if (p.M - row > (int64_t)ring.rows * step) copy(slot, (int64_t)row + (int64_t)ring.rows * step);
+            ring.commit();
+            slot = slot + 1 < ring.rows ? slot + 1 : 0;
+        }
         const f32x2 c1 = f2(s1 * inv), c2 = f2(s2 * inv);
-        forget_unpacked(cx);
-        forget_unpacked(cy);
-        if (affine) forget_unpacked(gw);
+        if constexpr (!kKeep) {
+            forget_unpacked(cx);
+            forget_unpacked(cy);
+        }
+        if (!kStaged && affine) forget_unpacked(gw);
         uint16_t* xr = dX + (int64_t)row * p.lddx;
 #pragma unroll
         for (int s = 0; s < V; ++s) {
-            f32x2 x[4], y[4], g[4];
-            unpack_pairs<DT>(cx[s], x);
-            unpack_pairs<DT>(cy[s], y);
-            if (affine) unpack_pairs<DT>(gw[s], g);
+            f32x2 xh[4], y[4], ge[4];
+            if constexpr (kKeep) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const f32x2 xh = f2_mul<true>(f2_sub<true>(x[e], mu), scale);
-                const f32x2 ge = affine ? f2_mul<true>(y[e], g[e]) : y[e];
-                y[e] = f2_mul<true>(scale, f2_sub<true>(ge, f2_fma<true>(xh, c2, c1)));
+                for (int e = 0; e < 4; ++e) {
+                    xh[e] = keep_xh[4 * s + e];
+                    ge[e] = keep_g[4 * s + e];
+                }
+            } else {
+                terms(s, xh, y, ge);
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = f2_mul<true>(scale, f2_sub<true>(ge[e], f2_fma<true>(xh[e], c2, c1)));
             store_slot<VEC>(xr, s, l, TL, D, pack_pairs<DT>(y));
         }
-        if (affine) forget_unpacked(gw);
+        if (!kStaged && affine) forget_unpacked(gw);
         row = next;
         mean = next_mean;
         rstd = next_rstd;
@@ -131,7 +189,7 @@ __global__ void __launch_bounds__(row_block(W), 1) kt_ln_backward_kernel(const L
                 cx[s] = nx[s];
                 cy[s] = ny[s];
             }
-        } else if (row < p.M) {
+        } else if (!RING && row < p.M) {
 #pragma unroll
             for (int s = 0; s < V; ++s) {
                 cx[s] = load_slot<VEC>(X + (int64_t)row * p.ldx, s, l, TL, D);
@@ -158,7 +216,7 @@ __global__ void __launch_bounds__(row_block(W), 1) kt_ln_backward_kernel(const L
                 }
         } else {
             constexpr int width = TL * V * 8;
-            if (which) __syncthreads();
+            __syncthreads();  // every team is done with gamma and its ring; the first sums have been read
 #pragma unroll
             for (int s = 0; s < V; ++s)
 #pragma unroll
@@ -208,12 +266,12 @@ __global__ void __launch_bounds__(256) kt_ln_column_sums_kernel(const float* __r
 
 }  // namespace
 
-// One block per SM: each keeps 8 / W rows in flight and the next ones' loads behind them.
+// As many blocks as are resident: each keeps 8 / W rows in flight and the next ones' loads behind them.
 int ln_backward_blocks(int64_t M, int64_t D) {
     RowShape shape;
     if (M < 0 || D < 1 || !row_shape(D, &shape)) return 0;
     const int teams = row_block(shape.W) / (32 * shape.W);
-    return (int)std::min<int64_t>((M + teams - 1) / teams, kMaxSms);
+    return (int)std::min<int64_t>((M + teams - 1) / teams, (int64_t)kMaxSms * ln_back_per_sm(shape.W, shape.V));
 }
 
 kt_status launch_ln_backward(int dtype, const LnBackward& p, int sms, int device, void* stream, const char** why) {
@@ -222,7 +280,7 @@ kt_status launch_ln_backward(int dtype, const LnBackward& p, int sms, int device
         *why = "rows of this length are not supported";
         return KT_ERR_UNSUPPORTED;
     }
-    const int grid = std::min(ln_backward_blocks(p.M, p.D), sms);
+    const int grid = std::min(ln_backward_blocks(p.M, p.D), sms * ln_back_per_sm(shape.W, shape.V));
     cudaError_t e = cudaSuccess;
     if (grid > 0) {
         const auto al = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; };
@@ -231,13 +289,30 @@ kt_status launch_ln_backward(int dtype, const LnBackward& p, int sms, int device
         auto go = [&](auto dt, auto v16) {
             return with_shape<decltype(v16)::value>(shape, [&](auto W, auto V) -> kt_status {
                 constexpr int w = decltype(W)::value, v = decltype(V)::value, teams = row_block(w) / (32 * w);
-                constexpr size_t smem = (w == 16 ? 2 : teams == 1 ? 0 : teams) * (size_t)(32 * w * v * 8) * sizeof(float);
-                static SmemOptIn opt_in;
-                auto kern = kt_ln_backward_kernel<decltype(dt)::value, w, v, decltype(v16)::value>;
+                constexpr int t = decltype(dt)::value;
+                constexpr bool al16 = decltype(v16)::value;
+                constexpr size_t sums = (w == 16 ? 2 : teams == 1 ? 0 : teams) * (size_t)(32 * w * v * 8) * sizeof(float);
+                constexpr size_t smem = std::max(sums, w <= kLnBackStagedWarps ? (size_t)staged_bytes(w, v) : 0);
                 cudaError_t le = cudaSuccess;
-                if (smem > 32 * 1024)
-                    le = opt_in(kern, (int)smem, device);
-                if (le == cudaSuccess) le = launch_pdl(kern, (unsigned)grid, row_block(w), smem, stream, p);
+                bool ring = false;
+                if constexpr (al16 && w < 16 && ln_back_per_sm(w, v) == 1) {
+                    // from three rows a team on they come through the ring
+                    ring = (int64_t)p.M >= 3 * (int64_t)grid * teams;
+                    if (ring) {
+                        constexpr size_t staged = w <= kLnBackStagedWarps ? (size_t)staged_bytes(w, v) : 0;
+                        constexpr size_t with_ring = std::max(sums, staged + RowRing<w, v, 2>::bytes);
+                        static SmemOptIn opt_in;
+                        auto kern = kt_ln_backward_kernel<t, w, v, true, true>;
+                        le = opt_in(kern, (int)with_ring, device);
+                        if (le == cudaSuccess) le = launch_pdl(kern, (unsigned)grid, row_block(w), with_ring, stream, p);
+                    }
+                }
+                if (!ring) {
+                    static SmemOptIn opt_in;
+                    auto kern = kt_ln_backward_kernel<t, w, v, al16, false>;
+                    if (smem > 32 * 1024) le = opt_in(kern, (int)smem, device);
+                    if (le == cudaSuccess) le = launch_pdl(kern, (unsigned)grid, row_block(w), smem, stream, p);
+                }
                 if (le != cudaSuccess) {
                     *why = cudaGetErrorString(le);
                     return KT_ERR_CUDA;

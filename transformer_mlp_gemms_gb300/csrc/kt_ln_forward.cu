@@ -4,42 +4,58 @@
 //
 // Bound by HBM: 2 D bytes read and 2 D written per row, against 8 operations per element.  A
 // team of warps (kt_rows.cuh) keeps its row in registers, so the row is read once although the
-// variance is a second pass over it; gamma and beta stay in registers as well, from row to row
-// of a persistent grid, and the next row's loads are issued before this row's reductions, so
-// that the memory has something to do while the team waits for its sums.
+// variance is a second pass over it; gamma and beta are in shared memory as fp32 (rows up to 2048
+// columns; registers beyond), and the next row's loads are issued before this row's reductions.
+// What else the time goes to is instructions: the deviations are unpacked once and kept as fp32,
+// two at a time (10 instructions per element before, 5 now: 65536 x 640 36 -> 30 us).
 #include "kt_ops_internal.h"
 #include "kt_rows.cuh"
 
 namespace kt {
 namespace {
 
+constexpr int kLnStagedWarps = 2;
+
+// Resident blocks per SM: as many rows in flight as the registers allow.
+constexpr int ln_per_sm(int W, int V) { return W == 16 ? 1 : V <= 1 ? 5 : V == 2 ? 4 : V == 3 && W <= kLnStagedWarps ? 3 : 2; }
+
 template <int DT, int W, int V, bool VEC>
-__global__ void __launch_bounds__(row_block(W), W == 16 ? 1 : 2) kt_ln_forward_kernel(const LnForward p) {
+__global__ void __launch_bounds__(row_block(W), ln_per_sm(W, V)) kt_ln_forward_kernel(const LnForward p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int TL = 32 * W, teams = row_block(W) / TL;
+    constexpr bool kStaged = W <= kLnStagedWarps;  // gamma and beta in shared memory
     __shared__ TeamLines<W> lines;
     const int team = threadIdx.x / TL, l = threadIdx.x % TL;
     const uint16_t* X = static_cast<const uint16_t*>(p.X);
     uint16_t* Y = static_cast<uint16_t*>(p.Y);
     const int D = p.D, step = (int)gridDim.x * teams;
     const float inv = 1.0f / (float)D;
+    extern __shared__ __align__(16) uint8_t smem[];  // gamma and beta
+    const bool affine = p.gamma != nullptr;
+    float4* gs = reinterpret_cast<float4*>(smem);
+    float4* bs = reinterpret_cast<float4*>(smem + staged_bytes(W, V));
+    if (kStaged && affine) {
+        stage_vector<DT, VEC, W, V>(static_cast<const uint16_t*>(p.gamma), gs, D);
+        stage_vector<DT, VEC, W, V>(static_cast<const uint16_t*>(p.beta), bs, D);
+    }
     int row = (int)blockIdx.x * teams + team;
-    if (row >= p.M) return;  // the whole team: its barriers are its own
     int turn = 0;
 
-    uint4 c[V], gw[V], bw[V];
+    uint4 c[V], gw[kStaged ? 1 : V], bw[kStaged ? 1 : V];
+    uint16_t first = 0, next_first = 0;
+    if (row < p.M) first = X[(int64_t)row * p.ldx];
 #pragma unroll
-    for (int s = 0; s < V; ++s) c[s] = load_slot<VEC>(X + (int64_t)row * p.ldx, s, l, TL, D);
-    uint16_t first = X[(int64_t)row * p.ldx], next_first = 0;
-    const bool affine = p.gamma != nullptr;
-    if (affine) {
+    for (int s = 0; s < V; ++s) c[s] = load_slot<VEC>(X + (int64_t)row * p.ldx, s, l, TL, row < p.M ? D : 0);
+    if (!kStaged && affine) {
 #pragma unroll
-        for (int s = 0; s < V; ++s) {
+        for (int s = 0; s < (kStaged ? 0 : V); ++s) {
             gw[s] = load_slot<VEC>(static_cast<const uint16_t*>(p.gamma), s, l, TL, D);
             bw[s] = load_slot<VEC>(static_cast<const uint16_t*>(p.beta), s, l, TL, D);
         }
     }
+    if (kStaged && affine) __syncthreads();
+    if (row >= p.M) return;  // the whole team: the barriers from here on are its own
     for (;;) {
         // the deviations are taken from the row's first element, exactly: a row far from zero
         // keeps its low bits in the sums
@@ -54,35 +70,31 @@ __global__ void __launch_bounds__(row_block(W), W == 16 ? 1 : 2) kt_ln_forward_k
             for (int s = 0; s < V; ++s) n[s] = load_slot<VEC>(X + (int64_t)next * p.ldx, s, l, TL, D);
         }
         const f32x2 origin = f2(x0);
-        f32x2 acc = f2(0.0f);
+        f32x2 d[4 * V], acc = f2(0.0f);  // the row's deviations
 #pragma unroll
         for (int s = 0; s < V; ++s) {
             f32x2 f[4];
             unpack_pairs<DT>(c[s], f);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                f32x2 d = f2_sub<true>(f[e], origin);
-                clear_past_end<VEC, W, V>(d, s, e, l, D);
-                acc = f2_add<true>(acc, d);
+                d[4 * s + e] = f2_sub<true>(f[e], origin);
+                clear_past_end<VEC, W, V>(d[4 * s + e], s, e, l, D);
+                acc = f2_add<true>(acc, d[4 * s + e]);
             }
         }
         float sum = acc.x + acc.y, none = 0.0f;
         team_add2<W>(sum, none, lines, turn, team);
         const float dmean = sum * inv;  // mean - x0
         const f32x2 shift = f2(dmean);
-        forget_unpacked(c);
         acc = f2(0.0f);
 #pragma unroll
-        for (int s = 0; s < V; ++s) {
-            f32x2 f[4];
-            unpack_pairs<DT>(c[s], f);
+        for (int s = 0; s < V; ++s)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                f32x2 d = f2_sub<true>(f2_sub<true>(f[e], origin), shift);
-                clear_past_end<VEC, W, V>(d, s, e, l, D);
-                acc = f2_fma<true>(d, d, acc);
+                d[4 * s + e] = f2_sub<true>(d[4 * s + e], shift);
+                clear_past_end<VEC, W, V>(d[4 * s + e], s, e, l, D);
+                acc = f2_fma<true>(d[4 * s + e], d[4 * s + e], acc);
             }
-        }
         float sq = acc.x + acc.y;
         none = 0.0f;
         team_add2<W>(sq, none, lines, turn, team);
@@ -92,24 +104,27 @@ __global__ void __launch_bounds__(row_block(W), W == 16 ? 1 : 2) kt_ln_forward_k
             if (p.rstd) p.rstd[row] = rstd;
         }
         const f32x2 scale = f2(rstd);
-        forget_unpacked(c);
         uint16_t* yr = Y + (int64_t)row * p.ldy;
 #pragma unroll
         for (int s = 0; s < V; ++s) {
             f32x2 f[4];
-            unpack_pairs<DT>(c[s], f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = f2_mul<true>(f2_sub<true>(f2_sub<true>(f[e], origin), shift), scale);
+            for (int e = 0; e < 4; ++e) f[e] = f2_mul<true>(d[4 * s + e], scale);
             if (affine) {
                 f32x2 g[4], b[4];
-                unpack_pairs<DT>(gw[s], g);
-                unpack_pairs<DT>(bw[s], b);
+                if constexpr (kStaged) {
+                    staged_pairs<W>(gs, s, l, g);
+                    staged_pairs<W>(bs, s, l, b);
+                } else {
+                    unpack_pairs<DT>(gw[s], g);
+                    unpack_pairs<DT>(bw[s], b);
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) f[e] = f2_fma<true>(f[e], g[e], b[e]);
             }
             store_slot<VEC>(yr, s, l, TL, D, pack_pairs<DT>(f));
         }
-        if (affine) {
+        if (!kStaged && affine) {
             forget_unpacked(gw);
             forget_unpacked(bw);
         }
@@ -133,12 +148,13 @@ kt_status launch_ln_forward(int dtype, const LnForward& p, int sms, void* stream
     const bool vec = p.D % 8 == 0 && p.ldx % 8 == 0 && p.ldy % 8 == 0 && al(p.X) && al(p.Y) && al(p.gamma) && al(p.beta);
     auto go = [&](auto dt, auto v16) {
         return with_shape<decltype(v16)::value>(shape, [&](auto W, auto V) -> kt_status {
-            constexpr int w = decltype(W)::value;
-            const int teams = row_block(w) / (32 * w);
+            constexpr int w = decltype(W)::value, t = decltype(dt)::value, v = decltype(V)::value;
+            constexpr bool al16 = decltype(v16)::value;
+            constexpr int teams = row_block(w) / (32 * w), per_sm = ln_per_sm(w, v);
+            constexpr int staged = w <= kLnStagedWarps ? 2 * staged_bytes(w, v) : 0;
             const int64_t blocks = ((int64_t)p.M + teams - 1) / teams;
-            const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)sms * (w == 16 ? 1 : 2));
-            cudaError_t e = launch_pdl(kt_ln_forward_kernel<decltype(dt)::value, w, decltype(V)::value, decltype(v16)::value>,
-                                       grid, row_block(w), 0, stream, p);
+            const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)sms * per_sm);
+            const cudaError_t e = launch_pdl(kt_ln_forward_kernel<t, w, v, al16>, grid, row_block(w), staged, stream, p);
             if (e != cudaSuccess) {
                 *why = cudaGetErrorString(e);
                 return KT_ERR_CUDA;

@@ -3,9 +3,9 @@
 //
 // Bound by HBM: 2 bytes read and 1 written per element.  The row stays in the registers of a
 // team of warps (kt_rows.cuh) between its largest magnitude and its rounding, so it is read
-// once; the grid is persistent and the next row's loads are in flight behind this row's
-// reduction.  The magnitudes are compared as the integers that their bits are, which orders
-// NaN above infinity above every number, so one maximum also tells whether the row is finite.
+// once; the grid is persistent, and the next rows arrive in a ring behind it.  The magnitudes
+// are compared as the integers that their bits are, which orders NaN above infinity above every
+// number, so one maximum (two 16-bit values at a time) also tells whether the row is finite.
 //
 // The nearest integer is decided exactly without a division per element: v times the rounded
 // inverse of the scale is off by less than 127 * 2^-22 = 3.1e-5, so only a product within
@@ -47,94 +47,142 @@ __device__ __forceinline__ void activate8(int act, float* v, const float* g) {
     }
 }
 
-template <int DT, int W, int V, bool VEC, bool ACT>
-__global__ void __launch_bounds__(row_block(W), W == 16 || ACT ? 1 : 2) kt_quantize_kernel(const QuantRows p) {
+// 8 quotients as integers in the bytes of lo and hi; v holds the values.  `inv`: the scale's
+// rounded inverse, in range.
+__device__ __forceinline__ void quantize8(const f32x2 (&v)[4], float scale, float inv, uint32_t& lo, uint32_t& hi) {
+    // adding 1.5 * 2^23 rounds to the nearest integer, ties to even, in the low bits
+    constexpr float kMagic = 12582912.0f;
+    uint32_t q[8];
+    float off = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const f32x2 t = f2_mul<true>(v[e], f2(inv)), m = f2_add<true>(t, f2(kMagic));
+        const f32x2 d = f2_sub<true>(t, f2_sub<true>(m, f2(kMagic)));
+        off = fmaxf(off, fmaxf(fabsf(d.x), fabsf(d.y)));
+        q[2 * e] = __float_as_uint(m.x);
+        q[2 * e + 1] = __float_as_uint(m.y);
+    }
+    if (off > 0.4999f) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            q[2 * e] = (uint32_t)nearest_by_remainder(v[e].x, scale, (int)(__uint_as_float(q[2 * e]) - kMagic));
+            q[2 * e + 1] = (uint32_t)nearest_by_remainder(v[e].y, scale, (int)(__uint_as_float(q[2 * e + 1]) - kMagic));
+        }
+    }
+    lo = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+    hi = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
+}
+// The same for a scale whose inverse is out of range (a row of subnormals), 0 or NaN.
+__device__ __noinline__ uint32_t quantize4_rare(float a, float b, float c, float d, float scale) {
+    if (!(scale > 0.0f)) return 0u;
+    return (uint32_t)(nearest_by_division(a, scale) & 255) | (uint32_t)(nearest_by_division(b, scale) & 255) << 8 |
+           (uint32_t)(nearest_by_division(c, scale) & 255) << 16 | (uint32_t)(nearest_by_division(d, scale) & 255) << 24;
+}
+
+constexpr int quant_per_sm(int W, bool ACT) { return W == 16 || ACT ? 1 : 2; }
+
+template <int DT, int W, int V, bool VEC, bool ACT, bool RING>
+__global__ void __launch_bounds__(row_block(W), quant_per_sm(W, ACT)) kt_quantize_kernel(const QuantRows p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int TL = 32 * W, teams = row_block(W) / TL;
     __shared__ TeamLines<W> lines;
+    extern __shared__ __align__(16) uint8_t smem[];
     const int team = threadIdx.x / TL, l = threadIdx.x % TL;
     const uint16_t* X = static_cast<const uint16_t*>(p.X);
     const int K = p.K, step = (int)gridDim.x * teams;
+    RowRing<W, V, 1> ring;
+    int slot = 0;
     int row = (int)blockIdx.x * teams + team;
     if (row >= p.M) return;  // the whole team: its barriers are its own
     int turn = 0;
-    uint4 c[V];
+    if constexpr (RING) {
+        ring.open(smem, team, l);
 #pragma unroll
-    for (int s = 0; s < V; ++s) c[s] = load_slot<VEC>(X + (int64_t)row * p.ldx, s, l, TL, K);
-    for (;;) {
-        const int next = p.M - row > step ? row + step : p.M;
-        uint4 n[V];
-        if (next < p.M) {
-#pragma unroll
-            for (int s = 0; s < V; ++s) n[s] = load_slot<VEC>(X + (int64_t)next * p.ldx, s, l, TL, K);
+        for (int i = 0; i < ring.rows; ++i) {
+            if (p.M - row > (int64_t)i * step) ring.copy(i, 0, X + ((int64_t)row + (int64_t)i * step) * p.ldx, l, K);
+            ring.commit();
         }
-        float a[ACT ? 8 * V : 8];  // ACT: the row's activated values
+    }
+    for (; row < p.M; row = p.M - row > step ? row + step : p.M) {
+        uint4 c[V];
+        if constexpr (RING) {
+            ring.wait_oldest();
+            ring.read(slot, 0, c);
+        } else {
+#pragma unroll
+            for (int s = 0; s < V; ++s) c[s] = load_slot<VEC>(X + (int64_t)row * p.ldx, s, l, TL, K);
+        }
+        f32x2 a[ACT ? 4 * V : 4];  // ACT: the row's activated values
         uint32_t most = 0;
+        if constexpr (ACT) {
 #pragma unroll
-        for (int s = 0; s < V; ++s) {
-            float* v = ACT ? a + 8 * s : a;
-            unpack8<DT>(c[s], v);
-            if constexpr (ACT) {
-                float g[8] = {};
-                if (p.act == KT_ACT_GEGLU)
-                    unpack8<DT>(load_slot<VEC>(X + (int64_t)row * p.ldx + K, s, l, TL, K), g);
+            for (int s = 0; s < V; ++s) {
+                float v[8], g[8] = {};
+                unpack8<DT>(c[s], v);
+                if (p.act == KT_ACT_GEGLU) unpack8<DT>(load_slot<VEC>(X + (int64_t)row * p.ldx + K, s, l, TL, K), g);
                 activate8(p.act, v, g);  // a column past the row: act(0) = 0
-            }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t bits = __float_as_uint(v[e]) & 0x7fffffffu;
-                most = bits > most ? bits : most;
+                for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[e]) & 0x7fffffffu);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a[4 * s + e] = f2(v[2 * e], v[2 * e + 1]);
             }
+        } else {
+            // the 16-bit patterns without their signs are ordered as the magnitudes are
+            uint32_t m2 = 0;
+#pragma unroll
+            for (int s = 0; s < V; ++s)
+                m2 = __vmaxu2(__vmaxu2(m2, __vmaxu2(c[s].x & 0x7fff7fffu, c[s].y & 0x7fff7fffu)),
+                              __vmaxu2(c[s].z & 0x7fff7fffu, c[s].w & 0x7fff7fffu));
+            float f[8];
+            unpack8<DT>(make_uint4(max(m2 & 0xffffu, m2 >> 16), 0u, 0u, 0u), f);
+            most = __float_as_uint(f[0]);
         }
         most = team_max<W>(most, lines, turn, team);
+        if constexpr (RING) {  // this lane has its part of the row: its slots take the row `rows` ahead
+            if (p.M - row > (int64_t)ring.rows * step) ring.copy(slot, 0, X + ((int64_t)row + (int64_t)ring.rows * step) * p.ldx, l, K);
+            ring.commit();
+            slot = slot + 1 < ring.rows ? slot + 1 : 0;
+        }
         const bool finite = most < 0x7f800000u;
         const float scale = finite ? __fdiv_rn(__uint_as_float(most), 127.0f) : __uint_as_float(0x7fffffffu);
         if (l == 0) p.scale[row] = scale;
-        // a scale whose inverse is out of range (a row of subnormals) divides every element
-        const bool fast = scale > 1e-37f, zero = !finite || scale == 0.0f;
+        const bool fast = scale > 1e-37f;
         const float inv = fast ? __fdiv_rn(1.0f, scale) : 0.0f;
         int8_t* qr = p.Q + (int64_t)row * p.ldq;
 #pragma unroll
         for (int s = 0; s < V; ++s) {
-            float* v = ACT ? a + 8 * s : a;
-            if constexpr (!ACT) unpack8<DT>(c[s], v);
-            uint32_t q[8];
+            f32x2 v[4];
+            if constexpr (ACT) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                // adding 1.5 * 2^23 rounds to the nearest integer, ties to even, in the low bits
-                const float t = v[e] * inv, m = t + 12582912.0f;
-                q[e] = __float_as_uint(m);
-                const float off = fabsf(t - (m - 12582912.0f));
-                if (zero) q[e] = 0;
-                else if (!fast) q[e] = (uint32_t)nearest_by_division(v[e], scale);
-                else if (off > 0.4999f) q[e] = (uint32_t)nearest_by_remainder(v[e], scale, (int)(m - 12582912.0f));
+                for (int e = 0; e < 4; ++e) v[e] = a[4 * s + e];
+            } else {
+                unpack_pairs<DT>(c[s], v);
+            }
+            uint32_t lo, hi;
+            if (fast) {
+                quantize8(v, scale, inv, lo, hi);
+            } else {
+                lo = quantize4_rare(v[0].x, v[0].y, v[1].x, v[1].y, scale);
+                hi = quantize4_rare(v[2].x, v[2].y, v[3].x, v[3].y, scale);
             }
             if constexpr (VEC) {
                 const int col = slot_col<true>(s, 0, l, TL);
-                if (col < K) {
-                    const uint32_t lo = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
-                    const uint32_t hi = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
-                    *reinterpret_cast<uint2*>(qr + col) = make_uint2(lo, hi);
-                }
+                if (col < K) *reinterpret_cast<uint2*>(qr + col) = make_uint2(lo, hi);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int col = slot_col<false>(s, e, l, TL);
-                    if (col < K) qr[col] = (int8_t)q[e];
+                    if (col < K) qr[col] = (int8_t)((e < 4 ? lo : hi) >> (8 * (e & 3)));
                 }
             }
         }
-        if (next >= p.M) break;
-        row = next;
-#pragma unroll
-        for (int s = 0; s < V; ++s) c[s] = n[s];
     }
 }
 
 }  // namespace
 
-kt_status launch_quantize(int dtype, const QuantRows& p, int sms, void* stream, const char** why) {
+kt_status launch_quantize(int dtype, const QuantRows& p, int sms, int device, void* stream, const char** why) {
     RowShape shape;
     if (!row_shape(p.K, &shape)) {
         *why = "rows of this length are not supported";
@@ -144,13 +192,25 @@ kt_status launch_quantize(int dtype, const QuantRows& p, int sms, void* stream, 
                      (reinterpret_cast<uintptr_t>(p.Q) & 7u) == 0;
     auto go = [&](auto dt, auto v16, auto act) {
         return with_shape<decltype(v16)::value>(shape, [&](auto W, auto V) -> kt_status {
-            constexpr int w = decltype(W)::value;
-            const int teams = row_block(w) / (32 * w);
+            constexpr int w = decltype(W)::value, t = decltype(dt)::value, v = decltype(V)::value;
+            constexpr bool al16 = decltype(v16)::value, with_act = decltype(act)::value;
+            constexpr int teams = row_block(w) / (32 * w), per_sm = quant_per_sm(w, with_act);
             const int64_t blocks = ((int64_t)p.M + teams - 1) / teams;
-            const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)sms * (w == 16 || decltype(act)::value ? 1 : 2));
-            cudaError_t e = launch_pdl(
-                kt_quantize_kernel<decltype(dt)::value, w, decltype(V)::value, decltype(v16)::value, decltype(act)::value>,
-                grid, row_block(w), 0, stream, p);
+            const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)sms * per_sm);
+            cudaError_t e = cudaSuccess;
+            bool ring = false;
+            if constexpr (al16 && !with_act) {
+                // from three rows a team on they come through the ring
+                ring = blocks >= 3 * (int64_t)sms * per_sm;
+                if (ring) {
+                    constexpr int smem = RowRing<w, v, 1>::bytes;
+                    static SmemOptIn opt_in;
+                    auto kern = kt_quantize_kernel<t, w, v, true, false, true>;
+                    e = opt_in(kern, smem, device);
+                    if (e == cudaSuccess) e = launch_pdl(kern, grid, row_block(w), smem, stream, p);
+                }
+            }
+            if (!ring) e = launch_pdl(kt_quantize_kernel<t, w, v, al16, with_act, false>, grid, row_block(w), 0, stream, p);
             if (e != cudaSuccess) {
                 *why = cudaGetErrorString(e);
                 return KT_ERR_CUDA;

@@ -120,7 +120,7 @@ __device__ __forceinline__ uint4 pack8(const float* y) {
 // again only after the next reduction's barrier, which every warp reaches after its reads.
 template <int W>
 struct TeamLines {
-    float4 v[2][row_block(W) / 32];
+    float2 v[2][row_block(W) / 32];
 };
 template <int W>
 __device__ __forceinline__ void team_barrier(int team) {
@@ -138,13 +138,13 @@ __device__ __forceinline__ void team_add2(float& a, float& b, TeamLines<W>& line
     b = warp_add(b);
     if constexpr (W > 1) {
         const int warp = threadIdx.x >> 5;
-        float4* line = lines.v[turn];
-        if ((threadIdx.x & 31) == 0) line[warp] = make_float4(a, b, 0.0f, 0.0f);
+        float2* line = lines.v[turn];
+        if ((threadIdx.x & 31) == 0) line[warp] = make_float2(a, b);
         team_barrier<W>(team);
         a = b = 0.0f;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            const float4 t = line[team * W + i];
+            const float2 t = line[team * W + i];
             a += t.x;
             b += t.y;
         }
@@ -157,7 +157,7 @@ __device__ __forceinline__ uint32_t team_max(uint32_t x, TeamLines<W>& lines, in
     x = __reduce_max_sync(0xffffffffu, x);
     if constexpr (W > 1) {
         const int warp = threadIdx.x >> 5;
-        float4* line = lines.v[turn];
+        float2* line = lines.v[turn];
         if ((threadIdx.x & 31) == 0) line[warp].x = __uint_as_float(x);
         team_barrier<W>(team);
         x = 0;
@@ -170,6 +170,64 @@ __device__ __forceinline__ uint32_t team_max(uint32_t x, TeamLines<W>& lines, in
     }
     return x;
 }
+
+// Rows on their way from global memory in shared memory, `rows` of them ahead: each lane copies
+// its own 16-byte slots asynchronously and reads only them, so nobody waits for another lane,
+// and what is in flight costs no registers.  (One bulk copy per row by one lane of the team was
+// slower than plain loads a row ahead: a copy takes its thread, and so its warp, about 0.1 us.)
+template <int W, int V, int T>  // T tensors
+struct RowRing {
+    static constexpr int TL = 32 * W, teams = row_block(W) / TL;
+    static constexpr int rows = V <= 2 ? 8 : V == 3 ? 6 : 4;
+    static constexpr int bytes = rows * T * V * row_block(W) * 16;
+    uint32_t base;  // this lane's first slot
+    __device__ __forceinline__ void open(const uint8_t* smem, int team, int l) {
+        base = smem_u32(smem) + (uint32_t)(team * rows * T * V * TL + l) * 16u;
+    }
+    __device__ __forceinline__ uint32_t at(int slot, int t, int s) const {
+        return base + (uint32_t)(((slot * T + t) * V + s) * TL) * 16u;
+    }
+    __device__ __forceinline__ void copy(int slot, int t, const uint16_t* row, int l, int D) const {
+#pragma unroll
+        for (int s = 0; s < V; ++s) {
+            const int c = 8 * (s * TL + l);
+            // past the row's end: zeros, read from nowhere
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at(slot, t, s)), "l"(row + (c < D ? c : 0)), "r"(c < D ? 16 : 0)
+                         : "memory");
+        }
+    }
+    static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    static __device__ __forceinline__ void wait_oldest() { asm volatile("cp.async.wait_group %0;" ::"n"(rows - 1) : "memory"); }
+    __device__ __forceinline__ void read(int slot, int t, uint4 (&c)[V]) const {
+#pragma unroll
+        for (int s = 0; s < V; ++s)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(c[s].x), "=r"(c[s].y), "=r"(c[s].z), "=r"(c[s].w) : "r"(at(slot, t, s)) : "memory");
+    }
+};
+
+// gamma or beta as fp32 in shared memory, in the order in which the lanes read it: 16 bytes of
+// slot s, half h (4 elements) of lane l at ((2 s + h) TL + l), so a warp's reads touch consecutive
+// addresses.  Saves the registers that the packed values take and their unpacking in every row.
+template <int DT, bool VEC, int W, int V>
+__device__ __forceinline__ void stage_vector(const uint16_t* v, float4* to, int D) {
+    constexpr int TL = 32 * W;
+    for (int i = threadIdx.x; i < V * TL; i += row_block(W)) {
+        const int s = i / TL, l = i % TL;
+        float f[8];
+        unpack8<DT>(load_slot<VEC>(v, s, l, TL, D), f);
+        to[(2 * s) * TL + l] = make_float4(f[0], f[1], f[2], f[3]);
+        to[(2 * s + 1) * TL + l] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+}
+template <int W>
+__device__ __forceinline__ void staged_pairs(const float4* from, int s, int l, f32x2 (&f)[4]) {
+    const float4 a = from[(2 * s) * 32 * W + l], b = from[(2 * s + 1) * 32 * W + l];
+    f[0] = f2(a.x, a.y);
+    f[1] = f2(a.z, a.w);
+    f[2] = f2(b.x, b.y);
+    f[3] = f2(b.z, b.w);
+}
+constexpr int staged_bytes(int W, int V) { return V * 32 * W * 8 * 4; }
 
 // Calls f(integral constants W, V) for the team shape; 13 shapes with 16-byte loads, 8 (the
 // shapes' slot counts rounded up) without.
