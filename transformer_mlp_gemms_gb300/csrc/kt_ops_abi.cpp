@@ -135,7 +135,7 @@ kt_status kt_quantize_rows(int64_t M, int64_t K, kt_dtype dtype, kt_act act, con
     if ((s = current_device(&dev, &sms)) != KT_OK) return s;
     const char* why = "";
     kt::QuantRows p = {X, Q, scale, ldx, ldq, (int)M, (int)K, (int)act};
-    return done(kt::launch_quantize(dtype, p, sms, dev, stream, &why), why);
+    return done(kt::launch_quantize(dtype, p, sms, stream, &why), why);
 }
 
 kt_status kt_linear_i8(int64_t M, int64_t N, int64_t K, kt_dtype dtype, const int8_t* Q, int64_t ldq, const int8_t* W,

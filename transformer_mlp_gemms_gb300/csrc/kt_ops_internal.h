@@ -48,7 +48,7 @@ struct QuantRows {
     int64_t ldx, ldq;
     int M, K, act;
 };
-kt_status launch_quantize(int dtype, const QuantRows& p, int sms, int device, void* stream, const char** why);
+kt_status launch_quantize(int dtype, const QuantRows& p, int sms, void* stream, const char** why);
 
 struct LinearI8 {
     const int8_t *Q, *W;

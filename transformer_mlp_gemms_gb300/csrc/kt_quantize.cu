@@ -3,7 +3,7 @@
 //
 // Bound by HBM: 2 bytes read and 1 written per element.  The row stays in the registers of a
 // team of warps (kt_rows.cuh) between its largest magnitude and its rounding, so it is read
-// once; the grid is persistent, and the next rows arrive in a ring behind it.  The magnitudes
+// once; the grid is persistent, and the next row's loads are in flight behind it.  The magnitudes
 // are compared as the integers that their bits are, which orders NaN above infinity above every
 // number, so one maximum (two 16-bit values at a time) also tells whether the row is finite.
 //
@@ -79,39 +79,30 @@ __device__ __noinline__ uint32_t quantize4_rare(float a, float b, float c, float
            (uint32_t)(nearest_by_division(c, scale) & 255) << 16 | (uint32_t)(nearest_by_division(d, scale) & 255) << 24;
 }
 
-constexpr int quant_per_sm(int W, bool ACT) { return W == 16 || ACT ? 1 : 2; }
+// Resident blocks per SM, as the registers allow.
+constexpr int quant_per_sm(int W, bool ACT) { return ACT ? 1 : W == 16 ? 1 : 3; }
 
-template <int DT, int W, int V, bool VEC, bool ACT, bool RING>
+template <int DT, int W, int V, bool VEC, bool ACT>
 __global__ void __launch_bounds__(row_block(W), quant_per_sm(W, ACT)) kt_quantize_kernel(const QuantRows p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int TL = 32 * W, teams = row_block(W) / TL;
     __shared__ TeamLines<W> lines;
-    extern __shared__ __align__(16) uint8_t smem[];
     const int team = threadIdx.x / TL, l = threadIdx.x % TL;
     const uint16_t* X = static_cast<const uint16_t*>(p.X);
     const int K = p.K, step = (int)gridDim.x * teams;
-    RowRing<W, V, 1> ring;
-    int slot = 0;
     int row = (int)blockIdx.x * teams + team;
     if (row >= p.M) return;  // the whole team: its barriers are its own
     int turn = 0;
-    if constexpr (RING) {
-        ring.open(smem, team, l);
+    uint4 c[V];
 #pragma unroll
-        for (int i = 0; i < ring.rows; ++i) {
-            if (p.M - row > (int64_t)i * step) ring.copy(i, 0, X + ((int64_t)row + (int64_t)i * step) * p.ldx, l, K);
-            ring.commit();
-        }
-    }
-    for (; row < p.M; row = p.M - row > step ? row + step : p.M) {
-        uint4 c[V];
-        if constexpr (RING) {
-            ring.wait_oldest();
-            ring.read(slot, 0, c);
-        } else {
+    for (int s = 0; s < V; ++s) c[s] = load_slot<VEC>(X + (int64_t)row * p.ldx, s, l, TL, K);
+    for (;;) {
+        const int next = p.M - row > step ? row + step : p.M;
+        uint4 n[V];  // the next row, on its way behind this one's reduction
+        if (next < p.M) {
 #pragma unroll
-            for (int s = 0; s < V; ++s) c[s] = load_slot<VEC>(X + (int64_t)row * p.ldx, s, l, TL, K);
+            for (int s = 0; s < V; ++s) n[s] = load_slot<VEC>(X + (int64_t)next * p.ldx, s, l, TL, K);
         }
         f32x2 a[ACT ? 4 * V : 4];  // ACT: the row's activated values
         uint32_t most = 0;
@@ -139,11 +130,6 @@ __global__ void __launch_bounds__(row_block(W), quant_per_sm(W, ACT)) kt_quantiz
             most = __float_as_uint(f[0]);
         }
         most = team_max<W>(most, lines, turn, team);
-        if constexpr (RING) {  // this lane has its part of the row: its slots take the row `rows` ahead
-            if (p.M - row > (int64_t)ring.rows * step) ring.copy(slot, 0, X + ((int64_t)row + (int64_t)ring.rows * step) * p.ldx, l, K);
-            ring.commit();
-            slot = slot + 1 < ring.rows ? slot + 1 : 0;
-        }
         const bool finite = most < 0x7f800000u;
         const float scale = finite ? __fdiv_rn(__uint_as_float(most), 127.0f) : __uint_as_float(0x7fffffffu);
         if (l == 0) p.scale[row] = scale;
@@ -177,12 +163,16 @@ __global__ void __launch_bounds__(row_block(W), quant_per_sm(W, ACT)) kt_quantiz
                 }
             }
         }
+        if (next >= p.M) break;
+        row = next;
+#pragma unroll
+        for (int s = 0; s < V; ++s) c[s] = n[s];
     }
 }
 
 }  // namespace
 
-kt_status launch_quantize(int dtype, const QuantRows& p, int sms, int device, void* stream, const char** why) {
+kt_status launch_quantize(int dtype, const QuantRows& p, int sms, void* stream, const char** why) {
     RowShape shape;
     if (!row_shape(p.K, &shape)) {
         *why = "rows of this length are not supported";
@@ -197,20 +187,7 @@ kt_status launch_quantize(int dtype, const QuantRows& p, int sms, int device, vo
             constexpr int teams = row_block(w) / (32 * w), per_sm = quant_per_sm(w, with_act);
             const int64_t blocks = ((int64_t)p.M + teams - 1) / teams;
             const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)sms * per_sm);
-            cudaError_t e = cudaSuccess;
-            bool ring = false;
-            if constexpr (al16 && !with_act) {
-                // from three rows a team on they come through the ring
-                ring = blocks >= 3 * (int64_t)sms * per_sm;
-                if (ring) {
-                    constexpr int smem = RowRing<w, v, 1>::bytes;
-                    static SmemOptIn opt_in;
-                    auto kern = kt_quantize_kernel<t, w, v, true, false, true>;
-                    e = opt_in(kern, smem, device);
-                    if (e == cudaSuccess) e = launch_pdl(kern, grid, row_block(w), smem, stream, p);
-                }
-            }
-            if (!ring) e = launch_pdl(kt_quantize_kernel<t, w, v, al16, with_act, false>, grid, row_block(w), 0, stream, p);
+            const cudaError_t e = launch_pdl(kt_quantize_kernel<t, w, v, al16, with_act>, grid, row_block(w), 0, stream, p);
             if (e != cudaSuccess) {
                 *why = cudaGetErrorString(e);
                 return KT_ERR_CUDA;
