@@ -1,4 +1,5 @@
-"""Build the in-tree shared library ``_build/libkt_mlp.so`` with nvcc for sm_103a.
+"""Build the in-tree shared library ``_build/libkt_mlp.so`` with nvcc for sm_103a, and the module
+``_build/_kt_ops.so`` that hands torch tensors to it (g++, torch's headers).
 
 Each translation unit is compiled in parallel, then linked with ``nvcc -shared``.
 The CUDA runtime is linked statically; the driver's tensor-map encoder is looked
@@ -20,6 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libkt_mlp.so")
+MODULE = os.path.join(BUILD, "_kt_ops.so")
+MODULE_SOURCE = os.path.join(CSRC, "kt_ops_py.cpp")
 
 SOURCES = ["kt_gemm_act.cu", "kt_gemm_geglu.cu", "kt_gemm_down.cu", "kt_mlp_two_act_f16.cu", "kt_mlp_two_act_bf16.cu",
            "kt_mlp_two_geglu.cu", "kt_fused.cu", "kt_mlp_kernels.cu", "kt_mlp_abi.cpp", "kt_planner.cpp",
@@ -51,6 +54,22 @@ def _stale(out: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _module_flags():
+    """(compile, link) flags of the Python module: this interpreter's and this torch's headers and libraries."""
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(os.path.abspath(torch.__file__))
+    lib, inc = os.path.join(home, "lib"), os.path.join(home, "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    compile_ = ["-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", inc,
+                "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    link = ["-L", BUILD, "-l:libkt_mlp.so", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda",
+            "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    return compile_, link
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -66,6 +85,14 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             if verbose:
                 print(" ".join(cmd), flush=True)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    module_obj = os.path.join(BUILD, "kt_ops_py.cpp.o")
+    if force or _stale(module_obj, [MODULE_SOURCE, os.path.join(INCLUDE, "kt_mlp.h"), os.path.join(INCLUDE, "kt_ops.h")]):
+        cmd = ["g++", "-c", MODULE_SOURCE, "-o", module_obj] + _module_flags()[0]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        module = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    else:
+        module = None
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -82,6 +109,17 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
+    if module is not None:
+        out, _ = module.communicate()
+        if module.returncode != 0:
+            raise RuntimeError(f"g++ failed on kt_ops_py.cpp:\n{out}")
+    if module is not None or _stale(MODULE, [module_obj]):
+        tmp = MODULE + f".tmp{os.getpid()}"
+        cmd = ["g++", "-shared", "-o", tmp, module_obj] + _module_flags()[1]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, MODULE)
     return LIB
 
 

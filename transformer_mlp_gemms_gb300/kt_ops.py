@@ -8,16 +8,22 @@ or strides) raises ``KtError`` with ``KT_ERR_INVALID`` before anything is launch
 library's own refusals do.  Nothing is computed here, and outputs are the caller's tensors.
 Work goes to torch's current stream of the tensors' device unless ``stream`` names another;
 tensors that other streams still use are the caller's to order, as with any torch call.
+
+The checks are compiled (``csrc/kt_ops_py.cpp``, built beside the library): in Python they would
+take longer than a small call does on the GPU.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 
 import torch
 
 from . import kt_mlp
-from .kt_mlp import KT_ACT_GEGLU, KT_ACT_NONE, KT_BF16, KT_ERR_INVALID, KT_F16, KtError, _check
+from .kt_mlp import KT_ACT_GEGLU, KT_ACT_NONE, KT_ERR_INVALID, KtError, _check
 
+MODULE_PATH = os.path.join(kt_mlp.HERE, "_build", "_kt_ops.so")
 _VP, _I64, _I32, _F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
 
 KT_LAYERNORM_MAX_D = 16384
@@ -49,95 +55,48 @@ SIGNATURES = {
     "kt_moe_destroy": ([_VP], _I32),
 }
 
-_DTYPES = {torch.float16: KT_F16, torch.bfloat16: KT_BF16}
-_F32_T, _I8_T, _I32_T = torch.float32, torch.int8, torch.int32
 _lib = None
-_fwd = _bwd = _quant = _lin = _moe = None  # the functions of the hot calls, once loaded
+_ext = None
 
 
 def load():
-    """The shared library with this header's signatures set (``OSError`` if it has not been built)."""
-    global _lib, _fwd, _bwd, _quant, _lin, _moe
+    """The shared library with this header's signatures set, and the module of the tensor calls
+    (``OSError`` if they have not been built)."""
+    global _lib, _ext
     if _lib is None:
         lib = kt_mlp.load()
         for name, (args, res) in SIGNATURES.items():
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = res
-        _fwd, _bwd, _quant = lib.kt_layernorm_forward, lib.kt_layernorm_backward, lib.kt_quantize_rows
-        _lin, _moe = lib.kt_linear_i8, lib.kt_moe_run
+        if not os.path.exists(MODULE_PATH):
+            raise OSError(f"{MODULE_PATH} not found: build it with `python -m transformer_mlp_gemms_gb300.build`")
+        spec = importlib.util.spec_from_file_location("_kt_ops", MODULE_PATH)
+        _ext = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_ext)
         _lib = lib
     return _lib
 
 
-def _bad(where: str, message: str):
-    raise KtError(KT_ERR_INVALID, where, message)
+def _calls():
+    """The module of the tensor calls."""
+    if _ext is None:
+        load()
+    return _ext
 
 
-def _size(where: str, name: str, t):
-    """(rows, columns, device index) of a matrix."""
-    shape = t.shape
-    if len(shape) != 2:
-        _bad(where, f"{name}: a matrix expected, got {list(shape)}")
-    return shape[0], shape[1], t.get_device()
-
-
-def _dtype(where: str, t) -> int:
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        _bad(where, f"float16 or bfloat16 expected, got {t.dtype}")
-    return code
-
-
-def _rows(where: str, name: str, t, shape, dtype, index) -> int:
-    """Checks a matrix with consecutive elements in a row; returns its row pitch."""
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
-        _bad(where, f"{name}: expected {dtype} {list(shape)} on device {index}, got {t.dtype} {list(t.shape)} on {t.device}")
-    s0, s1 = t.stride()
-    rows, cols = shape
-    if s1 != 1 and cols > 1:
-        _bad(where, f"{name}: elements of a row must be consecutive, strides are {t.stride()}")
-    if s0 < cols:
-        if rows > 1:
-            _bad(where, f"{name}: rows overlap, strides are {t.stride()}")
-        return cols  # the pitch of a single row is never used
-    return s0
-
-
-def _whole(where: str, name: str, t, shape, dtype, index) -> int:
-    """Checks a contiguous tensor of the given shape; returns its address."""
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
-        _bad(where, f"{name}: expected a contiguous {dtype} tensor {list(shape)} on device {index}, got {t.dtype} "
-                    f"{list(t.shape)} on {t.device}, strides {t.stride()}")
-    return t.data_ptr()
-
-
-def _on(where: str, index: int, stream) -> int:
-    """The stream to launch on; the tensors' device must be the current one."""
-    if index < 0:
-        _bad(where, "CUDA tensors expected")
-    if index != torch._C._cuda_getDevice():
-        _bad(where, f"the tensors are on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+def _fail(result, where: str):
+    """A tensor call's refusal: a text, or the library's status."""
+    if isinstance(result, str):
+        raise KtError(KT_ERR_INVALID, where, result)
+    _check(result, where)
 
 
 def kt_layernorm_forward(X, gamma, beta, eps, Y, mean=None, rstd=None, stream=None) -> None:
     """Y = layer norm of the rows of X; mean and rstd (fp32 [M]) receive the statistics if given."""
-    w = "kt_layernorm_forward"
-    M, D, dev = _size(w, "X", X)
-    code, dt = _dtype(w, X), X.dtype
-    s = _on(w, dev, stream)
-    ldx, ldy = _rows(w, "X", X, (M, D), dt, dev), _rows(w, "Y", Y, (M, D), dt, dev)
-    if _fwd is None:
-        load()
-    status = _fwd(M, D, code, X.data_ptr(), ldx, None if gamma is None else _whole(w, "gamma", gamma, (D,), dt, dev),
-                  None if beta is None else _whole(w, "beta", beta, (D,), dt, dev), eps, Y.data_ptr(), ldy,
-                  None if mean is None else _whole(w, "mean", mean, (M,), _F32_T, dev),
-                  None if rstd is None else _whole(w, "rstd", rstd, (M,), _F32_T, dev), s)
-    if status:
-        _check(status, w)
+    r = (_ext or _calls()).layernorm_forward(X, gamma, beta, eps, Y, mean, rstd, stream)
+    if r is not None:
+        _fail(r, "kt_layernorm_forward")
 
 
 def kt_layernorm_backward_workspace(M: int, D: int) -> int:
@@ -153,61 +112,23 @@ def layernorm_backward_workspace(M: int, D: int, device="cuda"):
 def kt_layernorm_backward(dY, X, gamma, mean, rstd, dX, dgamma=None, dbeta=None, workspace=None, stream=None) -> None:
     """dX, and with dgamma and dbeta (fp32 [D]) their sums over the rows, which need ``workspace``
     (``layernorm_backward_workspace``)."""
-    w = "kt_layernorm_backward"
-    M, D, dev = _size(w, "X", X)
-    code, dt, shape = _dtype(w, X), X.dtype, (M, D)
-    s = _on(w, dev, stream)
-    ldx, lddy, lddx = _rows(w, "X", X, shape, dt, dev), _rows(w, "dY", dY, shape, dt, dev), _rows(w, "dX", dX, shape, dt, dev)
-    size = at = 0
-    if workspace is not None:
-        if workspace.get_device() != dev or not workspace.is_contiguous():
-            _bad(w, f"workspace: a contiguous tensor on device {dev} expected")
-        size, at = workspace.nbytes, workspace.data_ptr()
-    if _bwd is None:
-        load()
-    status = _bwd(M, D, code, dY.data_ptr(), lddy, X.data_ptr(), ldx,
-                  None if gamma is None else _whole(w, "gamma", gamma, (D,), dt, dev),
-                  _whole(w, "mean", mean, (M,), _F32_T, dev), _whole(w, "rstd", rstd, (M,), _F32_T, dev), dX.data_ptr(), lddx,
-                  None if dgamma is None else _whole(w, "dgamma", dgamma, (D,), _F32_T, dev),
-                  None if dbeta is None else _whole(w, "dbeta", dbeta, (D,), _F32_T, dev), at, size, s)
-    if status:
-        _check(status, w)
+    r = (_ext or _calls()).layernorm_backward(dY, X, gamma, mean, rstd, dX, dgamma, dbeta, workspace, stream)
+    if r is not None:
+        _fail(r, "kt_layernorm_backward")
 
 
 def kt_quantize_rows(X, Q, scale, act: int = KT_ACT_NONE, stream=None) -> None:
     """Q (int8 [M][K]) and scale (fp32 [M]) of act(X); X is [M][K], or [M][2K] for KT_ACT_GEGLU."""
-    w = "kt_quantize_rows"
-    M, K, dev = _size(w, "Q", Q)
-    code = _dtype(w, X)
-    s = _on(w, dev, stream)
-    ldx = _rows(w, "X", X, (M, 2 * K if act == KT_ACT_GEGLU else K), X.dtype, dev)
-    ldq = _rows(w, "Q", Q, (M, K), _I8_T, dev)
-    if _quant is None:
-        load()
-    status = _quant(M, K, code, act, X.data_ptr(), ldx, Q.data_ptr(), ldq, _whole(w, "scale", scale, (M,), _F32_T, dev), s)
-    if status:
-        _check(status, w)
+    r = (_ext or _calls()).quantize_rows(X, Q, scale, act, stream)
+    if r is not None:
+        _fail(r, "kt_quantize_rows")
 
 
 def kt_linear_i8(Q, scale_x, W, scale_w, bias, Y, stream=None) -> None:
     """Y[m][n] = scale_x[m] scale_w[n] sum_k Q[m][k] W[n][k] (+ bias[n])."""
-    w = "kt_linear_i8"
-    M, K, dev = _size(w, "Q", Q)
-    N = _size(w, "W", W)[0]
-    code, dt = _dtype(w, Y), Y.dtype
-    s = _on(w, dev, stream)
-    ldq, ldw, ldy = _rows(w, "Q", Q, (M, K), _I8_T, dev), _rows(w, "W", W, (N, K), _I8_T, dev), _rows(w, "Y", Y, (M, N), dt, dev)
-    if M <= 1:
-        ldq = (ldq + 15) // 16 * 16  # the pitch of a single row is never used
-    if N <= 1:
-        ldw = (ldw + 15) // 16 * 16
-    if _lin is None:
-        load()
-    status = _lin(M, N, K, code, Q.data_ptr(), ldq, W.data_ptr(), ldw, _whole(w, "scale_x", scale_x, (M,), _F32_T, dev),
-                  _whole(w, "scale_w", scale_w, (N,), _F32_T, dev),
-                  None if bias is None else _whole(w, "bias", bias, (N,), dt, dev), Y.data_ptr(), ldy, s)
-    if status:
-        _check(status, w)
+    r = (_ext or _calls()).linear_i8(Q, scale_x, W, scale_w, bias, Y, stream)
+    if r is not None:
+        _fail(r, "kt_linear_i8")
 
 
 def kt_moe_plan(options: kt_moe_options) -> int:
@@ -217,11 +138,7 @@ def kt_moe_plan(options: kt_moe_options) -> int:
 
 
 def kt_moe_run(plan: int, tensors: kt_moe_tensors, stream=None) -> None:
-    if _moe is None:
-        load()
-    status = _moe(plan, ctypes.byref(tensors), kt_mlp._stream(stream))
-    if status:
-        _check(status, "kt_moe_run")
+    _check(load().kt_moe_run(plan, ctypes.byref(tensors), kt_mlp._stream(stream)), "kt_moe_run")
 
 
 def kt_moe_status(plan: int) -> int:
@@ -245,24 +162,13 @@ class MoePlan:
         self.handle = None
         self.handle = kt_moe_plan(kt_moe_options(max_tokens, D, F, experts, top_k, act, dtype, int(bool(bias)),
                                                  int(bool(normalize))))
-        self.torch_dtype = torch.float16 if dtype == KT_F16 else torch.bfloat16
+        self._sizes = (dtype, D, F, self.rows, experts, top_k)
 
     def run(self, X, W_router, W_up, W_down, Y, b_up=None, b_down=None, R=None, ids=None, weights=None, stream=None):
-        w, dt = "kt_moe_run", self.torch_dtype
-        T, D, dev = _size(w, "X", X)
-        E, shape, chosen = self.experts, (T, self.D), (T, self.top_k)
-        s = _on(w, dev, stream)
-        ldx = _rows(w, "X", X, shape, dt, dev)
-        if T <= 1:
-            ldx = (ldx + 7) // 8 * 8  # the pitch of a single row is never used
-        kt_moe_run(self.handle, kt_moe_tensors(
-            T, X.data_ptr(), ldx, _whole(w, "W_router", W_router, (E, D), dt, dev),
-            _whole(w, "W_up", W_up, (E, self.rows, D), dt, dev), _whole(w, "W_down", W_down, (E, D, self.F), dt, dev),
-            None if b_up is None else _whole(w, "b_up", b_up, (E, self.rows), dt, dev),
-            None if b_down is None else _whole(w, "b_down", b_down, (E, D), dt, dev),
-            None if R is None else _whole(w, "R", R, shape, dt, dev), _whole(w, "Y", Y, shape, dt, dev),
-            None if ids is None else _whole(w, "ids", ids, chosen, _I32_T, dev),
-            None if weights is None else _whole(w, "weights", weights, chosen, _F32_T, dev)), s)
+        r = (_ext or _calls()).moe_run(self.handle, self._sizes, X, W_router, W_up, W_down, Y, b_up, b_down, R, ids, weights,
+                                       stream)
+        if r is not None:
+            _fail(r, "kt_moe_run")
 
     def status(self) -> int:
         return kt_moe_status(self.handle)
