@@ -161,13 +161,14 @@ __global__ void __launch_bounds__(kDotWarps * 32) kt_linear_i8_dot_kernel(const 
 // of its 32 bytes in one stage, the others in the next), and the channels follow the same order.
 // Four bytes become two pairs of fp16 in five instructions: with the sign bit flipped a byte is
 // q + 128, and next to the byte 0x64 it is the fp16 number 1024 + (q + 128); 1152 is subtracted.
-constexpr int kTcStages = 4;  // of 64 columns; a step of 128 columns is two
+constexpr int kTcStages = 8;  // of 64 columns; a step of 128 columns is two
 constexpr int kTcGroups = 2;  // producers of even and of odd steps
-constexpr int kTcTokenWarps = 4, kTcChannelWarps = 4, kTcEpiWarps = 4;  // tokens, channels: per group
+constexpr int kTcTokenWarps = 4, kTcChannelWarps = 4, kTcEpiWarps = 8;  // tokens, channels: per group
+constexpr int kTcForward = 4;  // threads of a pair's second CTA that forward its full stages
 constexpr int kTcChannel0 = kTcGroups * kTcTokenWarps, kTcEpi0 = kTcChannel0 + kTcGroups * kTcChannelWarps;
-constexpr int kTcMmaWarp = kTcEpi0 + kTcEpiWarps, kTcThreads = (kTcMmaWarp + kTcStages) * 32;
-static_assert(kTcStages == 2 * kTcGroups && kTcEpi0 % 4 == 0, "a group's step has two stages of its own; epilogue warp q: lanes 32 q");
-constexpr uint32_t kTcACol = 384;  // tensor-memory column of the first operand's stages
+constexpr int kTcMmaWarp = kTcEpi0 + kTcEpiWarps, kTcThreads = (kTcMmaWarp + kTcForward) * 32;
+static_assert(kTcStages % (2 * kTcGroups) == 0 && kTcEpi0 % 4 == 0, "whole steps per round of the ring; epilogue warp q: lanes 32 q");
+constexpr uint32_t kTcACol = 256;  // tensor-memory column of the first operand's stages, after the accumulators
 __device__ int g_linear_i8_error;  // a bounded wait that ran out (never in normal operation)
 
 __device__ __forceinline__ void bytes_to_halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -245,6 +246,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
     extern __shared__ uint8_t raw[];
     using Smem = TcSmem<BN, PAIR>;
     constexpr int kShare = BN / PAIR;  // channels whose weights this CTA stages
+    constexpr int kBufs = 256 / BN >= 2 ? 2 : 1;  // accumulators
     Smem& sm = *reinterpret_cast<Smem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int* abort_flag = &sm.abort;
@@ -299,12 +301,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
             load(reg, k * 128);
             k += kTcGroups;
         };
-        uint32_t phase = 0;
+        uint32_t first = 2u * group, phase = 0;  // the step's first stage
         if (group < total) fetch();
-        for (int s = group; s < total; s += kTcGroups, phase ^= 1u) {
+        for (int s = group; s < total; s += kTcGroups) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t stage = 2u * group + h;
+                const uint32_t stage = first + h;
                 const bool ok = wait_phase(bar(sm.empty[stage]), phase ^ 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_PRODUCER, kLimit);
                 if (!__all_sync(0xffffffffu, ok)) return;
                 convert(reg[h], stage);
@@ -312,6 +314,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
                 if (lane == 0) mbar_arrive(bar(sm.full[stage]));
             }
             if (s + kTcGroups < total) fetch();
+            first += 2 * kTcGroups;
+            if (first >= kTcStages) {
+                first -= kTcStages;
+                phase ^= 1u;
+            }
         }
     };
     const bool wide_q = ((reinterpret_cast<uintptr_t>(p.Q) | (uintptr_t)p.ldq | (uintptr_t)p.K) & 31u) == 0;
@@ -395,16 +402,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
         if (PAIR == 2 && rank == 1) {
             // ------------------- the pair's second CTA: its full stages are told to the first -------------------
             // (an arrival that orders what came before it at cluster scope costs its thread about
-            // 0.35 us, as long as a stage takes: one thread per stage)
+            // 0.35 us, more than a stage takes: four threads in turn)
             if (lane == 0) {
-                const int s = warp - kTcMmaWarp;
-                const uint32_t first = mapa_rank(bar(sm.full[s]), 0u);
-                uint32_t phase = 0;
-                for (int i = s; i < 2 * total; i += kTcStages, phase ^= 1u) {
+                uint32_t s = warp - kTcMmaWarp, phase = 0;
+                for (int i = s; i < 2 * total; i += kTcForward) {
                     if (!wait_phase(bar(sm.full[s]), phase, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_MMA, kLimit)) break;
                     tc_fence_after();
                     tc_fence_before();
-                    mbar_arrive_cluster(first);
+                    mbar_arrive_cluster(mapa_rank(bar(sm.full[s]), 0u));
+                    s += kTcForward;
+                    if (s >= kTcStages) {
+                        s -= kTcStages;
+                        phase ^= 1u;
+                    }
                 }
             }
         } else if (warp == kTcMmaWarp && lane == 0) {
@@ -412,7 +422,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
             uint32_t stage = 0, phase = 0;
             bool ok = true;
             for (int t = 0; t < mine && ok; ++t) {
-                const uint32_t buf = t & 1u, use = (uint32_t)t >> 1;
+                const uint32_t buf = t % kBufs, use = (uint32_t)t / kBufs;
                 ok = wait_phase<PAIR == 2>(bar(sm.acc_empty[buf]), (use & 1u) ^ 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_MMA, kLimit);
                 for (int kb = 0; kb < kblocks && ok; ++kb) {
                     ok = wait_phase<PAIR == 2>(bar(sm.full[stage]), phase, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_MMA, kLimit);
@@ -444,21 +454,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
         for (int t = 0; t < mine; ++t) {
             const int tile = unit + t * units;
             const int m0 = (tile / tiles_n * PAIR + rank) * 128 + q * 32, n0 = (tile % tiles_n) * BN;
-            const uint32_t buf = t & 1u, use = (uint32_t)t >> 1;
+            const uint32_t buf = t % kBufs, use = (uint32_t)t / kBufs, cs = t & 1u;
             for (int i = ew * 32 + lane; i < BN; i += kTcEpiWarps * 32) {
                 float2 c = make_float2(0.0f, 0.0f);
                 if (n0 + i < p.N) {
                     c.x = p.sw[n0 + i];
                     if (p.bias) c.y = from_bits<DT>(static_cast<const uint16_t*>(p.bias)[n0 + i]);
                 }
-                sm.ch[buf][i] = c;
+                sm.ch[cs][i] = c;
             }
             const float sx = m0 + lane < p.M ? p.sx[m0 + lane] : 0.0f;
             const bool got = wait_phase(bar(sm.acc_full[buf]), use & 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_EPILOGUE, kLimit);
             if (!epi_all<kTcEpiWarps>(got)) break;  // also: every warp's part of ch is in place
             tc_fence_after();
+            if (64 * (ew >> 2) >= BN && lane == 0) {  // no columns for this warp
+                if (rank == 0) mbar_arrive(bar(sm.acc_empty[buf]));
+                else mbar_arrive_cluster_relaxed(mapa_rank(bar(sm.acc_empty[buf]), 0u));
+            }
 #pragma unroll 1
-            for (int c0 = 0; c0 < BN; c0 += 64) {
+            for (int c0 = 64 * (ew >> 2); c0 < BN; c0 += 128) {  // two warps per 32 rows, 64 columns each in turn
                 __syncwarp();  // the previous columns' stores have read the buffer
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
@@ -472,7 +486,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
                         uint32_t w[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float4 c = *reinterpret_cast<const float4*>(&sm.ch[buf][c0 + 32 * half + 8 * i + 2 * e]);
+                            const float4 c = *reinterpret_cast<const float4*>(&sm.ch[cs][c0 + 32 * half + 8 * i + 2 * e]);
                             w[e] = pack2<DT>(fmaf(__uint_as_float(r[8 * i + 2 * e]), sx * c.x, c.y),
                                              fmaf(__uint_as_float(r[8 * i + 2 * e + 1]), sx * c.z, c.w));
                         }
@@ -480,7 +494,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
                             make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
-                if (c0 + 64 >= BN) {  // the last columns have been read: the next tile may have the buffer
+                if (c0 + 128 >= BN) {  // this warp's last columns have been read: the next tile may have the buffer
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -584,13 +598,12 @@ kt_status launch_linear_i8(int dtype, const LinearI8& p, int sms, int device, vo
         const int pair = p.M > 128 ? 2 : 1;
         const int64_t tm = (p.M + 128 * pair - 1) / (128 * pair), units = sms / pair;
         auto cost = [&](int bn, int per) { return ((tm * ((p.N + bn - 1) / bn) + units - 1) / units) * per; };
-        const int64_t c192 = cost(192, 384), c128 = cost(128, 290), c64 = cost(64, 220);
+        const int64_t c256 = cost(256, 512), c128 = cost(128, 290), c64 = cost(64, 220);
         if (pair == 2) {
-            if (c192 <= c128 && c192 <= c64) return launch_tc<192, 2>(dtype, p, sms, device, stream, why);
+            if (c256 <= c128 && c256 <= c64) return launch_tc<256, 2>(dtype, p, sms, device, stream, why);
             if (c128 <= c64) return launch_tc<128, 2>(dtype, p, sms, device, stream, why);
             return launch_tc<64, 2>(dtype, p, sms, device, stream, why);
         }
-        if (c192 <= c128 && c192 <= c64) return launch_tc<192, 1>(dtype, p, sms, device, stream, why);
         if (c128 <= c64) return launch_tc<128, 1>(dtype, p, sms, device, stream, why);
         return launch_tc<64, 1>(dtype, p, sms, device, stream, why);
     }
