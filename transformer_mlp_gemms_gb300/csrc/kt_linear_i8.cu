@@ -233,7 +233,8 @@ __device__ __forceinline__ void commit_ta(uint32_t bar) {
 template <int BN, int PAIR>
 struct TcSmem {
     alignas(1024) uint8_t b[kTcStages][BN / PAIR * 128];  // [channel][64 fp16], 128-byte swizzle
-    alignas(128) uint8_t out[kTcEpiWarps][32 * 128];  // a warp's 32 rows x 64 columns of the output
+    static constexpr int kParts = (BN + 127) / 128;  // 64-column parts per epilogue warp
+    alignas(128) uint8_t out[kTcEpiWarps][kParts][32 * 128];  // 32 rows x 64 columns of the output each
     float2 ch[2][BN];                               // channel scale and bias of the tile
     alignas(8) uint64_t full[kTcStages], empty[kTcStages], acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
@@ -276,6 +277,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // the first tile's weights start on their way to L2 while the kernel before this one still runs
+    // (a prefetch reads nothing)
+    if (warp >= kTcChannel0 && warp < kTcEpi0 && unit < tiles) {
+        const int n0 = (unit % tiles_n) * BN + rank * kShare, lines = min((p.K + 127) / 128, 64);
+        for (int i = (int)threadIdx.x - kTcChannel0 * 32; i < kShare * lines; i += kTcGroups * kTcChannelWarps * 32)
+            if (n0 + i % kShare < p.N)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.W + (int64_t)(n0 + i % kShare) * p.ldw + i / kShare * 128));
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int steps = (p.K + 127) / 128, kblocks = 2 * steps;
     const int mine = tiles > unit ? (tiles - 1 - unit) / units + 1 : 0;
@@ -449,7 +458,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
     } else {
         // ------------------- epilogue -------------------
         const int q = warp & 3, ew = warp - kTcEpi0;
-        uint8_t* out = sm.out[ew];
         uint16_t* Y = static_cast<uint16_t*>(p.Y);
         for (int t = 0; t < mine; ++t) {
             const int tile = unit + t * units;
@@ -467,13 +475,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
             const bool got = wait_phase(bar(sm.acc_full[buf]), use & 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_EPILOGUE, kLimit);
             if (!epi_all<kTcEpiWarps>(got)) break;  // also: every warp's part of ch is in place
             tc_fence_after();
-            if (64 * (ew >> 2) >= BN && lane == 0) {  // no columns for this warp
-                if (rank == 0) mbar_arrive(bar(sm.acc_empty[buf]));
-                else mbar_arrive_cluster_relaxed(mapa_rank(bar(sm.acc_empty[buf]), 0u));
-            }
+            // first all of this warp's columns into shared memory, so that the next tile gets the
+            // accumulator soon; then the stores
+            const int first = 64 * (ew >> 2);
+            __syncwarp();  // the previous tile's stores have read the buffers
 #pragma unroll 1
-            for (int c0 = 64 * (ew >> 2); c0 < BN; c0 += 128) {  // two warps per 32 rows, 64 columns each in turn
-                __syncwarp();  // the previous columns' stores have read the buffer
+            for (int c0 = first; c0 < BN; c0 += 128) {
+                uint8_t* out = sm.out[ew][(c0 - first) / 128];
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     uint32_t r[32];
@@ -494,16 +502,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
                             make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
-                if (c0 + 128 >= BN) {  // this warp's last columns have been read: the next tile may have the buffer
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (rank == 0) mbar_arrive(bar(sm.acc_empty[buf]));
-                        else mbar_arrive_cluster_relaxed(mapa_rank(bar(sm.acc_empty[buf]), 0u));
-                    }
-                }
-                if (m0 >= p.M) continue;
-                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (rank == 0) mbar_arrive(bar(sm.acc_empty[buf]));
+                else mbar_arrive_cluster_relaxed(mapa_rank(bar(sm.acc_empty[buf]), 0u));
+            }
+            if (m0 >= p.M) continue;
+#pragma unroll 1
+            for (int c0 = first; c0 < BN; c0 += 128) {
+                const uint8_t* out = sm.out[ew][(c0 - first) / 128];
                 const int n = n0 + c0;
                 if (wide_y) {
                     // eight lanes store a row's 128 bytes
@@ -598,9 +607,10 @@ kt_status launch_linear_i8(int dtype, const LinearI8& p, int sms, int device, vo
         const int pair = p.M > 128 ? 2 : 1;
         const int64_t tm = (p.M + 128 * pair - 1) / (128 * pair), units = sms / pair;
         auto cost = [&](int bn, int per) { return ((tm * ((p.N + bn - 1) / bn) + units - 1) / units) * per; };
-        const int64_t c256 = cost(256, 512), c128 = cost(128, 290), c64 = cost(64, 220);
+        const int64_t c256 = cost(256, 512), c192 = cost(192, 400), c128 = cost(128, 290), c64 = cost(64, 220);
         if (pair == 2) {
-            if (c256 <= c128 && c256 <= c64) return launch_tc<256, 2>(dtype, p, sms, device, stream, why);
+            if (c256 <= c192 && c256 <= c128 && c256 <= c64) return launch_tc<256, 2>(dtype, p, sms, device, stream, why);
+            if (c192 <= c128 && c192 <= c64) return launch_tc<192, 2>(dtype, p, sms, device, stream, why);
             if (c128 <= c64) return launch_tc<128, 2>(dtype, p, sms, device, stream, why);
             return launch_tc<64, 2>(dtype, p, sms, device, stream, why);
         }
