@@ -405,8 +405,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     volatile int* abort_flag = &bars.abort;
     auto bar = [](uint64_t& b) { return smem_u32(&b); };
     // a run that failed is not added to: kt_moe_status clears the word and the counters
+    // by the last two warps: the first ones' logits start at once
     if (warp == kMoeWarps - 1 && lane == 0) bars.failed = *reinterpret_cast<volatile int*>(p.error);
-    if (threadIdx.x == 0) {
+    if (warp == kMoeWarps - 2 && lane == 0) {
         bars.ok = 1;
         bars.abort = 0;
         for (int s = 0; s < stages; ++s) {
