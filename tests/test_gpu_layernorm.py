@@ -41,7 +41,9 @@ def within(got, want, tol, what):
 # every team shape (1 to 16 warps, 1 to 5 slots), odd lengths and pitches, one row and many
 SHAPES = [(1, 1, 0), (3, 8, 0), (5, 33, 0), (9, 256, 0), (8, 264, 8), (33, 643, 6), (64, 640, 0), (129, 1000, 0), (729, 1152, 0),
           (37, 1280, 8), (17, 1281, 0), (16, 1536, 0), (11, 2048, 0), (7, 2056, 0), (5, 4096, 16), (6, 4099, 3), (4, 6144, 0),
-          (3, 8192, 0), (4, 8200, 0), (3, 12288, 0), (5, 16384, 0), (2, 16383, 1), (5000, 40, 0), (3001, 96, 5)]
+          (3, 8192, 0), (4, 8200, 0), (3, 12288, 0), (5, 16384, 0), (2, 16383, 1), (5000, 40, 0), (3001, 96, 5),
+          # many rows per team: the backward pass's rows come through the ring
+          (3800, 1280, 0), (9000, 640, 8), (4001, 1000, 0), (2500, 2048, 0), (1500, 4096, 0), (1000, 6144, 0), (700, 8192, 0)]
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])

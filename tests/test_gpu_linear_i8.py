@@ -79,7 +79,9 @@ def test_activations_as_they_are_quantised(name, M, K):
 
 SHAPES = [(1, 1, 16), (1, 8, 64), (3, 33, 48), (4, 10240, 1280), (7, 100, 4112), (8, 640, 640), (9, 31, 64), (16, 257, 144),
           (33, 64, 1152), (64, 512, 8192), (100, 130, 272), (127, 1000, 640), (128, 256, 128), (129, 255, 2048), (300, 4304, 1152),
-          (729, 1152, 4304), (1000, 520, 80), (2048, 72, 96)]
+          (729, 1152, 4304), (1000, 520, 80), (2048, 72, 96),
+          # several tiles per pair of each width
+          (1100, 4304, 272), (3000, 12800, 80), (1300, 10240, 144), (2000, 5000, 208), (140, 9728, 640), (5000, 640, 144)]
 
 
 @pytest.mark.parametrize("dtype,bias", [("f16", False), ("bf16", True)])

@@ -603,11 +603,13 @@ kt_status launch_tc(int dtype, const LinearI8& p, int sms, int device, void* str
 
 kt_status launch_linear_i8(int dtype, const LinearI8& p, int sms, int device, void* stream, const char** why) {
     if (p.M > KT_LINEAR_I8_DOT_ROWS) {
-        // tile width: the fewest rounds over the CTAs (or pairs), each costing its products' cycles
+        // tile width: rounds over the CTAs (or pairs) times a round's time.  Measured per round of
+        // 76 pairs (18 stages, K = 1152): 8.5, 7.5, 6.1 and 5.6 us for 256, 192, 128 and 64
+        // channels; 30.2, 25.0, 22.3 and 21.0 us for 72 stages.
         const int pair = p.M > 128 ? 2 : 1;
         const int64_t tm = (p.M + 128 * pair - 1) / (128 * pair), units = sms / pair;
         auto cost = [&](int bn, int per) { return ((tm * ((p.N + bn - 1) / bn) + units - 1) / units) * per; };
-        const int64_t c256 = cost(256, 512), c192 = cost(192, 400), c128 = cost(128, 290), c64 = cost(64, 220);
+        const int64_t c256 = cost(256, 85), c192 = cost(192, 75), c128 = cost(128, 61), c64 = cost(64, 56);
         if (pair == 2) {
             if (c256 <= c192 && c256 <= c128 && c256 <= c64) return launch_tc<256, 2>(dtype, p, sms, device, stream, why);
             if (c192 <= c128 && c192 <= c64) return launch_tc<192, 2>(dtype, p, sms, device, stream, why);

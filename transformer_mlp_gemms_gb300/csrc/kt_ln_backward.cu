@@ -237,18 +237,20 @@ __global__ void __launch_bounds__(row_block(W), ln_back_per_sm(W, V)) kt_ln_back
 }
 
 // Adds the blocks' rows of partial sums, in order: out[c] = sum_r partials[r][c] over the 2 D
-// columns (dgamma, then dbeta).  32 columns and 8 runs of rows per block.
-__global__ void __launch_bounds__(256) kt_ln_column_sums_kernel(const float* __restrict__ partials, int rows, int D,
-                                                                float* __restrict__ dgamma, float* __restrict__ dbeta) {
+// columns (dgamma, then dbeta).  32 columns and 16 runs of rows per block, so that a run's loads
+// (at most 30) are in flight together.
+constexpr int kSumRuns = 16;
+__global__ void __launch_bounds__(kSumRuns * 32) kt_ln_column_sums_kernel(const float* __restrict__ partials, int rows, int D,
+                                                                          float* __restrict__ dgamma, float* __restrict__ dbeta) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    __shared__ float part[8][32];
+    __shared__ float part[kSumRuns][32];
     const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
     const int c = (int)blockIdx.x * 32 + lane;
-    const int per = (rows + 7) / 8, r1 = min(rows, (run + 1) * per);
+    const int per = (rows + kSumRuns - 1) / kSumRuns, r1 = min(rows, (run + 1) * per);
     float v = 0.0f;
     if (c < 2 * D) {
-#pragma unroll 8
+#pragma unroll 10
         for (int r = run * per; r < r1; ++r) v += partials[(size_t)r * 2 * D + c];
     }
     part[run][lane] = v;
@@ -256,7 +258,7 @@ __global__ void __launch_bounds__(256) kt_ln_column_sums_kernel(const float* __r
     if (run == 0 && c < 2 * D) {
         v = part[0][lane];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) v += part[i][lane];
+        for (int i = 1; i < kSumRuns; ++i) v += part[i][lane];
         if (c < D)
             dgamma[c] = v;
         else
@@ -330,7 +332,7 @@ kt_status launch_ln_backward(int dtype, const LnBackward& p, int sms, int device
         if (s != KT_OK) return s;
     }
     if (p.dgamma) {
-        e = launch_pdl(kt_ln_column_sums_kernel, (unsigned)((2 * (int64_t)p.D + 31) / 32), 256, 0, stream, p.partials, grid,
+        e = launch_pdl(kt_ln_column_sums_kernel, (unsigned)((2 * (int64_t)p.D + 31) / 32), kSumRuns * 32, 0, stream, p.partials, grid,
                        p.D, p.dgamma, p.dbeta);
         if (e != cudaSuccess) {
             *why = cudaGetErrorString(e);
