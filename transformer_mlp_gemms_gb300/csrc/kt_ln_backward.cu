@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(row_block(W), ln_back_per_sm(W, V)) kt_ln_back
 }
 
 // Adds the blocks' rows of partial sums, in order: out[c] = sum_r partials[r][c] over the 2 D
-// columns (dgamma, then dbeta).  32 columns and 16 runs of rows per block, so that a run's loads
-// (at most 30) are in flight together.
+// columns (dgamma, then dbeta).  32 columns and 16 runs of rows per block (729 x 1152: 5.8 us for
+// the whole backward pass; 8 runs 6.3).
 constexpr int kSumRuns = 16;
 __global__ void __launch_bounds__(kSumRuns * 32) kt_ln_column_sums_kernel(const float* __restrict__ partials, int rows, int D,
                                                                           float* __restrict__ dgamma, float* __restrict__ dbeta) {
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kSumRuns * 32) kt_ln_column_sums_kernel(const 
     const int per = (rows + kSumRuns - 1) / kSumRuns, r1 = min(rows, (run + 1) * per);
     float v = 0.0f;
     if (c < 2 * D) {
-#pragma unroll 10
+#pragma unroll 4
         for (int r = run * per; r < r1; ++r) v += partials[(size_t)r * 2 * D + c];
     }
     part[run][lane] = v;
