@@ -33,7 +33,7 @@ namespace {
 constexpr int kMoeWarps = 16, kMoeThreads = kMoeWarps * 32;
 constexpr int kMoePairs = KT_MOE_MAX_TOKENS * KT_MOE_MAX_TOP_K;
 constexpr int kMoeWeightBytes = 128 * 128;  // a stage's weights: 128 rows x 64 columns
-constexpr int kMoeMaxStages = 10;
+constexpr int kMoeMaxStages = 12;
 constexpr int kMoeWeightThreads = 2;       // threads that issue the weights' copies, in turn
 constexpr int kMoeEpiWarps = 4;             // warps 4-7
 constexpr uint32_t kMoeAccCols = 128;       // tensor-memory columns of one accumulator buffer
