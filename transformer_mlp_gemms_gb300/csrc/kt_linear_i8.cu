@@ -161,14 +161,13 @@ __global__ void __launch_bounds__(kDotWarps * 32) kt_linear_i8_dot_kernel(const 
 // of its 32 bytes in one stage, the others in the next), and the channels follow the same order.
 // Four bytes become two pairs of fp16 in five instructions: with the sign bit flipped a byte is
 // q + 128, and next to the byte 0x64 it is the fp16 number 1024 + (q + 128); 1152 is subtracted.
-constexpr int kTcStages = 8;  // of 64 columns; a step of 128 columns is two
+constexpr int kTcSlots = 4;   // steps of 128 columns in the ring: 64 tensor-memory columns of tokens each
 constexpr int kTcGroups = 2;  // producers of even and of odd steps
 constexpr int kTcTokenWarps = 4, kTcChannelWarps = 4, kTcEpiWarps = 8;  // tokens, channels: per group
-constexpr int kTcForward = 4;  // threads of a pair's second CTA that forward its full stages
 constexpr int kTcChannel0 = kTcGroups * kTcTokenWarps, kTcEpi0 = kTcChannel0 + kTcGroups * kTcChannelWarps;
-constexpr int kTcMmaWarp = kTcEpi0 + kTcEpiWarps, kTcThreads = (kTcMmaWarp + kTcForward) * 32;
-static_assert(kTcStages % (2 * kTcGroups) == 0 && kTcEpi0 % 4 == 0, "whole steps per round of the ring; epilogue warp q: lanes 32 q");
-constexpr uint32_t kTcACol = 256;  // tensor-memory column of the first operand's stages, after the accumulators
+constexpr int kTcMmaWarp = kTcEpi0 + kTcEpiWarps, kTcThreads = (kTcMmaWarp + kTcSlots) * 32;
+static_assert(kTcSlots % kTcGroups == 0 && kTcEpi0 % 4 == 0, "a group has slots of its own; epilogue warp q: lanes 32 q");
+constexpr uint32_t kTcACol = 256;  // tensor-memory column of the first operand's slots, after the accumulators
 __device__ int g_linear_i8_error;  // a bounded wait that ran out (never in normal operation)
 
 __device__ __forceinline__ void bytes_to_halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -205,38 +204,48 @@ __device__ __forceinline__ void load32(const int8_t* p, int left, bool wide, uin
 }
 
 // The product with its first operand in tensor memory (PAIR = 2: 128 rows in each CTA's, half of
-// the channels in each CTA's shared memory, at the same places).
+// the channels in each CTA's shared memory, at the same places).  The whole warp calls it with the
+// same arguments and `leader` in one lane, so that they are in uniform registers, where the
+// instruction wants them; a lone thread's were moved there each time, 66 cycles per product.
 template <int PAIR>
 __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                           uint32_t accumulate) {
+                                           uint32_t accumulate, uint32_t leader) {
     if constexpr (PAIR == 2)
         asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-            "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            "{\n\t.reg .pred p, l;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %5, 0;\n\t"
+            "@l tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-            "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            "{\n\t.reg .pred p, l;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %5, 0;\n\t"
+            "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
             : "memory");
 }
 template <int PAIR>
-__device__ __forceinline__ void commit_ta(uint32_t bar) {
-    if constexpr (PAIR == 2) mma_commit_pair(bar);
-    else mma_commit(bar);
+__device__ __forceinline__ void commit_ta(uint32_t bar, uint32_t leader) {
+    if constexpr (PAIR == 2)
+        asm volatile(
+            "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %2, 0;\n\t"
+            "@l tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+            "h"((unsigned short)3), "r"(leader)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %1, 0;\n\t"
+            "@l tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+            "r"(leader)
+            : "memory");
 }
 
 template <int BN, int PAIR>
 struct TcSmem {
-    alignas(1024) uint8_t b[kTcStages][BN / PAIR * 128];  // [channel][64 fp16], 128-byte swizzle
+    alignas(1024) uint8_t b[kTcSlots][2][BN / PAIR * 128];  // [channel][64 fp16], 128-byte swizzle
     static constexpr int kParts = (BN + 127) / 128;  // 64-column parts per epilogue warp
     alignas(128) uint8_t out[kTcEpiWarps][kParts][32 * 128];  // 32 rows x 64 columns of the output each
     float2 ch[2][BN];                               // channel scale and bias of the tile
-    alignas(8) uint64_t full[kTcStages], empty[kTcStages], acc_full[2], acc_empty[2], drain;
+    alignas(8) uint64_t full[kTcSlots], empty[kTcSlots], acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     int abort;
 };
@@ -256,7 +265,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
     const int rank = PAIR == 2 ? (int)cluster_ctarank() : 0;
     const int unit = (int)blockIdx.x / PAIR, units = (int)gridDim.x / PAIR;  // CTAs or pairs
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kTcStages; ++s) {
+        for (int s = 0; s < kTcSlots; ++s) {
             // the first CTA of a pair also waits for the other's forwarded arrival
             mbar_init(bar(sm.full[s]), kTcTokenWarps + kTcChannelWarps + (PAIR == 2 && rank == 0 ? 1 : 0));
             mbar_init(bar(sm.empty[s]), 1);
@@ -286,14 +295,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(p.W + (int64_t)(n0 + i % kShare) * p.ldw + i / kShare * 128));
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int steps = (p.K + 127) / 128, kblocks = 2 * steps;
+    const int steps = (p.K + 127) / 128;
     const int mine = tiles > unit ? (tiles - 1 - unit) / units + 1 : 0;
     const int total = mine * steps;  // steps of all this CTA's tiles, in order
 
     // A producer group's loop over its steps of 128 columns, every kTcGroups-th of the CTA's: N
-    // pieces of 32 bytes per thread in registers; when their stages are free, the pieces' first
-    // halves are converted into one and the second halves into the other, and the next step's
-    // loads go out, to arrive while the other group converts.
+    // pieces of 32 bytes per thread in registers; when their slot is free, the pieces' first halves are
+    // converted into its first 64 columns and the second halves into the others, and the next
+    // step's loads go out, to arrive while the other group converts.
     auto produce = [&](auto pieces, int group, auto&& open_tile, auto&& load, auto&& convert) {
         constexpr int N = decltype(pieces)::value;
         uint4 reg[2][N];
@@ -310,22 +319,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
             load(reg, k * 128);
             k += kTcGroups;
         };
-        uint32_t first = 2u * group, phase = 0;  // the step's first stage
+        uint32_t slot = group, phase = 0;
         if (group < total) fetch();
         for (int s = group; s < total; s += kTcGroups) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t stage = first + h;
-                const bool ok = wait_phase(bar(sm.empty[stage]), phase ^ 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_PRODUCER, kLimit);
-                if (!__all_sync(0xffffffffu, ok)) return;
-                convert(reg[h], stage);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(sm.full[stage]));
-            }
+            const bool ok = wait_phase(bar(sm.empty[slot]), phase ^ 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_PRODUCER, kLimit);
+            if (!__all_sync(0xffffffffu, ok)) return;
+            convert(reg, slot);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(sm.full[slot]));
             if (s + kTcGroups < total) fetch();
-            first += 2 * kTcGroups;
-            if (first >= kTcStages) {
-                first -= kTcStages;
+            slot += kTcGroups;
+            if (slot >= kTcSlots) {
+                slot -= kTcSlots;
                 phase ^= 1u;
             }
         }
@@ -350,20 +355,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
 #pragma unroll
                 for (int j = 0; j < 4; ++j) load32(row + j * pitch8 + k, 8 * j < rows ? k_end - k : 0, wide_q, r[0][j], r[1][j]);
             },
-            [&](const uint4 (&r)[4], uint32_t stage) {
+            [&](const uint4 (&r)[2][4], uint32_t slot) {
                 tc_fence_after();
 #pragma unroll
-                for (int j = 0; j < 4; j += 2) {  // rows lane / 4 + 8 j and + 8 j + 8 of the warp's 32
-                    uint32_t h[16];
+                for (int half = 0; half < 2; ++half)
 #pragma unroll
-                    for (int o = 0; o < 2; ++o) {
-                        bytes_to_halves(r[j + o].x, h[2 * o], h[2 * o + 1]);
-                        bytes_to_halves(r[j + o].y, h[2 * o + 4], h[2 * o + 5]);
-                        bytes_to_halves(r[j + o].z, h[2 * o + 8], h[2 * o + 9]);
-                        bytes_to_halves(r[j + o].w, h[2 * o + 12], h[2 * o + 13]);
+                    for (int j = 0; j < 4; j += 2) {  // rows lane / 4 + 8 j and + 8 j + 8 of the warp's 32
+                        uint32_t h[16];
+#pragma unroll
+                        for (int o = 0; o < 2; ++o) {
+                            bytes_to_halves(r[half][j + o].x, h[2 * o], h[2 * o + 1]);
+                            bytes_to_halves(r[half][j + o].y, h[2 * o + 4], h[2 * o + 5]);
+                            bytes_to_halves(r[half][j + o].z, h[2 * o + 8], h[2 * o + 9]);
+                            bytes_to_halves(r[half][j + o].w, h[2 * o + 12], h[2 * o + 13]);
+                        }
+                        tmem_st_16x32(tmem + ((uint32_t)(q * 32 + 8 * j) << 16) + kTcACol + slot * 64u + 32u * half, h);
                     }
-                    tmem_st_16x32(tmem + ((uint32_t)(q * 32 + 8 * j) << 16) + kTcACol + stage * 32u, h);
-                }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
             });
@@ -378,7 +385,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
         const int64_t pitch32 = 32 * p.ldw;
         const int k_end = p.K - 32 * c;
         // words 2 c and 2 c + 1 of every eight: chunk 2 i + c / 2 of the row, swizzled by its number
-        const uint32_t dst = smem_u32(sm.b[0]) + (uint32_t)n_in * 128u + 8u * (c & 1);
+        const uint32_t dst = smem_u32(sm.b[0][0]) + (uint32_t)n_in * 128u + 8u * (c & 1);
         const uint32_t first = (uint32_t)((c >> 1) ^ (n_in & 7)) << 4;
         produce(
             std::integral_constant<int, kPieces>{}, (warp - kTcChannel0) / kTcChannelWarps,
@@ -391,69 +398,74 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
                 for (int j = 0; j < kPieces; ++j)
                     load32(row + j * pitch32 + k, 32 * j < rows ? k_end - k : 0, wide_w, r[0][j], r[1][j]);
             },
-            [&](const uint4 (&r)[kPieces], uint32_t stage) {
-                const uint32_t at = dst + stage * (uint32_t)(kShare * 128);
+            [&](const uint4 (&r)[2][kPieces], uint32_t slot) {
 #pragma unroll
-                for (int j = 0; j < kPieces; ++j) {
-                    const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t at = dst + (2u * slot + half) * (uint32_t)(kShare * 128);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // four bytes: two words
-                        uint32_t lo, hi;
-                        bytes_to_halves(w[i], lo, hi);
-                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + j * 32u * 128u + (first ^ (uint32_t)(2 * i) << 4)),
-                                     "r"(lo), "r"(hi)
-                                     : "memory");
+                    for (int j = 0; j < kPieces; ++j) {
+                        const uint32_t w[4] = {r[half][j].x, r[half][j].y, r[half][j].z, r[half][j].w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {  // four bytes: two words
+                            uint32_t lo, hi;
+                            bytes_to_halves(w[i], lo, hi);
+                            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + j * 32u * 128u + (first ^ (uint32_t)(2 * i) << 4)),
+                                         "r"(lo), "r"(hi)
+                                         : "memory");
+                        }
                     }
                 }
                 fence_async_smem();  // the tensor cores read it through the async proxy
             });
     } else if (warp >= kTcMmaWarp) {
         if (PAIR == 2 && rank == 1) {
-            // ------------------- the pair's second CTA: its full stages are told to the first -------------------
+            // ------------------- the pair's second CTA: its full slots are told to the first -------------------
             // (an arrival that orders what came before it at cluster scope costs its thread about
-            // 0.35 us, more than a stage takes: four threads in turn)
+            // 0.35 us: one thread per slot)
             if (lane == 0) {
-                uint32_t s = warp - kTcMmaWarp, phase = 0;
-                for (int i = s; i < 2 * total; i += kTcForward) {
-                    if (!wait_phase(bar(sm.full[s]), phase, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_MMA, kLimit)) break;
+                const int slot = warp - kTcMmaWarp;
+                const uint32_t to = mapa_rank(bar(sm.full[slot]), 0u);
+                uint32_t phase = 0;
+                for (int s = slot; s < total; s += kTcSlots, phase ^= 1u) {
+                    if (!wait_phase(bar(sm.full[slot]), phase, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_MMA, kLimit)) break;
                     tc_fence_after();
                     tc_fence_before();
-                    mbar_arrive_cluster(mapa_rank(bar(sm.full[s]), 0u));
-                    s += kTcForward;
-                    if (s >= kTcStages) {
-                        s -= kTcStages;
-                        phase ^= 1u;
-                    }
+                    mbar_arrive_cluster(to);
                 }
             }
-        } else if (warp == kTcMmaWarp && lane == 0) {
-            // ------------------- one thread issues the products -------------------
-            uint32_t stage = 0, phase = 0;
+        } else if (warp == kTcMmaWarp) {
+            // ------------------- one warp, of which one lane issues the products -------------------
+            uint32_t slot = 0, phase = 0;
+            const uint32_t leader = lane == 0;
             bool ok = true;
+            const uint64_t bd0 = smem_desc(smem_u32(sm.b[0][0]), 16u, 1024u);
             for (int t = 0; t < mine && ok; ++t) {
-                const uint32_t buf = t % kBufs, use = (uint32_t)t / kBufs;
-                ok = wait_phase<PAIR == 2>(bar(sm.acc_empty[buf]), (use & 1u) ^ 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_MMA, kLimit);
-                for (int kb = 0; kb < kblocks && ok; ++kb) {
-                    ok = wait_phase<PAIR == 2>(bar(sm.full[stage]), phase, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_MMA, kLimit);
+                const uint32_t buf = t % kBufs, use = (uint32_t)t / kBufs, d = tmem + buf * (uint32_t)BN;
+                ok = __all_sync(0xffffffffu, wait_phase<PAIR == 2>(bar(sm.acc_empty[buf]), (use & 1u) ^ 1u, abort_flag, &g_linear_i8_error,
+                                                                   DEV_TIMEOUT_MMA, kLimit));
+                for (int s = 0; s < steps && ok; ++s) {
+                    ok = __all_sync(0xffffffffu, wait_phase<PAIR == 2>(bar(sm.full[slot]), phase, abort_flag, &g_linear_i8_error,
+                                                                       DEV_TIMEOUT_MMA, kLimit));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t bd = smem_desc(smem_u32(sm.b[stage]), 16u, 1024u);
-                    const uint32_t a = tmem + kTcACol + stage * 32u;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f16_ta<PAIR>(tmem + buf * (uint32_t)BN, a + 8u * k, bd + (uint64_t)(2 * k), idesc, kb > 0 || k > 0);
-                    commit_ta<PAIR>(bar(sm.empty[stage]));
-                    if (++stage == kTcStages) {
-                        stage = 0;
+                    for (int k = 0; k < 8; ++k)
+                        mma_f16_ta<PAIR>(d, tmem + kTcACol + slot * 64u + 8u * k,
+                                         bd0 + (uint64_t)((2u * slot + k / 4) * (uint32_t)(kShare * 128 / 16) + 2u * (k % 4)), idesc,
+                                         s > 0 || k > 0, leader);
+                    commit_ta<PAIR>(bar(sm.empty[slot]), leader);
+                    if (++slot == kTcSlots) {
+                        slot = 0;
                         phase ^= 1u;
                     }
                 }
-                if (ok) commit_ta<PAIR>(bar(sm.acc_full[buf]));
+                if (ok) commit_ta<PAIR>(bar(sm.acc_full[buf]), leader);
             }
             if (!ok) {  // no product may still be running when tensor memory is freed
-                commit_ta<PAIR>(bar(sm.drain));
-                wait_drain(bar(sm.drain), 0u, 100000000ull);
+                commit_ta<PAIR>(bar(sm.drain), leader);
+                if (lane == 0) wait_drain(bar(sm.drain), 0u, 100000000ull);
             }
+            __syncwarp();
         }
     } else {
         // ------------------- epilogue -------------------
