@@ -133,6 +133,29 @@ def test_the_largest_sums(M, K):
     assert ((y.double() - yx).abs() <= tol + (ref.half(torch.float16) + extra) * yx.abs()).all()
 
 
+@pytest.mark.parametrize("M", [8, 100, 300])
+def test_sums_that_cancel_are_exact(M):
+    """Partial sums of 2^23 that come back to small integers, which float16 holds: not one unit lost."""
+    g = torch.Generator().manual_seed(M)
+    N, half = 80, 512
+    sign = torch.randint(0, 2, (1, half), generator=g) * 2 - 1
+    q1 = (127 * sign).expand(M, half).clone()
+    w1 = (127 * sign).expand(N, half).clone()
+    back = -w1
+    for n in range(N):  # up to 15 entries of the second half are off by one
+        at = torch.randperm(half, generator=g)[:n % 16]
+        back[n, at] += -back[n, at].sign()
+    q = torch.cat([q1, q1], 1).to(torch.int8).cuda()
+    w = torch.cat([w1, back], 1).to(torch.int8).cuda()
+    q[:, 3] = torch.randint(-127, 128, (M,), generator=g, dtype=torch.int32).to(torch.int8).cuda()  # rows differ
+    q[:, half + 3] = q[:, 3]
+    y = torch.empty(M, N, dtype=torch.float16, device="cuda")
+    kt_ops.kt_linear_i8(q, torch.ones(M, device="cuda"), w, torch.ones(N, device="cuda"), None, y)
+    exact = q.cpu().long() @ w.cpu().long().t()
+    assert exact.abs().max() <= 2048 and exact.unique().numel() > 10
+    assert torch.equal(y.cpu().long(), exact)
+
+
 def test_quantised_layer_in_a_graph_and_on_another_stream():
     g = torch.Generator().manual_seed(3)
     M, N, K = 200, 320, 640

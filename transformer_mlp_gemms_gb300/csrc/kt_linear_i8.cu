@@ -142,23 +142,31 @@ __global__ void __launch_bounds__(kDotWarps * 32) kt_linear_i8_dot_kernel(const 
 // the operands become fp16 on their way into the tensor cores, and the bytes that move stay one
 // per element.
 //
-// One persistent CTA per SM, tiles of 128 tokens x BN channels, k-blocks of 64:
+// One persistent CTA per SM: tiles of 128 tokens x BN channels, or, above 128 tokens, a pair of CTAs
+// (cta_group::2) with 128 tokens each and half of the channels' weights; steps of 128 columns
+// through a ring of four slots:
 //   warps 0-7    tokens: rows of 128 bytes (4 lanes x 32) from global memory, stored as fp16 into
-//                tensor memory, where the product reads its first operand (32 columns per stage of
-//                64, 4 stages).  That operand never passes through shared memory, whose bandwidth
-//                would bound the kernel: 128 x 192 x 64 takes the tensor cores 384 cycles, writing
-//                and reading the second operand takes shared memory the same 384, the first one's
-//                16 KB would add 256;
+//                tensor memory, where the product reads its first operand (64 columns per slot);
+//                as fp16 that operand never passes through shared memory, whose bandwidth, written
+//                and read, would bound the kernel;
 //   warps 8-15   channels: rows of the weight likewise, into shared memory as fp16, K-major with
 //                the 128-byte swizzle.  Both kinds are two groups of four warps that take the
-//                steps of 128 columns in turn, so that one's loads arrive while the other converts;
-//   warps 16-19  epilogue: accumulator x token scale x channel scale (+ bias), one rounding,
-//                rows of 64 columns put together in shared memory and stored as full lines;
-//   warp 20      one thread issues tcgen05.mma (fp16, fp32 accumulators, two buffers of BN
-//                columns, so that a tile's epilogue runs beside the next tile's products).
+//                steps in turn, so that one's loads arrive while the other converts;
+//   warps 16-23  epilogue: accumulator x token scale x channel scale (+ bias), one rounding, parts
+//                of 64 columns put together in shared memory, then stored as full lines;
+//   warp 24      issues tcgen05.mma (fp16, fp32 accumulators: two buffers, so that a tile's
+//                epilogue runs beside the next tile's products, or one of 192 or 256 columns);
+//   warps 24-27  of a pair's second CTA tell the first of its full slots.
 // A sum over k may take its terms in any order.  So the bytes of a step go where their lanes' places
 // in tensor memory are (lane c of a row's four: words 2 c and 2 c + 1 of every eight; the first 16
-// of its 32 bytes in one stage, the others in the next), and the channels follow the same order.
+// of its 32 bytes in the slot's first half, the others in the second), and the channels follow the
+// same order.
+// Bound by the products for long rows and many tokens: 8192 x 8192 x 8192 takes 637 us, 1.73
+// PFLOP/s (90% of the measured bf16 rate); 16384 x 4304 x 1152 takes 114 us, 1.42 PFLOP/s, where
+// a tile's 9 steps are followed by the wait for its accumulator.  The steps there, in us: a thread's
+// own row per load (32 wavefronts each) 279, rows shared by four lanes 258, row pointers kept 184,
+// two groups in turn 153, pairs 139, 256 channels with twice the ring 131, all parts staged before
+// the stores 125, one barrier per step and the products issued from uniform registers 114.
 // Four bytes become two pairs of fp16 in five instructions: with the sign bit flipped a byte is
 // q + 128, and next to the byte 0x64 it is the fp16 number 1024 + (q + 128); 1152 is subtracted.
 constexpr int kTcSlots = 4;   // steps of 128 columns in the ring: 64 tensor-memory columns of tokens each
@@ -616,12 +624,12 @@ kt_status launch_tc(int dtype, const LinearI8& p, int sms, int device, void* str
 kt_status launch_linear_i8(int dtype, const LinearI8& p, int sms, int device, void* stream, const char** why) {
     if (p.M > KT_LINEAR_I8_DOT_ROWS) {
         // tile width: rounds over the CTAs (or pairs) times a round's time.  Measured per round of
-        // 76 pairs (18 stages, K = 1152): 8.5, 7.5, 6.1 and 5.6 us for 256, 192, 128 and 64
-        // channels; 30.2, 25.0, 22.3 and 21.0 us for 72 stages.
+        // 76 pairs (9 steps, K = 1152): 8.6, 6.5, 5.2 and 4.6 us for 256, 192, 128 and 64 channels;
+        // 30.1, 21.7, 18.5 and 17.0 us for 36 steps.
         const int pair = p.M > 128 ? 2 : 1;
         const int64_t tm = (p.M + 128 * pair - 1) / (128 * pair), units = sms / pair;
         auto cost = [&](int bn, int per) { return ((tm * ((p.N + bn - 1) / bn) + units - 1) / units) * per; };
-        const int64_t c256 = cost(256, 85), c192 = cost(192, 75), c128 = cost(128, 61), c64 = cost(64, 56);
+        const int64_t c256 = cost(256, 86), c192 = cost(192, 65), c128 = cost(128, 52), c64 = cost(64, 46);
         if (pair == 2) {
             if (c256 <= c192 && c256 <= c128 && c256 <= c64) return launch_tc<256, 2>(dtype, p, sms, device, stream, why);
             if (c192 <= c128 && c192 <= c64) return launch_tc<192, 2>(dtype, p, sms, device, stream, why);
