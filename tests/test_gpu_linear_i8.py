@@ -190,3 +190,27 @@ def test_no_tokens():
     kt_ops.kt_linear_i8(q, s, torch.zeros(8, 64, dtype=torch.int8, device="cuda"), torch.zeros(8, device="cuda"), None,
                         torch.empty(0, 8, dtype=torch.float16, device="cuda"))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype,bias", [("f16", True), ("bf16", False)])
+@pytest.mark.parametrize("M,N,K", [(17, 1280, 5120), (100, 8192, 8192), (127, 131, 1168), (129, 520, 4304), (256, 512, 8192), (257, 510, 4112),
+                                   (729, 1152, 4304), (20, 8, 16384), (500, 65, 2064), (128, 640, 1040)])
+def test_long_rows_of_few_tiles(M, N, K, dtype, bias):
+    """Tiles whose steps are shared out: against the definition, at an odd pitch, and the same bits again."""
+    g = torch.Generator().manual_seed(M + N + K)
+    dt = DT[dtype]
+    q = torch.randint(-127, 128, (M, K + 16), generator=g, dtype=torch.int32).to(torch.int8).cuda()[:, :K]
+    w = torch.randint(-128, 128, (N, K), generator=g, dtype=torch.int32).to(torch.int8).cuda()
+    sx, sw = (torch.rand(M, generator=g) * 1e-3).cuda(), (torch.rand(N, generator=g) * 1e-2).cuda()
+    b = torch.randn(N, generator=g).to(dt).cuda() if bias else None
+    yx, tol = ref.linear_i8(q, sx, w, sw, b)
+    for pad in (0, 3):
+        whole = torch.full((M, N + pad), 7.0, dtype=dt, device="cuda")
+        kt_ops.kt_linear_i8(q, sx, w, sw, b, whole[:, :N])
+        y = whole[:, :N]
+        bad = ~((y.double() - yx).abs() <= tol + ref.half(dt) * yx.abs() + ref.floor(dt))
+        assert not bad.any(), (int(bad.sum()), bad.nonzero()[0].tolist(), y[bad][0].item(), yx[bad][0].item())
+        assert (whole[:, N:] == 7).all()
+        again = torch.empty_like(whole)[:, :N]
+        kt_ops.kt_linear_i8(q, sx, w, sw, b, again)
+        assert torch.equal(again, y)

@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(kDotWarps * 32) kt_linear_i8_dot_kernel(const 
 //   warp 24      issues tcgen05.mma (fp16, fp32 accumulators: two buffers, so that a tile's
 //                epilogue runs beside the next tile's products, or one of 192 or 256 columns);
 //   warps 24-27  of a pair's second CTA tell the first of its full slots.
+// Few tiles with long rows: a cluster per tile instead, each CTA with its share of the steps (SPLIT).
 // A sum over k may take its terms in any order.  So the bytes of a step go where their lanes' places
 // in tensor memory are (lane c of a row's four: words 2 c and 2 c + 1 of every eight; the first 16
 // of its 32 bytes in the slot's first half, the others in the second), and the channels follow the
@@ -258,7 +259,30 @@ struct TcSmem {
     int abort;
 };
 
-template <int DT, int BN, int PAIR>
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+// Four fp32 sums of a CTA of this cluster.
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// Byte of four columns (chunk) of a row of a split tile's sums, [128][BN] fp32: the chunks swizzled by
+// the row's number, so that neither rows over lanes nor columns over lanes share banks.
+template <int BN>
+__device__ __forceinline__ uint32_t split_at(int row, int chunk) {
+    return (uint32_t)(row * BN * 4 + ((chunk ^ (row & 7)) << 4));
+}
+
+// SPLIT (PAIR = 1): one tile per cluster of up to 8 CTAs, each with its share of the tile's steps.
+// Their sums meet through the cluster's shared memory: each CTA adds its share of the tile's rows
+// over all of them, in the order of their ranks, and stores it.
+template <int DT, int BN, int PAIR, bool SPLIT>
 __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const LinearI8 p, int tiles_n, int tiles, uint32_t idesc,
                                                                         int wide_y) {
     extern __shared__ uint8_t raw[];
@@ -271,7 +295,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
     constexpr unsigned long long kLimit = 4000000000ull;  // 4 s: far beyond any legitimate wait
     auto bar = [&](uint64_t& b) { return smem_u32(&b); };
     const int rank = PAIR == 2 ? (int)cluster_ctarank() : 0;
-    const int unit = (int)blockIdx.x / PAIR, units = (int)gridDim.x / PAIR;  // CTAs or pairs
+    const int splits = SPLIT ? (int)cluster_size() : 1, part = SPLIT ? (int)cluster_ctarank() : 0;
+    const int unit = (int)blockIdx.x / (PAIR * splits), units = (int)gridDim.x / (PAIR * splits);  // CTAs, pairs or clusters
+    const int all_steps = (p.K + 127) / 128, step0 = all_steps * part / splits;
+    const int steps = all_steps * (part + 1) / splits - step0;  // of a tile, in this CTA
     if (threadIdx.x == 0) {
         for (int s = 0; s < kTcSlots; ++s) {
             // the first CTA of a pair also waits for the other's forwarded arrival
@@ -297,13 +324,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
     // the first tile's weights start on their way to L2 while the kernel before this one still runs
     // (a prefetch reads nothing)
     if (warp >= kTcChannel0 && warp < kTcEpi0 && unit < tiles) {
-        const int n0 = (unit % tiles_n) * BN + rank * kShare, lines = min((p.K + 127) / 128, 64);
+        const int n0 = (unit % tiles_n) * BN + rank * kShare, lines = min(steps, 64);
         for (int i = (int)threadIdx.x - kTcChannel0 * 32; i < kShare * lines; i += kTcGroups * kTcChannelWarps * 32)
             if (n0 + i % kShare < p.N)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.W + (int64_t)(n0 + i % kShare) * p.ldw + i / kShare * 128));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.W + (int64_t)(n0 + i % kShare) * p.ldw + (step0 + i / kShare) * 128));
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int steps = (p.K + 127) / 128;
     const int mine = tiles > unit ? (tiles - 1 - unit) / units + 1 : 0;
     const int total = mine * steps;  // steps of all this CTA's tiles, in order
 
@@ -324,7 +350,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
                 open_tile((tile / tiles_n * PAIR + rank) * 128, (tile % tiles_n) * BN + rank * kShare);
                 opened = tile;
             }
-            load(reg, k * 128);
+            load(reg, (step0 + k) * 128);
             k += kTcGroups;
         };
         uint32_t slot = group, phase = 0;
@@ -498,6 +524,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
             // first all of this warp's columns into shared memory, so that the next tile gets the
             // accumulator soon; then the stores
             const int first = 64 * (ew >> 2);
+            if constexpr (SPLIT) {  // fp32, where the weights were: every product has read them
+#pragma unroll 1
+                for (int c0 = first; c0 < min(first + 64, BN); c0 += 32) {
+                    uint32_t r[32];
+                    tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + c0, r);
+                    tmem_wait_ld_only();
+                    reg_fence32(r);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4*>(sm.b[0][0] + split_at<BN>(q * 32 + lane, c0 / 4 + i)) =
+                            make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                }
+                break;
+            }
             __syncwarp();  // the previous tile's stores have read the buffers
 #pragma unroll 1
             for (int c0 = first; c0 < BN; c0 += 128) {
@@ -557,7 +597,43 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
     }
     tc_fence_before();
     __syncthreads();
-    if (PAIR == 2) cluster_sync_all();  // neither CTA leaves while the other may still signal it
+    if (PAIR == 2 || SPLIT) cluster_sync_all();  // neither CTA leaves while the other may still signal it; SPLIT: the sums are there
+    if constexpr (SPLIT) {
+        uint16_t* Y = static_cast<uint16_t*>(p.Y);
+        const int m0 = unit / tiles_n * 128, n0 = (unit % tiles_n) * BN;
+        const int row0 = 128 * part / splits, rows = min(128 * (part + 1) / splits, p.M - m0) - row0;
+        const uint32_t base = smem_u32(sm.b[0][0]);
+        for (int i = threadIdx.x; i < rows * (BN / 4); i += kTcThreads) {
+            const int r = row0 + i / (BN / 4), c = i % (BN / 4), n = n0 + 4 * c;
+            if (n >= p.N) continue;
+            const float sx = p.sx[m0 + r];
+            float4 v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < splits) v[j] = ld_cluster4(mapa_rank(base + split_at<BN>(r, c), (uint32_t)j));
+#pragma unroll
+            for (int j = 1; j < 8; ++j)
+                if (j < splits) {
+                    v[0].x += v[j].x;
+                    v[0].y += v[j].y;
+                    v[0].z += v[j].z;
+                    v[0].w += v[j].w;
+                }
+            const float4 a = *reinterpret_cast<const float4*>(&sm.ch[0][4 * c]), b = *reinterpret_cast<const float4*>(&sm.ch[0][4 * c + 2]);
+            const uint32_t lo = pack2<DT>(fmaf(v[0].x, sx * a.x, a.y), fmaf(v[0].y, sx * a.z, a.w));
+            const uint32_t hi = pack2<DT>(fmaf(v[0].z, sx * b.x, b.y), fmaf(v[0].w, sx * b.z, b.w));
+            uint16_t* y = Y + (int64_t)(m0 + r) * p.ldy + n;
+            if (wide_y) {
+                *reinterpret_cast<uint2*>(y) = make_uint2(lo, hi);
+            } else {
+                y[0] = (uint16_t)lo;
+                if (n + 1 < p.N) y[1] = (uint16_t)(lo >> 16);
+                if (n + 2 < p.N) y[2] = (uint16_t)hi;
+                if (n + 3 < p.N) y[3] = (uint16_t)(hi >> 16);
+            }
+        }
+        cluster_sync_all();  // the others have read this CTA's sums
+    }
     if (warp == kTcMmaWarp) {
         __syncwarp();
         tc_fence_after();
@@ -587,29 +663,71 @@ kt_status launch_dot(int dtype, const LinearI8& p, void* stream, const char** wh
     return KT_OK;
 }
 
-template <int BN, int PAIR>
-kt_status launch_tc(int dtype, const LinearI8& p, int sms, int device, void* stream, const char** why) {
-    const int tiles_m = (p.M + 128 * PAIR - 1) / (128 * PAIR), tiles_n = (p.N + BN - 1) / BN, tiles = tiles_m * tiles_n;
+inline int64_t tc_tiles(const LinearI8& p, int bn, int pair) {
+    return (int64_t)((p.M + 128 * pair - 1) / (128 * pair)) * ((p.N + bn - 1) / bn);
+}
+
+// The tensor-core kernel of a type, opted in to its shared memory.
+template <int BN, int PAIR, bool SPLIT>
+cudaError_t tc_kernel(int dtype, int device, decltype(&kt_linear_i8_tc_kernel<KT_F16, BN, PAIR, SPLIT>)* kern, int* smem) {
+    static SmemOptIn opt_in[2];  // by dtype
+    *kern = dtype == KT_BF16 ? kt_linear_i8_tc_kernel<KT_BF16, BN, PAIR, SPLIT> : kt_linear_i8_tc_kernel<KT_F16, BN, PAIR, SPLIT>;
+    *smem = (int)sizeof(TcSmem<BN, PAIR>) + 1024;
+    return opt_in[dtype == KT_BF16](*kern, *smem, device);
+}
+
+// attr: room for two.  `ctas` per cluster.
+inline cudaLaunchConfig_t tc_config(int grid, int ctas, int smem, void* stream, cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3(kTcThreads, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    return cfg;
+}
+
+// Clusters of ks (2, 4 or 8) CTAs that the device holds at once; 0 if it cannot say.
+template <int BN>
+int tc_clusters(int dtype, int ks, int device) {
+    static std::atomic<int> known[64][3];  // + 1, by device and ks: both types need the same
+    const int slot = ks == 2 ? 0 : ks == 4 ? 1 : 2;
+    int n = known[device & 63][slot].load(std::memory_order_relaxed) - 1;
+    if (n >= 0) return n;
+    decltype(&kt_linear_i8_tc_kernel<KT_F16, BN, 1, true>) kern;
+    int smem;
+    cudaLaunchAttribute attr[2];
+    n = 0;
+    if (tc_kernel<BN, 1, true>(dtype, device, &kern, &smem) == cudaSuccess) {
+        const cudaLaunchConfig_t cfg = tc_config(ks, ks, smem, nullptr, attr);
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+    }
+    known[device & 63][slot].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+// splits > 1 (SPLIT): clusters of so many CTAs, one tile each.
+template <int BN, int PAIR, bool SPLIT = false>
+kt_status launch_tc(int dtype, const LinearI8& p, int sms, int device, void* stream, const char** why, int splits = 1) {
+    const int tiles_n = (p.N + BN - 1) / BN, tiles = (int)tc_tiles(p, BN, PAIR);
     // whole 16-byte pieces of Y's rows: the last one too, as N is a multiple of 8
     const int wide = p.N % 8 == 0 && p.ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(p.Y) & 15u) == 0;
-    auto kern = dtype == KT_BF16 ? kt_linear_i8_tc_kernel<KT_BF16, BN, PAIR> : kt_linear_i8_tc_kernel<KT_F16, BN, PAIR>;
-    constexpr int smem = (int)sizeof(TcSmem<BN, PAIR>) + 1024;
-    static SmemOptIn opt_in[2];  // by dtype
-    cudaError_t e = opt_in[dtype == KT_BF16](kern, smem, device);
+    decltype(&kt_linear_i8_tc_kernel<KT_F16, BN, PAIR, SPLIT>) kern;
+    int smem;
+    cudaError_t e = tc_kernel<BN, PAIR, SPLIT>(dtype, device, &kern, &smem);
     if (e == cudaSuccess) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(std::min(tiles, sms / PAIR) * PAIR), 1, 1);
-        cfg.blockDim = dim3(kTcThreads, 1, 1);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = static_cast<cudaStream_t>(stream);
         cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = PAIR;
-        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = PAIR == 2 ? 2 : 1;
+        const int grid = SPLIT ? tiles * splits : std::min(tiles, sms / PAIR) * PAIR;
+        const cudaLaunchConfig_t cfg = tc_config(grid, PAIR * splits, smem, stream, attr);
         e = cudaLaunchKernelEx(&cfg, kern, p, tiles_n, tiles, make_idesc(KT_F16, BN, 128 * PAIR, 1), wide);
     }
     if (e != cudaSuccess) {
@@ -622,21 +740,52 @@ kt_status launch_tc(int dtype, const LinearI8& p, int sms, int device, void* str
 }  // namespace
 
 kt_status launch_linear_i8(int dtype, const LinearI8& p, int sms, int device, void* stream, const char** why) {
+    // Up to 16 tokens the integer products: 10240 channels of 1280, 8 tokens 6.8 us (tensor cores 9.3),
+    // 16 8.9 (9.4), 24 11.2 (9.6).
     if (p.M > KT_LINEAR_I8_DOT_ROWS) {
         // tile width: rounds over the CTAs (or pairs) times a round's time.  Measured per round of
         // 76 pairs (9 steps, K = 1152): 8.6, 6.5, 5.2 and 4.6 us for 256, 192, 128 and 64 channels;
         // 30.1, 21.7, 18.5 and 17.0 us for 36 steps.
-        const int pair = p.M > 128 ? 2 : 1;
-        const int64_t tm = (p.M + 128 * pair - 1) / (128 * pair), units = sms / pair;
-        auto cost = [&](int bn, int per) { return ((tm * ((p.N + bn - 1) / bn) + units - 1) / units) * per; };
-        const int64_t c256 = cost(256, 86), c192 = cost(192, 65), c128 = cost(128, 52), c64 = cost(64, 46);
+        constexpr int kWidths = 4;
+        constexpr int bn[kWidths] = {256, 192, 128, 64}, per[kWidths] = {86, 65, 52, 46};
+        const int pair = p.M > 128 ? 2 : 1, steps = (p.K + 127) / 128;
+        int best = -1;
+        int64_t best_cost = 0, best_rounds = 0;
+        for (int i = pair == 2 ? 0 : 2; i < kWidths; ++i) {
+            const int64_t t = tc_tiles(p, bn[i], pair), units = sms / pair, rounds = (t + units - 1) / units;
+            if (best >= 0 && rounds * per[i] >= best_cost) continue;
+            best = i;
+            best_cost = rounds * per[i];
+            best_rounds = rounds;
+        }
+        // A single round of long rows waits for one step's loads after another's: clusters that share
+        // a tile's steps, where all of them fit at once.  A round's time in us with s steps per CTA,
+        // measured from 2 to 64 steps (within 1.5 us): 2.6 + 0.55 s and 3.0 + 0.60 s for 64 and 128
+        // channels (pairs: the same), and split 4.6 + 0.57 s and 4.7 + 0.70 s.  64 x 1280 x 5120
+        // 24.0 -> 10.3 us, 729 x 1152 x 4304 22.9 -> 18.1 us; no gain below about 8 steps.
+        if (best_rounds == 1) {
+            double least = 0.9 * (bn[best] <= 64 ? 2.6 + 0.55 * steps : 3.0 + 0.60 * steps);
+            int width = 0, ways = 1;
+            for (const int w : {64, 128})
+                for (int ks = 2; ks <= 8 && ks <= steps; ks *= 2) {
+                    const int s = (steps + ks - 1) / ks;
+                    const double time = w == 64 ? 4.6 + 0.57 * s : 4.7 + 0.70 * s;
+                    if (time >= least || tc_tiles(p, w, 1) * ks > sms) continue;
+                    if (tc_tiles(p, w, 1) > (w == 64 ? tc_clusters<64>(dtype, ks, device) : tc_clusters<128>(dtype, ks, device))) continue;
+                    least = time;
+                    width = w;
+                    ways = ks;
+                }
+            if (width == 64) return launch_tc<64, 1, true>(dtype, p, sms, device, stream, why, ways);
+            if (width == 128) return launch_tc<128, 1, true>(dtype, p, sms, device, stream, why, ways);
+        }
         if (pair == 2) {
-            if (c256 <= c192 && c256 <= c128 && c256 <= c64) return launch_tc<256, 2>(dtype, p, sms, device, stream, why);
-            if (c192 <= c128 && c192 <= c64) return launch_tc<192, 2>(dtype, p, sms, device, stream, why);
-            if (c128 <= c64) return launch_tc<128, 2>(dtype, p, sms, device, stream, why);
+            if (best == 0) return launch_tc<256, 2>(dtype, p, sms, device, stream, why);
+            if (best == 1) return launch_tc<192, 2>(dtype, p, sms, device, stream, why);
+            if (best == 2) return launch_tc<128, 2>(dtype, p, sms, device, stream, why);
             return launch_tc<64, 2>(dtype, p, sms, device, stream, why);
         }
-        if (c128 <= c64) return launch_tc<128, 1>(dtype, p, sms, device, stream, why);
+        if (best == 2) return launch_tc<128, 1>(dtype, p, sms, device, stream, why);
         return launch_tc<64, 1>(dtype, p, sms, device, stream, why);
     }
     // warps of a block that share a weight row's columns: as many as leave a step of 512 to each and
