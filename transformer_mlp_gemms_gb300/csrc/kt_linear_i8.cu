@@ -20,7 +20,9 @@ __device__ __forceinline__ float from_bits(uint16_t u) {
 // A few tokens.  Bound by the weight's bytes: each is read once (per 8 tokens) and meets 8
 // tokens in four-way integer products into 32-bit sums.  Eight lanes share a weight row (128
 // consecutive bytes per step), a warp covers 8 rows, and the tokens' rows are in shared
-// memory, read as 128-byte broadcasts to the four groups of a warp.
+// memory, read as 128-byte broadcasts to the four groups of a warp.  4 x 10240 x 1280 takes 6.7 us, 2
+// TB/s: one round of loads whose latency nothing hides, after a launch (10.3 us before the weights were
+// loaded ahead and sent for during the kernel before, 7.8 before the warps shared long rows).
 constexpr int kDotWarps = 4, kDotTokens = 8;
 constexpr int kDotAhead = 4;     // steps of 128 columns in registers
 constexpr int kDotChunk = 4096;  // columns of the tokens staged at a time, a multiple of kDotAhead * 128
@@ -748,7 +750,9 @@ kt_status launch_linear_i8(int dtype, const LinearI8& p, int sms, int device, vo
         // 30.1, 21.7, 18.5 and 17.0 us for 36 steps.
         constexpr int kWidths = 4;
         constexpr int bn[kWidths] = {256, 192, 128, 64}, per[kWidths] = {86, 65, 52, 46};
-        const int pair = p.M > 128 ? 2 : 1, steps = (p.K + 127) / 128;
+        // One CTA per tile, not a pair, where all tiles fit at once: a pair's start and end cost 1 us
+        // (1000 x 1152 x 1152 9.4 -> 8.2 us, 1000 x 1152 x 320 6.3 -> 4.9).
+        const int pair = p.M > 128 && tc_tiles(p, 128, 1) > sms ? 2 : 1, steps = (p.K + 127) / 128;
         int best = -1;
         int64_t best_cost = 0, best_rounds = 0;
         for (int i = pair == 2 ? 0 : 2; i < kWidths; ++i) {

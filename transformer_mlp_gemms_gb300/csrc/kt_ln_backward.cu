@@ -7,6 +7,9 @@
 // shared memory for teams of 16 warps, whose threads have too few).  At the end a block adds
 // its teams' sums in team order and writes one row of partial sums; a second kernel adds the
 // rows of all blocks in order.  No atomics: the same bits from run to run.
+// The sums take most of the registers, so an SM holds 8 warps; long batches therefore copy the
+// next rows into shared memory asynchronously while a row is at work (48 -> 45 us for 32768 x
+// 1280, 5.6 TB/s; without the paired arithmetic 58).  729 x 1152 takes 5.8 us: two dependent kernels.
 #include "kt_ops_internal.h"
 #include "kt_rows.cuh"
 

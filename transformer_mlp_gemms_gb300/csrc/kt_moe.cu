@@ -23,7 +23,10 @@
 // the up into the down projections, so the memory is busy while the blocks wait for one another's
 // H.  A first form with mma.sync, whose warps took weights from global memory straight to
 // registers four steps ahead, spent its time on the tokens' operand and on strip ends: it read
-// 1.5 to 1.75 TB/s at every size (52 us for 1 of 8 x 1280 x 5120, 800 us for 64 tokens of 32).
+// 1.5 to 1.75 TB/s at every size.  Measured, in us, that form and this one: 1 token, 2 of 8 x 1280 x
+// 5120 52 and 32; 9 tokens, 2 of 16 x 1152 x 4304 124 and 52; 64 tokens, 4 of 32 x 1280 x 5120 800
+// and 218 (5.8 TB/s).  What remains beside the weights is about 20 us: logits, choices, two
+// grid-wide waits, and the first pass through each phase's instructions.
 #include "kt_ops_internal.h"
 #include "kt_rows.cuh"
 

@@ -11,7 +11,8 @@
 // inverse of the scale is off by less than 127 * 2^-22 = 3.1e-5, so only a product within
 // 1e-4 of a half-integer can go to the wrong side, and the exact remainder of those few tells.
 // (A 64-bit division there instead took 66 us for 16384 x 1152: bf16 values have many ties with
-// their row's maximum, and this GPU has next to no 64-bit rate.)
+// their row's maximum, and this GPU has next to no 64-bit rate.)  16384 x 1152 takes 14.3 us, 4.0
+// TB/s, with 60% of the issue slots in use; 729 x 1152 2.9 us.
 #include "kt_ops_internal.h"
 #include "kt_rows.cuh"
 
