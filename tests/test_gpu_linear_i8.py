@@ -214,3 +214,26 @@ def test_long_rows_of_few_tiles(M, N, K, dtype, bias):
         again = torch.empty_like(whole)[:, :N]
         kt_ops.kt_linear_i8(q, sx, w, sw, b, again)
         assert torch.equal(again, y)
+
+
+def test_long_rows_captured_and_on_another_stream():
+    g = torch.Generator().manual_seed(5)
+    M, N, K = 40, 640, 4096
+    q = torch.randint(-127, 128, (M, K), generator=g, dtype=torch.int32).to(torch.int8).cuda()
+    w = torch.randint(-127, 128, (N, K), generator=g, dtype=torch.int32).to(torch.int8).cuda()
+    sx, sw = (torch.rand(M, generator=g) * 1e-3).cuda(), (torch.rand(N, generator=g) * 1e-2).cuda()
+    y = torch.full((M, N), float("nan"), dtype=torch.float16, device="cuda")
+    z = torch.full_like(y, float("nan"))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            kt_ops.kt_linear_i8(q, sx, w, sw, None, y)
+    graph.replay()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        kt_ops.kt_linear_i8(q, sx, w, sw, None, z)
+    torch.cuda.synchronize()
+    yx, tol = ref.linear_i8(q, sx, w, sw, None)
+    assert ((y.double() - yx).abs() <= tol + ref.half(torch.float16) * yx.abs() + ref.floor(torch.float16)).all()
+    assert torch.equal(y, z)
