@@ -11,7 +11,7 @@
 //   routing   every block finds all tokens' experts for itself (the same order everywhere) and
 //             lists the (token, expert) pairs by expert;
 //   up        its share of the up projections: H[pair][f], pairs in the list's order;
-//   down      its share of the down projections: Z[split][pair][d], once every block's H is there;
+//   down      its share of the down projections: Z[split][pair][d], each expert's once its H is there;
 //   y         grid barrier; its share of y: the weighted sum over a token's pairs.
 //
 // The projections are tcgen05 products with the weights as the 128-row operand (GEGLU: 64 value
@@ -21,12 +21,14 @@
 // come by TMA, 16 KB per stage of a ring that takes the rest of shared memory (100 to 180 KB in
 // flight per SM), issued by a thread that waits for nothing but free stages: it runs on from
 // the up into the down projections, so the memory is busy while the blocks wait for one another's
-// H.  A first form with mma.sync, whose warps took weights from global memory straight to
+// H, and a down projection waits for its own expert's alone (with one wait for all of H, 32 tokens, 2
+// of 8 x 1280 x 5120, took 74 us, here 66; 64 tokens, 8 of 16 x 2560 x 2560, 121 and 107).  A
+// first form with mma.sync, whose warps took weights from global memory straight to
 // registers four steps ahead, spent its time on the tokens' operand and on strip ends: it read
 // 1.5 to 1.75 TB/s at every size.  Measured, in us, that form and this one: 1 token, 2 of 8 x 1280 x
 // 5120 52 and 32; 9 tokens, 2 of 16 x 1152 x 4304 124 and 52; 64 tokens, 4 of 32 x 1280 x 5120 800
-// and 218 (5.8 TB/s).  What remains beside the weights is about 20 us: logits, choices, two
-// grid-wide waits, and the first pass through each phase's instructions.
+// and 217 (5.8 TB/s).  What remains beside the weights is about 20 us: logits, choices,
+// the waits for H and for all sums, and the first pass through each phase's instructions.
 #include "kt_ops_internal.h"
 #include "kt_rows.cuh"
 
@@ -368,6 +370,7 @@ struct MoeBars {
     uint64_t full[kMoeMaxStages], empty[kMoeMaxStages], acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     int abort, ok, failed;
+    int stored[kMoeEpiWarps];  // up items whose part of H each epilogue warp has stored
 };
 
 // Pairs per group of the down products' columns, for T tokens.
@@ -386,6 +389,15 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm,
         " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
+}
+
+__device__ __forceinline__ void st_release_cta(uint32_t addr, int v) {
+    asm volatile("st.release.cta.shared.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ int ld_acquire_cta(uint32_t addr) {
+    int v;
+    asm volatile("ld.acquire.cta.shared.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
@@ -413,6 +425,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     if (warp == kMoeWarps - 2 && lane == 0) {
         bars.ok = 1;
         bars.abort = 0;
+        for (int q = 0; q < kMoeEpiWarps; ++q) bars.stored[q] = 0;
         for (int s = 0; s < stages; ++s) {
             mbar_init(bar(bars.full[s]), 2);
             mbar_init(bar(bars.empty[s]), 1);
@@ -453,18 +466,23 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         const uint32_t every = weights ? kMoeWeightThreads : 1, mine = warp == 3 ? 1 : 0;
         uint32_t stage = 0, phase = 0, armed = 0, armed_phase = 0, count = 0;
         bool ok = true;
+        int ready = -1;  // the last active expert whose H is known to be there
         for (int ph = 0; ph < 2 && ok; ++ph) {
             const bool up = ph == 0;
-            if (!up && !weights) {
-                ok = wait_blocks(p.barriers + 1, gridDim.x, p);
-                if (!ok) *abort_flag = 1;
-                asm volatile("fence.proxy.async;" ::: "memory");  // H was stored by other threads; TMA reads it
-            }
             const int n_items = up ? m.up_items : m.down_items;
             for (int i = up ? (int)blockIdx.x : m.first_down; i < n_items && ok; i += grid) {
                 const MoeItem it = moe_item(p, route, m, up, i);
                 const int e = route.active[it.a], start = route.start[it.a], n = route.start[it.a + 1] - start;
                 const int groups = (n + group - 1) / group;
+                if (!up && !weights && it.a != ready) {
+                    ready = it.a;
+                    ok = wait_blocks(p.ready + it.a, (unsigned)m.up_tiles, p);
+                    if (!ok) {
+                        *abort_flag = 1;
+                        break;
+                    }
+                    asm volatile("fence.proxy.async;" ::: "memory");  // H was stored by other threads; TMA reads it
+                }
                 for (int kb = it.kb0; kb < it.kb1; ++kb, ++count) {
                     if (count % every == mine) {
                         ok = wait_phase(bar(bars.empty[stage]), phase ^ 1u, abort_flag, p.error, DEV_TIMEOUT_PRODUCER, p.wait_limit_ns);
@@ -611,18 +629,37 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                 tc_fence_before();
                 if (up && m.gated) epi_bar_sync<kMoeEpiWarps>();  // the gates have been read
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(bars.acc_empty[buf]));
-            }
-            if (up && live) {
-                // this block's part of H is stored: for the TMA reads of other blocks too
-                __threadfence();
-                asm volatile("fence.proxy.async;" ::: "memory");
-                epi_bar_sync<kMoeEpiWarps>();
-                if (warp == 4 && lane == 0) {
-                    __threadfence();
-                    atomicAdd(p.barriers + 1, 1u);
+                if (lane == 0) {
+                    mbar_arrive(bar(bars.acc_empty[buf]));
+                    if (up) st_release_cta(smem_u32(&bars.stored[q]), (int)t + 1);
                 }
             }
+        }
+    } else if (warp == 4 + kMoeEpiWarps) {
+        // ------------------ tells all blocks of this one's stored tiles of H ------------------
+        // by a warp of its own: the fence waits for the stores, 1 to 2 us while the weights come, and
+        // in the epilogue's warps that held up short items (20 tokens, 2 of 16 x 640 x 2560: 46 us, here 41)
+        const int mine = m.up_items > (int)blockIdx.x ? (m.up_items - 1 - (int)blockIdx.x) / grid + 1 : 0;
+        unsigned long long t0 = global_ns();
+        for (int done = 0; done < mine;) {
+            const int v = lane < kMoeEpiWarps ? ld_acquire_cta(smem_u32(&bars.stored[lane])) : mine;
+            const int upto = __reduce_min_sync(0xffffffffu, v);
+            if (upto > done) {
+                __threadfence();
+                asm volatile("fence.proxy.async;" ::: "memory");
+                if (lane == 0)
+                    for (int j = done; j < upto; ++j) atomicAdd(p.ready + ((int)blockIdx.x + j * grid) / m.up_tiles, 1u);
+                done = upto;
+                t0 = global_ns();
+            } else {
+                __nanosleep(40);
+            }
+            const bool late = global_ns() - t0 > 2 * p.wait_limit_ns;
+            if (late) {
+                atomicCAS(p.error, 0, DEV_TIMEOUT_EPILOGUE);
+                *abort_flag = 1;
+            }
+            if (__any_sync(0xffffffffu, late || *abort_flag != 0)) break;
         }
     }
     tc_fence_before();
@@ -633,7 +670,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         tmem_dealloc<1>(tmem, 2 * kMoeAccCols);
     }
     if (*abort_flag) return;
-    if (!grid_barrier(p.barriers + 2, p, &bars.ok)) return;
+    if (!grid_barrier(p.barriers + 1, p, &bars.ok)) return;
+    // no block waits for an expert's H any more
+    if (blockIdx.x == 0 && (int)threadIdx.x < route.n_active) p.ready[threadIdx.x] = 0u;
 
     // y: 8 lanes per 4 columns of a token, each adding up every eighth (choice, split), so that
     // the loads are in flight together; warps dealt out to the blocks in turn
@@ -677,9 +716,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     }
     // the last block to get here leaves the counters at zero: every block is past every barrier
     __syncthreads();
-    if (threadIdx.x == 0 && atomicAdd(p.barriers + 3, 1u) == gridDim.x - 1) {
+    if (threadIdx.x == 0 && atomicAdd(p.barriers + 2, 1u) == gridDim.x - 1) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p.barriers[i] = 0u;
+        for (int i = 0; i < 3; ++i) p.barriers[i] = 0u;
     }
 }
 
@@ -734,10 +773,10 @@ kt_status launch_moe_t(int act, const MoeParams& p, int sms, int device, void* s
 
 }  // namespace
 
-// Workspace: [barrier counters, error word: 256 bytes][choices][H][Z].
+// Workspace: [barrier counters, error word: 256 bytes][a counter per active expert][choices][H][Z].
 size_t moe_workspace(int64_t T, int64_t D, int64_t F, int64_t top_k) {
     const size_t pairs = (size_t)(T * top_k);
-    return 256 + round256(pairs * sizeof(float2)) + round256(2 * pairs * (size_t)F * 2) +
+    return kMoeControlBytes + round256(pairs * sizeof(float2)) + round256(2 * pairs * (size_t)F * 2) +
            round256(moe_z_rows((int)pairs) * (size_t)D * sizeof(float));
 }
 
@@ -745,7 +784,8 @@ void moe_carve(MoeParams* p, int64_t max_tokens, void* workspace) {
     unsigned char* w = static_cast<unsigned char*>(workspace);
     p->barriers = reinterpret_cast<unsigned*>(w);
     p->error = reinterpret_cast<int*>(w + 128);
-    w += 256;
+    p->ready = reinterpret_cast<unsigned*>(w + 256);
+    w += kMoeControlBytes;
     p->choices = reinterpret_cast<float2*>(w);
     w += round256((size_t)(max_tokens * p->top_k) * sizeof(float2));
     p->H = reinterpret_cast<uint16_t*>(w);

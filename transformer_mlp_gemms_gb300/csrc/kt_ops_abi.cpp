@@ -186,7 +186,7 @@ kt_status kt_moe_plan(const kt_moe_options* o, kt_moe_plan_t* out) {
     const size_t bytes = kt::moe_workspace(o->max_tokens, o->D, o->F, o->top_k);
     cudaError_t e = cudaMalloc(&plan->workspace, bytes);
     // the counters and the error word start at zero, on the device before this returns
-    if (e == cudaSuccess) e = cudaMemset(plan->workspace, 0, 256);
+    if (e == cudaSuccess) e = cudaMemset(plan->workspace, 0, kt::kMoeControlBytes);
     if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
     if (e != cudaSuccess) {
         cudaFree(plan->workspace);
@@ -254,7 +254,7 @@ kt_status kt_moe_status(kt_moe_plan_t plan) {
     e = cudaMemcpy(&word, plan->p.error, sizeof(word), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_failed("cudaMemcpy", e);
     if (word == 0) return done(KT_OK, "");
-    e = cudaMemset(plan->workspace, 0, 256);
+    e = cudaMemset(plan->workspace, 0, kt::kMoeControlBytes);
     if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
     if (e != cudaSuccess) return cuda_failed("clearing the plan's counters", e);
     return kt::report(KT_ERR_TIMEOUT, "a device-side wait ran out");

@@ -73,6 +73,7 @@ struct MoeParams {
     uint16_t* H;         // [2][T * top_k][F]: the hidden layer's rounding, then the remainder's
     float* Z;            // [splits][T * top_k][D]: each pair's output before its weight
     unsigned* barriers;  // grid barrier counters, zero between runs
+    unsigned* ready;     // of each active expert: tiles of its H that are stored; zero between runs
     int* error;          // device error word
     unsigned long long wait_limit_ns;
 };
@@ -81,6 +82,7 @@ KT_HOST_DEVICE inline int moe_splits(int pairs) { return pairs >= 1024 ? 1 : pai
 inline size_t moe_z_rows(int max_pairs) {  // for any number of pairs up to max_pairs
     return max_pairs >= 1024 ? max_pairs : max_pairs * 32 < 1024 ? max_pairs * 32 : 1024;
 }
+constexpr size_t kMoeControlBytes = 256 + KT_MOE_MAX_EXPERTS * sizeof(unsigned);  // counters and error word, zero at first
 size_t moe_workspace(int64_t T, int64_t D, int64_t F, int64_t top_k);
 void moe_carve(MoeParams* p, int64_t max_tokens, void* workspace);
 kt_status launch_moe(int act, int dtype, const MoeParams& p, int sms, int device, void* stream, const char** why);
