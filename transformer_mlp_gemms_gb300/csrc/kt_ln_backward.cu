@@ -19,9 +19,10 @@ namespace {
 __device__ __forceinline__ float of_pair(const f32x2& v, int e) { return e & 1 ? v.y : v.x; }
 
 // Resident blocks per SM, and whether a row's xhat and g stay in registers between the averages
-// and dx (else they are computed twice): what the registers allow beside the sums of dgamma and dbeta.
+// and dx (else they are computed twice): what the registers allow beside the sums of dgamma and dbeta
+// (and, without 16-byte loads, the next row's elements one by one).
 constexpr int ln_back_per_sm(int W, int V) { return W == 16 ? 1 : V <= 1 ? 3 : V == 2 ? 2 : 1; }
-constexpr bool ln_back_keeps(int W, int V) { return W < 16 && V >= 3; }
+constexpr bool ln_back_keeps(int W, int V, bool VEC) { return VEC && W < 16 && V >= 3; }
 constexpr int kLnBackStagedWarps = 2;  // gamma in shared memory up to so many warps per row
 
 template <int DT, int W, int V, bool VEC, bool RING>
@@ -31,7 +32,7 @@ __global__ void __launch_bounds__(row_block(W), ln_back_per_sm(W, V)) kt_ln_back
     constexpr int TL = 32 * W, teams = row_block(W) / TL;
     constexpr bool kSmemSums = W == 16;
     constexpr bool kAhead = !RING && W != 16;  // the next row's loads in flight during this row's sums
-    constexpr bool kKeep = ln_back_keeps(W, V), kStaged = W <= kLnBackStagedWarps;
+    constexpr bool kKeep = ln_back_keeps(W, V, VEC), kStaged = W <= kLnBackStagedWarps;
     __shared__ TeamLines<W> lines;
     // gamma, then the ring; the final addition's [teams][TL * V * 8] where they were; or [2][..] (kSmemSums)
     extern __shared__ __align__(16) uint8_t smem[];
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(row_block(W), ln_back_per_sm(W, V)) kt_ln_back
             ring.read(slot, 1, cy);
         }
         const int next = p.M - row > step ? row + step : p.M;
-        uint4 nx[V], ny[V];
+        SlotAhead<VEC> nx[V], ny[V];
         if (next < p.M) {
             next_mean = p.mean[next];
             next_rstd = p.rstd[next];
@@ -103,8 +104,8 @@ __global__ void __launch_bounds__(row_block(W), ln_back_per_sm(W, V)) kt_ln_back
         if (kAhead && next < p.M) {
 #pragma unroll
             for (int s = 0; s < V; ++s) {
-                nx[s] = load_slot<VEC>(X + (int64_t)next * p.ldx, s, l, TL, D);
-                ny[s] = load_slot<VEC>(dY + (int64_t)next * p.lddy, s, l, TL, D);
+                nx[s].load(X + (int64_t)next * p.ldx, s, l, TL, D);
+                ny[s].load(dY + (int64_t)next * p.lddy, s, l, TL, D);
             }
         }
         const f32x2 mu = f2(mean), scale = f2(rstd);
@@ -189,8 +190,8 @@ __global__ void __launch_bounds__(row_block(W), ln_back_per_sm(W, V)) kt_ln_back
         if (kAhead) {
 #pragma unroll
             for (int s = 0; s < V; ++s) {
-                cx[s] = nx[s];
-                cy[s] = ny[s];
+                cx[s] = nx[s].slot();
+                cy[s] = ny[s].slot();
             }
         } else if (!RING && row < p.M) {
 #pragma unroll

@@ -65,11 +65,11 @@ __global__ void __launch_bounds__(row_block(W), ln_per_sm(W, V)) kt_ln_forward_k
         unpack8<DT>(make_uint4(first, 0u, 0u, 0u), f0);
         const float x0 = f0[0];
         const int next = p.M - row > step ? row + step : p.M;
-        uint4 n[V];
+        SlotAhead<VEC> n[V];
         if (next < p.M) {
             next_first = X[(int64_t)next * p.ldx];
 #pragma unroll
-            for (int s = 0; s < V; ++s) n[s] = load_slot<VEC>(X + (int64_t)next * p.ldx, s, l, TL, D);
+            for (int s = 0; s < V; ++s) n[s].load(X + (int64_t)next * p.ldx, s, l, TL, D);
         }
         const f32x2 origin = f2(x0);
         f32x2 d[4 * V], acc = f2(0.0f);  // the row's deviations
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(row_block(W), ln_per_sm(W, V)) kt_ln_forward_k
         row = next;
         first = next_first;
 #pragma unroll
-        for (int s = 0; s < V; ++s) c[s] = n[s];
+        for (int s = 0; s < V; ++s) c[s] = n[s].slot();
     }
 }
 

@@ -100,10 +100,10 @@ __global__ void __launch_bounds__(row_block(W), quant_per_sm(W, ACT)) kt_quantiz
     for (int s = 0; s < V; ++s) c[s] = load_slot<VEC>(X + (int64_t)row * p.ldx, s, l, TL, K);
     for (;;) {
         const int next = p.M - row > step ? row + step : p.M;
-        uint4 n[V];  // the next row, on its way behind this one's reduction
+        SlotAhead<VEC> n[V];  // the next row, on its way behind this one's reduction
         if (next < p.M) {
 #pragma unroll
-            for (int s = 0; s < V; ++s) n[s] = load_slot<VEC>(X + (int64_t)next * p.ldx, s, l, TL, K);
+            for (int s = 0; s < V; ++s) n[s].load(X + (int64_t)next * p.ldx, s, l, TL, K);
         }
         f32x2 a[ACT ? 4 * V : 4];  // ACT: the row's activated values
         uint32_t most = 0;
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(row_block(W), quant_per_sm(W, ACT)) kt_quantiz
         if (next >= p.M) break;
         row = next;
 #pragma unroll
-        for (int s = 0; s < V; ++s) c[s] = n[s];
+        for (int s = 0; s < V; ++s) c[s] = n[s].slot();
     }
 }
 
