@@ -27,8 +27,8 @@
 // registers four steps ahead, spent its time on the tokens' operand and on strip ends: it read
 // 1.5 to 1.75 TB/s at every size.  Measured, in us, that form and this one: 1 token, 2 of 8 x 1280 x
 // 5120 52 and 32; 9 tokens, 2 of 16 x 1152 x 4304 124 and 52; 64 tokens, 4 of 32 x 1280 x 5120 800
-// and 217 (5.8 TB/s).  What remains beside the weights is about 20 us: logits, choices,
-// the waits for H and for all sums, and the first pass through each phase's instructions.
+// and 217 (5.8 TB/s).  What remains beside the weights is about 20 us: logits, choices and lists
+// (4 to 7), the first weights' latency, the waits for H and for all sums.
 #include "kt_ops_internal.h"
 #include "kt_rows.cuh"
 
