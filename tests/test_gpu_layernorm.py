@@ -225,3 +225,8 @@ def test_refusals_with_tensors():
         with pytest.raises(kt_mlp.KtError) as e:
             call()
         assert e.value.status == kt_mlp.KT_ERR_INVALID
+
+
+@pytest.mark.parametrize("M,D,pad", [(1000, 2051, 0), (1300, 1281, 2), (700, 4099, 3), (500, 8191, 0), (400, 8200, 1), (5000, 257, 0), (4000, 770, 5)])
+def test_several_rows_per_team_at_any_pitch(M, D, pad):
+    test_forward_and_backward(M, D, pad, "f16")

@@ -19,7 +19,7 @@ namespace {
 constexpr int kLnStagedWarps = 2;
 
 // Resident blocks per SM: as many rows in flight as the registers allow.
-constexpr int ln_per_sm(int W, int V) { return W == 16 ? 1 : V <= 1 ? 5 : V == 2 ? 4 : V == 3 && W <= kLnStagedWarps ? 3 : 2; }
+constexpr int ln_per_sm(int W, int V) { return W == 16 ? (V <= 2 ? 2 : 1) : V <= 1 ? 5 : V == 2 ? 4 : V == 3 && W <= kLnStagedWarps ? 3 : 2; }
 
 template <int DT, int W, int V, bool VEC>
 __global__ void __launch_bounds__(row_block(W), ln_per_sm(W, V)) kt_ln_forward_kernel(const LnForward p) {
@@ -141,15 +141,15 @@ __global__ void __launch_bounds__(row_block(W), ln_per_sm(W, V)) kt_ln_forward_k
 }  // namespace
 
 kt_status launch_ln_forward(int dtype, const LnForward& p, int sms, void* stream, const char** why) {
+    const auto al = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; };
+    const bool vec = p.D % 8 == 0 && p.ldx % 8 == 0 && p.ldy % 8 == 0 && al(p.X) && al(p.Y) && al(p.gamma) && al(p.beta);
     RowShape shape;
-    if (!row_shape(p.D, &shape)) {
+    if (!(vec ? row_shape(p.D, &shape) : scalar_row_shape(p.D, &shape))) {
         *why = "rows of this length are not supported";
         return KT_ERR_UNSUPPORTED;
     }
-    const auto al = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; };
-    const bool vec = p.D % 8 == 0 && p.ldx % 8 == 0 && p.ldy % 8 == 0 && al(p.X) && al(p.Y) && al(p.gamma) && al(p.beta);
     auto go = [&](auto dt, auto v16) {
-        return with_shape<decltype(v16)::value>(shape, [&](auto W, auto V) -> kt_status {
+        return with_shape<decltype(v16)::value, !decltype(v16)::value>(shape, [&](auto W, auto V) -> kt_status {
             constexpr int w = decltype(W)::value, t = decltype(dt)::value, v = decltype(V)::value;
             constexpr bool al16 = decltype(v16)::value;
             constexpr int teams = row_block(w) / (32 * w), per_sm = ln_per_sm(w, v);

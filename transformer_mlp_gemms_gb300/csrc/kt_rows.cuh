@@ -256,9 +256,21 @@ __device__ __forceinline__ void staged_pairs(const float4* from, int s, int l, f
 }
 constexpr int staged_bytes(int W, int V) { return V * 32 * W * 8 * 4; }
 
+// The same without 16-byte loads, for kernels whose lanes hold little else: from 2049
+// columns on two slots per lane of more warps, as far as there are any, since the next row's elements
+// take a register each (layer norm of 4000 x 4001: 25 us with four slots of 4 warps, here 20; below,
+// the barriers cost more: 32768 x 1281 54 us with 2 warps, 78 with 4).
+inline bool scalar_row_shape(int64_t D, RowShape* out) {
+    if (!row_shape(D, out)) return false;
+    if (out->W <= 2 || D > 32 * 16 * 2 * 8) return true;
+    out->V = 2;
+    for (out->W = 8; out->W < 16 && D > 32ll * out->W * 2 * 8;) out->W *= 2;
+    return true;
+}
+
 // Calls f(integral constants W, V) for the team shape; 13 shapes with 16-byte loads, 8 (the
-// shapes' slot counts rounded up) without.
-template <bool VEC, typename F>
+// shapes' slot counts rounded up; PAIRS: scalar_row_shape's) without.
+template <bool VEC, bool PAIRS = false, typename F>
 kt_status with_shape(const RowShape& s, F&& f) {
 #define KT_SHAPE(w, v) \
     if (s.W == w && s.V <= v) return f(std::integral_constant<int, w>{}, std::integral_constant<int, v>{})
@@ -278,8 +290,13 @@ kt_status with_shape(const RowShape& s, F&& f) {
         KT_SHAPE(16, 3);
     }
     KT_SHAPE(2, 4);
-    KT_SHAPE(4, 4);
-    KT_SHAPE(8, 4);
+    if constexpr (PAIRS) {  // scalar_row_shape's
+        KT_SHAPE(8, 2);
+        KT_SHAPE(16, 2);
+    } else {
+        KT_SHAPE(4, 4);
+        KT_SHAPE(8, 4);
+    }
     KT_SHAPE(16, 4);
 #undef KT_SHAPE
     return KT_ERR_UNSUPPORTED;
