@@ -237,3 +237,50 @@ def test_long_rows_captured_and_on_another_stream():
     yx, tol = ref.linear_i8(q, sx, w, sw, None)
     assert ((y.double() - yx).abs() <= tol + ref.half(torch.float16) * yx.abs() + ref.floor(torch.float16)).all()
     assert torch.equal(y, z)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("M,N,K", [(4, 1280, 640), (16, 520, 1296), (64, 640, 4096), (300, 520, 272), (729, 4304, 640)])
+def test_new_values_in_the_same_buffers_are_read(M, N, K, captured):
+    """Tokens and weights quantised into the same buffers again and again, each product right behind
+    its operands' writes: every step's result is that of the step alone, bit for bit."""
+    g = torch.Generator().manual_seed(M + K)
+    steps = 12
+    x = (torch.randn(steps, M, K, generator=g) * torch.exp(torch.randn(steps, M, 1, generator=g))).to(torch.bfloat16).cuda()
+    wf = (torch.randn(steps, N, K, generator=g) / K ** 0.5).to(torch.bfloat16).cuda()
+
+    def buffers():
+        return (torch.zeros(M, K, dtype=torch.int8, device="cuda"), torch.zeros(M, device="cuda"),
+                torch.zeros(N, K, dtype=torch.int8, device="cuda"), torch.zeros(N, device="cuda"))
+
+    def step(i, b, y):
+        kt_ops.kt_quantize_rows(wf[i], b[2], b[3])
+        kt_ops.kt_quantize_rows(x[i], b[0], b[1])
+        kt_ops.kt_linear_i8(*b, None, y)
+
+    alone = torch.full((steps, M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    for i in range(steps):
+        b = buffers()
+        step(i, b, alone[i])
+        torch.cuda.synchronize()
+        qx, sx = ref.quantize(x[i])
+        assert torch.equal(b[0], qx) and torch.equal(b[1], sx)
+        yx, tol = ref.linear_i8(*b, None)
+        assert ((alone[i].double() - yx).abs() <= tol + ref.half(torch.bfloat16) * yx.abs()).all()
+    b = buffers()
+    got = torch.full_like(alone, float("nan"))
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for i in range(steps):
+                step(i, b, got[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        got.fill_(float("nan"))
+        graph.replay()
+    else:
+        for i in range(steps):
+            step(i, b, got[i])
+    torch.cuda.synchronize()
+    for i in range(steps):
+        assert torch.equal(got[i], alone[i]), i

@@ -56,8 +56,8 @@ __global__ void __launch_bounds__(kDotWarps * 32) kt_linear_i8_dot_kernel(const 
         for (int u = 0; u < kDotAhead; ++u) {
             x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
             if (k + 128 * u + k8 * 16 < p.K) {
-                x[u] = __ldg(reinterpret_cast<const uint4*>(w0 + k + 128 * u + k8 * 16));
-                y[u] = __ldg(reinterpret_cast<const uint4*>(w1 + k + 128 * u + k8 * 16));
+                x[u] = *reinterpret_cast<const uint4*>(w0 + k + 128 * u + k8 * 16);
+                y[u] = *reinterpret_cast<const uint4*>(w1 + k + 128 * u + k8 * 16);
             }
         }
     };
@@ -200,17 +200,20 @@ __device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&r
 }
 
 // 32 bytes at p: one load where every row starts on a 32-byte boundary, else two.  Bytes at or
-// past `left` are zeros (left is a multiple of 16).
+// past `left` are zeros (left is a multiple of 16).  Ordinary loads, here and for the few tokens, not
+// the read-only path's: this kernel is resident while the one before it may still write Q (or W),
+// so they are not read-only for its lifetime, which that path requires; griddepcontrol.wait orders
+// ordinary loads.
 __device__ __forceinline__ void load32(const int8_t* p, int left, bool wide, uint4& a, uint4& b) {
     a = b = make_uint4(0u, 0u, 0u, 0u);
     if (wide) {
         if (left > 0)
-            asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+            asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                          : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
                          : "l"(p));
     } else {
-        if (left > 0) a = __ldg(reinterpret_cast<const uint4*>(p));
-        if (left > 16) b = __ldg(reinterpret_cast<const uint4*>(p + 16));
+        if (left > 0) a = *reinterpret_cast<const uint4*>(p);
+        if (left > 16) b = *reinterpret_cast<const uint4*>(p + 16);
     }
 }
 
