@@ -230,3 +230,31 @@ def test_refusals_with_tensors():
 @pytest.mark.parametrize("M,D,pad", [(1000, 2051, 0), (1300, 1281, 2), (700, 4099, 3), (500, 8191, 0), (400, 8200, 1), (5000, 257, 0), (4000, 770, 5)])
 def test_several_rows_per_team_at_any_pitch(M, D, pad):
     test_forward_and_backward(M, D, pad, "f16")
+
+
+@pytest.mark.parametrize("M,D", [(729, 1152), (100, 643), (3800, 1280)])
+def test_new_values_in_the_same_workspace_are_read(M, D):
+    """Backward passes of changing inputs right behind one another through one workspace: each step's
+    sums are those of the step alone, bit for bit."""
+    steps = 10
+    gamma, _ = affine(D, torch.float16, 20)
+    inputs = []
+    for i in range(steps):
+        x, dy = rows(M, D, 0, torch.float16, 21 + i), rows(M, D, 0, torch.float16, 51 + i, 0.3)
+        _, mean, rstd = ref.layernorm(x, None, None, EPS)
+        inputs.append((dy, x, gamma, mean.float(), rstd.float()))
+    ws = kt_ops.layernorm_backward_workspace(M, D)
+
+    def step(i):
+        out = torch.full((M, D), float("nan"), dtype=torch.float16, device="cuda"), *(torch.full((2, D), float("nan"), device="cuda"))
+        kt_ops.kt_layernorm_backward(*inputs[i], *out, ws)
+        return out
+
+    alone = []
+    for i in range(steps):
+        alone.append(step(i))
+        torch.cuda.synchronize()
+    again = [step(i) for i in range(steps)]
+    torch.cuda.synchronize()
+    for a, b in zip(alone, again):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))

@@ -242,10 +242,11 @@ __global__ void __launch_bounds__(row_block(W), ln_back_per_sm(W, V)) kt_ln_back
 
 // Adds the blocks' rows of partial sums, in order: out[c] = sum_r partials[r][c] over the 2 D
 // columns (dgamma, then dbeta).  32 columns and 16 runs of rows per block (729 x 1152: 5.8 us for
-// the whole backward pass; 8 runs 6.3).
+// the whole backward pass; 8 runs 6.3).  `partials` is still being written when this kernel starts, so
+// it carries no promise that would let its loads pass griddepcontrol.wait.
 constexpr int kSumRuns = 16;
-__global__ void __launch_bounds__(kSumRuns * 32) kt_ln_column_sums_kernel(const float* __restrict__ partials, int rows, int D,
-                                                                          float* __restrict__ dgamma, float* __restrict__ dbeta) {
+__global__ void __launch_bounds__(kSumRuns * 32) kt_ln_column_sums_kernel(const float* partials, int rows, int D, float* dgamma,
+                                                                          float* dbeta) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ float part[kSumRuns][32];
