@@ -198,3 +198,22 @@ def test_refusals_of_a_run():
         assert e.value.status == kt_mlp.KT_ERR_INVALID
     torch.cuda.synchronize()
     assert plan.status() == kt_mlp.KT_OK
+
+
+@pytest.mark.parametrize("T,D,F,E,k,act,dtype", [(1, 640, 1280, 8, 2, "geglu", "bf16"), (20, 640, 2560, 16, 2, "geglu", "f16"),
+                                                 (64, 256, 520, 12, 4, "gelu_tanh", "bf16")])
+def test_new_tokens_through_the_same_workspace(T, D, F, E, k, act, dtype):
+    """Runs of changing tokens right behind one another: no block reads a hidden layer or a sum of the
+    run before, so every result is that of the run alone, bit for bit."""
+    steps = 16
+    t = problem(T, D, F, E, k, act, dtype, False, 9)
+    xs = [problem(T, D, F, E, k, act, dtype, False, 30 + i)["X"] * (1.0 + i) for i in range(steps)]
+    plan = plan_of(T, D, F, E, k, act, dtype, False, True)
+    alone = [run(plan, {**t, "X": x})[0] for x in xs]
+    check(run(plan, {**t, "X": xs[3]}), reference({**t, "X": xs[3]}, None, k, act, True))
+    for _ in range(3):
+        again = [torch.full_like(x, float("nan")) for x in xs]
+        for x, y in zip(xs, again):
+            plan.run(x, t["W_router"], t["W_up"], t["W_down"], y)
+        assert plan.status() == kt_mlp.KT_OK
+        assert all(torch.equal(a, b) for a, b in zip(alone, again))

@@ -645,6 +645,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             const int v = lane < kMoeEpiWarps ? ld_acquire_cta(smem_u32(&bars.stored[lane])) : mine;
             const int upto = __reduce_min_sync(0xffffffffu, v);
             if (upto > done) {
+                __syncwarp();  // lanes 0 to 3 have each seen one warp's stores: all of them before lane 0 tells
                 __threadfence();
                 asm volatile("fence.proxy.async;" ::: "memory");
                 if (lane == 0)
