@@ -49,6 +49,24 @@ def layernorm_bounds(x, gamma, beta, y, rstd, dtype):
     return y_tol, mean_tol, rstd * r
 
 
+def layernorm_bounds_about_the_mean(x, gamma, beta, y, mean, rstd, dtype):
+    """As layernorm_bounds, for rows whose first element may be anything.  The kernel's deviations
+    are those from an origin o, the number of the row's type nearest to a first mean that is off by
+    CHAIN roundings of avg|x|; the mean is o plus the deviations' average, which is off by CHAIN
+    roundings of B = avg|x - o|, the variance their squares' average less that average's square,
+    and so no worse than CHAIN roundings of 1 + (the average over the spread)^2.  (The bounds of
+    layernorm_bounds hold too: o is at most as far from the mean as the first element is.)"""
+    x = x.double()
+    apart = half(dtype) * mean.abs() + floor(dtype) + CHAIN * U * x.abs().mean(1)  # |mean - o|
+    off = CHAIN * U * ((x - mean[:, None]).abs().mean(1) + apart)
+    r = CHAIN * U * (1.0 + (apart * rstd) ** 2) + (off * rstd) ** 2
+    g = gamma.double().abs() if gamma is not None else torch.ones_like(x[0])
+    b = beta.double().abs() if beta is not None else torch.zeros_like(x[0])
+    xhat = (x - mean[:, None]).abs() * rstd[:, None]
+    y_tol = half(dtype) * y.abs() + floor(dtype) + g * ((off * rstd)[:, None] + xhat * (r[:, None] + 4 * U)) * 1.01 + 4 * U * b
+    return y_tol, off + 2 * U * mean.abs(), rstd * r
+
+
 def layernorm_backward(dy, x, gamma, mean, rstd):
     """(dx, dgamma, dbeta) in 64 bits."""
     dy, x, r = dy.double(), x.double(), rstd.double()[:, None]

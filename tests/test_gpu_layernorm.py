@@ -258,3 +258,33 @@ def test_new_values_in_the_same_workspace_are_read(M, D):
     torch.cuda.synchronize()
     for a, b in zip(alone, again):
         assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("column", [0, 7, -1])
+@pytest.mark.parametrize("dtype,outlier", [("f16", 3e3), ("f16", -3e4), ("bf16", 6e4), ("bf16", 1e6)])
+@pytest.mark.parametrize("D", [40, 643, 1280, 4096, 4099, 16384])
+def test_one_value_far_from_the_others(D, dtype, outlier, column):
+    """One large value in a row, the first one too: the mean and the other elements keep their digits."""
+    dt, M = DT[dtype], 7
+    x = rows(M, D, 0, dt, D, 0.5)
+    x[:, column] = outlier
+    gamma, beta = affine(D, dt, D + 1)
+    y, mean, rstd = torch.empty_like(x), torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    kt_ops.kt_layernorm_forward(x, gamma, beta, EPS, y, mean, rstd)
+    yx, mx, rx = ref.layernorm(x, gamma, beta, EPS)
+    ty, tm, tr = ref.layernorm_bounds_about_the_mean(x, gamma, beta, yx, mx, rx, dt)
+    within(mean, mx, tm, "mean")
+    within(rstd, rx, tr, "rstd")
+    within(y, yx, ty, "y")
+
+
+@pytest.mark.parametrize("value", [1e-30, 1e30, 2e36, 3e38])
+def test_equal_values_of_any_size(value):
+    """Rows without spread whose sum may be beyond fp32: y is beta and the mean the value, exactly."""
+    for D in (72, 643, 1152, 16384):
+        gamma, beta = affine(D, torch.bfloat16, D)
+        x = torch.full((3, D), value, dtype=torch.bfloat16, device="cuda")
+        y, mean, rstd = torch.empty_like(x), torch.empty(3, device="cuda"), torch.empty(3, device="cuda")
+        kt_ops.kt_layernorm_forward(x, gamma, beta, EPS, y, mean, rstd)
+        assert (y == beta).all() and (mean == x[:, 0].float()).all()
+        assert torch.allclose(rstd, torch.full_like(rstd, EPS ** -0.5), rtol=4e-7)

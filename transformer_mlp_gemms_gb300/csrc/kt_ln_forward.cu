@@ -7,7 +7,7 @@
 // variance is a second pass over it; gamma and beta are in shared memory as fp32 (rows up to 2048
 // columns; registers beyond), and the next row's loads are issued before this row's reductions.
 // What else the time goes to is instructions: the deviations are unpacked once and kept as fp32,
-// two at a time (10 instructions per element before, 5 now).  65536 x 640 takes 28.9 us, 5.8 TB/s;
+// two at a time (10 instructions per element before, 5 now).  65536 x 640 takes 29.0 us, 5.8 TB/s;
 // 32768 x 1280 27.6 us, 6.1 TB/s; a few rows 2.3 us, a launch's latency.  A ring of rows ahead in
 // shared memory, as the backward pass has, is slower here: 36 us for the first.
 #include "kt_ops_internal.h"
@@ -45,8 +45,6 @@ __global__ void __launch_bounds__(row_block(W), ln_per_sm(W, V)) kt_ln_forward_k
     int turn = 0;
 
     uint4 c[V], gw[kStaged ? 1 : V], bw[kStaged ? 1 : V];
-    uint16_t first = 0, next_first = 0;
-    if (row < p.M) first = X[(int64_t)row * p.ldx];
 #pragma unroll
     for (int s = 0; s < V; ++s) c[s] = load_slot<VEC>(X + (int64_t)row * p.ldx, s, l, TL, row < p.M ? D : 0);
     if (!kStaged && affine) {
@@ -59,59 +57,65 @@ __global__ void __launch_bounds__(row_block(W), ln_per_sm(W, V)) kt_ln_forward_k
     if (kStaged && affine) __syncthreads();
     if (row >= p.M) return;  // the whole team: the barriers from here on are its own
     for (;;) {
-        // the deviations are taken from the row's first element, exactly: a row far from zero
-        // keeps its low bits in the sums
-        float f0[8];
-        unpack8<DT>(make_uint4(first, 0u, 0u, 0u), f0);
-        const float x0 = f0[0];
         const int next = p.M - row > step ? row + step : p.M;
         SlotAhead<VEC> n[V];
         if (next < p.M) {
-            next_first = X[(int64_t)next * p.ldx];
 #pragma unroll
             for (int s = 0; s < V; ++s) n[s].load(X + (int64_t)next * p.ldx, s, l, TL, D);
         }
-        const f32x2 origin = f2(x0);
-        f32x2 d[4 * V], acc = f2(0.0f);  // the row's deviations
+        // a first mean, of terms x / D: no sum overflows that the mean does not
+        const f32x2 share = f2(inv);
+        f32x2 d[4 * V], acc = f2(0.0f);  // the row, then its deviations
 #pragma unroll
         for (int s = 0; s < V; ++s) {
             f32x2 f[4];
             unpack_pairs<DT>(c[s], f);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                d[4 * s + e] = f2_sub<true>(f[e], origin);
-                clear_past_end<VEC, W, V>(d[4 * s + e], s, e, l, D);
-                acc = f2_add<true>(acc, d[4 * s + e]);
+                d[4 * s + e] = f[e];
+                acc = f2_fma<true>(f[e], share, acc);  // past the row's end: zeros
             }
         }
-        float sum = acc.x + acc.y, none = 0.0f;
-        team_add2<W>(sum, none, lines, turn, team);
-        const float dmean = sum * inv;  // mean - x0
-        const f32x2 shift = f2(dmean);
+        float about = acc.x + acc.y, none = 0.0f;
+        team_add2<W>(about, none, lines, turn, team);
+        // The deviations are those from the 16-bit number nearest to it: a difference of two such
+        // numbers is off by one fp32 rounding of itself, so neither a row far from zero nor a value
+        // far from the others costs the rest its digits, and a row of equal values has none at all.
+        // Their average corrects the mean, and its square the variance; it is below the spread of
+        // any row that is not all equal (the values stand on the same 16-bit grid), so that
+        // the difference keeps its digits.
+        float near[8];
+        unpack8<DT>(make_uint4(pack2<DT>(about, 0.0f) & 0xffffu, 0u, 0u, 0u), near);
+        const f32x2 origin = f2(near[0]);
+        f32x2 squares = f2(0.0f);
         acc = f2(0.0f);
 #pragma unroll
         for (int s = 0; s < V; ++s)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                d[4 * s + e] = f2_sub<true>(d[4 * s + e], shift);
+                d[4 * s + e] = f2_sub<true>(d[4 * s + e], origin);
                 clear_past_end<VEC, W, V>(d[4 * s + e], s, e, l, D);
-                acc = f2_fma<true>(d[4 * s + e], d[4 * s + e], acc);
+                acc = f2_add<true>(acc, d[4 * s + e]);
+                squares = f2_fma<true>(d[4 * s + e], d[4 * s + e], squares);
             }
-        float sq = acc.x + acc.y;
-        none = 0.0f;
-        team_add2<W>(sq, none, lines, turn, team);
-        const float rstd = 1.0f / sqrtf(sq * inv + p.eps);
+        float sum = acc.x + acc.y, sq = squares.x + squares.y;
+        team_add2<W>(sum, sq, lines, turn, team);
+        const float dmean = sum * inv;  // mean - origin
+        float var = sq * inv;
+        if (var < __uint_as_float(0x7f800000u)) var = fmaxf(fmaf(-dmean, dmean, var), 0.0f);
+        const float rstd = 1.0f / sqrtf(var + p.eps);
         if (l == 0) {
-            if (p.mean) p.mean[row] = x0 + dmean;
+            const float mean = near[0] + dmean;  // `about`: a row with an infinity, or differences beyond fp32
+            if (p.mean) p.mean[row] = fabsf(mean) < __uint_as_float(0x7f800000u) ? mean : about;
             if (p.rstd) p.rstd[row] = rstd;
         }
-        const f32x2 scale = f2(rstd);
+        const f32x2 scale = f2(rstd), shift = f2(-dmean * rstd);
         uint16_t* yr = Y + (int64_t)row * p.ldy;
 #pragma unroll
         for (int s = 0; s < V; ++s) {
             f32x2 f[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = f2_mul<true>(d[4 * s + e], scale);
+            for (int e = 0; e < 4; ++e) f[e] = f2_fma<true>(d[4 * s + e], scale, shift);
             if (affine) {
                 f32x2 g[4], b[4];
                 if constexpr (kStaged) {
@@ -132,7 +136,6 @@ __global__ void __launch_bounds__(row_block(W), ln_per_sm(W, V)) kt_ln_forward_k
         }
         if (next >= p.M) break;
         row = next;
-        first = next_first;
 #pragma unroll
         for (int s = 0; s < V; ++s) c[s] = n[s].slot();
     }
