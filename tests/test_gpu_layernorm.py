@@ -288,3 +288,23 @@ def test_equal_values_of_any_size(value):
         kt_ops.kt_layernorm_forward(x, gamma, beta, EPS, y, mean, rstd)
         assert (y == beta).all() and (mean == x[:, 0].float()).all()
         assert torch.allclose(rstd, torch.full_like(rstd, EPS ** -0.5), rtol=4e-7)
+
+
+@pytest.mark.parametrize("D", [5, 72, 643, 1152, 1280, 2051, 4096, 4099, 16383])
+@pytest.mark.parametrize("value,eps", [(2e36, 1e-5), (1e33, 1e-20)])
+def test_gradients_of_large_equal_values(D, value, eps):
+    """mean * rstd beyond fp32: xhat is 0 throughout and dx finite, whatever the row's length leaves
+    over of a lane's slots."""
+    M = 600
+    x = torch.full((M, D), value, dtype=torch.bfloat16, device="cuda")
+    dy = rows(M, D, 0, torch.bfloat16, D, 0.3)
+    gamma, _ = affine(D, torch.bfloat16, D)
+    mean, rstd = x[:, 0].float(), torch.full((M,), eps ** -0.5, device="cuda")
+    dx = torch.full((M, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dgamma, dbeta = torch.full((D,), float("nan"), device="cuda"), torch.full((D,), float("nan"), device="cuda")
+    kt_ops.kt_layernorm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, kt_ops.layernorm_backward_workspace(M, D))
+    dxx, dgx, dbx = ref.layernorm_backward(dy, x, gamma, mean, rstd)
+    tx, tg, tb = ref.layernorm_backward_bounds(dy, x, gamma, mean, rstd, dxx, x.dtype)
+    within(dx, dxx, tx, "dx")
+    within(dgamma, dgx, tg, "dgamma")
+    within(dbeta, dbx, tb, "dbeta")

@@ -111,8 +111,8 @@ __global__ void __launch_bounds__(row_block(W), ln_back_per_sm(W, V)) kt_ln_back
         const f32x2 mu = f2(mean), scale = f2(rstd);
         f32x2 a1 = f2(0.0f), a2 = f2(0.0f);
         f32x2 keep_xh[kKeep ? 4 * V : 1], keep_g[kKeep ? 4 * V : 1];
-        // xhat, dy and g of slot s
-        auto terms = [&](int s, f32x2 (&xh)[4], f32x2 (&y)[4], f32x2 (&ge)[4]) {
+        // x - mean, xhat, dy and g of slot s
+        auto terms = [&](int s, f32x2 (&dev)[4], f32x2 (&xh)[4], f32x2 (&y)[4], f32x2 (&ge)[4]) {
             f32x2 x[4], g[4];
             unpack_pairs<DT>(cx[s], x);
             unpack_pairs<DT>(cy[s], y);
@@ -122,19 +122,25 @@ __global__ void __launch_bounds__(row_block(W), ln_back_per_sm(W, V)) kt_ln_back
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                xh[e] = f2_mul<true>(f2_sub<true>(x[e], mu), scale);
+                dev[e] = f2_sub<true>(x[e], mu);
+                xh[e] = f2_mul<true>(dev[e], scale);
                 ge[e] = affine ? f2_mul<true>(y[e], g[e]) : y[e];
             }
         };
 #pragma unroll
         for (int s = 0; s < V; ++s) {
-            f32x2 xh[4], y[4], ge[4];
-            terms(s, xh, y, ge);
+            f32x2 dev[4], xh[4], y[4], ge[4];
+            terms(s, dev, xh, y, ge);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                // columns past the row's end have dy = 0 and add nothing to either average
+                // Columns past the row's end add nothing to either average: dy is 0 there.  But with x = 0
+                // their xhat may be beyond fp32 where the row's own are not, and 0 * inf is no number.
+                // With 16-byte slots, of which only the last ones are concerned, it is set to 0; without,
+                // where a test of each element would cost registers that are not there, the sum is of
+                // g (x - mean), which is finite, and rstd comes after it.
+                if constexpr (VEC) clear_past_end<VEC, W, V>(xh[e], s, e, l, D);
                 a1 = f2_add<true>(a1, ge[e]);
-                a2 = f2_fma<true>(ge[e], xh[e], a2);
+                a2 = f2_fma<true>(ge[e], VEC ? xh[e] : dev[e], a2);
                 if constexpr (kKeep) {
                     keep_xh[4 * s + e] = xh[e];
                     keep_g[4 * s + e] = ge[e];
@@ -154,6 +160,7 @@ __global__ void __launch_bounds__(row_block(W), ln_back_per_sm(W, V)) kt_ln_back
             }
         }
         float s1 = a1.x + a1.y, s2 = a2.x + a2.y;
+        if constexpr (!VEC) s2 = rstd == 0.0f ? 0.0f : s2 * rstd;  // 0: a row whose variance is beyond fp32
         team_add2<W>(s1, s2, lines, turn, team);
         if constexpr (RING) {  // this lane has its part of the row: its slots take the row `rows` ahead
             if (p.M - row > (int64_t)ring.rows * step) copy(slot, (int64_t)row + (int64_t)ring.rows * step);
@@ -169,7 +176,7 @@ __global__ void __launch_bounds__(row_block(W), ln_back_per_sm(W, V)) kt_ln_back
         uint16_t* xr = dX + (int64_t)row * p.lddx;
 #pragma unroll
         for (int s = 0; s < V; ++s) {
-            f32x2 xh[4], y[4], ge[4];
+            f32x2 dev[4], xh[4], y[4], ge[4];
             if constexpr (kKeep) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -177,7 +184,7 @@ __global__ void __launch_bounds__(row_block(W), ln_back_per_sm(W, V)) kt_ln_back
                     ge[e] = keep_g[4 * s + e];
                 }
             } else {
-                terms(s, xh, y, ge);
+                terms(s, dev, xh, y, ge);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] = f2_mul<true>(scale, f2_sub<true>(ge[e], f2_fma<true>(xh[e], c2, c1)));
