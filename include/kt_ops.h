@@ -103,6 +103,23 @@ kt_status kt_linear_i8(int64_t M, int64_t N, int64_t K, kt_dtype dtype, const in
                        void* stream);
 
 /*
+ * kt_linear_i8_status -- wait for `stream` and read the current device's error word of kt_linear_i8,
+ * as kt_mlp_status does a plan's: KT_ERR_TIMEOUT if a bounded device-side wait ran out in any of
+ * the device's calls since it was last asked (the word is cleared).  Such a call stores NaN in every
+ * element of Y that it could not compute, so that what is computed from it shows it as well.
+ */
+kt_status kt_linear_i8_status(void* stream);
+
+/*
+ * kt_linear_i8_debug_stall -- failure-injection hook for tests, as kt_mlp_debug_stall.  With enable = 1
+ * the following calls of this process with more than KT_LINEAR_I8_DOT_ROWS rows wait, in the block
+ * of their first tile, on a barrier nobody signals, bounded as every other wait then is by `limit_us`
+ * microseconds; the wait runs out and the call ends with that block's tiles NaN.  enable = 0
+ * restores normal calls.  No GPU fault is involved.
+ */
+kt_status kt_linear_i8_debug_stall(int enable, int64_t limit_us);
+
+/*
  * The mixture-of-experts feed-forward layer for a few tokens.  For each token x of X[T][D]:
  *   logits[e] = x . W_router[e]                     (exact to about 48 bits, as an order hangs on them)
  *   its experts: the top_k largest logits, a tie going to the lower index

@@ -284,3 +284,32 @@ def test_new_values_in_the_same_buffers_are_read(M, N, K, captured):
     torch.cuda.synchronize()
     for i in range(steps):
         assert torch.equal(got[i], alone[i]), i
+
+
+# one CTA per tile of both widths, a pair per tile of each width, clusters that share a tile
+@pytest.mark.parametrize("M,N,K", [(100, 130, 272), (100, 1500, 272), (140, 9728, 640), (5000, 640, 144), (1300, 10240, 144), (2000, 5000, 208),
+                                   (64, 1280, 5120), (100, 8192, 4096)])
+def test_a_wait_that_runs_out_is_reported_and_shows(M, N, K):
+    """The first block waits, for 20 ms, on a barrier that nobody signals: the status says so, its tiles
+    are NaN and nothing is left unwritten, and the next call is right again."""
+    g = torch.Generator().manual_seed(M)
+    q = torch.randint(-127, 128, (M, K), generator=g, dtype=torch.int32).to(torch.int8).cuda()
+    w = torch.randint(-127, 128, (N, K), generator=g, dtype=torch.int32).to(torch.int8).cuda()
+    sx, sw = (torch.rand(M, generator=g) * 1e-3).cuda(), (torch.rand(N, generator=g) * 1e-2).cuda()
+    want = torch.empty(M, N, dtype=torch.float16, device="cuda")
+    kt_ops.kt_linear_i8(q, sx, w, sw, None, want)
+    assert kt_ops.kt_linear_i8_status() == kt_mlp.KT_OK
+    got = torch.full((M, N + 3), 7.0, dtype=torch.float16, device="cuda")
+    kt_ops.kt_linear_i8_debug_stall(True, 20000)
+    try:
+        kt_ops.kt_linear_i8(q, sx, w, sw, None, got[:, :N])
+        assert kt_ops.kt_linear_i8_status() == kt_mlp.KT_ERR_TIMEOUT
+    finally:
+        kt_ops.kt_linear_i8_debug_stall(False)
+    bad = got[:, :N].isnan()
+    assert bad[0, 0] and (bad | (got[:, :N] == want)).all()
+    assert (got[:, N:] == 7).all()
+    assert kt_ops.kt_linear_i8_status() == kt_mlp.KT_OK
+    kt_ops.kt_linear_i8(q, sx, w, sw, None, got[:, :N])
+    assert kt_ops.kt_linear_i8_status() == kt_mlp.KT_OK
+    assert torch.equal(got[:, :N], want)

@@ -191,3 +191,15 @@ def test_gradient_formulas_agree_with_differences(affine):
             down = loss(x, gamma, beta)
             flat[i] = keep
             assert abs((up - down) / (2 * h) - grad.reshape(-1)[i]) < 1e-6
+
+
+@pytest.mark.parametrize("limit_us", [0, -1, 10_000_001])
+def test_linear_i8_debug_stall_refuses_a_limit(lib, limit_us):
+    assert lib.kt_linear_i8_debug_stall(1, limit_us) == INVALID
+    assert lib.kt_linear_i8_debug_stall(0, limit_us) == kt_mlp.KT_OK
+
+
+def test_linear_i8_status_without_a_gpu(lib):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    assert lib.kt_linear_i8_status(None) in (kt_mlp.KT_ERR_CUDA, UNSUPPORTED)

@@ -179,7 +179,9 @@ constexpr int kTcChannel0 = kTcGroups * kTcTokenWarps, kTcEpi0 = kTcChannel0 + k
 constexpr int kTcMmaWarp = kTcEpi0 + kTcEpiWarps, kTcThreads = (kTcMmaWarp + kTcSlots) * 32;
 static_assert(kTcSlots % kTcGroups == 0 && kTcEpi0 % 4 == 0, "a group has slots of its own; epilogue warp q: lanes 32 q");
 constexpr uint32_t kTcACol = 256;  // tensor-memory column of the first operand's slots, after the accumulators
-__device__ int g_linear_i8_error;  // a bounded wait that ran out (never in normal operation)
+// A bounded wait that ran out (never in normal operation), until kt_linear_i8_status asks.  The
+// elements that the call then cannot compute are stored as NaN, so that its own Y shows it too.
+__device__ int g_linear_i8_error;
 
 __device__ __forceinline__ void bytes_to_halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
     const uint32_t u = w ^ 0x80808080u, big = 0x64806480u;
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
     Smem& sm = *reinterpret_cast<Smem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int* abort_flag = &sm.abort;
-    constexpr unsigned long long kLimit = 4000000000ull;  // 4 s: far beyond any legitimate wait
+    const unsigned long long limit = p.wait_limit_ns;
     auto bar = [&](uint64_t& b) { return smem_u32(&b); };
     const int rank = PAIR == 2 ? (int)cluster_ctarank() : 0;
     const int splits = SPLIT ? (int)cluster_size() : 1, part = SPLIT ? (int)cluster_ctarank() : 0;
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
         uint32_t slot = group, phase = 0;
         if (group < total) fetch();
         for (int s = group; s < total; s += kTcGroups) {
-            const bool ok = wait_phase(bar(sm.empty[slot]), phase ^ 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_PRODUCER, kLimit);
+            const bool ok = wait_phase(bar(sm.empty[slot]), phase ^ 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_PRODUCER, limit);
             if (!__all_sync(0xffffffffu, ok)) return;
             convert(reg, slot);
             __syncwarp();
@@ -467,7 +469,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
                 const uint32_t to = mapa_rank(bar(sm.full[slot]), 0u);
                 uint32_t phase = 0;
                 for (int s = slot; s < total; s += kTcSlots, phase ^= 1u) {
-                    if (!wait_phase(bar(sm.full[slot]), phase, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_MMA, kLimit)) break;
+                    if (!wait_phase(bar(sm.full[slot]), phase, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_MMA, limit)) break;
                     tc_fence_after();
                     tc_fence_before();
                     mbar_arrive_cluster(to);
@@ -478,14 +480,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
             uint32_t slot = 0, phase = 0;
             const uint32_t leader = lane == 0;
             bool ok = true;
+            if (p.stall_ns && unit == 0 && part == 0)  // the tests' hook: nobody signals this barrier yet
+                ok = __all_sync(0xffffffffu, wait_phase(bar(sm.drain), 0u, abort_flag, &g_linear_i8_error, DEV_INJECTED_STALL, p.stall_ns));
             const uint64_t bd0 = smem_desc(smem_u32(sm.b[0][0]), 16u, 1024u);
             for (int t = 0; t < mine && ok; ++t) {
                 const uint32_t buf = t % kBufs, use = (uint32_t)t / kBufs, d = tmem + buf * (uint32_t)BN;
                 ok = __all_sync(0xffffffffu, wait_phase<PAIR == 2>(bar(sm.acc_empty[buf]), (use & 1u) ^ 1u, abort_flag, &g_linear_i8_error,
-                                                                   DEV_TIMEOUT_MMA, kLimit));
+                                                                   DEV_TIMEOUT_MMA, limit));
                 for (int s = 0; s < steps && ok; ++s) {
                     ok = __all_sync(0xffffffffu, wait_phase<PAIR == 2>(bar(sm.full[slot]), phase, abort_flag, &g_linear_i8_error,
-                                                                       DEV_TIMEOUT_MMA, kLimit));
+                                                                       DEV_TIMEOUT_MMA, limit));
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
@@ -511,7 +515,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
         // ------------------- epilogue -------------------
         const int q = warp & 3, ew = warp - kTcEpi0;
         uint16_t* Y = static_cast<uint16_t*>(p.Y);
-        for (int t = 0; t < mine; ++t) {
+        int t = 0;
+        for (; t < mine; ++t) {
             const int tile = unit + t * units;
             const int m0 = (tile / tiles_n * PAIR + rank) * 128 + q * 32, n0 = (tile % tiles_n) * BN;
             const uint32_t buf = t % kBufs, use = (uint32_t)t / kBufs, cs = t & 1u;
@@ -524,7 +529,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
                 sm.ch[cs][i] = c;
             }
             const float sx = m0 + lane < p.M ? p.sx[m0 + lane] : 0.0f;
-            const bool got = wait_phase(bar(sm.acc_full[buf]), use & 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_EPILOGUE, kLimit);
+            const bool got = wait_phase(bar(sm.acc_full[buf]), use & 1u, abort_flag, &g_linear_i8_error, DEV_TIMEOUT_EPILOGUE, limit);
             if (!epi_all<kTcEpiWarps>(got)) break;  // also: every warp's part of ch is in place
             tc_fence_after();
             // first all of this warp's columns into shared memory, so that the next tile gets the
@@ -600,9 +605,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) kt_linear_i8_tc_kernel(const Li
                 }
             }
         }
+        if constexpr (!SPLIT) {  // tiles left by a wait that ran out
+#pragma unroll 1
+            for (; t < mine; ++t) {
+                const int tile = unit + t * units;
+                const int m0 = (tile / tiles_n * PAIR + rank) * 128 + q * 32, n0 = (tile % tiles_n) * BN;
+#pragma unroll 1
+                for (int r = 0; r < 32 && m0 + r < p.M; ++r)
+#pragma unroll 1
+                    for (int c = 32 * (ew >> 2) + lane; c < BN && n0 + c < p.N; c += 64) Y[(int64_t)(m0 + r) * p.ldy + n0 + c] = 0x7fffu;
+            }
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (SPLIT) {  // no sums from this CTA: NaN in their place, and so in the whole tile
+        if (*abort_flag)
+            for (int i = threadIdx.x; i < 128 * BN; i += kTcThreads) reinterpret_cast<float*>(sm.b[0][0])[i] = __uint_as_float(0x7fffffffu);
+    }
     if (PAIR == 2 || SPLIT) cluster_sync_all();  // neither CTA leaves while the other may still signal it; SPLIT: the sums are there
     if constexpr (SPLIT) {
         uint16_t* Y = static_cast<uint16_t*>(p.Y);
@@ -744,6 +764,20 @@ kt_status launch_tc(int dtype, const LinearI8& p, int sms, int device, void* str
 }
 
 }  // namespace
+
+kt_status linear_i8_status(void* stream, int* word, const char** why) {
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_linear_i8_error, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess && *word != 0) {
+        const int none = 0;
+        e = cudaMemcpyToSymbolAsync(g_linear_i8_error, &none, sizeof(int), 0, cudaMemcpyHostToDevice, st);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    }
+    if (e == cudaSuccess) return KT_OK;
+    *why = cudaGetErrorString(e);
+    return KT_ERR_CUDA;
+}
 
 kt_status launch_linear_i8(int dtype, const LinearI8& p, int sms, int device, void* stream, const char** why) {
     // Up to 16 tokens the integer products: 10240 channels of 1280, 8 tokens 6.8 us (tensor cores 9.3),

@@ -49,6 +49,10 @@ kt_status current_device(int* device, int* sms) {
     return KT_OK;
 }
 
+constexpr unsigned long long kWaitLimitNs = 4000000000ull;  // 4 s: far beyond any legitimate wait
+constexpr int64_t kMostStallUs = 10000000;
+std::atomic<int64_t> g_linear_stall_us{0};  // kt_linear_i8_debug_stall's limit; 0: off
+
 kt_status done(kt_status s, const char* why) { return kt::report(s, s == KT_OK ? "" : why); }
 
 // What the row operators have in common: sizes, dtype, pitches.
@@ -156,8 +160,27 @@ kt_status kt_linear_i8(int64_t M, int64_t N, int64_t K, kt_dtype dtype, const in
     int dev, sms;
     if ((s = current_device(&dev, &sms)) != KT_OK) return s;
     const char* why = "";
-    kt::LinearI8 p = {Q, W, scale_x, scale_w, bias, Y, ldq, ldw, ldy, (int)M, (int)N, (int)K};
+    const unsigned long long stall_ns = 1000ull * (unsigned long long)g_linear_stall_us.load(std::memory_order_relaxed);
+    kt::LinearI8 p = {Q,   W,      scale_x, scale_w, bias,    Y,       ldq, ldw, ldy, (int)M, (int)N, (int)K, stall_ns ? stall_ns : kWaitLimitNs,
+                      stall_ns};
     return done(kt::launch_linear_i8(dtype, p, sms, dev, stream, &why), why);
+}
+
+kt_status kt_linear_i8_status(void* stream) {
+    int dev, sms, word = 0;
+    kt_status s;
+    if ((s = current_device(&dev, &sms)) != KT_OK) return s;
+    const char* why = "";
+    if ((s = kt::linear_i8_status(stream, &word, &why)) != KT_OK) return kt::report(s, why);
+    if (word == 0) return done(KT_OK, "");
+    return kt::report(KT_ERR_TIMEOUT, word == kt::DEV_INJECTED_STALL ? "a bounded device wait ran out (injected stall)"
+                                                                     : "a bounded device wait ran out");
+}
+
+kt_status kt_linear_i8_debug_stall(int enable, int64_t limit_us) {
+    if (enable && (limit_us < 1 || limit_us > kMostStallUs)) return bad("limit_us must be in [1, 10 000 000]");
+    g_linear_stall_us.store(enable ? limit_us : 0, std::memory_order_relaxed);
+    return done(KT_OK, "");
 }
 
 kt_status kt_moe_plan(const kt_moe_options* o, kt_moe_plan_t* out) {
@@ -201,7 +224,7 @@ kt_status kt_moe_plan(const kt_moe_options* o, kt_moe_plan_t* out) {
     p.E = (int)o->experts;
     p.top_k = (int)o->top_k;
     p.normalize = o->normalize;
-    p.wait_limit_ns = 4000000000ull;  // 4 s: far beyond any legitimate wait
+    p.wait_limit_ns = kWaitLimitNs;
     kt::moe_carve(&p, o->max_tokens, plan->workspace);
     *out = plan;
     return done(KT_OK, "");

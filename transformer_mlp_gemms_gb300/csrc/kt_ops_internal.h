@@ -57,8 +57,11 @@ struct LinearI8 {
     void* Y;
     int64_t ldq, ldw, ldy;
     int M, N, K;
+    unsigned long long wait_limit_ns, stall_ns;  // bound of every device-side wait; the tests' hook (0: off)
 };
 kt_status launch_linear_i8(int dtype, const LinearI8& p, int sms, int device, void* stream, const char** why);
+// The current device's error word once `stream` is done, cleared if it was set.
+kt_status linear_i8_status(void* stream, int* word, const char** why);
 
 // The mixture-of-experts layer (kt_moe.cu).
 struct MoeParams {

@@ -49,6 +49,8 @@ SIGNATURES = {
     "kt_layernorm_backward_workspace": ([_I64, _I64], ctypes.c_size_t),
     "kt_quantize_rows": ([_I64, _I64, _I32, _I32, _VP, _I64, _VP, _I64, _VP, _VP], _I32),
     "kt_linear_i8": ([_I64, _I64, _I64, _I32, _VP, _I64, _VP, _I64, _VP, _VP, _VP, _VP, _I64, _VP], _I32),
+    "kt_linear_i8_status": ([_VP], _I32),
+    "kt_linear_i8_debug_stall": ([_I32, _I64], _I32),
     "kt_moe_plan": ([ctypes.POINTER(kt_moe_options), ctypes.POINTER(_VP)], _I32),
     "kt_moe_run": ([_VP, ctypes.POINTER(kt_moe_tensors), _VP], _I32),
     "kt_moe_status": ([_VP], _I32),
@@ -129,6 +131,16 @@ def kt_linear_i8(Q, scale_x, W, scale_w, bias, Y, stream=None) -> None:
     r = (_ext or _calls()).linear_i8(Q, scale_x, W, scale_w, bias, Y, stream)
     if r is not None:
         _fail(r, "kt_linear_i8")
+
+
+def kt_linear_i8_status(stream=None) -> int:
+    """Waits for the stream and returns the status code of the device's kt_linear_i8 calls (does not
+    raise on KT_ERR_TIMEOUT)."""
+    return load().kt_linear_i8_status(kt_mlp._stream(stream))
+
+
+def kt_linear_i8_debug_stall(enable: bool, limit_us: int = 0) -> None:
+    _check(load().kt_linear_i8_debug_stall(int(bool(enable)), limit_us), "kt_linear_i8_debug_stall")
 
 
 def kt_moe_plan(options: kt_moe_options) -> int:
