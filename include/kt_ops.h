@@ -175,8 +175,11 @@ kt_status kt_moe_plan(const kt_moe_options* options, kt_moe_plan_t* out);
  */
 kt_status kt_moe_run(kt_moe_plan_t plan, const kt_moe_tensors* tensors, void* stream);
 
-/* kt_moe_status -- wait for the plan's last stream and read its device error word, as kt_mlp_status:
- * KT_ERR_TIMEOUT if a bounded device-side wait ran out (the word is cleared, the plan usable again). */
+/*
+ * kt_moe_status -- wait for the plan's device (all its streams: a captured run may have been replayed
+ * on any) and read the plan's error word: KT_ERR_TIMEOUT if a bounded device-side wait ran out (the
+ * word is cleared, the plan usable again).  Y of that run, and of runs behind it, is not written.
+ */
 kt_status kt_moe_status(kt_moe_plan_t plan);
 
 /* kt_moe_destroy -- free the plan's workspace (after synchronising its device). */

@@ -217,3 +217,23 @@ def test_new_tokens_through_the_same_workspace(T, D, F, E, k, act, dtype):
             plan.run(x, t["W_router"], t["W_up"], t["W_down"], y)
         assert plan.status() == kt_mlp.KT_OK
         assert all(torch.equal(a, b) for a, b in zip(alone, again))
+
+
+def test_the_status_covers_replays_on_any_stream():
+    """A graph captured on one stream and replayed on another: the status waits for the replays."""
+    t = problem(4, 64, 64, 8, 2, "silu", "f16", False, 10)
+    plan = plan_of(4, 64, 64, 8, 2, "silu", "f16", False, True)
+    want, _, _ = run(plan, t)
+    got = torch.full_like(want, float("nan"))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan.run(t["X"], t["W_router"], t["W_up"], t["W_down"], got)
+    side, done = torch.cuda.Stream(), torch.cuda.Event()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # about 0.1 s
+        graph.replay()
+        done.record()
+    assert plan.status() == kt_mlp.KT_OK
+    assert done.query()
+    assert torch.equal(got, want)

@@ -71,9 +71,25 @@ struct kt_moe_plan_s {
     int device = -1, sms = 0;
     void* workspace = nullptr;
     kt::MoeParams p;
-    void* last_stream = nullptr;
     bool ran = false;
 };
+
+namespace {
+
+// Makes a device current, and the former one again at its end.
+struct OnDevice {
+    int prev = -1, device;
+    explicit OnDevice(int d) : device(d) {
+        cudaGetDevice(&prev);
+        if (prev != device) cudaSetDevice(device);
+    }
+    ~OnDevice() {
+        if (prev >= 0 && prev != device) cudaSetDevice(prev);
+    }
+    OnDevice(const OnDevice&) = delete;
+};
+
+}  // namespace
 
 extern "C" {
 
@@ -262,7 +278,6 @@ kt_status kt_moe_run(kt_moe_plan_t plan, const kt_moe_tensors* t, void* stream) 
     p.weights = t->weights;
     p.ldx = t->ldx;
     p.T = (int)t->tokens;
-    plan->last_stream = stream;
     plan->ran = true;
     const char* why = "";
     return done(kt::launch_moe(plan->o.act, plan->o.dtype, p, plan->sms, plan->device, stream, &why), why);
@@ -271,26 +286,27 @@ kt_status kt_moe_run(kt_moe_plan_t plan, const kt_moe_tensors* t, void* stream) 
 kt_status kt_moe_status(kt_moe_plan_t plan) {
     if (!plan) return bad("plan is NULL");
     if (!plan->ran) return done(KT_OK, "");
-    cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(plan->last_stream));
-    if (e != cudaSuccess) return cuda_failed("cudaStreamSynchronize", e);
+    // the whole device: a captured run may have been replayed on any stream
+    const OnDevice on(plan->device);
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return cuda_failed("cudaDeviceSynchronize", e);
     int word = 0;
     e = cudaMemcpy(&word, plan->p.error, sizeof(word), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_failed("cudaMemcpy", e);
     if (word == 0) return done(KT_OK, "");
     e = cudaMemset(plan->workspace, 0, kt::kMoeControlBytes);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_failed("clearing the plan's counters", e);
     return kt::report(KT_ERR_TIMEOUT, "a device-side wait ran out");
 }
 
 kt_status kt_moe_destroy(kt_moe_plan_t plan) {
     if (!plan) return bad("plan is NULL");
-    int prev = -1;
-    cudaGetDevice(&prev);
-    if (prev != plan->device) cudaSetDevice(plan->device);
-    cudaDeviceSynchronize();
-    cudaFree(plan->workspace);
-    if (prev >= 0 && prev != plan->device) cudaSetDevice(prev);
+    {
+        const OnDevice on(plan->device);
+        cudaDeviceSynchronize();
+        cudaFree(plan->workspace);
+    }
     delete plan;
     return done(KT_OK, "");
 }

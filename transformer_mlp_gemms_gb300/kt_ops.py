@@ -154,7 +154,7 @@ def kt_moe_run(plan: int, tensors: kt_moe_tensors, stream=None) -> None:
 
 
 def kt_moe_status(plan: int) -> int:
-    """Returns the status code (does not raise on KT_ERR_TIMEOUT)."""
+    """Waits for the plan's device and returns the status code (does not raise on KT_ERR_TIMEOUT)."""
     return load().kt_moe_status(plan)
 
 
