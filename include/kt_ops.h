@@ -182,6 +182,14 @@ kt_status kt_moe_run(kt_moe_plan_t plan, const kt_moe_tensors* tensors, void* st
  */
 kt_status kt_moe_status(kt_moe_plan_t plan);
 
+/*
+ * kt_moe_debug_stall -- failure-injection hook for tests, as kt_mlp_debug_stall.  With enable = 1 the
+ * first block of the plan's following runs waits on a barrier nobody signals, bounded as every
+ * other wait then is by `limit_us` microseconds; the wait runs out, the other blocks give up,
+ * and the run ends without its output.  enable = 0 restores normal runs.  No GPU fault is involved.
+ */
+kt_status kt_moe_debug_stall(kt_moe_plan_t plan, int enable, int64_t limit_us);
+
 /* kt_moe_destroy -- free the plan's workspace (after synchronising its device). */
 kt_status kt_moe_destroy(kt_moe_plan_t plan);
 

@@ -237,3 +237,43 @@ def test_the_status_covers_replays_on_any_stream():
     assert plan.status() == kt_mlp.KT_OK
     assert done.query()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T,D,F,E,k,act,dtype", [(1, 640, 1280, 8, 2, "geglu", "bf16"), (9, 256, 4304, 16, 2, "gelu_tanh", "f16"),
+                                                 (64, 256, 520, 12, 4, "geglu", "bf16")])
+def test_a_wait_that_runs_out_is_reported_and_the_plan_recovers(T, D, F, E, k, act, dtype):
+    """The first block waits, for 20 ms, on a barrier that nobody signals; the others give up with it.
+    Runs behind it do nothing until the status has been asked."""
+    t = problem(T, D, F, E, k, act, dtype, False, 11)
+    plan = plan_of(T, D, F, E, k, act, dtype, False, True)
+    want, _, _ = run(plan, t)
+    got = torch.full_like(want, 7.0)
+    args = (t["X"], t["W_router"], t["W_up"], t["W_down"], got)
+    kt_ops.kt_moe_debug_stall(plan.handle, True, 20000)
+    plan.run(*args)
+    kt_ops.kt_moe_debug_stall(plan.handle, False)
+    plan.run(*args)
+    assert plan.status() == kt_mlp.KT_ERR_TIMEOUT
+    assert (got == 7).all()
+    assert plan.status() == kt_mlp.KT_OK
+    for _ in range(2):
+        again, _, _ = run(plan, t)
+        assert torch.equal(again, want)
+
+
+def test_the_status_sees_a_replay_that_ran_out_on_another_stream():
+    t = problem(4, 64, 64, 8, 2, "silu", "f16", False, 10)
+    plan = plan_of(4, 64, 64, 8, 2, "silu", "f16", False, True)
+    want, _, _ = run(plan, t)
+    got = torch.full_like(want, 7.0)
+    kt_ops.kt_moe_debug_stall(plan.handle, True, 20000)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan.run(t["X"], t["W_router"], t["W_up"], t["W_down"], got)
+    kt_ops.kt_moe_debug_stall(plan.handle, False)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        graph.replay()
+    assert plan.status() == kt_mlp.KT_ERR_TIMEOUT
+    again, _, _ = run(plan, t)
+    assert torch.equal(again, want)

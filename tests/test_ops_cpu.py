@@ -203,3 +203,7 @@ def test_linear_i8_status_without_a_gpu(lib):
     if torch.cuda.is_available():
         pytest.skip("a GPU is present")
     assert lib.kt_linear_i8_status(None) in (kt_mlp.KT_ERR_CUDA, UNSUPPORTED)
+
+
+def test_moe_debug_stall_refuses_a_null_plan(lib):
+    assert lib.kt_moe_debug_stall(None, 1, 1000) == INVALID

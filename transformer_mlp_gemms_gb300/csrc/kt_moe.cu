@@ -517,6 +517,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         // ------------------ one thread issues the products ------------------
         uint32_t stage = 0, phase = 0, t = 0;
         bool ok = true;
+        if (p.stall_ns && blockIdx.x == 0)  // the tests' hook: nobody signals this barrier yet
+            ok = wait_phase(bar(bars.drain), 0u, abort_flag, p.error, DEV_INJECTED_STALL, p.stall_ns);
         for (int ph = 0; ph < 2 && ok; ++ph) {
             const bool up = ph == 0;
             const int n_items = up ? m.up_items : m.down_items;

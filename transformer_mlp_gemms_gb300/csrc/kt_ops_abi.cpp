@@ -297,7 +297,16 @@ kt_status kt_moe_status(kt_moe_plan_t plan) {
     e = cudaMemset(plan->workspace, 0, kt::kMoeControlBytes);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_failed("clearing the plan's counters", e);
-    return kt::report(KT_ERR_TIMEOUT, "a device-side wait ran out");
+    return kt::report(KT_ERR_TIMEOUT, word == kt::DEV_INJECTED_STALL ? "a device-side wait ran out (injected stall)"
+                                                                     : "a device-side wait ran out");
+}
+
+kt_status kt_moe_debug_stall(kt_moe_plan_t plan, int enable, int64_t limit_us) {
+    if (!plan) return bad("plan is NULL");
+    if (enable && (limit_us < 1 || limit_us > kMostStallUs)) return bad("limit_us must be in [1, 10 000 000]");
+    plan->p.stall_ns = enable ? 1000ull * (unsigned long long)limit_us : 0;
+    plan->p.wait_limit_ns = enable ? plan->p.stall_ns : kWaitLimitNs;
+    return done(KT_OK, "");
 }
 
 kt_status kt_moe_destroy(kt_moe_plan_t plan) {

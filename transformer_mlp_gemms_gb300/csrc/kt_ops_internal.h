@@ -78,7 +78,7 @@ struct MoeParams {
     unsigned* barriers;  // grid barrier counters, zero between runs
     unsigned* ready;     // of each active expert: tiles of its H that are stored; zero between runs
     int* error;          // device error word
-    unsigned long long wait_limit_ns;
+    unsigned long long wait_limit_ns, stall_ns;  // bound of every device-side wait; the tests' hook (0: off)
 };
 // Splits of the down projection along F that there is room for: up to 32 while pairs are few.
 KT_HOST_DEVICE inline int moe_splits(int pairs) { return pairs >= 1024 ? 1 : pairs * 32 < 1024 ? 32 : 1024 / pairs; }

@@ -54,6 +54,7 @@ SIGNATURES = {
     "kt_moe_plan": ([ctypes.POINTER(kt_moe_options), ctypes.POINTER(_VP)], _I32),
     "kt_moe_run": ([_VP, ctypes.POINTER(kt_moe_tensors), _VP], _I32),
     "kt_moe_status": ([_VP], _I32),
+    "kt_moe_debug_stall": ([_VP, _I32, _I64], _I32),
     "kt_moe_destroy": ([_VP], _I32),
 }
 
@@ -156,6 +157,10 @@ def kt_moe_run(plan: int, tensors: kt_moe_tensors, stream=None) -> None:
 def kt_moe_status(plan: int) -> int:
     """Waits for the plan's device and returns the status code (does not raise on KT_ERR_TIMEOUT)."""
     return load().kt_moe_status(plan)
+
+
+def kt_moe_debug_stall(plan: int, enable: bool, limit_us: int = 0) -> None:
+    _check(load().kt_moe_debug_stall(plan, int(bool(enable)), limit_us), "kt_moe_debug_stall")
 
 
 def kt_moe_destroy(plan: int) -> None:
