@@ -95,7 +95,9 @@ kt_status kt_quantize_rows(int64_t M, int64_t K, kt_dtype dtype, kt_act act, con
  * KT_LINEAR_I8_DOT_ROWS; above, they run on the tensor cores as 16-bit floats, which hold every
  * int8 and every product, into fp32: exact as long as the partial sums stay below 2^24 (always
  * for K <= 1024; for longer rows unless |Q| and |W| are near 127 throughout with equal signs),
- * and beyond that rounded as fp32 sums are.  One rounding to dtype at the end.
+ * and beyond that rounded as fp32 sums are.  Where the sums are exact a row's result does not hang
+ * on M; where they are not, it may differ between calls of few and of many rows, within these
+ * roundings.  One rounding to dtype at the end.
  */
 #define KT_LINEAR_I8_DOT_ROWS 16
 kt_status kt_linear_i8(int64_t M, int64_t N, int64_t K, kt_dtype dtype, const int8_t* Q, int64_t ldq, const int8_t* W,

@@ -313,3 +313,22 @@ def test_a_wait_that_runs_out_is_reported_and_shows(M, N, K):
     kt_ops.kt_linear_i8(q, sx, w, sw, None, got[:, :N])
     assert kt_ops.kt_linear_i8_status() == kt_mlp.KT_OK
     assert torch.equal(got[:, :N], want)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("K", [64, 1024])
+def test_a_row_is_the_same_in_calls_of_any_length(K, dtype):
+    """Exact sums, then the same roundings: on the integer products of few tokens, on one tile and on
+    many."""
+    g = torch.Generator().manual_seed(K)
+    N, dt = 10240, DT[dtype]
+    q = torch.randint(-128, 128, (300, K), generator=g, dtype=torch.int32).to(torch.int8).cuda()
+    w = torch.randint(-128, 128, (N, K), generator=g, dtype=torch.int32).to(torch.int8).cuda()
+    sx, sw = (torch.rand(300, generator=g) * 1e-3).cuda(), (torch.rand(N, generator=g) * 1e-2).cuda()
+    b = torch.randn(N, generator=g).to(dt).cuda()
+    first = torch.empty(16, N, dtype=dt, device="cuda")
+    kt_ops.kt_linear_i8(q[:16], sx[:16], w, sw, b, first)
+    for M in (1, 17, 130, 300):
+        y = torch.empty(M, N, dtype=dt, device="cuda")
+        kt_ops.kt_linear_i8(q[:M], sx[:M], w, sw, b, y)
+        assert torch.equal(y[:16], first[:M])

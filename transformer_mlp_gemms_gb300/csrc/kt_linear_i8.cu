@@ -132,8 +132,8 @@ __global__ void __launch_bounds__(kDotWarps * 32) kt_linear_i8_dot_kernel(const 
     for (int r = 0; r < 2; ++r) {
         const int n = n0 + r;
         if (n >= p.N) break;
-        float v = (float)sum[r] * (sx * p.sw[n]);
-        if (p.bias) v += from_bits<DT>(static_cast<const uint16_t*>(p.bias)[n]);
+        // the same roundings as for many tokens: a row's result does not hang on how many are with it
+        const float v = fmaf((float)sum[r], sx * p.sw[n], p.bias ? from_bits<DT>(static_cast<const uint16_t*>(p.bias)[n]) : 0.0f);
         static_cast<uint16_t*>(p.Y)[(int64_t)(m0 + k8) * p.ldy + n] = to_bits<DT>(v);
     }
 }
