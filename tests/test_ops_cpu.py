@@ -4,6 +4,8 @@ gradients against differences."""
 import ctypes
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -207,3 +209,25 @@ def test_linear_i8_status_without_a_gpu(lib):
 
 def test_moe_debug_stall_refuses_a_null_plan(lib):
     assert lib.kt_moe_debug_stall(None, 1, 1000) == INVALID
+
+
+def test_the_library_builds_without_torch(lib, tmp_path):
+    """A C user of the headers needs nvcc alone: no torch, and so no module."""
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "from transformer_mlp_gemms_gb300 import build as b\n"
+            f"b.MODULE = {str(tmp_path / '_kt_ops.so')!r}\n"
+            "print(b.build())")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    assert "left out" in r.stdout and r.stdout.split()[-1] == kbuild.LIB
+    assert not (tmp_path / "_kt_ops.so").exists()
+
+
+def test_the_module_is_built_anew_for_another_torch(lib, tmp_path, monkeypatch):
+    assert kbuild._module_is_for(kbuild._module_for())
+    monkeypatch.setattr(kbuild, "MODULE_STAMP", str(tmp_path / "stamp"))
+    assert not kbuild._module_is_for(kbuild._module_for())  # built by nobody knows what
+    (tmp_path / "stamp").write_text(kbuild._module_for())
+    assert kbuild._module_is_for(kbuild._module_for())
+    monkeypatch.setattr(torch, "__version__", "another")
+    assert not kbuild._module_is_for(kbuild._module_for())

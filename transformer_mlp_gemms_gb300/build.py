@@ -3,7 +3,9 @@
 
 Each translation unit is compiled in parallel, then linked with ``nvcc -shared``.
 The CUDA runtime is linked statically; the driver's tensor-map encoder is looked
-up at run time, so the library has no link-time dependency on libcuda.
+up at run time, so the library has no link-time dependency on libcuda.  The library comes first and
+needs nothing else; the module is left out, with a line that says so, where this interpreter
+has no torch or no headers, and is built anew for another torch or interpreter.
 
     python -m transformer_mlp_gemms_gb300.build [--force] [--verbose]
 """
@@ -22,7 +24,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libkt_mlp.so")
 MODULE = os.path.join(BUILD, "_kt_ops.so")
+MODULE_OBJ = os.path.join(BUILD, "kt_ops_py.cpp.o")
+MODULE_STAMP = os.path.join(BUILD, "_kt_ops.for")  # the torch and interpreter that the module was built for
 MODULE_SOURCE = os.path.join(CSRC, "kt_ops_py.cpp")
+MODULE_DEPS = [MODULE_SOURCE, os.path.join(INCLUDE, "kt_mlp.h"), os.path.join(INCLUDE, "kt_ops.h")]
 
 SOURCES = ["kt_gemm_act.cu", "kt_gemm_geglu.cu", "kt_gemm_down.cu", "kt_mlp_two_act_f16.cu", "kt_mlp_two_act_bf16.cu",
            "kt_mlp_two_geglu.cu", "kt_fused.cu", "kt_mlp_kernels.cu", "kt_mlp_abi.cpp", "kt_planner.cpp",
@@ -55,19 +60,40 @@ def _stale(out: str, deps) -> bool:
 
 
 def _module_flags():
-    """(compile, link) flags of the Python module: this interpreter's and this torch's headers and libraries."""
+    """(compile, link) flags of the Python module: this interpreter's and this torch's headers and
+    libraries.  None where they are not there."""
     import sysconfig
 
-    import torch
+    python = sysconfig.get_paths()["include"]
+    try:
+        import torch
+    except ImportError:
+        return None
+    if not os.path.exists(os.path.join(python, "Python.h")):
+        return None
     home = os.path.dirname(os.path.abspath(torch.__file__))
     lib, inc = os.path.join(home, "lib"), os.path.join(home, "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
-    compile_ = ["-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", inc,
+    compile_ = ["-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-I", python, "-isystem", inc,
                 "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
                 f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     link = ["-L", BUILD, "-l:libkt_mlp.so", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda",
             "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
     return compile_, link
+
+
+def _module_for() -> str:
+    """What the module's binary interface depends on, as text."""
+    import torch
+    return f"python {sys.version} {sys.implementation.cache_tag}\ntorch {torch.__version__} {os.path.abspath(torch.__file__)}\n"
+
+
+def _module_is_for(what: str) -> bool:
+    try:
+        with open(MODULE_STAMP) as f:
+            return f.read() == what
+    except OSError:
+        return False
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -85,14 +111,13 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             if verbose:
                 print(" ".join(cmd), flush=True)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
-    module_obj = os.path.join(BUILD, "kt_ops_py.cpp.o")
-    if force or _stale(module_obj, [MODULE_SOURCE, os.path.join(INCLUDE, "kt_mlp.h"), os.path.join(INCLUDE, "kt_ops.h")]):
-        cmd = ["g++", "-c", MODULE_SOURCE, "-o", module_obj] + _module_flags()[0]
+    flags = _module_flags()
+    module = None
+    if flags is not None and (force or not _module_is_for(_module_for()) or _stale(MODULE_OBJ, MODULE_DEPS)):
+        cmd = ["g++", "-c", MODULE_SOURCE, "-o", MODULE_OBJ] + flags[0]
         if verbose:
             print(" ".join(cmd), flush=True)
         module = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-    else:
-        module = None
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -109,17 +134,23 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
+    if flags is None:
+        print(f"{os.path.basename(MODULE)} left out: no torch or no Python.h for this interpreter ({os.path.basename(LIB)} is complete)",
+              flush=True)
+        return LIB
     if module is not None:
         out, _ = module.communicate()
         if module.returncode != 0:
             raise RuntimeError(f"g++ failed on kt_ops_py.cpp:\n{out}")
-    if module is not None or _stale(MODULE, [module_obj]):
+    if module is not None or _stale(MODULE, [MODULE_OBJ]):
         tmp = MODULE + f".tmp{os.getpid()}"
-        cmd = ["g++", "-shared", "-o", tmp, module_obj] + _module_flags()[1]
+        cmd = ["g++", "-shared", "-o", tmp, MODULE_OBJ] + flags[1]
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
         os.replace(tmp, MODULE)
+        with open(MODULE_STAMP, "w") as f:
+            f.write(_module_for())
     return LIB
 
 
