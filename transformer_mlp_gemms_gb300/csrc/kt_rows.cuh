@@ -137,11 +137,6 @@ __device__ __forceinline__ void forget_unpacked(uint4 (&c)[V]) {
     for (int s = 0; s < V; ++s) asm volatile("" : "+r"(c[s].x), "+r"(c[s].y), "+r"(c[s].z), "+r"(c[s].w));
 }
 
-template <int DT>
-__device__ __forceinline__ uint4 pack8(const float* y) {
-    return make_uint4(pack2<DT>(y[0], y[1]), pack2<DT>(y[2], y[3]), pack2<DT>(y[4], y[5]), pack2<DT>(y[6], y[7]));
-}
-
 // Reductions over a team, the same bits in every lane.  Across warps they go through one of
 // two shared-memory lines in turn, so one barrier per reduction is enough: a line is written
 // again only after the next reduction's barrier, which every warp reaches after its reads.
