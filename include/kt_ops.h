@@ -127,9 +127,10 @@ kt_status kt_linear_i8_debug_stall(int enable, int64_t limit_us);
  *   its experts: the top_k largest logits, a tie going to the lower index
  *   weight_j = exp(logit_j) / sum of exp over all experts, or over the chosen ones (normalize)
  *   y = sum_j weight_j * ( act(x . W_up[e_j]^T + b_up[e_j]) . W_down[e_j]^T + b_down[e_j] )  (+ R)
- * in fp32 with one rounding to dtype at the end.  The hidden layer is kept as two 16-bit parts
- * (its rounding and the remainder's), so it carries no rounding of its own; with KT_F16 a hidden
- * value beyond 65504 is infinite, as in kt_mlp_run.  A NaN among a token's logits makes that
+ * in fp32 with one rounding to dtype at the end.  The hidden layer is kept as two 16-bit parts, its
+ * rounding and the remainder's: to 2^-17 of its value with KT_BF16 (about 2e-6 of an output, which
+ * is itself rounded to 2^-9), to 2^-22 with KT_F16, there never better than 2^-25 in absolute terms;
+ * with KT_F16 a hidden value beyond 65504 is infinite, as in kt_mlp_run.  A NaN among a token's logits makes that
  * token's weights and outputs NaN; its experts are still valid indices.
  */
 #define KT_MOE_MAX_TOKENS 64

@@ -8,7 +8,7 @@
 // columns; registers beyond), and the next row's loads are issued before this row's reductions.
 // What else the time goes to is instructions: the deviations are unpacked once and kept as fp32,
 // two at a time (10 instructions per element before, 5 now).  65536 x 640 takes 29.0 us, 5.8 TB/s;
-// 32768 x 1280 27.6 us, 6.1 TB/s; a few rows 2.3 us, a launch's latency.  A ring of rows ahead in
+// 32768 x 1280 27.6 us, 6.1 TB/s; 65536 x 642 42 us; a few rows 2.3 us, a launch's latency.  A ring of rows ahead in
 // shared memory, as the backward pass has, is slower here: 36 us for the first.
 #include "kt_ops_internal.h"
 #include "kt_rows.cuh"

@@ -77,7 +77,7 @@ __device__ __forceinline__ uint4 load_slot(const uint16_t* __restrict__ row, int
 
 // A slot on its way: the loads go out, and `slot` takes what came.  Without 16-byte loads the
 // elements wait one by one: packing them where they are loaded would wait for them there (layer
-// norm of 65536 x 642: 114 us, here 44; its gradients 107 and 85).
+// norm of 65536 x 642: 114 us, here 42; its gradients 107 and 85).
 template <bool VEC>
 struct SlotAhead {
     uint4 w;
@@ -254,7 +254,7 @@ constexpr int staged_bytes(int W, int V) { return V * 32 * W * 8 * 4; }
 // The same without 16-byte loads, for kernels whose lanes hold little else: from 2049
 // columns on two slots per lane of more warps, as far as there are any, since the next row's elements
 // take a register each (layer norm of 4000 x 4001: 25 us with four slots of 4 warps, here 20; below,
-// the barriers cost more: 32768 x 1281 54 us with 2 warps, 78 with 4).
+// the barriers cost more: 32768 x 1281 51 us with 2 warps, 78 with 4).
 inline bool scalar_row_shape(int64_t D, RowShape* out) {
     if (!row_shape(D, out)) return false;
     if (out->W <= 2 || D > 32 * 16 * 2 * 8) return true;
