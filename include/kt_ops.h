@@ -160,7 +160,7 @@ typedef struct {
     const void* b_up;       /* [E][F_up], iff bias                                                   */
     const void* b_down;     /* [E][D], iff bias                                                      */
     const void* R;          /* [T][D] contiguous, or NULL: a residual added to the fp32 result       */
-    void* Y;                /* [T][D] contiguous; may be R, or X where ldx = D                       */
+    void* Y;                /* [T][D] contiguous; may be R, or X where ldx = D or T = 1              */
     int32_t* ids;           /* [T][top_k] the chosen experts, best first, or NULL                    */
     float* weights;         /* [T][top_k] their weights, or NULL                                     */
 } kt_moe_tensors;

@@ -277,3 +277,14 @@ def test_the_status_sees_a_replay_that_ran_out_on_another_stream():
     assert plan.status() == kt_mlp.KT_ERR_TIMEOUT
     again, _, _ = run(plan, t)
     assert torch.equal(again, want)
+
+
+def test_one_token_in_place_in_a_wider_row():
+    t = problem(1, 64, 136, 8, 2, "silu", "f16", False, 12)
+    plan = plan_of(1, 64, 136, 8, 2, "silu", "f16", False, True)
+    want, _, _ = run(plan, t, R=t["X"])
+    wide = torch.full((1, 96), 7.0, dtype=torch.float16, device="cuda")
+    wide[:, :64] = t["X"]
+    x = wide[:, :64]
+    got, _, _ = run(plan, {**t, "X": x}, R=x, Y=x)
+    assert torch.equal(got, want) and (wide[:, 64:] == 7).all()

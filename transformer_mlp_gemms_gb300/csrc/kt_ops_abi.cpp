@@ -260,7 +260,7 @@ kt_status kt_moe_run(kt_moe_plan_t plan, const kt_moe_tensors* t, void* stream) 
         !aligned(t->b_up, 16) || !aligned(t->b_down, 16) || !aligned(t->R, 16) || !aligned(t->Y, 16) ||
         !aligned(t->ids, 4) || !aligned(t->weights, 4))
         return bad("device pointers must be 16-byte aligned (ids and weights: 4)");
-    if (t->Y == t->X && t->ldx != plan->o.D) return bad("Y may be X only where ldx = D");
+    if (t->Y == t->X && t->ldx != plan->o.D && t->tokens > 1) return bad("Y may be X only where ldx = D, or for a single token");
     int cur = -1;
     cudaError_t e = cudaGetDevice(&cur);
     if (e != cudaSuccess) return cuda_failed("cudaGetDevice", e);
