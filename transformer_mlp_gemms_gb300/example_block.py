@@ -80,7 +80,8 @@ def quantised_mlp(M=729, D=1152, F=4304, seed=0):
     plan = kt_mlp.Plan(M, D, F, kt_mlp.KT_ACT_GELU_TANH, kt_mlp.KT_F16, False, layernorm=True, ln_eps=EPS,
                        weight_layout=kt_mlp.KT_W_OUT_IN)
     plan.run_ex(x, w_up, w_down, exact, ln_gamma=gamma, ln_beta=beta)
-    torch.cuda.synchronize()
+    if kt_ops.kt_linear_i8_status() != kt_mlp.KT_OK or plan.status() != kt_mlp.KT_OK:  # both wait for the stream
+        raise RuntimeError("an MLP reported " + kt_mlp.kt_last_error())
     return y, exact
 
 
