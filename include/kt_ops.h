@@ -11,7 +11,7 @@
  * They share the library, the status codes, kt_last_error(), the kt_dtype and kt_act values and
  * the [out][in] weight order (KT_W_OUT_IN) of kt_mlp.h.  All pointers are device pointers that
  * the caller owns.  A row pitch ("ld...") counts elements from one row to the next; a row of C
- * columns needs ld >= C.  Every call is asynchronous on `stream` (a cudaStream_t; NULL = the
+ * columns needs ld >= C.  Every call that computes is asynchronous on `stream` (a cudaStream_t; NULL = the
  * legacy default stream) of the current device, may be captured into a CUDA graph, reads its
  * inputs and writes its outputs in stream order only, and returns KT_ERR_INVALID or
  * KT_ERR_UNSUPPORTED before anything is launched where its arguments do not fit.  Results are

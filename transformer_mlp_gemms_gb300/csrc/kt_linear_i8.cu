@@ -164,8 +164,8 @@ __global__ void __launch_bounds__(kDotWarps * 32) kt_linear_i8_dot_kernel(const 
 // in tensor memory are (lane c of a row's four: words 2 c and 2 c + 1 of every eight; the first 16
 // of its 32 bytes in the slot's first half, the others in the second), and the channels follow the
 // same order.
-// Bound by the products for long rows and many tokens: 8192 x 8192 x 8192 takes 637 us, 1.73
-// PFLOP/s (90% of the measured bf16 rate); 16384 x 4304 x 1152 takes 114 us, 1.42 PFLOP/s, where
+// Bound by the products for long rows and many tokens: 8192 x 8192 x 8192 takes 640 us, 1.72
+// PFLOP/s (90% of the measured bf16 rate); 16384 x 4304 x 1152 takes 115 us, 1.41 PFLOP/s, where
 // a tile's 9 steps are followed by the wait for its accumulator.  The steps there, in us: a thread's
 // own row per load (32 wavefronts each) 279, rows shared by four lanes 258, row pointers kept 184,
 // two groups in turn 153, pairs 139, 256 channels with twice the ring 131, all parts staged before
