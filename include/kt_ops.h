@@ -6,7 +6,12 @@
  *   kt_quantize_rows / kt_linear_i8                each token's activations in 8-bit integers,
  *                                                  and the linear layer on 8-bit weights;
  *   kt_moe_plan / kt_moe_run / ...                 a whole mixture-of-experts feed-forward layer
- *                                                  for a few tokens (decoding), router included.
+ *                                                  for a few tokens (decoding), router included;
+ *   kt_glu_forward / kt_glu_backward               the gated up projection (both projections, the
+ *                                                  activation and the product) and its gradients;
+ *   kt_linear_forward / kt_linear_backward         a 16-bit linear layer and its gradients;
+ *   kt_adamw                                       an AdamW step over many tensors at once, moments
+ *                                                  in 32 bits or in 8.
  *
  * They share the library, the status codes, kt_last_error(), the kt_dtype and kt_act values and
  * the [out][in] weight order (KT_W_OUT_IN) of kt_mlp.h.  All pointers are device pointers that
@@ -195,6 +200,121 @@ kt_status kt_moe_debug_stall(kt_moe_plan_t plan, int enable, int64_t limit_us);
 
 /* kt_moe_destroy -- free the plan's workspace (after synchronising its device). */
 kt_status kt_moe_destroy(kt_moe_plan_t plan);
+
+/*
+ * kt_glu_forward -- a gated block's up projection in one kernel: for each token x of X[M][D],
+ *   [value | gate] = x . W^T (+ bias),   h = value * act(gate)
+ *   W: [2F][D], F value rows, then F gate rows; bias: [2F] of dtype or NULL; act: any kt_act but
+ *   KT_ACT_GEGLU (the gate's activation; KT_ACT_NONE: a bilinear unit).
+ *   H: [M][F], pitch ldh.  P: [M][2F], pitch ldp: value and gate, kept for kt_glu_backward; or NULL.
+ * fp32 sums, h from them, and one rounding to dtype of each element of H and P.
+ *   M >= 0 (0: nothing is done); D, F and the pitches multiples of 8, all pointers 16-byte aligned
+ *   (tensor copies); D and F up to 2^24.
+ * Errors: INVALID (NULL or misaligned pointer, negative size, pitch below its row, unknown dtype or act),
+ * UNSUPPORTED (sizes or pitches that are no multiples of 8, or too large; device not sm_103), CUDA.
+ */
+kt_status kt_glu_forward(int64_t M, int64_t D, int64_t F, kt_dtype dtype, kt_act act, const void* X, int64_t ldx,
+                         const void* W, const void* bias, void* H, int64_t ldh, void* P, int64_t ldp, void* stream);
+
+/*
+ * kt_glu_backward -- the gradients of kt_glu_forward from dH and the P that it kept:
+ *   dvalue = dh * act(gate),  dgate = dh * value * act'(gate),   dp = [dvalue | dgate]
+ *   dX = dp . W,   dW = dp^T . X,   db = sum of dp over the tokens
+ * dp is rounded to dtype once, as the products' operand (db is summed before that); fp32 sums, and one rounding
+ * of each element of dX and dW.  An element of dp beyond dtype's range is infinite.
+ *   dX: [M][D], pitch lddx; dW: [2F][D]; db: [2F] fp32; each may be NULL: it is then not computed.
+ *   M = 0 writes zeros to dW and db.
+ *   workspace: kt_glu_backward_workspace(M, D, F) bytes, 16-byte aligned, its content irrelevant before
+ *   and after; two calls that may run at the same time need one each.
+ * Sizes, alignment and errors as kt_glu_forward's, plus INVALID for a workspace that is too small.
+ */
+kt_status kt_glu_backward(int64_t M, int64_t D, int64_t F, kt_dtype dtype, kt_act act, const void* dH, int64_t lddh,
+                          const void* P, int64_t ldp, const void* X, int64_t ldx, const void* W, void* dX, int64_t lddx,
+                          void* dW, float* db, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that kt_glu_backward needs (0 for sizes that it refuses). */
+size_t kt_glu_backward_workspace(int64_t M, int64_t D, int64_t F);
+
+/*
+ * kt_linear_forward -- Y[M][N] = round(X[M][K] . W[N][K]^T (+ bias[N])), fp32 sums.
+ * Sizes, alignment and errors as kt_glu_forward's (N and K in the places of F and D).
+ */
+kt_status kt_linear_forward(int64_t M, int64_t N, int64_t K, kt_dtype dtype, const void* X, int64_t ldx, const void* W,
+                            const void* bias, void* Y, int64_t ldy, void* stream);
+
+/*
+ * kt_linear_backward -- its gradients: dX[M][K] = dY . W, dW[N][K] = dY^T . X, db[N] = sum of dY over the
+ * tokens (fp32); each may be NULL.  M = 0 writes zeros to dW and db.  The workspace
+ * (kt_linear_backward_workspace bytes, 16-byte aligned) is needed with db alone.
+ */
+kt_status kt_linear_backward(int64_t M, int64_t N, int64_t K, kt_dtype dtype, const void* dY, int64_t lddy, const void* X,
+                             int64_t ldx, const void* W, void* dX, int64_t lddx, void* dW, float* db, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that kt_linear_backward needs (0 for sizes that it refuses). */
+size_t kt_linear_backward_workspace(int64_t M, int64_t N, int64_t K);
+
+/*
+ * kt_adamw -- one AdamW step over `count` tensors, a launch for up to 360 of them.  With t the step's number,
+ * for every value, in fp32 and each operation rounded on its own:
+ *   g' = g * *grad_scale (where it is given)
+ *   m = m * b1 + g' * (1 - b1)        v = v * b2 + (g' * (1 - b2)) * g'        r = sqrt(v)
+ *   p = p * (1 - lr * weight_decay) - (m * (lr / (1 - b1^t))) / (r * (1 / sqrt(1 - b2^t)) + eps)
+ * where the constants in brackets are computed in 64 bits and rounded to 32.
+ *   param_dtype, grad_dtype: KT_F16, KT_BF16 or KT_F32, the same for all tensors.  fp32 parameters may have
+ *   16-bit copies (copy_dtype), which receive the new parameters' rounding.
+ *   state_bits 32: m and v are fp32.  8: they are e4m3 with a scale for each KT_ADAMW_BLOCK values of a
+ *   tensor (the last block may be shorter); v then holds r, and m = e4m3 * scale, v = (e4m3 * scale)^2.  A
+ *   block whose largest magnitude is `most` has scale = most / 448 and holds each value times (448 / most), rounded
+ *   to the nearest (a root above zero: to 2^-9 at least); one whose magnitudes are below 2^-100 is held as
+ *   zeros with scale 0.  A NaN makes its block's scale NaN.  Zeros everywhere are the state before the first step.
+ *   step >= 1; or step_device, an int64 on the device that is read when the kernel runs (a captured call then counts
+ *   on); lr and the others are the call's.
+ * Any n >= 0 and any alignment to the elements; tensors whose addresses are 16-byte aligned (8-bit
+ * moments: 8) take wide loads.  Tensors must not overlap one another.
+ * Errors: INVALID (NULL or misaligned pointer, negative n, unknown dtype or bits, a copy without fp32 parameters,
+ * beta outside [0, 1), eps or lr negative or not finite, weight_decay not finite, step below 1), UNSUPPORTED
+ * (device not sm_103), CUDA.
+ */
+#define KT_F32 2
+#define KT_ADAMW_BLOCK 256
+
+typedef struct {
+    void* param;          /* [n] of param_dtype, updated                                            */
+    const void* grad;     /* [n] of grad_dtype                                                      */
+    void* m;              /* [n] fp32 or e4m3, updated                                              */
+    void* v;              /* [n] fp32 or e4m3 (of the root), updated                                */
+    float* m_scale;       /* [ceil(n / KT_ADAMW_BLOCK)] with state_bits = 8, else NULL              */
+    float* v_scale;
+    void* copy;           /* [n] of copy_dtype, or NULL                                             */
+    int64_t n;
+    double weight_decay;
+} kt_adamw_tensor;
+
+typedef struct {
+    int32_t param_dtype, grad_dtype, copy_dtype, state_bits;
+    double lr, beta1, beta2, eps;
+    int64_t step;
+    const int64_t* step_device;  /* or NULL                                                          */
+    const float* grad_scale;     /* on the device, or NULL                                           */
+} kt_adamw_options;
+
+kt_status kt_adamw(int64_t count, const kt_adamw_tensor* tensors, const kt_adamw_options* options, void* stream);
+
+/*
+ * kt_matmul_status -- wait for `stream` and read the current device's error word of the calls on the tensor cores
+ * above (kt_glu_*, kt_linear_forward, kt_linear_backward): KT_ERR_TIMEOUT if a bounded
+ * device-side wait ran out in any of the device's calls since it was last asked (the word is cleared).  Such
+ * a call stores NaN in every element that it could not compute.
+ */
+kt_status kt_matmul_status(void* stream);
+
+/*
+ * kt_matmul_debug_stall -- failure-injection hook for tests, as kt_linear_i8_debug_stall: with enable = 1 the
+ * first block of the following calls' products waits on a barrier nobody signals, bounded as every
+ * other wait then is by `limit_us` microseconds.
+ */
+kt_status kt_matmul_debug_stall(int enable, int64_t limit_us);
 
 #ifdef __cplusplus
 }

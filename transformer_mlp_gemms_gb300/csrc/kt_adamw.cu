@@ -1,0 +1,276 @@
+// kt_adamw.cu -- one AdamW step over many tensors in one launch, moments in fp32 or in 8 bits.
+//
+//   m = b1 m + (1 - b1) g,   v = b2 v + ((1 - b2) g) g,   r = sqrt(v),
+//   p = p (1 - lr wd) - (m (lr / (1 - b1^t))) / (r / sqrt(1 - b2^t) + eps)
+//
+// in fp32 with every operation rounded on its own (no contraction), so that the step is the same bits
+// whatever carries it out.  8-bit moments are e4m3 with a scale for each 256 values of a tensor: m, and r
+// in the place of v, whose square would have twice the range; a root above zero is held as 2^-9 of its scale
+// at least, since the step divides by it.
+//
+// Bound by memory: 28 bytes per value with fp32 parameters, bf16 gradients and copies and fp32 moments, 10
+// with 16-bit parameters and 8-bit moments; about 50 instructions a value.  A warp takes 256 values at a time
+// (a scale's block), eight consecutive ones per lane, and holds them in registers throughout: their
+// largest magnitude is one warp reduction.  The tensors' addresses come as the launch's parameters, so no
+// table is kept on the device, and a captured call carries its own.  A block takes a run of
+// consecutive chunks, across tensors' ends.
+#include <cuda_fp8.h>
+
+#include "kt_ops_internal.h"
+#include "kt_gemm.cuh"
+
+namespace kt {
+namespace {
+
+constexpr int kAdBlock = 256, kAdWarps = 8, kAdChunk = kAdBlock * kAdWarps;  // values of a scale, of a thread block's round
+
+template <int N>
+struct AdTable {
+    AdamwEntry e[N];
+    int count;
+    int64_t chunks;
+    AdamwStep s;
+};
+
+// eight values as fp32, from consecutive elements or (STRIDED) from every 32nd, those past the end as zeros
+template <int T, bool STRIDED>
+__device__ __forceinline__ void ad_load(const void* at, int64_t i, int left, float* f) {
+    if constexpr (!STRIDED) {
+        if constexpr (T == KT_F32) {
+            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(at) + i);
+            const float4 a = p[0], b = p[1];
+            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+        } else {
+            unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(at) + i), f);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            f[e] = 0.0f;
+            if (32 * e < left) {
+                if constexpr (T == KT_F32) {
+                    f[e] = static_cast<const float*>(at)[i + 32 * e];
+                } else {
+                    float t[8];
+                    unpack8<T>(make_uint4(static_cast<const uint16_t*>(at)[i + 32 * e], 0u, 0u, 0u), t);
+                    f[e] = t[0];
+                }
+            }
+        }
+    }
+}
+template <int T, bool STRIDED>
+__device__ __forceinline__ void ad_store(void* at, int64_t i, int left, const float* f) {
+    if constexpr (!STRIDED) {
+        if constexpr (T == KT_F32) {
+            float4* p = reinterpret_cast<float4*>(static_cast<float*>(at) + i);
+            p[0] = make_float4(f[0], f[1], f[2], f[3]);
+            p[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(at) + i) =
+                make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (32 * e < left) {
+                if constexpr (T == KT_F32) static_cast<float*>(at)[i + 32 * e] = f[e];
+                else static_cast<uint16_t*>(at)[i + 32 * e] = (uint16_t)(pack2<T>(f[e], 0.0f) & 0xffffu);
+            }
+    }
+}
+
+// eight e4m3 values
+template <bool STRIDED>
+__device__ __forceinline__ void ad_load8(const void* at, int64_t i, int left, float* f) {
+    if constexpr (!STRIDED) {
+        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(at) + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t u = j < 2 ? w.x : w.y;
+            const float2 t = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u >> (16 * (j & 1))), __NV_E4M3)));
+            f[2 * j] = t.x;
+            f[2 * j + 1] = t.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            f[e] = 0.0f;
+            if (32 * e < left) f[e] = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(at)[i + 32 * e], __NV_E4M3)));
+        }
+    }
+}
+
+// Eight values of this lane (32 lanes: a block of 256) in e4m3: the scale, most / 448, and each value times
+// 448 / most, rounded to the nearest.  A block with no magnitude of 2^-100 or more is held as zeros (the
+// quotient would overflow).  A NaN is the largest as bits, and makes the scale a NaN.
+template <bool ROOT, bool STRIDED>
+__device__ __forceinline__ void ad_store8(void* at, float* scale, int64_t i, int left, int lane, const float* f) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(f[e]) & 0x7fffffffu);
+    const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, most));
+    const bool zero = top < 0x1p-100f;
+    const float inverse = zero ? 0.0f : __fdiv_rn(448.0f, top);
+    if (lane == 0) *scale = zero ? 0.0f : __fdiv_rn(top, 448.0f);
+    float q[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        q[e] = __fmul_rn(f[e], inverse);
+        if (ROOT && q[e] > 0.0f) q[e] = fmaxf(q[e], 0x1p-9f);
+    }
+    if constexpr (!STRIDED) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * j], q[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(at) + i) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (32 * e < left) static_cast<uint8_t*>(at)[i + 32 * e] = __nv_cvt_float_to_fp8(q[e], __NV_SATFINITE, __NV_E4M3);
+    }
+}
+
+// The step of 256 values of one tensor, from `at` on.
+template <int PT, int GT, bool BITS8, bool STRIDED>
+__device__ __forceinline__ void ad_block(const AdamwEntry& t, const AdamwStep& s, int64_t at, int lane, float rate, float root, float scale) {
+    const int64_t i = at + (STRIDED ? lane : 8 * lane);
+    const int left = STRIDED ? (int)min((int64_t)kAdBlock, t.n - at) - lane : 256;
+    float p[8], g[8], m[8], v[8], sm = 0.0f, sv = 0.0f;
+    ad_load<GT, STRIDED>(t.g, i, left, g);
+    if constexpr (BITS8) {
+        ad_load8<STRIDED>(t.m, i, left, m);
+        ad_load8<STRIDED>(t.v, i, left, v);
+        sm = t.ms[at / kAdBlock];
+        sv = t.vs[at / kAdBlock];
+    } else {
+        ad_load<KT_F32, STRIDED>(t.m, i, left, m);
+        ad_load<KT_F32, STRIDED>(t.v, i, left, v);
+    }
+    ad_load<PT, STRIDED>(t.p, i, left, p);
+    float r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if constexpr (BITS8) {
+            m[e] = __fmul_rn(m[e], sm);
+            v[e] = __fmul_rn(v[e], sv);
+            v[e] = __fmul_rn(v[e], v[e]);
+        }
+        if (s.grad_scale) g[e] = __fmul_rn(g[e], scale);
+        m[e] = __fadd_rn(__fmul_rn(m[e], s.b1), __fmul_rn(g[e], s.c1));
+        v[e] = __fadd_rn(__fmul_rn(v[e], s.b2), __fmul_rn(__fmul_rn(g[e], s.c2), g[e]));
+        r[e] = __fsqrt_rn(v[e]);
+        p[e] = __fsub_rn(__fmul_rn(p[e], t.keep), __fdiv_rn(__fmul_rn(m[e], rate), __fadd_rn(__fmul_rn(r[e], root), s.eps)));
+    }
+    ad_store<PT, STRIDED>(t.p, i, left, p);
+    if (PT == KT_F32 && t.copy) {
+        if (s.copy_dtype == KT_BF16) ad_store<KT_BF16, STRIDED>(t.copy, i, left, p);
+        else ad_store<KT_F16, STRIDED>(t.copy, i, left, p);
+    }
+    if constexpr (BITS8) {
+        if constexpr (STRIDED) {  // what is past the end has no part in the scale (its r would be the root of zero)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (32 * e >= left) m[e] = r[e] = 0.0f;
+        }
+        ad_store8<false, STRIDED>(t.m, t.ms + at / kAdBlock, i, left, lane, m);
+        ad_store8<true, STRIDED>(t.v, t.vs + at / kAdBlock, i, left, lane, r);
+    } else {
+        ad_store<KT_F32, STRIDED>(t.m, i, left, m);
+        ad_store<KT_F32, STRIDED>(t.v, i, left, v);
+    }
+}
+
+template <int PT, int GT, bool BITS8, int N>
+__global__ void __launch_bounds__(kAdWarps * 32) kt_adamw_kernel(const __grid_constant__ AdTable<N> tab) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const AdamwStep& s = tab.s;
+    float rate = s.rate, root = s.root;
+    if (s.step) {  // the step's number is on the device
+        __shared__ float on_device[2];
+        if (threadIdx.x == 0) {
+            const double t = (double)*s.step;
+            on_device[0] = (float)(s.lr / (1.0 - pow(s.beta1, t)));
+            on_device[1] = (float)(1.0 / sqrt(1.0 - pow(s.beta2, t)));
+        }
+        __syncthreads();
+        rate = on_device[0];
+        root = on_device[1];
+    }
+    const float scale = s.grad_scale ? *s.grad_scale : 1.0f;
+    int64_t c = tab.chunks * blockIdx.x / gridDim.x;
+    const int64_t end = tab.chunks * (blockIdx.x + 1) / gridDim.x;
+    if (c >= end) return;
+    int t = 0;
+    for (int hi = tab.count; hi - t > 1;) {  // the last tensor whose first chunk is at or before c
+        const int mid = (t + hi) >> 1;
+        if (tab.e[mid].first <= c) t = mid;
+        else hi = mid;
+    }
+    for (; c < end; ++c) {
+        while (t + 1 < tab.count && tab.e[t + 1].first <= c) ++t;
+        const AdamwEntry& e = tab.e[t];
+        const int64_t at = (c - e.first) * kAdChunk + warp * kAdBlock;
+        if (at >= e.n) continue;
+        if (e.wide && at + kAdBlock <= e.n) ad_block<PT, GT, BITS8, false>(e, s, at, lane, rate, root, scale);
+        else ad_block<PT, GT, BITS8, true>(e, s, at, lane, rate, root, scale);
+    }
+}
+
+template <int PT, int GT, bool BITS8, int N>
+cudaError_t ad_launch(const AdamwEntry* e, int count, const AdamwStep& s, int sms, void* stream) {
+    AdTable<N> tab;
+    int64_t chunks = 0;
+    for (int i = 0; i < count; ++i) {
+        tab.e[i] = e[i];
+        tab.e[i].first = chunks;
+        chunks += (e[i].n + kAdChunk - 1) / kAdChunk;
+    }
+    tab.count = count;
+    tab.chunks = chunks;
+    tab.s = s;
+    if (chunks == 0) return cudaSuccess;
+    const unsigned grid = (unsigned)std::min<int64_t>(chunks, (int64_t)sms * 8);
+    return launch_pdl(kt_adamw_kernel<PT, GT, BITS8, N>, grid, (unsigned)(kAdWarps * 32), (size_t)0, stream, tab);
+}
+
+constexpr int kAdFew = 24, kAdMany = 360;
+static_assert(sizeof(AdTable<kAdMany>) <= 32764, "a launch's parameters");
+
+template <int PT, int GT, bool BITS8>
+cudaError_t ad_all(const AdamwEntry* e, int count, const AdamwStep& s, int sms, void* stream) {
+    for (int at = 0; at < count; at += kAdMany) {
+        const int n = std::min(count - at, kAdMany);
+        const cudaError_t r = n <= kAdFew ? ad_launch<PT, GT, BITS8, kAdFew>(e + at, n, s, sms, stream)
+                                          : ad_launch<PT, GT, BITS8, kAdMany>(e + at, n, s, sms, stream);
+        if (r != cudaSuccess) return r;
+    }
+    return cudaSuccess;
+}
+
+template <int PT, int GT>
+cudaError_t ad_bits(const AdamwEntry* e, int count, const AdamwStep& s, int sms, void* stream) {
+    return s.bits == 8 ? ad_all<PT, GT, true>(e, count, s, sms, stream) : ad_all<PT, GT, false>(e, count, s, sms, stream);
+}
+template <int PT>
+cudaError_t ad_grads(const AdamwEntry* e, int count, const AdamwStep& s, int sms, void* stream) {
+    if (s.grad_dtype == KT_F32) return ad_bits<PT, KT_F32>(e, count, s, sms, stream);
+    return s.grad_dtype == KT_BF16 ? ad_bits<PT, KT_BF16>(e, count, s, sms, stream) : ad_bits<PT, KT_F16>(e, count, s, sms, stream);
+}
+
+}  // namespace
+
+kt_status launch_adamw(const AdamwEntry* e, int count, const AdamwStep& s, int sms, void* stream, const char** why) {
+    const cudaError_t r = s.param_dtype == KT_F32    ? ad_grads<KT_F32>(e, count, s, sms, stream)
+                          : s.param_dtype == KT_BF16 ? ad_grads<KT_BF16>(e, count, s, sms, stream)
+                                                     : ad_grads<KT_F16>(e, count, s, sms, stream);
+    if (r != cudaSuccess) {
+        *why = cudaGetErrorString(r);
+        return KT_ERR_CUDA;
+    }
+    return KT_OK;
+}
+
+}  // namespace kt

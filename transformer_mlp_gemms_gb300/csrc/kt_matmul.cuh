@@ -1,0 +1,59 @@
+// kt_matmul.cuh -- what the products of kt_matmul.cu and kt_linear_fp8.cu share.
+#pragma once
+#include "kt_gemm.cuh"
+
+namespace kt {
+
+constexpr int kBand = 8;  // tile rows of a band
+
+// The t-th tile: bands of kBand tile rows, in each column after column.
+__device__ __forceinline__ void band_tile(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
+    const int per = kBand * tiles_n, band = t / per, in = t - band * per;
+    const int rows = min(kBand, tiles_m - band * kBand);
+    tn = in / rows;
+    tm = band * kBand + in - tn * rows;
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+// Four fp32 sums of a CTA of this cluster.
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// 32 bias values from column `col` on, zeros in groups of 8 at or past `limit`.  Ordinary loads: the kernel
+// before this one may still be writing a bias while this one is already resident.
+template <int DT>
+__device__ __forceinline__ void bias32(const void* bias, int col, int limit, float* b) {
+    const uint16_t* at = static_cast<const uint16_t*>(bias) + col;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (col + 8 * g < limit) w = *reinterpret_cast<const uint4*>(at + 8 * g);
+        unpack8<DT>(w, b + 8 * g);
+    }
+}
+
+// The current device's error word once `stream` is done, cleared if it was set.
+template <typename Symbol>
+kt_status error_word(const Symbol& symbol, void* stream, int* word, const char** why) {
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemcpyFromSymbolAsync(word, symbol, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess && *word != 0) {
+        const int none = 0;
+        e = cudaMemcpyToSymbolAsync(symbol, &none, sizeof(int), 0, cudaMemcpyHostToDevice, st);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    }
+    if (e == cudaSuccess) return KT_OK;
+    *why = cudaGetErrorString(e);
+    return KT_ERR_CUDA;
+}
+
+}  // namespace kt

@@ -7,6 +7,7 @@
 #include <cstdio>
 #include <cstring>
 #include <new>
+#include <vector>
 
 #include "kt_ops_internal.h"
 
@@ -52,6 +53,7 @@ kt_status current_device(int* device, int* sms) {
 constexpr unsigned long long kWaitLimitNs = 4000000000ull;  // 4 s: far beyond any legitimate wait
 constexpr int64_t kMostStallUs = 10000000;
 std::atomic<int64_t> g_linear_stall_us{0};  // kt_linear_i8_debug_stall's limit; 0: off
+std::atomic<int64_t> g_matmul_stall_us{0};  // kt_matmul_debug_stall's
 
 kt_status done(kt_status s, const char* why) { return kt::report(s, s == KT_OK ? "" : why); }
 
@@ -63,6 +65,68 @@ kt_status check_rows(int64_t M, int64_t D, int dtype) {
     if (D > KT_LAYERNORM_MAX_D) return kt::report(KT_ERR_UNSUPPORTED, "rows longer than KT_LAYERNORM_MAX_D");
     return KT_OK;
 }
+
+// The products of kt_matmul.cu: sizes, and what a tensor copy needs of a matrix.
+kt_status check_product(int64_t M, int64_t D, int64_t F, int dtype) {
+    if (M < 0 || D < 1 || F < 1) return bad("the row count must not be negative and the other sizes at least 1");
+    if (!known_dtype(dtype)) return bad("unknown dtype");
+    if (D % 8 || F % 8) return kt::report(KT_ERR_UNSUPPORTED, "row lengths must be multiples of 8");
+    if (M > INT32_MAX / 2 || D > (1 << 24) || F > (1 << 24)) return kt::report(KT_ERR_UNSUPPORTED, "M above 2^30 or a row length above 2^24");
+    return KT_OK;
+}
+kt_status check_matrix(const void* p, int64_t ld, int64_t cols) {
+    if (!aligned(p, 16)) return bad("device pointers must be 16-byte aligned");
+    if (ld < cols) return bad("a row pitch is below the row length");
+    if (ld % 8) return kt::report(KT_ERR_UNSUPPORTED, "row pitches must be multiples of 8");
+    if (ld > (int64_t)1 << 38) return kt::report(KT_ERR_UNSUPPORTED, "a row pitch above 2^38");
+    return KT_OK;
+}
+kt::Matmul product(int64_t M, int64_t N, int64_t K) {
+    kt::Matmul a = {};
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.stall_ns = 1000ull * (unsigned long long)g_matmul_stall_us.load(std::memory_order_relaxed);
+    a.wait_limit_ns = a.stall_ns ? a.stall_ns : kWaitLimitNs;
+    return a;
+}
+// What dX = dP . W and dW = dP^T . X have in common, for dP [M][N], W [N][K], X [M][K].
+kt_status gradients(int64_t M, int64_t N, int64_t K, int dtype, const void* dP, int64_t lddp, const void* X, int64_t ldx, const void* W,
+                    void* dX, int64_t lddx, void* dW, int sms, int device, void* stream) {
+    const char* why = "";
+    kt_status s = KT_OK;
+    if (dW) {
+        kt::Matmul a = product(N, K, M);
+        a.A = dP;
+        a.lda = lddp;
+        a.a_mn = true;
+        a.B = X;
+        a.ldb = ldx;
+        a.b_mn = true;
+        a.C = dW;
+        a.ldc = K;
+        s = kt::launch_matmul(dtype, a, sms, device, stream, &why);
+    }
+    if (s == KT_OK && dX) {
+        kt::Matmul a = product(M, K, N);
+        a.A = dP;
+        a.lda = lddp;
+        a.B = W;
+        a.ldb = K;
+        a.b_mn = true;
+        a.C = dX;
+        a.ldc = lddx;
+        s = kt::launch_matmul(dtype, a, sms, device, stream, &why);
+    }
+    return done(s, why);
+}
+kt_status zeros(void* p, size_t bytes, void* stream) {
+    if (!p || !bytes) return KT_OK;
+    const cudaError_t e = cudaMemsetAsync(p, 0, bytes, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KT_OK : cuda_failed("cudaMemsetAsync", e);
+}
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+int epilogue_of(int act) { return kt::up_epilogue(act); }
 
 }  // namespace
 
@@ -317,6 +381,228 @@ kt_status kt_moe_destroy(kt_moe_plan_t plan) {
         cudaFree(plan->workspace);
     }
     delete plan;
+    return done(KT_OK, "");
+}
+
+kt_status kt_glu_forward(int64_t M, int64_t D, int64_t F, kt_dtype dtype, kt_act act, const void* X, int64_t ldx,
+                         const void* W, const void* bias, void* H, int64_t ldh, void* P, int64_t ldp, void* stream) {
+    kt_status s = check_product(M, D, F, dtype);
+    if (s != KT_OK) return s;
+    if (!known_act(act) || act == KT_ACT_GEGLU) return bad("unknown activation of the gate");
+    if ((M > 0 && (!X || !H)) || !W) return bad("X, W and H must be non-NULL");
+    if ((s = check_matrix(X, ldx, D)) != KT_OK || (s = check_matrix(W, D, D)) != KT_OK || (s = check_matrix(H, ldh, F)) != KT_OK) return s;
+    if (P && (s = check_matrix(P, ldp, 2 * F)) != KT_OK) return s;
+    if (!aligned(bias, 16)) return bad("device pointers must be 16-byte aligned");
+    if (M == 0) return done(KT_OK, "");
+    int dev, sms;
+    if ((s = current_device(&dev, &sms)) != KT_OK) return s;
+    kt::Matmul a = product(M, F, D);
+    a.gated = true;
+    a.act = epilogue_of(act);
+    a.A = X;
+    a.lda = ldx;
+    a.B = W;
+    a.ldb = D;
+    a.bias = bias;
+    a.C = H;
+    a.ldc = ldh;
+    a.P = P;
+    a.ldp = ldp;
+    const char* why = "";
+    return done(kt::launch_matmul(dtype, a, sms, dev, stream, &why), why);
+}
+
+size_t kt_glu_backward_workspace(int64_t M, int64_t D, int64_t F) {
+    if (M < 0 || M > INT32_MAX / 2 || D < 8 || D % 8 || D > (1 << 24) || F < 8 || F % 8 || F > (1 << 24)) return 0;
+    return up256((size_t)(M ? M : 1) * 4 * (size_t)F) + (size_t)kt::column_sum_rows(M, F) * 2 * (size_t)F * sizeof(float);
+}
+
+kt_status kt_glu_backward(int64_t M, int64_t D, int64_t F, kt_dtype dtype, kt_act act, const void* dH, int64_t lddh,
+                          const void* P, int64_t ldp, const void* X, int64_t ldx, const void* W, void* dX, int64_t lddx,
+                          void* dW, float* db, void* workspace, size_t workspace_bytes, void* stream) {
+    kt_status s = check_product(M, D, F, dtype);
+    if (s != KT_OK) return s;
+    if (!known_act(act) || act == KT_ACT_GEGLU) return bad("unknown activation of the gate");
+    if ((M > 0 && (!dH || !P || !X)) || !W) return bad("dH, P, X and W must be non-NULL");
+    if ((s = check_matrix(dH, lddh, F)) != KT_OK || (s = check_matrix(P, ldp, 2 * F)) != KT_OK ||
+        (s = check_matrix(X, ldx, D)) != KT_OK || (s = check_matrix(W, D, D)) != KT_OK || (s = check_matrix(dW, D, D)) != KT_OK)
+        return s;
+    if (dX && (s = check_matrix(dX, lddx, D)) != KT_OK) return s;
+    if (!aligned(db, 4) || !aligned(workspace, 16)) return bad("db must be aligned to its elements and the workspace to 16 bytes");
+    if (!workspace || workspace_bytes < kt_glu_backward_workspace(M, D, F))
+        return bad("the workspace is smaller than kt_glu_backward_workspace says");
+    int dev, sms;
+    if ((s = current_device(&dev, &sms)) != KT_OK) return s;
+    if (M == 0) {
+        if ((s = zeros(dW, (size_t)4 * F * D, stream)) != KT_OK || (s = zeros(db, (size_t)8 * F, stream)) != KT_OK) return s;
+        return done(KT_OK, "");
+    }
+    const char* why = "";
+    kt::GluBackward g = {};
+    g.dH = dH;
+    g.lddh = lddh;
+    g.P = P;
+    g.ldp = ldp;
+    g.dP = workspace;
+    g.partials = db ? reinterpret_cast<float*>(static_cast<char*>(workspace) + up256((size_t)M * 4 * (size_t)F)) : nullptr;
+    g.db = db;
+    g.M = (int)M;
+    g.F = (int)F;
+    g.act = epilogue_of(act);
+    if ((s = kt::launch_glu_backward(dtype, g, stream, &why)) != KT_OK) return kt::report(s, why);
+    return gradients(M, 2 * F, D, dtype, workspace, 2 * F, X, ldx, W, dX, lddx, dW, sms, dev, stream);
+}
+
+kt_status kt_linear_forward(int64_t M, int64_t N, int64_t K, kt_dtype dtype, const void* X, int64_t ldx, const void* W,
+                            const void* bias, void* Y, int64_t ldy, void* stream) {
+    kt_status s = check_product(M, K, N, dtype);
+    if (s != KT_OK) return s;
+    if ((M > 0 && (!X || !Y)) || !W) return bad("X, W and Y must be non-NULL");
+    if ((s = check_matrix(X, ldx, K)) != KT_OK || (s = check_matrix(W, K, K)) != KT_OK || (s = check_matrix(Y, ldy, N)) != KT_OK) return s;
+    if (!aligned(bias, 16)) return bad("device pointers must be 16-byte aligned");
+    if (M == 0) return done(KT_OK, "");
+    int dev, sms;
+    if ((s = current_device(&dev, &sms)) != KT_OK) return s;
+    kt::Matmul a = product(M, N, K);
+    a.A = X;
+    a.lda = ldx;
+    a.B = W;
+    a.ldb = K;
+    a.bias = bias;
+    a.C = Y;
+    a.ldc = ldy;
+    const char* why = "";
+    return done(kt::launch_matmul(dtype, a, sms, dev, stream, &why), why);
+}
+
+size_t kt_linear_backward_workspace(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || M > INT32_MAX / 2 || N < 8 || N % 8 || N > (1 << 24) || K < 8 || K % 8 || K > (1 << 24)) return 0;
+    return (size_t)kt::column_sum_rows(M, N) * (size_t)N * sizeof(float);
+}
+
+kt_status kt_linear_backward(int64_t M, int64_t N, int64_t K, kt_dtype dtype, const void* dY, int64_t lddy, const void* X,
+                             int64_t ldx, const void* W, void* dX, int64_t lddx, void* dW, float* db, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+    kt_status s = check_product(M, K, N, dtype);
+    if (s != KT_OK) return s;
+    if ((M > 0 && (!dY || !X)) || !W) return bad("dY, X and W must be non-NULL");
+    if ((s = check_matrix(dY, lddy, N)) != KT_OK || (s = check_matrix(X, ldx, K)) != KT_OK || (s = check_matrix(W, K, K)) != KT_OK ||
+        (s = check_matrix(dW, K, K)) != KT_OK)
+        return s;
+    if (dX && (s = check_matrix(dX, lddx, K)) != KT_OK) return s;
+    if (!aligned(db, 4) || !aligned(workspace, 16)) return bad("db must be aligned to its elements and the workspace to 16 bytes");
+    if (db && (!workspace || workspace_bytes < kt_linear_backward_workspace(M, N, K)))
+        return bad("the workspace is smaller than kt_linear_backward_workspace says");
+    int dev, sms;
+    if ((s = current_device(&dev, &sms)) != KT_OK) return s;
+    if (M == 0) {
+        if ((s = zeros(dW, (size_t)2 * N * K, stream)) != KT_OK || (s = zeros(db, (size_t)4 * N, stream)) != KT_OK) return s;
+        return done(KT_OK, "");
+    }
+    if (db) {
+        const char* why = "";
+        kt::GluBackward g = {};
+        g.dH = dY;
+        g.lddh = lddy;
+        g.partials = static_cast<float*>(workspace);
+        g.db = db;
+        g.M = (int)M;
+        g.F = (int)N;
+        if ((s = kt::launch_glu_backward(dtype, g, stream, &why)) != KT_OK) return kt::report(s, why);
+    }
+    return gradients(M, N, K, dtype, dY, lddy, X, ldx, W, dX, lddx, dW, sms, dev, stream);
+}
+
+kt_status kt_adamw(int64_t count, const kt_adamw_tensor* tensors, const kt_adamw_options* o, void* stream) {
+    if (count < 0 || count > INT32_MAX || (count > 0 && !tensors) || !o) return bad("a negative count, or no tensors or options");
+    auto known = [](int d) { return known_dtype(d) || d == KT_F32; };
+    if (!known(o->param_dtype) || !known(o->grad_dtype)) return bad("unknown dtype");
+    if (o->state_bits != 8 && o->state_bits != 32) return bad("state_bits must be 8 or 32");
+    auto beta = [](double b) { return b >= 0.0 && b < 1.0; };
+    auto size = [](double x) { return x >= 0.0 && x < 3.0e38; };
+    if (!beta(o->beta1) || !beta(o->beta2)) return bad("beta1 and beta2 must be in [0, 1)");
+    if (!size(o->lr) || !size(o->eps)) return bad("lr and eps must be finite and not negative");
+    if (!o->step_device && o->step < 1) return bad("step must be at least 1");
+    if (!aligned(o->step_device, 8) || !aligned(o->grad_scale, 4)) return bad("a pointer is not aligned to its elements");
+    const size_t pb = o->param_dtype == KT_F32 ? 4 : 2, gb = o->grad_dtype == KT_F32 ? 4 : 2, sb = o->state_bits == 8 ? 1 : 4;
+    kt::AdamwEntry few[64];
+    std::vector<kt::AdamwEntry> many;
+    kt::AdamwEntry* e = few;
+    if (count > 64) {
+        try {
+            many.resize((size_t)count);
+        } catch (...) {
+            return kt::report(KT_ERR_NOMEM, "host allocation failed");
+        }
+        e = many.data();
+    }
+    int live = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const kt_adamw_tensor& t = tensors[i];
+        if (t.n < 0 || t.n > (int64_t)1 << 48) return bad("a tensor's length is negative or above 2^48");
+        if (!(std::fabs(t.weight_decay) < 3.0e38)) return bad("weight_decay must be finite");
+        if (t.copy && (o->param_dtype != KT_F32 || !known_dtype(o->copy_dtype))) return bad("a 16-bit copy goes with fp32 parameters");
+        if (t.n == 0) continue;
+        if (!t.param || !t.grad || !t.m || !t.v) return bad("param, grad, m and v must be non-NULL");
+        if (o->state_bits == 8 && (!t.m_scale || !t.v_scale)) return bad("8-bit moments need their scales");
+        if (!aligned(t.param, pb) || !aligned(t.grad, gb) || !aligned(t.m, sb) || !aligned(t.v, sb) || !aligned(t.m_scale, 4) ||
+            !aligned(t.v_scale, 4) || !aligned(t.copy, 2))
+            return bad("a pointer is not aligned to its elements");
+        kt::AdamwEntry& x = e[live++];
+        x.p = t.param;
+        x.g = t.grad;
+        x.m = t.m;
+        x.v = t.v;
+        x.ms = t.m_scale;
+        x.vs = t.v_scale;
+        x.copy = t.copy;
+        x.n = t.n;
+        x.first = 0;
+        x.keep = (float)(1.0 - o->lr * t.weight_decay);
+        const size_t state = o->state_bits == 8 ? 8 : 16;
+        x.wide = aligned(t.param, 16) && aligned(t.grad, 16) && aligned(t.m, state) && aligned(t.v, state) && aligned(t.copy, 16);
+    }
+    if (!live) return done(KT_OK, "");
+    kt_status s;
+    int dev, sms;
+    if ((s = current_device(&dev, &sms)) != KT_OK) return s;
+    kt::AdamwStep a = {};
+    a.param_dtype = o->param_dtype;
+    a.grad_dtype = o->grad_dtype;
+    a.copy_dtype = o->copy_dtype;
+    a.bits = o->state_bits;
+    a.b1 = (float)o->beta1;
+    a.c1 = (float)(1.0 - o->beta1);
+    a.b2 = (float)o->beta2;
+    a.c2 = (float)(1.0 - o->beta2);
+    a.eps = (float)o->eps;
+    a.lr = o->lr;
+    a.beta1 = o->beta1;
+    a.beta2 = o->beta2;
+    if (!o->step_device) {
+        a.rate = (float)(o->lr / (1.0 - std::pow(o->beta1, (double)o->step)));
+        a.root = (float)(1.0 / std::sqrt(1.0 - std::pow(o->beta2, (double)o->step)));
+    }
+    a.step = o->step_device;
+    a.grad_scale = o->grad_scale;
+    const char* why = "";
+    return done(kt::launch_adamw(e, live, a, sms, stream, &why), why);
+}
+
+kt_status kt_matmul_status(void* stream) {
+    int dev, sms, word = 0;
+    kt_status s;
+    if ((s = current_device(&dev, &sms)) != KT_OK) return s;
+    const char* why = "";
+    if ((s = kt::matmul_status(stream, &word, &why)) != KT_OK) return kt::report(s, why);
+    if (word == 0) return done(KT_OK, "");
+    return kt::report(KT_ERR_TIMEOUT, word == kt::DEV_INJECTED_STALL ? "a bounded device wait ran out (injected stall)"
+                                                                     : "a bounded device wait ran out");
+}
+
+kt_status kt_matmul_debug_stall(int enable, int64_t limit_us) {
+    if (enable && (limit_us < 1 || limit_us > kMostStallUs)) return bad("limit_us must be in [1, 10 000 000]");
+    g_matmul_stall_us.store(enable ? limit_us : 0, std::memory_order_relaxed);
     return done(KT_OK, "");
 }
 

@@ -90,6 +90,60 @@ size_t moe_workspace(int64_t T, int64_t D, int64_t F, int64_t top_k);
 void moe_carve(MoeParams* p, int64_t max_tokens, void* workspace);
 kt_status launch_moe(int act, int dtype, const MoeParams& p, int sms, int device, void* stream, const char** why);
 
+// Products of 16-bit matrices (kt_matmul.cu): C[M][N] = round(A . B^T (+ bias)).
+struct Matmul {
+    const void* A;        // [M][K] or, a_mn, [K][M]; pitch lda
+    const void* B;        // [N][K] or, b_mn, [K][N]; pitch ldb.  gated: [2N][K], value rows, then gate rows
+    void* C;              // [M][N], pitch ldc.  gated: value * act(gate)
+    const void* bias;     // [N] (gated: [2N]) or null
+    void* P;              // gated: [M][2N], value and gate, pitch ldp; or null
+    int64_t lda, ldb, ldc, ldp;
+    int M, N, K, act;     // act: gated, an Epi
+    bool a_mn, b_mn, gated;
+    unsigned long long wait_limit_ns, stall_ns;
+};
+// How a product is run: CTAs per tile, accumulator columns per tile, CTAs that share a tile's sums.
+struct MatmulShape {
+    int pair, BN, splits;
+};
+MatmulShape matmul_shape(const Matmul& a, int sms, int device);
+kt_status launch_matmul_as(int dtype, const Matmul& a, const MatmulShape& s, int sms, int device, void* stream, const char** why);
+kt_status launch_matmul(int dtype, const Matmul& a, int sms, int device, void* stream, const char** why);
+kt_status matmul_status(void* stream, int* word, const char** why);
+
+// The elementwise part of the backward pass of a gated block, and column sums (kt_glu.cu).
+struct GluBackward {
+    const void *dH, *P;  // dH: [M][F]; P: [M][2F]; null P: column sums of dH alone
+    void* dP;            // [M][2F] contiguous
+    float* partials;     // [column_sum_rows][2F] (F without P), or null: no sums
+    float* db;           // [2F] (F)
+    int64_t lddh, ldp;
+    int M, F, act;       // act: an Epi
+};
+int column_sum_rows(int64_t M, int64_t F);
+kt_status launch_glu_backward(int dtype, const GluBackward& p, void* stream, const char** why);
+
+// AdamW over many tensors (kt_adamw.cu).
+struct AdamwEntry {
+    void* p;
+    const void* g;
+    void *m, *v;
+    float *ms, *vs;  // 8-bit moments: their scales
+    void* copy;      // 16-bit copy of fp32 parameters, or null
+    int64_t n;
+    int64_t first;   // the launch's: the tensor's first chunk
+    float keep;      // 1 - lr * weight decay
+    int wide;        // every address allows its vector loads
+};
+struct AdamwStep {
+    int param_dtype, grad_dtype, copy_dtype, bits;
+    float b1, c1, b2, c2, eps, rate, root;  // c = 1 - b; rate = lr / (1 - beta1^t), root = 1 / sqrt(1 - beta2^t)
+    double lr, beta1, beta2;                // for a step number on the device
+    const int64_t* step;                    // it, or null
+    const float* grad_scale;                // or null
+};
+kt_status launch_adamw(const AdamwEntry* e, int count, const AdamwStep& s, int sms, void* stream, const char** why);
+
 // Opt a kernel in to `bytes` of dynamic shared memory on the current device, once per device: the
 // attribute stays.  `done` belongs to the kernel (a static of its launch function).
 struct SmemOptIn {

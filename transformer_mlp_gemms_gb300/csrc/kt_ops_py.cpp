@@ -18,6 +18,7 @@
 #include <algorithm>
 #include <cstdio>
 #include <string>
+#include <vector>
 
 #include "kt_ops.h"
 
@@ -244,12 +245,199 @@ PyObject* moe_run(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// glu_forward(X, W, bias, H, P, act, stream)
+PyObject* glu_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 7, [&] {
+        const at::Tensor &X = matrix(a[0], "X"), &H = matrix(a[3], "H");
+        const int64_t M = X.size(0), D = X.size(1), F = H.size(1), act = integer(a[5], "act");
+        const c10::Device dev = X.device();
+        const at::ScalarType dt = X.scalar_type();
+        const kt_dtype c = code(X, "X");
+        const Rows x = rows(X, "X", M, D, dt, dev, 8), h = rows(H, "H", M, F, dt, dev, 8);
+        Rows p = {nullptr, 0};
+        if (a[4] != Py_None) p = rows(tensor(a[4], "P"), "P", M, 2 * F, dt, dev, 8);
+        if (a[1] == Py_None) refuse("W", "a torch tensor expected");
+        void* W = whole(a[1], "W", {2 * F, D}, dt, dev);
+        void* b = whole(a[2], "bias", {2 * F}, dt, dev);
+        void* s = stream_of(a[6], dev);
+        return kt_glu_forward(M, D, F, c, (kt_act)act, x.p, x.ld, W, b, h.p, h.ld, p.p, p.ld, s);
+    });
+}
+
+// A workspace's address and size.
+struct Space {
+    void* p;
+    size_t bytes;
+};
+Space space(PyObject* o, c10::Device dev) {
+    if (o == Py_None) return {nullptr, 0};
+    const at::Tensor& w = tensor(o, "workspace");
+    if (w.device() != dev || !w.is_contiguous()) refuse("workspace", "a contiguous tensor on the other tensors' device expected");
+    return {w.data_ptr(), w.nbytes()};
+}
+
+// glu_backward(dH, P, X, W, dX, dW, db, act, workspace, stream)
+PyObject* glu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 10, [&] {
+        const at::Tensor &dH = matrix(a[0], "dH"), &X = matrix(a[2], "X");
+        const int64_t M = X.size(0), D = X.size(1), F = dH.size(1), act = integer(a[7], "act");
+        const c10::Device dev = X.device();
+        const at::ScalarType dt = X.scalar_type();
+        const kt_dtype c = code(X, "X");
+        const Rows x = rows(X, "X", M, D, dt, dev, 8), dh = rows(dH, "dH", M, F, dt, dev, 8),
+                   p = rows(tensor(a[1], "P"), "P", M, 2 * F, dt, dev, 8);
+        Rows dx = {nullptr, 0};
+        if (a[4] != Py_None) dx = rows(tensor(a[4], "dX"), "dX", M, D, dt, dev, 8);
+        if (a[3] == Py_None) refuse("W", "a torch tensor expected");
+        void* W = whole(a[3], "W", {2 * F, D}, dt, dev);
+        void* dW = whole(a[5], "dW", {2 * F, D}, dt, dev);
+        void* db = whole(a[6], "db", {2 * F}, at::kFloat, dev);
+        const Space ws = space(a[8], dev);
+        void* s = stream_of(a[9], dev);
+        return kt_glu_backward(M, D, F, c, (kt_act)act, dh.p, dh.ld, p.p, p.ld, x.p, x.ld, W, dx.p, dx.ld, dW, (float*)db, ws.p, ws.bytes, s);
+    });
+}
+
+// linear_forward(X, W, bias, Y, stream)
+PyObject* linear_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 5, [&] {
+        const at::Tensor &X = matrix(a[0], "X"), &Y = matrix(a[3], "Y");
+        const int64_t M = X.size(0), K = X.size(1), N = Y.size(1);
+        const c10::Device dev = X.device();
+        const at::ScalarType dt = X.scalar_type();
+        const kt_dtype c = code(X, "X");
+        const Rows x = rows(X, "X", M, K, dt, dev, 8), y = rows(Y, "Y", M, N, dt, dev, 8);
+        if (a[1] == Py_None) refuse("W", "a torch tensor expected");
+        void* W = whole(a[1], "W", {N, K}, dt, dev);
+        void* b = whole(a[2], "bias", {N}, dt, dev);
+        void* s = stream_of(a[4], dev);
+        return kt_linear_forward(M, N, K, c, x.p, x.ld, W, b, y.p, y.ld, s);
+    });
+}
+
+// linear_backward(dY, X, W, dX, dW, db, workspace, stream)
+PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 8, [&] {
+        const at::Tensor &dY = matrix(a[0], "dY"), &X = matrix(a[1], "X");
+        const int64_t M = X.size(0), K = X.size(1), N = dY.size(1);
+        const c10::Device dev = X.device();
+        const at::ScalarType dt = X.scalar_type();
+        const kt_dtype c = code(X, "X");
+        const Rows x = rows(X, "X", M, K, dt, dev, 8), dy = rows(dY, "dY", M, N, dt, dev, 8);
+        Rows dx = {nullptr, 0};
+        if (a[3] != Py_None) dx = rows(tensor(a[3], "dX"), "dX", M, K, dt, dev, 8);
+        if (a[2] == Py_None) refuse("W", "a torch tensor expected");
+        void* W = whole(a[2], "W", {N, K}, dt, dev);
+        void* dW = whole(a[4], "dW", {N, K}, dt, dev);
+        void* db = whole(a[5], "db", {N}, at::kFloat, dev);
+        const Space ws = space(a[6], dev);
+        void* s = stream_of(a[7], dev);
+        return kt_linear_backward(M, N, K, c, dy.p, dy.ld, x.p, x.ld, W, dx.p, dx.ld, dW, (float*)db, ws.p, ws.bytes, s);
+    });
+}
+
+double number(PyObject* o, const char* name) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        refuse(name, "a number expected");
+    }
+    return v;
+}
+
+// A list or tuple of as many items as there are parameters; None: none.
+PyObject* items(PyObject* o, const char* name, Py_ssize_t want) {
+    if (o == Py_None) return nullptr;
+    if (!PyList_Check(o) && !PyTuple_Check(o)) refuse(name, "a list or tuple expected");
+    if (want >= 0 && PySequence_Fast_GET_SIZE(o) != want) refuse(name, "as many items as parameters expected");
+    return o;
+}
+
+int32_t any_code(at::ScalarType t, const char* name) {
+    if (t == at::kFloat) return KT_F32;
+    if (t == at::kHalf) return KT_F16;
+    if (t == at::kBFloat16) return KT_BF16;
+    refuse(name, "float32, float16 or bfloat16 expected");
+}
+
+// A contiguous tensor of n elements of a type and device.
+void* flat(PyObject* list, Py_ssize_t i, const char* name, int64_t numel, at::ScalarType dtype, c10::Device dev) {
+    const at::Tensor& t = tensor(PySequence_Fast_GET_ITEM(list, i), name);
+    if (t.numel() != numel || t.scalar_type() != dtype || t.device() != dev || !t.is_contiguous()) misfit(name, t, {numel}, dtype, dev);
+    return t.data_ptr();
+}
+
+// adamw(params, grads, m, v, step, lr, beta1, beta2, eps, weight_decay, m_scales, v_scales, copies, grad_scale, stream)
+PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 15, [&]() -> kt_status {
+        PyObject* params = items(a[0], "params", -1);
+        if (!params) refuse("params", "a list or tuple expected");
+        const Py_ssize_t count = PySequence_Fast_GET_SIZE(params);
+        PyObject *grads = items(a[1], "grads", count), *ms = items(a[2], "m", count), *vs = items(a[3], "v", count);
+        if (!grads || !ms || !vs) refuse("grads, m and v", "lists or tuples expected");
+        PyObject *mscales = items(a[10], "m_scales", count), *vscales = items(a[11], "v_scales", count), *copies = items(a[12], "copies", count);
+        kt_adamw_options o = {};
+        o.lr = number(a[5], "lr");
+        o.beta1 = number(a[6], "beta1");
+        o.beta2 = number(a[7], "beta2");
+        o.eps = number(a[8], "eps");
+        const bool one_decay = PyFloat_Check(a[9]) || PyLong_Check(a[9]);
+        PyObject* decays = one_decay ? nullptr : items(a[9], "weight_decay", count);
+        if (!one_decay && !decays) refuse("weight_decay", "a number, or a list or tuple of them expected");
+        const double decay = one_decay ? number(a[9], "weight_decay") : 0.0;
+        if (!count) return KT_OK;
+        const at::Tensor& first = tensor(PySequence_Fast_GET_ITEM(params, 0), "params");
+        const c10::Device dev = first.device();
+        const at::ScalarType pt = first.scalar_type(), gt = tensor(PySequence_Fast_GET_ITEM(grads, 0), "grads").scalar_type(),
+                             st = tensor(PySequence_Fast_GET_ITEM(ms, 0), "m").scalar_type();
+        o.param_dtype = any_code(pt, "params");
+        o.grad_dtype = any_code(gt, "grads");
+        if (st != at::kFloat && st != at::kFloat8_e4m3fn) refuse("m", "float32 or float8_e4m3fn expected");
+        o.state_bits = st == at::kFloat ? 32 : 8;
+        if ((o.state_bits == 8) != (mscales != nullptr) || (o.state_bits == 8) != (vscales != nullptr))
+            refuse("m_scales and v_scales", "expected with float8_e4m3fn moments, and with them alone");
+        at::ScalarType ct = at::kBFloat16;
+        if (copies) {
+            ct = tensor(PySequence_Fast_GET_ITEM(copies, 0), "copies").scalar_type();
+            o.copy_dtype = code(tensor(PySequence_Fast_GET_ITEM(copies, 0), "copies"), "copies");
+        }
+        if (THPVariable_Check(a[4])) {
+            o.step_device = (const int64_t*)whole(a[4], "step", tensor(a[4], "step").dim() ? at::IntArrayRef{1} : at::IntArrayRef{}, at::kLong, dev);
+        } else {
+            o.step = integer(a[4], "step");
+        }
+        if (a[13] != Py_None)
+            o.grad_scale = (const float*)whole(a[13], "grad_scale", tensor(a[13], "grad_scale").dim() ? at::IntArrayRef{1} : at::IntArrayRef{}, at::kFloat, dev);
+        std::vector<kt_adamw_tensor> t((size_t)count);
+        for (Py_ssize_t i = 0; i < count; ++i) {
+            const int64_t numel = tensor(PySequence_Fast_GET_ITEM(params, i), "params").numel();
+            const int64_t blocks = (numel + KT_ADAMW_BLOCK - 1) / KT_ADAMW_BLOCK;
+            t[i].param = flat(params, i, "params", numel, pt, dev);
+            t[i].grad = flat(grads, i, "grads", numel, gt, dev);
+            t[i].m = flat(ms, i, "m", numel, st, dev);
+            t[i].v = flat(vs, i, "v", numel, st, dev);
+            t[i].m_scale = mscales ? (float*)flat(mscales, i, "m_scales", blocks, at::kFloat, dev) : nullptr;
+            t[i].v_scale = vscales ? (float*)flat(vscales, i, "v_scales", blocks, at::kFloat, dev) : nullptr;
+            t[i].copy = copies ? flat(copies, i, "copies", numel, ct, dev) : nullptr;
+            t[i].n = numel;
+            t[i].weight_decay = decays ? number(PySequence_Fast_GET_ITEM(decays, i), "weight_decay") : decay;
+        }
+        void* s = stream_of(a[14], dev);
+        return kt_adamw(count, t.data(), &o, s);
+    });
+}
+
 PyMethodDef kMethods[] = {
     {"layernorm_forward", (PyCFunction)(void*)layernorm_forward, METH_FASTCALL, nullptr},
     {"layernorm_backward", (PyCFunction)(void*)layernorm_backward, METH_FASTCALL, nullptr},
     {"quantize_rows", (PyCFunction)(void*)quantize_rows, METH_FASTCALL, nullptr},
     {"linear_i8", (PyCFunction)(void*)linear_i8, METH_FASTCALL, nullptr},
     {"moe_run", (PyCFunction)(void*)moe_run, METH_FASTCALL, nullptr},
+    {"glu_forward", (PyCFunction)(void*)glu_forward, METH_FASTCALL, nullptr},
+    {"glu_backward", (PyCFunction)(void*)glu_backward, METH_FASTCALL, nullptr},
+    {"linear_forward", (PyCFunction)(void*)linear_forward, METH_FASTCALL, nullptr},
+    {"linear_backward", (PyCFunction)(void*)linear_backward, METH_FASTCALL, nullptr},
+    {"adamw", (PyCFunction)(void*)adamw, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_kt_ops", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

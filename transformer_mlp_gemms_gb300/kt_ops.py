@@ -29,6 +29,7 @@ _VP, _I64, _I32, _F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_
 KT_LAYERNORM_MAX_D = 16384
 KT_LINEAR_I8_DOT_ROWS = 16
 KT_MOE_MAX_TOKENS, KT_MOE_MAX_EXPERTS, KT_MOE_MAX_TOP_K = 64, 256, 16
+KT_F32, KT_ADAMW_BLOCK = 2, 256
 
 
 class kt_moe_options(ctypes.Structure):
@@ -39,6 +40,17 @@ class kt_moe_options(ctypes.Structure):
 class kt_moe_tensors(ctypes.Structure):
     _fields_ = [("tokens", _I64), ("X", _VP), ("ldx", _I64)] + \
                [(n, _VP) for n in ("W_router", "W_up", "W_down", "b_up", "b_down", "R", "Y", "ids", "weights")]
+
+
+class kt_adamw_tensor(ctypes.Structure):
+    _fields_ = [(n, _VP) for n in ("param", "grad", "m", "v", "m_scale", "v_scale", "copy")] + \
+               [("n", _I64), ("weight_decay", ctypes.c_double)]
+
+
+class kt_adamw_options(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("param_dtype", "grad_dtype", "copy_dtype", "state_bits")] + \
+               [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps")] + \
+               [("step", _I64), ("step_device", _VP), ("grad_scale", _VP)]
 
 
 # every entry point declared in include/kt_ops.h, with its ctypes signature
@@ -56,6 +68,15 @@ SIGNATURES = {
     "kt_moe_status": ([_VP], _I32),
     "kt_moe_debug_stall": ([_VP, _I32, _I64], _I32),
     "kt_moe_destroy": ([_VP], _I32),
+    "kt_glu_forward": ([_I64] * 3 + [_I32] * 2 + [_VP, _I64, _VP, _VP, _VP, _I64, _VP, _I64, _VP], _I32),
+    "kt_glu_backward_workspace": ([_I64] * 3, ctypes.c_size_t),
+    "kt_glu_backward": ([_I64] * 3 + [_I32] * 2 + [_VP, _I64] * 3 + [_VP, _VP, _I64, _VP, _VP, _VP, ctypes.c_size_t, _VP], _I32),
+    "kt_linear_forward": ([_I64] * 3 + [_I32, _VP, _I64, _VP, _VP, _VP, _I64, _VP], _I32),
+    "kt_linear_backward_workspace": ([_I64] * 3, ctypes.c_size_t),
+    "kt_linear_backward": ([_I64] * 3 + [_I32] + [_VP, _I64] * 2 + [_VP, _VP, _I64, _VP, _VP, _VP, ctypes.c_size_t, _VP], _I32),
+    "kt_adamw": ([_I64, ctypes.POINTER(kt_adamw_tensor), ctypes.POINTER(kt_adamw_options), _VP], _I32),
+    "kt_matmul_status": ([_VP], _I32),
+    "kt_matmul_debug_stall": ([_I32, _I64], _I32),
 }
 
 _lib = None
@@ -200,3 +221,75 @@ class MoePlan:
             self.close()
         except Exception:
             pass
+
+
+def kt_glu_forward(X, W, bias, H, P, act: int, stream=None) -> None:
+    """H = value * act(gate) with [value | gate] = X W^T (+ bias), W [2F][D]; P [M][2F] receives value and
+    gate if given (``kt_glu_backward`` wants them)."""
+    r = (_ext or _calls()).glu_forward(X, W, bias, H, P, act, stream)
+    if r is not None:
+        _fail(r, "kt_glu_forward")
+
+
+def kt_glu_backward_workspace(M: int, D: int, F: int) -> int:
+    """Bytes of workspace of kt_glu_backward (0 for sizes that it refuses)."""
+    return load().kt_glu_backward_workspace(M, D, F)
+
+
+def glu_backward_workspace(M: int, D: int, F: int, device="cuda"):
+    """A workspace tensor for kt_glu_backward, to be kept from call to call on one stream."""
+    return torch.empty(kt_glu_backward_workspace(M, D, F), dtype=torch.uint8, device=device)
+
+
+def kt_glu_backward(dH, P, X, W, dX, dW, db, act: int, workspace, stream=None) -> None:
+    """dX [M][D], dW [2F][D] and db (fp32 [2F]) from dH and the P that kt_glu_forward kept; each of the
+    three may be None."""
+    r = (_ext or _calls()).glu_backward(dH, P, X, W, dX, dW, db, act, workspace, stream)
+    if r is not None:
+        _fail(r, "kt_glu_backward")
+
+
+def kt_linear_forward(X, W, bias, Y, stream=None) -> None:
+    """Y = X W^T (+ bias), W [N][K]."""
+    r = (_ext or _calls()).linear_forward(X, W, bias, Y, stream)
+    if r is not None:
+        _fail(r, "kt_linear_forward")
+
+
+def kt_linear_backward_workspace(M: int, N: int, K: int) -> int:
+    """Bytes of workspace of kt_linear_backward (0 for sizes that it refuses)."""
+    return load().kt_linear_backward_workspace(M, N, K)
+
+
+def linear_backward_workspace(M: int, N: int, K: int, device="cuda"):
+    """A workspace tensor for kt_linear_backward, to be kept from call to call on one stream."""
+    return torch.empty(kt_linear_backward_workspace(M, N, K), dtype=torch.uint8, device=device)
+
+
+def kt_linear_backward(dY, X, W, dX, dW, db=None, workspace=None, stream=None) -> None:
+    """dX [M][K], dW [N][K] and db (fp32 [N], needs ``workspace``); each may be None."""
+    r = (_ext or _calls()).linear_backward(dY, X, W, dX, dW, db, workspace, stream)
+    if r is not None:
+        _fail(r, "kt_linear_backward")
+
+
+def kt_adamw(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, m_scales=None,
+             v_scales=None, copies=None, grad_scale=None, stream=None) -> None:
+    """One AdamW step over lists of contiguous tensors, in place.  ``m`` and ``v`` are float32, or float8_e4m3fn
+    with ``m_scales`` and ``v_scales`` (float32, one for each KT_ADAMW_BLOCK values; ``v`` then holds the second
+    moment's root).  ``step``: a number from 1 on, or an int64 tensor on the device.  ``weight_decay``: a number,
+    or one for each tensor.  ``copies``: 16-bit tensors that receive fp32 parameters' rounding."""
+    r = (_ext or _calls()).adamw(params, grads, m, v, step, lr, beta1, beta2, eps, weight_decay, m_scales, v_scales, copies,
+                                 grad_scale, stream)
+    if r is not None:
+        _fail(r, "kt_adamw")
+
+
+def kt_matmul_status(stream=None) -> int:
+    """Waits for the stream and returns the status code of the device's products (does not raise on
+    KT_ERR_TIMEOUT)."""
+    return load().kt_matmul_status(kt_mlp._stream(stream))
+
+
+def kt_matmul_debug_stall(enable: bool, limit_us: int = 0) -> None:
+    _check(load().kt_matmul_debug_stall(int(bool(enable)), limit_us), "kt_matmul_debug_stall")
