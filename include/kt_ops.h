@@ -11,7 +11,9 @@
  *                                                  activation and the product) and its gradients;
  *   kt_linear_forward / kt_linear_backward         a 16-bit linear layer and its gradients;
  *   kt_adamw                                       an AdamW step over many tensors at once, moments
- *                                                  in 32 bits or in 8.
+ *                                                  in 32 bits or in 8;
+ *   kt_quantize_fp8 / kt_linear_fp8                activations in 8-bit floating point, and the linear
+ *                                                  layer on it, with a scale for each block of 128.
  *
  * They share the library, the status codes, kt_last_error(), the kt_dtype and kt_act values and
  * the [out][in] weight order (KT_W_OUT_IN) of kt_mlp.h.  All pointers are device pointers that
@@ -302,8 +304,34 @@ typedef struct {
 kt_status kt_adamw(int64_t count, const kt_adamw_tensor* tensors, const kt_adamw_options* options, void* stream);
 
 /*
+ * kt_quantize_fp8 -- activations in 8-bit floating point (e4m3), a scale for each token and run of 128 columns:
+ *   v = act(X[m][:]) (fp32);  of each run:  most = max|v|,  scale[m][j] = most / 448,
+ *   Q[m][k] = the e4m3 number nearest to v * (448 / most)  (both quotients and the product rounded to fp32)
+ * A run with no magnitude of 2^-100 or more has scale 0 and Q = 0; one with a NaN or an infinity has a scale
+ * that is none either, so that whatever is computed from it shows it.
+ *   act: KT_ACT_NONE quantises X[M][K]; an activation the hidden layer of an MLP as it is computed: X is then the
+ *   up projection's output, [M][K], or [M][2K] for KT_ACT_GEGLU (value columns, then gate columns).
+ *   M >= 0, K >= 1; any pitch and alignment to the elements.  scale: [M][ceil(K / 128)] fp32.
+ */
+kt_status kt_quantize_fp8(int64_t M, int64_t K, kt_dtype dtype, kt_act act, const void* X, int64_t ldx, void* Q, int64_t ldq,
+                          float* scale, void* stream);
+
+/*
+ * kt_linear_fp8 -- the linear layer on 8-bit floating point with a scale for each block of 128:
+ *   Y[m][n] = round( sum_j scale_x[m][j] scale_w[n / 128][j] sum_{k in run j} Q[m][k] W[n][k]  (+ bias[n]) )
+ *   Q: e4m3 [M][K], pitch ldq; scale_x: [M][ceil(K / 128)] fp32.  W: e4m3 [N][K], pitch ldw;
+ *   scale_w: [ceil(N / 128)][ceil(K / 128)] fp32.  bias: [N] of dtype or NULL.  Y: [M][N] of dtype, pitch ldy.
+ * The sums of a run and over the runs are fp32, with one rounding to dtype at the end.
+ *   M >= 0, N a multiple of 8, K, ldq and ldw multiples of 16, ldy a multiple of 8; Q, W, Y and bias 16-byte
+ *   aligned.  Up to KT_LINEAR_FP8_FEW tokens the weights are the tensor cores' first operand.
+ */
+#define KT_LINEAR_FP8_FEW 64
+kt_status kt_linear_fp8(int64_t M, int64_t N, int64_t K, kt_dtype dtype, const void* Q, int64_t ldq, const void* W, int64_t ldw,
+                        const float* scale_x, const float* scale_w, const void* bias, void* Y, int64_t ldy, void* stream);
+
+/*
  * kt_matmul_status -- wait for `stream` and read the current device's error word of the calls on the tensor cores
- * above (kt_glu_*, kt_linear_forward, kt_linear_backward): KT_ERR_TIMEOUT if a bounded
+ * above (kt_glu_*, kt_linear_forward, kt_linear_backward, kt_linear_fp8): KT_ERR_TIMEOUT if a bounded
  * device-side wait ran out in any of the device's calls since it was last asked (the word is cleared).  Such
  * a call stores NaN in every element that it could not compute.
  */

@@ -1,0 +1,674 @@
+// kt_linear_fp8.cu -- activations in 8-bit floating point with a scale for each token and run of 128 columns, and
+// the linear layer on them, its weights with a scale for each block of 128 x 128:
+//
+//   Y[m][n] = round( sum_j sx[m][j] sw[n / 128][j] sum_{k in run j} Q[m][k] W[n][k]  (+ bias[n]) )
+//
+// The products are tcgen05.mma kind::f8f6f4 with fp32 accumulators.  A run's sum has scales of its own,
+// so each run has an accumulator of its own: while the tensor cores work on the next, the epilogue warps
+// take the finished one out of tensor memory and add it, times its scales, to fp32 sums in their registers.
+//
+// Many tokens: a CTA (or, cta_group::2, a pair) per tile of 128 (256) tokens x BN channels, persistent, in bands
+// as kt_matmul.cu; eight epilogue warps share the tile's columns, so that a thread has one token's row and
+// BN / 2 sums.  The tokens' scales come through shared memory, eight runs at a time, [run][token]: read from
+// where they lie they would cost a line per lane.
+// Few tokens (SWAP): the weights are the first operand, 128 channels a tile, and the tokens the second,
+// 16 to 64 columns, so that no tensor-core row is idle; a thread has one channel.  Bound by the weights' bytes.
+// Few tiles with long rows: a cluster per tile, each CTA with its share of the runs; the sums meet in the
+// cluster's shared memory, added in the order of the ranks.
+#include <cuda_fp8.h>
+
+#include "kt_ops_internal.h"
+#include "kt_gemm.cuh"
+#include "kt_matmul.cuh"
+
+namespace kt {
+
+__device__ int g_fp8_error;
+
+namespace {
+
+constexpr int kRun = 128;
+constexpr uint32_t kF8ABytes = 128 * kRun;
+
+// ---------------------------------------------------------------------------
+// The quantiser
+// ---------------------------------------------------------------------------
+
+constexpr int kQuantThreads = 256;
+
+__device__ __forceinline__ float activate(float z, int act) {
+    f32x2 v = f2(z, 0.0f);
+    switch (act) {
+        case EPI_GELU_ERF: return act_f2<EPI_GELU_ERF, true>(v).x;
+        case EPI_GELU_TANH: return act_f2<EPI_GELU_TANH, true>(v).x;
+        case EPI_GELU_SIGMOID: return act_f2<EPI_GELU_SIGMOID, true>(v).x;
+        case EPI_SILU: return act_f2<EPI_SILU, true>(v).x;
+        default: return z;
+    }
+}
+
+// Sixteen lanes per run of 128 columns, eight columns each: consecutive ones (WIDE: 16-byte loads, 8-byte
+// stores), else every sixteenth.  Bound by memory: 3 bytes per element.
+template <int DT, bool WIDE>
+__global__ void __launch_bounds__(kQuantThreads) kt_quantize_fp8_kernel(const QuantFp8 p, int runs) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int l = threadIdx.x & 15;
+    const int64_t total = (int64_t)p.M * runs, stride = (int64_t)gridDim.x * (kQuantThreads / 16);
+    // the two halves of a warp may end apart: the whole warp goes on while either has a run
+    for (int64_t i = (int64_t)blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4); (i & ~(int64_t)1) < total; i += stride) {
+        const bool live = i < total;
+        const int64_t row = live ? i / runs : 0;
+        const int run = live ? (int)(i - row * runs) : 0, k0 = run * kRun, end = live ? min(kRun, p.K - k0) : 0;
+        float f[8];
+        auto load = [&](const uint16_t* at, float* to) {
+            if constexpr (WIDE) {
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (8 * l < end) w = *reinterpret_cast<const uint4*>(at + 8 * l);
+                unpack8<DT>(w, to);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float t[8] = {};
+                    if (l + 16 * e < end) unpack8<DT>(make_uint4(at[l + 16 * e], 0u, 0u, 0u), t);
+                    to[e] = t[0];
+                }
+            }
+        };
+        const uint16_t* x = static_cast<const uint16_t*>(p.X) + row * p.ldx + k0;
+        load(x, f);
+        if (p.act == EPI_GEGLU) {
+            float g[8];
+            load(x + p.K, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] *= activate(g[e], EPI_GELU_ERF);
+        } else if (p.act != EPI_NONE) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = activate(f[e], p.act);
+        }
+        uint32_t most = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(f[e]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        const float top = __uint_as_float(most);
+        const bool zero = top < 0x1p-100f;
+        const float inverse = zero ? 0.0f : __fdiv_rn(448.0f, top);
+        if (live && l == 0) p.scale[row * runs + run] = zero ? 0.0f : __fdiv_rn(top, 448.0f);
+        uint8_t* q = p.Q + row * p.ldq + k0;
+        if constexpr (WIDE) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[j] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(f[2 * j], inverse), __fmul_rn(f[2 * j + 1], inverse)), __NV_SATFINITE, __NV_E4M3);
+            if (8 * l < end) *reinterpret_cast<uint2*>(q + 8 * l) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (l + 16 * e < end) q[l + 16 * e] = __nv_cvt_float_to_fp8(__fmul_rn(f[e], inverse), __NV_SATFINITE, __NV_E4M3);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The linear layer
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+struct F8Params {
+    int M, N, runs, tiles_m, tiles_n, stages;
+    uint32_t idesc;
+    const float *sx, *sw;
+    const void* bias;
+    void* Y;
+    int64_t ldy;
+    unsigned long long wait_limit_ns, stall_ns;
+};
+
+template <int PAIR, int BN, bool SWAP>
+struct F8 {
+    static constexpr int kEpi = SWAP ? 4 : 8;               // epilogue warps
+    static constexpr int kCols = SWAP ? BN : BN / 2;        // sums per thread
+    static constexpr int kBufs = BN > 128 ? 2 : BN > 64 ? 4 : 8;  // accumulators
+    static constexpr int kThreads = (kEpi + 4) * 32;        // warps 0-2: copies of A, products, copies of B; 3: none; then the epilogue
+    static constexpr uint32_t kBBytes = (uint32_t)(BN / PAIR) * kRun;
+    static constexpr uint32_t kStage = kF8ABytes + kBBytes;
+    static constexpr int kChunk = 8;                        // runs of scales in shared memory at a time
+    static constexpr uint32_t kScales = SWAP ? 0u : 2u * kChunk * 128u * 4u;
+    static constexpr uint32_t kStaging = SWAP ? 0u : (uint32_t)kEpi * 2048u;
+    static constexpr int kFit = (int)((kSmemBudget - 1024 - 512 - kScales - kStaging) / kStage);
+    static constexpr int kStages = kFit < 10 ? kFit : 10;
+};
+
+template <int DT, int PAIR, int BN, bool SWAP>
+__global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
+    kt_linear_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                         const __grid_constant__ CUtensorMap tmY, const __grid_constant__ F8Params p) {
+    using C = F8<PAIR, BN, SWAP>;
+    constexpr int kEpi = C::kEpi, kCols = C::kCols, kBufs = C::kBufs, kStages = C::kStages;
+    extern __shared__ uint8_t raw[];
+    uint8_t* const at = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    const uint32_t base = smem_u32(at);
+    const uint32_t staging = base + kStages * C::kStage;
+    float* const scales = reinterpret_cast<float*>(at + kStages * C::kStage + C::kStaging);  // [2][kChunk][128]
+    const uint32_t bars = staging + C::kStaging + C::kScales;
+    const uint32_t bar_full = bars, bar_empty = bars + 80u, bar_accf = bars + 160u, bar_acce = bars + 224u, bar_drain = bars + 288u,
+                   bar_stall = bars + 296u;
+    uint32_t* const words = reinterpret_cast<uint32_t*>(at + (bars - base) + 304u);
+    volatile int* const abort_flag = reinterpret_cast<volatile int*>(words + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned long long limit = p.wait_limit_ns;
+    const uint32_t rank = PAIR == 2 ? (cluster_ctarank() & 1u) : 0u;
+    const int splits = PAIR == 1 ? (int)cluster_size() : 1, part = PAIR == 1 ? (int)cluster_ctarank() : 0;
+    const bool leader = rank == 0;
+    const int unit0 = (int)blockIdx.x / (PAIR * splits), units = (int)gridDim.x / (PAIR * splits);
+    const int tiles = p.tiles_m * p.tiles_n;
+    const int run0 = p.runs * part / splits, runs = p.runs * (part + 1) / splits - run0;  // of a tile, in this CTA
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(bar_full + 8u * s, 1);
+            mbar_init(bar_empty + 8u * s, 1);
+        }
+        for (int b = 0; b < kBufs; ++b) {
+            mbar_init(bar_accf + 8u * b, 1);
+            mbar_init(bar_acce + 8u * b, kEpi * PAIR);
+        }
+        mbar_init(bar_drain, 1);
+        mbar_init(bar_stall, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+        prefetch_tmap(&tmA);
+        prefetch_tmap(&tmB);
+        if (!SWAP) prefetch_tmap(&tmY);
+    }
+    if (warp == 1) tmem_alloc<PAIR>(smem_u32(words), kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    if (PAIR == 2) cluster_sync_relaxed();
+    tc_fence_after();
+    const uint32_t tmem = words[0];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // first token and first channel of tile t (of the pair's tile)
+    auto origin = [&](int t, int& m, int& n) {
+        if constexpr (SWAP) {
+            m = 0;
+            n = t * 128;
+        } else {
+            int tm, tn;
+            band_tile(t, p.tiles_m, p.tiles_n, tm, tn);
+            m = tm * PAIR * 128;
+            n = tn * BN;
+        }
+    };
+
+    if (warp == 0 || warp == 2) {
+        // ------------------- copies -------------------
+        if (lane == 0) {
+            const bool a_role = warp == 0;
+            uint32_t stage = 0, phase = 0, used = 0, used_phase = 0;
+            if (a_role && p.stall_ns && blockIdx.x == 0)  // the tests' hook: nobody signals this barrier
+                wait_phase(bar_stall, 0, abort_flag, &g_fp8_error, DEV_INJECTED_STALL, p.stall_ns);
+            for (int t = unit0; t < tiles && !*abort_flag; t += units) {
+                int m, n;
+                origin(t, m, n);
+                const int a_row = SWAP ? n : m + (int)rank * 128, b_row = SWAP ? m : n + (int)rank * (BN / PAIR);
+                for (int j = 0; j < runs; ++j) {
+                    if (!wait_turn(bar_empty + 8u * stage, phase ^ 1u, abort_flag, &g_fp8_error, DEV_TIMEOUT_PRODUCER, limit)) break;
+                    const uint32_t sA = base + stage * C::kStage;
+                    const uint32_t fb = PAIR == 2 ? mapa_rank(bar_full + 8u * stage, 0) : bar_full + 8u * stage;
+                    if (a_role && leader) mbar_arrive_expect_tx(bar_full + 8u * stage, PAIR * C::kStage);
+                    const int x = (run0 + j) * (kRun / 2);  // the maps count pairs of bytes
+                    if constexpr (PAIR == 2) tma_load_2d_pair(a_role ? sA : sA + kF8ABytes, a_role ? &tmA : &tmB, fb, x, a_role ? a_row : b_row);
+                    else tma_load_2d(a_role ? sA : sA + kF8ABytes, a_role ? &tmA : &tmB, fb, x, a_role ? a_row : b_row);
+                    used |= 1u << stage;
+                    used_phase = (used_phase & ~(1u << stage)) | (phase << stage);
+                    if (++stage == (uint32_t)kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (*abort_flag) {  // no copy may still be on its way into memory that is about to be released
+                if (a_role && leader)
+                    for (int s = 0; s < kStages; ++s)
+                        if (used & (1u << s)) wait_drain(bar_full + 8u * s, (used_phase >> s) & 1u, 100000000ull);
+                const unsigned long long t0 = global_ns();
+                while (global_ns() - t0 < 100000ull) __nanosleep(1000);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------- products -------------------
+        if (lane == 0 && leader) {
+            uint32_t stage = 0, phase = 0, buf = 0, use = 0;
+            const uint64_t ad0 = smem_desc(base, 16u, 1024u), bd0 = smem_desc(base + kF8ABytes, 16u, 1024u);
+            bool ok = true, any = false;
+            for (int t = unit0; t < tiles && ok; t += units)
+                for (int j = 0; j < runs; ++j) {
+                    const uint32_t fb = bar_full + 8u * stage, ab = bar_acce + 8u * buf;
+                    ok = (mbar_test_wait(fb, phase) || wait_turn(fb, phase, abort_flag, &g_fp8_error, DEV_TIMEOUT_MMA, limit)) &&
+                         wait_turn<PAIR == 2>(ab, (use & 1u) ^ 1u, abort_flag, &g_fp8_error, DEV_TIMEOUT_MMA, limit);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem + buf * (uint32_t)BN;
+                    const uint64_t ad = ad0 + stage * (C::kStage >> 4), bd = bd0 + stage * (C::kStage >> 4);
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; ++k) {  // 32 columns each
+                        if constexpr (PAIR == 2) mma_f8_pair(d, ad + 2 * k, bd + 2 * k, p.idesc, k > 0);
+                        else mma_f8(d, ad + 2 * k, bd + 2 * k, p.idesc, k > 0);
+                    }
+                    any = true;
+                    if constexpr (PAIR == 2) {
+                        mma_commit_pair(bar_empty + 8u * stage);
+                        mma_commit_pair(bar_accf + 8u * buf);
+                    } else {
+                        mma_commit(bar_empty + 8u * stage);
+                        mma_commit(bar_accf + 8u * buf);
+                    }
+                    if (++stage == (uint32_t)kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (++buf == (uint32_t)kBufs) {
+                        buf = 0;
+                        ++use;
+                    }
+                }
+            if (*abort_flag && any) {  // no product may still be running when tensor memory is freed
+                if constexpr (PAIR == 2) mma_commit_pair(bar_drain);
+                else mma_commit(bar_drain);
+                wait_drain(bar_drain, 0u, 100000000ull);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ------------------- epilogue -------------------
+        const int ew = warp - 4, q = warp & 3, c0 = SWAP ? 0 : (ew >> 2) * kCols;  // lanes of tensor memory, first column
+        uint32_t buf = 0, use = 0;
+        bool ok = true;
+        // The tokens' scales, kChunk runs at a time: thread i of the 256 takes four runs of token i / 2, into
+        // registers a chunk ahead.
+        const int st = (int)threadIdx.x - 128, srow = st >> 1, srun = (st & 1) * 4;
+        float ahead[4] = {};
+        auto fetch = [&](int t, int chunk) {
+            int m, n;
+            origin(t, m, n);
+            m += (int)rank * 128 + srow;
+            const int j = chunk * C::kChunk + srun;
+            const float* from = p.sx + (int64_t)m * p.runs + run0 + j;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ahead[i] = m < p.M && j + i < runs ? from[i] : 0.0f;
+        };
+        const int chunks = (runs + C::kChunk - 1) / C::kChunk;
+        uint32_t slot = 0;  // of the chunk in use
+        if (!SWAP && unit0 < tiles) fetch(unit0, 0);
+        for (int t = unit0; t < tiles; t += units) {
+            int m, n;
+            origin(t, m, n);
+            float sum[kCols];
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) sum[i] = 0.0f;
+            const float* sw = p.sw + (int64_t)((n + c0) / 128) * p.runs + run0;  // the same for all of the warp's columns
+            const bool live = n + c0 < p.N;
+            float w_next = live ? sw[0] : 0.0f;
+            constexpr int kPer = SWAP ? (BN + 31) / 32 : 1;  // SWAP: tokens lane and lane + 32
+            float x_next[kPer];
+            auto tokens = [&](int j) {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) x_next[i] = lane + 32 * i < p.M ? p.sx[(int64_t)(lane + 32 * i) * p.runs + run0 + j] : 0.0f;
+            };
+            if constexpr (SWAP) tokens(0);
+#pragma unroll 1
+            for (int j = 0; j < runs; ++j) {
+                if constexpr (!SWAP) {
+                    if (j % C::kChunk == 0) {
+                        slot ^= 1u;
+                        float* to = scales + slot * (C::kChunk * 128) + srun * 128 + srow;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) to[128 * i] = ahead[i];
+                        asm volatile("bar.sync 1, %0;" ::"n"(kEpi * 32) : "memory");
+                        if (j / C::kChunk + 1 < chunks) fetch(t, j / C::kChunk + 1);
+                        else if (t + units < tiles) fetch(t + units, 0);
+                    }
+                }
+                const float w = w_next;
+                float x[kPer];
+                if constexpr (SWAP) {
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) x[i] = x_next[i] * w;
+                    if (j + 1 < runs) tokens(j + 1);
+                } else {
+                    x[0] = w * scales[slot * (C::kChunk * 128) + (j % C::kChunk) * 128 + 32 * q + lane];
+                }
+                if (live && j + 1 < runs) w_next = sw[j + 1];
+                ok = ok && wait_turn(bar_accf + 8u * buf, use & 1u, abort_flag, &g_fp8_error, DEV_TIMEOUT_EPILOGUE, limit);
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+                const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * (uint32_t)BN + (uint32_t)c0;
+                // 16 columns at a time, the next 16 on their way: a wide tile's 128 sums leave no registers for more.
+                // (After a wait that ran out the sums are of no use, and are NaN below.)
+                uint32_t r[2][16];
+                tmem_ld16(acc, r[0]);
+#pragma unroll
+                for (int c = 0; c < kCols; c += 16) {
+                    uint32_t(&now)[16] = r[c / 16 & 1];
+                    tmem_wait_ld(now);
+                    if (c + 16 < kCols) tmem_ld16(acc + (uint32_t)c + 16u, r[c / 16 + 1 & 1]);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        f32x2 s;
+                        if constexpr (SWAP) s = f2(__shfl_sync(0xffffffffu, x[c / 32], c % 32 + i), __shfl_sync(0xffffffffu, x[c / 32], c % 32 + i + 1));
+                        else s = f2(x[0]);
+                        const f32x2 v = f2_fma<true>(f2(__uint_as_float(now[i]), __uint_as_float(now[i + 1])), s, f2(sum[c + i], sum[c + i + 1]));
+                        sum[c + i] = v.x;
+                        sum[c + i + 1] = v.y;
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR == 2) mbar_arrive_cluster_relaxed(mapa_rank(bar_acce + 8u * buf, 0));
+                    else mbar_arrive_relaxed(bar_acce + 8u * buf);
+                }
+                if (++buf == (uint32_t)kBufs) {
+                    buf = 0;
+                    ++use;
+                }
+            }
+            if (!ok) {
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) sum[i] = __uint_as_float(0x7fffffffu);
+            }
+            if (splits > 1) {
+                // (one tile per cluster) the sums go where the operands were: 4 columns of 32 rows per 512 bytes
+#pragma unroll
+                for (int i = 0; i < kCols; i += 4)
+                    st_shared_v4(base + (uint32_t)((q * BN + c0 + i) * 128 + lane * 16), __float_as_uint(sum[i]), __float_as_uint(sum[i + 1]),
+                                 __float_as_uint(sum[i + 2]), __float_as_uint(sum[i + 3]));
+            } else if constexpr (SWAP) {
+                const int col = n + 32 * q + lane;
+                if (col < p.N) {
+                    float b[8] = {};
+                    if (p.bias) unpack8<DT>(make_uint4(static_cast<const uint16_t*>(p.bias)[col], 0u, 0u, 0u), b);
+                    uint16_t* y = static_cast<uint16_t*>(p.Y) + col;
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i)
+                        if (i < p.M) y[(int64_t)i * p.ldy] = (uint16_t)(pack2<DT>(sum[i] + b[0], 0.0f) & 0xffffu);
+                }
+            } else {
+                const int y = m + (int)rank * 128 + 32 * q;
+#pragma unroll
+                for (int c = 0; c < kCols; c += 32) {
+                    const int col = n + c0 + c;
+                    if (col >= p.N || y >= p.M) continue;
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        if (p.bias && col + i < p.N) {
+                            float b[8];
+                            unpack8<DT>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + col + i), b);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) sum[c + i + e] += b[e];
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) w[(i + e) / 2] = pack2<DT>(sum[c + i + e], sum[c + i + e + 1]);
+                    }
+                    stage_and_store_packed(&tmY, staging + (uint32_t)ew * 2048u, lane, w, col, y);
+                }
+            }
+        }
+        if (!SWAP && lane == 0) bulk_wait0();
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (PAIR == 1 && splits > 1) {
+        if (*abort_flag)  // no sums from this CTA: NaN in their place, and so in the whole tile
+            for (int i = threadIdx.x; i < 128 * BN; i += C::kThreads) reinterpret_cast<uint32_t*>(at)[i] = 0x7fffffffu;
+        cluster_sync_all();  // every CTA's sums are there
+        if (warp >= 4) {
+            int m, n;
+            origin(unit0, m, n);
+            // four columns of 32 rows, over the cluster's CTAs
+            auto four = [&](int q, int c) {
+                const uint32_t from = base + (uint32_t)((q * BN + c) * 128 + lane * 16);
+                float4 x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < splits) x[j] = ld_cluster4(mapa_rank(from, (uint32_t)j));
+#pragma unroll
+                for (int j = 1; j < 8; ++j)
+                    if (j < splits) {
+                        x[0].x += x[j].x;
+                        x[0].y += x[j].y;
+                        x[0].z += x[j].z;
+                        x[0].w += x[j].w;
+                    }
+                return x[0];
+            };
+            if constexpr (SWAP) {
+                for (int u = part + splits * (warp - 4); u < BN; u += splits * kEpi) {  // units of 4 tokens x 32 channels
+                    const int q = u & 3, c = u >> 2 << 2, col = n + 32 * q + lane;
+                    if (c >= p.M) continue;
+                    const float4 s = four(q, c);
+                    if (col >= p.N) continue;
+                    float b[8] = {};
+                    if (p.bias) unpack8<DT>(make_uint4(static_cast<const uint16_t*>(p.bias)[col], 0u, 0u, 0u), b);
+                    const float v[4] = {s.x, s.y, s.z, s.w};
+                    uint16_t* y = static_cast<uint16_t*>(p.Y) + (int64_t)c * p.ldy + col;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (c + i < p.M) y[(int64_t)i * p.ldy] = (uint16_t)(pack2<DT>(v[i] + b[0], 0.0f) & 0xffffu);
+                }
+            } else {
+                for (int u = part + splits * (warp - 4); u < BN / 8; u += splits * kEpi) {  // units of 32 x 32
+                    const int q = u & 3, c = 32 * (u >> 2), col = n + c, y = m + 32 * q;
+                    if (col >= p.N || y >= p.M) continue;
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 s = four(q, c + 4 * i);
+                        v[4 * i] = s.x, v[4 * i + 1] = s.y, v[4 * i + 2] = s.z, v[4 * i + 3] = s.w;
+                    }
+                    if (p.bias) {
+                        float b[32];
+                        bias32<DT>(p.bias, col, p.N, b);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] += b[i];
+                    }
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] = pack2<DT>(v[2 * i], v[2 * i + 1]);
+                    stage_and_store_packed(&tmY, staging + (uint32_t)(warp - 4) * 2048u, lane, w, col, y);
+                }
+                if (lane == 0) bulk_wait0();
+                __syncwarp();
+            }
+        }
+    }
+    if (PAIR == 2 || splits > 1) cluster_sync_all();  // neither leaves while another may still signal or read it
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc<PAIR>(tmem, kTmemCols);
+    }
+}
+
+constexpr int kF8Smem = kSmemBudget;
+
+template <int DT, int PAIR, int BN, bool SWAP>
+cudaError_t f8_prepare(int device) {
+    static SmemOptIn opt_in;
+    return opt_in(kt_linear_fp8_kernel<DT, PAIR, BN, SWAP>, kF8Smem, device);
+}
+
+template <int PAIR, int BN, bool SWAP>
+cudaLaunchConfig_t f8_config(int grid, int cluster, void* stream, cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3(F8<PAIR, BN, SWAP>::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kF8Smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cfg;
+}
+
+// Clusters of ks CTAs that the device holds at once (one CTA per SM, whatever the tile); 0 if it cannot say.
+int f8_clusters(int ks, int device) {
+    static std::atomic<int> known[64][9];  // + 1
+    int n = known[device & 63][ks].load(std::memory_order_relaxed) - 1;
+    if (n >= 0) return n;
+    n = 0;
+    if (f8_prepare<KT_F16, 1, 128, false>(device) == cudaSuccess) {
+        cudaLaunchAttribute attr[2];
+        const cudaLaunchConfig_t cfg = f8_config<1, 128, false>(ks, ks, nullptr, attr);
+        if (cudaOccupancyMaxActiveClusters(&n, kt_linear_fp8_kernel<KT_F16, 1, 128, false>, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+    }
+    known[device & 63][ks].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+template <int PAIR, int BN, bool SWAP>
+kt_status f8_launch(int dtype, const LinearFp8& a, int splits, int sms, int device, void* stream, const char** why) {
+    F8Params p = {};
+    p.M = a.M;
+    p.N = a.N;
+    p.runs = (a.K + kRun - 1) / kRun;
+    p.tiles_m = SWAP ? 1 : (a.M + 128 * PAIR - 1) / (128 * PAIR);
+    p.tiles_n = (a.N + (SWAP ? 128 : BN) - 1) / (SWAP ? 128 : BN);
+    p.idesc = 1u << 4 | (uint32_t)(BN >> 3) << 17 | (uint32_t)(128 * PAIR >> 4) << 24;  // fp32 sums, e4m3 operands, both K-major
+    p.sx = a.sx;
+    p.sw = a.sw;
+    p.bias = a.bias;
+    p.Y = a.Y;
+    p.ldy = a.ldy;
+    p.wait_limit_ns = a.wait_limit_ns;
+    p.stall_ns = a.stall_ns;
+    CUtensorMap tm[3];
+    // bytes in pairs: rows of K / 2 16-bit elements
+    auto encode = [&](CUtensorMap* m, const void* at, int64_t ld, int64_t rows, int box_rows) {
+        const uint64_t dims[2] = {(uint64_t)a.K / 2, (uint64_t)rows}, strides[1] = {(uint64_t)ld};
+        const uint32_t box[2] = {kRun / 2, (uint32_t)box_rows};
+        return encode_tmap_nd(m, at, KT_F16, 2, dims, strides, box, 128, why);
+    };
+    const uint64_t dims[2] = {(uint64_t)a.N, (uint64_t)a.M}, strides[1] = {(uint64_t)a.ldy * 2};
+    const uint32_t box[2] = {kStoreCols, 32};
+    if (SWAP) {
+        if (!encode(tm, a.W, a.ldw, a.N, 128) || !encode(tm + 1, a.Q, a.ldq, a.M, BN)) return KT_ERR_CUDA;
+        tm[2] = tm[0];
+    } else if (!encode(tm, a.Q, a.ldq, a.M, 128) || !encode(tm + 1, a.W, a.ldw, a.N, BN / PAIR) ||
+               !encode_tmap_nd(tm + 2, a.Y, dtype, 2, dims, strides, box, 64, why)) {
+        return KT_ERR_CUDA;
+    }
+    const int tiles = p.tiles_m * p.tiles_n;
+    const int grid = splits > 1 ? tiles * splits : std::min(tiles, sms / PAIR) * PAIR;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = f8_config<PAIR, BN, SWAP>(grid, PAIR * splits, stream, attr);
+    cudaError_t e = dtype == KT_BF16 ? f8_prepare<KT_BF16, PAIR, BN, SWAP>(device) : f8_prepare<KT_F16, PAIR, BN, SWAP>(device);
+    if (e == cudaSuccess)
+        e = dtype == KT_BF16 ? cudaLaunchKernelEx(&cfg, kt_linear_fp8_kernel<KT_BF16, PAIR, BN, SWAP>, tm[0], tm[1], tm[2], p)
+                             : cudaLaunchKernelEx(&cfg, kt_linear_fp8_kernel<KT_F16, PAIR, BN, SWAP>, tm[0], tm[1], tm[2], p);
+    if (e != cudaSuccess) {
+        *why = cudaGetErrorString(e);
+        return KT_ERR_CUDA;
+    }
+    return KT_OK;
+}
+
+}  // namespace
+
+kt_status launch_quantize_fp8(int dtype, const QuantFp8& p, int sms, void* stream, const char** why) {
+    const int runs = (p.K + kRun - 1) / kRun;
+    const bool wide = p.K % 8 == 0 && p.ldx % 8 == 0 && p.ldq % 8 == 0 && (reinterpret_cast<uintptr_t>(p.X) & 15u) == 0 &&
+                      (reinterpret_cast<uintptr_t>(p.Q) & 7u) == 0;
+    const int64_t blocks = ((int64_t)p.M * runs + kQuantThreads / 16 - 1) / (kQuantThreads / 16);
+    const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)sms * 32);
+    auto go = [&](auto kern) { return launch_pdl(kern, grid, (unsigned)kQuantThreads, (size_t)0, stream, p, runs); };
+    const cudaError_t e = dtype == KT_BF16 ? (wide ? go(kt_quantize_fp8_kernel<KT_BF16, true>) : go(kt_quantize_fp8_kernel<KT_BF16, false>))
+                                           : (wide ? go(kt_quantize_fp8_kernel<KT_F16, true>) : go(kt_quantize_fp8_kernel<KT_F16, false>));
+    if (e != cudaSuccess) {
+        *why = cudaGetErrorString(e);
+        return KT_ERR_CUDA;
+    }
+    return KT_OK;
+}
+
+Fp8Shape linear_fp8_shape(const LinearFp8& a, int sms, int device) {
+    const int runs = (a.K + kRun - 1) / kRun;
+    Fp8Shape best = {};
+    double least = 1e30;
+    auto consider = [&](int pair, int bn, int swap, int64_t tiles, double step, double round) {
+        const int64_t units = sms / pair, rounds = (tiles + units - 1) / units;
+        const double time = rounds * (runs * step + 0.7) + round;
+        if (time < least) {
+            least = time;
+            best = {pair, bn, swap, 1};
+        }
+        if (pair == 2) return;
+        for (int ks = 2; ks <= 8; ks *= 2) {
+            if (tiles * ks > sms || runs < 2 * ks || tiles > f8_clusters(ks, device)) continue;
+            const double split = (runs + ks - 1) / ks * step + round + 2.0;
+            if (split < least) {
+                least = split;
+                best = {1, bn, swap, ks};
+            }
+        }
+    };
+    if (a.M <= KT_LINEAR_FP8_FEW) {
+        consider(1, a.M <= 16 ? 16 : a.M <= 32 ? 32 : 64, 1, (a.N + 127) / 128, 0.20, 3.0);
+        return best;
+    }
+    auto tiles = [&](int rows, int bn) { return (int64_t)((a.M + rows - 1) / rows) * ((a.N + bn - 1) / bn); };
+    consider(2, 256, 0, tiles(256, 256), 0.36, 4.0);
+    consider(2, 128, 0, tiles(256, 128), 0.25, 3.5);
+    consider(1, 128, 0, tiles(128, 128), 0.26, 3.0);
+    return best;
+}
+
+kt_status launch_linear_fp8_as(int dtype, const LinearFp8& a, const Fp8Shape& s, int sms, int device, void* stream, const char** why) {
+    if (s.swap) {
+        if (s.BN == 16) return f8_launch<1, 16, true>(dtype, a, s.splits, sms, device, stream, why);
+        if (s.BN == 32) return f8_launch<1, 32, true>(dtype, a, s.splits, sms, device, stream, why);
+        return f8_launch<1, 64, true>(dtype, a, s.splits, sms, device, stream, why);
+    }
+    if (s.pair == 1) return f8_launch<1, 128, false>(dtype, a, s.splits, sms, device, stream, why);
+    if (s.BN == 128) return f8_launch<2, 128, false>(dtype, a, 1, sms, device, stream, why);
+    return f8_launch<2, 256, false>(dtype, a, 1, sms, device, stream, why);
+}
+
+kt_status launch_linear_fp8(int dtype, const LinearFp8& a, int sms, int device, void* stream, const char** why) {
+    return launch_linear_fp8_as(dtype, a, linear_fp8_shape(a, sms, device), sms, device, stream, why);
+}
+
+kt_status linear_fp8_status(void* stream, int* word, const char** why) { return error_word(g_fp8_error, stream, word, why); }
+
+}  // namespace kt

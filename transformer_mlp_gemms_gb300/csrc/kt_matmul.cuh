@@ -14,6 +14,16 @@ __device__ __forceinline__ void band_tile(int t, int tiles_m, int tiles_n, int& 
     tm = band * kBand + in - tn * rows;
 }
 
+// As wait_phase, for waits that many warps enter often: the timer is read only after some tries, each of which
+// already suspends the thread for a while.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait_turn(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int code, unsigned long long limit_ns) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+        if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    return wait_phase<CLUSTER>(bar, parity, abort_flag, err, code, limit_ns);
+}
+
 __device__ __forceinline__ uint32_t cluster_size() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));

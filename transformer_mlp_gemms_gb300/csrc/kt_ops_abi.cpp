@@ -589,12 +589,54 @@ kt_status kt_adamw(int64_t count, const kt_adamw_tensor* tensors, const kt_adamw
     return done(kt::launch_adamw(e, live, a, sms, stream, &why), why);
 }
 
+kt_status kt_quantize_fp8(int64_t M, int64_t K, kt_dtype dtype, kt_act act, const void* X, int64_t ldx, void* Q, int64_t ldq,
+                          float* scale, void* stream) {
+    if (M < 0 || K < 1) return bad("the row count must not be negative and the row length at least 1");
+    if (!known_dtype(dtype)) return bad("unknown dtype");
+    if (!known_act(act)) return bad("unknown activation");
+    if (M > INT32_MAX / 2 || K > (1 << 24)) return kt::report(KT_ERR_UNSUPPORTED, "M above 2^30 or K above 2^24");
+    if (ldx < (act == KT_ACT_GEGLU ? 2 * K : K) || ldq < K) return bad("a row pitch is below the row length");
+    if (M > 0 && (!X || !Q || !scale)) return bad("X, Q and scale must be non-NULL");
+    if (!aligned(X, 2) || !aligned(scale, 4)) return bad("a pointer is not aligned to its elements");
+    if (M == 0) return done(KT_OK, "");
+    kt_status s;
+    int dev, sms;
+    if ((s = current_device(&dev, &sms)) != KT_OK) return s;
+    const char* why = "";
+    kt::QuantFp8 p = {X, static_cast<uint8_t*>(Q), scale, ldx, ldq, (int)M, (int)K, epilogue_of(act)};
+    return done(kt::launch_quantize_fp8(dtype, p, sms, stream, &why), why);
+}
+
+kt_status kt_linear_fp8(int64_t M, int64_t N, int64_t K, kt_dtype dtype, const void* Q, int64_t ldq, const void* W, int64_t ldw,
+                        const float* scale_x, const float* scale_w, const void* bias, void* Y, int64_t ldy, void* stream) {
+    if (M < 0 || N < 1 || K < 1) return bad("M must not be negative, N and K at least 1");
+    if (!known_dtype(dtype)) return bad("unknown dtype");
+    if (ldq < K || ldw < K || ldy < N) return bad("a row pitch is below the row length");
+    if ((M > 0 && (!Q || !scale_x || !Y)) || !W || !scale_w) return bad("Q, W, scale_x, scale_w and Y must be non-NULL");
+    if (!aligned(Q, 16) || !aligned(W, 16) || !aligned(Y, 16) || !aligned(bias, 16)) return bad("Q, W, Y and bias must be 16-byte aligned");
+    if (!aligned(scale_x, 4) || !aligned(scale_w, 4)) return bad("a pointer is not aligned to its elements");
+    if (K % 16 || ldq % 16 || ldw % 16 || N % 8 || ldy % 8)
+        return kt::report(KT_ERR_UNSUPPORTED, "K and the pitches of Q and W must be multiples of 16, N and Y's pitch of 8");
+    if (M > INT32_MAX / 2 || N > (1 << 24) || K > (1 << 24) || ldq > (int64_t)1 << 38 || ldw > (int64_t)1 << 38 || ldy > (int64_t)1 << 38)
+        return kt::report(KT_ERR_UNSUPPORTED, "M above 2^30, N or K above 2^24, or a pitch above 2^38");
+    if (M == 0) return done(KT_OK, "");
+    kt_status s;
+    int dev, sms;
+    if ((s = current_device(&dev, &sms)) != KT_OK) return s;
+    const char* why = "";
+    const unsigned long long stall_ns = 1000ull * (unsigned long long)g_matmul_stall_us.load(std::memory_order_relaxed);
+    kt::LinearFp8 a = {Q, W, scale_x, scale_w, bias, Y, ldq, ldw, ldy, (int)M, (int)N, (int)K, stall_ns ? stall_ns : kWaitLimitNs, stall_ns};
+    return done(kt::launch_linear_fp8(dtype, a, sms, dev, stream, &why), why);
+}
+
 kt_status kt_matmul_status(void* stream) {
-    int dev, sms, word = 0;
+    int dev, sms, word = 0, word8 = 0;
     kt_status s;
     if ((s = current_device(&dev, &sms)) != KT_OK) return s;
     const char* why = "";
-    if ((s = kt::matmul_status(stream, &word, &why)) != KT_OK) return kt::report(s, why);
+    if ((s = kt::matmul_status(stream, &word, &why)) != KT_OK || (s = kt::linear_fp8_status(stream, &word8, &why)) != KT_OK)
+        return kt::report(s, why);
+    if (word == 0) word = word8;
     if (word == 0) return done(KT_OK, "");
     return kt::report(KT_ERR_TIMEOUT, word == kt::DEV_INJECTED_STALL ? "a bounded device wait ran out (injected stall)"
                                                                      : "a bounded device wait ran out");

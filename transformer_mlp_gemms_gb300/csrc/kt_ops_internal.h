@@ -144,6 +144,33 @@ struct AdamwStep {
 };
 kt_status launch_adamw(const AdamwEntry* e, int count, const AdamwStep& s, int sms, void* stream, const char** why);
 
+// The linear layer in 8-bit floating point, and its quantiser (kt_linear_fp8.cu).
+struct QuantFp8 {
+    const void* X;
+    uint8_t* Q;
+    float* scale;  // [M][ceil(K / 128)]
+    int64_t ldx, ldq;
+    int M, K, act;  // act: an Epi
+};
+kt_status launch_quantize_fp8(int dtype, const QuantFp8& p, int sms, void* stream, const char** why);
+struct LinearFp8 {
+    const void *Q, *W;
+    const float *sx, *sw;
+    const void* bias;
+    void* Y;
+    int64_t ldq, ldw, ldy;
+    int M, N, K;
+    unsigned long long wait_limit_ns, stall_ns;
+};
+// CTAs per tile, channels (or, swap, tokens) per tile, whether the weights are the first operand, CTAs that share a tile's runs.
+struct Fp8Shape {
+    int pair, BN, swap, splits;
+};
+Fp8Shape linear_fp8_shape(const LinearFp8& a, int sms, int device);
+kt_status launch_linear_fp8_as(int dtype, const LinearFp8& a, const Fp8Shape& s, int sms, int device, void* stream, const char** why);
+kt_status launch_linear_fp8(int dtype, const LinearFp8& a, int sms, int device, void* stream, const char** why);
+kt_status linear_fp8_status(void* stream, int* word, const char** why);
+
 // Opt a kernel in to `bytes` of dynamic shared memory on the current device, once per device: the
 // attribute stays.  `done` belongs to the kernel (a static of its launch function).
 struct SmemOptIn {

@@ -427,6 +427,39 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// quantize_fp8(X, Q, scale, act, stream)
+PyObject* quantize_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 5, [&] {
+        const at::Tensor &X = matrix(a[0], "X"), &Q = matrix(a[1], "Q");
+        const int64_t M = Q.size(0), K = Q.size(1), act = integer(a[3], "act");
+        const c10::Device dev = Q.device();
+        const kt_dtype c = code(X, "X");
+        const Rows x = rows(X, "X", M, act == KT_ACT_GEGLU ? 2 * K : K, X.scalar_type(), dev), q = rows(Q, "Q", M, K, at::kFloat8_e4m3fn, dev);
+        if (a[2] == Py_None) refuse("scale", "a torch tensor expected");
+        void* scale = whole(a[2], "scale", {M, (K + 127) / 128}, at::kFloat, dev);
+        void* s = stream_of(a[4], dev);
+        return kt_quantize_fp8(M, K, c, (kt_act)act, x.p, x.ld, q.p, q.ld, (float*)scale, s);
+    });
+}
+
+// linear_fp8(Q, scale_x, W, scale_w, bias, Y, stream)
+PyObject* linear_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 7, [&] {
+        const at::Tensor &Q = matrix(a[0], "Q"), &W = matrix(a[2], "W"), &Y = matrix(a[5], "Y");
+        const int64_t M = Q.size(0), K = Q.size(1), N = W.size(0);
+        const c10::Device dev = Q.device();
+        const kt_dtype c = code(Y, "Y");
+        const Rows q = rows(Q, "Q", M, K, at::kFloat8_e4m3fn, dev, 16), w = rows(W, "W", N, K, at::kFloat8_e4m3fn, dev, 16),
+                   y = rows(Y, "Y", M, N, Y.scalar_type(), dev, 8);
+        if (a[1] == Py_None || a[3] == Py_None) refuse("scale_x and scale_w", "torch tensors expected");
+        void* sx = whole(a[1], "scale_x", {M, (K + 127) / 128}, at::kFloat, dev);
+        void* sw = whole(a[3], "scale_w", {(N + 127) / 128, (K + 127) / 128}, at::kFloat, dev);
+        void* bias = whole(a[4], "bias", {N}, Y.scalar_type(), dev);
+        void* s = stream_of(a[6], dev);
+        return kt_linear_fp8(M, N, K, c, q.p, q.ld, w.p, w.ld, (const float*)sx, (const float*)sw, bias, y.p, y.ld, s);
+    });
+}
+
 PyMethodDef kMethods[] = {
     {"layernorm_forward", (PyCFunction)(void*)layernorm_forward, METH_FASTCALL, nullptr},
     {"layernorm_backward", (PyCFunction)(void*)layernorm_backward, METH_FASTCALL, nullptr},
@@ -438,6 +471,8 @@ PyMethodDef kMethods[] = {
     {"linear_forward", (PyCFunction)(void*)linear_forward, METH_FASTCALL, nullptr},
     {"linear_backward", (PyCFunction)(void*)linear_backward, METH_FASTCALL, nullptr},
     {"adamw", (PyCFunction)(void*)adamw, METH_FASTCALL, nullptr},
+    {"quantize_fp8", (PyCFunction)(void*)quantize_fp8, METH_FASTCALL, nullptr},
+    {"linear_fp8", (PyCFunction)(void*)linear_fp8, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_kt_ops", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

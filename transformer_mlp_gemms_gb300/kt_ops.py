@@ -30,6 +30,7 @@ KT_LAYERNORM_MAX_D = 16384
 KT_LINEAR_I8_DOT_ROWS = 16
 KT_MOE_MAX_TOKENS, KT_MOE_MAX_EXPERTS, KT_MOE_MAX_TOP_K = 64, 256, 16
 KT_F32, KT_ADAMW_BLOCK = 2, 256
+KT_LINEAR_FP8_FEW = 64
 
 
 class kt_moe_options(ctypes.Structure):
@@ -75,6 +76,8 @@ SIGNATURES = {
     "kt_linear_backward_workspace": ([_I64] * 3, ctypes.c_size_t),
     "kt_linear_backward": ([_I64] * 3 + [_I32] + [_VP, _I64] * 2 + [_VP, _VP, _I64, _VP, _VP, _VP, ctypes.c_size_t, _VP], _I32),
     "kt_adamw": ([_I64, ctypes.POINTER(kt_adamw_tensor), ctypes.POINTER(kt_adamw_options), _VP], _I32),
+    "kt_quantize_fp8": ([_I64, _I64, _I32, _I32, _VP, _I64, _VP, _I64, _VP, _VP], _I32),
+    "kt_linear_fp8": ([_I64, _I64, _I64, _I32, _VP, _I64, _VP, _I64, _VP, _VP, _VP, _VP, _I64, _VP], _I32),
     "kt_matmul_status": ([_VP], _I32),
     "kt_matmul_debug_stall": ([_I32, _I64], _I32),
 }
@@ -283,6 +286,21 @@ def kt_adamw(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, we
                                  grad_scale, stream)
     if r is not None:
         _fail(r, "kt_adamw")
+
+
+def kt_quantize_fp8(X, Q, scale, act: int = KT_ACT_NONE, stream=None) -> None:
+    """Q (float8_e4m3fn [M][K]) and scale (fp32 [M][ceil(K / 128)]) of act(X); X is [M][K], or [M][2K] for
+    KT_ACT_GEGLU."""
+    r = (_ext or _calls()).quantize_fp8(X, Q, scale, act, stream)
+    if r is not None:
+        _fail(r, "kt_quantize_fp8")
+
+
+def kt_linear_fp8(Q, scale_x, W, scale_w, bias, Y, stream=None) -> None:
+    """Y = (Q scale_x) (W scale_w)^T (+ bias), scales for runs of 128 columns and blocks of 128 x 128."""
+    r = (_ext or _calls()).linear_fp8(Q, scale_x, W, scale_w, bias, Y, stream)
+    if r is not None:
+        _fail(r, "kt_linear_fp8")
 
 
 def kt_matmul_status(stream=None) -> int:
