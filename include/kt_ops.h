@@ -246,8 +246,8 @@ kt_status kt_linear_forward(int64_t M, int64_t N, int64_t K, kt_dtype dtype, con
 
 /*
  * kt_linear_backward -- its gradients: dX[M][K] = dY . W, dW[N][K] = dY^T . X, db[N] = sum of dY over the
- * tokens (fp32); each may be NULL.  M = 0 writes zeros to dW and db.  The workspace
- * (kt_linear_backward_workspace bytes, 16-byte aligned) is needed with db alone.
+ * tokens (fp32); each may be NULL.  M = 0 writes zeros to dW and db.  workspace: kt_linear_backward_workspace
+ * bytes, as kt_glu_backward's.
  */
 kt_status kt_linear_backward(int64_t M, int64_t N, int64_t K, kt_dtype dtype, const void* dY, int64_t lddy, const void* X,
                              int64_t ldx, const void* W, void* dX, int64_t lddx, void* dW, float* db, void* workspace,

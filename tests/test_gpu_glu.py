@@ -109,13 +109,14 @@ def test_gated_gradients(M, D, F, dtype, bias):
     if bias:
         near(db, dbx, tb)
     assert dxs[:, D:].isnan().all()
-    # each gradient alone
-    only = torch.empty_like(dx)
-    kt_ops.kt_glu_backward(dh, p, x, w, only, None, None, ACTS[name], ws)
-    assert torch.equal(only, dx)
-    only = torch.empty_like(dw)
-    kt_ops.kt_glu_backward(dh, p, x, w, None, only, None, ACTS[name], ws)
-    assert torch.equal(only, dw)
+    # the same bits again; and each gradient alone, whose sums may be shared out in another way
+    again = [torch.empty_like(dx), torch.empty_like(dw)]
+    kt_ops.kt_glu_backward(dh, p, x, w, *again, None, ACTS[name], ws)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+    kt_ops.kt_glu_backward(dh, p, x, w, again[0].fill_(float("nan")), None, None, ACTS[name], ws)
+    near(again[0], dxx, tx)
+    kt_ops.kt_glu_backward(dh, p, x, w, None, again[1].fill_(float("nan")), None, ACTS[name], ws)
+    near(again[1], dwx, tw)
 
 
 # also long sums of few tiles, which a cluster shares
@@ -137,7 +138,7 @@ def test_linear_layer(M, N, K, dtype, bias):
     dxs, dx = nans(M, K, dt, 16)
     dw = torch.full((N, K), float("nan"), dtype=dt, device="cuda")
     db = torch.full((N,), float("nan"), device="cuda") if bias else None
-    kt_ops.kt_linear_backward(dy, x, w, dx, dw, db, kt_ops.linear_backward_workspace(M, N, K) if bias else None)
+    kt_ops.kt_linear_backward(dy, x, w, dx, dw, db, kt_ops.linear_backward_workspace(M, N, K))
     assert kt_ops.kt_matmul_status() == kt_mlp.KT_OK
     dxx, tx, dwx, tw, dbx, tb = ref.linear_backward(dy, x, w, dt)
     near(dx, dxx, tx)

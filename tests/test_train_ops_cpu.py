@@ -78,7 +78,7 @@ def test_workspace_sizes(lib):
     assert linear(-1, 64, 64) == linear(4, 4, 64) == linear(4, 64, 0) == 0
     assert glu(0, 64, 64) >= 2 * 64 * 4 and linear(0, 64, 64) >= 64 * 4
     assert glu(1000, 64, 64) >= 1000 * 2 * 64 * 2 + 2 * 64 * 4
-    assert linear(1 << 20, 64, 64) <= 128 * 64 * 4
+    assert linear(1 << 20, 64, 64) <= 128 * 64 * 4 + (42 << 20)  # partial sums of at most 80 pairs of CTAs, two tiles each
 
 
 def adamw(lib, tensor, options, count=1):

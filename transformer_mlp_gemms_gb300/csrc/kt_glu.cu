@@ -81,6 +81,17 @@ __device__ __forceinline__ uint4 pack_pairs(const f32x2 (&f)[4]) {
     return make_uint4(pack2<DT>(f[0].x, f[0].y), pack2<DT>(f[1].x, f[1].y), pack2<DT>(f[2].x, f[2].y), pack2<DT>(f[3].x, f[3].y));
 }
 
+// The counters of the products behind this kernel.
+__device__ __forceinline__ void zero_counters(int* at) {
+    if (at && blockIdx.x == 0 && blockIdx.y == 0)
+        for (int i = threadIdx.x; i < (int)(kGradientsCounters / sizeof(int)); i += blockDim.x) at[i] = 0;
+}
+__global__ void __launch_bounds__(256) kt_zero_kernel(int* at) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    zero_counters(at);
+}
+
 // Block (x, y): 256 hidden columns, rows [y per, (y + 1) per); a warp takes every eighth row, four of them
 // on their way at a time.  EPI < 0: the sums of dh alone.
 template <int DT, int EPI>
@@ -88,6 +99,7 @@ __global__ void __launch_bounds__(kGluThreads) kt_glu_backward_kernel(const GluB
     constexpr bool GATED = EPI >= 0;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    zero_counters(p.zero);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = (int)blockIdx.x * kGluCols + 8 * lane;
     const bool mine = col < p.F;
@@ -211,6 +223,13 @@ cudaError_t glu_dispatch(const GluBackward& p, int rows, int per, void* stream) 
 int column_sum_rows(int64_t M, int64_t F) {
     const int64_t across = (F + kGluCols - 1) / kGluCols, most = (M + 31) / 32;
     return (int)std::max<int64_t>(1, std::min({most, (1216 + across - 1) / across, (int64_t)128}));
+}
+
+kt_status launch_zero(int* at, void* stream, const char** why) {
+    const cudaError_t e = launch_pdl(kt_zero_kernel, 1u, 256u, (size_t)0, stream, at);
+    if (e == cudaSuccess) return KT_OK;
+    *why = cudaGetErrorString(e);
+    return KT_ERR_CUDA;
 }
 
 kt_status launch_glu_backward(int dtype, const GluBackward& p, void* stream, const char** why) {

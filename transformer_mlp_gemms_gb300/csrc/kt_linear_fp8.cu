@@ -114,23 +114,6 @@ __global__ void __launch_bounds__(kQuantThreads) kt_quantize_fp8_kernel(const Qu
 // The linear layer
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
 struct F8Params {
     int M, N, runs, tiles_m, tiles_n, stages;
     uint32_t idesc;
@@ -173,7 +156,7 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
     uint32_t* const words = reinterpret_cast<uint32_t*>(at + (bars - base) + 304u);
     volatile int* const abort_flag = reinterpret_cast<volatile int*>(words + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (uniform for the compiler)
     const unsigned long long limit = p.wait_limit_ns;
     const uint32_t rank = PAIR == 2 ? (cluster_ctarank() & 1u) : 0u;
     const int splits = PAIR == 1 ? (int)cluster_size() : 1, part = PAIR == 1 ? (int)cluster_ctarank() : 0;
@@ -223,32 +206,34 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
     };
 
     if (warp == 0 || warp == 2) {
-        // ------------------- copies -------------------
-        if (lane == 0) {
-            const bool a_role = warp == 0;
-            uint32_t stage = 0, phase = 0, used = 0, used_phase = 0;
-            if (a_role && p.stall_ns && blockIdx.x == 0)  // the tests' hook: nobody signals this barrier
-                wait_phase(bar_stall, 0, abort_flag, &g_fp8_error, DEV_INJECTED_STALL, p.stall_ns);
-            for (int t = unit0; t < tiles && !*abort_flag; t += units) {
-                int m, n;
-                origin(t, m, n);
-                const int a_row = SWAP ? n : m + (int)rank * 128, b_row = SWAP ? m : n + (int)rank * (BN / PAIR);
-                for (int j = 0; j < runs; ++j) {
-                    if (!wait_turn(bar_empty + 8u * stage, phase ^ 1u, abort_flag, &g_fp8_error, DEV_TIMEOUT_PRODUCER, limit)) break;
-                    const uint32_t sA = base + stage * C::kStage;
-                    const uint32_t fb = PAIR == 2 ? mapa_rank(bar_full + 8u * stage, 0) : bar_full + 8u * stage;
-                    if (a_role && leader) mbar_arrive_expect_tx(bar_full + 8u * stage, PAIR * C::kStage);
-                    const int x = (run0 + j) * (kRun / 2);  // the maps count pairs of bytes
-                    if constexpr (PAIR == 2) tma_load_2d_pair(a_role ? sA : sA + kF8ABytes, a_role ? &tmA : &tmB, fb, x, a_role ? a_row : b_row);
-                    else tma_load_2d(a_role ? sA : sA + kF8ABytes, a_role ? &tmA : &tmB, fb, x, a_role ? a_row : b_row);
-                    used |= 1u << stage;
-                    used_phase = (used_phase & ~(1u << stage)) | (phase << stage);
-                    if (++stage == (uint32_t)kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+        // ------------------- copies: one lane issues what the whole warp has in uniform registers -------------------
+        const bool a_role = warp == 0;
+        const uint32_t one = lane == 0, arm = one && leader;
+        uint32_t stage = 0, phase = 0, used = 0, used_phase = 0;
+        bool ok = true;
+        if (a_role && p.stall_ns && blockIdx.x == 0)  // the tests' hook: nobody signals this barrier
+            ok = __all_sync(0xffffffffu, wait_phase(bar_stall, 0, abort_flag, &g_fp8_error, DEV_INJECTED_STALL, p.stall_ns));
+        const uint32_t full0 = PAIR == 2 ? mapa_rank(bar_full, 0) : bar_full;
+        const CUtensorMap* const map = a_role ? &tmA : &tmB;
+        for (int t = unit0; t < tiles && ok; t += units) {
+            int m, n;
+            origin(t, m, n);
+            const int row = a_role ? (SWAP ? n : m + (int)rank * 128) : (SWAP ? m : n + (int)rank * (BN / PAIR));
+            for (int j = 0; j < runs; ++j) {
+                ok = __all_sync(0xffffffffu, wait_turn(bar_empty + 8u * stage, phase ^ 1u, abort_flag, &g_fp8_error, DEV_TIMEOUT_PRODUCER, limit));
+                if (!ok) break;
+                if (a_role) expect_tx_if(bar_full + 8u * stage, PAIR * C::kStage, arm);
+                // the maps count pairs of bytes
+                load_if<PAIR>(base + stage * C::kStage + (a_role ? 0u : kF8ABytes), map, full0 + 8u * stage, (run0 + j) * (kRun / 2), row, one);
+                used |= 1u << stage;
+                used_phase = (used_phase & ~(1u << stage)) | (phase << stage);
+                if (++stage == (uint32_t)kStages) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
+        }
+        if (lane == 0) {
             if (*abort_flag) {  // no copy may still be on its way into memory that is about to be released
                 if (a_role && leader)
                     for (int s = 0; s < kStages; ++s)
@@ -258,33 +243,26 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
             }
         }
     } else if (warp == 1) {
-        // ------------------- products -------------------
-        if (lane == 0 && leader) {
+        // ------------------- products, likewise -------------------
+        if (leader) {
+            const uint32_t one = lane == 0;
             uint32_t stage = 0, phase = 0, buf = 0, use = 0;
             const uint64_t ad0 = smem_desc(base, 16u, 1024u), bd0 = smem_desc(base + kF8ABytes, 16u, 1024u);
             bool ok = true, any = false;
             for (int t = unit0; t < tiles && ok; t += units)
                 for (int j = 0; j < runs; ++j) {
-                    const uint32_t fb = bar_full + 8u * stage, ab = bar_acce + 8u * buf;
-                    ok = (mbar_test_wait(fb, phase) || wait_turn(fb, phase, abort_flag, &g_fp8_error, DEV_TIMEOUT_MMA, limit)) &&
-                         wait_turn<PAIR == 2>(ab, (use & 1u) ^ 1u, abort_flag, &g_fp8_error, DEV_TIMEOUT_MMA, limit);
+                    ok = __all_sync(0xffffffffu,
+                                    wait_turn(bar_full + 8u * stage, phase, abort_flag, &g_fp8_error, DEV_TIMEOUT_MMA, limit) &&
+                                        wait_turn<PAIR == 2>(bar_acce + 8u * buf, (use & 1u) ^ 1u, abort_flag, &g_fp8_error, DEV_TIMEOUT_MMA, limit));
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t d = tmem + buf * (uint32_t)BN;
                     const uint64_t ad = ad0 + stage * (C::kStage >> 4), bd = bd0 + stage * (C::kStage >> 4);
 #pragma unroll
-                    for (uint32_t k = 0; k < 4; ++k) {  // 32 columns each
-                        if constexpr (PAIR == 2) mma_f8_pair(d, ad + 2 * k, bd + 2 * k, p.idesc, k > 0);
-                        else mma_f8(d, ad + 2 * k, bd + 2 * k, p.idesc, k > 0);
-                    }
+                    for (uint32_t k = 0; k < 4; ++k) mma_if<PAIR, true>(d, ad + 2 * k, bd + 2 * k, p.idesc, k > 0, one);  // 32 columns each
                     any = true;
-                    if constexpr (PAIR == 2) {
-                        mma_commit_pair(bar_empty + 8u * stage);
-                        mma_commit_pair(bar_accf + 8u * buf);
-                    } else {
-                        mma_commit(bar_empty + 8u * stage);
-                        mma_commit(bar_accf + 8u * buf);
-                    }
+                    commit_if<PAIR>(bar_empty + 8u * stage, one);
+                    commit_if<PAIR>(bar_accf + 8u * buf, one);
                     if (++stage == (uint32_t)kStages) {
                         stage = 0;
                         phase ^= 1u;
@@ -294,10 +272,9 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
                         ++use;
                     }
                 }
-            if (*abort_flag && any) {  // no product may still be running when tensor memory is freed
-                if constexpr (PAIR == 2) mma_commit_pair(bar_drain);
-                else mma_commit(bar_drain);
-                wait_drain(bar_drain, 0u, 100000000ull);
+            if (!ok && any) {  // no product may still be running when tensor memory is freed
+                commit_if<PAIR>(bar_drain, one);
+                if (lane == 0) wait_drain(bar_drain, 0u, 100000000ull);
             }
         }
         __syncwarp();

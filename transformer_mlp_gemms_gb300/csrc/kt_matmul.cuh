@@ -24,6 +24,58 @@ __device__ __forceinline__ bool wait_turn(uint32_t bar, uint32_t parity, volatil
     return wait_phase<CLUSTER>(bar, parity, abort_flag, err, code, limit_ns);
 }
 
+// What one thread issues, called by a whole warp with the same arguments and `one` in one lane: the arguments are then in
+// uniform registers, where these instructions read them.  From a branch of a single lane each would be moved there
+// first, and a step of the ring took 0.28 us however few products it had.
+__device__ __forceinline__ void expect_tx_if(uint32_t bar, uint32_t bytes, uint32_t one) {
+    asm volatile("{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %2, 0;\n\t@l mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes),
+                 "r"(one)
+                 : "memory");
+}
+template <int PAIR>
+__device__ __forceinline__ void load_if(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int x, int y, uint32_t one) {
+    if constexpr (PAIR == 2)
+        asm volatile(
+            "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %5, 0;\n\t"
+            "@l cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(y), "r"(one)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %5, 0;\n\t"
+            "@l cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(y), "r"(one)
+            : "memory");
+}
+#define KT_MMA_IF(group, kind)                                                                                          \
+    asm volatile("{\n\t.reg .pred p, l;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %5, 0;\n\t"                           \
+                 "@l tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(ad), "l"(bd), \
+                 "r"(idesc), "r"(accumulate), "r"(one)                                                                \
+                 : "memory")
+template <int PAIR, bool FP8>
+__device__ __forceinline__ void mma_if(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accumulate, uint32_t one) {
+    if constexpr (PAIR == 2 && FP8) KT_MMA_IF("2", "f8f6f4");
+    else if constexpr (PAIR == 2) KT_MMA_IF("2", "f16");
+    else if constexpr (FP8) KT_MMA_IF("1", "f8f6f4");
+    else KT_MMA_IF("1", "f16");
+}
+#undef KT_MMA_IF
+// Arrive on the barrier (at this offset in both CTAs of a pair) once all products so far are done.
+template <int PAIR>
+__device__ __forceinline__ void commit_if(uint32_t bar, uint32_t one) {
+    if constexpr (PAIR == 2)
+        asm volatile(
+            "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %2, 0;\n\t"
+            "@l tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+            "h"((unsigned short)3), "r"(one)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %1, 0;\n\t"
+            "@l tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(one)
+            : "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_size() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));

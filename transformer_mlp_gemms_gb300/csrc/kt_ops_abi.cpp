@@ -90,35 +90,35 @@ kt::Matmul product(int64_t M, int64_t N, int64_t K) {
     a.wait_limit_ns = a.stall_ns ? a.stall_ns : kWaitLimitNs;
     return a;
 }
-// What dX = dP . W and dW = dP^T . X have in common, for dP [M][N], W [N][K], X [M][K].
+// dX = dP . W and dW = dP^T . X in one launch, for dP [M][N], W [N][K], X [M][K].  scratch: as launch_gradients has it.
 kt_status gradients(int64_t M, int64_t N, int64_t K, int dtype, const void* dP, int64_t lddp, const void* X, int64_t ldx, const void* W,
-                    void* dX, int64_t lddx, void* dW, int sms, int device, void* stream) {
-    const char* why = "";
-    kt_status s = KT_OK;
+                    void* dX, int64_t lddx, void* dW, void* scratch, int sms, int device, void* stream) {
+    kt::Matmul a[2];
+    int count = 0;
     if (dW) {
-        kt::Matmul a = product(N, K, M);
-        a.A = dP;
-        a.lda = lddp;
-        a.a_mn = true;
-        a.B = X;
-        a.ldb = ldx;
-        a.b_mn = true;
-        a.C = dW;
-        a.ldc = K;
-        s = kt::launch_matmul(dtype, a, sms, device, stream, &why);
+        kt::Matmul& w = a[count++] = product(N, K, M);
+        w.A = dP;
+        w.lda = lddp;
+        w.a_mn = true;
+        w.B = X;
+        w.ldb = ldx;
+        w.b_mn = true;
+        w.C = dW;
+        w.ldc = K;
     }
-    if (s == KT_OK && dX) {
-        kt::Matmul a = product(M, K, N);
-        a.A = dP;
-        a.lda = lddp;
-        a.B = W;
-        a.ldb = K;
-        a.b_mn = true;
-        a.C = dX;
-        a.ldc = lddx;
-        s = kt::launch_matmul(dtype, a, sms, device, stream, &why);
+    if (dX) {
+        kt::Matmul& x = a[count++] = product(M, K, N);
+        x.A = dP;
+        x.lda = lddp;
+        x.B = W;
+        x.ldb = K;
+        x.b_mn = true;
+        x.C = dX;
+        x.ldc = lddx;
     }
-    return done(s, why);
+    if (!count) return done(KT_OK, "");
+    const char* why = "";
+    return done(kt::launch_gradients(dtype, a, count, scratch, sms, device, stream, &why), why);
 }
 kt_status zeros(void* p, size_t bytes, void* stream) {
     if (!p || !bytes) return KT_OK;
@@ -126,6 +126,7 @@ kt_status zeros(void* p, size_t bytes, void* stream) {
     return e == cudaSuccess ? KT_OK : cuda_failed("cudaMemsetAsync", e);
 }
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+const size_t kScratch = kt::kGradientsCounters + kt::gradients_partials();  // of launch_gradients
 int epilogue_of(int act) { return kt::up_epilogue(act); }
 
 }  // namespace
@@ -414,7 +415,7 @@ kt_status kt_glu_forward(int64_t M, int64_t D, int64_t F, kt_dtype dtype, kt_act
 
 size_t kt_glu_backward_workspace(int64_t M, int64_t D, int64_t F) {
     if (M < 0 || M > INT32_MAX / 2 || D < 8 || D % 8 || D > (1 << 24) || F < 8 || F % 8 || F > (1 << 24)) return 0;
-    return up256((size_t)(M ? M : 1) * 4 * (size_t)F) + (size_t)kt::column_sum_rows(M, F) * 2 * (size_t)F * sizeof(float);
+    return up256((size_t)(M ? M : 1) * 4 * (size_t)F) + up256((size_t)kt::column_sum_rows(M, F) * 2 * (size_t)F * sizeof(float)) + kScratch;
 }
 
 kt_status kt_glu_backward(int64_t M, int64_t D, int64_t F, kt_dtype dtype, kt_act act, const void* dH, int64_t lddh,
@@ -437,6 +438,8 @@ kt_status kt_glu_backward(int64_t M, int64_t D, int64_t F, kt_dtype dtype, kt_ac
         if ((s = zeros(dW, (size_t)4 * F * D, stream)) != KT_OK || (s = zeros(db, (size_t)8 * F, stream)) != KT_OK) return s;
         return done(KT_OK, "");
     }
+    char* const sums = static_cast<char*>(workspace) + up256((size_t)M * 4 * (size_t)F);
+    char* const scratch = sums + up256((size_t)kt::column_sum_rows(M, F) * 2 * (size_t)F * sizeof(float));
     const char* why = "";
     kt::GluBackward g = {};
     g.dH = dH;
@@ -444,13 +447,14 @@ kt_status kt_glu_backward(int64_t M, int64_t D, int64_t F, kt_dtype dtype, kt_ac
     g.P = P;
     g.ldp = ldp;
     g.dP = workspace;
-    g.partials = db ? reinterpret_cast<float*>(static_cast<char*>(workspace) + up256((size_t)M * 4 * (size_t)F)) : nullptr;
+    g.partials = db ? reinterpret_cast<float*>(sums) : nullptr;
     g.db = db;
+    g.zero = reinterpret_cast<int*>(scratch);
     g.M = (int)M;
     g.F = (int)F;
     g.act = epilogue_of(act);
     if ((s = kt::launch_glu_backward(dtype, g, stream, &why)) != KT_OK) return kt::report(s, why);
-    return gradients(M, 2 * F, D, dtype, workspace, 2 * F, X, ldx, W, dX, lddx, dW, sms, dev, stream);
+    return gradients(M, 2 * F, D, dtype, workspace, 2 * F, X, ldx, W, dX, lddx, dW, scratch, sms, dev, stream);
 }
 
 kt_status kt_linear_forward(int64_t M, int64_t N, int64_t K, kt_dtype dtype, const void* X, int64_t ldx, const void* W,
@@ -477,7 +481,7 @@ kt_status kt_linear_forward(int64_t M, int64_t N, int64_t K, kt_dtype dtype, con
 
 size_t kt_linear_backward_workspace(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || M > INT32_MAX / 2 || N < 8 || N % 8 || N > (1 << 24) || K < 8 || K % 8 || K > (1 << 24)) return 0;
-    return (size_t)kt::column_sum_rows(M, N) * (size_t)N * sizeof(float);
+    return up256((size_t)kt::column_sum_rows(M, N) * (size_t)N * sizeof(float)) + kScratch;
 }
 
 kt_status kt_linear_backward(int64_t M, int64_t N, int64_t K, kt_dtype dtype, const void* dY, int64_t lddy, const void* X,
@@ -491,7 +495,7 @@ kt_status kt_linear_backward(int64_t M, int64_t N, int64_t K, kt_dtype dtype, co
         return s;
     if (dX && (s = check_matrix(dX, lddx, K)) != KT_OK) return s;
     if (!aligned(db, 4) || !aligned(workspace, 16)) return bad("db must be aligned to its elements and the workspace to 16 bytes");
-    if (db && (!workspace || workspace_bytes < kt_linear_backward_workspace(M, N, K)))
+    if (!workspace || workspace_bytes < kt_linear_backward_workspace(M, N, K))
         return bad("the workspace is smaller than kt_linear_backward_workspace says");
     int dev, sms;
     if ((s = current_device(&dev, &sms)) != KT_OK) return s;
@@ -499,18 +503,23 @@ kt_status kt_linear_backward(int64_t M, int64_t N, int64_t K, kt_dtype dtype, co
         if ((s = zeros(dW, (size_t)2 * N * K, stream)) != KT_OK || (s = zeros(db, (size_t)4 * N, stream)) != KT_OK) return s;
         return done(KT_OK, "");
     }
+    char* const scratch = static_cast<char*>(workspace) + up256((size_t)kt::column_sum_rows(M, N) * (size_t)N * sizeof(float));
+    const char* why = "";
     if (db) {
-        const char* why = "";
         kt::GluBackward g = {};
         g.dH = dY;
         g.lddh = lddy;
         g.partials = static_cast<float*>(workspace);
         g.db = db;
+        g.zero = reinterpret_cast<int*>(scratch);
         g.M = (int)M;
         g.F = (int)N;
-        if ((s = kt::launch_glu_backward(dtype, g, stream, &why)) != KT_OK) return kt::report(s, why);
+        s = kt::launch_glu_backward(dtype, g, stream, &why);
+    } else {
+        s = kt::launch_zero(reinterpret_cast<int*>(scratch), stream, &why);
     }
-    return gradients(M, N, K, dtype, dY, lddy, X, ldx, W, dX, lddx, dW, sms, dev, stream);
+    if (s != KT_OK) return kt::report(s, why);
+    return gradients(M, N, K, dtype, dY, lddy, X, ldx, W, dX, lddx, dW, scratch, sms, dev, stream);
 }
 
 kt_status kt_adamw(int64_t count, const kt_adamw_tensor* tensors, const kt_adamw_options* o, void* stream) {

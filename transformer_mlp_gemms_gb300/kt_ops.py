@@ -269,8 +269,8 @@ def linear_backward_workspace(M: int, N: int, K: int, device="cuda"):
     return torch.empty(kt_linear_backward_workspace(M, N, K), dtype=torch.uint8, device=device)
 
 
-def kt_linear_backward(dY, X, W, dX, dW, db=None, workspace=None, stream=None) -> None:
-    """dX [M][K], dW [N][K] and db (fp32 [N], needs ``workspace``); each may be None."""
+def kt_linear_backward(dY, X, W, dX, dW, db, workspace, stream=None) -> None:
+    """dX [M][K], dW [N][K] and db (fp32 [N]); each may be None."""
     r = (_ext or _calls()).linear_backward(dY, X, W, dX, dW, db, workspace, stream)
     if r is not None:
         _fail(r, "kt_linear_backward")
