@@ -81,15 +81,15 @@ __device__ __forceinline__ uint4 pack_pairs(const f32x2 (&f)[4]) {
     return make_uint4(pack2<DT>(f[0].x, f[0].y), pack2<DT>(f[1].x, f[1].y), pack2<DT>(f[2].x, f[2].y), pack2<DT>(f[3].x, f[3].y));
 }
 
-// The counters of the products behind this kernel.
-__device__ __forceinline__ void zero_counters(int* at) {
+// The flags of the products behind this kernel.
+__device__ __forceinline__ void zero_flags(int* at) {
     if (at && blockIdx.x == 0 && blockIdx.y == 0)
-        for (int i = threadIdx.x; i < (int)(kGradientsCounters / sizeof(int)); i += blockDim.x) at[i] = 0;
+        for (int i = threadIdx.x; i < (int)(kGradientsFlags / sizeof(int)); i += blockDim.x) at[i] = 0;
 }
 __global__ void __launch_bounds__(256) kt_zero_kernel(int* at) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    zero_counters(at);
+    zero_flags(at);
 }
 
 // Block (x, y): 256 hidden columns, rows [y per, (y + 1) per); a warp takes every eighth row, four of them
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kGluThreads) kt_glu_backward_kernel(const GluB
     constexpr bool GATED = EPI >= 0;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    zero_counters(p.zero);
+    zero_flags(p.zero);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = (int)blockIdx.x * kGluCols + 8 * lane;
     const bool mine = col < p.F;

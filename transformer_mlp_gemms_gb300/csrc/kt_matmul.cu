@@ -17,11 +17,12 @@
 //   warps 2-9: epilogue.
 // SPLIT: few tiles with long sums: a cluster per tile, each CTA with its share of the steps; the fp32 sums meet
 // in the cluster's shared memory, added in the order of the ranks.
-// SHARED (the gradients): both products of a backward pass in one launch, dW's tiles and dX's, on pairs.  Whole
-// rounds of tiles go one to a pair; the steps of the tiles that are left, of both products, are dealt out
-// evenly before them, so that every pair ends at the same time.  A tile whose steps fall to several pairs is
-// summed by the last of them to finish, from fp32 partial sums in the workspace, in the order of the steps, while
-// the products of the whole tiles are already running.
+// SHARED (the gradients): both products of a backward pass in one launch, on pairs, as two lists of tiles.  Either
+// whole tiles are dealt out in turn; or, where that would leave many pairs idle at the end, only whole rounds of
+// them are, after the steps of the tiles that are left, which are dealt out evenly.  A tile whose steps fall to several
+// pairs is summed by the last of them: the others leave fp32 partial sums in the workspace and raise a flag.
+// A pair goes through its share backwards, so that what others wait for comes first and what waits for others comes
+// last, and a pair waits for pairs of lower numbers alone, which were launched before it.
 //
 // Every wait is bounded: one that runs out leaves an error word and NaN in the elements that the call
 // could not compute.
@@ -38,68 +39,71 @@ namespace {
 constexpr int kMmThreads = 11 * 32;
 constexpr int kMmEpi = 8;
 constexpr uint32_t kMmABytes = 128 * 128;  // one step of 128 rows
+constexpr size_t kSlot = 128 * 256;        // partial sums of a CTA
 
 struct MmProduct {
     int M, N;                 // of the output (GATED: N = F)
     int BN, tiles_m, tiles_n, kblocks;
     int a_mn, b_mn;
     uint32_t idesc, b_bytes;  // b_bytes: one step of a CTA's share of B
-    int rounds;               // SHARED: whole rounds of tiles
+    int rounds;               // SHARED: whole rounds of tiles (-1: all tiles in turn)
     int left;                 // SHARED: tiles after them
 };
 struct MmParams {
     MmProduct of[2];          // SHARED: two, else the first
-    int stages, act, has_p;
+    int stages, atoms, act, has_p;  // atoms: 64-deep steps of K per stage of the ring
     uint32_t stage_bytes;
     const void* bias;
     // SHARED: the steps of the tiles left, of both products, and the pairs that they are dealt to
     int steps, sharers;
-    float* partials;          // [sharers][2][2 CTAs][128][BN]
-    int* counters;            // [tiles left, of both products][2 CTAs], zero before the launch
+    float* partials;          // [sharers][2 CTAs][128][256]
+    int* flags;               // [sharers][2 CTAs], zero before the launch
     unsigned long long wait_limit_ns, stall_ns;
 };
 
 // A run of steps of one tile, for a CTA or pair.
 struct MmItem {
     int product, tile, kb0, kb1;
-    int slot;                 // SHARED: where the partial sums of a part of a tile go (of this pair's two), or -1: a whole tile
 };
 
 // The items of unit `unit` of `units`, in order: every role of the CTA (or pair) walks through the same ones.
 template <bool SHARED>
 struct MmWalk {
     const MmParams& p;
-    int unit, units, product = 0, round = 0, at = -1, end = 0, first = 0;
-    __device__ __forceinline__ MmWalk(const MmParams& q, int u, int n) : p(q), unit(u), units(n) {}
+    int unit, units, product = 0, round = 0, at, low;
+    __device__ __forceinline__ MmWalk(const MmParams& q, int u, int n) : p(q), unit(u), units(n) {
+        at = low = 0;
+        if (SHARED && u < q.sharers) {
+            low = (int)((int64_t)q.steps * u / q.sharers);
+            at = (int)((int64_t)q.steps * (u + 1) / q.sharers);
+        }
+    }
     __device__ __forceinline__ bool next(MmItem& it) {
         if constexpr (!SHARED) {
-            it = {0, unit + round * units, 0, p.of[0].kblocks, -1};
+            it = {0, unit + round * units, 0, p.of[0].kblocks};
             ++round;
             return it.tile < p.of[0].tiles_m * p.of[0].tiles_n;
         } else {
-            if (at < 0) {
-                at = first = unit < p.sharers ? (int)((int64_t)p.steps * unit / p.sharers) : 0;
-                end = unit < p.sharers ? (int)((int64_t)p.steps * (unit + 1) / p.sharers) : 0;
+            if (at > low) {  // backwards through this pair's share of steps
+                const int steps0 = p.of[0].left * p.of[0].kblocks, i = at > steps0, kb = p.of[i].kblocks;
+                const int t = (at - 1 - (i ? steps0 : 0)) / kb, start = t * kb + (i ? steps0 : 0);  // the tile's first step
+                it = {i, p.of[i].rounds * units + t, max(low - start, 0), at - start};
+                at = max(start, low);
+                return true;
             }
-            if (at >= end) {
-                for (; product < 2; ++product, round = 0)
-                    if (round < p.of[product].rounds) {
-                        it = {product, unit + round * units, 0, p.of[product].kblocks, -1};
-                        ++round;
-                        return true;
-                    }
-                return false;
+            if (p.of[0].rounds < 0) {  // all tiles of both products in turn
+                const int tiles0 = p.of[0].tiles_m * p.of[0].tiles_n, t = unit + round * units, i = t >= tiles0;
+                ++round;
+                it = {i, i ? t - tiles0 : t, 0, p.of[i].kblocks};
+                return it.tile < p.of[i].tiles_m * p.of[i].tiles_n;
             }
-            const int steps0 = p.of[0].left * p.of[0].kblocks;
-            const int i = at >= steps0, kb = p.of[i].kblocks, t = (at - (i ? steps0 : 0)) / kb;
-            const int start = t * kb + (i ? steps0 : 0);  // of the tile
-            it.product = i;
-            it.tile = p.of[i].rounds * units + t;
-            it.kb0 = at - start;
-            it.kb1 = min(kb, end - start);
-            it.slot = it.kb1 - it.kb0 == kb ? -1 : at == first ? 0 : 1;
-            at = start + it.kb1;
-            return true;
+            for (; product < 2; ++product, round = 0)
+                if (round < p.of[product].rounds) {
+                    it = {product, unit + round * units, 0, p.of[product].kblocks};
+                    ++round;
+                    return true;
+                }
+            return false;
         }
     }
 };
@@ -204,33 +208,29 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             share(it);
             const MmProduct& o = p.of[SHARED ? it.product : 0];
             const CUtensorMap *mA = SHARED && it.product ? &tmV : &tmA, *mB = SHARED && it.product ? &tmG : &tmB;
+            const CUtensorMap* const map = a_role ? mA : mB;
             const bool mn = a_role ? o.a_mn : o.b_mn;
-            const uint32_t b_bytes = o.b_bytes, bytes = PAIR * (kMmABytes + b_bytes);
+            const uint32_t atoms = (uint32_t)p.atoms, operand = a_role ? kMmABytes : o.b_bytes, bytes = PAIR * atoms * (kMmABytes + o.b_bytes);
             int m, n;
             origin(it, m, n);
-            for (int kb = it.kb0; kb < it.kb1; ++kb) {
+            const int row = a_role ? m : n;
+            for (int kb = it.kb0; kb < it.kb1; kb += (int)atoms) {
                 ok = __all_sync(0xffffffffu, wait_turn(bar_empty + 8u * stage, phase ^ 1u, abort_flag, &g_matmul_error, DEV_TIMEOUT_PRODUCER, limit));
                 if (!ok) break;
-                const uint32_t sA = base + stage * stage_bytes, sB = sA + kMmABytes, fb = full0 + 8u * stage;
+                // (a stage may reach past the item's steps, and past K, where zeros are filled in: its products end in time)
+                const uint32_t to = base + stage * stage_bytes + (a_role ? 0u : atoms * kMmABytes), fb = full0 + 8u * stage;
                 const int k = kb * kAtomK;
-                if (a_role) {
-                    expect_tx_if(bar_full + 8u * stage, bytes, arm);
-                    if (mn) {
-                        load_if<PAIR>(sA, mA, fb, m, k, one);
-                        load_if<PAIR>(sA + 8192u, mA, fb, m + 64, k, one);
-                    } else {
-                        load_if<PAIR>(sA, mA, fb, k, m, one);
-                    }
-                    used |= 1u << stage;
-                    used_phase = (used_phase & ~(1u << stage)) | (phase << stage);
-                } else if (GATED) {
-                    load_if<PAIR>(sB, mB, fb, k, n, one);
-                    load_if<PAIR>(sB + b_bytes / 2, mB, fb, k, o.N + n, one);
-                } else if (mn) {
-                    for (uint32_t j = 0; j < b_bytes; j += 8192u) load_if<PAIR>(sB + j, mB, fb, n + (int)(j / 128u), k, one);
+                if (a_role) expect_tx_if(bar_full + 8u * stage, bytes, arm);
+                if (mn) {  // 64 columns each
+                    for (uint32_t j = 0; j * 8192u < operand; ++j) load_if<PAIR>(to + j * atoms * 8192u, map, fb, row + 64 * (int)j, k, one);
                 } else {
-                    load_if<PAIR>(sB, mB, fb, k, n, one);
+                    for (uint32_t i = 0; i < atoms; ++i) {
+                        if (GATED && !a_role) load3_if<PAIR>(to + i * operand, map, fb, k + 64 * (int)i, n, 0, one);
+                        else load_if<PAIR>(to + i * operand, map, fb, k + 64 * (int)i, row, one);
+                    }
                 }
+                used |= 1u << stage;
+                used_phase = (used_phase & ~(1u << stage)) | (phase << stage);
                 if (++stage == (uint32_t)p.stages) {
                     stage = 0;
                     phase ^= 1u;
@@ -259,28 +259,51 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             for (auto w = walk(); ok && w.next(it); ++local) {
                 share(it);
                 const MmProduct& o = p.of[SHARED ? it.product : 0];
-                const uint64_t ad0 = smem_desc(base, o.a_mn ? 8192u : 16u, 1024u);
-                const uint64_t bd0 = smem_desc(base + kMmABytes, o.b_mn ? 8192u : 16u, 1024u);
-                // 16 columns of K further: 32 bytes of a K-major row, 16 rows of an MN-major box
-                const uint32_t a_step = o.a_mn ? 128u : 2u, b_step = o.b_mn ? 128u : 2u, idesc = o.idesc;
                 const uint32_t buf = local & 1, d = tmem + buf * (uint32_t)kAccSlot;
                 ok = __all_sync(0xffffffffu, wait_phase<PAIR == 2>(bar_acce + 8u * buf, ((local >> 1) & 1u) ^ 1u, abort_flag, &g_matmul_error,
                                                                    DEV_TIMEOUT_MMA, limit));
                 if (!ok) break;
                 tc_fence_after();
-                for (int kb = it.kb0; kb < it.kb1; ++kb) {
-                    ok = __all_sync(0xffffffffu, wait_turn(bar_full + 8u * stage, phase, abort_flag, &g_matmul_error, DEV_TIMEOUT_MMA, limit));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t ad = ad0 + stage * stage16, bd = bd0 + stage * stage16;
+                any = true;
+                // The steps of one item, for operands of known order.  K-major: [64-deep step][row], 16 columns of K
+                // further are 32 bytes.  MN-major: [64 columns][K], 16 columns of K further are 16 rows of 128 bytes.
+                auto steps = [&](auto a_mn, auto b_mn, auto atoms_) {
+                    constexpr uint32_t kA = decltype(a_mn)::value ? 128u : 2u, kB = decltype(b_mn)::value ? 128u : 2u, kAtoms = decltype(atoms_)::value;
+                    const uint64_t ad0 = smem_desc(base, decltype(a_mn)::value ? kAtoms * 8192u : 16u, 1024u);
+                    const uint64_t bd0 = smem_desc(base + kAtoms * kMmABytes, decltype(b_mn)::value ? kAtoms * 8192u : 16u, 1024u);
+                    const uint32_t idesc = o.idesc, a16 = decltype(a_mn)::value ? 512u : kMmABytes >> 4, b16 = decltype(b_mn)::value ? 512u : o.b_bytes >> 4;
+                    uint32_t acc = 0;
+                    for (int kb = it.kb0; kb < it.kb1; kb += (int)kAtoms) {
+                        ok = __all_sync(0xffffffffu, wait_turn(bar_full + 8u * stage, phase, abort_flag, &g_matmul_error, DEV_TIMEOUT_MMA, limit));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t ad = ad0 + stage * stage16, bd = bd0 + stage * stage16;
 #pragma unroll
-                    for (uint32_t k = 0; k < 4; ++k) mma_if<PAIR, false>(d, ad + k * a_step, bd + k * b_step, idesc, kb > it.kb0 || k > 0, one);
-                    any = true;
-                    commit_if<PAIR>(bar_empty + 8u * stage, one);
-                    if (++stage == (uint32_t)p.stages) {
-                        stage = 0;
-                        phase ^= 1u;
+                        for (uint32_t i = 0; i < kAtoms; ++i) {
+                            if (i > 0 && kb + (int)i >= it.kb1) break;
+#pragma unroll
+                            for (uint32_t k = 0; k < 4; ++k) {
+                                mma_if<PAIR, false>(d, ad + i * a16 + k * kA, bd + i * b16 + k * kB, idesc, acc, one);
+                                acc = 1;
+                            }
+                        }
+                        commit_if<PAIR>(bar_empty + 8u * stage, one);
+                        if (++stage == (uint32_t)p.stages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
+                };
+                constexpr std::false_type kK{};
+                constexpr std::true_type kMN{};
+                constexpr std::integral_constant<uint32_t, 1> kOne{};
+                constexpr std::integral_constant<uint32_t, 2> kTwo{};
+                if constexpr (SHARED) {
+                    if (o.a_mn) steps(kMN, kMN, kTwo);
+                    else steps(kK, kMN, kTwo);
+                } else {
+                    if (p.atoms == 1) steps(kK, kK, kOne);
+                    else steps(kK, kK, kTwo);
                 }
                 if (ok) commit_if<PAIR>(bar_accf + 8u * buf, one);
             }
@@ -376,11 +399,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                     }
                     store(&tmC, w, col);
                 }
-            } else if (SHARED && it.slot >= 0) {
-                // A part of a tile's steps: partial sums into this pair's slot, [16 columns][4 columns][128 rows] of
-                // 16 bytes, so that a warp's accesses are 512 consecutive bytes; then the tile's count.
-                const size_t half_tile = (size_t)128 * 256;  // floats of a slot of one CTA
-                float4* const mine = reinterpret_cast<float4*>(p.partials + ((size_t)(unit0 * 2 + it.slot) * 2 + rank) * half_tile) + 32 * q + lane;
+            } else if (SHARED && it.kb1 < o.kblocks) {
+                // A part of a tile's steps, not the last: partial sums into this pair's slot, [16 columns][4 columns][128
+                // rows] of 16 bytes, so that a warp's accesses are 512 consecutive bytes; then the flag.
+                float4* const mine = reinterpret_cast<float4*>(p.partials + (size_t)(unit0 * 2 + (int)rank) * kSlot) + 32 * q + lane;
                 for (int g = half; g < o.BN / 32; g += 2) {
                     uint32_t r[32];
                     if (ok) {
@@ -396,45 +418,39 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                         __stcg(mine + (8 * g + i) * 128, make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
                                                                      __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])));
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_relaxed(mapa_rank(bar_acce + 8u * buf, 0));
-                // the pairs that have steps of this tile: first .. last
-                const int steps0 = p.of[0].left * p.of[0].kblocks, t = it.tile - o.rounds * units;
-                const int64_t start = (int64_t)t * o.kblocks + (it.product ? steps0 : 0);
-                const int first = (int)(((start + 1) * p.sharers - 1) / p.steps);
-                const int last = (int)(((start + o.kblocks) * p.sharers - 1) / p.steps);
-                epi_bar_sync<kMmEpi>();  // every warp's sums precede the count
+                epi_bar_sync<kMmEpi>();  // every warp's sums precede the flag
                 if (ew == 0 && lane == 0) {
                     __threadfence();
-                    const int count = atomicAdd(p.counters + (size_t)(t + (it.product ? p.of[0].left : 0)) * 2 + rank, 1);
-                    words[2] = count == last - first;
-                    __threadfence();
+                    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p.flags + unit0 * 2 + (int)rank), "r"(1) : "memory");
                 }
-                epi_bar_sync<kMmEpi>();
-                if (words[2]) {
-                    const bool starts = (int)((int64_t)p.steps * first / p.sharers) == start;  // the first pair's share begins with this tile
-                    const float4* const from = reinterpret_cast<const float4*>(p.partials + rank * half_tile) + 32 * q + lane;
-                    for (int g = half; g < o.BN / 32; g += 2) {
-                        const int col = n + 32 * g;
-                        if (col >= o.N || y >= o.M) continue;
-                        float v[32];
+            } else if (SHARED && it.kb0 > 0) {
+                // The last part of a tile's steps: the other pairs' sums in the order of the steps, then this one's.
+                const int64_t start = (int64_t)(it.tile - o.rounds * units) * o.kblocks + (it.product ? p.of[0].left * p.of[0].kblocks : 0);
+                const int first = (int)(((start + 1) * p.sharers - 1) / p.steps);  // the pair that has the tile's first step
+                bool there = ok;
+                if (ew == 0 && lane < unit0 - first && there)  // (a lane per pair; there are fewer than 32)
+                    there = wait_flag(p.flags + (first + lane) * 2 + (int)rank, abort_flag, &g_matmul_error, limit);
+                ok = epi_all<kMmEpi>(there);
+                const float4* const from = reinterpret_cast<const float4*>(p.partials + (int)rank * kSlot) + 32 * q + lane;
+                for (int g = half; g < o.BN / 32; g += 2) {
+                    const int col = n + 32 * g;
+                    if (col >= o.N || y >= o.M) continue;
+                    float v[32];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-                        // three pairs' sums on their way at a time
-                        for (int u0 = first; u0 <= last; u0 += 3) {
-                            float4 x[3][8];
+                    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+                    if (ok) {
+                        for (int u0 = first; u0 < unit0; u0 += 2) {  // two pairs' sums on their way at a time
+                            float4 x[2][8];
 #pragma unroll
-                            for (int j = 0; j < 3; ++j) {
-                                const int u = u0 + j;
-                                if (u > last) break;
-                                const float4* part_of = from + (size_t)(u * 2 + (u == first && !starts)) * 2 * (half_tile / 4) + (size_t)(8 * g) * 128;
+                            for (int j = 0; j < 2; ++j) {
+                                if (u0 + j >= unit0) break;
+                                const float4* part_of = from + (size_t)(u0 + j) * 2 * (kSlot / 4) + (size_t)(8 * g) * 128;
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) x[j][i] = __ldcg(part_of + i * 128);
                             }
 #pragma unroll
-                            for (int j = 0; j < 3; ++j) {
-                                if (u0 + j > last) break;
+                            for (int j = 0; j < 2; ++j) {
+                                if (u0 + j >= unit0) break;
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
                                     v[4 * i] += x[j][i].x;
@@ -444,12 +460,15 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                                 }
                             }
                         }
-                        uint32_t w[16];
-                        pack32<DT>(v, w);
-                        store(mC, w, col);
                     }
+                    float own[32];
+                    columns(32u * g, nullptr, 0, 0, own);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] += own[i];
+                    uint32_t w[16];
+                    pack32<DT>(v, w);
+                    store(mC, w, col);
                 }
-                epi_bar_sync<kMmEpi>();  // words[2] is free for the next tile
             } else {
                 for (int g = half; g < o.BN / 32; g += 2) {
                     const int col = n + 32 * g;
@@ -460,9 +479,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                     pack32<DT>(v, w);
                     store(mC, w, col);
                 }
-            }
-            if constexpr (SHARED) {
-                if (it.slot >= 0) continue;  // (handed back above)
             }
             tc_fence_before();
             __syncwarp();
@@ -486,7 +502,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             const int ew = warp - 2;
             const uint32_t stg = staging + (uint32_t)ew * 4096u;
             int m, n;
-            origin(MmItem{0, unit0, 0, 0, -1}, m, n);
+            origin(MmItem{0, unit0, 0, 0}, m, n);
             for (int u = part + splits * ew; u < p.of[0].BN / 8; u += splits * kMmEpi) {  // units of this CTA: every splits-th
                 const int q = u & 3, col = n + 32 * (u >> 2), y = m + 32 * q;
                 if (col >= p.of[0].N || y >= p.of[0].M) continue;
@@ -623,13 +639,22 @@ bool mm_encode(CUtensorMap* m, int dtype, const void* at, int64_t ld, int64_t ro
     const uint32_t box[2] = {(uint32_t)box_cols, (uint32_t)box_rows};
     return encode_tmap_nd(m, at, dtype, 2, dims, strides, box, swizzle, why);
 }
+// An operand's map; rows: of the tile in one CTA.
+bool mm_operand(CUtensorMap* m, int dtype, const void* at, int64_t ld, bool mn, int64_t outer, int64_t K, int rows, int atoms, const char** why) {
+    return mn ? mm_encode(m, dtype, at, ld, K, outer, 64 * atoms, 64, 128, why) : mm_encode(m, dtype, at, ld, outer, K, rows, 64, 128, why);
+}
+// GATED: the weight as [value, gate][F][K], `rows` of each in one copy
+bool mm_gated(CUtensorMap* m, int dtype, const Matmul& a, int rows, const char** why) {
+    const uint64_t dims[3] = {(uint64_t)a.K, (uint64_t)a.N, 2}, strides[2] = {(uint64_t)a.ldb * 2, (uint64_t)a.N * (uint64_t)a.ldb * 2};
+    const uint32_t box[3] = {64, (uint32_t)rows, 2};
+    return encode_tmap_nd(m, a.B, dtype, 3, dims, strides, box, 128, why);
+}
 // a product's maps of A, B and C
-bool mm_maps(CUtensorMap* a_map, CUtensorMap* b_map, CUtensorMap* c_map, int dtype, const Matmul& a, int bn, int pair, const char** why) {
-    const int b_rows = a.gated ? bn / pair / 2 : bn / pair;
-    return (a.a_mn ? mm_encode(a_map, dtype, a.A, a.lda, a.K, a.M, 64, 64, 128, why) : mm_encode(a_map, dtype, a.A, a.lda, a.M, a.K, 128, 64, 128, why)) &&
-           (a.b_mn ? mm_encode(b_map, dtype, a.B, a.ldb, a.K, a.N, 64, 64, 128, why)
-                   : mm_encode(b_map, dtype, a.B, a.ldb, a.gated ? 2 * (int64_t)a.N : a.N, a.K, b_rows, 64, 128, why)) &&
-           mm_encode(c_map, dtype, a.C, a.ldc, a.M, a.N, 32, kStoreCols, 64, why);
+bool mm_maps(CUtensorMap* tm, int dtype, const Matmul& a, int bn, int pair, int atoms, const char** why) {
+    const int share = bn / pair;
+    return mm_operand(tm, dtype, a.A, a.lda, a.a_mn, a.M, a.K, 128, atoms, why) &&
+           (a.gated ? mm_gated(tm + 1, dtype, a, share / 2, why) : mm_operand(tm + 1, dtype, a.B, a.ldb, a.b_mn, a.N, a.K, share, atoms, why)) &&
+           mm_encode(tm + 2, dtype, a.C, a.ldc, a.M, a.N, 32, kStoreCols, 64, why);
 }
 
 kt_status mm_done(cudaError_t e, const char** why) {
@@ -642,26 +667,27 @@ kt_status mm_done(cudaError_t e, const char** why) {
 
 MatmulShape matmul_shape(const Matmul& a, int sms, int device) {
     const int steps = (a.K + kAtomK - 1) / kAtomK;
+    // us per 64-deep step and per launch, measured from 10 to 80 steps
     struct {
-        int pair, bn;
+        int pair, bn, atoms;
         double step, round;
-    } const kinds[] = {{2, 256, 0.30, 4.0}, {2, 128, 0.21, 3.5}, {1, 128, 0.25, 3.0}, {1, 64, 0.20, 3.0}};
+    } const kinds[] = {{2, 256, 1, 0.26, 6.0}, {2, 128, 2, 0.17, 5.3}, {1, 128, 2, 0.17, 4.9}, {1, 64, 2, 0.155, 4.5}};
     MatmulShape best = {};
     double least = 1e30;
     for (const auto& k : kinds) {
         const int64_t t = mm_tiles(a, k.bn, k.pair), units = sms / k.pair, rounds = (t + units - 1) / units;
-        const double time = rounds * (steps * k.step + 0.5) + k.round;
+        const double time = rounds * steps * k.step + (rounds - 1) * 0.5 + k.round;
         if (time < least) {
             least = time;
-            best = {k.pair, k.bn, 1};
+            best = {k.pair, k.bn, 1, k.atoms};
         }
         if (a.gated || k.pair == 2) continue;
         for (int ks = 2; ks <= 8; ks *= 2) {
             if (t * ks > sms || steps < 2 * ks || t > mm_clusters(ks, device)) continue;
-            const double split = (steps + ks - 1) / ks * k.step + k.round + 2.5;
+            const double split = (steps + ks - 1) / ks * k.step + k.round + 2.3;
             if (split < least) {
                 least = split;
-                best = {1, k.bn, ks};
+                best = {1, k.bn, ks, k.atoms};
             }
         }
     }
@@ -671,7 +697,8 @@ MatmulShape matmul_shape(const Matmul& a, int sms, int device) {
 kt_status launch_matmul_as(int dtype, const Matmul& a, const MatmulShape& s, int sms, int device, void* stream, const char** why) {
     MmParams p = {};
     p.of[0] = mm_product(dtype, a, s.BN, s.pair);
-    p.stage_bytes = kMmABytes + p.of[0].b_bytes;
+    p.atoms = s.atoms;
+    p.stage_bytes = (uint32_t)s.atoms * (kMmABytes + p.of[0].b_bytes);
     p.stages = std::min(8, kMmRing / (int)p.stage_bytes);
     p.act = a.act;
     p.has_p = a.P != nullptr;
@@ -679,7 +706,7 @@ kt_status launch_matmul_as(int dtype, const Matmul& a, const MatmulShape& s, int
     p.wait_limit_ns = a.wait_limit_ns;
     p.stall_ns = a.stall_ns;
     CUtensorMap tm[6];
-    if (!mm_maps(tm, tm + 1, tm + 2, dtype, a, s.BN, s.pair, why)) return KT_ERR_CUDA;
+    if (!mm_maps(tm, dtype, a, s.BN, s.pair, s.atoms, why)) return KT_ERR_CUDA;
     tm[3] = tm[4] = tm[5] = tm[2];
     if (a.P) {
         uint16_t* P = static_cast<uint16_t*>(a.P);
@@ -696,42 +723,93 @@ kt_status launch_matmul(int dtype, const Matmul& a, int sms, int device, void* s
     return launch_matmul_as(dtype, a, matmul_shape(a, sms, device), sms, device, stream, why);
 }
 
-size_t gradients_partials() { return (size_t)(kMaxSms / 2) * 2 * 2 * 128 * 256 * sizeof(float); }
+size_t gradients_partials() { return (size_t)(kMaxSms / 2) * 2 * kSlot * sizeof(float); }
 
-kt_status launch_gradients_as(int dtype, const Matmul* a, int count, const int* bn, void* scratch, int sms, int device, void* stream, const char** why) {
+kt_status launch_gradients_as(int dtype, const Matmul* a, int count, const GradientsShape& s, void* scratch, int sms, int device, void* stream, const char** why) {
+    constexpr int kAtoms = 2;
     MmParams p = {};
     CUtensorMap tm[6];
     const int units = sms / 2;
+    int tiles = 0;
     for (int i = 0; i < 2; ++i) {
         if (i >= count) {
             std::memcpy(tm + 3, tm, 3 * sizeof(CUtensorMap));
+            p.of[i].kblocks = 1;
             continue;
         }
-        p.of[i] = mm_product(dtype, a[i], bn[i], 2);
-        const int tiles = p.of[i].tiles_m * p.of[i].tiles_n;
-        p.of[i].rounds = tiles / units;
-        p.of[i].left = tiles % units;
+        p.of[i] = mm_product(dtype, a[i], s.bn[i], 2);
+        const int n = p.of[i].tiles_m * p.of[i].tiles_n;
+        tiles += n;
+        p.of[i].rounds = s.share ? n / units : -1;
+        p.of[i].left = s.share ? n % units : 0;
         p.steps += p.of[i].left * p.of[i].kblocks;
-        p.stage_bytes = std::max(p.stage_bytes, kMmABytes + p.of[i].b_bytes);
-        if (!mm_maps(tm + 3 * i, tm + 3 * i + 1, tm + 3 * i + 2, dtype, a[i], bn[i], 2, why)) return KT_ERR_CUDA;
+        p.stage_bytes = std::max(p.stage_bytes, kAtoms * (kMmABytes + p.of[i].b_bytes));
+        if (!mm_maps(tm + 3 * i, dtype, a[i], s.bn[i], 2, kAtoms, why)) return KT_ERR_CUDA;
     }
-    if (count == 1) p.of[1].kblocks = 1;
+    p.atoms = kAtoms;
     p.stages = std::min(8, kMmRing / (int)p.stage_bytes);
-    p.sharers = std::max(1, std::min(units, p.steps / kGradientsLeast));
-    p.counters = static_cast<int*>(scratch);
-    p.partials = reinterpret_cast<float*>(static_cast<char*>(scratch) + kGradientsCounters);
+    // a tile falls to 32 pairs at most (a lane each)
+    p.sharers = std::min(units, p.steps / kGradientsLeast);
+    for (int i = 0; i < count; ++i)
+        if (p.of[i].left) p.sharers = std::min<int64_t>(p.sharers, 30ll * p.steps / p.of[i].kblocks);
+    if (p.steps) p.sharers = std::max(1, p.sharers);
+    p.flags = static_cast<int*>(scratch);
+    p.partials = reinterpret_cast<float*>(static_cast<char*>(scratch) + kGradientsFlags);
     p.wait_limit_ns = a[0].wait_limit_ns;
     p.stall_ns = a[0].stall_ns;
-    const int busy = p.of[0].rounds || p.of[1].rounds ? units : p.sharers;
+    const int busy = !s.share ? std::min(tiles, units) : p.of[0].rounds + p.of[1].rounds > 0 ? units : p.sharers;
     return mm_done(dtype == KT_BF16 ? mm_launch<KT_BF16, 2, false, false, true>(tm, p, 2 * busy, 2, device, stream)
                                     : mm_launch<KT_F16, 2, false, false, true>(tm, p, 2 * busy, 2, device, stream),
                    why);
 }
 
+GradientsShape gradients_shape(const Matmul* a, int count, int sms) {
+    const int units = sms / 2;
+    GradientsShape best = {};
+    double least = 1e30;
+    for (int mask = 0; mask < 1 << count; ++mask) {
+        int64_t tiles[2] = {}, steps[2] = {};
+        double step[2] = {}, tile[2] = {};
+        GradientsShape s = {};
+        for (int i = 0; i < count; ++i) {
+            s.bn[i] = mask >> i & 1 ? 128 : 256;
+            tiles[i] = mm_tiles(a[i], s.bn[i], 2);
+            steps[i] = (a[i].K + kAtomK - 1) / kAtomK;
+            step[i] = s.bn[i] == 256 ? 0.29 : 0.18;  // us, measured; a tile of few steps takes its epilogue's time
+            tile[i] = std::max(steps[i] * step[i], s.bn[i] == 256 ? 1.9 : 1.2);
+        }
+        // in turn: the pair with the most
+        double most = 0.0;
+        for (int u = 0; u < units; ++u) {
+            const int64_t n0 = tiles[0] > u ? (tiles[0] - u - 1) / units + 1 : 0, all = tiles[0] + tiles[1] > u ? (tiles[0] + tiles[1] - u - 1) / units + 1 : 0;
+            most = std::max(most, n0 * tile[0] + (all - n0) * tile[1]);
+        }
+        // shared: the whole rounds, an even share of the rest, and partial sums on their way through memory, of which
+        // whole tiles hide some
+        double share = 0.0, rest = 0.0;
+        int64_t rounds = 0, left_steps = 0;
+        for (int i = 0; i < count; ++i) {
+            rounds += tiles[i] / units;
+            share += (double)(tiles[i] / units) * tile[i];
+            rest += (double)(tiles[i] % units) * tile[i];
+            left_steps += tiles[i] % units * steps[i];
+        }
+        const int64_t sharers = std::max<int64_t>(1, std::min<int64_t>(units, left_steps / kGradientsLeast));
+        share += rest / (double)sharers + (rounds ? 3.0 : 6.0);
+        for (int k = 0; k < 2; ++k) {
+            const double time = k ? share : most;
+            if (time < least && !(k && left_steps == 0)) {
+                least = time;
+                best = s;
+                best.share = k;
+            }
+        }
+    }
+    return best;
+}
+
 kt_status launch_gradients(int dtype, const Matmul* a, int count, void* scratch, int sms, int device, void* stream, const char** why) {
-    int bn[2];
-    for (int i = 0; i < count; ++i) bn[i] = mm_tiles(a[i], 256, 2) < sms / 2 ? 128 : 256;
-    return launch_gradients_as(dtype, a, count, bn, scratch, sms, device, stream, why);
+    return launch_gradients_as(dtype, a, count, gradients_shape(a, count, sms), scratch, sms, device, stream, why);
 }
 
 kt_status matmul_status(void* stream, int* word, const char** why) { return error_word(g_matmul_error, stream, word, why); }

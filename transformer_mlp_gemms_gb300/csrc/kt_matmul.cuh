@@ -32,21 +32,22 @@ __device__ __forceinline__ void expect_tx_if(uint32_t bar, uint32_t bytes, uint3
                  "r"(one)
                  : "memory");
 }
+#define KT_LOAD_IF(dim, group, coords, ...)                                                                                  \
+    asm volatile("{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %3, 0;\n\t"                                                              \
+                 "@l cp.async.bulk.tensor." dim ".shared::cluster.global.tile.mbarrier::complete_tx::bytes" group " [%0], [%1, " coords "], [%2];\n\t}" ::"r"(dst), \
+                 "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(one), __VA_ARGS__                                          \
+                 : "memory")
 template <int PAIR>
 __device__ __forceinline__ void load_if(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int x, int y, uint32_t one) {
-    if constexpr (PAIR == 2)
-        asm volatile(
-            "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %5, 0;\n\t"
-            "@l cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(y), "r"(one)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %5, 0;\n\t"
-            "@l cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(y), "r"(one)
-            : "memory");
+    if constexpr (PAIR == 2) KT_LOAD_IF("2d", ".cta_group::2", "{%4, %5}", "r"(x), "r"(y));
+    else KT_LOAD_IF("2d", "", "{%4, %5}", "r"(x), "r"(y));
 }
+template <int PAIR>
+__device__ __forceinline__ void load3_if(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int x, int y, int z, uint32_t one) {
+    if constexpr (PAIR == 2) KT_LOAD_IF("3d", ".cta_group::2", "{%4, %5, %6}", "r"(x), "r"(y), "r"(z));
+    else KT_LOAD_IF("3d", "", "{%4, %5, %6}", "r"(x), "r"(y), "r"(z));
+}
+#undef KT_LOAD_IF
 #define KT_MMA_IF(group, kind)                                                                                          \
     asm volatile("{\n\t.reg .pred p, l;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %5, 0;\n\t"                           \
                  "@l tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(ad), "l"(bd), \
@@ -74,6 +75,24 @@ __device__ __forceinline__ void commit_if(uint32_t bar, uint32_t one) {
             "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %1, 0;\n\t"
             "@l tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(one)
             : "memory");
+}
+
+// Waits until another CTA's flag is raised, as the wait on a barrier: bounded, and given up where this CTA aborts.
+__device__ __forceinline__ bool wait_flag(const int* flag, volatile int* abort_flag, int* err, unsigned long long limit_ns) {
+    const unsigned long long t0 = global_ns();
+    for (uint32_t i = 1;; ++i) {
+        int v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+        if (v) return true;
+        if ((i & 15u) == 0) {
+            if (*abort_flag) return false;
+            if (global_ns() - t0 > limit_ns) {
+                *abort_flag = 1;
+                atomicCAS(err, 0, DEV_TIMEOUT_EPILOGUE);
+                return false;
+            }
+        }
+    }
 }
 
 __device__ __forceinline__ uint32_t cluster_size() {

@@ -2,6 +2,7 @@
 // the mixture-of-experts plans, launches.  No call lets a C++ exception out.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdio>
@@ -117,6 +118,7 @@ kt_status gradients(int64_t M, int64_t N, int64_t K, int dtype, const void* dP, 
         x.ldc = lddx;
     }
     if (!count) return done(KT_OK, "");
+    if (count == 2 && a[1].K > a[0].K) std::swap(a[0], a[1]);
     const char* why = "";
     return done(kt::launch_gradients(dtype, a, count, scratch, sms, device, stream, &why), why);
 }
@@ -126,7 +128,7 @@ kt_status zeros(void* p, size_t bytes, void* stream) {
     return e == cudaSuccess ? KT_OK : cuda_failed("cudaMemsetAsync", e);
 }
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
-const size_t kScratch = kt::kGradientsCounters + kt::gradients_partials();  // of launch_gradients
+const size_t kScratch = kt::kGradientsFlags + kt::gradients_partials();  // of launch_gradients
 int epilogue_of(int act) { return kt::up_epilogue(act); }
 
 }  // namespace

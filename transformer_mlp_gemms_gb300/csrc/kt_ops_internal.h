@@ -102,19 +102,24 @@ struct Matmul {
     bool a_mn, b_mn, gated;
     unsigned long long wait_limit_ns, stall_ns;
 };
-// How a product is run: CTAs per tile, accumulator columns per tile, CTAs that share a tile's sums.
+// How a product is run: CTAs per tile, accumulator columns per tile, CTAs that share a tile's sums, 64-deep steps per
+// stage of the ring.
 struct MatmulShape {
-    int pair, BN, splits;
+    int pair, BN, splits, atoms;
 };
 MatmulShape matmul_shape(const Matmul& a, int sms, int device);
 kt_status launch_matmul_as(int dtype, const Matmul& a, const MatmulShape& s, int sms, int device, void* stream, const char** why);
 kt_status launch_matmul(int dtype, const Matmul& a, int sms, int device, void* stream, const char** why);
-// One or two products of a backward pass in one launch.  scratch: counters (zero before the launch, kGradientsCounters bytes),
-// then gradients_partials() bytes; bn: the products' tile widths, 128 or 256.
-constexpr size_t kGradientsCounters = 2 * 2 * (kMaxSms / 2) * sizeof(int);  // of fewer than a round of tiles each
+// One or two products of a backward pass in one launch, the one with longer sums first.  scratch: flags (zero before the
+// launch, kGradientsFlags bytes), then gradients_partials() bytes.
+constexpr size_t kGradientsFlags = kMaxSms * sizeof(int);  // a flag per CTA
 constexpr int kGradientsLeast = 4;  // steps that a pair's share of the last tiles has at least
+struct GradientsShape {
+    int bn[2], share;  // tile widths (128 or 256); 1: the last tiles' steps are shared out
+};
 size_t gradients_partials();
-kt_status launch_gradients_as(int dtype, const Matmul* a, int count, const int* bn, void* scratch, int sms, int device, void* stream, const char** why);
+GradientsShape gradients_shape(const Matmul* a, int count, int sms);
+kt_status launch_gradients_as(int dtype, const Matmul* a, int count, const GradientsShape& s, void* scratch, int sms, int device, void* stream, const char** why);
 kt_status launch_gradients(int dtype, const Matmul* a, int count, void* scratch, int sms, int device, void* stream, const char** why);
 kt_status matmul_status(void* stream, int* word, const char** why);
 
@@ -124,13 +129,13 @@ struct GluBackward {
     void* dP;            // [M][2F] contiguous
     float* partials;     // [column_sum_rows][2F] (F without P), or null: no sums
     float* db;           // [2F] (F)
-    int* zero;           // kGradientsCounters bytes to be zeroed, or null
+    int* zero;           // kGradientsFlags bytes to be zeroed, or null
     int64_t lddh, ldp;
     int M, F, act;       // act: an Epi
 };
 int column_sum_rows(int64_t M, int64_t F);
 kt_status launch_glu_backward(int dtype, const GluBackward& p, void* stream, const char** why);
-kt_status launch_zero(int* at, void* stream, const char** why);  // kGradientsCounters bytes
+kt_status launch_zero(int* at, void* stream, const char** why);  // kGradientsFlags bytes
 
 // AdamW over many tensors (kt_adamw.cu).
 struct AdamwEntry {
