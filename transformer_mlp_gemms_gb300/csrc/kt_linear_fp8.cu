@@ -156,10 +156,10 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
     uint32_t* const words = reinterpret_cast<uint32_t*>(at + (bars - base) + 304u);
     volatile int* const abort_flag = reinterpret_cast<volatile int*>(words + 1);
 
-    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (uniform for the compiler)
+    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
     const unsigned long long limit = p.wait_limit_ns;
-    const uint32_t rank = PAIR == 2 ? (cluster_ctarank() & 1u) : 0u;
-    const int splits = PAIR == 1 ? (int)cluster_size() : 1, part = PAIR == 1 ? (int)cluster_ctarank() : 0;
+    const uint32_t rank = PAIR == 2 ? (uint32_t)uniform((int)(cluster_ctarank() & 1u)) : 0u;
+    const int splits = PAIR == 1 ? uniform((int)cluster_size()) : 1, part = PAIR == 1 ? uniform((int)cluster_ctarank()) : 0;
     const bool leader = rank == 0;
     const int unit0 = (int)blockIdx.x / (PAIR * splits), units = (int)gridDim.x / (PAIR * splits);
     const int tiles = p.tiles_m * p.tiles_n;
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
     __syncthreads();
     if (PAIR == 2) cluster_sync_relaxed();
     tc_fence_after();
-    const uint32_t tmem = words[0];
+    const uint32_t tmem = (uint32_t)uniform((int)words[0]);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
         bool ok = true;
         if (a_role && p.stall_ns && blockIdx.x == 0)  // the tests' hook: nobody signals this barrier
             ok = __all_sync(0xffffffffu, wait_phase(bar_stall, 0, abort_flag, &g_fp8_error, DEV_INJECTED_STALL, p.stall_ns));
-        const uint32_t full0 = PAIR == 2 ? mapa_rank(bar_full, 0) : bar_full;
+        const uint32_t full0 = PAIR == 2 ? (uint32_t)uniform((int)mapa_rank(bar_full, 0)) : bar_full;
         const CUtensorMap* const map = a_role ? &tmA : &tmB;
         for (int t = unit0; t < tiles && ok; t += units) {
             int m, n;

@@ -30,6 +30,8 @@
 #include "kt_gemm.cuh"
 #include "kt_matmul.cuh"
 
+#include <cmath>
+
 namespace kt {
 
 __device__ int g_matmul_error;
@@ -74,8 +76,8 @@ struct MmWalk {
     __device__ __forceinline__ MmWalk(const MmParams& q, int u, int n) : p(q), unit(u), units(n) {
         at = low = 0;
         if (SHARED && u < q.sharers) {
-            low = (int)((int64_t)q.steps * u / q.sharers);
-            at = (int)((int64_t)q.steps * (u + 1) / q.sharers);
+            low = uniform((int)((int64_t)q.steps * u / q.sharers));
+            at = uniform((int)((int64_t)q.steps * (u + 1) / q.sharers));
         }
     }
     __device__ __forceinline__ bool next(MmItem& it) {
@@ -124,6 +126,52 @@ __device__ __forceinline__ void pack32(const float* v, uint32_t* w) {
     for (int i = 0; i < 16; ++i) w[i] = pack2<DT>(v[2 * i], v[2 * i + 1]);
 }
 
+// A shared tile's columns (of this warp's half of the groups of 32): the other pairs' sums in the order of the steps, then
+// this one's from tensor memory.
+template <int DT>
+__device__ __forceinline__ uint32_t sum_shared(const CUtensorMap* tm, const float4* from, int first, int last, bool ok, uint32_t acc, int half, int cols,
+                                            int n, int y, uint32_t stg, uint32_t stores) {
+    const int lane = threadIdx.x & 31;
+    for (int g = half; 32 * g < cols; g += 2) {
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = ok ? 0.0f : __uint_as_float(0x7fffffffu);
+        if (ok) {
+            for (int u0 = first; u0 < last; u0 += 3) {  // three pairs' sums on their way at a time
+                float4 x[3][8];
+#pragma unroll
+                for (int j = 0; j < 3; ++j) {
+                    if (u0 + j >= last) break;
+                    const float4* part_of = from + (size_t)(u0 + j) * 2 * (kSlot / 4) + (size_t)(8 * g) * 128;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[j][i] = __ldcg(part_of + i * 128);
+                }
+#pragma unroll
+                for (int j = 0; j < 3; ++j) {
+                    if (u0 + j >= last) break;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        v[4 * i] += x[j][i].x;
+                        v[4 * i + 1] += x[j][i].y;
+                        v[4 * i + 2] += x[j][i].z;
+                        v[4 * i + 3] += x[j][i].w;
+                    }
+                }
+            }
+            uint32_t own[32];
+            tmem_ld32(acc + 32u * g, own);
+            tmem_wait_ld_only();
+            reg_fence32(own);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(own[i]);
+        }
+        uint32_t w[16];
+        pack32<DT>(v, w);
+        stage_and_store_packed(tm, stg + (stores++ & 1u) * 2048u, lane, w, n + 32 * g, y, true);
+    }
+    return stores;
+}
+
 template <int DT, int PAIR, bool GATED, bool SPLIT, bool SHARED>
 __global__ void __launch_bounds__(kMmThreads, 1)
     kt_matmul_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -144,17 +192,17 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     uint32_t* const words = reinterpret_cast<uint32_t*>(at + (bars - base) + 176u);
     volatile int* const abort_flag = reinterpret_cast<volatile int*>(words + 1);
 
-    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (uniform for the compiler)
+    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
     const unsigned long long limit = p.wait_limit_ns;
-    const uint32_t rank = PAIR == 2 ? (cluster_ctarank() & 1u) : 0u;
-    const int splits = SPLIT ? (int)cluster_size() : 1, part = SPLIT ? (int)cluster_ctarank() : 0;
+    const uint32_t rank = PAIR == 2 ? (uint32_t)uniform((int)(cluster_ctarank() & 1u)) : 0u;
+    const int splits = SPLIT ? uniform((int)cluster_size()) : 1, part = SPLIT ? uniform((int)cluster_ctarank()) : 0;
     const bool leader = rank == 0;
     const int unit0 = (int)blockIdx.x / (PAIR * splits), units = (int)gridDim.x / (PAIR * splits);
     auto walk = [&]() { return MmWalk<SHARED>(p, unit0, units); };
     auto share = [&](MmItem& it) {  // SPLIT: this CTA's share of the steps
         if constexpr (SPLIT) {
-            it.kb1 = (int)((int64_t)p.of[0].kblocks * (part + 1) / splits);
-            it.kb0 = (int)((int64_t)p.of[0].kblocks * part / splits);
+            it.kb1 = uniform((int)((int64_t)p.of[0].kblocks * (part + 1) / splits));
+            it.kb0 = uniform((int)((int64_t)p.of[0].kblocks * part / splits));
         }
     };
 
@@ -181,7 +229,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     __syncthreads();
     if (PAIR == 2) cluster_sync_relaxed();  // the other CTA's barriers are initialised before any signal to them
     tc_fence_after();
-    const uint32_t tmem = words[0];
+    const uint32_t tmem = (uint32_t)uniform((int)words[0]);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -202,7 +250,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         bool ok = true;
         if (a_role && p.stall_ns && blockIdx.x == 0)  // the tests' hook: nobody signals this barrier
             ok = __all_sync(0xffffffffu, wait_phase(bar_stall, 0, abort_flag, &g_matmul_error, DEV_INJECTED_STALL, p.stall_ns));
-        const uint32_t full0 = PAIR == 2 ? mapa_rank(bar_full, 0) : bar_full;
+        const uint32_t full0 = PAIR == 2 ? (uint32_t)uniform((int)mapa_rank(bar_full, 0)) : bar_full;
         MmItem it;
         for (auto w = walk(); ok && w.next(it);) {
             share(it);
@@ -431,44 +479,9 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 if (ew == 0 && lane < unit0 - first && there)  // (a lane per pair; there are fewer than 32)
                     there = wait_flag(p.flags + (first + lane) * 2 + (int)rank, abort_flag, &g_matmul_error, limit);
                 ok = epi_all<kMmEpi>(there);
-                const float4* const from = reinterpret_cast<const float4*>(p.partials + (int)rank * kSlot) + 32 * q + lane;
-                for (int g = half; g < o.BN / 32; g += 2) {
-                    const int col = n + 32 * g;
-                    if (col >= o.N || y >= o.M) continue;
-                    float v[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-                    if (ok) {
-                        for (int u0 = first; u0 < unit0; u0 += 2) {  // two pairs' sums on their way at a time
-                            float4 x[2][8];
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                if (u0 + j >= unit0) break;
-                                const float4* part_of = from + (size_t)(u0 + j) * 2 * (kSlot / 4) + (size_t)(8 * g) * 128;
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) x[j][i] = __ldcg(part_of + i * 128);
-                            }
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                if (u0 + j >= unit0) break;
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    v[4 * i] += x[j][i].x;
-                                    v[4 * i + 1] += x[j][i].y;
-                                    v[4 * i + 2] += x[j][i].z;
-                                    v[4 * i + 3] += x[j][i].w;
-                                }
-                            }
-                        }
-                    }
-                    float own[32];
-                    columns(32u * g, nullptr, 0, 0, own);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] += own[i];
-                    uint32_t w[16];
-                    pack32<DT>(v, w);
-                    store(mC, w, col);
-                }
+                if (y < o.M)
+                    stores = sum_shared<DT>(mC, reinterpret_cast<const float4*>(p.partials + (int)rank * kSlot) + 32 * q + lane, first, unit0, ok, acc, half,
+                                            min(o.BN, o.N - n), n, y, stg, stores);
             } else {
                 for (int g = half; g < o.BN / 32; g += 2) {
                     const int col = n + 32 * g;
@@ -749,10 +762,9 @@ kt_status launch_gradients_as(int dtype, const Matmul* a, int count, const Gradi
     p.atoms = kAtoms;
     p.stages = std::min(8, kMmRing / (int)p.stage_bytes);
     // a tile falls to 32 pairs at most (a lane each)
-    p.sharers = std::min(units, p.steps / kGradientsLeast);
+    p.sharers = p.steps ? std::max(1, std::min(s.share, std::min(units, p.steps))) : 0;
     for (int i = 0; i < count; ++i)
-        if (p.of[i].left) p.sharers = std::min<int64_t>(p.sharers, 30ll * p.steps / p.of[i].kblocks);
-    if (p.steps) p.sharers = std::max(1, p.sharers);
+        if (p.of[i].left) p.sharers = (int)std::min<int64_t>(p.sharers, std::max<int64_t>(1, 30ll * p.steps / p.of[i].kblocks));
     p.flags = static_cast<int*>(scratch);
     p.partials = reinterpret_cast<float*>(static_cast<char*>(scratch) + kGradientsFlags);
     p.wait_limit_ns = a[0].wait_limit_ns;
@@ -764,6 +776,7 @@ kt_status launch_gradients_as(int dtype, const Matmul* a, int count, const Gradi
 }
 
 GradientsShape gradients_shape(const Matmul* a, int count, int sms) {
+    constexpr double kSharing = 7.0;  // us
     const int units = sms / 2;
     GradientsShape best = {};
     double least = 1e30;
@@ -775,7 +788,9 @@ GradientsShape gradients_shape(const Matmul* a, int count, int sms) {
             s.bn[i] = mask >> i & 1 ? 128 : 256;
             tiles[i] = mm_tiles(a[i], s.bn[i], 2);
             steps[i] = (a[i].K + kAtomK - 1) / kAtomK;
-            step[i] = s.bn[i] == 256 ? 0.29 : 0.18;  // us, measured; a tile of few steps takes its epilogue's time
+            // us, measured; rows that start between 128-byte lines take half as long again; a tile of few steps takes its
+            // epilogue's time
+            step[i] = (s.bn[i] == 256 ? 0.27 : 0.165) * ((a[i].lda | a[i].ldb) % 64 ? 1.5 : 1.0);
             tile[i] = std::max(steps[i] * step[i], s.bn[i] == 256 ? 1.9 : 1.2);
         }
         // in turn: the pair with the most
@@ -784,24 +799,29 @@ GradientsShape gradients_shape(const Matmul* a, int count, int sms) {
             const int64_t n0 = tiles[0] > u ? (tiles[0] - u - 1) / units + 1 : 0, all = tiles[0] + tiles[1] > u ? (tiles[0] + tiles[1] - u - 1) / units + 1 : 0;
             most = std::max(most, n0 * tile[0] + (all - n0) * tile[1]);
         }
-        // shared: the whole rounds, an even share of the rest, and partial sums on their way through memory, of which
-        // whole tiles hide some
-        double share = 0.0, rest = 0.0;
-        int64_t rounds = 0, left_steps = 0;
+        // shared: the whole rounds, an even share of the rest, the adding of a tile's partial sums (of a pair: 0.9 or 0.5
+        // us; the two together are least at the root below), and their way through memory
+        double share = kSharing, rest = 0.0, adding = 0.0;
+        int64_t left_steps = 0;
         for (int i = 0; i < count; ++i) {
-            rounds += tiles[i] / units;
+            const int64_t n = tiles[i] % units;
             share += (double)(tiles[i] / units) * tile[i];
-            rest += (double)(tiles[i] % units) * tile[i];
-            left_steps += tiles[i] % units * steps[i];
+            rest += (double)n * tile[i];
+            if (n) adding = std::max(adding, (double)steps[i] * (s.bn[i] == 256 ? 0.9 : 0.5));
+            left_steps += n * steps[i];
         }
-        const int64_t sharers = std::max<int64_t>(1, std::min<int64_t>(units, left_steps / kGradientsLeast));
-        share += rest / (double)sharers + (rounds ? 3.0 : 6.0);
+        int sharers = 0;
+        if (left_steps) {
+            adding /= (double)left_steps;  // of each sharer
+            sharers = (int)std::max(1.0, std::min({(double)units, (double)(left_steps / kGradientsLeast), std::sqrt(rest / adding)}));
+            share += rest / sharers + adding * sharers;
+        }
         for (int k = 0; k < 2; ++k) {
             const double time = k ? share : most;
-            if (time < least && !(k && left_steps == 0)) {
+            if (time < least && (!k || sharers)) {
                 least = time;
                 best = s;
-                best.share = k;
+                best.share = k ? sharers : 0;
             }
         }
     }

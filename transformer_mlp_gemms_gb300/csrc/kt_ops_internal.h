@@ -115,7 +115,7 @@ kt_status launch_matmul(int dtype, const Matmul& a, int sms, int device, void* s
 constexpr size_t kGradientsFlags = kMaxSms * sizeof(int);  // a flag per CTA
 constexpr int kGradientsLeast = 4;  // steps that a pair's share of the last tiles has at least
 struct GradientsShape {
-    int bn[2], share;  // tile widths (128 or 256); 1: the last tiles' steps are shared out
+    int bn[2], share;  // tile widths (128 or 256); the pairs that the last tiles' steps are shared out to, 0: none are
 };
 size_t gradients_partials();
 GradientsShape gradients_shape(const Matmul* a, int count, int sms);
