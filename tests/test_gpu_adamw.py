@@ -191,6 +191,28 @@ def test_the_definition_is_the_usual_one():
     assert ((t[0].double() - p).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("kind", ["any", "near powers", "few bits", "wide"])
+def test_roots_and_quotients_are_correctly_rounded(kind):
+    """p = -(m / (sqrt(v) + 1)) bit for bit (halved moments, no gradient, lr 1, a correction of 1 / sqrt(1 - 1/4)): random
+    significands, ones next to powers of two, ones of few bits, and magnitudes past those that the quick way takes."""
+    n = 1 << 23
+    g = torch.Generator(device="cuda").manual_seed(len(kind))
+    bits = lambda lo, hi: torch.randint(lo, hi, (n,), generator=g, device="cuda", dtype=torch.int64)  # noqa: E731
+
+    def values(span):
+        significand = {"near powers": (bits(-40, 40) + (1 << 23)) % (1 << 23), "few bits": bits(0, 1 << 12) << 11}.get(kind, bits(0, 1 << 23))
+        return (((127 + bits(-span, span + 1)) << 23) | significand).to(torch.int32).view(torch.float32)
+
+    span = 126 if kind == "wide" else 20
+    m, v = values(span) * torch.where(bits(0, 2) == 0, 1.0, -1.0), values(span)
+    m[:1000], v[:2000:2] = 0.0, 0.0
+    p, zero = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    a, r = m * 0.5 * (1.0 / (1.0 - 0.5 ** 2)), torch.sqrt(v * 0.5)
+    want = 0.0 - a / (r * (1.0 / (1.0 - 0.5 ** 2) ** 0.5) + 1e-6)
+    kt_ops.kt_adamw([p], [zero], [m.clone()], [v.clone()], 2, 1.0, 0.5, 0.5, 1e-6)
+    assert torch.equal(p, want)
+
+
 def test_on_another_stream_and_without_tensors():
     t = Tensors(torch.Generator().manual_seed(6), [300, 5000], "f32", "bf16", 32, "")
     grads = t.grads()

@@ -19,6 +19,12 @@
 #include "kt_ops_internal.h"
 #include "kt_gemm.cuh"
 
+#ifndef AD_BLOCKS
+#define AD_BLOCKS 4
+#endif
+#ifndef AD_GRID
+#define AD_GRID 8
+#endif
 namespace kt {
 namespace {
 
@@ -131,6 +137,37 @@ __device__ __forceinline__ void ad_store8(void* at, float* scale, int64_t i, int
     }
 }
 
+// The sum of a product and another number, each rounded: the assembler makes one rounding of a paired product and a paired
+// sum, .rn or not, but cannot where the sum is a product with a one that it does not know.
+__device__ __forceinline__ f32x2 sum_rn(f32x2 product, f32x2 other, f32x2 one) { return f2_fma<true>(product, one, other); }
+
+// Correctly rounded square roots and quotients of pairs by the method of Markstein (Computation of elementary functions
+// on the IBM RISC System/6000 processor, 1990): an approximation, refined once, and a last step from the exact
+// residue.  For operands whose intermediate results are normal numbers (the caller's check); tested against the
+// library's own.  At a time of two values they take a third of the instructions of __fsqrt_rn and __fdiv_rn, whose branches
+// for the other operands are taken per value.
+__device__ __forceinline__ float rsqrt_approx(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ f32x2 negated(f32x2 v) { return f2(-v.x, -v.y); }
+__device__ __forceinline__ f32x2 root_rn(f32x2 v) {
+    const f32x2 y = f2(rsqrt_approx(v.x), rsqrt_approx(v.y));
+    f32x2 g = f2_mul<true>(v, y), h = f2_mul<true>(y, f2(0.5f));
+    const f32x2 e = f2_fma<true>(negated(h), g, f2(0.5f));
+    g = f2_fma<true>(g, e, g);
+    h = f2_fma<true>(h, e, h);
+    return f2_fma<true>(f2_fma<true>(negated(g), g, v), h, g);
+}
+__device__ __forceinline__ f32x2 quotient_rn(f32x2 a, f32x2 b) {
+    f32x2 y = f2_rcp(b);
+    const f32x2 nb = negated(b);
+    y = f2_fma<true>(y, f2_fma<true>(nb, y, f2(1.0f)), y);
+    const f32x2 q = f2_mul<true>(a, y);
+    return f2_fma<true>(f2_fma<true>(nb, q, a), y, q);
+}
+
 // The step of 256 values of one tensor, from `at` on.
 template <int PT, int GT, bool BITS8, bool STRIDED>
 __device__ __forceinline__ void ad_block(const AdamwEntry& t, const AdamwStep& s, int64_t at, int lane, float rate, float root, float scale) {
@@ -148,19 +185,54 @@ __device__ __forceinline__ void ad_block(const AdamwEntry& t, const AdamwStep& s
         ad_load<KT_F32, STRIDED>(t.v, i, left, v);
     }
     ad_load<PT, STRIDED>(t.p, i, left, p);
-    float r[8];
+    float r[8], a[8], d[8];
+    // the most and the least magnitudes as bits, of v and of the numerators that are not zero
+    uint32_t v_most = 0, v_least = ~0u, a_most = 0, a_least = ~0u;
+    const f32x2 b1 = f2(s.b1), c1 = f2(s.c1), b2 = f2(s.b2), c2 = f2(s.c2), one = f2(s.one);
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        f32x2 gg = f2(g[e], g[e + 1]), mm = f2(m[e], m[e + 1]), vv = f2(v[e], v[e + 1]);
+        if constexpr (BITS8) {
+            mm = f2_mul<true>(mm, f2(sm));
+            vv = f2_mul<true>(vv, f2(sv));
+            vv = f2_mul<true>(vv, vv);
+        }
+        if (s.grad_scale) gg = f2_mul<true>(gg, f2(scale));
+        mm = sum_rn(f2_mul<true>(mm, b1), f2_mul<true>(gg, c1), one);
+        vv = sum_rn(f2_mul<true>(vv, b2), f2_mul<true>(f2_mul<true>(gg, c2), gg), one);
+        const f32x2 aa = f2_mul<true>(mm, f2(rate));
+        m[e] = mm.x, m[e + 1] = mm.y, v[e] = vv.x, v[e + 1] = vv.y, a[e] = aa.x, a[e + 1] = aa.y;
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        if constexpr (BITS8) {
-            m[e] = __fmul_rn(m[e], sm);
-            v[e] = __fmul_rn(v[e], sv);
-            v[e] = __fmul_rn(v[e], v[e]);
+        const uint32_t bv = __float_as_uint(v[e]), ba = __float_as_uint(a[e]) & 0x7fffffffu;
+        v_most = max(v_most, bv);
+        v_least = min(v_least, bv);
+        a_most = max(a_most, ba);
+        a_least = min(a_least, ba - 1u);
+    }
+    // Within these the root lies in 2^-39 .. 2^30, the denominator in 2^-39 .. 2^51 (s.plain: eps and the correction are not
+    // out of the way), the quotient in 2^-121 .. 2^99, and no residue below is subnormal.
+    if (s.plain && v_least >= 0x18800000u /* 2^-78 */ && v_most <= 0x5d800000u /* 2^60 */ && a_least >= 0x1c800000u - 1u /* 2^-70 */ &&
+        a_most <= 0x5d800000u) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            const f32x2 rr = root_rn(f2(v[e], v[e + 1]));
+            const f32x2 dd = sum_rn(f2_mul<true>(rr, f2(root)), f2(s.eps), one);
+            const f32x2 qq = quotient_rn(f2(a[e], a[e + 1]), dd);
+            r[e] = rr.x, r[e + 1] = rr.y, d[e] = qq.x, d[e + 1] = qq.y;
         }
-        if (s.grad_scale) g[e] = __fmul_rn(g[e], scale);
-        m[e] = __fadd_rn(__fmul_rn(m[e], s.b1), __fmul_rn(g[e], s.c1));
-        v[e] = __fadd_rn(__fmul_rn(v[e], s.b2), __fmul_rn(__fmul_rn(g[e], s.c2), g[e]));
-        r[e] = __fsqrt_rn(v[e]);
-        p[e] = __fsub_rn(__fmul_rn(p[e], t.keep), __fdiv_rn(__fmul_rn(m[e], rate), __fadd_rn(__fmul_rn(r[e], root), s.eps)));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            r[e] = __fsqrt_rn(v[e]);
+            d[e] = __fdiv_rn(a[e], __fadd_rn(__fmul_rn(r[e], root), s.eps));
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        const f32x2 pp = sum_rn(f2_mul<true>(f2(p[e], p[e + 1]), f2(t.keep)), f2(-d[e], -d[e + 1]), one);
+        p[e] = pp.x, p[e + 1] = pp.y;
     }
     ad_store<PT, STRIDED>(t.p, i, left, p);
     if (PT == KT_F32 && t.copy) {
@@ -182,7 +254,7 @@ __device__ __forceinline__ void ad_block(const AdamwEntry& t, const AdamwStep& s
 }
 
 template <int PT, int GT, bool BITS8, int N>
-__global__ void __launch_bounds__(kAdWarps * 32) kt_adamw_kernel(const __grid_constant__ AdTable<N> tab) {
+__global__ void __launch_bounds__(kAdWarps * 32, AD_BLOCKS) kt_adamw_kernel(const __grid_constant__ AdTable<N> tab) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -232,7 +304,7 @@ cudaError_t ad_launch(const AdamwEntry* e, int count, const AdamwStep& s, int sm
     tab.chunks = chunks;
     tab.s = s;
     if (chunks == 0) return cudaSuccess;
-    const unsigned grid = (unsigned)std::min<int64_t>(chunks, (int64_t)sms * 8);
+    const unsigned grid = (unsigned)std::min<int64_t>(chunks, (int64_t)sms * AD_GRID);
     return launch_pdl(kt_adamw_kernel<PT, GT, BITS8, N>, grid, (unsigned)(kAdWarps * 32), (size_t)0, stream, tab);
 }
 

@@ -595,6 +595,9 @@ kt_status kt_adamw(int64_t count, const kt_adamw_tensor* tensors, const kt_adamw
         a.root = (float)(1.0 / std::sqrt(1.0 - std::pow(o->beta2, (double)o->step)));
     }
     a.step = o->step_device;
+    // on the device the step is 1 at least, and the correction largest there
+    a.one = 1.0f;
+    a.plain = 1.0 / std::sqrt(1.0 - o->beta2) <= 0x1p20 && o->eps <= 0x1p20;
     a.grad_scale = o->grad_scale;
     const char* why = "";
     return done(kt::launch_adamw(e, live, a, sms, stream, &why), why);

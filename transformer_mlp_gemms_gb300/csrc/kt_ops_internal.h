@@ -155,6 +155,8 @@ struct AdamwStep {
     double lr, beta1, beta2;                // for a step number on the device
     const int64_t* step;                    // it, or null
     const float* grad_scale;                // or null
+    float one;                              // 1
+    int plain;                              // root and eps up to 2^20: the quick roots and quotients apply
 };
 kt_status launch_adamw(const AdamwEntry* e, int count, const AdamwStep& s, int sms, void* stream, const char** why);
 
