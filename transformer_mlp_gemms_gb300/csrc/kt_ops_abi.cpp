@@ -600,7 +600,7 @@ kt_status kt_adamw(int64_t count, const kt_adamw_tensor* tensors, const kt_adamw
     a.plain = 1.0 / std::sqrt(1.0 - o->beta2) <= 0x1p20 && o->eps <= 0x1p20;
     a.grad_scale = o->grad_scale;
     const char* why = "";
-    return done(kt::launch_adamw(e, live, a, sms, stream, &why), why);
+    return done(kt::launch_adamw(e, live, a, sms, dev, stream, &why), why);
 }
 
 kt_status kt_quantize_fp8(int64_t M, int64_t K, kt_dtype dtype, kt_act act, const void* X, int64_t ldx, void* Q, int64_t ldq,

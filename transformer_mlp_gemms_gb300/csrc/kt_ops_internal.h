@@ -158,7 +158,7 @@ struct AdamwStep {
     float one;                              // 1
     int plain;                              // root and eps up to 2^20: the quick roots and quotients apply
 };
-kt_status launch_adamw(const AdamwEntry* e, int count, const AdamwStep& s, int sms, void* stream, const char** why);
+kt_status launch_adamw(const AdamwEntry* e, int count, const AdamwStep& s, int sms, int device, void* stream, const char** why);
 
 // The linear layer in 8-bit floating point, and its quantiser (kt_linear_fp8.cu).
 struct QuantFp8 {
