@@ -12,8 +12,8 @@
 // with 16-bit parameters and 8-bit moments; about 50 instructions a value.  A warp takes 256 values at a time
 // (a scale's block), eight consecutive ones per lane, and holds them in registers throughout: their
 // largest magnitude is one warp reduction.  The tensors' addresses come as the launch's parameters, so no
-// table is kept on the device, and a captured call carries its own.  A block takes a run of
-// consecutive chunks, across tensors' ends.
+// table is kept on the device, and a captured call carries its own.  A block takes every
+// gridDim-th chunk, across tensors, so that what runs at a time lies together in memory.
 #include <cuda_fp8.h>
 
 #include "kt_ops_internal.h"
@@ -347,8 +347,8 @@ __global__ void __launch_bounds__(kAdWarps * 32, 4) kt_adamw_kernel(const __grid
         root = on_device[1];
     }
     const float scale = s.grad_scale ? *s.grad_scale : 1.0f;
-    int64_t c = tab.chunks * blockIdx.x / gridDim.x;
-    const int64_t end = tab.chunks * (blockIdx.x + 1) / gridDim.x;
+    int64_t c = blockIdx.x;
+    const int64_t end = tab.chunks, step = gridDim.x;
     if (c >= end) return;
     int t = 0;
     for (int hi = tab.count; hi - t > 1;) {  // the last tensor whose first chunk is at or before c
@@ -376,12 +376,12 @@ __global__ void __launch_bounds__(kAdWarps * 32, 4) kt_adamw_kernel(const __grid
             if (++ahead_stage == kStages) ahead_stage = 0;
         };
 #pragma unroll
-        for (int k = 0; k < kStages - 1; ++k) send(c + k, scales[k]);
-        for (; c < end; ++c) {
+        for (int k = 0; k < kStages - 1; ++k) send(c + k * step, scales[k]);
+        for (; c < end; c += step) {
             const float2 now = scales[0];  // (moved on before the next are asked for, so that no move waits for a load)
 #pragma unroll
             for (int k = 0; k + 2 < kStages; ++k) scales[k] = scales[k + 1];
-            send(c + kStages - 1, scales[kStages - 2]);
+            send(c + (kStages - 1) * step, scales[kStages - 2]);
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
             while (t + 1 < tab.count && tab.e[t + 1].first <= c) ++t;
             const AdamwEntry& e = tab.e[t];
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kAdWarps * 32, 4) kt_adamw_kernel(const __grid
             if (++stage == kStages) stage = 0;
         }
     } else {
-        for (; c < end; ++c) {
+        for (; c < end; c += step) {
             while (t + 1 < tab.count && tab.e[t + 1].first <= c) ++t;
             const AdamwEntry& e = tab.e[t];
             const int64_t at = (c - e.first) * kAdChunk + warp * kAdBlock;
@@ -417,7 +417,7 @@ cudaError_t ad_launch(const AdamwEntry* e, int count, const AdamwStep& s, int sm
     tab.chunks = chunks;
     tab.s = s;
     if (chunks == 0) return cudaSuccess;
-    const unsigned grid = (unsigned)std::min<int64_t>(chunks, (int64_t)sms * 4);
+    const unsigned grid = (unsigned)std::min<int64_t>(chunks, (int64_t)sms * 16);
     constexpr int kSmem = BITS8 ? AdAhead<PT, GT>::kStages * AdAhead<PT, GT>::kBytes : 0;
     static SmemOptIn opt_in;
     if (const cudaError_t r = opt_in(kt_adamw_kernel<PT, GT, BITS8, N>, kSmem, device); r != cudaSuccess) return r;

@@ -114,6 +114,22 @@ __global__ void __launch_bounds__(kQuantThreads) kt_quantize_fp8_kernel(const Qu
 // The linear layer
 // ---------------------------------------------------------------------------
 
+// 8 or 16 columns of a warp's lanes of tensor memory
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+__device__ __forceinline__ void tmem_wait_cols(uint32_t (&r)[16]) { tmem_wait_ld(r); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_cols(uint32_t (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
+}
+
 struct F8Params {
     int M, N, runs, tiles_m, tiles_n, stages;
     uint32_t idesc;
@@ -133,7 +149,7 @@ struct F8 {
     static constexpr uint32_t kBBytes = (uint32_t)(BN / PAIR) * kRun;
     static constexpr uint32_t kStage = kF8ABytes + kBBytes;
     static constexpr int kChunk = 8;                        // runs of scales in shared memory at a time
-    static constexpr uint32_t kScales = SWAP ? 0u : 2u * kChunk * 128u * 4u;
+    static constexpr uint32_t kScales = SWAP ? 0u : 2u * kChunk * (128u + 2u) * 4u;  // [2][kChunk][128], then [2][2][kChunk]
     static constexpr uint32_t kStaging = SWAP ? 0u : (uint32_t)kEpi * 2048u;
     static constexpr int kFit = (int)((kSmemBudget - 1024 - 512 - kScales - kStaging) / kStage);
     static constexpr int kStages = kFit < 10 ? kFit : 10;
@@ -283,31 +299,40 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
         const int ew = warp - 4, q = warp & 3, c0 = SWAP ? 0 : (ew >> 2) * kCols;  // lanes of tensor memory, first column
         uint32_t buf = 0, use = 0;
         bool ok = true;
-        // The tokens' scales, kChunk runs at a time: thread i of the 256 takes four runs of token i / 2, into
-        // registers a chunk ahead.
-        const int st = (int)threadIdx.x - 128, srow = st >> 1, srun = (st & 1) * 4;
-        float ahead[4] = {};
-        auto fetch = [&](int t, int chunk) {
+        // The scales, kChunk runs at a time, copied into shared memory a chunk ahead: thread i of the 256 takes four
+        // runs of token i / 2, and of the first sixteen each one of a block of 128 channels.
+        const int st = (int)threadIdx.x - 128;
+        auto copy = [&](float* to, const float* from, bool there) {  // (zero where there is none)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(there ? 4 : 0) : "memory");
+        };
+        auto fetch = [&](int t, int chunk, uint32_t slot) {
             int m, n;
             origin(t, m, n);
-            m += (int)rank * 128 + srow;
-            const int j = chunk * C::kChunk + srun;
-            const float* from = p.sx + (int64_t)m * p.runs + run0 + j;
+            m += (int)rank * 128 + (st >> 1);
+            const int j = chunk * C::kChunk + (st & 1) * 4;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ahead[i] = m < p.M && j + i < runs ? from[i] : 0.0f;
+            for (int i = 0; i < 4; ++i) {
+                const bool there = m < p.M && j + i < runs;
+                copy(scales + (slot * C::kChunk + (st & 1) * 4 + i) * 128 + (st >> 1), there ? p.sx + (int64_t)m * p.runs + run0 + j + i : p.sx, there);
+            }
+            if (st < 2 * C::kChunk) {
+                const int block = st / C::kChunk, r = chunk * C::kChunk + st % C::kChunk;
+                const bool there = block * 128 < BN && n + block * 128 < p.N && r < runs;
+                copy(scales + 2 * C::kChunk * 128 + slot * 2 * C::kChunk + st, there ? p.sw + (int64_t)(n / 128 + block) * p.runs + run0 + r : p.sw, there);
+            }
         };
         const int chunks = (runs + C::kChunk - 1) / C::kChunk;
         uint32_t slot = 0;  // of the chunk in use
-        if (!SWAP && unit0 < tiles) fetch(unit0, 0);
+        if (!SWAP && unit0 < tiles) fetch(unit0, 0, 1u);
         for (int t = unit0; t < tiles; t += units) {
             int m, n;
             origin(t, m, n);
             float sum[kCols];
 #pragma unroll
             for (int i = 0; i < kCols; ++i) sum[i] = 0.0f;
-            const float* sw = p.sw + (int64_t)((n + c0) / 128) * p.runs + run0;  // the same for all of the warp's columns
-            const bool live = n + c0 < p.N;
-            float w_next = live ? sw[0] : 0.0f;
+            const float* sw = p.sw + (int64_t)(n / 128) * p.runs + run0;  // (SWAP: one block of channels)
+            float w_next = 0.0f;
+            if constexpr (SWAP) w_next = sw[0];
             constexpr int kPer = SWAP ? (BN + 31) / 32 : 1;  // SWAP: tokens lane and lane + 32
             float x_next[kPer];
             auto tokens = [&](int j) {
@@ -317,42 +342,42 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
             if constexpr (SWAP) tokens(0);
 #pragma unroll 1
             for (int j = 0; j < runs; ++j) {
-                if constexpr (!SWAP) {
-                    if (j % C::kChunk == 0) {
-                        slot ^= 1u;
-                        float* to = scales + slot * (C::kChunk * 128) + srun * 128 + srow;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) to[128 * i] = ahead[i];
-                        asm volatile("bar.sync 1, %0;" ::"n"(kEpi * 32) : "memory");
-                        if (j / C::kChunk + 1 < chunks) fetch(t, j / C::kChunk + 1);
-                        else if (t + units < tiles) fetch(t + units, 0);
-                    }
-                }
-                const float w = w_next;
                 float x[kPer];
                 if constexpr (SWAP) {
+                    const float w = w_next;
 #pragma unroll
                     for (int i = 0; i < kPer; ++i) x[i] = x_next[i] * w;
-                    if (j + 1 < runs) tokens(j + 1);
+                    if (j + 1 < runs) {
+                        tokens(j + 1);
+                        w_next = sw[j + 1];
+                    }
                 } else {
-                    x[0] = w * scales[slot * (C::kChunk * 128) + (j % C::kChunk) * 128 + 32 * q + lane];
+                    const int in = j % C::kChunk;
+                    if (in == 0) {
+                        slot ^= 1u;
+                        asm volatile("cp.async.wait_all;" ::: "memory");
+                        asm volatile("bar.sync 1, %0;" ::"n"(kEpi * 32) : "memory");
+                        if (j / C::kChunk + 1 < chunks) fetch(t, j / C::kChunk + 1, slot ^ 1u);
+                        else if (t + units < tiles) fetch(t + units, 0, slot ^ 1u);
+                    }
+                    x[0] = scales[2 * C::kChunk * 128 + (slot * 2 + c0 / 128) * C::kChunk + in] * scales[(slot * C::kChunk + in) * 128 + 32 * q + lane];
                 }
-                if (live && j + 1 < runs) w_next = sw[j + 1];
                 ok = ok && wait_turn(bar_accf + 8u * buf, use & 1u, abort_flag, &g_fp8_error, DEV_TIMEOUT_EPILOGUE, limit);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
                 const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * (uint32_t)BN + (uint32_t)c0;
-                // 16 columns at a time, the next 16 on their way: a wide tile's 128 sums leave no registers for more.
-                // (After a wait that ran out the sums are of no use, and are NaN below.)
-                uint32_t r[2][16];
-                tmem_ld16(acc, r[0]);
+                // 8 columns at a time (16 where there are few sums), the next on their way: a wide tile's 128 sums leave
+                // no registers for more.  (After a wait that ran out the sums are of no use, and are NaN below.)
+                constexpr int kLd = kCols > 64 ? 8 : 16;
+                uint32_t r[2][kLd];
+                tmem_ld_cols(acc, r[0]);
 #pragma unroll
-                for (int c = 0; c < kCols; c += 16) {
-                    uint32_t(&now)[16] = r[c / 16 & 1];
-                    tmem_wait_ld(now);
-                    if (c + 16 < kCols) tmem_ld16(acc + (uint32_t)c + 16u, r[c / 16 + 1 & 1]);
+                for (int c = 0; c < kCols; c += kLd) {
+                    uint32_t(&now)[kLd] = r[c / kLd & 1];
+                    tmem_wait_cols(now);
+                    if (c + kLd < kCols) tmem_ld_cols(acc + (uint32_t)(c + kLd), r[c / kLd + 1 & 1]);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
+                    for (int i = 0; i < kLd; i += 2) {
                         f32x2 s;
                         if constexpr (SWAP) s = f2(__shfl_sync(0xffffffffu, x[c / 32], c % 32 + i), __shfl_sync(0xffffffffu, x[c / 32], c % 32 + i + 1));
                         else s = f2(x[0]);
