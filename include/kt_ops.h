@@ -325,7 +325,7 @@ kt_status kt_quantize_fp8(int64_t M, int64_t K, kt_dtype dtype, kt_act act, cons
  *   M >= 0, N a multiple of 8, K, ldq and ldw multiples of 16, ldy a multiple of 8; Q, W, Y and bias 16-byte
  *   aligned.  Up to KT_LINEAR_FP8_FEW tokens the weights are the tensor cores' first operand.
  */
-#define KT_LINEAR_FP8_FEW 64
+#define KT_LINEAR_FP8_FEW 32
 kt_status kt_linear_fp8(int64_t M, int64_t N, int64_t K, kt_dtype dtype, const void* Q, int64_t ldq, const void* W, int64_t ldw,
                         const float* scale_x, const float* scale_w, const void* bias, void* Y, int64_t ldy, void* stream);
 

@@ -35,7 +35,7 @@ SOURCES = ["kt_gemm_act.cu", "kt_gemm_geglu.cu", "kt_gemm_down.cu", "kt_mlp_two_
            "kt_matmul.cu", "kt_glu.cu", "kt_adamw.cu", "kt_linear_fp8.cu", "kt_ops_abi.cpp"]
 HEADERS = [os.path.join(CSRC, "kt_internal.h"), os.path.join(CSRC, "kt_gemm.cuh"), os.path.join(INCLUDE, "kt_mlp.h"),
            os.path.join(CSRC, "kt_ops_internal.h"), os.path.join(CSRC, "kt_rows.cuh"),
-           os.path.join(CSRC, "kt_matmul.cuh"), os.path.join(INCLUDE, "kt_ops.h")]
+           os.path.join(CSRC, "kt_matmul.cuh"), os.path.join(CSRC, "kt_exact.cuh"), os.path.join(INCLUDE, "kt_ops.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -12,13 +12,14 @@
 // BN / 2 sums.  The tokens' scales come through shared memory, eight runs at a time, [run][token]: read from
 // where they lie they would cost a line per lane.
 // Few tokens (SWAP): the weights are the first operand, 128 channels a tile, and the tokens the second,
-// 16 to 64 columns, so that no tensor-core row is idle; a thread has one channel.  Bound by the weights' bytes.
+// 16 or 32 columns, so that no tensor-core row is idle; a thread has one channel.  Bound by the weights' bytes.
 // Few tiles with long rows: a cluster per tile, each CTA with its share of the runs; the sums meet in the
 // cluster's shared memory, added in the order of the ranks.
 #include <cuda_fp8.h>
 
 #include "kt_ops_internal.h"
 #include "kt_gemm.cuh"
+#include "kt_exact.cuh"
 #include "kt_matmul.cuh"
 
 namespace kt {
@@ -34,7 +35,7 @@ constexpr uint32_t kF8ABytes = 128 * kRun;
 // The quantiser
 // ---------------------------------------------------------------------------
 
-constexpr int kQuantThreads = 256;
+constexpr int kQuantThreads = 256, kQuantRows = 4;
 
 __device__ __forceinline__ float activate(float z, int act) {
     f32x2 v = f2(z, 0.0f);
@@ -47,65 +48,77 @@ __device__ __forceinline__ float activate(float z, int act) {
     }
 }
 
-// Sixteen lanes per run of 128 columns, eight columns each: consecutive ones (WIDE: 16-byte loads, 8-byte
-// stores), else every sixteenth.  Bound by memory: 3 bytes per element.
-template <int DT, bool WIDE>
-__global__ void __launch_bounds__(kQuantThreads) kt_quantize_fp8_kernel(const QuantFp8 p, int runs) {
+// Eight elements of a run in 16 bits: consecutive ones (WIDE, a 16-byte load), else every sixteenth; zeros past its end.
+template <bool WIDE>
+__device__ __forceinline__ uint4 run_slot(const uint16_t* at, int l, int end) {
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (WIDE) {
+        if (8 * l < end) w = *reinterpret_cast<const uint4*>(at + 8 * l);
+    } else {
+        uint32_t u[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = l + 16 * e < end ? at[l + 16 * e] : 0u;
+        w = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
+    }
+    return w;
+}
+
+// Sixteen lanes per run of 128 columns, four rows of it at a time, whose loads go out together.  Bound by memory, 3 bytes
+// per element.  ACT: the activation of X is quantised.
+template <int DT, bool WIDE, bool ACT>
+__global__ void __launch_bounds__(kQuantThreads) kt_quantize_fp8_kernel(const QuantFp8 p, int runs, int64_t total) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int kPer = kQuantThreads / 16;
     const int l = threadIdx.x & 15;
-    const int64_t total = (int64_t)p.M * runs, stride = (int64_t)gridDim.x * (kQuantThreads / 16);
     // the two halves of a warp may end apart: the whole warp goes on while either has a run
-    for (int64_t i = (int64_t)blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4); (i & ~(int64_t)1) < total; i += stride) {
+    for (int64_t i = (int64_t)blockIdx.x * kPer + (threadIdx.x >> 4); (i & ~(int64_t)1) < total; i += (int64_t)gridDim.x * kPer) {
         const bool live = i < total;
-        const int64_t row = live ? i / runs : 0;
-        const int run = live ? (int)(i - row * runs) : 0, k0 = run * kRun, end = live ? min(kRun, p.K - k0) : 0;
-        float f[8];
-        auto load = [&](const uint16_t* at, float* to) {
+        const int64_t group = !live ? 0 : total <= INT32_MAX ? (int64_t)((uint32_t)i / (uint32_t)runs) : i / runs;
+        const int64_t row0 = group * kQuantRows;
+        const int run = live ? (int)(i - group * runs) : 0, end = live ? min(kRun, p.K - run * kRun) : 0;
+        const int rows = (int)min((int64_t)kQuantRows, p.M - row0);
+        const uint16_t* x = static_cast<const uint16_t*>(p.X) + row0 * p.ldx + run * kRun;
+        uint4 w[kQuantRows], gate[ACT ? kQuantRows : 1];
+#pragma unroll
+        for (int a = 0; a < kQuantRows; ++a) {
+            w[a] = run_slot<WIDE>(x + a * p.ldx, l, a < rows ? end : 0);
+            if constexpr (ACT) gate[a] = p.act == EPI_GEGLU ? run_slot<WIDE>(x + a * p.ldx + p.K, l, a < rows ? end : 0) : w[a];
+        }
+#pragma unroll
+        for (int a = 0; a < kQuantRows; ++a) {
+            float f[8];
+            unpack8<DT>(w[a], f);
+            if constexpr (ACT) {
+                float g[8];
+                unpack8<DT>(gate[a], g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = p.act == EPI_GEGLU ? f[e] * activate(g[e], EPI_GELU_ERF) : activate(f[e], p.act);
+            }
+            float most = fabsf(f[0]);
+#pragma unroll
+            for (int e = 1; e < 8; ++e) most = max_nan(most, fabsf(f[e]));
+#pragma unroll
+            for (int o = 8; o; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+            f32x2 both;  // most / 448, 448 / most
+            if (most >= 0x1p-60f && most <= 0x1p60f) both = quotient_rn(f2(most, 448.0f), f2(448.0f, most), f2(-448.0f, -most));
+            else both = most < 0x1p-100f ? f2(0.0f) : f2(__fdiv_rn(most, 448.0f), __fdiv_rn(448.0f, most));
+            if (a >= rows || !end) continue;
+            if (l == 0) p.scale[(row0 + a) * runs + run] = both.x;
+            uint32_t q[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const f32x2 t = f2_mul<true>(f2(f[2 * j], f[2 * j + 1]), f2(both.y));
+                q[j] = __nv_cvt_float2_to_fp8x2(make_float2(t.x, t.y), __NV_SATFINITE, __NV_E4M3);
+            }
+            uint8_t* to = p.Q + (row0 + a) * p.ldq + run * kRun;
             if constexpr (WIDE) {
-                uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                if (8 * l < end) w = *reinterpret_cast<const uint4*>(at + 8 * l);
-                unpack8<DT>(w, to);
+                if (8 * l < end) *reinterpret_cast<uint2*>(to + 8 * l) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float t[8] = {};
-                    if (l + 16 * e < end) unpack8<DT>(make_uint4(at[l + 16 * e], 0u, 0u, 0u), t);
-                    to[e] = t[0];
-                }
+                for (int e = 0; e < 8; ++e)
+                    if (l + 16 * e < end) to[l + 16 * e] = (uint8_t)(q[e >> 1] >> (8 * (e & 1)));
             }
-        };
-        const uint16_t* x = static_cast<const uint16_t*>(p.X) + row * p.ldx + k0;
-        load(x, f);
-        if (p.act == EPI_GEGLU) {
-            float g[8];
-            load(x + p.K, g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] *= activate(g[e], EPI_GELU_ERF);
-        } else if (p.act != EPI_NONE) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = activate(f[e], p.act);
-        }
-        uint32_t most = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(f[e]) & 0x7fffffffu);
-#pragma unroll
-        for (int o = 8; o; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-        const float top = __uint_as_float(most);
-        const bool zero = top < 0x1p-100f;
-        const float inverse = zero ? 0.0f : __fdiv_rn(448.0f, top);
-        if (live && l == 0) p.scale[row * runs + run] = zero ? 0.0f : __fdiv_rn(top, 448.0f);
-        uint8_t* q = p.Q + row * p.ldq + k0;
-        if constexpr (WIDE) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w[j] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(f[2 * j], inverse), __fmul_rn(f[2 * j + 1], inverse)), __NV_SATFINITE, __NV_E4M3);
-            if (8 * l < end) *reinterpret_cast<uint2*>(q + 8 * l) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (l + 16 * e < end) q[l + 16 * e] = __nv_cvt_float_to_fp8(__fmul_rn(f[e], inverse), __NV_SATFINITE, __NV_E4M3);
         }
     }
 }
@@ -265,20 +278,20 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
             uint32_t stage = 0, phase = 0, buf = 0, use = 0;
             const uint64_t ad0 = smem_desc(base, 16u, 1024u), bd0 = smem_desc(base + kF8ABytes, 16u, 1024u);
             bool ok = true, any = false;
+            // Narrow tiles are bound by this warp's instructions: both barriers of the next step are asked for before this
+            // one's products, and the answers are there after them (1024 x 1024 x 8192 17.0 -> 16.3 us; wide tiles
+            // lose by it, 8192^3 369 -> 378).
+            constexpr bool kAhead = BN <= 128;
+            uint32_t full = 0u, free = 0u;
             for (int t = unit0; t < tiles && ok; t += units)
                 for (int j = 0; j < runs; ++j) {
                     ok = __all_sync(0xffffffffu,
-                                    wait_turn(bar_full + 8u * stage, phase, abort_flag, &g_fp8_error, DEV_TIMEOUT_MMA, limit) &&
-                                        wait_turn<PAIR == 2>(bar_acce + 8u * buf, (use & 1u) ^ 1u, abort_flag, &g_fp8_error, DEV_TIMEOUT_MMA, limit));
+                                    (full || wait_turn(bar_full + 8u * stage, phase, abort_flag, &g_fp8_error, DEV_TIMEOUT_MMA, limit)) &&
+                                        (free || wait_turn(bar_acce + 8u * buf, (use & 1u) ^ 1u, abort_flag, &g_fp8_error, DEV_TIMEOUT_MMA, limit)));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t d = tmem + buf * (uint32_t)BN;
+                    const uint32_t d = tmem + buf * (uint32_t)BN, now = stage, which = buf;
                     const uint64_t ad = ad0 + stage * (C::kStage >> 4), bd = bd0 + stage * (C::kStage >> 4);
-#pragma unroll
-                    for (uint32_t k = 0; k < 4; ++k) mma_if<PAIR, true>(d, ad + 2 * k, bd + 2 * k, p.idesc, k > 0, one);  // 32 columns each
-                    any = true;
-                    commit_if<PAIR>(bar_empty + 8u * stage, one);
-                    commit_if<PAIR>(bar_accf + 8u * buf, one);
                     if (++stage == (uint32_t)kStages) {
                         stage = 0;
                         phase ^= 1u;
@@ -287,6 +300,15 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
                         buf = 0;
                         ++use;
                     }
+                    if constexpr (kAhead) {
+                        full = mbar_test_wait(bar_full + 8u * stage, phase);
+                        free = mbar_test_wait(bar_acce + 8u * buf, (use & 1u) ^ 1u);
+                    }
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; ++k) mma_if<PAIR, true>(d, ad + 2 * k, bd + 2 * k, p.idesc, k > 0, one);  // 32 columns each
+                    any = true;
+                    commit_if<PAIR>(bar_accf + 8u * which, one);
+                    commit_if<PAIR>(bar_empty + 8u * now, one);
                 }
             if (!ok && any) {  // no product may still be running when tensor memory is freed
                 commit_if<PAIR>(bar_drain, one);
@@ -333,7 +355,7 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
             const float* sw = p.sw + (int64_t)(n / 128) * p.runs + run0;  // (SWAP: one block of channels)
             float w_next = 0.0f;
             if constexpr (SWAP) w_next = sw[0];
-            constexpr int kPer = SWAP ? (BN + 31) / 32 : 1;  // SWAP: tokens lane and lane + 32
+            constexpr int kPer = SWAP ? (BN + 31) / 32 : 1;  // SWAP: token lane
             float x_next[kPer];
             auto tokens = [&](int j) {
 #pragma unroll
@@ -612,11 +634,15 @@ kt_status launch_quantize_fp8(int dtype, const QuantFp8& p, int sms, void* strea
     const int runs = (p.K + kRun - 1) / kRun;
     const bool wide = p.K % 8 == 0 && p.ldx % 8 == 0 && p.ldq % 8 == 0 && (reinterpret_cast<uintptr_t>(p.X) & 15u) == 0 &&
                       (reinterpret_cast<uintptr_t>(p.Q) & 7u) == 0;
-    const int64_t blocks = ((int64_t)p.M * runs + kQuantThreads / 16 - 1) / (kQuantThreads / 16);
-    const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)sms * 32);
-    auto go = [&](auto kern) { return launch_pdl(kern, grid, (unsigned)kQuantThreads, (size_t)0, stream, p, runs); };
-    const cudaError_t e = dtype == KT_BF16 ? (wide ? go(kt_quantize_fp8_kernel<KT_BF16, true>) : go(kt_quantize_fp8_kernel<KT_BF16, false>))
-                                           : (wide ? go(kt_quantize_fp8_kernel<KT_F16, true>) : go(kt_quantize_fp8_kernel<KT_F16, false>));
+    const int64_t total = (int64_t)((p.M + kQuantRows - 1) / kQuantRows) * runs, per = kQuantThreads / 16;
+    const unsigned grid = (unsigned)std::min<int64_t>((total + per - 1) / per, (int64_t)sms * 64);
+    auto go = [&](auto dt, auto wide_, auto act) {
+        return launch_pdl(kt_quantize_fp8_kernel<decltype(dt)::value, decltype(wide_)::value, decltype(act)::value>, grid, (unsigned)kQuantThreads, (size_t)0,
+                          stream, p, runs, total);
+    };
+    auto by_act = [&](auto dt, auto wide_) { return p.act == EPI_NONE ? go(dt, wide_, std::false_type{}) : go(dt, wide_, std::true_type{}); };
+    auto by_width = [&](auto dt) { return wide ? by_act(dt, std::true_type{}) : by_act(dt, std::false_type{}); };
+    const cudaError_t e = dtype == KT_BF16 ? by_width(std::integral_constant<int, KT_BF16>{}) : by_width(std::integral_constant<int, KT_F16>{});
     if (e != cudaSuccess) {
         *why = cudaGetErrorString(e);
         return KT_ERR_CUDA;
@@ -628,9 +654,10 @@ Fp8Shape linear_fp8_shape(const LinearFp8& a, int sms, int device) {
     const int runs = (a.K + kRun - 1) / kRun;
     Fp8Shape best = {};
     double least = 1e30;
-    auto consider = [&](int pair, int bn, int swap, int64_t tiles, double step, double round) {
+    // us per run of 128 columns, of a launch, and of sharing a tile's runs; measured from 5 to 128 runs
+    auto consider = [&](int pair, int bn, int swap, int64_t tiles, double step, double round, double sharing) {
         const int64_t units = sms / pair, rounds = (tiles + units - 1) / units;
-        const double time = rounds * (runs * step + 0.7) + round;
+        const double time = rounds * runs * step + (rounds - 1) * 0.7 + round;
         if (time < least) {
             least = time;
             best = {pair, bn, swap, 1};
@@ -638,7 +665,7 @@ Fp8Shape linear_fp8_shape(const LinearFp8& a, int sms, int device) {
         if (pair == 2) return;
         for (int ks = 2; ks <= 8; ks *= 2) {
             if (tiles * ks > sms || runs < 2 * ks || tiles > f8_clusters(ks, device)) continue;
-            const double split = (runs + ks - 1) / ks * step + round + 2.0;
+            const double split = (runs + ks - 1) / ks * step + round + sharing;
             if (split < least) {
                 least = split;
                 best = {1, bn, swap, ks};
@@ -646,21 +673,22 @@ Fp8Shape linear_fp8_shape(const LinearFp8& a, int sms, int device) {
         }
     };
     if (a.M <= KT_LINEAR_FP8_FEW) {
-        consider(1, a.M <= 16 ? 16 : a.M <= 32 ? 32 : 64, 1, (a.N + 127) / 128, 0.20, 3.0);
+        const int64_t tiles = (a.N + 127) / 128;
+        if (a.M <= 16) consider(1, 16, 1, tiles, 0.235, 3.4, 1.2);
+        else consider(1, 32, 1, tiles, 0.245, 3.9, 1.2);
         return best;
     }
     auto tiles = [&](int rows, int bn) { return (int64_t)((a.M + rows - 1) / rows) * ((a.N + bn - 1) / bn); };
-    consider(2, 256, 0, tiles(256, 256), 0.36, 4.0);
-    consider(2, 128, 0, tiles(256, 128), 0.25, 3.5);
-    consider(1, 128, 0, tiles(128, 128), 0.26, 3.0);
+    consider(2, 256, 0, tiles(256, 256), 0.37, 5.9, 0.0);
+    consider(2, 128, 0, tiles(256, 128), 0.27, 5.0, 0.0);
+    consider(1, 128, 0, tiles(128, 128), 0.25, 4.8, 3.0);
     return best;
 }
 
 kt_status launch_linear_fp8_as(int dtype, const LinearFp8& a, const Fp8Shape& s, int sms, int device, void* stream, const char** why) {
     if (s.swap) {
         if (s.BN == 16) return f8_launch<1, 16, true>(dtype, a, s.splits, sms, device, stream, why);
-        if (s.BN == 32) return f8_launch<1, 32, true>(dtype, a, s.splits, sms, device, stream, why);
-        return f8_launch<1, 64, true>(dtype, a, s.splits, sms, device, stream, why);
+        return f8_launch<1, 32, true>(dtype, a, s.splits, sms, device, stream, why);
     }
     if (s.pair == 1) return f8_launch<1, 128, false>(dtype, a, s.splits, sms, device, stream, why);
     if (s.BN == 128) return f8_launch<2, 128, false>(dtype, a, 1, sms, device, stream, why);

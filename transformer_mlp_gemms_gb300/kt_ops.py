@@ -30,7 +30,7 @@ KT_LAYERNORM_MAX_D = 16384
 KT_LINEAR_I8_DOT_ROWS = 16
 KT_MOE_MAX_TOKENS, KT_MOE_MAX_EXPERTS, KT_MOE_MAX_TOP_K = 64, 256, 16
 KT_F32, KT_ADAMW_BLOCK = 2, 256
-KT_LINEAR_FP8_FEW = 64
+KT_LINEAR_FP8_FEW = 32
 
 
 class kt_moe_options(ctypes.Structure):
