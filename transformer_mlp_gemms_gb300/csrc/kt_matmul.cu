@@ -17,8 +17,8 @@
 //   warps 2-9: epilogue.
 // SPLIT: few tiles with long sums: a cluster per tile, each CTA with its share of the steps; the fp32 sums meet
 // in the cluster's shared memory, added in the order of the ranks.
-// SHARED (the gradients): both products of a backward pass in one launch, on pairs, as two lists of tiles.  Either
-// whole tiles are dealt out in turn; or, where that would leave many pairs idle at the end, only whole rounds of
+// SHARED (gradients): both products of a backward pass in one launch, on pairs, as two lists of tiles, unless each is
+// quicker in a launch of its own (few tiles with long sums, which clusters share out more finely).  Either whole tiles are dealt out in turn; or, where that would leave many pairs idle at the end, only whole rounds of
 // them are, after the steps of the tiles that are left, which are dealt out evenly.  A tile whose steps fall to several
 // pairs is summed by the last of them: the others leave fp32 partial sums in the workspace and raise a flag.
 // A pair goes through its share backwards, so that what others wait for comes first and what waits for others comes
@@ -346,10 +346,14 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 constexpr std::true_type kMN{};
                 constexpr std::integral_constant<uint32_t, 1> kOne{};
                 constexpr std::integral_constant<uint32_t, 2> kTwo{};
-                if constexpr (SHARED) {
-                    if (o.a_mn) steps(kMN, kMN, kTwo);
-                    else steps(kK, kMN, kTwo);
-                } else {
+                if constexpr (GATED) {
+                    if (p.atoms == 1) steps(kK, kK, kOne);
+                    else steps(kK, kK, kTwo);
+                } else if (o.a_mn) {
+                    steps(kMN, kMN, kTwo);
+                } else if (o.b_mn) {
+                    steps(kK, kMN, kTwo);
+                } else if constexpr (!SHARED) {
                     if (p.atoms == 1) steps(kK, kK, kOne);
                     else steps(kK, kK, kTwo);
                 }
@@ -678,6 +682,9 @@ kt_status mm_done(cudaError_t e, const char** why) {
 
 }  // namespace
 
+// How much longer a step takes where rows of an operand start between 128-byte lines.
+static double off_lines(const Matmul& a) { return (a.lda | a.ldb) % 64 ? 1.5 : 1.0; }
+
 MatmulShape matmul_shape(const Matmul& a, int sms, int device) {
     const int steps = (a.K + kAtomK - 1) / kAtomK;
     // us per 64-deep step and per launch, measured from 10 to 80 steps
@@ -685,23 +692,19 @@ MatmulShape matmul_shape(const Matmul& a, int sms, int device) {
         int pair, bn, atoms;
         double step, round;
     } const kinds[] = {{2, 256, 1, 0.26, 6.0}, {2, 128, 2, 0.17, 5.3}, {1, 128, 2, 0.17, 4.9}, {1, 64, 2, 0.155, 4.5}};
+    constexpr double kSharing = 2.3;  // of a tile by a cluster
     MatmulShape best = {};
-    double least = 1e30;
+    best.us = 1e30;
     for (const auto& k : kinds) {
         const int64_t t = mm_tiles(a, k.bn, k.pair), units = sms / k.pair, rounds = (t + units - 1) / units;
-        const double time = rounds * steps * k.step + (rounds - 1) * 0.5 + k.round;
-        if (time < least) {
-            least = time;
-            best = {k.pair, k.bn, 1, k.atoms};
-        }
+        const int atoms = a.a_mn || a.b_mn ? 2 : k.atoms;
+        const double step = k.step * off_lines(a), time = rounds * steps * step + (rounds - 1) * 0.5 + k.round;
+        if (time < best.us) best = {k.pair, k.bn, 1, atoms, time};
         if (a.gated || k.pair == 2) continue;
         for (int ks = 2; ks <= 8; ks *= 2) {
             if (t * ks > sms || steps < 2 * ks || t > mm_clusters(ks, device)) continue;
-            const double split = (steps + ks - 1) / ks * k.step + k.round + 2.3;
-            if (split < least) {
-                least = split;
-                best = {1, k.bn, ks, k.atoms};
-            }
+            const double split = (steps + ks - 1) / ks * step + k.round + kSharing;
+            if (split < best.us) best = {1, k.bn, ks, atoms, split};
         }
     }
     return best;
@@ -776,10 +779,10 @@ kt_status launch_gradients_as(int dtype, const Matmul* a, int count, const Gradi
 }
 
 GradientsShape gradients_shape(const Matmul* a, int count, int sms) {
-    constexpr double kSharing = 7.0;  // us
+    constexpr double kSharing = 7.0, kLaunch = 6.0;  // us
     const int units = sms / 2;
     GradientsShape best = {};
-    double least = 1e30;
+    best.us = 1e30;
     for (int mask = 0; mask < 1 << count; ++mask) {
         int64_t tiles[2] = {}, steps[2] = {};
         double step[2] = {}, tile[2] = {};
@@ -788,9 +791,8 @@ GradientsShape gradients_shape(const Matmul* a, int count, int sms) {
             s.bn[i] = mask >> i & 1 ? 128 : 256;
             tiles[i] = mm_tiles(a[i], s.bn[i], 2);
             steps[i] = (a[i].K + kAtomK - 1) / kAtomK;
-            // us, measured; rows that start between 128-byte lines take half as long again; a tile of few steps takes its
-            // epilogue's time
-            step[i] = (s.bn[i] == 256 ? 0.27 : 0.165) * ((a[i].lda | a[i].ldb) % 64 ? 1.5 : 1.0);
+            // us, measured; a tile of few steps takes its epilogue's time
+            step[i] = (s.bn[i] == 256 ? 0.27 : 0.165) * off_lines(a[i]);
             tile[i] = std::max(steps[i] * step[i], s.bn[i] == 256 ? 1.9 : 1.2);
         }
         // in turn: the pair with the most
@@ -818,18 +820,37 @@ GradientsShape gradients_shape(const Matmul* a, int count, int sms) {
         }
         for (int k = 0; k < 2; ++k) {
             const double time = k ? share : most;
-            if (time < least && (!k || sharers)) {
-                least = time;
+            if (time + kLaunch < best.us && (!k || sharers)) {
                 best = s;
                 best.share = k ? sharers : 0;
+                best.us = time + kLaunch;
             }
         }
     }
     return best;
 }
 
-kt_status launch_gradients(int dtype, const Matmul* a, int count, void* scratch, int sms, int device, void* stream, const char** why) {
-    return launch_gradients_as(dtype, a, count, gradients_shape(a, count, sms), scratch, sms, device, stream, why);
+kt_status launch_gradients(int dtype, const Matmul* a, int count, void* scratch, bool zeroed, int sms, int device, void* stream, const char** why) {
+    const GradientsShape both = gradients_shape(a, count, sms);
+    // each on its own, where that is quicker: clusters on few tiles with long sums
+    MatmulShape each[2];
+    double us = -1.5 * (count - 1);  // (the second launch's beginning is hidden)
+    for (int i = 0; i < count; ++i) {
+        each[i] = matmul_shape(a[i], sms, device);
+        us += each[i].us;
+    }
+    if (both.us <= us) {
+        if (both.share && !zeroed) {
+            const kt_status s = launch_zero(static_cast<int*>(scratch), stream, why);
+            if (s != KT_OK) return s;
+        }
+        return launch_gradients_as(dtype, a, count, both, scratch, sms, device, stream, why);
+    }
+    for (int i = 0; i < count; ++i) {
+        const kt_status s = launch_matmul_as(dtype, a[i], each[i], sms, device, stream, why);
+        if (s != KT_OK) return s;
+    }
+    return KT_OK;
 }
 
 kt_status matmul_status(void* stream, int* word, const char** why) { return error_word(g_matmul_error, stream, word, why); }

@@ -91,9 +91,9 @@ kt::Matmul product(int64_t M, int64_t N, int64_t K) {
     a.wait_limit_ns = a.stall_ns ? a.stall_ns : kWaitLimitNs;
     return a;
 }
-// dX = dP . W and dW = dP^T . X in one launch, for dP [M][N], W [N][K], X [M][K].  scratch: as launch_gradients has it.
+// dX = dP . W and dW = dP^T . X, for dP [M][N], W [N][K], X [M][K].  scratch: as launch_gradients has it.
 kt_status gradients(int64_t M, int64_t N, int64_t K, int dtype, const void* dP, int64_t lddp, const void* X, int64_t ldx, const void* W,
-                    void* dX, int64_t lddx, void* dW, void* scratch, int sms, int device, void* stream) {
+                    void* dX, int64_t lddx, void* dW, void* scratch, bool zeroed, int sms, int device, void* stream) {
     kt::Matmul a[2];
     int count = 0;
     if (dW) {
@@ -120,7 +120,7 @@ kt_status gradients(int64_t M, int64_t N, int64_t K, int dtype, const void* dP, 
     if (!count) return done(KT_OK, "");
     if (count == 2 && a[1].K > a[0].K) std::swap(a[0], a[1]);
     const char* why = "";
-    return done(kt::launch_gradients(dtype, a, count, scratch, sms, device, stream, &why), why);
+    return done(kt::launch_gradients(dtype, a, count, scratch, zeroed, sms, device, stream, &why), why);
 }
 kt_status zeros(void* p, size_t bytes, void* stream) {
     if (!p || !bytes) return KT_OK;
@@ -456,7 +456,7 @@ kt_status kt_glu_backward(int64_t M, int64_t D, int64_t F, kt_dtype dtype, kt_ac
     g.F = (int)F;
     g.act = epilogue_of(act);
     if ((s = kt::launch_glu_backward(dtype, g, stream, &why)) != KT_OK) return kt::report(s, why);
-    return gradients(M, 2 * F, D, dtype, workspace, 2 * F, X, ldx, W, dX, lddx, dW, scratch, sms, dev, stream);
+    return gradients(M, 2 * F, D, dtype, workspace, 2 * F, X, ldx, W, dX, lddx, dW, scratch, true, sms, dev, stream);
 }
 
 kt_status kt_linear_forward(int64_t M, int64_t N, int64_t K, kt_dtype dtype, const void* X, int64_t ldx, const void* W,
@@ -516,12 +516,9 @@ kt_status kt_linear_backward(int64_t M, int64_t N, int64_t K, kt_dtype dtype, co
         g.zero = reinterpret_cast<int*>(scratch);
         g.M = (int)M;
         g.F = (int)N;
-        s = kt::launch_glu_backward(dtype, g, stream, &why);
-    } else {
-        s = kt::launch_zero(reinterpret_cast<int*>(scratch), stream, &why);
+        if ((s = kt::launch_glu_backward(dtype, g, stream, &why)) != KT_OK) return kt::report(s, why);
     }
-    if (s != KT_OK) return kt::report(s, why);
-    return gradients(M, N, K, dtype, dY, lddy, X, ldx, W, dX, lddx, dW, scratch, sms, dev, stream);
+    return gradients(M, N, K, dtype, dY, lddy, X, ldx, W, dX, lddx, dW, scratch, db != nullptr, sms, dev, stream);
 }
 
 kt_status kt_adamw(int64_t count, const kt_adamw_tensor* tensors, const kt_adamw_options* o, void* stream) {

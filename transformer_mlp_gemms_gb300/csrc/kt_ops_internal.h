@@ -106,21 +106,23 @@ struct Matmul {
 // stage of the ring.
 struct MatmulShape {
     int pair, BN, splits, atoms;
+    double us;  // what it is expected to take
 };
 MatmulShape matmul_shape(const Matmul& a, int sms, int device);
 kt_status launch_matmul_as(int dtype, const Matmul& a, const MatmulShape& s, int sms, int device, void* stream, const char** why);
 kt_status launch_matmul(int dtype, const Matmul& a, int sms, int device, void* stream, const char** why);
-// One or two products of a backward pass in one launch, the one with longer sums first.  scratch: flags (zero before the
-// launch, kGradientsFlags bytes), then gradients_partials() bytes.
+// One or two products of a backward pass, in one launch (the one with longer sums first) or each in its own.  scratch:
+// flags (kGradientsFlags bytes, set to zero here unless zeroed), then gradients_partials() bytes.
 constexpr size_t kGradientsFlags = kMaxSms * sizeof(int);  // a flag per CTA
 constexpr int kGradientsLeast = 4;  // steps that a pair's share of the last tiles has at least
 struct GradientsShape {
     int bn[2], share;  // tile widths (128 or 256); the pairs that the last tiles' steps are shared out to, 0: none are
+    double us;         // what it is expected to take
 };
 size_t gradients_partials();
 GradientsShape gradients_shape(const Matmul* a, int count, int sms);
 kt_status launch_gradients_as(int dtype, const Matmul* a, int count, const GradientsShape& s, void* scratch, int sms, int device, void* stream, const char** why);
-kt_status launch_gradients(int dtype, const Matmul* a, int count, void* scratch, int sms, int device, void* stream, const char** why);
+kt_status launch_gradients(int dtype, const Matmul* a, int count, void* scratch, bool zeroed, int sms, int device, void* stream, const char** why);
 kt_status matmul_status(void* stream, int* word, const char** why);
 
 // The elementwise part of the backward pass of a gated block, and column sums (kt_glu.cu).
