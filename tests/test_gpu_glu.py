@@ -324,3 +324,39 @@ def test_offsets_past_32_bits():
     _, _, dwx, tw, dbx, tb = ref.linear_backward(x, y, dw, dt)
     near(dw, dwx, tw)
     near(db, dbx, tb)
+
+
+@pytest.mark.parametrize("M,D,F", [(1, 4304, 64), (5, 2304, 1152), (33, 5120, 40), (128, 8192, 264), (200, 4096, 320)])
+@pytest.mark.parametrize("dtype,bias", [("f16", True), ("bf16", False)])
+def test_gated_projection_of_few_tiles_with_long_sums(M, D, F, dtype, bias):
+    g = torch.Generator().manual_seed(2 * M + D + F)
+    dt, name = DT[dtype], sorted(ACTS)[(M + F) % len(ACTS)]
+    x, w = randn(g, M, D, dtype=dt, pad=24), randn(g, 2 * F, D, dtype=dt, std=D ** -0.5)
+    b = randn(g, 2 * F, dtype=dt, std=0.2) if bias else None
+    hs, h = nans(M, F, dt, 8)
+    ps, p = nans(M, 2 * F, dt, 16)
+    kt_ops.kt_glu_forward(x, w, b, h, p, ACTS[name])
+    assert kt_ops.kt_matmul_status() == kt_mlp.KT_OK
+    hx, th, px, tp = ref.glu(x, w, b, name, dt)
+    near(p, px, tp)
+    near(h, hx, th)
+    assert hs[:, F:].isnan().all() and ps[:, 2 * F:].isnan().all()
+    alone = torch.empty_like(h)
+    kt_ops.kt_glu_forward(x, w, b, alone, None, ACTS[name])
+    assert torch.equal(alone, h)
+
+
+@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 31, 100, 127, 128, 129])
+@pytest.mark.parametrize("N", [8, 24, 64, 120, 136])
+def test_rows_and_columns_that_end_inside_a_tile(M, N):
+    """What a tile reads beyond its operands may be anything, NaN too: none of it reaches a result."""
+    dt, K = torch.bfloat16, 328
+    g = torch.Generator().manual_seed(M + N)
+    junk = torch.full((4096, 4096), float("nan"), dtype=dt, device="cuda")
+    kt_ops.kt_linear_forward(junk, junk, None, torch.empty_like(junk))  # NaN in every block's shared memory
+    x, w, b = randn(g, M, K, dtype=dt), randn(g, N, K, dtype=dt, std=K ** -0.5), randn(g, N, dtype=dt)
+    ys, y = nans(M, N, dt, 8)
+    kt_ops.kt_linear_forward(x, w, b, y)
+    yx, ty = ref.product(x.double(), w.double(), b)
+    near(y, yx, ref.rounded(yx, ty, dt))
+    assert ys[:, N:].isnan().all()

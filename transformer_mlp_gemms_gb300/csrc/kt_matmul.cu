@@ -16,7 +16,7 @@
 //   warp 0: copies of A, and each step's byte count; warp 10: copies of B; warp 1: products;
 //   warps 2-9: epilogue.
 // SPLIT: few tiles with long sums: a cluster per tile, each CTA with its share of the steps; the fp32 sums meet
-// in the cluster's shared memory, added in the order of the ranks.
+// in the cluster's shared memory, added in an order that the place of the sum alone decides.
 // SHARED (gradients): both products of a backward pass in one launch, on pairs, as two lists of tiles, unless each is
 // quicker in a launch of its own (few tiles with long sums, which clusters share out more finely).  Either whole tiles are dealt out in turn; or, where that would leave many pairs idle at the end, only whole rounds of
 // them are, after the steps of the tiles that are left, which are dealt out evenly.  A tile whose steps fall to several
@@ -55,6 +55,7 @@ struct MmParams {
     MmProduct of[2];          // SHARED: two, else the first
     int stages, atoms, act, has_p;  // atoms: 64-deep steps of K per stage of the ring
     uint32_t stage_bytes;
+    uint32_t a_bytes, step_bytes;  // the room of one step of A; the bytes of one step's copies
     const void* bias;
     // SHARED: the steps of the tiles left, of both products, and the pairs that they are dealt to
     int steps, sharers;
@@ -121,6 +122,17 @@ __device__ __forceinline__ void gate32(const float* v, const float* g, uint32_t*
 }
 
 template <int DT>
+__device__ __forceinline__ void gate_any(int act, const float* v, const float* g, uint32_t* w) {
+    switch (act) {
+        case EPI_GELU_ERF: return gate32<DT, EPI_GELU_ERF>(v, g, w);
+        case EPI_GELU_TANH: return gate32<DT, EPI_GELU_TANH>(v, g, w);
+        case EPI_GELU_SIGMOID: return gate32<DT, EPI_GELU_SIGMOID>(v, g, w);
+        case EPI_SILU: return gate32<DT, EPI_SILU>(v, g, w);
+        default: return gate32<DT, EPI_NONE>(v, g, w);
+    }
+}
+
+template <int DT>
 __device__ __forceinline__ void pack32(const float* v, uint32_t* w) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = pack2<DT>(v[2 * i], v[2 * i + 1]);
@@ -178,13 +190,13 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                      const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmX,
                      const __grid_constant__ MmParams p) {
-    static_assert(!(SPLIT && (GATED || PAIR == 2)), "a split tile is one CTA's, not gated");
+    static_assert(!(SPLIT && PAIR == 2), "a split tile is one CTA's");
     static_assert(!SHARED || (PAIR == 2 && !GATED && !SPLIT), "shared steps are pairs', of plain products");
     // SHARED: tmV, tmG and tmX are the second product's maps of A, B and C
     extern __shared__ uint8_t raw[];
     uint8_t* const at = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     const uint32_t base = smem_u32(at);
-    const uint32_t stage_bytes = p.stage_bytes;
+    const uint32_t stage_bytes = p.stage_bytes, a_bytes = SHARED || PAIR == 2 ? kMmABytes : p.a_bytes;
     const uint32_t staging = base + (uint32_t)p.stages * stage_bytes;  // two 2 KB buffers per epilogue warp
     const uint32_t bars = staging + kMmEpi * 4096u;
     const uint32_t bar_full = bars, bar_empty = bars + 64u, bar_accf = bars + 128u, bar_acce = bars + 144u, bar_drain = bars + 160u,
@@ -258,7 +270,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             const CUtensorMap *mA = SHARED && it.product ? &tmV : &tmA, *mB = SHARED && it.product ? &tmG : &tmB;
             const CUtensorMap* const map = a_role ? mA : mB;
             const bool mn = a_role ? o.a_mn : o.b_mn;
-            const uint32_t atoms = (uint32_t)p.atoms, operand = a_role ? kMmABytes : o.b_bytes, bytes = PAIR * atoms * (kMmABytes + o.b_bytes);
+            const uint32_t atoms = (uint32_t)p.atoms, operand = a_role ? a_bytes : o.b_bytes, bytes = SHARED ? PAIR * atoms * (kMmABytes + o.b_bytes) : p.step_bytes;
             int m, n;
             origin(it, m, n);
             const int row = a_role ? m : n;
@@ -266,7 +278,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 ok = __all_sync(0xffffffffu, wait_turn(bar_empty + 8u * stage, phase ^ 1u, abort_flag, &g_matmul_error, DEV_TIMEOUT_PRODUCER, limit));
                 if (!ok) break;
                 // (a stage may reach past the item's steps, and past K, where zeros are filled in: its products end in time)
-                const uint32_t to = base + stage * stage_bytes + (a_role ? 0u : atoms * kMmABytes), fb = full0 + 8u * stage;
+                const uint32_t to = base + stage * stage_bytes + (a_role ? 0u : atoms * a_bytes), fb = full0 + 8u * stage;
                 const int k = kb * kAtomK;
                 if (a_role) expect_tx_if(bar_full + 8u * stage, bytes, arm);
                 if (mn) {  // 64 columns each
@@ -318,8 +330,8 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 auto steps = [&](auto a_mn, auto b_mn, auto atoms_) {
                     constexpr uint32_t kA = decltype(a_mn)::value ? 128u : 2u, kB = decltype(b_mn)::value ? 128u : 2u, kAtoms = decltype(atoms_)::value;
                     const uint64_t ad0 = smem_desc(base, decltype(a_mn)::value ? kAtoms * 8192u : 16u, 1024u);
-                    const uint64_t bd0 = smem_desc(base + kAtoms * kMmABytes, decltype(b_mn)::value ? kAtoms * 8192u : 16u, 1024u);
-                    const uint32_t idesc = o.idesc, a16 = decltype(a_mn)::value ? 512u : kMmABytes >> 4, b16 = decltype(b_mn)::value ? 512u : o.b_bytes >> 4;
+                    const uint64_t bd0 = smem_desc(base + kAtoms * a_bytes, decltype(b_mn)::value ? kAtoms * 8192u : 16u, 1024u);
+                    const uint32_t idesc = o.idesc, a16 = decltype(a_mn)::value ? 512u : a_bytes >> 4, b16 = decltype(b_mn)::value ? 512u : o.b_bytes >> 4;
                     uint32_t acc = 0;
                     for (int kb = it.kb0; kb < it.kb1; kb += (int)kAtoms) {
                         ok = __all_sync(0xffffffffu, wait_turn(bar_full + 8u * stage, phase, abort_flag, &g_matmul_error, DEV_TIMEOUT_MMA, limit));
@@ -442,13 +454,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                         pack32<DT>(gt, w);
                         store(&tmG, w, col);
                     }
-                    switch (p.act) {
-                        case EPI_GELU_ERF: gate32<DT, EPI_GELU_ERF>(v, gt, w); break;
-                        case EPI_GELU_TANH: gate32<DT, EPI_GELU_TANH>(v, gt, w); break;
-                        case EPI_GELU_SIGMOID: gate32<DT, EPI_GELU_SIGMOID>(v, gt, w); break;
-                        case EPI_SILU: gate32<DT, EPI_SILU>(v, gt, w); break;
-                        default: gate32<DT, EPI_NONE>(v, gt, w); break;
-                    }
+                    gate_any<DT>(p.act, v, gt, w);
                     store(&tmC, w, col);
                 }
             } else if (SHARED && it.kb1 < o.kblocks) {
@@ -518,41 +524,71 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         if (warp >= 2 && warp < 10) {
             const int ew = warp - 2;
             const uint32_t stg = staging + (uint32_t)ew * 4096u;
+            const MmProduct& o = p.of[0];
+            const uint16_t* bias = static_cast<const uint16_t*>(p.bias);
             int m, n;
             origin(MmItem{0, unit0, 0, 0}, m, n);
-            for (int u = part + splits * ew; u < p.of[0].BN / 8; u += splits * kMmEpi) {  // units of this CTA: every splits-th
-                const int q = u & 3, col = n + 32 * (u >> 2), y = m + 32 * q;
-                if (col >= p.of[0].N || y >= p.of[0].M) continue;
-                float v[32];
+            uint32_t stores = 0;
+            // 32 x 32 sums, with their bias
+            auto sums = [&](int unit, const uint16_t* b, int col, float* v) {
+                uint32_t from = base + (uint32_t)unit * 4096u + (uint32_t)lane * 16u;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t from = base + (uint32_t)u * 4096u + (uint32_t)(i * 512 + lane * 16);
-                    float4 x[8];
+                for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+                for (int j0 = 0; j0 < splits; j0 += 2) {  // two CTAs' sums on their way at a time, from this one's on
+                    float4 x[2][8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < splits) x[j] = ld_cluster4(mapa_rank(from, (uint32_t)j));
+                    for (int j = 0; j < 2; ++j) {
+                        if (j0 + j >= splits) break;
+                        const int from_rank = part + j0 + j, at_rank = from_rank < splits ? from_rank : from_rank - splits;
+                        const uint32_t at_j = mapa_rank(from, (uint32_t)at_rank);
 #pragma unroll
-                    for (int j = 1; j < 8; ++j)
-                        if (j < splits) {
-                            x[0].x += x[j].x;
-                            x[0].y += x[j].y;
-                            x[0].z += x[j].z;
-                            x[0].w += x[j].w;
+                        for (int i = 0; i < 8; ++i) x[j][i] = ld_cluster4(at_j + (uint32_t)i * 512u);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (j0 + j >= splits) break;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            v[4 * i] += x[j][i].x;
+                            v[4 * i + 1] += x[j][i].y;
+                            v[4 * i + 2] += x[j][i].z;
+                            v[4 * i + 3] += x[j][i].w;
                         }
-                    v[4 * i] = x[0].x;
-                    v[4 * i + 1] = x[0].y;
-                    v[4 * i + 2] = x[0].z;
-                    v[4 * i + 3] = x[0].w;
+                    }
                 }
-                if (p.bias) {
-                    float b[32];
-                    bias32<DT>(p.bias, col, p.of[0].N, b);
+                if (b) {
+                    float add[32];
+                    bias32<DT>(b, col, o.N, add);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] += b[i];
+                    for (int i = 0; i < 32; ++i) v[i] += add[i];
                 }
+            };
+            auto store = [&](const CUtensorMap* tm, const uint32_t* w, int col, int y) {
+                stage_and_store_packed(tm, stg + (stores++ & 1u) * 2048u, lane, w, col, y, true);
+            };
+            const int units_here = (GATED ? o.BN / 2 : o.BN) / 8;
+            for (int u = part + splits * ew; u < units_here; u += splits * kMmEpi) {  // units of this CTA: every splits-th
+                const int q = u & 3, col = n + 32 * (u >> 2), y = m + 32 * q;
+                if (col >= o.N || y >= o.M) continue;
+                float v[32];
                 uint32_t w[16];
-                pack32<DT>(v, w);
-                stage_and_store_packed(&tmC, stg, lane, w, col, y);
+                sums(u, bias, col, v);
+                if constexpr (GATED) {
+                    float gt[32];
+                    if (p.has_p) {
+                        pack32<DT>(v, w);
+                        store(&tmV, w, col, y);
+                    }
+                    sums(u + units_here, bias ? bias + o.N : nullptr, col, gt);
+                    if (p.has_p) {
+                        pack32<DT>(gt, w);
+                        store(&tmG, w, col, y);
+                    }
+                    gate_any<DT>(p.act, v, gt, w);
+                } else {
+                    pack32<DT>(v, w);
+                }
+                store(&tmC, w, col, y);
             }
             if (lane == 0) bulk_wait0();
             __syncwarp();
@@ -622,7 +658,9 @@ cudaError_t mm_launch(const CUtensorMap* tm, const MmParams& p, int grid, int cl
 template <int DT>
 cudaError_t mm_dispatch(const CUtensorMap* tm, const MmParams& p, const MatmulShape& s, bool gated, int sms, int device, void* stream) {
     const int tiles = p.of[0].tiles_m * p.of[0].tiles_n;
-    if (s.splits > 1) return mm_launch<DT, 1, false, true, false>(tm, p, tiles * s.splits, s.splits, device, stream);
+    if (s.splits > 1)
+        return gated ? mm_launch<DT, 1, true, true, false>(tm, p, tiles * s.splits, s.splits, device, stream)
+                     : mm_launch<DT, 1, false, true, false>(tm, p, tiles * s.splits, s.splits, device, stream);
     const int grid = std::min(tiles, sms / s.pair) * s.pair;
     if (gated)
         return s.pair == 2 ? mm_launch<DT, 2, true, false, false>(tm, p, grid, 2, device, stream) : mm_launch<DT, 1, true, false, false>(tm, p, grid, 1, device, stream);
@@ -667,9 +705,9 @@ bool mm_gated(CUtensorMap* m, int dtype, const Matmul& a, int rows, const char**
     return encode_tmap_nd(m, a.B, dtype, 3, dims, strides, box, 128, why);
 }
 // a product's maps of A, B and C
-bool mm_maps(CUtensorMap* tm, int dtype, const Matmul& a, int bn, int pair, int atoms, const char** why) {
+bool mm_maps(CUtensorMap* tm, int dtype, const Matmul& a, int bn, int pair, int atoms, int a_rows, const char** why) {
     const int share = bn / pair;
-    return mm_operand(tm, dtype, a.A, a.lda, a.a_mn, a.M, a.K, 128, atoms, why) &&
+    return mm_operand(tm, dtype, a.A, a.lda, a.a_mn, a.M, a.K, a_rows, atoms, why) &&
            (a.gated ? mm_gated(tm + 1, dtype, a, share / 2, why) : mm_operand(tm + 1, dtype, a.B, a.ldb, a.b_mn, a.N, a.K, share, atoms, why)) &&
            mm_encode(tm + 2, dtype, a.C, a.ldc, a.M, a.N, 32, kStoreCols, 64, why);
 }
@@ -692,18 +730,19 @@ MatmulShape matmul_shape(const Matmul& a, int sms, int device) {
         int pair, bn, atoms;
         double step, round;
     } const kinds[] = {{2, 256, 1, 0.26, 6.0}, {2, 128, 2, 0.17, 5.3}, {1, 128, 2, 0.17, 4.9}, {1, 64, 2, 0.155, 4.5}};
-    constexpr double kSharing = 2.3;  // of a tile by a cluster
+    // nor are the operands sooner there than memory brings them: tiles that keep it busy gain nothing by sharing
+    const double bytes = ((double)a.M + (double)a.N * (a.gated ? 2.0 : 1.0)) * a.K * 2.0, brought = bytes / 6.8e6;
     MatmulShape best = {};
     best.us = 1e30;
     for (const auto& k : kinds) {
         const int64_t t = mm_tiles(a, k.bn, k.pair), units = sms / k.pair, rounds = (t + units - 1) / units;
         const int atoms = a.a_mn || a.b_mn ? 2 : k.atoms;
-        const double step = k.step * off_lines(a), time = rounds * steps * step + (rounds - 1) * 0.5 + k.round;
+        const double step = k.step * off_lines(a), time = std::max(rounds * steps * step, brought) + (rounds - 1) * 0.5 + k.round;
         if (time < best.us) best = {k.pair, k.bn, 1, atoms, time};
-        if (a.gated || k.pair == 2) continue;
-        for (int ks = 2; ks <= 8; ks *= 2) {
+        if (k.pair == 2) continue;
+        for (int ks = 2; ks <= 8; ++ks) {
             if (t * ks > sms || steps < 2 * ks || t > mm_clusters(ks, device)) continue;
-            const double split = (steps + ks - 1) / ks * step + k.round + kSharing;
+            const double split = std::max((steps + ks - 1) / ks * step, brought) + k.round + (a.gated ? 2.4 + 0.3 * ks : 2.0 + 0.15 * ks);
             if (split < best.us) best = {1, k.bn, ks, atoms, split};
         }
     }
@@ -714,7 +753,13 @@ kt_status launch_matmul_as(int dtype, const Matmul& a, const MatmulShape& s, int
     MmParams p = {};
     p.of[0] = mm_product(dtype, a, s.BN, s.pair);
     p.atoms = s.atoms;
-    p.stage_bytes = (uint32_t)s.atoms * (kMmABytes + p.of[0].b_bytes);
+    // Copies ask for no rows that A does not have, and few rows leave their room in the ring to the weights (4 x 1280 x
+    // 2 5120 11.0 to 13.6 -> 7.8 us, weights from memory).  The products read 128 rows all the same: what lies there, whatever
+    // it is, reaches rows of the accumulator that nobody reads.
+    const int a_rows = s.pair == 1 && !a.a_mn ? std::min(128, a.M) : 128;
+    p.a_bytes = (uint32_t)(a_rows + 7) / 8 * 1024u;
+    p.step_bytes = (uint32_t)s.pair * s.atoms * ((uint32_t)a_rows * 128u + p.of[0].b_bytes);
+    p.stage_bytes = (uint32_t)s.atoms * (p.a_bytes + p.of[0].b_bytes);
     p.stages = std::min(8, kMmRing / (int)p.stage_bytes);
     p.act = a.act;
     p.has_p = a.P != nullptr;
@@ -722,7 +767,7 @@ kt_status launch_matmul_as(int dtype, const Matmul& a, const MatmulShape& s, int
     p.wait_limit_ns = a.wait_limit_ns;
     p.stall_ns = a.stall_ns;
     CUtensorMap tm[6];
-    if (!mm_maps(tm, dtype, a, s.BN, s.pair, s.atoms, why)) return KT_ERR_CUDA;
+    if (!mm_maps(tm, dtype, a, s.BN, s.pair, s.atoms, a_rows, why)) return KT_ERR_CUDA;
     tm[3] = tm[4] = tm[5] = tm[2];
     if (a.P) {
         uint16_t* P = static_cast<uint16_t*>(a.P);
@@ -760,7 +805,7 @@ kt_status launch_gradients_as(int dtype, const Matmul* a, int count, const Gradi
         p.of[i].left = s.share ? n % units : 0;
         p.steps += p.of[i].left * p.of[i].kblocks;
         p.stage_bytes = std::max(p.stage_bytes, kAtoms * (kMmABytes + p.of[i].b_bytes));
-        if (!mm_maps(tm + 3 * i, dtype, a[i], s.bn[i], 2, kAtoms, why)) return KT_ERR_CUDA;
+        if (!mm_maps(tm + 3 * i, dtype, a[i], s.bn[i], 2, kAtoms, 128, why)) return KT_ERR_CUDA;
     }
     p.atoms = kAtoms;
     p.stages = std::min(8, kMmRing / (int)p.stage_bytes);
