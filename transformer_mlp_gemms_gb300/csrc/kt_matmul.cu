@@ -389,38 +389,41 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             const MmProduct& o = p.of[SHARED ? it.product : 0];
             const CUtensorMap* const mC = SHARED && it.product ? &tmX : &tmC;
             const uint32_t buf = local & 1;
-            ok = ok && wait_phase(bar_accf + 8u * buf, (local >> 1) & 1u, abort_flag, &g_matmul_error, DEV_TIMEOUT_EPILOGUE, limit);
-            ok = __all_sync(0xffffffffu, ok);
-            tc_fence_after();
             int m, n;
             origin(it, m, n);
             if (PAIR == 2) n -= (int)rank * (GATED ? o.BN / 4 : o.BN / 2);  // every column of the tile
-            const int y = m + 32 * q;
-            const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * (uint32_t)kAccSlot;
-            // 32 columns of the accumulator (NaN where there is none), with their bias
-            auto columns = [&](uint32_t from, const uint16_t* bias, int col, int limit_col, float* v) {
-                uint32_t r[32];
-                if (ok) {
-                    tmem_ld32(acc + from, r);
-                    tmem_wait_ld_only();
-                    reg_fence32(r);
-                } else {
+            // The bias of this warp's columns, asked for before its sums are there: eight values per lane, in the order of
+            // the groups of 32 (GATED: the values' groups, then the gates').
+            uint4 ahead = make_uint4(0u, 0u, 0u, 0u);
+            if (!SPLIT && !SHARED && p.bias && lane < 16) {
+                const int g = half + 2 * (GATED ? lane >> 2 & 1 : lane >> 2), col = n + 32 * g + 8 * (lane & 3);
+                if (32 * g < (GATED ? o.BN / 2 : o.BN) && col < o.N)
+                    ahead = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + (GATED && lane >= 8 ? o.N : 0) + col);
+            }
+            ok = ok && wait_phase(bar_accf + 8u * buf, (local >> 1) & 1u, abort_flag, &g_matmul_error, DEV_TIMEOUT_EPILOGUE, limit);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            // 32 sums (NaN where there are none), with their bias, the warp's `group`-th
+            auto finish = [&](const uint32_t* r, int group, float* v) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = 0x7fffffffu;
-                }
-                if (bias) {
-                    bias32<DT>(bias, col, limit_col, v);
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(ok ? r[i] : 0x7fffffffu);
+                if (p.bias) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(r[i]);
-                } else {
+                    for (int i = 0; i < 32; i += 8) {
+                        float b[8];
+                        const int from = 4 * group + i / 8;
+                        unpack8<DT>(make_uint4(__shfl_sync(0xffffffffu, ahead.x, from), __shfl_sync(0xffffffffu, ahead.y, from),
+                                               __shfl_sync(0xffffffffu, ahead.z, from), __shfl_sync(0xffffffffu, ahead.w, from)), b);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                        for (int e = 0; e < 8; ++e) v[i + e] += b[e];
+                    }
                 }
             };
+            const int y = m + 32 * q;
+            const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * (uint32_t)kAccSlot;
             auto store = [&](const CUtensorMap* tm, const uint32_t* w, int col) {
                 stage_and_store_packed(tm, stg + (stores++ & 1u) * 2048u, lane, w, col, y, true);
             };
-            const uint16_t* bias = static_cast<const uint16_t*>(p.bias);
             if constexpr (SPLIT) {
                 // the sums go where the operands were (every product has read them): 32 x 32 units of
                 // [4 columns][32 rows], 16 bytes each
@@ -438,18 +441,25 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 }
             } else if constexpr (GATED) {
                 const int share = o.BN / PAIR, hs = share / 2;  // accumulator: per share its value columns, then its gates
+#pragma unroll 1
                 for (int g = half; g < o.BN / 64; g += 2) {
                     const int c = 32 * g, col = n + c;
                     if (col >= o.N || y >= o.M) continue;
-                    const uint32_t from = (uint32_t)(c / hs * share + c % hs);
+                    const uint32_t from = acc + (uint32_t)(c / hs * share + c % hs);
+                    uint32_t rv[32], rg[32];
+                    tmem_ld32(from, rv);
+                    tmem_ld32(from + (uint32_t)hs, rg);
+                    tmem_wait_ld_only();
+                    reg_fence32(rv);
+                    reg_fence32(rg);
                     float v[32], gt[32];
                     uint32_t w[16];
-                    columns(from, bias, col, o.N, v);
+                    finish(rv, g >> 1, v);
                     if (p.has_p) {
                         pack32<DT>(v, w);
                         store(&tmV, w, col);
                     }
-                    columns(from + (uint32_t)hs, bias ? bias + o.N : nullptr, col, o.N, gt);
+                    finish(rg, 2 + (g >> 1), gt);
                     if (p.has_p) {
                         pack32<DT>(gt, w);
                         store(&tmG, w, col);
@@ -493,12 +503,16 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                     stores = sum_shared<DT>(mC, reinterpret_cast<const float4*>(p.partials + (int)rank * kSlot) + 32 * q + lane, first, unit0, ok, acc, half,
                                             min(o.BN, o.N - n), n, y, stg, stores);
             } else {
+#pragma unroll 1
                 for (int g = half; g < o.BN / 32; g += 2) {
                     const int col = n + 32 * g;
                     if (col >= o.N || y >= o.M) continue;
+                    uint32_t r[32], w[16];
+                    tmem_ld32(acc + 32u * g, r);
+                    tmem_wait_ld_only();
+                    reg_fence32(r);
                     float v[32];
-                    uint32_t w[16];
-                    columns(32u * g, bias, col, o.N, v);
+                    finish(r, g >> 1, v);
                     pack32<DT>(v, w);
                     store(mC, w, col);
                 }
