@@ -445,10 +445,13 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 for (int g = half; g < o.BN / 64; g += 2) {
                     const int c = 32 * g, col = n + c;
                     if (col >= o.N || y >= o.M) continue;
-                    const uint32_t from = acc + (uint32_t)(c / hs * share + c % hs);
                     uint32_t rv[32], rg[32];
-                    tmem_ld32(from, rv);
-                    tmem_ld32(from + (uint32_t)hs, rg);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 16) {  // (a share may have 48 columns of either)
+                        const uint32_t from = acc + (uint32_t)((c + i) / hs * share + (c + i) % hs);
+                        tmem_ld16(from, *reinterpret_cast<uint32_t(*)[16]>(rv + i));
+                        tmem_ld16(from + (uint32_t)hs, *reinterpret_cast<uint32_t(*)[16]>(rg + i));
+                    }
                     tmem_wait_ld_only();
                     reg_fence32(rv);
                     reg_fence32(rg);
@@ -743,7 +746,7 @@ MatmulShape matmul_shape(const Matmul& a, int sms, int device) {
     struct {
         int pair, bn, atoms;
         double step, round;
-    } const kinds[] = {{2, 256, 1, 0.26, 6.0}, {2, 128, 2, 0.17, 5.3}, {1, 128, 2, 0.17, 4.9}, {1, 64, 2, 0.155, 4.5}};
+    } const kinds[] = {{2, 256, 1, 0.26, 6.0}, {2, 192, 1, 0.198, 5.6}, {2, 128, 2, 0.17, 5.3}, {1, 128, 2, 0.17, 4.9}, {1, 64, 2, 0.155, 4.5}};
     // nor are the operands sooner there than memory brings them: tiles that keep it busy gain nothing by sharing
     const double bytes = ((double)a.M + (double)a.N * (a.gated ? 2.0 : 1.0)) * a.K * 2.0, brought = bytes / 6.8e6;
     MatmulShape best = {};
@@ -751,6 +754,7 @@ MatmulShape matmul_shape(const Matmul& a, int sms, int device) {
     for (const auto& k : kinds) {
         const int64_t t = mm_tiles(a, k.bn, k.pair), units = sms / k.pair, rounds = (t + units - 1) / units;
         const int atoms = a.a_mn || a.b_mn ? 2 : k.atoms;
+        if (k.bn == 192 && (a.a_mn || a.b_mn)) continue;  // (MN-major operands come in boxes of 64 columns per CTA)
         const double step = k.step * off_lines(a), time = std::max(rounds * steps * step, brought) + (rounds - 1) * 0.5 + k.round;
         if (time < best.us) best = {k.pair, k.bn, 1, atoms, time};
         if (k.pair == 2) continue;
