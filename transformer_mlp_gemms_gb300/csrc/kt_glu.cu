@@ -104,7 +104,6 @@ __global__ void __launch_bounds__(kGluThreads) kt_glu_backward_kernel(const GluB
     const int col = (int)blockIdx.x * kGluCols + 8 * lane;
     const bool mine = col < p.F;
     const int row0 = (int)blockIdx.y * per, row1 = min(row0 + per, p.M);
-    const int64_t out_ld = 2 * (int64_t)p.F;
     f32x2 sv[4], sg[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) sv[i] = sg[i] = f2(0.0f);
@@ -144,8 +143,8 @@ __global__ void __launch_bounds__(kGluThreads) kt_glu_backward_kernel(const GluB
                         sv[i] = f2_add<true>(sv[i], dv[i]);
                         sg[i] = f2_add<true>(sg[i], dg[i]);
                     }
-                    *reinterpret_cast<uint4*>(dP + row * out_ld) = pack_pairs<DT>(dv);
-                    *reinterpret_cast<uint4*>(dP + row * out_ld + p.F) = pack_pairs<DT>(dg);
+                    *reinterpret_cast<uint4*>(dP + row * p.lddp) = pack_pairs<DT>(dv);
+                    *reinterpret_cast<uint4*>(dP + row * p.lddp + p.F) = pack_pairs<DT>(dg);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) sv[i] = f2_add<true>(sv[i], dh[i]);

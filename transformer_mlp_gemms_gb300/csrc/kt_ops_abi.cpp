@@ -127,6 +127,9 @@ kt_status zeros(void* p, size_t bytes, void* stream) {
     const cudaError_t e = cudaMemsetAsync(p, 0, bytes, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? KT_OK : cuda_failed("cudaMemsetAsync", e);
 }
+// The pitch of dP in the workspace: whole 128-byte lines, as a product's copies of 64 columns take longer
+// where rows start between lines (the gradients of 729 x 1152 x 2 4304 41.8 -> 41.1 us).
+int64_t dp_pitch(int64_t F) { return (2 * F + 63) / 64 * 64; }
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 const size_t kScratch = kt::kGradientsFlags + kt::gradients_partials();  // of launch_gradients
 int epilogue_of(int act) { return kt::up_epilogue(act); }
@@ -417,7 +420,7 @@ kt_status kt_glu_forward(int64_t M, int64_t D, int64_t F, kt_dtype dtype, kt_act
 
 size_t kt_glu_backward_workspace(int64_t M, int64_t D, int64_t F) {
     if (M < 0 || M > INT32_MAX / 2 || D < 8 || D % 8 || D > (1 << 24) || F < 8 || F % 8 || F > (1 << 24)) return 0;
-    return up256((size_t)(M ? M : 1) * 4 * (size_t)F) + up256((size_t)kt::column_sum_rows(M, F) * 2 * (size_t)F * sizeof(float)) + kScratch;
+    return up256((size_t)(M ? M : 1) * 2 * (size_t)dp_pitch(F)) + up256((size_t)kt::column_sum_rows(M, F) * 2 * (size_t)F * sizeof(float)) + kScratch;
 }
 
 kt_status kt_glu_backward(int64_t M, int64_t D, int64_t F, kt_dtype dtype, kt_act act, const void* dH, int64_t lddh,
@@ -440,7 +443,7 @@ kt_status kt_glu_backward(int64_t M, int64_t D, int64_t F, kt_dtype dtype, kt_ac
         if ((s = zeros(dW, (size_t)4 * F * D, stream)) != KT_OK || (s = zeros(db, (size_t)8 * F, stream)) != KT_OK) return s;
         return done(KT_OK, "");
     }
-    char* const sums = static_cast<char*>(workspace) + up256((size_t)M * 4 * (size_t)F);
+    char* const sums = static_cast<char*>(workspace) + up256((size_t)M * 2 * (size_t)dp_pitch(F));
     char* const scratch = sums + up256((size_t)kt::column_sum_rows(M, F) * 2 * (size_t)F * sizeof(float));
     const char* why = "";
     kt::GluBackward g = {};
@@ -449,6 +452,7 @@ kt_status kt_glu_backward(int64_t M, int64_t D, int64_t F, kt_dtype dtype, kt_ac
     g.P = P;
     g.ldp = ldp;
     g.dP = workspace;
+    g.lddp = dp_pitch(F);
     g.partials = db ? reinterpret_cast<float*>(sums) : nullptr;
     g.db = db;
     g.zero = reinterpret_cast<int*>(scratch);
@@ -456,7 +460,7 @@ kt_status kt_glu_backward(int64_t M, int64_t D, int64_t F, kt_dtype dtype, kt_ac
     g.F = (int)F;
     g.act = epilogue_of(act);
     if ((s = kt::launch_glu_backward(dtype, g, stream, &why)) != KT_OK) return kt::report(s, why);
-    return gradients(M, 2 * F, D, dtype, workspace, 2 * F, X, ldx, W, dX, lddx, dW, scratch, true, sms, dev, stream);
+    return gradients(M, 2 * F, D, dtype, workspace, g.lddp, X, ldx, W, dX, lddx, dW, scratch, true, sms, dev, stream);
 }
 
 kt_status kt_linear_forward(int64_t M, int64_t N, int64_t K, kt_dtype dtype, const void* X, int64_t ldx, const void* W,

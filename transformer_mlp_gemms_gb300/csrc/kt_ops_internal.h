@@ -128,11 +128,11 @@ kt_status matmul_status(void* stream, int* word, const char** why);
 // The elementwise part of the backward pass of a gated block, and column sums (kt_glu.cu).
 struct GluBackward {
     const void *dH, *P;  // dH: [M][F]; P: [M][2F]; null P: column sums of dH alone
-    void* dP;            // [M][2F] contiguous
+    void* dP;            // [M][2F], pitch lddp
     float* partials;     // [column_sum_rows][2F] (F without P), or null: no sums
     float* db;           // [2F] (F)
     int* zero;           // kGradientsFlags bytes to be zeroed, or null
-    int64_t lddh, ldp;
+    int64_t lddh, ldp, lddp;
     int M, F, act;       // act: an Epi
 };
 int column_sum_rows(int64_t M, int64_t F);
