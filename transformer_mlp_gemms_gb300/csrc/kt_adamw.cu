@@ -8,8 +8,9 @@
 // in the place of v, whose square would have twice the range; a root above zero is held as 2^-9 of its scale
 // at least, since the step divides by it.
 //
-// Bound by memory: 28 bytes per value with fp32 parameters, bf16 gradients and copies and fp32 moments, 10
-// with 16-bit parameters and 8-bit moments; about 50 instructions a value.  A warp takes 256 values at a time
+// Bound by memory with fp32 moments: 28 bytes per value with fp32 parameters, bf16 gradients and copies.  With 16-bit
+// parameters and 8-bit moments there are 10 bytes and 59 instructions a value, and the instructions bind: 157 million
+// values in 310 to 336 us, 4.7 to 5.1 TB/s, the schedulers busy 75 % of the time.  A warp takes 256 values at a time
 // (a scale's block), eight consecutive ones per lane, and holds them in registers throughout: their
 // largest magnitude is one warp reduction.  The tensors' addresses come as the launch's parameters, so no
 // table is kept on the device, and a captured call carries its own.  A block takes every
