@@ -273,9 +273,11 @@ size_t kt_linear_backward_workspace(int64_t M, int64_t N, int64_t K);
  *   step >= 1; or step_device, an int64 on the device that is read when the kernel runs (a captured call then counts
  *   on); lr and the others are the call's.
  * Any n >= 0 and any alignment to the elements; tensors whose addresses are 16-byte aligned (8-bit
- * moments: 8) take wide loads.  Tensors must not overlap one another.
+ * moments: 8) take wide loads.  Tensors must not overlap one another; a parameter or moment that is listed
+ * twice is refused.
  * Errors: INVALID (NULL or misaligned pointer, negative n, unknown dtype or bits, a copy without fp32 parameters,
- * beta outside [0, 1), eps or lr negative or not finite, weight_decay not finite, step below 1), UNSUPPORTED
+ * beta outside [0, 1), eps or lr negative or not finite, weight_decay not finite, step below 1, a tensor listed
+ * twice), UNSUPPORTED
  * (device not sm_103), CUDA.
  */
 #define KT_F32 2

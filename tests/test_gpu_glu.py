@@ -360,3 +360,52 @@ def test_rows_and_columns_that_end_inside_a_tile(M, N):
     yx, ty = ref.product(x.double(), w.double(), b)
     near(y, yx, ref.rounded(yx, ty, dt))
     assert ys[:, N:].isnan().all()
+
+
+@pytest.mark.parametrize("M", [3, 128])
+def test_a_wait_that_runs_out_in_a_shared_gated_tile_shows(M):
+    """Few tiles with long sums: one CTA of a cluster gives up, and its tile shows it."""
+    g = torch.Generator().manual_seed(M)
+    D, F, dt = 4096, 200, torch.bfloat16
+    x, w, b = randn(g, M, D, dtype=dt), randn(g, 2 * F, D, dtype=dt, std=0.02), randn(g, 2 * F, dtype=dt)
+    want, got = torch.empty(M, F, dtype=dt, device="cuda"), torch.full((M, F), 7.0, dtype=dt, device="cuda")
+    p, q = torch.empty(M, 2 * F, dtype=dt, device="cuda"), torch.full((M, 2 * F), 7.0, dtype=dt, device="cuda")
+    kt_ops.kt_glu_forward(x, w, b, want, p, kt_mlp.KT_ACT_SILU)
+    kt_ops.kt_matmul_debug_stall(True, 20000)
+    try:
+        kt_ops.kt_glu_forward(x, w, b, got, q, kt_mlp.KT_ACT_SILU)
+        assert kt_ops.kt_matmul_status() == kt_mlp.KT_ERR_TIMEOUT
+    finally:
+        kt_ops.kt_matmul_debug_stall(False)
+    for a, c in ((got, want), (q, p)):
+        assert a[0, 0].isnan() and (a.isnan() | (a == c)).all()
+    kt_ops.kt_glu_forward(x, w, b, got, q, kt_mlp.KT_ACT_SILU)
+    assert kt_ops.kt_matmul_status() == kt_mlp.KT_OK and torch.equal(got, want) and torch.equal(q, p)
+
+
+def test_a_workspace_of_two_graphs_replayed_in_turn():
+    """Both graphs' gradients are those of the inputs at each replay, whichever ran before."""
+    g = torch.Generator().manual_seed(9)
+    dt = torch.float16
+    sizes = [(300, 264, 520), (4096, 72, 136)]
+    ws = max((kt_ops.glu_backward_workspace(*s) for s in sizes), key=lambda t: t.numel())
+    calls = []
+    for M, D, F in sizes:
+        x, w = randn(g, M, D, dtype=dt), randn(g, 2 * F, D, dtype=dt, std=D ** -0.5)
+        p, dh = randn(g, M, 2 * F, dtype=dt), randn(g, M, F, dtype=dt, std=0.5)
+        out = torch.empty(M, D, dtype=dt, device="cuda"), torch.empty(2 * F, D, dtype=dt, device="cuda"), torch.empty(2 * F, device="cuda")
+        run = lambda x=x, w=w, p=p, dh=dh, out=out: kt_ops.kt_glu_backward(dh, p, x, w, *out, kt_mlp.KT_ACT_GELU_TANH, ws)
+        run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        calls.append((graph, out, [t.clone() for t in out]))
+    for i in (0, 1, 1, 0, 1, 0):
+        graph, out, want = calls[i]
+        for t in out:
+            t.fill_(float("nan"))
+        graph.replay()
+        for t, u in zip(out, want):
+            assert torch.equal(t, u)
+    assert kt_ops.kt_matmul_status() == kt_mlp.KT_OK

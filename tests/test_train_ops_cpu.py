@@ -82,7 +82,7 @@ def test_workspace_sizes(lib):
 
 
 def adamw(lib, tensor, options, count=1):
-    t = kt_ops.kt_adamw_tensor(**{**dict(param=P, grad=P, m=P, v=P, m_scale=None, v_scale=None, copy=None, n=100, weight_decay=0.0), **tensor})
+    t = kt_ops.kt_adamw_tensor(**{**dict(param=P, grad=P, m=P + 4096, v=P + 8192, m_scale=None, v_scale=None, copy=None, n=100, weight_decay=0.0), **tensor})
     o = kt_ops.kt_adamw_options(**{**dict(param_dtype=2, grad_dtype=1, copy_dtype=1, state_bits=32, lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8,
                                           step=1, step_device=None, grad_scale=None), **options})
     return lib.kt_adamw(count, ctypes.byref(t), ctypes.byref(o), None)
@@ -94,10 +94,23 @@ def adamw(lib, tensor, options, count=1):
     (dict(weight_decay=float("nan")), {}), (dict(copy=P), dict(param_dtype=1)), (dict(copy=P), dict(copy_dtype=2)), ({}, dict(param_dtype=3)),
     ({}, dict(grad_dtype=-1)), ({}, dict(state_bits=16)), ({}, dict(state_bits=8)), ({}, dict(lr=-1.0)), ({}, dict(lr=float("nan"))),
     ({}, dict(eps=float("inf"))), ({}, dict(beta1=1.0)), ({}, dict(beta2=-0.1)), ({}, dict(beta2=float("nan"))), ({}, dict(step=0)),
-    ({}, dict(step_device=P + 4)), ({}, dict(grad_scale=P + 2)),
+    ({}, dict(step_device=P + 4)), ({}, dict(grad_scale=P + 2)), (dict(m=P), {}), (dict(v=P + 4096), {}),
 ])
 def test_adamw_refusals(lib, tensor, options):
     assert adamw(lib, tensor, options) == INVALID and kt_mlp.kt_last_error()
+
+
+@pytest.mark.parametrize("count", [2, 64, 65, 400])
+def test_adamw_refuses_tied_parameters(lib, count):
+    o = kt_ops.kt_adamw_options(param_dtype=2, grad_dtype=2, state_bits=32, lr=1e-3, beta1=0.9, beta2=0.99, eps=0.0, step=1)
+    tensors = (kt_ops.kt_adamw_tensor * count)()
+    for i, t in enumerate(tensors):
+        t.n = 4
+        t.param, t.grad, t.m, t.v = (P + 1024 * (4 * i + j) for j in range(4))
+    tensors[count - 1].param = tensors[0].param
+    assert lib.kt_adamw(count, tensors, ctypes.byref(o), None) == INVALID and "twice" in kt_mlp.kt_last_error()
+    tensors[0].n = 0  # an empty tensor is not updated
+    assert lib.kt_adamw(count, tensors, ctypes.byref(o), None) != INVALID
 
 
 def test_adamw_without_tensors(lib):

@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <functional>
 #include <new>
 #include <vector>
 
@@ -538,15 +539,20 @@ kt_status kt_adamw(int64_t count, const kt_adamw_tensor* tensors, const kt_adamw
     if (!aligned(o->step_device, 8) || !aligned(o->grad_scale, 4)) return bad("a pointer is not aligned to its elements");
     const size_t pb = o->param_dtype == KT_F32 ? 4 : 2, gb = o->grad_dtype == KT_F32 ? 4 : 2, sb = o->state_bits == 8 ? 1 : 4;
     kt::AdamwEntry few[64];
+    const void* few_written[3 * 64];  // the addresses that the call writes to
     std::vector<kt::AdamwEntry> many;
+    std::vector<const void*> many_written;
     kt::AdamwEntry* e = few;
+    const void** written = few_written;
     if (count > 64) {
         try {
             many.resize((size_t)count);
+            many_written.resize(3 * (size_t)count);
         } catch (...) {
             return kt::report(KT_ERR_NOMEM, "host allocation failed");
         }
         e = many.data();
+        written = many_written.data();
     }
     int live = 0;
     for (int64_t i = 0; i < count; ++i) {
@@ -560,6 +566,9 @@ kt_status kt_adamw(int64_t count, const kt_adamw_tensor* tensors, const kt_adamw
         if (!aligned(t.param, pb) || !aligned(t.grad, gb) || !aligned(t.m, sb) || !aligned(t.v, sb) || !aligned(t.m_scale, 4) ||
             !aligned(t.v_scale, 4) || !aligned(t.copy, 2))
             return bad("a pointer is not aligned to its elements");
+        written[3 * live] = t.param;
+        written[3 * live + 1] = t.m;
+        written[3 * live + 2] = t.v;
         kt::AdamwEntry& x = e[live++];
         x.p = t.param;
         x.g = t.grad;
@@ -575,6 +584,9 @@ kt_status kt_adamw(int64_t count, const kt_adamw_tensor* tensors, const kt_adamw
         x.wide = aligned(t.param, 16) && aligned(t.grad, 16) && aligned(t.m, state) && aligned(t.v, state) && aligned(t.copy, 16);
     }
     if (!live) return done(KT_OK, "");
+    // (tied weights, say: two blocks would update the same values)
+    std::sort(written, written + 3 * live, std::less<const void*>());
+    if (std::adjacent_find(written, written + 3 * live) != written + 3 * live) return bad("a parameter or moment is listed twice");
     kt_status s;
     int dev, sms;
     if ((s = current_device(&dev, &sms)) != KT_OK) return s;
