@@ -14,7 +14,7 @@
 // Few tokens (SWAP): the weights are the first operand, 128 channels a tile, and the tokens the second,
 // 16 or 32 columns, so that no tensor-core row is idle; a thread has one channel.  Bound by the weights' bytes.
 // Bound, with many tokens, by the epilogue warps' sums: 8192 x 8192 x 8192 in 369 to 380 us, 2.9 PFLOP/s, the tensor
-// pipe busy 63 % of the time.  4 x 10240 x 1280: 5.9 us, 2.2 TB/s, a launch and one round of loads.
+// pipe busy 63 % of the time.  4 x 10240 x 1280: 5.4 us, 2.4 TB/s, a launch and one round of loads.
 // Few tiles with long rows: a cluster per tile, each CTA with its share of the runs; the sums meet in the
 // cluster's shared memory, added in the order of the ranks.
 #include <cuda_fp8.h>
@@ -159,10 +159,13 @@ template <int PAIR, int BN, bool SWAP>
 struct F8 {
     static constexpr int kEpi = SWAP ? 4 : 8;               // epilogue warps
     static constexpr int kCols = SWAP ? BN : BN / 2;        // sums per thread
-    static constexpr int kBufs = BN > 128 ? 2 : BN > 64 ? 4 : 8;  // accumulators
+    static constexpr int kBufs = BN > 128 ? 2 : BN > 64 ? 4 : 8;  // accumulators (of kRuns runs each)
     static constexpr int kThreads = (kEpi + 4) * 32;        // warps 0-2: copies of A, products, copies of B; 3: none; then the epilogue
     static constexpr uint32_t kBBytes = (uint32_t)(BN / PAIR) * kRun;
-    static constexpr uint32_t kStage = kF8ABytes + kBBytes;
+    // Runs of a step (a stage of the ring, a wait and a signal of each role): two of them where a run is little work
+    // (16 x 4096 x 16384 13.0 -> 11.3 us, 4 x 10240 x 1280 6.2 -> 5.7).
+    static constexpr int kRuns = SWAP ? 2 : 1;
+    static constexpr uint32_t kStage = kRuns * (kF8ABytes + kBBytes);
     static constexpr int kChunk = 8;                        // runs of scales in shared memory at a time
     static constexpr uint32_t kScales = SWAP ? 0u : 2u * kChunk * (128u + 2u) * 4u;  // [2][kChunk][128], then [2][2][kChunk]
     static constexpr uint32_t kStaging = SWAP ? 0u : (uint32_t)kEpi * 2048u;
@@ -175,7 +178,7 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
     kt_linear_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ CUtensorMap tmY, const __grid_constant__ F8Params p) {
     using C = F8<PAIR, BN, SWAP>;
-    constexpr int kEpi = C::kEpi, kCols = C::kCols, kBufs = C::kBufs, kStages = C::kStages;
+    constexpr int kEpi = C::kEpi, kCols = C::kCols, kBufs = C::kBufs, kStages = C::kStages, kRuns = C::kRuns;
     extern __shared__ uint8_t raw[];
     uint8_t* const at = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     const uint32_t base = smem_u32(at);
@@ -250,12 +253,15 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
             int m, n;
             origin(t, m, n);
             const int row = a_role ? (SWAP ? n : m + (int)rank * 128) : (SWAP ? m : n + (int)rank * (BN / PAIR));
-            for (int j = 0; j < runs; ++j) {
+            for (int j = 0; j < runs; j += kRuns) {
                 ok = __all_sync(0xffffffffu, wait_turn(bar_empty + 8u * stage, phase ^ 1u, abort_flag, &g_fp8_error, DEV_TIMEOUT_PRODUCER, limit));
                 if (!ok) break;
                 if (a_role) expect_tx_if(bar_full + 8u * stage, PAIR * C::kStage, arm);
-                // the maps count pairs of bytes
-                load_if<PAIR>(base + stage * C::kStage + (a_role ? 0u : kF8ABytes), map, full0 + 8u * stage, (run0 + j) * (kRun / 2), row, one);
+                // the maps count pairs of bytes (a step may reach past the runs, and past K, where zeros are filled in)
+#pragma unroll
+                for (int i = 0; i < kRuns; ++i)
+                    load_if<PAIR>(base + stage * C::kStage + (a_role ? (uint32_t)i * kF8ABytes : kRuns * kF8ABytes + (uint32_t)i * C::kBBytes), map,
+                                  full0 + 8u * stage, (run0 + j + i) * (kRun / 2), row, one);
                 used |= 1u << stage;
                 used_phase = (used_phase & ~(1u << stage)) | (phase << stage);
                 if (++stage == (uint32_t)kStages) {
@@ -278,7 +284,7 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
         if (leader) {
             const uint32_t one = lane == 0;
             uint32_t stage = 0, phase = 0, buf = 0, use = 0;
-            const uint64_t ad0 = smem_desc(base, 16u, 1024u), bd0 = smem_desc(base + kF8ABytes, 16u, 1024u);
+            const uint64_t ad0 = smem_desc(base, 16u, 1024u), bd0 = smem_desc(base + kRuns * kF8ABytes, 16u, 1024u);
             bool ok = true, any = false;
             // Narrow tiles are bound by this warp's instructions: both barriers of the next step are asked for before this
             // one's products, and the answers are there after them (1024 x 1024 x 8192 17.0 -> 16.3 us; wide tiles
@@ -286,13 +292,13 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
             constexpr bool kAhead = BN <= 128;
             uint32_t full = 0u, free = 0u;
             for (int t = unit0; t < tiles && ok; t += units)
-                for (int j = 0; j < runs; ++j) {
+                for (int j = 0; j < runs; j += kRuns) {
                     ok = __all_sync(0xffffffffu,
                                     (full || wait_turn(bar_full + 8u * stage, phase, abort_flag, &g_fp8_error, DEV_TIMEOUT_MMA, limit)) &&
                                         (free || wait_turn(bar_acce + 8u * buf, (use & 1u) ^ 1u, abort_flag, &g_fp8_error, DEV_TIMEOUT_MMA, limit)));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t d = tmem + buf * (uint32_t)BN, now = stage, which = buf;
+                    const uint32_t d = tmem + buf * (uint32_t)(kRuns * BN), now = stage, which = buf;
                     const uint64_t ad = ad0 + stage * (C::kStage >> 4), bd = bd0 + stage * (C::kStage >> 4);
                     if (++stage == (uint32_t)kStages) {
                         stage = 0;
@@ -307,7 +313,12 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
                         free = mbar_test_wait(bar_acce + 8u * buf, (use & 1u) ^ 1u);
                     }
 #pragma unroll
-                    for (uint32_t k = 0; k < 4; ++k) mma_if<PAIR, true>(d, ad + 2 * k, bd + 2 * k, p.idesc, k > 0, one);  // 32 columns each
+                    for (uint32_t i = 0; i < (uint32_t)kRuns; ++i) {
+                        if (i > 0 && j + (int)i >= runs) break;
+#pragma unroll
+                        for (uint32_t k = 0; k < 4; ++k)  // 32 columns each
+                            mma_if<PAIR, true>(d + i * (uint32_t)BN, ad + i * (kF8ABytes >> 4) + 2 * k, bd + i * (C::kBBytes >> 4) + 2 * k, p.idesc, k > 0, one);
+                    }
                     any = true;
                     commit_if<PAIR>(bar_accf + 8u * which, one);
                     commit_if<PAIR>(bar_empty + 8u * now, one);
@@ -355,26 +366,23 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kCols; ++i) sum[i] = 0.0f;
             const float* sw = p.sw + (int64_t)(n / 128) * p.runs + run0;  // (SWAP: one block of channels)
-            float w_next = 0.0f;
-            if constexpr (SWAP) w_next = sw[0];
-            constexpr int kPer = SWAP ? (BN + 31) / 32 : 1;  // SWAP: token lane
-            float x_next[kPer];
+            float w_next[kRuns], x_next[kRuns];  // SWAP: lane l has token l's
             auto tokens = [&](int j) {
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) x_next[i] = lane + 32 * i < p.M ? p.sx[(int64_t)(lane + 32 * i) * p.runs + run0 + j] : 0.0f;
+                for (int i = 0; i < kRuns; ++i) {
+                    const bool there = j + i < runs;
+                    w_next[i] = there ? sw[j + i] : 0.0f;
+                    x_next[i] = there && lane < p.M ? p.sx[(int64_t)lane * p.runs + run0 + j + i] : 0.0f;
+                }
             };
             if constexpr (SWAP) tokens(0);
 #pragma unroll 1
-            for (int j = 0; j < runs; ++j) {
-                float x[kPer];
+            for (int j = 0; j < runs; j += kRuns) {
+                float x[kRuns];
                 if constexpr (SWAP) {
-                    const float w = w_next;
 #pragma unroll
-                    for (int i = 0; i < kPer; ++i) x[i] = x_next[i] * w;
-                    if (j + 1 < runs) {
-                        tokens(j + 1);
-                        w_next = sw[j + 1];
-                    }
+                    for (int i = 0; i < kRuns; ++i) x[i] = x_next[i] * w_next[i];
+                    if (j + kRuns < runs) tokens(j + kRuns);
                 } else {
                     const int in = j % C::kChunk;
                     if (in == 0) {
@@ -389,21 +397,23 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
                 ok = ok && wait_turn(bar_accf + 8u * buf, use & 1u, abort_flag, &g_fp8_error, DEV_TIMEOUT_EPILOGUE, limit);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
-                const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * (uint32_t)BN + (uint32_t)c0;
+                const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * (uint32_t)(kRuns * BN) + (uint32_t)c0;
                 // 8 columns at a time (16 where there are few sums), the next on their way: a wide tile's 128 sums leave
                 // no registers for more.  (After a wait that ran out the sums are of no use, and are NaN below.)
                 constexpr int kLd = kCols > 64 ? 8 : 16;
                 uint32_t r[2][kLd];
                 tmem_ld_cols(acc, r[0]);
 #pragma unroll
-                for (int c = 0; c < kCols; c += kLd) {
-                    uint32_t(&now)[kLd] = r[c / kLd & 1];
+                for (int a = 0; a < kRuns * kCols; a += kLd) {
+                    uint32_t(&now)[kLd] = r[a / kLd & 1];
+                    const int c = a % kCols;
                     tmem_wait_cols(now);
-                    if (c + kLd < kCols) tmem_ld_cols(acc + (uint32_t)(c + kLd), r[c / kLd + 1 & 1]);
+                    if (a >= kCols && j + a / kCols >= runs) break;  // (nothing was added up there)
+                    if (a + kLd < kRuns * kCols) tmem_ld_cols(acc + (uint32_t)(a + kLd), r[a / kLd + 1 & 1]);
 #pragma unroll
                     for (int i = 0; i < kLd; i += 2) {
                         f32x2 s;
-                        if constexpr (SWAP) s = f2(__shfl_sync(0xffffffffu, x[c / 32], c % 32 + i), __shfl_sync(0xffffffffu, x[c / 32], c % 32 + i + 1));
+                        if constexpr (SWAP) s = f2(__shfl_sync(0xffffffffu, x[a / kCols], c + i), __shfl_sync(0xffffffffu, x[a / kCols], c + i + 1));
                         else s = f2(x[0]);
                         const f32x2 v = f2_fma<true>(f2(__uint_as_float(now[i]), __uint_as_float(now[i + 1])), s, f2(sum[c + i], sum[c + i + 1]));
                         sum[c + i] = v.x;
@@ -665,7 +675,7 @@ Fp8Shape linear_fp8_shape(const LinearFp8& a, int sms, int device) {
             best = {pair, bn, swap, 1};
         }
         if (pair == 2) return;
-        for (int ks = 2; ks <= 8; ks *= 2) {
+        for (int ks = 2; ks <= 8; ++ks) {
             if (tiles * ks > sms || runs < 2 * ks || tiles > f8_clusters(ks, device)) continue;
             const double split = (runs + ks - 1) / ks * step + round + sharing;
             if (split < least) {
@@ -676,8 +686,8 @@ Fp8Shape linear_fp8_shape(const LinearFp8& a, int sms, int device) {
     };
     if (a.M <= KT_LINEAR_FP8_FEW) {
         const int64_t tiles = (a.N + 127) / 128;
-        if (a.M <= 16) consider(1, 16, 1, tiles, 0.235, 3.4, 1.2);
-        else consider(1, 32, 1, tiles, 0.245, 3.9, 1.2);
+        if (a.M <= 16) consider(1, 16, 1, tiles, 0.186, 3.5, 1.4);
+        else consider(1, 32, 1, tiles, 0.195, 4.0, 1.4);
         return best;
     }
     auto tiles = [&](int rows, int bn) { return (int64_t)((a.M + rows - 1) / rows) * ((a.N + bn - 1) / bn); };
