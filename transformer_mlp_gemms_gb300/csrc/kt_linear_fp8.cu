@@ -159,12 +159,13 @@ template <int PAIR, int BN, bool SWAP>
 struct F8 {
     static constexpr int kEpi = SWAP ? 4 : 8;               // epilogue warps
     static constexpr int kCols = SWAP ? BN : BN / 2;        // sums per thread
-    static constexpr int kBufs = BN > 128 ? 2 : BN > 64 ? 4 : 8;  // accumulators (of kRuns runs each)
+    static constexpr int kBufs = BN > 64 ? 2 : 8;           // accumulators (of kRuns runs each)
     static constexpr int kThreads = (kEpi + 4) * 32;        // warps 0-2: copies of A, products, copies of B; 3: none; then the epilogue
     static constexpr uint32_t kBBytes = (uint32_t)(BN / PAIR) * kRun;
-    // Runs of a step (a stage of the ring, a wait and a signal of each role): two of them where a run is little work
-    // (16 x 4096 x 16384 13.0 -> 11.3 us, 4 x 10240 x 1280 6.2 -> 5.7).
-    static constexpr int kRuns = SWAP ? 2 : 1;
+    // Runs of a step (a stage of the ring, a wait and a signal of each role).  A step costs the issuing warp about 500 cycles
+    // whatever it holds; a wide tile's run keeps the tensor cores busy that long, narrower ones go by twos
+    // (16 x 4096 x 16384 13.0 -> 11.3 us, 1024 x 1024 x 8192 15.9 -> 14.9, or unshared 21.4 -> 19.0).
+    static constexpr int kRuns = BN > 128 ? 1 : 2;
     static constexpr uint32_t kStage = kRuns * (kF8ABytes + kBBytes);
     static constexpr int kChunk = 8;                        // runs of scales in shared memory at a time
     static constexpr uint32_t kScales = SWAP ? 0u : 2u * kChunk * (128u + 2u) * 4u;  // [2][kChunk][128], then [2][2][kChunk]
@@ -392,7 +393,10 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
                         if (j / C::kChunk + 1 < chunks) fetch(t, j / C::kChunk + 1, slot ^ 1u);
                         else if (t + units < tiles) fetch(t + units, 0, slot ^ 1u);
                     }
-                    x[0] = scales[2 * C::kChunk * 128 + (slot * 2 + c0 / 128) * C::kChunk + in] * scales[(slot * C::kChunk + in) * 128 + 32 * q + lane];
+#pragma unroll
+                    for (int i = 0; i < kRuns; ++i)  // (chunks are whole steps; past the runs there are zeros)
+                        x[i] = scales[2 * C::kChunk * 128 + (slot * 2 + c0 / 128) * C::kChunk + in + i] *
+                               scales[(slot * C::kChunk + in + i) * 128 + 32 * q + lane];
                 }
                 ok = ok && wait_turn(bar_accf + 8u * buf, use & 1u, abort_flag, &g_fp8_error, DEV_TIMEOUT_EPILOGUE, limit);
                 ok = __all_sync(0xffffffffu, ok);
@@ -409,12 +413,12 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
                     const int c = a % kCols;
                     tmem_wait_cols(now);
                     if (a >= kCols && j + a / kCols >= runs) break;  // (nothing was added up there)
-                    if (a + kLd < kRuns * kCols) tmem_ld_cols(acc + (uint32_t)(a + kLd), r[a / kLd + 1 & 1]);
+                    if (a + kLd < kRuns * kCols) tmem_ld_cols(acc + (uint32_t)((a + kLd) / kCols * BN + (a + kLd) % kCols), r[a / kLd + 1 & 1]);
 #pragma unroll
                     for (int i = 0; i < kLd; i += 2) {
                         f32x2 s;
                         if constexpr (SWAP) s = f2(__shfl_sync(0xffffffffu, x[a / kCols], c + i), __shfl_sync(0xffffffffu, x[a / kCols], c + i + 1));
-                        else s = f2(x[0]);
+                        else s = f2(x[a / kCols]);
                         const f32x2 v = f2_fma<true>(f2(__uint_as_float(now[i]), __uint_as_float(now[i + 1])), s, f2(sum[c + i], sum[c + i + 1]));
                         sum[c + i] = v.x;
                         sum[c + i + 1] = v.y;
@@ -691,9 +695,12 @@ Fp8Shape linear_fp8_shape(const LinearFp8& a, int sms, int device) {
         return best;
     }
     auto tiles = [&](int rows, int bn) { return (int64_t)((a.M + rows - 1) / rows) * ((a.N + bn - 1) / bn); };
+    // (rows that start between 128-byte lines cost the narrow tiles, which read more per product: 769 x 2200 x 2576 takes
+    // 13.9 us with 256 channels, 11.3 with pairs' 128 and 12.5 with a single CTA's, 1024 x 1024 x 8192 29.0, 19.1 and 19.0)
+    const bool off = (a.ldq | a.ldw) % 128 != 0;
     consider(2, 256, 0, tiles(256, 256), 0.37, 5.9, 0.0);
-    consider(2, 128, 0, tiles(256, 128), 0.27, 5.0, 0.0);
-    consider(1, 128, 0, tiles(128, 128), 0.25, 4.8, 3.0);
+    consider(2, 128, 0, tiles(256, 128), off ? 0.3 : 0.22, 5.0, 0.0);
+    consider(1, 128, 0, tiles(128, 128), off ? 0.36 : 0.22, 4.8, 3.3);
     return best;
 }
 
