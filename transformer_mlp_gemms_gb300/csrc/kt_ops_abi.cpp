@@ -7,7 +7,6 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
-#include <functional>
 #include <new>
 #include <vector>
 
@@ -539,7 +538,9 @@ kt_status kt_adamw(int64_t count, const kt_adamw_tensor* tensors, const kt_adamw
     if (!aligned(o->step_device, 8) || !aligned(o->grad_scale, 4)) return bad("a pointer is not aligned to its elements");
     const size_t pb = o->param_dtype == KT_F32 ? 4 : 2, gb = o->grad_dtype == KT_F32 ? 4 : 2, sb = o->state_bits == 8 ? 1 : 4;
     kt::AdamwEntry few[64];
-    const void* few_written[3 * 64];  // the addresses that the call writes to
+    // the addresses that the call writes to, each in the first free place from its own on
+    const void* few_written[512] = {};
+    size_t places = 512;
     std::vector<kt::AdamwEntry> many;
     std::vector<const void*> many_written;
     kt::AdamwEntry* e = few;
@@ -547,7 +548,8 @@ kt_status kt_adamw(int64_t count, const kt_adamw_tensor* tensors, const kt_adamw
     if (count > 64) {
         try {
             many.resize((size_t)count);
-            many_written.resize(3 * (size_t)count);
+            while (places < 6 * (size_t)count) places *= 2;
+            many_written.resize(places);
         } catch (...) {
             return kt::report(KT_ERR_NOMEM, "host allocation failed");
         }
@@ -566,9 +568,12 @@ kt_status kt_adamw(int64_t count, const kt_adamw_tensor* tensors, const kt_adamw
         if (!aligned(t.param, pb) || !aligned(t.grad, gb) || !aligned(t.m, sb) || !aligned(t.v, sb) || !aligned(t.m_scale, 4) ||
             !aligned(t.v_scale, 4) || !aligned(t.copy, 2))
             return bad("a pointer is not aligned to its elements");
-        written[3 * live] = t.param;
-        written[3 * live + 1] = t.m;
-        written[3 * live + 2] = t.v;
+        for (const void* p : {(const void*)t.param, (const void*)t.m, (const void*)t.v}) {
+            size_t at = (size_t)(((uint64_t)(uintptr_t)p * 0x9e3779b97f4a7c15ull) >> 32) & (places - 1);
+            for (; written[at]; at = (at + 1) & (places - 1))
+                if (written[at] == p) return bad("a parameter or moment is listed twice");  // (two blocks would update it)
+            written[at] = p;
+        }
         kt::AdamwEntry& x = e[live++];
         x.p = t.param;
         x.g = t.grad;
@@ -584,9 +589,6 @@ kt_status kt_adamw(int64_t count, const kt_adamw_tensor* tensors, const kt_adamw
         x.wide = aligned(t.param, 16) && aligned(t.grad, 16) && aligned(t.m, state) && aligned(t.v, state) && aligned(t.copy, 16);
     }
     if (!live) return done(KT_OK, "");
-    // (tied weights, say: two blocks would update the same values)
-    std::sort(written, written + 3 * live, std::less<const void*>());
-    if (std::adjacent_find(written, written + 3 * live) != written + 3 * live) return bad("a parameter or moment is listed twice");
     kt_status s;
     int dev, sms;
     if ((s = current_device(&dev, &sms)) != KT_OK) return s;
