@@ -170,16 +170,20 @@ __global__ void __launch_bounds__(kGluThreads) kt_glu_backward_kernel(const GluB
     }
 }
 
-// db[c] = the sum of `rows` partial sums, eight at a time, in a fixed order.
+// db[c] = the sum of `rows` partial sums (kMostRows at most), in a fixed order: a warp takes every eighth, all of them on
+// their way at a time.
+constexpr int kMostRows = 128;
 __global__ void __launch_bounds__(256) kt_column_sums_kernel(const float* partials, float* db, int rows, int cols) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ float sums[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = (int)blockIdx.x * 32 + lane;
+    float x[kMostRows / 8];
+#pragma unroll
+    for (int i = 0; i < kMostRows / 8; ++i) x[i] = warp + 8 * i < rows && c < cols ? partials[(int64_t)(warp + 8 * i) * cols + c] : 0.0f;
     float t = 0.0f;
-    if (c < cols)
-#pragma unroll 4
-        for (int r = warp; r < rows; r += 8) t += partials[(int64_t)r * cols + c];
+#pragma unroll
+    for (int i = 0; i < kMostRows / 8; ++i) t += x[i];
     sums[warp][lane] = t;
     __syncthreads();
     if (warp || c >= cols) return;
@@ -218,10 +222,10 @@ cudaError_t glu_dispatch(const GluBackward& p, int rows, int per, void* stream) 
 }  // namespace
 
 // Rows of blocks (and of partial sums): enough blocks for eight per SM, 32 rows each at least, and no more
-// than 128 partial sums per column.
+// than kMostRows partial sums per column.
 int column_sum_rows(int64_t M, int64_t F) {
     const int64_t across = (F + kGluCols - 1) / kGluCols, most = (M + 31) / 32;
-    return (int)std::max<int64_t>(1, std::min({most, (1216 + across - 1) / across, (int64_t)128}));
+    return (int)std::max<int64_t>(1, std::min({most, (1216 + across - 1) / across, (int64_t)kMostRows}));
 }
 
 kt_status launch_zero(int* at, void* stream, const char** why) {
