@@ -747,25 +747,34 @@ static double off_lines(const Matmul& a) { return (a.lda | a.ldb) % 64 ? 1.5 : 1
 
 MatmulShape matmul_shape(const Matmul& a, int sms, int device) {
     const int steps = (a.K + kAtomK - 1) / kAtomK;
-    // us per 64-deep step and per launch, measured from 10 to 80 steps
+    // us per 64-deep step and per launch, measured from 10 to 80 steps (2048 x 1280 x 5120: 27.4, 22.9, 31.8, 31.8 and 43.2 us
+    // in this order; 331 x 640 x 2560: 16.1, 13.7, 11.7, 11.1 and 10.7)
     struct {
         int pair, bn, atoms;
         double step, round;
     } const kinds[] = {{2, 256, 1, 0.26, 6.0}, {2, 192, 1, 0.198, 5.6}, {2, 128, 2, 0.17, 5.3}, {1, 128, 2, 0.17, 4.9}, {1, 64, 2, 0.155, 4.5}};
+    // bytes per us that L2 brings to all SMs: fewer where rows start between 128-byte lines, and half as many where they start
+    // between 32-byte sectors (a step of the second kind takes 0.36 us in 5000 x 1000 x 1000)
+    const bool lines = (a.lda | a.ldb) % 64 == 0, sectors = (a.lda | a.ldb) % 16 == 0;
+    const double rate = lines ? 23.0e6 : sectors ? 17.0e6 : 12.5e6;
     // nor are the operands sooner there than memory brings them: tiles that keep it busy gain nothing by sharing
     const double bytes = ((double)a.M + (double)a.N * (a.gated ? 2.0 : 1.0)) * a.K * 2.0, brought = bytes / 6.8e6;
     MatmulShape best = {};
     best.us = 1e30;
     for (const auto& k : kinds) {
+        if (k.bn == 192 && (a.a_mn || a.b_mn)) continue;  // (MN-major operands come in boxes of 64 columns per CTA)
         const int64_t t = mm_tiles(a, k.bn, k.pair), units = sms / k.pair, rounds = (t + units - 1) / units;
         const int atoms = a.a_mn || a.b_mn ? 2 : k.atoms;
-        if (k.bn == 192 && (a.a_mn || a.b_mn)) continue;  // (MN-major operands come in boxes of 64 columns per CTA)
-        const double step = k.step * off_lines(a), time = std::max(rounds * steps * step, brought) + (rounds - 1) * 0.5 + k.round;
+        const double step_bytes = 128.0 * ((k.pair == 1 && !a.a_mn ? std::min(128, a.M) : 128) + k.bn / k.pair);
+        const double alone = k.step * (!sectors ? 1.35 : !lines && k.pair == 1 ? 1.25 : 1.0);
+        auto step = [&](int64_t ctas) { return std::max(alone, (double)ctas * step_bytes / rate); };
+        const double time = std::max(rounds * steps * step(std::min(t, units) * k.pair), brought) + (rounds - 1) * 0.5 + k.round;
         if (time < best.us) best = {k.pair, k.bn, 1, atoms, time};
         if (k.pair == 2) continue;
         for (int ks = 2; ks <= 8; ++ks) {
             if (t * ks > sms || steps < 2 * ks || t > mm_clusters(ks, device)) continue;
-            const double split = std::max((steps + ks - 1) / ks * step, brought) + k.round + (a.gated ? 2.4 + 0.3 * ks : 2.0 + 0.15 * ks);
+            // (a tile's sharing by a cluster: 2.3 to 3.2 us, 4.8 of a gated one)
+            const double split = std::max((steps + ks - 1) / ks * step(t * ks), brought) + k.round + (a.gated ? 2.4 + 0.3 * ks : 2.0 + 0.15 * ks);
             if (split < best.us) best = {1, k.bn, ks, atoms, split};
         }
     }

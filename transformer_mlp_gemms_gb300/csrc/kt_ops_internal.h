@@ -105,7 +105,7 @@ struct Matmul {
 // How a product is run: CTAs per tile, accumulator columns per tile, CTAs that share a tile's sums, 64-deep steps per
 // stage of the ring.
 struct MatmulShape {
-    int pair, BN, splits, atoms;
+    int pair, BN, splits, atoms;  // (atoms: 2 with an MN-major operand)
     double us;  // what it is expected to take
 };
 MatmulShape matmul_shape(const Matmul& a, int sms, int device);
