@@ -342,7 +342,8 @@ kt_status kt_matmul_status(void* stream);
 /*
  * kt_matmul_debug_stall -- failure-injection hook for tests, as kt_linear_i8_debug_stall: with enable = 1 the
  * first block of the following calls' products waits on a barrier nobody signals, bounded as every
- * other wait then is by `limit_us` microseconds.
+ * other wait then is by `limit_us` microseconds; the blocks that add up a gradient's tile together never hear
+ * from it.
  */
 kt_status kt_matmul_debug_stall(int enable, int64_t limit_us);
 

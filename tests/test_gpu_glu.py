@@ -409,3 +409,64 @@ def test_a_workspace_of_two_graphs_replayed_in_turn():
         for t, u in zip(out, want):
             assert torch.equal(t, u)
     assert kt_ops.kt_matmul_status() == kt_mlp.KT_OK
+
+
+@pytest.mark.parametrize("M,N,K", [(700, 5000, 1288), (16384, 1280, 2560), (331, 640, 2560), (64, 2560, 264)])
+def test_a_wait_that_runs_out_in_a_linear_layers_gradients_shows(M, N, K):
+    """The first block stalls for 20 ms and raises no flag for its partial sums: the blocks that add them give up their
+    tiles.  What could not be computed is NaN, all else is as it is without the stall, and the next call is right."""
+    g = torch.Generator().manual_seed(M + N)
+    dt = torch.bfloat16
+    x, w, dy = randn(g, M, K, dtype=dt), randn(g, N, K, dtype=dt, std=K ** -0.5), randn(g, M, N, dtype=dt, std=0.25)
+    ws = kt_ops.linear_backward_workspace(M, N, K)
+
+    def run(bias):
+        out = torch.full((M, K), 7.0, dtype=dt, device="cuda"), torch.full((N, K), 7.0, dtype=dt, device="cuda")
+        kt_ops.kt_linear_backward(dy, x, w, *out, torch.empty(N, device="cuda") if bias else None, ws)
+        return out
+
+    for bias in (False, True):
+        want = run(bias)
+        assert kt_ops.kt_matmul_status() == kt_mlp.KT_OK
+        kt_ops.kt_matmul_debug_stall(True, 20000)
+        try:
+            got = run(bias)
+            assert kt_ops.kt_matmul_status() == kt_mlp.KT_ERR_TIMEOUT
+        finally:
+            kt_ops.kt_matmul_debug_stall(False)
+        assert any(a.isnan().any() for a in got)
+        for a, b in zip(got, want):
+            assert (a.isnan() | (a == b)).all()
+        for a, b in zip(run(bias), want):
+            assert torch.equal(a, b)
+        assert kt_ops.kt_matmul_status() == kt_mlp.KT_OK
+
+
+@pytest.mark.parametrize("M,D,F", [(729, 1152, 4304), (5000, 264, 2560), (4096, 640, 2560)])
+def test_a_wait_that_runs_out_in_a_gated_blocks_gradients_shows(M, D, F):
+    g = torch.Generator().manual_seed(M)
+    dt = torch.float16
+    x, w = randn(g, M, D, dtype=dt), randn(g, 2 * F, D, dtype=dt, std=D ** -0.5)
+    p, dh = randn(g, M, 2 * F, dtype=dt), randn(g, M, F, dtype=dt, std=0.5)
+    ws = kt_ops.glu_backward_workspace(M, D, F)
+
+    def run():
+        out = torch.full((M, D), 7.0, dtype=dt, device="cuda"), torch.full((2 * F, D), 7.0, dtype=dt, device="cuda"), torch.empty(2 * F, device="cuda")
+        kt_ops.kt_glu_backward(dh, p, x, w, *out, kt_mlp.KT_ACT_SILU, ws)
+        return out
+
+    want = run()
+    assert kt_ops.kt_matmul_status() == kt_mlp.KT_OK
+    kt_ops.kt_matmul_debug_stall(True, 20000)
+    try:
+        got = run()
+        assert kt_ops.kt_matmul_status() == kt_mlp.KT_ERR_TIMEOUT
+    finally:
+        kt_ops.kt_matmul_debug_stall(False)
+    assert got[0].isnan().any() or got[1].isnan().any()
+    for a, b in zip(got, want):
+        assert (a.isnan() | (a == b)).all()
+    assert torch.equal(got[2], want[2])  # the bias gradient hangs on neither product
+    for a, b in zip(run(), want):
+        assert torch.equal(a, b)
+    assert kt_ops.kt_matmul_status() == kt_mlp.KT_OK

@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
+                if (lane == 0 && ok) {  // (what was not seen is not given back, as in kt_matmul.cu)
                     if constexpr (PAIR == 2) mbar_arrive_cluster_relaxed(mapa_rank(bar_acce + 8u * buf, 0));
                     else mbar_arrive_relaxed(bar_acce + 8u * buf);
                 }

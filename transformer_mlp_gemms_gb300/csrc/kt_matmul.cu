@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                                                                      __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])));
                 }
                 epi_bar_sync<kMmEpi>();  // every warp's sums precede the flag
-                if (ew == 0 && lane == 0) {
+                if (ew == 0 && lane == 0 && !(p.stall_ns && blockIdx.x == 0)) {  // (the tests' hook: the stalled block raises none)
                     __threadfence();
                     asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p.flags + unit0 * 2 + (int)rank), "r"(1) : "memory");
                 }
@@ -506,10 +506,12 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 bool there = ok;
                 if (ew == 0 && lane < unit0 - first && there)  // (a lane per pair; there are fewer than 32)
                     there = wait_flag(p.flags + (first + lane) * 2 + (int)rank, abort_flag, &g_matmul_error, limit);
-                ok = epi_all<kMmEpi>(there);
+                // A flag that does not come spoils this tile alone: `ok` stays as it is, since the barriers still work and this
+                // item's sums were seen.
+                const bool whole = epi_all<kMmEpi>(there);
                 if (y < o.M)
-                    stores = sum_shared<DT>(mC, reinterpret_cast<const float4*>(p.partials + (int)rank * kSlot) + 32 * q + lane, first, unit0, ok, acc, half,
-                                            min(o.BN, o.N - n), n, y, stg, stores);
+                    stores = sum_shared<DT>(mC, reinterpret_cast<const float4*>(p.partials + (int)rank * kSlot) + 32 * q + lane, first, unit0, whole, acc,
+                                            half, min(o.BN, o.N - n), n, y, stg, stores);
             } else {
 #pragma unroll 1
                 for (int g = half; g < o.BN / 32; g += 2) {
@@ -527,7 +529,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
+            // An accumulator whose sums this warp has not seen is not given back: the barrier does not tell whose arrivals it
+            // counts, and two items' from one CTA would let the products overwrite what the other CTA still reads.  The products
+            // wait for it in vain then, as long as any wait.
+            if (lane == 0 && ok) {
                 if constexpr (PAIR == 2) mbar_arrive_cluster_relaxed(mapa_rank(bar_acce + 8u * buf, 0));
                 else mbar_arrive_relaxed(bar_acce + 8u * buf);
             }
