@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
             const uint32_t one = lane == 0;
             uint32_t stage = 0, phase = 0, buf = 0, use = 0;
             const uint64_t ad0 = smem_desc(base, 16u, 1024u), bd0 = smem_desc(base + kRuns * kF8ABytes, 16u, 1024u);
-            bool ok = true, any = false;
+            bool ok = true;
             // Narrow tiles are bound by this warp's instructions: both barriers of the next step are asked for before this
             // one's products, and the answers are there after them (1024 x 1024 x 8192 17.0 -> 16.3 us; wide tiles
             // lose by it, 8192^3 369 -> 378).
@@ -320,14 +320,10 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
                         for (uint32_t k = 0; k < 4; ++k)  // 32 columns each
                             mma_if<PAIR, true>(d + i * (uint32_t)BN, ad + i * (kF8ABytes >> 4) + 2 * k, bd + i * (C::kBBytes >> 4) + 2 * k, p.idesc, k > 0, one);
                     }
-                    any = true;
                     commit_if<PAIR>(bar_accf + 8u * which, one);
                     commit_if<PAIR>(bar_empty + 8u * now, one);
                 }
-            if (!ok && any) {  // no product may still be running when tensor memory is freed
-                commit_if<PAIR>(bar_drain, one);
-                if (lane == 0) wait_drain(bar_drain, 0u, 100000000ull);
-            }
+            settle<PAIR>(ok, bar_drain, bar_full, stage, phase, (uint32_t)kStages);
         }
         __syncwarp();
     } else if (warp >= 4) {

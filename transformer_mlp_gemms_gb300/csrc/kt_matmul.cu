@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         if (leader) {
             const uint32_t one = lane == 0, stage16 = stage_bytes >> 4;
             uint32_t stage = 0, phase = 0;
-            bool ok = true, any = false;
+            bool ok = true;
             int local = 0;
             MmItem it;
             for (auto w = walk(); ok && w.next(it); ++local) {
@@ -329,7 +329,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                                                                    DEV_TIMEOUT_MMA, limit));
                 if (!ok) break;
                 tc_fence_after();
-                any = true;
                 // The steps of one item, for operands of known order.  K-major: [64-deep step][row], 16 columns of K
                 // further are 32 bytes.  MN-major: [64 columns][K], 16 columns of K further are 16 rows of 128 bytes.
                 auto steps = [&](auto a_mn, auto b_mn, auto atoms_) {
@@ -376,10 +375,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 }
                 if (ok) commit_if<PAIR>(bar_accf + 8u * buf, one);
             }
-            if (!ok && any) {  // no product may still be running when tensor memory is freed
-                commit_if<PAIR>(bar_drain, one);
-                if (lane == 0) wait_drain(bar_drain, 0u, 100000000ull);
-            }
+            settle<PAIR>(ok, bar_drain, bar_full, stage, phase, (uint32_t)p.stages);
         }
         __syncwarp();
     } else {

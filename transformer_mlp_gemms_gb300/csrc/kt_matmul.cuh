@@ -82,6 +82,27 @@ __device__ __forceinline__ void commit_if(uint32_t bar, uint32_t one) {
             : "memory");
 }
 
+// The end of the warp that issues a CTA's (or pair's) products.  It waits for the last of them, whether or not it knows that
+// an epilogue warp has given up, which may come later: none may be running when tensor memory is freed.  Those that
+// were issued have waited for their copies.  Where some were not (ok false), copies of the stages from `stage` on may be
+// on their way into memory that is about to be released, from warps that ended before this CTA gave up: they get 1 ms
+// each to land (a copy takes a few microseconds; what nobody counted does not show).
+template <int PAIR>
+__device__ __forceinline__ void settle(bool ok, uint32_t bar_drain, uint32_t bar_full, uint32_t stage, uint32_t phase, uint32_t stages) {
+    const uint32_t one = (threadIdx.x & 31u) == 0;
+    commit_if<PAIR>(bar_drain, one);
+    if (one) {
+        wait_drain(bar_drain, 0u, 100000000ull);
+        for (uint32_t s = ok ? stages : 0u; s < stages; ++s) {
+            wait_drain(bar_full + 8u * stage, phase, 1000000ull);
+            if (++stage == stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+}
+
 // Waits until another CTA's flag is raised, as the wait on a barrier: bounded, and given up where this CTA aborts.
 __device__ __forceinline__ bool wait_flag(const int* flag, volatile int* abort_flag, int* err, unsigned long long limit_ns) {
     const unsigned long long t0 = global_ns();
