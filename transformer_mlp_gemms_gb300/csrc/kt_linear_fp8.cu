@@ -291,12 +291,13 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
             // one's products, and the answers are there after them (1024 x 1024 x 8192 17.0 -> 16.3 us; wide tiles
             // lose by it, 8192^3 369 -> 378).
             constexpr bool kAhead = BN <= 128;
+            // (accumulators come back from both CTAs of a pair: acquired at cluster scope)
             uint32_t full = 0u, free = 0u;
             for (int t = unit0; t < tiles && ok; t += units)
                 for (int j = 0; j < runs; j += kRuns) {
                     ok = __all_sync(0xffffffffu,
                                     (full || wait_turn(bar_full + 8u * stage, phase, abort_flag, &g_fp8_error, DEV_TIMEOUT_MMA, limit)) &&
-                                        (free || wait_turn(bar_acce + 8u * buf, (use & 1u) ^ 1u, abort_flag, &g_fp8_error, DEV_TIMEOUT_MMA, limit)));
+                                        (free || wait_turn<PAIR == 2>(bar_acce + 8u * buf, (use & 1u) ^ 1u, abort_flag, &g_fp8_error, DEV_TIMEOUT_MMA, limit)));
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t d = tmem + buf * (uint32_t)(kRuns * BN), now = stage, which = buf;
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(F8<PAIR, BN, SWAP>::kThreads, 1)
                     }
                     if constexpr (kAhead) {
                         full = mbar_test_wait(bar_full + 8u * stage, phase);
-                        free = mbar_test_wait(bar_acce + 8u * buf, (use & 1u) ^ 1u);
+                        free = PAIR == 2 ? mbar_test_wait_cluster(bar_acce + 8u * buf, (use & 1u) ^ 1u) : mbar_test_wait(bar_acce + 8u * buf, (use & 1u) ^ 1u);
                     }
 #pragma unroll
                     for (uint32_t i = 0; i < (uint32_t)kRuns; ++i) {

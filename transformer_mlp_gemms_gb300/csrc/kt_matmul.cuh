@@ -82,6 +82,19 @@ __device__ __forceinline__ void commit_if(uint32_t bar, uint32_t one) {
             : "memory");
 }
 
+// As mbar_test_wait, acquiring at cluster scope as mbar_try_wait_cluster does.
+__device__ __forceinline__ uint32_t mbar_test_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok;
+}
+
 // The end of the warp that issues a CTA's (or pair's) products.  It waits for the last of them, whether or not it knows that
 // an epilogue warp has given up, which may come later: none may be running when tensor memory is freed.  Those that
 // were issued have waited for their copies.  Where some were not (ok false), copies of the stages from `stage` on may be
