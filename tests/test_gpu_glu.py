@@ -470,3 +470,128 @@ def test_a_wait_that_runs_out_in_a_gated_blocks_gradients_shows(M, D, F):
     for a, b in zip(run(), want):
         assert torch.equal(a, b)
     assert kt_ops.kt_matmul_status() == kt_mlp.KT_OK
+
+
+# sizes whose last tiles' steps are shared out, joined behind flags in the workspace (checked by the flags that were raised)
+def gated_gradients(M, D, F, dt, g, bias, ws):
+    """(inputs, outputs, call) of a gated block's gradients."""
+    x, w = randn(g, M, D, dtype=dt), randn(g, 2 * F, D, dtype=dt, std=D ** -0.5)
+    p, dh = randn(g, M, 2 * F, dtype=dt), randn(g, M, F, dtype=dt, std=0.5)
+    out = [torch.empty(M, D, dtype=dt, device="cuda"), torch.empty(2 * F, D, dtype=dt, device="cuda")]
+    db = torch.empty(2 * F, device="cuda") if bias else None
+    return [dh, p, x, w], out + [db] * bias, lambda ws=ws: kt_ops.kt_glu_backward(dh, p, x, w, *out, db, kt_mlp.KT_ACT_GELU_TANH, ws)
+
+
+def linear_gradients(M, N, K, dt, g, bias, ws):
+    x, w, dy = randn(g, M, K, dtype=dt), randn(g, N, K, dtype=dt, std=K ** -0.5), randn(g, M, N, dtype=dt, std=0.25)
+    out = [torch.empty(M, K, dtype=dt, device="cuda"), torch.empty(N, K, dtype=dt, device="cuda")]
+    db = torch.empty(N, device="cuda") if bias else None
+    return [dy, x, w], out + [db] * bias, lambda ws=ws: kt_ops.kt_linear_backward(dy, x, w, *out, db, ws)
+
+
+SHARED = [(gated_gradients, (729, 1152, 4304)), (gated_gradients, (5000, 264, 2560)), (linear_gradients, (700, 5000, 1288)),
+          (linear_gradients, (16384, 1280, 2560))]
+
+
+def room(make, size):
+    return (kt_ops.glu_backward_workspace if make is gated_gradients else kt_ops.linear_backward_workspace)(*size)
+
+
+def renew(inputs, g):
+    for t in inputs:
+        t.copy_(torch.randn(t.shape, generator=g, dtype=torch.float32, device="cuda") * 0.2)
+
+
+@pytest.mark.parametrize("bias", [False, True])
+def test_shared_gradients_of_graphs_with_one_workspace(bias):
+    """New values before each replay, another graph in between, whose flags and partial sums stay in the workspace: each
+    replay's results are those of a call of its own with a workspace of its own, bit for bit."""
+    g, gd = torch.Generator().manual_seed(3), torch.Generator(device="cuda").manual_seed(3)
+    ws = max((room(*s) for s in SHARED), key=lambda t: t.numel())
+    ws.fill_(255)
+    calls = []
+    for make, size in SHARED:
+        inputs, out, run = make(*size, torch.bfloat16, g, bias, ws)
+        run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        calls.append((graph, inputs, out, run, room(make, size)))
+    for i in (0, 1, 1, 2, 0, 3, 2, 2, 3, 1, 0):
+        graph, inputs, out, run, own = calls[i]
+        renew(inputs, gd)
+        run(own.fill_(0))
+        want = [t.clone() for t in out]
+        for t in out:
+            t.fill_(float("nan"))
+        graph.replay()
+        for t, u in zip(out, want):
+            assert torch.equal(t, u), i
+    assert kt_ops.kt_matmul_status() == kt_mlp.KT_OK
+
+
+@pytest.mark.parametrize("make,size", SHARED)
+def test_shared_gradients_again_and_again_into_the_same_buffers(make, size):
+    """Values written anew right before each of ten steps, eager and in one graph."""
+    g, gd = torch.Generator().manual_seed(4), torch.Generator(device="cuda").manual_seed(4)
+    ws = room(make, size)
+    inputs, out, run = make(*size, torch.float16, g, True, ws)
+    new = []
+    for _ in range(3):
+        renew(inputs, gd)
+        new.append([t.clone() for t in inputs])
+    want = []
+    for n in new:
+        for t, u in zip(inputs, n):
+            t.copy_(u)
+        torch.cuda.synchronize()
+        run(room(make, size))
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in out])
+    got = [[torch.empty_like(t) for t in out] for _ in range(10)]
+
+    def steps():
+        for i, to in enumerate(got):
+            for t, u in zip(inputs, new[i % 3]):
+                t.copy_(u)
+            run()
+            for t, u in zip(to, out):
+                t.copy_(u)
+
+    def check():
+        torch.cuda.synchronize()
+        assert kt_ops.kt_matmul_status() == kt_mlp.KT_OK
+        for i, to in enumerate(got):
+            for t, u in zip(to, want[i % 3]):
+                assert torch.equal(t, u), i
+                t.fill_(float("nan"))
+
+    steps()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        steps()
+    for _ in range(2):
+        graph.replay()
+        check()
+
+
+def test_shared_gradients_on_three_streams_at_once():
+    g = torch.Generator().manual_seed(5)
+    calls = []
+    for make, size in SHARED[:3]:
+        ws = room(make, size)
+        inputs, out, run = make(*size, torch.bfloat16, g, True, ws)
+        run()
+        torch.cuda.synchronize()
+        calls.append((out, [t.clone() for t in out], run, torch.cuda.Stream()))
+    for _ in range(20):
+        for out, _, run, stream in calls:
+            with torch.cuda.stream(stream):
+                run()
+    torch.cuda.synchronize()
+    assert kt_ops.kt_matmul_status() == kt_mlp.KT_OK
+    for out, want, _, _ in calls:
+        for t, u in zip(out, want):
+            assert torch.equal(t, u)
