@@ -223,3 +223,41 @@ def test_on_another_stream_and_without_tensors():
     t.follow(grads, 1)
     t.check()
     kt_ops.kt_adamw([], [], [], [], 1, 1e-3)
+
+
+def exact_quotients(a, b):
+    """AdamW as a division: p = -(a / |b|), for a next to b in magnitude.  Moments that hardly move (beta1 = 1 - 2^-30 is 1 in
+    fp32, and a gradient times 2^-30 is lost beside a), a second moment of the gradient's square alone (whose root is the
+    gradient), no eps, and a rate of 2^-30 / (1 - beta1) = 1."""
+    p = torch.zeros_like(a)
+    kt_ops.kt_adamw([p], [b.clone()], [a.clone()], [torch.zeros_like(a)], 1, 2.0 ** -30, 1 - 2.0 ** -30, 0.0, 0.0)
+    return -p
+
+
+@pytest.mark.parametrize("exponent", [0, -38, 29])
+def test_quotients_of_every_divisor_are_correctly_rounded(exponent):
+    """Every significand as the divisor, for numerators at and next to powers of two, where a divisor next to the next
+    power leaves the quotient next to the middle of two numbers (1.0 / 0x1.fffffep+0, 0x1.aaaaa6p+0 / 0x1.fffffap+0).
+    The once refined reciprocal has to be the nearest number for that, which hangs on the hardware's approximation."""
+    b = (torch.arange(1 << 23, device="cuda", dtype=torch.int32) + 0x3F800000).view(torch.float32)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    some = (torch.randint(0, 1 << 23, b.shape, generator=g, device="cuda", dtype=torch.int32) + 0x3F800000).view(torch.float32)
+    up = 2.0 ** -23
+    numerators = [1.0, 1 + up, 1 + 2 * up, 1 + 3 * up, 2 - up, 2 - 2 * up, 2 - 3 * up, 1.5, float.fromhex("0x1.aaaaa6p+0"), 4 / 3, 1.75]
+    for a in [torch.full_like(b, n) for n in numerators] + [some, b.flip(0), b]:
+        want = (a.double() / b.double()).float()  # (of 24-bit numbers: the 53-bit quotient's rounding does not decide)
+        assert torch.equal(exact_quotients(a * 2.0 ** exponent, b * 2.0 ** exponent), want)
+
+
+def test_roots_of_every_number_are_correctly_rounded():
+    """Both parities of the exponent: p = -(m 2^15 / (sqrt(v) 2^15)) with m the exact root, so that any other root than that
+    leaves something else than -1."""
+    v = (torch.arange(1 << 24, device="cuda", dtype=torch.int32) + 0x3F800000).view(torch.float32)
+    m = v.double().sqrt().float()
+    p, zero, beta = torch.zeros_like(v), torch.zeros_like(v), 1 - 2.0 ** -30
+    kt_ops.kt_adamw([p], [zero], [m.clone()], [v.clone()], 1, 2.0 ** -15, beta, beta, 0.0)
+    assert (p == -1).all()
+    p.zero_()
+    off = torch.nextafter(m, torch.full_like(m, float("inf")))  # another root would show
+    kt_ops.kt_adamw([p], [zero], [off], [v.clone()], 1, 2.0 ** -15, beta, beta, 0.0)
+    assert (p != -1).all()
