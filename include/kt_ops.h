@@ -223,7 +223,9 @@ kt_status kt_glu_forward(int64_t M, int64_t D, int64_t F, kt_dtype dtype, kt_act
  *   dvalue = dh * act(gate),  dgate = dh * value * act'(gate),   dp = [dvalue | dgate]
  *   dX = dp . W,   dW = dp^T . X,   db = sum of dp over the tokens
  * dp is rounded to dtype once, as the products' operand (db is summed before that); fp32 sums, and one rounding
- * of each element of dX and dW.  An element of dp beyond dtype's range is infinite.
+ * of each element of dX and dW.  An element of dp beyond dtype's range is infinite; with KT_F16 one below 2^-14 is
+ * held to 2^-25 in absolute terms, so that one below that adds nothing to dX and dW, however many tokens have it.
+ * Gradients that small want a loss scale (a power of two on dH, which is the same one on dX, dW and db).
  *   dX: [M][D], pitch lddx; dW: [2F][D]; db: [2F] fp32; each may be NULL: it is then not computed.
  *   M = 0 writes zeros to dW and db.
  *   workspace: kt_glu_backward_workspace(M, D, F) bytes, 16-byte aligned, its content irrelevant before
@@ -323,7 +325,8 @@ kt_status kt_quantize_fp8(int64_t M, int64_t K, kt_dtype dtype, kt_act act, cons
  *   Y[m][n] = round( sum_j scale_x[m][j] scale_w[n / 128][j] sum_{k in run j} Q[m][k] W[n][k]  (+ bias[n]) )
  *   Q: e4m3 [M][K], pitch ldq; scale_x: [M][ceil(K / 128)] fp32.  W: e4m3 [N][K], pitch ldw;
  *   scale_w: [ceil(N / 128)][ceil(K / 128)] fp32.  bias: [N] of dtype or NULL.  Y: [M][N] of dtype, pitch ldy.
- * The sums of a run and over the runs are fp32, with one rounding to dtype at the end.
+ * The sums of a run and over the runs are fp32, with one rounding to dtype at the end.  The two scales' product is
+ * taken first, in fp32: past its range it is infinite, and below 2^-126 it has fewer digits.
  *   M >= 0, N a multiple of 8, K, ldq and ldw multiples of 16, ldy a multiple of 8; Q, W, Y and bias 16-byte
  *   aligned.  Up to KT_LINEAR_FP8_FEW tokens the weights are the tensor cores' first operand.
  */

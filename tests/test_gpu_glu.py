@@ -595,3 +595,29 @@ def test_shared_gradients_on_three_streams_at_once():
     for out, want, _, _ in calls:
         for t, u in zip(out, want):
             assert torch.equal(t, u)
+
+
+@pytest.mark.parametrize("M", [40, 729])
+def test_gradients_below_the_normal_numbers(M):
+    """Gradients near 1e-6 in float16: dp is held to 2^-25 in absolute terms, and all of it that is below is lost.  The same
+    gradients under a loss scale of 2^10 keep what dh has."""
+    g = torch.Generator().manual_seed(M)
+    D, F, dt = 264, 520, torch.float16
+    x, w = randn(g, M, D, dtype=dt), randn(g, 2 * F, D, dtype=dt, std=D ** -0.5)
+    p, dh = randn(g, M, 2 * F, dtype=dt), randn(g, M, F, dtype=dt, std=1e-6)
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(2 * F, device="cuda")
+    off = []
+    for scale in (1.0, 1024.0):
+        scaled = dh * scale  # exact: dh is a multiple of 2^-24
+        kt_ops.kt_glu_backward(scaled, p, x, w, dx, dw, db, kt_mlp.KT_ACT_SILU, kt_ops.glu_backward_workspace(M, D, F))
+        dxx, tx, dwx, tw, dbx, tb = ref.glu_backward(scaled, p, x, w, "silu", dt)
+        near(dx, dxx, tx)
+        near(dw, dwx, tw)
+        near(db, dbx, tb)
+        off.append(((dw.double() - dwx).norm() / dwx.norm()).item())
+    assert off[1] < off[0] / 4
+    # columns whose elements of dp are all below 2^-25 are lost, but not to the bias gradient
+    p[:, F:] = -40.0
+    dh.fill_(2.0 ** -10)
+    kt_ops.kt_glu_backward(dh, p, x, w, dx, dw, db, kt_mlp.KT_ACT_SILU, kt_ops.glu_backward_workspace(M, D, F))
+    assert not dx.any() and not dw.any() and db.all()
