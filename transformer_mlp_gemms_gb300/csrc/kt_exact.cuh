@@ -15,8 +15,8 @@ __device__ __forceinline__ f32x2 sum_rn(f32x2 product, f32x2 other, f32x2 one) {
 // wants the reciprocal that is nearest to 1 / b.  One refinement gives that from any approximation to one unit, but for 32
 // significands of b whose reciprocals lie next to the middle of two numbers: quotients such as 1.0 / 0x1.fffffep+0 and
 // 0x1.aaaaa6p+0 / 0x1.fffffap+0 could then be one unit off.  This hardware's approximation is good enough there too: the
-// tests try every divisor's and every root's significand.  At a time of two values they take a third of the instructions of __fsqrt_rn and __fdiv_rn, whose branches
-// for the other operands are taken per value.
+// tests try every divisor's and every root's significand.  At a time of two values they take a third of the instructions
+// of __fsqrt_rn and __fdiv_rn, whose branches for the other operands are taken per value.
 __device__ __forceinline__ float rsqrt_approx(float x) {
     float y;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -24,10 +24,11 @@
 // A pair goes through its share backwards, so that what others wait for comes first and what waits for others comes
 // last, and a pair waits for pairs of lower numbers alone, which were launched before it.
 //
-// Bound by the tensor cores where K is long (16384 tokens x 1280 x 5120 bf16: linear 118 us, 1.82 PFLOP/s; the
-// gradients of a gated block 454 us, 1.89 PFLOP/s, the tensor pipe busy 94 % of the time; the gated projection 215 us,
-// 2.0 PFLOP/s, and 250 us with p, whose 335 MB pass through the shared memory that the operands need too); for few
-// tokens by the weights' bytes and a launch (4 x 1280 x 2 5120 in 8 us, 3.3 TB/s).
+// Bound by the tensor cores where K is long.  16384 tokens x 1280 x 5120 bf16, a call alone on a cool GPU: linear 118 us,
+// 1.82 PFLOP/s; the products of a gated block's gradients 454 us, 1.89 PFLOP/s, the tensor pipe busy 94 % of the time; the
+// gated projection 215 us, 2.0 PFLOP/s, and 250 us with p, whose 335 MB pass through the shared memory that the operands
+// need too.  Calls in sequence run at the 1.4 to 1.5 GHz that the power cap leaves: 137, 512, 256 and 283 us.  For few
+// tokens the weights' bytes and a launch bind (4 x 1280 x 2 5120 in 8 to 9 us, 3 TB/s).
 //
 // Every wait is bounded: one that runs out leaves an error word and NaN in the elements that the call
 // could not compute.

@@ -128,7 +128,7 @@ kt_status zeros(void* p, size_t bytes, void* stream) {
     return e == cudaSuccess ? KT_OK : cuda_failed("cudaMemsetAsync", e);
 }
 // The pitch of dP in the workspace: whole 128-byte lines, as a product's copies of 64 columns take longer
-// where rows start between lines (the gradients of 729 x 1152 x 2 4304 41.8 -> 41.1 us).
+// where rows start between lines (1.7 % of the gradients of 729 x 1152 x 2 4304).
 int64_t dp_pitch(int64_t F) { return (2 * F + 63) / 64 * 64; }
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 const size_t kScratch = kt::kGradientsFlags + kt::gradients_partials();  // of launch_gradients

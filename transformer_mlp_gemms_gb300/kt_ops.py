@@ -1,5 +1,6 @@
 """Binding of ``include/kt_ops.h``: layer norm and its gradients, 8-bit rows and the 8-bit
-linear layer, and the mixture-of-experts layer for a few tokens.
+linear layer, the mixture-of-experts layer for a few tokens, a gated block and a linear layer
+with their gradients, AdamW, and the linear layer in 8-bit floating point with its quantiser.
 
 The functions carry the names of the C entry points and take torch tensors: sizes and row
 pitches come from the tensors, which may be row slices of wider ones (any stride between
